@@ -81,7 +81,8 @@ typedef int fp8la_status;
 #define FP8LA_ERR_DEVICE_TIMEOUT -5  /* a bounded wait inside a kernel ran out */
 #define FP8LA_ERR_DEVICE_ARG     -6  /* a kernel found a device-side argument it
                                         cannot use (m_offsets of fp8_grouped_gemm or
-                                        fp8_quantize_pertensor_grouped) */
+                                        fp8_quantize_pertensor_grouped, ids of
+                                        fp8_moe_layer) */
 
 /*
  * Per-tensor E4M3 quantisation ([P1] risks paragraph: E4M3 spans +-448 and
@@ -299,6 +300,87 @@ FP8LA_API fp8la_status fp8_grouped_gemm(int32_t num_groups, const int32_t *m_off
                               int64_t ldc, int64_t N, int64_t K,
                               const float *scale_a, const float *scale_b,
                               fp8la_stream_t stream);
+
+/* Element types of activations and logits. */
+#define FP8LA_TYPE_F32 0
+#define FP8LA_TYPE_BF16 1
+
+/*
+ * Mixture-of-experts router.  For each token t with logits z[0..E):
+ *
+ *   ids[t][j]     = the top_k experts of largest z, larger first, equal
+ *                   logits by the lowest index
+ *   weights[t][j] = exp(z_j - max z) / s, with s the sum of exp(z - max z)
+ *                   over the chosen experts (renormalise != 0) or over all
+ *
+ * An expert of logit -inf is never chosen: where fewer than top_k others are
+ * left, the remaining slots get id -1 and weight 0 (a token whose logits are
+ * all -inf gets no expert at all).  NaN counts as the largest logit; a token
+ * with a NaN or +inf logit has NaN weights.  Arithmetic is fp32.
+ *
+ * With m_offsets and order (both or neither NULL) the pairs t * top_k + j are
+ * also sorted by expert, in increasing pair number within an expert:
+ * order[m_offsets[e] .. m_offsets[e+1]) are expert e's pairs, and the pairs
+ * without an expert follow from order[m_offsets[E]] on.  m_offsets is what
+ * fp8_quantize_pertensor_grouped and fp8_grouped_gemm take, for activation
+ * rows gathered in that order.
+ *
+ * logits: fp32 or bf16 (dtype, FP8LA_TYPE_*) [tokens][ld], ld >= E; ids:
+ * int32 and weights: fp32 [tokens][top_k]; m_offsets: int32 [E + 1]; order:
+ * int32 [tokens * top_k].  1 <= top_k <= min(E, 16), E <= 1024 (beyond:
+ * FP8LA_ERR_UNSUPPORTED).  workspace: fp8_moe_route_workspace_bytes(tokens,
+ * E) bytes, 4-byte aligned, needed only for the sort; it keeps nothing
+ * between calls.  One launch, or two for a sort of more than 128 tokens.
+ */
+FP8LA_API int64_t fp8_moe_route_workspace_bytes(int64_t tokens, int32_t num_experts);
+FP8LA_API fp8la_status fp8_moe_route(const void *logits, int32_t dtype, int64_t tokens,
+                           int32_t num_experts, int64_t ld, int32_t top_k,
+                           int32_t renormalise, int32_t *ids, float *weights,
+                           int32_t *m_offsets, int32_t *order,
+                           void *workspace, int64_t workspace_bytes,
+                           fp8la_stream_t stream);
+
+#define FP8LA_ACT_SILU 0       /* g / (1 + exp(-g)) */
+#define FP8LA_ACT_GELU_TANH 1  /* g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
+
+/*
+ * Mixture-of-experts layer for up to 128 tokens, all of it in two launches,
+ * with FP8 weights and full-precision activations:
+ *
+ *   [g; u] = scale13[e] * dec(W13[e]) x_t        (rows 0..F-1 are g)
+ *   h      = act(g) * u
+ *   y_t    = bf16_rn( sum_j weights[t][j] * scale2[e_j] * dec(W2[e_j]) h ),
+ *            e_j = ids[t][j], slots with id -1 left out
+ *
+ * Sums are FP32.  x and h enter the tensor cores as the sum of two E4M3
+ * values under a power-of-two scale per 256 or 512 elements: 8 significant
+ * bits, which is exact for bf16 x except for elements below 2^-15 of their
+ * neighbourhood's largest, and for fp32 x and for h no worse than a rounding
+ * to bf16.  A token whose x holds an infinity or NaN gets a NaN row.  Tokens
+ * with no expert get a zero row.  The result does not depend on timing.
+ *
+ * x: fp32 or bf16 [tokens][ldx]; ids: int32, weights: fp32 [tokens][top_k]
+ * (from fp8_moe_route or any other router; an id twice in a token counts
+ * twice).  Ids outside -1..E-1 make the call write no y and record
+ * FP8LA_ERR_DEVICE_ARG.  w13: [E][2F][ld13] and w2: [E][D][ld2] codes of
+ * `format` (FP8LA_FORMAT_*), experts expert_stride13 / expert_stride2 codes
+ * apart; 16-byte aligned, with ld13, ld2 and the strides multiples of 16.
+ * scale13, scale2: fp32 [E].  y: bf16 [tokens][ldy].  All device.  Limits
+ * (FP8LA_ERR_UNSUPPORTED): tokens <= 128, top_k <= 16, E <= 1024, D and F
+ * <= 2^20.  workspace: fp8_moe_layer_workspace_bytes(tokens, top_k, D, F)
+ * bytes, 16-byte aligned; it keeps nothing between calls, but calls that may
+ * run at the same time need one each.
+ */
+FP8LA_API int64_t fp8_moe_layer_workspace_bytes(int64_t tokens, int32_t top_k,
+                                      int64_t D, int64_t F);
+FP8LA_API fp8la_status fp8_moe_layer(
+    const void *x, int32_t x_dtype, int64_t tokens, int64_t D, int64_t ldx,
+    const int32_t *ids, const float *weights, int32_t top_k,
+    int32_t num_experts, const uint8_t *w13, int64_t ld13,
+    int64_t expert_stride13, const float *scale13, const uint8_t *w2,
+    int64_t ld2, int64_t expert_stride2, const float *scale2, int64_t F,
+    int32_t format, int32_t activation, uint16_t *y, int64_t ldy,
+    void *workspace, int64_t workspace_bytes, fp8la_stream_t stream);
 
 /*
  * Synchronise `stream`, then read and clear the current device's status

@@ -26,6 +26,11 @@ FP8LA_ERR_DEVICE_TIMEOUT = -5
 FP8LA_ERR_DEVICE_ARG = -6
 FP8LA_FORMAT_E4M3 = 0
 FP8LA_FORMAT_E5M2 = 1
+FP8LA_TYPE_F32 = 0
+FP8LA_TYPE_BF16 = 1
+FP8LA_ACT_SILU = 0
+FP8LA_ACT_GELU_TANH = 1
+_ACTIVATIONS = {"silu": FP8LA_ACT_SILU, "gelu_tanh": FP8LA_ACT_GELU_TANH}
 _FORMATS = {"e4m3": FP8LA_FORMAT_E4M3, "e5m2": FP8LA_FORMAT_E5M2}
 
 # (name, restype, argtypes) of every entry point in include/fp8la.h.
@@ -47,6 +52,13 @@ SIGNATURES = [
      [_P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I64, _P, _I64, _P, _I64, _P]),
     ("fp8_grouped_gemm", _S,
      [_I32, _P, _I64, _P, _I64, _P, _I64, _I64, _P, _I64, _I64, _I64, _P, _P, _P]),
+    ("fp8_moe_route_workspace_bytes", _I64, [_I64, _I32]),
+    ("fp8_moe_route", _S,
+     [_P, _I32, _I64, _I32, _I64, _I32, _I32, _P, _P, _P, _P, _P, _I64, _P]),
+    ("fp8_moe_layer_workspace_bytes", _I64, [_I64, _I32, _I64, _I64]),
+    ("fp8_moe_layer", _S,
+     [_P, _I32, _I64, _I64, _I64, _P, _P, _I32, _I32, _P, _I64, _I64, _P, _P, _I64, _I64, _P,
+      _I64, _I32, _I32, _P, _I64, _P, _I64, _P]),
     ("fp8_get_device_status", _S, [_P]),
     ("fp8la_set_wait_timeout_ns", _S, [_I64]),
     ("fp8la_diag_gemm_withheld_arrival", _S, [_P, _I64, _P, _I64, _P, _I64, _P, _P, _P]),
@@ -147,6 +159,35 @@ def fp8_grouped_gemm(num_groups, m_offsets, m_capacity, A, lda, B, ldb,
                      b_group_stride, C, ldc, N, K, scale_a, scale_b, stream):
     return _call("fp8_grouped_gemm", num_groups, m_offsets, m_capacity, A, lda,
                  B, ldb, b_group_stride, C, ldc, N, K, scale_a, scale_b, stream)
+
+
+def _bytes(name, *args):
+    n = getattr(load(), name)(*args)
+    if n < 0:
+        raise Fp8laError(n, name)
+    return n
+
+
+def fp8_moe_route_workspace_bytes(tokens, num_experts):
+    return _bytes("fp8_moe_route_workspace_bytes", tokens, num_experts)
+
+
+def fp8_moe_route(logits, dtype, tokens, num_experts, ld, top_k, renormalise, ids, weights,
+                  m_offsets, order, workspace, workspace_bytes, stream):
+    return _call("fp8_moe_route", logits, dtype, tokens, num_experts, ld, top_k, renormalise,
+                 ids, weights, m_offsets, order, workspace, workspace_bytes, stream)
+
+
+def fp8_moe_layer_workspace_bytes(tokens, top_k, D, F):
+    return _bytes("fp8_moe_layer_workspace_bytes", tokens, top_k, D, F)
+
+
+def fp8_moe_layer(x, x_dtype, tokens, D, ldx, ids, weights, top_k, num_experts, w13, ld13,
+                  expert_stride13, scale13, w2, ld2, expert_stride2, scale2, F, fmt, activation,
+                  y, ldy, workspace, workspace_bytes, stream):
+    return _call("fp8_moe_layer", x, x_dtype, tokens, D, ldx, ids, weights, top_k, num_experts,
+                 w13, ld13, expert_stride13, scale13, w2, ld2, expert_stride2, scale2, F, fmt,
+                 activation, y, ldy, workspace, workspace_bytes, stream)
 
 
 def fp8_get_device_status(stream):
@@ -338,6 +379,95 @@ def grouped_gemm(m_offsets, A, B, scale_a, scale_b, C=None):
                      ldb, bstride, _ptr(C), _ld(C), N, K,
                      _ptr(scale_a), _ptr(scale_b), _stream())
     return C
+
+
+def _dtype_code(t):
+    import torch
+    assert t.dtype in (torch.float32, torch.bfloat16)
+    return FP8LA_TYPE_BF16 if t.dtype == torch.bfloat16 else FP8LA_TYPE_F32
+
+
+def _workspace(workspace, need, device):
+    """The caller's workspace, or a fresh one from torch's allocator."""
+    import torch
+    if need == 0:
+        return None, 0
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def moe_route(logits, top_k, renormalise=True, sort=True, ids=None, weights=None,
+              m_offsets=None, order=None, workspace=None):
+    """logits: fp32 or bf16 CUDA [T][E] (row stride may exceed E).
+
+    Returns (ids int32 [T][top_k], weights fp32 [T][top_k], m_offsets int32
+    [E+1], order int32 [T*top_k]); the last two, the pairs sorted by expert,
+    are None with sort=False.  Ties go to the lowest index; a slot without an
+    expert (all other logits -inf) has id -1 and weight 0.  Nothing is
+    synchronised.
+    """
+    import torch
+    assert logits.dim() == 2 and logits.stride(1) == 1
+    T, E = logits.shape
+    dev = logits.device
+    if ids is None:
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    if weights is None:
+        weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    assert ids.dtype == torch.int32 and ids.shape == (T, top_k) and ids.is_contiguous()
+    assert (weights.dtype == torch.float32 and weights.shape == (T, top_k)
+            and weights.is_contiguous())
+    nbytes = 0
+    if sort:
+        if m_offsets is None:
+            m_offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        if order is None:
+            order = torch.empty(T * top_k, dtype=torch.int32, device=dev)
+        assert m_offsets.dtype == torch.int32 and m_offsets.shape == (E + 1,)
+        assert order.dtype == torch.int32 and order.shape == (T * top_k,)
+        assert m_offsets.is_contiguous() and order.is_contiguous()
+        workspace, nbytes = _workspace(workspace, fp8_moe_route_workspace_bytes(T, E), dev)
+    else:
+        m_offsets = order = workspace = None
+    fp8_moe_route(_ptr(logits), _dtype_code(logits), T, E, _ld(logits), top_k,
+                  int(renormalise), _ptr(ids), _ptr(weights), _ptr(m_offsets), _ptr(order),
+                  _ptr(workspace), nbytes, _stream())
+    return ids, weights, m_offsets, order
+
+
+def moe_layer(x, ids, weights, w13, scale13, w2, scale2, y=None, workspace=None, fmt="e4m3",
+              activation="silu"):
+    """Mixture-of-experts layer for up to 128 tokens: x fp32 or bf16 CUDA
+    [T][D], ids int32 and weights fp32 [T][top_k] -> y bf16 [T][D].
+
+    w13 uint8 [E][2F][D] (gate rows, then up rows) and w2 uint8 [E][D][F] are
+    codes of fmt ("e4m3" or "e5m2") with row strides that are multiples of
+    16; scale13, scale2 fp32 [E].  activation: "silu" or "gelu_tanh".
+    Nothing is synchronised.
+    """
+    import torch
+    T, D = x.shape
+    E, F = w13.shape[0], w2.shape[2]
+    top_k = ids.shape[1]
+    assert x.stride(1) == 1 and w13.shape == (E, 2 * F, D) and w2.shape == (E, D, F)
+    assert w13.dtype == torch.uint8 and w2.dtype == torch.uint8
+    assert w13.stride(2) == 1 and w2.stride(2) == 1
+    assert ids.dtype == torch.int32 and ids.shape == (T, top_k) and ids.is_contiguous()
+    assert (weights.dtype == torch.float32 and weights.shape == (T, top_k)
+            and weights.is_contiguous())
+    assert scale13.dtype == torch.float32 and scale13.numel() == E and scale13.is_contiguous()
+    assert scale2.dtype == torch.float32 and scale2.numel() == E and scale2.is_contiguous()
+    if y is None:
+        y = torch.empty((T, D), dtype=torch.bfloat16, device=x.device)
+    assert y.dtype == torch.bfloat16 and y.shape == (T, D) and y.stride(1) == 1
+    workspace, nbytes = _workspace(workspace, fp8_moe_layer_workspace_bytes(T, top_k, D, F),
+                                   x.device)
+    fp8_moe_layer(_ptr(x), _dtype_code(x), T, D, _ld(x), _ptr(ids), _ptr(weights), top_k, E,
+                  _ptr(w13), w13.stride(1), w13.stride(0), _ptr(scale13), _ptr(w2),
+                  w2.stride(1), w2.stride(0), _ptr(scale2), F, _FORMATS[fmt],
+                  _ACTIVATIONS[activation], _ptr(y), _ld(y), _ptr(workspace), nbytes, _stream())
+    return y
 
 
 def device_status():

@@ -154,7 +154,7 @@ const char *fp8la_status_string(fp8la_status s) {
   }
 }
 
-int fp8la_version(void) { return 101; }
+int fp8la_version(void) { return 200; }
 
 fp8la_status fp8la_diag_withheld_arrival(
     int32_t kernel, const uint8_t *A, int64_t lda, const uint8_t *B,
