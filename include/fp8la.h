@@ -82,7 +82,7 @@ typedef int fp8la_status;
 #define FP8LA_ERR_DEVICE_ARG     -6  /* a kernel found a device-side argument it
                                         cannot use (m_offsets of fp8_grouped_gemm or
                                         fp8_quantize_pertensor_grouped, ids of
-                                        fp8_moe_layer) */
+                                        fp8_moe_layer, segments of fp8la_lora_*) */
 
 /*
  * Per-tensor E4M3 quantisation ([P1] risks paragraph: E4M3 spans +-448 and
@@ -381,6 +381,78 @@ FP8LA_API fp8la_status fp8_moe_layer(
     int64_t ld2, int64_t expert_stride2, const float *scale2, int64_t F,
     int32_t format, int32_t activation, uint16_t *y, int64_t ldy,
     void *workspace, int64_t workspace_bytes, fp8la_stream_t stream);
+
+/*
+ * Low-rank adapters of many requests beside a shared projection: adds every
+ * request's adapter to a projection that was computed for all of them at
+ * once (by fp8_gemm, say).  The rows come in segments; segment s, the rows
+ * m_offsets[s] .. m_offsets[s+1]-1, uses adapter i = adapter_ids[s]:
+ *
+ *   v[t]   = A_i x[t]                                  (fp32, rank values)
+ *   out[t] = bf16_rn( base[t] + alpha[i] * sum_j v[t][j] B_i[j] )
+ *
+ * Rows of a segment with id -1, and rows after the last segment, get
+ * out = base and v = 0.  Segments may be empty and may share an adapter.
+ * Both factors have the rank as the slow dimension; adapters of lower rank
+ * are padded with zero rows.
+ *
+ * base, out: bf16 [rows][ld] (out may be base, else they must not overlap);
+ * x: fp32 or bf16 (x_dtype) [rows][ldx]; A: bf16 [num_adapters][rank][lda],
+ * lda >= K; B: bf16 [num_adapters][rank][ldb], ldb >= N; adapters stride_a,
+ * stride_b elements apart; alpha: fp32 [num_adapters]; m_offsets: int32
+ * [num_segments + 1], starting at 0, non-decreasing, at most rows;
+ * adapter_ids: int32 [num_segments], -1 .. num_adapters-1.  v: fp32
+ * [rows][ldv], ldv >= rank, or NULL (the backward pass wants it).  All
+ * device; the host reads none of it.  Offsets or ids that break these rules
+ * make the call write no output and record FP8LA_ERR_DEVICE_ARG.
+ * fp32 operands enter the tensor cores as sums of bf16 terms: three (24
+ * significant bits) for v, two (16) for out; sums are fp32, in a fixed order.  Pointers need their
+ * type's alignment; 16-byte rows are read and written fastest.
+ * Limits (FP8LA_ERR_UNSUPPORTED): rank <= 128, num_segments <= 1024, rows
+ * <= 2^19, K and N <= 2^22, num_adapters <= 16383.  workspace:
+ * fp8la_lora_apply_workspace_bytes(...) bytes, 16-byte aligned.  Two
+ * launches.
+ */
+FP8LA_API int64_t fp8la_lora_apply_workspace_bytes(int64_t rows, int32_t num_segments,
+                                         int64_t K, int32_t rank);
+FP8LA_API fp8la_status fp8la_lora_apply(
+    const uint16_t *base, int64_t ld_base, const void *x, int32_t x_dtype,
+    int64_t ldx, int64_t rows, const uint16_t *A, int64_t lda,
+    int64_t stride_a, const uint16_t *B, int64_t ldb, int64_t stride_b,
+    const float *alpha, int32_t num_adapters, int32_t rank, int64_t K,
+    int64_t N, int32_t num_segments, const int32_t *m_offsets,
+    const int32_t *adapter_ids, uint16_t *out, int64_t ld_out, float *v,
+    int64_t ldv, void *workspace, int64_t workspace_bytes,
+    fp8la_stream_t stream);
+
+/*
+ * Backward pass of fp8la_lora_apply for the adapters and their input (the
+ * shared projection's own gradient with respect to x is dx_base, e.g. from
+ * fp8_gemm_ex on E5M2 gradients):
+ *
+ *   dv[t] = alpha[i] * B_i dy[t]
+ *   dx[t] = bf16_rn( dx_base[t] + sum_j dv[t][j] A_i[j] )
+ *   dA[i][j] = sum_t dv[t][j] x[t],   dB[i][j] = alpha[i] sum_t v[t][j] dy[t]
+ *
+ * summed over the rows of all segments with adapter i; adapters without rows
+ * get zero gradients.  dy: fp32 or bf16 [rows][ld_dy]; x and v as in the
+ * forward call; dx_base, dx: bf16 (dx may be dx_base); dA: fp32
+ * [num_adapters][rank][K] and dB: fp32 [num_adapters][rank][N], dense,
+ * overwritten.  Everything else, the limits, refusals and the rounding as
+ * for fp8la_lora_apply (dA and dB with three terms).  Three launches; results do not depend on timing.
+ */
+FP8LA_API int64_t fp8la_lora_backward_workspace_bytes(int64_t rows, int32_t num_segments,
+                                            int64_t N, int32_t rank);
+FP8LA_API fp8la_status fp8la_lora_backward(
+    const void *dy, int32_t dy_dtype, int64_t ld_dy, const void *x,
+    int32_t x_dtype, int64_t ldx, const float *v, int64_t ldv, int64_t rows,
+    const uint16_t *A, int64_t lda, int64_t stride_a, const uint16_t *B,
+    int64_t ldb, int64_t stride_b, const float *alpha, int32_t num_adapters,
+    int32_t rank, int64_t K, int64_t N, int32_t num_segments,
+    const int32_t *m_offsets, const int32_t *adapter_ids,
+    const uint16_t *dx_base, int64_t ld_dx_base, uint16_t *dx, int64_t ld_dx,
+    float *dA, float *dB, void *workspace, int64_t workspace_bytes,
+    fp8la_stream_t stream);
 
 /*
  * Synchronise `stream`, then read and clear the current device's status

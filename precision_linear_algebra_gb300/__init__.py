@@ -59,6 +59,14 @@ SIGNATURES = [
     ("fp8_moe_layer", _S,
      [_P, _I32, _I64, _I64, _I64, _P, _P, _I32, _I32, _P, _I64, _I64, _P, _P, _I64, _I64, _P,
       _I64, _I32, _I32, _P, _I64, _P, _I64, _P]),
+    ("fp8la_lora_apply_workspace_bytes", _I64, [_I64, _I32, _I64, _I32]),
+    ("fp8la_lora_apply", _S,
+     [_P, _I64, _P, _I32, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I32, _I32, _I64,
+      _I64, _I32, _P, _P, _P, _I64, _P, _I64, _P, _I64, _P]),
+    ("fp8la_lora_backward_workspace_bytes", _I64, [_I64, _I32, _I64, _I32]),
+    ("fp8la_lora_backward", _S,
+     [_P, _I32, _I64, _P, _I32, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I32,
+      _I32, _I64, _I64, _I32, _P, _P, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P]),
     ("fp8_get_device_status", _S, [_P]),
     ("fp8la_set_wait_timeout_ns", _S, [_I64]),
     ("fp8la_diag_gemm_withheld_arrival", _S, [_P, _I64, _P, _I64, _P, _I64, _P, _P, _P]),
@@ -188,6 +196,32 @@ def fp8_moe_layer(x, x_dtype, tokens, D, ldx, ids, weights, top_k, num_experts, 
     return _call("fp8_moe_layer", x, x_dtype, tokens, D, ldx, ids, weights, top_k, num_experts,
                  w13, ld13, expert_stride13, scale13, w2, ld2, expert_stride2, scale2, F, fmt,
                  activation, y, ldy, workspace, workspace_bytes, stream)
+
+
+def fp8la_lora_apply_workspace_bytes(rows, num_segments, K, rank):
+    return _bytes("fp8la_lora_apply_workspace_bytes", rows, num_segments, K, rank)
+
+
+def fp8la_lora_apply(base, ld_base, x, x_dtype, ldx, rows, A, lda, stride_a, B, ldb, stride_b,
+                     alpha, num_adapters, rank, K, N, num_segments, m_offsets, adapter_ids, out,
+                     ld_out, v, ldv, workspace, workspace_bytes, stream):
+    return _call("fp8la_lora_apply", base, ld_base, x, x_dtype, ldx, rows, A, lda, stride_a, B,
+                 ldb, stride_b, alpha, num_adapters, rank, K, N, num_segments, m_offsets,
+                 adapter_ids, out, ld_out, v, ldv, workspace, workspace_bytes, stream)
+
+
+def fp8la_lora_backward_workspace_bytes(rows, num_segments, N, rank):
+    return _bytes("fp8la_lora_backward_workspace_bytes", rows, num_segments, N, rank)
+
+
+def fp8la_lora_backward(dy, dy_dtype, ld_dy, x, x_dtype, ldx, v, ldv, rows, A, lda, stride_a, B,
+                        ldb, stride_b, alpha, num_adapters, rank, K, N, num_segments, m_offsets,
+                        adapter_ids, dx_base, ld_dx_base, dx, ld_dx, dA, dB, workspace,
+                        workspace_bytes, stream):
+    return _call("fp8la_lora_backward", dy, dy_dtype, ld_dy, x, x_dtype, ldx, v, ldv, rows, A,
+                 lda, stride_a, B, ldb, stride_b, alpha, num_adapters, rank, K, N, num_segments,
+                 m_offsets, adapter_ids, dx_base, ld_dx_base, dx, ld_dx, dA, dB, workspace,
+                 workspace_bytes, stream)
 
 
 def fp8_get_device_status(stream):
@@ -468,6 +502,84 @@ def moe_layer(x, ids, weights, w13, scale13, w2, scale2, y=None, workspace=None,
                   w2.stride(1), w2.stride(0), _ptr(scale2), F, _FORMATS[fmt],
                   _ACTIVATIONS[activation], _ptr(y), _ld(y), _ptr(workspace), nbytes, _stream())
     return y
+
+
+def _check_adapters(x, A, B, alpha, m_offsets, adapter_ids, N):
+    import torch
+    n, R, K = A.shape
+    assert x.dim() == 2 and x.shape[1] == K and x.stride(1) == 1
+    assert A.dtype == torch.bfloat16 and B.dtype == torch.bfloat16
+    assert B.shape == (n, R, N) and A.stride(2) == 1 and B.stride(2) == 1
+    assert alpha.dtype == torch.float32 and alpha.shape == (n,) and alpha.is_contiguous()
+    assert m_offsets.dtype == torch.int32 and adapter_ids.dtype == torch.int32
+    assert m_offsets.is_contiguous() and adapter_ids.is_contiguous()
+    assert m_offsets.numel() == adapter_ids.numel() + 1
+    return n, R, K
+
+
+def lora_apply(base, x, A, B, alpha, m_offsets, adapter_ids, out=None, v=None, workspace=None):
+    """Adds each request's low-rank adapter to a shared projection's output.
+
+    base bf16 [T][N] (e.g. from gemm), x fp32 or bf16 [T][K], A bf16 [n][R][K],
+    B bf16 [n][R][N], alpha fp32 [n]; segment s, the rows m_offsets[s] ..
+    m_offsets[s+1]-1 (int32 [S+1]), uses adapter adapter_ids[s] (int32 [S],
+    -1: none).  Returns (out bf16 [T][N] = base + alpha v B, v fp32 [T][R] =
+    x A^T); out may be base.  All CUDA; nothing is synchronised.
+    """
+    import torch
+    T, N = base.shape
+    n, R, K = _check_adapters(x, A, B, alpha, m_offsets, adapter_ids, N)
+    assert base.dtype == torch.bfloat16 and base.stride(1) == 1 and x.shape[0] == T
+    if out is None:
+        out = torch.empty((T, N), dtype=torch.bfloat16, device=x.device)
+    assert out.dtype == torch.bfloat16 and out.shape == (T, N) and out.stride(1) == 1
+    if v is None:
+        v = torch.empty((T, R), dtype=torch.float32, device=x.device)
+    assert v.dtype == torch.float32 and v.shape == (T, R) and v.stride(1) == 1
+    S = adapter_ids.numel()
+    workspace, nbytes = _workspace(workspace, fp8la_lora_apply_workspace_bytes(T, S, K, R),
+                                   x.device)
+    fp8la_lora_apply(_ptr(base), _ld(base), _ptr(x), _dtype_code(x), _ld(x), T, _ptr(A),
+                     A.stride(1), A.stride(0), _ptr(B), B.stride(1), B.stride(0), _ptr(alpha),
+                     n, R, K, N, S, _ptr(m_offsets), _ptr(adapter_ids), _ptr(out), _ld(out),
+                     _ptr(v), _ld(v), _ptr(workspace), nbytes, _stream())
+    return out, v
+
+
+def lora_backward(dy, x, v, A, B, alpha, m_offsets, adapter_ids, dx_base, dx=None, dA=None,
+                  dB=None, workspace=None):
+    """Backward pass of lora_apply.
+
+    dy fp32 or bf16 [T][N], v as lora_apply returned it, dx_base bf16 [T][K]
+    the shared projection's gradient with respect to x.  Returns (dx bf16
+    [T][K] = dx_base + dv A, dA fp32 [n][R][K], dB fp32 [n][R][N]); dx may be
+    dx_base.  All CUDA; nothing is synchronised.
+    """
+    import torch
+    T, N = dy.shape
+    n, R, K = _check_adapters(x, A, B, alpha, m_offsets, adapter_ids, N)
+    assert dy.stride(1) == 1 and x.shape[0] == T
+    assert dx_base.dtype == torch.bfloat16 and dx_base.shape == (T, K)
+    assert dx_base.stride(1) == 1
+    assert v.dtype == torch.float32 and v.shape == (T, R) and v.stride(1) == 1
+    if dx is None:
+        dx = torch.empty((T, K), dtype=torch.bfloat16, device=x.device)
+    assert dx.dtype == torch.bfloat16 and dx.shape == (T, K) and dx.stride(1) == 1
+    if dA is None:
+        dA = torch.empty((n, R, K), dtype=torch.float32, device=x.device)
+    if dB is None:
+        dB = torch.empty((n, R, N), dtype=torch.float32, device=x.device)
+    assert dA.dtype == torch.float32 and dA.shape == (n, R, K) and dA.is_contiguous()
+    assert dB.dtype == torch.float32 and dB.shape == (n, R, N) and dB.is_contiguous()
+    S = adapter_ids.numel()
+    workspace, nbytes = _workspace(workspace, fp8la_lora_backward_workspace_bytes(T, S, N, R),
+                                   x.device)
+    fp8la_lora_backward(_ptr(dy), _dtype_code(dy), _ld(dy), _ptr(x), _dtype_code(x), _ld(x),
+                        _ptr(v), _ld(v), T, _ptr(A), A.stride(1), A.stride(0), _ptr(B),
+                        B.stride(1), B.stride(0), _ptr(alpha), n, R, K, N, S, _ptr(m_offsets),
+                        _ptr(adapter_ids), _ptr(dx_base), _ld(dx_base), _ptr(dx), _ld(dx),
+                        _ptr(dA), _ptr(dB), _ptr(workspace), nbytes, _stream())
+    return dx, dA, dB
 
 
 def device_status():

@@ -1,16 +1,17 @@
 """GPU: the router and the few-token mixture-of-experts layer against their
 definitions in 64 bits.
 
-Bounds of the layer, from its roundings (u = 2^-9 is half a BF16 step):
-* an activation enters as two E4M3 terms, 8 significant bits: relative error
-  at most u, none for a BF16 value above 2^-15 of its K slice's largest, and
-  an absolute error of at most 2^-22 of the slice's largest;
-* h takes the same path, y is rounded once to BF16 (u).
+Bounds of the layer, from its roundings:
+* an activation enters as two E4M3 terms: relative error at most 2^-9 (half a
+  step of 2^-3, twice, the second on a remainder that is at most half of its
+  binade), none for a BF16 value above 2^-15 of its K slice's largest, and an
+  absolute error of at most 2^-22 of the slice's largest;
+* h takes the same path, y is rounded once to BF16 (2^-8).
 Elementwise the errors are propagated through |W| (worst case, with the
 library's 2^-22 K max|a| max|b| for the FP32 accumulation).  That grows like K
 where real errors grow like sqrt(K), so the norm is bounded too: independent
-relative errors of at most u each give at most u in the norm of the result,
-u for each of the roundings (x if FP32, h, y)."""
+relative errors give at most themselves in the norm of the result, 2^-8 for y
+and 2^-9 for each of x (if FP32) and h."""
 
 import math
 
@@ -142,7 +143,7 @@ def make_layer(T, E, k, D, F, dtype="bfloat16", fmt="e4m3", seed=0, ldpad=0):
 
 
 def layer_ref(c, activation):
-    """(y, elementwise bound), fp64, and the number of 8-bit roundings."""
+    """(y, elementwise bound), fp64, and the bound in the norm."""
     import torch
     ft = getattr(torch, FP8[c["fmt"]][0])
     x, ids, w = c["x"].double(), c["ids"].cpu(), c["weights"].double()
@@ -180,7 +181,7 @@ def layer_ref(c, activation):
         b.index_add_(0, tok, we.abs() * dy)
     # the last term: half of BF16's smallest number, where y underflows
     b = b + 2.0 ** -8 * (y.abs() + b) + 2.0 ** -134
-    return y, b, 3 if xr else 2
+    return y, b, 2.0 ** -8 + 2.0 ** -9 * (2 if xr else 1)
 
 
 def check_layer(fl, c, activation="silu", **kw):
@@ -188,14 +189,14 @@ def check_layer(fl, c, activation="silu", **kw):
     y = fl.moe_layer(activation=activation, **c, **kw)
     torch.cuda.synchronize()
     assert fl.device_status() == 0
-    ref, bound, n = layer_ref(c, activation)
+    ref, bound, rel = layer_ref(c, activation)
     err = (y.double() - ref).abs()
     assert torch.isfinite(y.float()).all()
     bad = ~(err <= bound)
     assert not bad.any(), "%d of %d outside the bound, worst ratio %g" % (
         bad.sum(), bad.numel(), (err / bound)[bad].max())
     floor = 2.0 ** -134 * math.sqrt(err.numel())
-    assert err.norm() <= n * 2.0 ** -9 * ref.norm() + floor, (err.norm() / ref.norm()).item()
+    assert err.norm() <= rel * ref.norm() + floor, (err.norm() / ref.norm()).item()
     return y
 
 
