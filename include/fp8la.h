@@ -344,8 +344,8 @@ FP8LA_API fp8la_status fp8_moe_route(const void *logits, int32_t dtype, int64_t 
 #define FP8LA_ACT_GELU_TANH 1  /* g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
 
 /*
- * Mixture-of-experts layer for up to 128 tokens, all of it in two launches,
- * with FP8 weights and full-precision activations:
+ * Mixture-of-experts layer for up to 128 tokens, all of it in four
+ * launches, with FP8 weights and full-precision activations:
  *
  *   [g; u] = scale13[e] * dec(W13[e]) x_t        (rows 0..F-1 are g)
  *   h      = act(g) * u
@@ -353,10 +353,10 @@ FP8LA_API fp8la_status fp8_moe_route(const void *logits, int32_t dtype, int64_t 
  *            e_j = ids[t][j], slots with id -1 left out
  *
  * Sums are FP32.  x and h enter the tensor cores as the sum of two E4M3
- * values under a power-of-two scale per 256 or 512 elements: 8 significant
- * bits, which is exact for bf16 x except for elements below 2^-15 of their
- * neighbourhood's largest, and for fp32 x and for h no worse than a rounding
- * to bf16.  A token whose x holds an infinity or NaN gets a NaN row.  Tokens
+ * values under a power-of-two scale (of a token, or of 128 elements of h): 8
+ * significant bits, which is exact for bf16 x except for elements below 2^-15
+ * of the token's largest, and for fp32 x and for h no worse than a rounding to
+ * bf16.  A token whose x holds an infinity or NaN gets a NaN row.  Tokens
  * with no expert get a zero row.  The result does not depend on timing.
  *
  * x: fp32 or bf16 [tokens][ldx]; ids: int32, weights: fp32 [tokens][top_k]
@@ -367,12 +367,13 @@ FP8LA_API fp8la_status fp8_moe_route(const void *logits, int32_t dtype, int64_t 
  * apart; 16-byte aligned, with ld13, ld2 and the strides multiples of 16.
  * scale13, scale2: fp32 [E].  y: bf16 [tokens][ldy].  All device.  Limits
  * (FP8LA_ERR_UNSUPPORTED): tokens <= 128, top_k <= 16, E <= 1024, D and F
- * <= 2^20.  workspace: fp8_moe_layer_workspace_bytes(tokens, top_k, D, F)
- * bytes, 16-byte aligned; it keeps nothing between calls, but calls that may
+ * <= 2^20.  workspace: fp8_moe_layer_workspace_bytes(tokens, top_k, E, D,
+ * F) bytes, 16-byte aligned; it keeps nothing between calls, but calls that may
  * run at the same time need one each.
  */
 FP8LA_API int64_t fp8_moe_layer_workspace_bytes(int64_t tokens, int32_t top_k,
-                                      int64_t D, int64_t F);
+                                      int32_t num_experts, int64_t D,
+                                      int64_t F);
 FP8LA_API fp8la_status fp8_moe_layer(
     const void *x, int32_t x_dtype, int64_t tokens, int64_t D, int64_t ldx,
     const int32_t *ids, const float *weights, int32_t top_k,

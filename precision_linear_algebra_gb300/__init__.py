@@ -55,7 +55,7 @@ SIGNATURES = [
     ("fp8_moe_route_workspace_bytes", _I64, [_I64, _I32]),
     ("fp8_moe_route", _S,
      [_P, _I32, _I64, _I32, _I64, _I32, _I32, _P, _P, _P, _P, _P, _I64, _P]),
-    ("fp8_moe_layer_workspace_bytes", _I64, [_I64, _I32, _I64, _I64]),
+    ("fp8_moe_layer_workspace_bytes", _I64, [_I64, _I32, _I32, _I64, _I64]),
     ("fp8_moe_layer", _S,
      [_P, _I32, _I64, _I64, _I64, _P, _P, _I32, _I32, _P, _I64, _I64, _P, _P, _I64, _I64, _P,
       _I64, _I32, _I32, _P, _I64, _P, _I64, _P]),
@@ -186,8 +186,8 @@ def fp8_moe_route(logits, dtype, tokens, num_experts, ld, top_k, renormalise, id
                  ids, weights, m_offsets, order, workspace, workspace_bytes, stream)
 
 
-def fp8_moe_layer_workspace_bytes(tokens, top_k, D, F):
-    return _bytes("fp8_moe_layer_workspace_bytes", tokens, top_k, D, F)
+def fp8_moe_layer_workspace_bytes(tokens, top_k, num_experts, D, F):
+    return _bytes("fp8_moe_layer_workspace_bytes", tokens, top_k, num_experts, D, F)
 
 
 def fp8_moe_layer(x, x_dtype, tokens, D, ldx, ids, weights, top_k, num_experts, w13, ld13,
@@ -495,8 +495,8 @@ def moe_layer(x, ids, weights, w13, scale13, w2, scale2, y=None, workspace=None,
     if y is None:
         y = torch.empty((T, D), dtype=torch.bfloat16, device=x.device)
     assert y.dtype == torch.bfloat16 and y.shape == (T, D) and y.stride(1) == 1
-    workspace, nbytes = _workspace(workspace, fp8_moe_layer_workspace_bytes(T, top_k, D, F),
-                                   x.device)
+    workspace, nbytes = _workspace(workspace,
+                                   fp8_moe_layer_workspace_bytes(T, top_k, E, D, F), x.device)
     fp8_moe_layer(_ptr(x), _dtype_code(x), T, D, _ld(x), _ptr(ids), _ptr(weights), top_k, E,
                   _ptr(w13), w13.stride(1), w13.stride(0), _ptr(scale13), _ptr(w2),
                   w2.stride(1), w2.stride(0), _ptr(scale2), F, _FORMATS[fmt],

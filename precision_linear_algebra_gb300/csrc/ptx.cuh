@@ -126,6 +126,17 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap,
       : "memory");
 }
 
+// Untiled copy of `bytes` bytes (a multiple of 16, both addresses 16-byte
+// aligned) into shared memory, signalled on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src,
+                                          uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
+      "[%1], %2, [%3];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
 // TMA store of a 2-D box from shared memory (bulk-group completion).  The
 // innermost coordinate times the element size must be a multiple of 16
 // bytes; elements outside the tensor are not written.

@@ -323,7 +323,7 @@ def test_layer_streams_graph_and_workspace():
     fl = lib()
     c = make_layer(9, 8, 2, 256, 192)
     want = fl.moe_layer(**c)
-    ws = torch.full((fl.fp8_moe_layer_workspace_bytes(9, 2, 256, 192),), 0xFF,
+    ws = torch.full((fl.fp8_moe_layer_workspace_bytes(9, 2, 8, 256, 192),), 0xFF,
                     dtype=torch.uint8, device="cuda")
     y = torch.zeros_like(want)
     s = torch.cuda.Stream()
