@@ -260,8 +260,10 @@ def fp8la_version():
 
 # ------------------------------------------------------ torch conveniences
 def _stream():
+    """The current stream's handle, without building a torch.cuda.Stream (3 us
+    of the 4 us that a small launch takes)."""
     import torch
-    return torch.cuda.current_stream().cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _ptr(t):
@@ -417,8 +419,19 @@ def grouped_gemm(m_offsets, A, B, scale_a, scale_b, C=None):
 
 def _dtype_code(t):
     import torch
-    assert t.dtype in (torch.float32, torch.bfloat16)
-    return FP8LA_TYPE_BF16 if t.dtype == torch.bfloat16 else FP8LA_TYPE_F32
+    dt = t.dtype
+    assert dt == torch.bfloat16 or dt == torch.float32
+    return FP8LA_TYPE_BF16 if dt == torch.bfloat16 else FP8LA_TYPE_F32
+
+
+def _out(t, shape, dtype, device, dense=True):
+    """An output: the caller's tensor, checked, or a new one."""
+    import torch
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    assert t.dtype == dtype and t.shape == shape
+    assert t.is_contiguous() if dense else t.stride(-1) == 1
+    return t
 
 
 def _workspace(workspace, need, device):
@@ -427,7 +440,7 @@ def _workspace(workspace, need, device):
     if need == 0:
         return None, 0
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        return torch.empty(need, dtype=torch.uint8, device=device), need
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -445,22 +458,12 @@ def moe_route(logits, top_k, renormalise=True, sort=True, ids=None, weights=None
     assert logits.dim() == 2 and logits.stride(1) == 1
     T, E = logits.shape
     dev = logits.device
-    if ids is None:
-        ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-    if weights is None:
-        weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
-    assert ids.dtype == torch.int32 and ids.shape == (T, top_k) and ids.is_contiguous()
-    assert (weights.dtype == torch.float32 and weights.shape == (T, top_k)
-            and weights.is_contiguous())
+    ids = _out(ids, (T, top_k), torch.int32, dev)
+    weights = _out(weights, (T, top_k), torch.float32, dev)
     nbytes = 0
     if sort:
-        if m_offsets is None:
-            m_offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
-        if order is None:
-            order = torch.empty(T * top_k, dtype=torch.int32, device=dev)
-        assert m_offsets.dtype == torch.int32 and m_offsets.shape == (E + 1,)
-        assert order.dtype == torch.int32 and order.shape == (T * top_k,)
-        assert m_offsets.is_contiguous() and order.is_contiguous()
+        m_offsets = _out(m_offsets, (E + 1,), torch.int32, dev)
+        order = _out(order, (T * top_k,), torch.int32, dev)
         workspace, nbytes = _workspace(workspace, fp8_moe_route_workspace_bytes(T, E), dev)
     else:
         m_offsets = order = workspace = None
@@ -492,9 +495,7 @@ def moe_layer(x, ids, weights, w13, scale13, w2, scale2, y=None, workspace=None,
             and weights.is_contiguous())
     assert scale13.dtype == torch.float32 and scale13.numel() == E and scale13.is_contiguous()
     assert scale2.dtype == torch.float32 and scale2.numel() == E and scale2.is_contiguous()
-    if y is None:
-        y = torch.empty((T, D), dtype=torch.bfloat16, device=x.device)
-    assert y.dtype == torch.bfloat16 and y.shape == (T, D) and y.stride(1) == 1
+    y = _out(y, (T, D), torch.bfloat16, x.device, dense=False)
     workspace, nbytes = _workspace(workspace,
                                    fp8_moe_layer_workspace_bytes(T, top_k, E, D, F), x.device)
     fp8_moe_layer(_ptr(x), _dtype_code(x), T, D, _ld(x), _ptr(ids), _ptr(weights), top_k, E,
@@ -530,12 +531,8 @@ def lora_apply(base, x, A, B, alpha, m_offsets, adapter_ids, out=None, v=None, w
     T, N = base.shape
     n, R, K = _check_adapters(x, A, B, alpha, m_offsets, adapter_ids, N)
     assert base.dtype == torch.bfloat16 and base.stride(1) == 1 and x.shape[0] == T
-    if out is None:
-        out = torch.empty((T, N), dtype=torch.bfloat16, device=x.device)
-    assert out.dtype == torch.bfloat16 and out.shape == (T, N) and out.stride(1) == 1
-    if v is None:
-        v = torch.empty((T, R), dtype=torch.float32, device=x.device)
-    assert v.dtype == torch.float32 and v.shape == (T, R) and v.stride(1) == 1
+    out = _out(out, (T, N), torch.bfloat16, x.device, dense=False)
+    v = _out(v, (T, R), torch.float32, x.device, dense=False)
     S = adapter_ids.numel()
     workspace, nbytes = _workspace(workspace, fp8la_lora_apply_workspace_bytes(T, S, K, R),
                                    x.device)
@@ -562,15 +559,9 @@ def lora_backward(dy, x, v, A, B, alpha, m_offsets, adapter_ids, dx_base, dx=Non
     assert dx_base.dtype == torch.bfloat16 and dx_base.shape == (T, K)
     assert dx_base.stride(1) == 1
     assert v.dtype == torch.float32 and v.shape == (T, R) and v.stride(1) == 1
-    if dx is None:
-        dx = torch.empty((T, K), dtype=torch.bfloat16, device=x.device)
-    assert dx.dtype == torch.bfloat16 and dx.shape == (T, K) and dx.stride(1) == 1
-    if dA is None:
-        dA = torch.empty((n, R, K), dtype=torch.float32, device=x.device)
-    if dB is None:
-        dB = torch.empty((n, R, N), dtype=torch.float32, device=x.device)
-    assert dA.dtype == torch.float32 and dA.shape == (n, R, K) and dA.is_contiguous()
-    assert dB.dtype == torch.float32 and dB.shape == (n, R, N) and dB.is_contiguous()
+    dx = _out(dx, (T, K), torch.bfloat16, x.device, dense=False)
+    dA = _out(dA, (n, R, K), torch.float32, x.device)
+    dB = _out(dB, (n, R, N), torch.float32, x.device)
     S = adapter_ids.numel()
     workspace, nbytes = _workspace(workspace, fp8la_lora_backward_workspace_bytes(T, S, N, R),
                                    x.device)

@@ -60,8 +60,10 @@ constexpr int kABytes = 2 * BM * BK;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTokens = 128;
 constexpr int kMaxTopK = 16;
-constexpr int kMaxPairs = kMaxTokens * kMaxTopK;
 constexpr int kSlack = 64;          // positions past the last pair that are read
+
+// Starts: three 16-bit words for each expert, and warp sums.
+constexpr int kStartsBytes = kMaxExperts * 6 + 256;
 
 // TT: most tokens of a tile.
 template <int TT>
@@ -74,12 +76,14 @@ struct Cfg {
   static constexpr int kB = kA + STAGES * kABytes;
   static constexpr int kScale = kB + STAGES * kBBytes;
   static constexpr int kTop = kScale + STAGES * kScaleBytes;  // [4][TT] words
-  static constexpr int kBar = kTop + 4 * TT * 4;
+  static constexpr int kStarts = kTop + 4 * TT * 4;      // gate/up: Starts
+  static constexpr int kBar = kStarts + kStartsBytes;
   static constexpr int kNumBars = 2 * STAGES + 6;
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kEnd = kMisc + 32;
   static constexpr int kAlloc = kEnd + 1024;
   static_assert(kB % 1024 == 0 && kBBytes % 1024 == 0, "swizzle atoms");
+  static_assert(kMaxExperts * 4 <= STAGES * kBBytes, "the starts' counters");
   static_assert(kScale % 16 == 0 && kBar % 8 == 0, "alignment");
   static_assert(kAlloc <= 227 * 1024, "shared memory");
 };
@@ -189,230 +193,204 @@ __device__ __forceinline__ float activate(float g, int gelu) {
     const float t = tanhf(0.7978845608028654f * (g + 0.044715f * g * g * g));
     return 0.5f * g * (1.0f + t);
   }
-  return g / (1.0f + __expf(-g));
+  return __fdividef(g, 1.0f + __expf(-g));
 }
 
 // 16 elements of a token from d on, as loaded (BF16: the first 8 words), and
 // their values.
+template <bool F32>
 __device__ __forceinline__ void load_x16(const LayerArgs &a, int t, int d,
                                          uint32_t (&w)[16]) {
   const int64_t at = static_cast<int64_t>(t) * a.ldx + d;
-  if (a.x_bf16) {
-    const uint16_t *p = static_cast<const uint16_t *>(a.x) + at;
-    if (a.x_vec && d + 16 <= a.D) {
+  if (a.x_vec && d + 16 <= a.D) {
+    const uint4 *p = reinterpret_cast<const uint4 *>(
+        static_cast<const char *>(a.x) + at * (F32 ? 4 : 2));
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint4 v = *(reinterpret_cast<const uint4 *>(p) + i);
-        w[4 * i] = v.x;
-        w[4 * i + 1] = v.y;
-        w[4 * i + 2] = v.z;
-        w[4 * i + 3] = v.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        w[i] = (d + 2 * i < a.D ? p[2 * i] : 0) |
-               (d + 2 * i + 1 < a.D ? p[2 * i + 1] : 0) << 16;
+    for (int i = 0; i < (F32 ? 4 : 2); ++i) {
+      const uint4 v = p[i];
+      w[4 * i] = v.x;
+      w[4 * i + 1] = v.y;
+      w[4 * i + 2] = v.z;
+      w[4 * i + 3] = v.w;
     }
+  } else if (F32) {
+    const uint32_t *p = static_cast<const uint32_t *>(a.x) + at;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = d + i < a.D ? p[i] : 0;
   } else {
-    const float *p = static_cast<const float *>(a.x) + at;
-    if (a.x_vec && d + 16 <= a.D) {
+    const uint16_t *p = static_cast<const uint16_t *>(a.x) + at;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 v = *(reinterpret_cast<const uint4 *>(p) + i);
-        w[4 * i] = v.x;
-        w[4 * i + 1] = v.y;
-        w[4 * i + 2] = v.z;
-        w[4 * i + 3] = v.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) w[i] = d + i < a.D ? __float_as_uint(p[i]) : 0;
-    }
+    for (int i = 0; i < 8; ++i)
+      w[i] = (d + 2 * i < a.D ? p[2 * i] : 0) |
+             (d + 2 * i + 1 < a.D ? p[2 * i + 1] : 0) << 16;
   }
 }
-__device__ __forceinline__ float x_value(const uint32_t (&w)[16], int bf16, int i) {
-  return __uint_as_float(
-      !bf16 ? w[i] : i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+template <bool F32>
+__device__ __forceinline__ float x_value(const uint32_t (&w)[16], int i) {
+  return __uint_as_float(F32     ? w[i]
+                         : i & 1 ? w[i >> 1] & 0xffff0000u
+                                 : w[i >> 1] << 16);
 }
 
-// ------------------------------------------------------------------ prepare
-// Every CTA sorts the pairs by itself (places come from counts, so all CTAs
-// agree); the first one writes the plan, and all of them share out the tokens.
-template <int TT>
-__global__ void __launch_bounds__(kPrepThreads)
-    moe_prepare_kernel(const LayerArgs a) {
-  __shared__ uint16_t by_warp[kPrepWarps][kMaxExperts];
-  __shared__ uint16_t first_pos[kMaxExperts], first_tile[kMaxExperts];
-  __shared__ int16_t pos_of[kMaxPairs];
-  __shared__ int warp_sums[2][kPrepWarps];
-  __shared__ uint32_t tops[kPrepWarps];
+// Where each expert's pairs and tiles begin, by a whole CTA.
+struct Starts {
+  uint16_t count[kMaxExperts], first_pos[kMaxExperts], first_tile[kMaxExperts];
+  int warp_sums[2][32];
+};
+
+// Counts the pairs of each expert and fills *s; returns the number of tiles,
+// -1 if an id is out of range.  counter: kMaxExperts words of shared memory,
+// free for TMA to write afterwards.  Ends with a barrier.
+template <int TT, int THREADS>
+__device__ __forceinline__ int find_starts(const LayerArgs &a, Starts *s,
+                                           uint32_t *counter) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int pairs = a.T * a.k;
-  const int groups = (pairs + 31) / 32;
-  const int plan_warps = min(kPrepWarps, groups);
-  for (int w = 0; w < plan_warps; ++w)
-    for (int e = threadIdx.x; e < a.E; e += kPrepThreads) by_warp[w][e] = 0;
+  for (int e = threadIdx.x; e < a.E; e += THREADS) counter[e] = 0;
   __syncthreads();
-  pdl_wait();
-  pdl_launch_dependents();
-  // The first token's x is on its way while the plan is made.
-  constexpr int kRound = 16 * kPrepThreads;
-  uint32_t xw[16];
-  if (16 * threadIdx.x < a.D) load_x16(a, blockIdx.x, 16 * threadIdx.x, xw);
   bool bad = false;
-  const int g_lo = warp < plan_warps ? groups * warp / plan_warps : 0;
-  const int g_hi = warp < plan_warps ? groups * (warp + 1) / plan_warps : 0;
-  for (int gr = g_lo; gr < g_hi; ++gr) {
-    const int p = 32 * gr + lane;
-    int id = p < pairs ? a.ids[p] : -1;
-    if (id < -1 || id >= a.E) {
-      bad = true;
-      id = -1;
-    }
-    const uint32_t same = __match_any_sync(0xffffffffu, id);
-    if (id >= 0 && (same & ((1u << lane) - 1u)) == 0)
-      by_warp[warp][id] = static_cast<uint16_t>(by_warp[warp][id] + __popc(same));
-    __syncwarp();
+  const int pairs = a.T * a.k;
+  for (int p = threadIdx.x; p < pairs; p += THREADS) {
+    const int id = __ldcg(a.ids + p);
+    if (id >= 0 && id < a.E) atomicAdd(&counter[id], 1u);
+    else bad |= id != -1;
   }
-  bad = __syncthreads_or(bad);
-  // Scan over the experts: pairs (low half) and tiles (high half) in one word,
-  // padded positions in another.
-  constexpr int kPer = kMaxExperts / kPrepThreads;
-  int c[kPer], sum = 0, padded = 0;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int e = threadIdx.x * kPer + i;
-    c[i] = 0;
-    if (e < a.E)
-      for (int w = 0; w < plan_warps; ++w) c[i] += by_warp[w][e];
-    sum += c[i] | ((c[i] + TT - 1) / TT) << 16;
-    padded += (c[i] + 3) & ~3;
+  if (__syncthreads_or(bad)) return -1;
+  // A thread has `per` consecutive experts.  Pairs (low half) and tiles (high
+  // half) are scanned in one word, padded positions in another.
+  const int per = (a.E + THREADS - 1) / THREADS;
+  const int e0 = threadIdx.x * per, e1 = min(e0 + per, a.E);
+  int tiles = 0, padded = 0;
+  for (int e = e0; e < e1; ++e) {
+    const int n = static_cast<int>(counter[e]);
+    tiles += (n + TT - 1) / TT;
+    padded += (n + 3) & ~3;
   }
-  int incl = sum, pincl = padded;
+  int t_incl = tiles, p_incl = padded;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int o = __shfl_up_sync(0xffffffffu, incl, d);
-    const int q = __shfl_up_sync(0xffffffffu, pincl, d);
+    const int t = __shfl_up_sync(0xffffffffu, t_incl, d);
+    const int q = __shfl_up_sync(0xffffffffu, p_incl, d);
     if (lane >= d) {
-      incl += o;
-      pincl += q;
+      t_incl += t;
+      p_incl += q;
     }
   }
   if (lane == 31) {
-    warp_sums[0][warp] = incl;
-    warp_sums[1][warp] = pincl;
+    s->warp_sums[0][warp] = t_incl;
+    s->warp_sums[1][warp] = p_incl;
   }
   __syncthreads();
-  int at = incl - sum, pat = pincl - padded, all = 0;
-#pragma unroll
-  for (int w = 0; w < kPrepWarps; ++w) {
-    const int v = warp_sums[0][w];
+  int t_at = t_incl - tiles, p_at = p_incl - padded, all = 0;
+  for (int w = 0; w < THREADS / 32; ++w) {
+    const int v = s->warp_sums[0][w];
     if (w < warp) {
-      at += v;
-      pat += warp_sums[1][w];
+      t_at += v;
+      p_at += s->warp_sums[1][w];
     }
     all += v;
   }
-  const int n_tiles = bad ? 0 : all >> 16;
-  const bool first_cta = blockIdx.x == 0;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int e = threadIdx.x * kPer + i;
-    if (e < a.E && c[i] > 0) {
-      // From here on: where each warp's next pair of the expert goes, its
-      // first position and its first tile.
-      int next = 0;
-      for (int w = 0; w < plan_warps; ++w) {
-        const int n = by_warp[w][e];
-        by_warp[w][e] = static_cast<uint16_t>(next);
-        next += n;
-      }
-      first_pos[e] = static_cast<uint16_t>(pat);
-      first_tile[e] = static_cast<uint16_t>(at >> 16);
-      if (first_cta && !bad) {
-        int t = at >> 16;
-        for (int done = 0; done < c[i]; done += TT, ++t)
-          a.p.tiles[t] = {e, pat + done, min(TT, c[i] - done), 0};
-      }
-    }
-    at += c[i] | ((c[i] + TT - 1) / TT) << 16;
-    pat += (c[i] + 3) & ~3;
+  for (int e = e0; e < e1; ++e) {
+    const int n = static_cast<int>(counter[e]);
+    s->count[e] = static_cast<uint16_t>(n);
+    s->first_pos[e] = static_cast<uint16_t>(p_at);
+    s->first_tile[e] = static_cast<uint16_t>(t_at);
+    t_at += (n + TT - 1) / TT;
+    p_at += (n + 3) & ~3;
   }
+  fence_proxy_async_smem();
   __syncthreads();
-  for (int gr = g_lo; gr < g_hi; ++gr) {
-    const int p = 32 * gr + lane;
-    const int id = p < pairs && !bad ? a.ids[p] : -1;
-    const uint32_t same = __match_any_sync(0xffffffffu, id);
-    const int rank = __popc(same & ((1u << lane) - 1u));
-    int pos = -1, tile = 0;
-    if (id >= 0) {
-      const int place = by_warp[warp][id] + rank;
-      pos = first_pos[id] + place;
-      tile = first_tile[id] + place / TT;
-    }
-    if (p < pairs) {
-      pos_of[p] = static_cast<int16_t>(pos);
-      if (first_cta) {
-        a.p.pos[p] = pos;
-        a.p.tile_of[p] = tile;
-      }
-    }
-    __syncwarp();
-    if (id >= 0 && rank == 0)
-      by_warp[warp][id] = static_cast<uint16_t>(by_warp[warp][id] + __popc(same));
-    __syncwarp();
+  return all;
+}
+
+static_assert(sizeof(Starts) == kStartsBytes, "shared memory");
+
+template <int TT>
+__device__ __forceinline__ Tile tile_of_expert(const Starts *s, int e, int tile) {
+  const int done = (tile - s->first_tile[e]) * TT;
+  return {e, s->first_pos[e] + done, min(TT, s->count[e] - done), 0};
+}
+
+// ------------------------------------------------------------------ prepare
+// One CTA for each token.  It finds the starts by itself (counts do not depend
+// on order) and the places of its own pairs: the rank of a pair in its expert
+// is the number of earlier pairs with the same id.
+template <int TT, bool F32>
+__global__ void __launch_bounds__(kPrepThreads)
+    moe_prepare_kernel(const LayerArgs a) {
+  __shared__ Starts s;
+  __shared__ uint32_t counter[kMaxExperts];
+  __shared__ int pos_of[kMaxTopK];
+  __shared__ uint32_t tops[kPrepWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = blockIdx.x;
+  pdl_wait();
+  pdl_launch_dependents();
+  constexpr int kRound = 16 * kPrepThreads;
+  uint32_t xw[16], top = 0;
+  for (int d = 16 * threadIdx.x; d < a.D; d += kRound) {
+    load_x16<F32>(a, t, d, xw);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      top = max(top, __float_as_uint(x_value<F32>(xw, i)) & 0x7fffffffu);
   }
-  if (first_cta && threadIdx.x == 0) {
-    *a.p.n_tiles = bad ? -1 : n_tiles;
-    if (bad) atomicOr(a.status, kStatusBadDeviceArg);
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (lane == 0) tops[warp] = top;
+  const int n_tiles = find_starts<TT, kPrepThreads>(a, &s, counter);
+  if (t == 0 && threadIdx.x == 0) {
+    *a.p.n_tiles = n_tiles;
+    if (n_tiles < 0) atomicOr(a.status, kStatusBadDeviceArg);
   }
+  if (n_tiles < 0) return;
+  if (t == 0)
+    for (int e = threadIdx.x; e < a.E; e += kPrepThreads)
+      for (int i = s.first_tile[e], n = (s.count[e] + TT - 1) / TT; n > 0; --n, ++i)
+        a.p.tiles[i] = tile_of_expert<TT>(&s, e, i);
   const int cells = n_tiles * ((a.F + BM - 1) / BM);
-  for (int i = blockIdx.x * kPrepThreads + threadIdx.x; i < cells;
-       i += gridDim.x * kPrepThreads)
+  for (int i = t * kPrepThreads + threadIdx.x; i < cells; i += gridDim.x * kPrepThreads)
     a.p.arrived[i] = 0;
 
-  // Codes of x: each token's once, written to the rows of all its pairs.
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
-    uint32_t top = 0;
-    for (int d = 16 * threadIdx.x; d < a.D; d += kRound) {
-      if (t != blockIdx.x || d >= kRound) load_x16(a, t, d, xw);
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        top = max(top, __float_as_uint(x_value(xw, a.x_bf16, i)) & 0x7fffffffu);
+  for (int w = 0; w < kPrepWarps; ++w) top = max(top, tops[w]);
+  float inv, scale;
+  group_scale(top, inv, scale);
+  for (int j = warp; j < a.k; j += kPrepWarps) {
+    const int pair = t * a.k + j;
+    const int id = __ldcg(a.ids + pair);
+    int rank = 0;
+    for (int p = lane; p < pair; p += 32) rank += __ldcg(a.ids + p) == id;
+    rank = __reduce_add_sync(0xffffffffu, rank);
+    if (lane == 0) {
+      const int pos = id < 0 ? -1 : s.first_pos[id] + rank;
+      pos_of[j] = pos;
+      a.p.pos[pair] = pos;
+      if (id >= 0) {
+        a.p.tile_of[pair] = s.first_tile[id] + rank / TT;
+        a.p.xs[pos] = scale;
+      }
     }
-    top = __reduce_max_sync(0xffffffffu, top);
-    __syncthreads();  // of pos_of too, in the first round
-    if (lane == 0) tops[warp] = top;
-    __syncthreads();
+  }
+  __syncthreads();
+  // The token's codes, to the rows of all its pairs.  What lies between D and
+  // a row's padded end becomes zeros.
+  for (int d = 16 * threadIdx.x; d < a.D; d += kRound) {
+    if (a.D > kRound) load_x16<F32>(a, t, d, xw);
+    uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int w = 0; w < kPrepWarps; ++w) top = max(top, tops[w]);
-    float inv, scale;
-    group_scale(top, inv, scale);
-    if (threadIdx.x < a.k && pos_of[t * a.k + threadIdx.x] >= 0)
-      a.p.xs[pos_of[t * a.k + threadIdx.x]] = scale;
-    for (int d = 16 * threadIdx.x; d < a.D; d += kRound) {
-      if (t != blockIdx.x || a.D > kRound) load_x16(a, t, d, xw);
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t h0, h1, l0, l1;
-        split_codes(x_value(xw, a.x_bf16, 4 * i) * inv,
-                    x_value(xw, a.x_bf16, 4 * i + 1) * inv, h0, l0);
-        split_codes(x_value(xw, a.x_bf16, 4 * i + 2) * inv,
-                    x_value(xw, a.x_bf16, 4 * i + 3) * inv, h1, l1);
-        hi[i] = h0 | h1 << 16;
-        lo[i] = l0 | l1 << 16;
-      }
-      for (int j = 0; j < a.k; ++j) {
-        const int pos = pos_of[t * a.k + j];
-        if (pos < 0) continue;
-        // A row's codes past D, up to its padded end, are zeros.
-        uint8_t *row = a.p.xc + static_cast<int64_t>(pos) * a.Dc + d;
-        *reinterpret_cast<uint4 *>(row) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4 *>(row + static_cast<int64_t>(a.P) * a.Dc) =
-            make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      }
+    for (int i = 0; i < 4; ++i) {
+      uint32_t h0, h1, l0, l1;
+      split_codes(x_value<F32>(xw, 4 * i) * inv, x_value<F32>(xw, 4 * i + 1) * inv,
+                  h0, l0);
+      split_codes(x_value<F32>(xw, 4 * i + 2) * inv,
+                  x_value<F32>(xw, 4 * i + 3) * inv, h1, l1);
+      hi[i] = h0 | h1 << 16;
+      lo[i] = l0 | l1 << 16;
+    }
+    for (int j = 0; j < a.k; ++j) {
+      if (pos_of[j] < 0) continue;
+      uint8_t *row = a.p.xc + static_cast<int64_t>(pos_of[j]) * a.Dc + d;
+      *reinterpret_cast<uint4 *>(row) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4 *>(row + static_cast<int64_t>(a.P) * a.Dc) =
+          make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
   }
 }
@@ -466,14 +444,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // The gate/up kernel needs the plan at once.  The down kernel can only have
-  // started after every CTA of the gate/up kernel passed this point, so the
-  // plan is final for it too; it waits where it first needs h.
-  if (UP) {
-    pdl_wait();
-    pdl_launch_dependents();
-  }
-  const int n_tiles = max(0, __ldcg(a.p.n_tiles));
+  // Neither kernel waits here for the one before it.  That one lets its
+  // dependents start only after its own wait, so what precedes it is final:
+  // the ids for the gate/up kernel, which finds the starts of the experts by
+  // itself, and the plan for the down kernel.  So both fill their rings with
+  // weights at once, and wait where they need codes.
+  Starts *starts = reinterpret_cast<Starts *>(sbase + C::kStarts);
+  const int n_tiles =
+      max(0, UP ? find_starts<TT, kThreads>(
+                      a, starts, reinterpret_cast<uint32_t *>(sbase + C::kB))
+                : __ldcg(a.p.n_tiles));
   const int K = UP ? a.D : a.F;
   const int rows = UP ? a.F : a.D;          // output rows (h or y)
   constexpr int kRows = UP ? BM : 2 * BM;   // of an item
@@ -483,23 +463,43 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t u0 = ranges.begin(blockIdx.x), u1 = ranges.begin(blockIdx.x + 1);
   const uint32_t tmem_base = *tmem_slot;
 
-  // The CTA's share of the item that holds stage u: the tile is innermost
-  // (tiles of one expert are neighbours, so its weights are still in L2 for
-  // the second), then the row block.
+  // The CTA's n-th item: first those that it shares with its neighbours (so
+  // that their parts are long there when the kernel ends), then the others.
+  // In an item's index the tile is innermost (tiles of one expert are
+  // neighbours, so its weights are still in L2 for the second), then the row
+  // block.
   struct Item {
     Tile t;
     int64_t index;
     int tile, r, c0, c1, npad;
   };
-  auto item = [&](int64_t u) {
+  const int64_t i0 = nk > 0 && u1 > u0 ? u0 / nk : 0;
+  const int items = u1 > u0 ? static_cast<int>((u1 - 1) / nk - i0) + 1 : 0;
+  const int head = items > 1 && u0 > i0 * nk;
+  const int ends = head + (items > 1 && u1 < (i0 + items) * nk);
+  auto item = [&](int n) {
     Item w;
-    w.index = u / nk;
-    w.c0 = static_cast<int>(u - w.index * nk);
-    w.c1 = static_cast<int>(min(static_cast<int64_t>(nk), u1 - w.index * nk));
+    w.index = i0 + (n >= ends ? n - ends + head : n < head ? 0 : items - 1);
+    const int64_t v = w.index * nk;
+    w.c0 = static_cast<int>(max(u0 - v, static_cast<int64_t>(0)));
+    w.c1 = static_cast<int>(min(u1 - v, static_cast<int64_t>(nk)));
     w.r = static_cast<int>(w.index / n_tiles);
     w.tile = static_cast<int>(w.index - static_cast<int64_t>(w.r) * n_tiles);
-    const int4 v = __ldcg(reinterpret_cast<const int4 *>(a.p.tiles + w.tile));
-    w.t = {v.x, v.y, v.z, v.w};
+    if (UP) {
+      // The last expert whose first tile is not after this one and that has
+      // any (one without shares its first tile with the next).
+      int lo = 0, hi = a.E - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (starts->first_tile[mid] <= w.tile) lo = mid;
+        else hi = mid - 1;
+      }
+      while (starts->count[lo] == 0) --lo;
+      w.t = tile_of_expert<TT>(starts, lo, w.tile);
+    } else {
+      const int4 q = __ldcg(reinterpret_cast<const int4 *>(a.p.tiles + w.tile));
+      w.t = {q.x, q.y, q.z, q.w};
+    }
     w.npad = (w.t.count + 7) & ~7;
     return w;
   };
@@ -526,22 +526,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     a.p.hs + static_cast<int64_t>(c) * a.P + w.t.first,
                     4 * w.npad, full_bar(s));
       };
-      // The down kernel fills its ring with weights before it waits for h.
       int ahead = 0;
-      if (!UP) {
-        for (int64_t u = u0; u < u1 && ahead < C::STAGES;) {
-          const Item w = item(u);
-          for (int c = w.c0; c < w.c1 && ahead < C::STAGES; ++c, ++u)
-            load_w(w, c, ahead++);
-        }
-        pdl_wait();
-        pdl_launch_dependents();
+      for (int n = 0; n < items && ahead < C::STAGES; ++n) {
+        const Item w = item(n);
+        for (int c = w.c0; c < w.c1 && ahead < C::STAGES; ++c)
+          load_w(w, c, ahead++);
       }
+      pdl_wait();
+      pdl_launch_dependents();
       uint32_t s = 0, ph = 0, issued = 0;
       bool ok = true;
-      for (int64_t u = u0; ok && u < u1;) {
-        const Item w = item(u);
-        u += w.c1 - w.c0;
+      for (int n = 0; ok && n < items; ++n) {
+        const Item w = item(n);
         for (int c = w.c0; c < w.c1; ++c) {
           if (ahead > 0) {
             --ahead;
@@ -571,9 +567,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       uint32_t s = 0, ph = 0, g = 0;
       bool ok = true;
-      for (int64_t u = u0; ok && u < u1;) {
-        const Item w = item(u);
-        u += w.c1 - w.c0;
+      for (int n = 0; ok && n < items; ++n) {
+        const Item w = item(n);
         const uint32_t idesc = idesc_e4m3_f32(BM, 2 * w.npad) | a.fmt_bits;
         for (int c = w.c0; c < w.c1; ++c) {
           const uint32_t b = g & 1u;
@@ -605,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    if (!UP) pdl_wait();
+    pdl_wait();
     const int quarter = warp & 3, half = warp >> 2;
     const int row = 32 * quarter + lane;  // TMEM lane
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -620,9 +615,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     uint32_t g = 0, s = 0;
     bool ok = true;
-    for (int64_t u = u0; ok && u < u1;) {
-      const Item w = item(u);
-      u += w.c1 - w.c0;
+    for (int n = 0; ok && n < items; ++n) {
+      const Item w = item(n);
       // Where a part of a shared item goes: slot 0 if it began in an earlier
       // CTA, else 1.
       const bool shared = w.c0 > 0 || w.c1 < nk;
@@ -713,13 +707,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // h, its largest over the 128 rows, and the codes.
 #pragma unroll
         for (int q = 0; q < kG; ++q)
+          if (16 * q + 8 * half < w.npad) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int col = 16 * q + 8 * half + j;
-            const float h = f < a.F && col < w.t.count
-                                ? activate(gs[q][j], a.gelu) * us[q][j] : 0.0f;
-            gs[q][j] = h;
-            if (16 * q + 8 * half < w.npad) {
+            for (int j = 0; j < 8; ++j) {
+              const int col = 16 * q + 8 * half + j;
+              const float h = f < a.F && col < w.t.count
+                                  ? activate(gs[q][j], a.gelu) * us[q][j] : 0.0f;
+              gs[q][j] = h;
               const uint32_t top =
                   __reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7fffffffu);
               if (lane == 0) tops[quarter * TT + col] = top;
@@ -823,44 +817,53 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------ combine
-// y of one token and one row block of the down kernel.
+// y of one token and one row block of the down kernel.  The places of the
+// parts follow from the plan, so they are worked out, a slot for each thread,
+// before the down kernel has finished; after that one round of loads remains.
 template <int TT>
 __global__ void __launch_bounds__(2 * BM)
     moe_combine_kernel(const LayerArgs a) {
+  __shared__ const float *part[kMaxTopK];
+  __shared__ int parts[kMaxTopK];
+  __shared__ float weight[kMaxTopK];
   const int t = blockIdx.x, r = blockIdx.y;
   const int d = r * 2 * BM + threadIdx.x;
-  const int nk = (a.F + BK - 1) / BK, rb = (a.D + 2 * BM - 1) / (2 * BM);
-  pdl_wait();
   const int n_tiles = __ldcg(a.p.n_tiles);
-  if (n_tiles < 0) return;
-  float out = 0.0f;
-  const Ranges ranges(static_cast<int64_t>(n_tiles) * rb * nk, a.grid);
-  for (int q = 0; q < a.k; ++q) {
-    const int pair = t * a.k + q;
-    const int pos = __ldcg(a.p.pos + pair);
-    if (pos < 0) continue;
-    const int tile = __ldcg(a.p.tile_of + pair);
-    const float weight = __ldcg(a.weights + pair);
-    const int64_t u = (static_cast<int64_t>(r) * n_tiles + tile) * nk;
-    const int first = ranges.owner(u), last = ranges.owner(u + nk - 1);
-    float sum = 0.0f;
-    if (first == last) {
-      if (d < a.D) sum = __ldcg(a.p.out + static_cast<int64_t>(pos) * a.Dc + d);
-    } else {
-      const int col = pos - __ldcg(&a.p.tiles[tile].first);
-#pragma unroll 4
-      for (int p = first; p <= last; ++p)
-        sum += __ldcg(a.p.parts +
-                      ((static_cast<int64_t>(p) * 2 + (p > first ? 0 : 1)) * TT +
-                       col) * 256 + threadIdx.x);
+  if (threadIdx.x < a.k) {
+    const int q = threadIdx.x, pair = t * a.k + q;
+    const int pos = n_tiles > 0 ? __ldcg(a.p.pos + pair) : -1;
+    parts[q] = 0;
+    if (pos >= 0) {
+      const int nk = (a.F + BK - 1) / BK, rb = (a.D + 2 * BM - 1) / (2 * BM);
+      const Ranges ranges(static_cast<int64_t>(n_tiles) * rb * nk, a.grid);
+      const int tile = __ldcg(a.p.tile_of + pair);
+      weight[q] = __ldcg(a.weights + pair);
+      const int64_t u = (static_cast<int64_t>(r) * n_tiles + tile) * nk;
+      const int first = ranges.owner(u), last = ranges.owner(u + nk - 1);
+      parts[q] = last - first + 1;
+      // The first CTA's part is in its slot 1, the others' in their slots 0.
+      part[q] = first == last
+                    ? a.p.out + static_cast<int64_t>(pos) * a.Dc + r * 2 * BM
+                    : a.p.parts + ((static_cast<int64_t>(first) * 2 + 1) * TT +
+                                   pos - __ldcg(&a.p.tiles[tile].first)) * 256;
     }
-    out = fmaf(weight, sum, out);
   }
-  if (d < a.D) {
-    const __nv_bfloat16 o = __float2bfloat16_rn(out);
-    a.y[static_cast<int64_t>(t) * a.ldy + d] =
-        *reinterpret_cast<const uint16_t *>(&o);
+  __syncthreads();
+  pdl_wait();
+  if (n_tiles < 0 || d >= a.D) return;
+  float out = 0.0f;
+#pragma unroll 4
+  for (int q = 0; q < a.k; ++q) {
+    const int n = parts[q];
+    if (n == 0) continue;
+    float sum = __ldcg(part[q] + threadIdx.x);
+    const float *p = part[q] + TT * 256;
+#pragma unroll 4
+    for (int i = 1; i < n; ++i, p += 2 * TT * 256) sum += __ldcg(p + threadIdx.x);
+    out = fmaf(weight[q], sum, out);
   }
+  const __nv_bfloat16 o = __float2bfloat16_rn(out);
+  a.y[static_cast<int64_t>(t) * a.ldy + d] = *reinterpret_cast<const uint16_t *>(&o);
 }
 
 // Codes [outer][rows][K] as boxes of box_rows rows x 128 K, box_outer deep.
@@ -891,8 +894,15 @@ int64_t positions(int64_t pairs, int64_t E) {
   return round16(pairs + 3 * (E < pairs ? E : pairs) + kSlack);
 }
 
-// Sizes of a tile of tokens: 16 leave more of shared memory to the weight ring.
-int tile_tokens(int64_t T) { return T <= 16 ? 16 : 64; }
+// Tokens of a tile.  Tiles of 16 leave more of shared memory to the weight
+// ring (6 stages against 4) but read the weights of an expert with more
+// tokens again, from L2.  Measured, us for a layer with tiles of 16 / of 64,
+// by the mean number of tokens of an expert: 3 (24 tokens, 8 of 64 experts)
+// 115 / 130; 8 (64 tokens) 124 / 138; 8 (32 tokens, 2 of 8) 139 / 146; 16 (64
+// tokens, 2 of 8) 185 / 152; 16 (128 tokens, 8 of 64) 147 / 148.
+int tile_tokens(int64_t T, int64_t k, int64_t E) {
+  return T <= 16 || T * k <= 8 * E ? 16 : 64;
+}
 
 struct Layout {
   int64_t P, n_tiles, tile, pos, tile_of, arrived, xc, xs, hc, hs, parts, out,
@@ -918,7 +928,7 @@ Layout layout(int64_t T, int64_t k, int64_t E, int64_t D, int64_t F, int grid) {
   l.xs = take(l.P * 4);
   l.hc = take(2 * l.P * Fc);
   l.hs = take((F + BK - 1) / BK * l.P * 4);
-  l.parts = take(static_cast<int64_t>(grid) * 2 * tile_tokens(T) * 256 * 4);
+  l.parts = take(static_cast<int64_t>(grid) * 2 * tile_tokens(T, k, E) * 256 * 4);
   l.out = take(l.P * Dc * 4);
   l.total = at;
   return l;
@@ -964,7 +974,9 @@ fp8la_status launch_layer(const CUtensorMap &tm13, const CUtensorMap &tmx,
       }) != cudaSuccess)
     return FP8LA_ERR_CUDA;
   const dim3 combine(a.T, (a.D + 2 * BM - 1) / (2 * BM), 1);
-  if (!launch_pdl(moe_prepare_kernel<TT>, a.T, kPrepThreads, 0, s, a) ||
+  if (!launch_pdl(a.x_bf16 ? moe_prepare_kernel<TT, false>
+                           : moe_prepare_kernel<TT, true>,
+                  a.T, kPrepThreads, 0, s, a) ||
       !launch_pdl(up, a.grid, kThreads, C::kAlloc, s, tm13, tmx, a) ||
       !launch_pdl(down, a.grid, kThreads, C::kAlloc, s, tm2, tmh, a) ||
       !launch_pdl(moe_combine_kernel<TT>, combine, 2 * BM, 0, s, a))
@@ -1075,6 +1087,7 @@ extern "C" fp8la_status fp8_moe_layer(
   a.status = status;
   a.timeout_ns = wait_timeout_ns();
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return tile_tokens(tokens) == 16 ? launch_layer<16>(tm13, tmx, tm2, tmh, a, s)
+  return tile_tokens(tokens, top_k, num_experts) == 16
+             ? launch_layer<16>(tm13, tmx, tm2, tmh, a, s)
                                    : launch_layer<64>(tm13, tmx, tm2, tmh, a, s);
 }

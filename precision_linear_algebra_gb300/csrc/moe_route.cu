@@ -351,7 +351,11 @@ extern "C" fp8la_status fp8_moe_route(
   a.order = order;
   a.hist = static_cast<int32_t *>(workspace);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int ctas = tokens == 0 ? 1 : static_cast<int>((tokens + per - 1) / per);
+  // Without the sort nothing ties the tokens together: one for each warp.
+  if (!sort) a.tokens_per_cta = kWarps;
+  const int ctas = tokens == 0 ? 1
+                               : static_cast<int>((tokens + a.tokens_per_cta - 1) /
+                                                  a.tokens_per_cta);
   route_kernel<<<ctas, kThreads, 0, s>>>(a);
   if (sort && ctas > 1) {
     cudaLaunchConfig_t cfg = {};

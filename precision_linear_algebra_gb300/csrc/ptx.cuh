@@ -126,6 +126,16 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap,
       : "memory");
 }
 
+// Brings a 3-D box into L2 only.
+__device__ __forceinline__ void tma_prefetch_3d(const void *tmap, int32_t c0,
+                                                int32_t c1, int32_t c2) {
+  asm volatile(
+      "cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+          reinterpret_cast<uint64_t>(tmap)),
+      "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
 // Untiled copy of `bytes` bytes (a multiple of 16, both addresses 16-byte
 // aligned) into shared memory, signalled on `bar`.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src,
