@@ -403,19 +403,14 @@ FP8LA_API fp8la_status fp8_moe_layer(
  * stride_b elements apart; alpha: fp32 [num_adapters]; m_offsets: int32
  * [num_segments + 1], starting at 0, non-decreasing, at most rows;
  * adapter_ids: int32 [num_segments], -1 .. num_adapters-1.  v: fp32
- * [rows][ldv], ldv >= rank, or NULL (the backward pass wants it).  All
- * device; the host reads none of it.  Offsets or ids that break these rules
+ * [rows][ldv], ldv >= rank (the backward pass wants it).  All device; the host reads none of it.  Offsets or ids that break these rules
  * make the call write no output and record FP8LA_ERR_DEVICE_ARG.
  * fp32 operands enter the tensor cores as sums of bf16 terms: three (24
  * significant bits) for v, two (16) for out; sums are fp32, in a fixed order.  Pointers need their
  * type's alignment; 16-byte rows are read and written fastest.
  * Limits (FP8LA_ERR_UNSUPPORTED): rank <= 128, num_segments <= 1024, rows
- * <= 2^19, K and N <= 2^22, num_adapters <= 16383.  workspace:
- * fp8la_lora_apply_workspace_bytes(...) bytes, 16-byte aligned.  Two
- * launches.
+ * <= 2^19, K and N <= 2^22, num_adapters <= 65535.  Two launches.
  */
-FP8LA_API int64_t fp8la_lora_apply_workspace_bytes(int64_t rows, int32_t num_segments,
-                                         int64_t K, int32_t rank);
 FP8LA_API fp8la_status fp8la_lora_apply(
     const uint16_t *base, int64_t ld_base, const void *x, int32_t x_dtype,
     int64_t ldx, int64_t rows, const uint16_t *A, int64_t lda,
@@ -423,8 +418,7 @@ FP8LA_API fp8la_status fp8la_lora_apply(
     const float *alpha, int32_t num_adapters, int32_t rank, int64_t K,
     int64_t N, int32_t num_segments, const int32_t *m_offsets,
     const int32_t *adapter_ids, uint16_t *out, int64_t ld_out, float *v,
-    int64_t ldv, void *workspace, int64_t workspace_bytes,
-    fp8la_stream_t stream);
+    int64_t ldv, fp8la_stream_t stream);
 
 /*
  * Backward pass of fp8la_lora_apply for the adapters and their input (the
@@ -440,10 +434,11 @@ FP8LA_API fp8la_status fp8la_lora_apply(
  * forward call; dx_base, dx: bf16 (dx may be dx_base); dA: fp32
  * [num_adapters][rank][K] and dB: fp32 [num_adapters][rank][N], dense,
  * overwritten.  Everything else, the limits, refusals and the rounding as
- * for fp8la_lora_apply (dA and dB with three terms).  Three launches; results do not depend on timing.
+ * for fp8la_lora_apply (dA and dB with three terms).  workspace:
+ * fp8la_lora_workspace_bytes(rows, rank) bytes, 16-byte aligned; it keeps
+ * nothing between calls.  Three launches; results do not depend on timing.
  */
-FP8LA_API int64_t fp8la_lora_backward_workspace_bytes(int64_t rows, int32_t num_segments,
-                                            int64_t N, int32_t rank);
+FP8LA_API int64_t fp8la_lora_workspace_bytes(int64_t rows, int32_t rank);
 FP8LA_API fp8la_status fp8la_lora_backward(
     const void *dy, int32_t dy_dtype, int64_t ld_dy, const void *x,
     int32_t x_dtype, int64_t ldx, const float *v, int64_t ldv, int64_t rows,

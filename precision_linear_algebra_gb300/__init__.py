@@ -59,11 +59,10 @@ SIGNATURES = [
     ("fp8_moe_layer", _S,
      [_P, _I32, _I64, _I64, _I64, _P, _P, _I32, _I32, _P, _I64, _I64, _P, _P, _I64, _I64, _P,
       _I64, _I32, _I32, _P, _I64, _P, _I64, _P]),
-    ("fp8la_lora_apply_workspace_bytes", _I64, [_I64, _I32, _I64, _I32]),
     ("fp8la_lora_apply", _S,
      [_P, _I64, _P, _I32, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I32, _I32, _I64,
-      _I64, _I32, _P, _P, _P, _I64, _P, _I64, _P, _I64, _P]),
-    ("fp8la_lora_backward_workspace_bytes", _I64, [_I64, _I32, _I64, _I32]),
+      _I64, _I32, _P, _P, _P, _I64, _P, _I64, _P]),
+    ("fp8la_lora_workspace_bytes", _I64, [_I64, _I32]),
     ("fp8la_lora_backward", _S,
      [_P, _I32, _I64, _P, _I32, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I32,
       _I32, _I64, _I64, _I32, _P, _P, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P]),
@@ -198,20 +197,16 @@ def fp8_moe_layer(x, x_dtype, tokens, D, ldx, ids, weights, top_k, num_experts, 
                  activation, y, ldy, workspace, workspace_bytes, stream)
 
 
-def fp8la_lora_apply_workspace_bytes(rows, num_segments, K, rank):
-    return _bytes("fp8la_lora_apply_workspace_bytes", rows, num_segments, K, rank)
-
-
 def fp8la_lora_apply(base, ld_base, x, x_dtype, ldx, rows, A, lda, stride_a, B, ldb, stride_b,
                      alpha, num_adapters, rank, K, N, num_segments, m_offsets, adapter_ids, out,
-                     ld_out, v, ldv, workspace, workspace_bytes, stream):
+                     ld_out, v, ldv, stream):
     return _call("fp8la_lora_apply", base, ld_base, x, x_dtype, ldx, rows, A, lda, stride_a, B,
                  ldb, stride_b, alpha, num_adapters, rank, K, N, num_segments, m_offsets,
-                 adapter_ids, out, ld_out, v, ldv, workspace, workspace_bytes, stream)
+                 adapter_ids, out, ld_out, v, ldv, stream)
 
 
-def fp8la_lora_backward_workspace_bytes(rows, num_segments, N, rank):
-    return _bytes("fp8la_lora_backward_workspace_bytes", rows, num_segments, N, rank)
+def fp8la_lora_workspace_bytes(rows, rank):
+    return _bytes("fp8la_lora_workspace_bytes", rows, rank)
 
 
 def fp8la_lora_backward(dy, dy_dtype, ld_dy, x, x_dtype, ldx, v, ldv, rows, A, lda, stride_a, B,
@@ -518,7 +513,7 @@ def _check_adapters(x, A, B, alpha, m_offsets, adapter_ids, N):
     return n, R, K
 
 
-def lora_apply(base, x, A, B, alpha, m_offsets, adapter_ids, out=None, v=None, workspace=None):
+def lora_apply(base, x, A, B, alpha, m_offsets, adapter_ids, out=None, v=None):
     """Adds each request's low-rank adapter to a shared projection's output.
 
     base bf16 [T][N] (e.g. from gemm), x fp32 or bf16 [T][K], A bf16 [n][R][K],
@@ -533,13 +528,10 @@ def lora_apply(base, x, A, B, alpha, m_offsets, adapter_ids, out=None, v=None, w
     assert base.dtype == torch.bfloat16 and base.stride(1) == 1 and x.shape[0] == T
     out = _out(out, (T, N), torch.bfloat16, x.device, dense=False)
     v = _out(v, (T, R), torch.float32, x.device, dense=False)
-    S = adapter_ids.numel()
-    workspace, nbytes = _workspace(workspace, fp8la_lora_apply_workspace_bytes(T, S, K, R),
-                                   x.device)
     fp8la_lora_apply(_ptr(base), _ld(base), _ptr(x), _dtype_code(x), _ld(x), T, _ptr(A),
                      A.stride(1), A.stride(0), _ptr(B), B.stride(1), B.stride(0), _ptr(alpha),
-                     n, R, K, N, S, _ptr(m_offsets), _ptr(adapter_ids), _ptr(out), _ld(out),
-                     _ptr(v), _ld(v), _ptr(workspace), nbytes, _stream())
+                     n, R, K, N, adapter_ids.numel(), _ptr(m_offsets), _ptr(adapter_ids),
+                     _ptr(out), _ld(out), _ptr(v), _ld(v), _stream())
     return out, v
 
 
@@ -562,13 +554,11 @@ def lora_backward(dy, x, v, A, B, alpha, m_offsets, adapter_ids, dx_base, dx=Non
     dx = _out(dx, (T, K), torch.bfloat16, x.device, dense=False)
     dA = _out(dA, (n, R, K), torch.float32, x.device)
     dB = _out(dB, (n, R, N), torch.float32, x.device)
-    S = adapter_ids.numel()
-    workspace, nbytes = _workspace(workspace, fp8la_lora_backward_workspace_bytes(T, S, N, R),
-                                   x.device)
+    workspace, nbytes = _workspace(workspace, fp8la_lora_workspace_bytes(T, R), x.device)
     fp8la_lora_backward(_ptr(dy), _dtype_code(dy), _ld(dy), _ptr(x), _dtype_code(x), _ld(x),
                         _ptr(v), _ld(v), T, _ptr(A), A.stride(1), A.stride(0), _ptr(B),
-                        B.stride(1), B.stride(0), _ptr(alpha), n, R, K, N, S, _ptr(m_offsets),
-                        _ptr(adapter_ids), _ptr(dx_base), _ld(dx_base), _ptr(dx), _ld(dx),
+                        B.stride(1), B.stride(0), _ptr(alpha), n, R, K, N,
+                        adapter_ids.numel(), _ptr(m_offsets), _ptr(adapter_ids), _ptr(dx_base), _ld(dx_base), _ptr(dx), _ld(dx),
                         _ptr(dA), _ptr(dB), _ptr(workspace), nbytes, _stream())
     return dx, dA, dB
 

@@ -11,16 +11,19 @@
 //
 // Both factors are stored with the rank as the slow dimension, so that three
 // kernels make up both directions:
-//   shrink   V[t][j]  = sum_k X[t][k] P_i[j][k]       (x, A) and (dy, B)
+//   shrink   V[t][j]  = sum_k X[t][k] P_i[j][k]         (x, A) and (dy, B)
 //   expand   Y[t][n]  = base + sum_j V[t][j] P_i[j][n]  (v, B) and (dv, A)
-//   outer    G_i[j][n] = sum_t V[t][j] X[t][n]        (dv, x) and (v, dy)
+//   outer    G_i[j][n] = sum_t V[t][j] X[t][n]          (dv, x) and (v, dy)
 //
-// Bound: HBM.  With R between 8 and 128 every element of X, Y or a factor
-// meets few FMAs, so the kernels read each operand once, straight from global
-// memory into the fragments of mma.sync (m16n8k16), with no shared memory in
-// between: a contraction may take its index in any order, so each lane loads
-// 16 consecutive elements of a row and calls them its fragment's, and output
-// columns are dealt out so that each lane owns 16 consecutive ones.
+// Bound: HBM.  With R between 8 and 128 every element of X or Y meets few
+// FMAs; X and Y are read and written once, and the factors, V and the sums
+// are small enough to stay on the chip.  The products are mma.sync m16n8k16
+// with fragments from shared memory, filled by cp.async several stages ahead
+// (shrink, outer), or straight from registers (expand, where a warp keeps its
+// 64 columns of the factor and streams rows past them: output columns are
+// dealt out so that each lane owns 16 consecutive ones).  Sums over a long
+// axis (K in shrink, rows in outer) are shared out over a cluster of CTAs and
+// added through distributed shared memory in rank order.
 //
 // Precision: products of BF16 operands are exact and sums FP32.  An FP32
 // operand (x or dy given as FP32, v and dv always) enters as a sum of BF16
@@ -39,7 +42,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxSegments = 1024;
 constexpr int kMaxRank = 128;
-constexpr int kMaxSplitK = 32;
+constexpr int kMaxCluster = 8;
 
 struct Segments {
   const int32_t *offsets;   // [S + 1]
@@ -136,6 +139,86 @@ __device__ __forceinline__ void load_pairs(const void *p, int64_t c, int64_t wid
   }
 }
 
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile(
+      "ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(addr));
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile(
+      "ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(addr));
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Copies `rows` rows of COLS elements of SIZE bytes, from column c of a matrix
+// with `width` columns on, to shared memory (rows LD bytes apart), zeros where
+// the matrix has no element or r >= valid.  Asynchronous where the matrix has
+// 16-byte rows; else at once, by plain loads and stores.
+template <int COLS, int SIZE, int LD>
+__device__ __forceinline__ void copy_tile(uint32_t dst, const char *src, int64_t ld,
+                                          int rows, int valid, int64_t c,
+                                          int64_t width, bool vec) {
+  constexpr int kUnits = COLS * SIZE / 16;  // 16-byte units of a row
+  constexpr int kPer = 16 / SIZE;
+  for (int i = threadIdx.x; i < rows * kUnits; i += kThreads) {
+    const int r = i / kUnits, u = i % kUnits;
+    const int64_t cc = c + u * kPer;
+    const int n = r < valid && cc < width
+                      ? static_cast<int>(min(static_cast<int64_t>(kPer), width - cc)) : 0;
+    const char *p = src + (n > 0 ? (r * ld + cc) * SIZE : 0);
+    const uint32_t d = dst + r * LD + u * 16;
+    if (vec) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(p),
+                   "r"(n * SIZE)
+                   : "memory");
+    } else {
+      uint32_t w[4] = {0, 0, 0, 0};
+      if (SIZE == 4) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j < n) w[j] = reinterpret_cast<const uint32_t *>(p)[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < n)
+            w[j >> 1] |= static_cast<uint32_t>(
+                             reinterpret_cast<const uint16_t *>(p)[j])
+                         << (16 * (j & 1));
+      }
+      st_shared_v4(d, w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t n;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+  return n;
+}
+
+// Sum over the cluster's CTAs, in rank order, of the float at address `addr`
+// of each one's shared memory.
+__device__ __forceinline__ float cluster_sum(uint32_t addr, uint32_t n) {
+  float s = 0.0f;
+  for (uint32_t p = 0; p < n; ++p) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                 : "=f"(v)
+                 : "r"(mapa_shared(addr, p)));
+    s += v;
+  }
+  return s;
+}
+
 // Exclusive prefix sum over the CTA; total in *all.
 __device__ __forceinline__ int block_exclusive(int v, int *warp_sums, int *all) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -218,98 +301,173 @@ struct ShrinkArgs {
   const uint16_t *P;
   int64_t ldp, stride_p;
   int64_t K;
-  int32_t R, Rp;
+  int32_t R;
   int32_t x_vec, p_vec;
-  float *part;  // [K splits][T][Rp]
+  const float *alpha;  // null: 1
+  float *V;            // [T][ldv]
+  int64_t ldv;
 };
 
-// MT row fragments of 16 rows, NJ rank fragments of 8.  The CTA's eight
-// warps take 64-wide K blocks in turn and add their sums in a fixed order.
-template <bool F32, int MT, int NJ>
+// MW groups of warps share out the rows (MF fragments of 16 each), KW = 8 / MW
+// the K of a stage; NJ rank fragments of 8 (even where more than one).
+template <bool F32, int MW, int MF, int NJ>
+struct ShrinkCfg {
+  static constexpr int TM = 16 * MW * MF;
+  static constexpr int KW = kWarps / MW;
+  static constexpr int KS = F32 && KW < 8 ? 64 : 128;  // K of a stage
+  static constexpr int kSteps = KS / 16;               // MMA steps of a stage
+  static constexpr int RP = 8 * (NJ == 1 ? 2 : NJ);    // ranks in shared memory
+  // Padded rows: fragment loads touch every bank once.
+  static constexpr int kLdX = KS * (F32 ? 4 : 2) + (F32 ? 32 : 16);
+  static constexpr int kLdP = KS * 2 + 16;
+  static constexpr int kX = TM * kLdX;
+  static constexpr int kStage = kX + RP * kLdP;
+  static constexpr int STAGES = kStage * 4 <= 216 * 1024 ? 4 : 3;
+  static constexpr int kRing = STAGES * kStage;
+  static constexpr int kLdR = 8 * NJ + 2;              // of the sums, in floats
+  static constexpr int kRed = KW * TM * kLdR * 4;
+  static constexpr int kSmem = kRing > kRed ? kRing : kRed;
+  static_assert(kSmem <= 226 * 1024, "shared memory");
+  static_assert(kSteps % KW == 0, "every K group has steps");
+};
+
+// grid: x = rank in the cluster (K split), y = row tile.
+template <bool F32, int MW, int MF, int NJ>
 __global__ void __launch_bounds__(kThreads)
     lora_shrink_kernel(const ShrinkArgs a) {
-  constexpr int TM = 16 * MT;
+  using C = ShrinkCfg<F32, MW, MF, NJ>;
   constexpr int NT = F32 ? 3 : 1;
-  extern __shared__ float red[];  // [kWarps][TM][8 NJ]
+  extern __shared__ __align__(16) char smem[];
   __shared__ int warp_sums[kWarps];
   __shared__ Found slot;
   pdl_wait();
   pdl_launch_dependents();
-  const Found f = find_tile(a.seg, blockIdx.y, TM, warp_sums, &slot);
-  if (f.rows == 0 || f.id < 0) return;
+  const Found f = find_tile(a.seg, blockIdx.y, C::TM, warp_sums, &slot);
+  if (f.rows == 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t crank = cluster_ctarank(), csize = cluster_size();
+  if (f.id < 0) {  // rows without an adapter
+    if (crank == 0)
+      for (int i = threadIdx.x; i < f.rows * a.R; i += kThreads)
+        a.V[(f.row0 + static_cast<int64_t>(i / a.R)) * a.ldv + i % a.R] = 0.0f;
+    return;
+  }
   const int g = lane >> 2, q = lane & 3;
-  const int64_t nkb = (a.K + 63) / 64;
-  const int64_t kb0 = nkb * blockIdx.x / gridDim.x;
-  const int64_t kb1 = nkb * (blockIdx.x + 1) / gridDim.x;
-  const uint16_t *P = a.P + f.id * a.stride_p;
-  const int xs = F32 ? 4 : 2;
-  float acc[MT][NJ][4];
+  const int mw = warp % MW, kw = warp / MW;
+  const int64_t nst = (a.K + C::KS - 1) / C::KS;
+  const int s0 = static_cast<int>(nst * crank / csize);
+  const int s1 = static_cast<int>(nst * (crank + 1) / csize);
+  constexpr int kSize = F32 ? 4 : 2;
+  const char *X = static_cast<const char *>(a.X) + f.row0 * a.ldx * kSize;
+  const char *P = reinterpret_cast<const char *>(a.P + f.id * a.stride_p);
+  const uint32_t base = smem_addr(smem);
+  // Rows of fragments that hold no row of the tile are not loaded.
+  const int xrows = min(C::TM, (f.rows + 15) / 16 * 16);
+  auto fill = [&](int s) {
+    if (s < s1) {
+      const uint32_t d = base + (s - s0) % C::STAGES * C::kStage;
+      const int64_t k = static_cast<int64_t>(s) * C::KS;
+      copy_tile<C::KS, kSize, C::kLdX>(d, X, a.ldx, xrows, f.rows, k, a.K, a.x_vec);
+      copy_tile<C::KS, 2, C::kLdP>(d + C::kX, P, a.ldp, C::RP, a.R, k, a.K, a.p_vec);
+    }
+    cp_async_commit();
+  };
+  float acc[MF][NJ][4];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int m = 0; m < MF; ++m)
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
       for (int c = 0; c < 4; ++c) acc[m][j][c] = 0.0f;
-  for (int64_t kb = kb0 + warp; kb < kb1; kb += kWarps) {
-    const int64_t k = kb * 64 + 16 * q;
-    uint32_t xa[MT][2][NT][8];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+  for (int s = 0; s < C::STAGES - 1; ++s) fill(s0 + s);
+  for (int s = s0; s < s1; ++s) {
+    cp_async_wait<C::STAGES - 2>();
+    __syncthreads();
+    fill(s + C::STAGES - 1);
+    char *sx = smem + (s - s0) % C::STAGES * C::kStage;
+    const uint32_t st = smem_addr(sx);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = 16 * m + 8 * h + g;
-        const char *p = static_cast<const char *>(a.X) +
-                        (f.row0 + static_cast<int64_t>(r)) * a.ldx * xs;
-        load_pairs<F32, 8, NT>(r < f.rows ? p : nullptr, k, a.K, a.x_vec,
-                               xa[m][h]);
-      }
+    for (int i = 0; i < C::kSteps / C::KW; ++i) {
+      const int k = 16 * (kw + i * C::KW);
+      uint32_t b[(NJ + 1) / 2][4];
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const int r = 8 * j + g;
-      uint32_t pb[1][8];
-      load_pairs<false, 8, 1>(r < a.R ? P + r * a.ldp : nullptr, k, a.K,
-                              a.p_vec, pb);
+      for (int j = 0; j < (NJ + 1) / 2; ++j)
+        ldmatrix4(st + C::kX + (16 * j + (lane & 7) + 8 * (lane >> 4)) * C::kLdP +
+                      (k + 8 * ((lane >> 3) & 1)) * 2,
+                  b[j]);
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int m = 0; m < MF; ++m) {
+        const int r0 = 16 * (mw * MF + m);
+        if (r0 >= f.rows) continue;
+        uint32_t x[4][NT];
+        if (F32) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
+          for (int h = 0; h < 4; ++h) {
+            const float2 v = *reinterpret_cast<const float2 *>(
+                sx + (r0 + g + 8 * (h & 1)) * C::kLdX + (k + 2 * q + 8 * (h >> 1)) * 4);
+            split_pair<NT>(v.x, v.y, x[h]);
+          }
+        } else {
+          uint32_t w[4];
+          ldmatrix4(st + (r0 + (lane & 15)) * C::kLdX + (k + 8 * (lane >> 4)) * 2, w);
+#pragma unroll
+          for (int h = 0; h < 4; ++h) x[h][0] = w[h];
+        }
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
 #pragma unroll
           for (int t = 0; t < NT; ++t)
-            mma16816(acc[m][j], xa[m][0][t][2 * s], xa[m][1][t][2 * s],
-                     xa[m][0][t][2 * s + 1], xa[m][1][t][2 * s + 1],
-                     pb[0][2 * s], pb[0][2 * s + 1]);
+            mma16816(acc[m][j], x[0][t], x[1][t], x[2][t], x[3][t],
+                     b[j >> 1][2 * (j & 1)], b[j >> 1][2 * (j & 1) + 1]);
+      }
     }
   }
+  // Sums of the K groups, then of the cluster's CTAs.
+  cp_async_wait<0>();
+  __syncthreads();
+  float *red = reinterpret_cast<float *>(smem);
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int m = 0; m < MF; ++m)
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        red[(warp * TM + 16 * m + g + 8 * (c >> 1)) * (8 * NJ) + 8 * j + 2 * q +
-            (c & 1)] = acc[m][j][c];
+      for (int c = 0; c < 4; c += 2)
+        *reinterpret_cast<float2 *>(
+            red + (kw * C::TM + 16 * (mw * MF + m) + g + 4 * c) * C::kLdR + 8 * j +
+            2 * q) = make_float2(acc[m][j][c], acc[m][j][c + 1]);
   __syncthreads();
-  float *out = a.part + (static_cast<int64_t>(blockIdx.x) * a.seg.T + f.row0) * a.Rp;
-  for (int i = threadIdx.x; i < f.rows * a.Rp; i += kThreads) {
-    const int r = i / a.Rp, j = i - r * a.Rp;
-    float s = 0.0f;
-    if (j < 8 * NJ)
+  const float alpha = a.alpha ? a.alpha[f.id] : 1.0f;
+  const int cells = f.rows * a.R;
+  if (C::KW > 1 || csize == 1)
+    for (int i = threadIdx.x; i < cells; i += kThreads) {
+      const int r = i / a.R, j = i - r * a.R;
+      float s = red[r * C::kLdR + j];
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) s += red[(w * TM + r) * (8 * NJ) + j];
-    out[static_cast<int64_t>(r) * a.Rp + j] = s;
+      for (int w = 1; w < C::KW; ++w) s += red[(w * C::TM + r) * C::kLdR + j];
+      if (csize == 1)
+        a.V[(f.row0 + static_cast<int64_t>(r)) * a.ldv + j] = s * alpha;
+      else
+        red[r * C::kLdR + j] = s;
+    }
+  if (csize == 1) return;
+  cluster_sync_all();
+  for (int i = static_cast<int>(crank) * kThreads + threadIdx.x; i < cells;
+       i += static_cast<int>(csize) * kThreads) {
+    const int r = i / a.R, j = i - r * a.R;
+    a.V[(f.row0 + static_cast<int64_t>(r)) * a.ldv + j] =
+        cluster_sum(base + 4u * (r * C::kLdR + j), csize) * alpha;
   }
+  cluster_sync_all();  // no CTA leaves while its sums are read
 }
 
 // ------------------------------------------------------------------- expand
 struct ExpandArgs {
   Segments seg;
-  const float *part;     // [splits][T][Rp]
-  int32_t splits, R, Rp;
-  const float *alpha;    // [n]
-  int32_t scale_v;       // v_out gets alpha v (backward) instead of v
-  float *v_out;          // [T][ldv]
+  const float *V;        // [T][ldv]
   int64_t ldv;
+  int32_t R;
+  const float *alpha;    // null: 1
   const uint16_t *P;     // [n][R][ldp]
   int64_t ldp, stride_p;
   int64_t N;
@@ -373,59 +531,62 @@ __global__ void __launch_bounds__(kThreads)
     lora_expand_kernel(const ExpandArgs a) {
   constexpr int kLd = 16 * KR + 8;  // padded row of a term, in BF16
   constexpr bool kHold = KR <= 4;   // the factor stays in registers
-  __shared__ __align__(16) uint16_t sv[2][TM][kLd];
+  extern __shared__ __align__(16) uint16_t sv[];  // [2][TM][kLd]
   __shared__ int warp_sums[kWarps];
   __shared__ Found slot;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, q = lane & 3;
+  const int64_t col = static_cast<int64_t>(blockIdx.x) * kExpandCols + 64 * warp;
+  const int64_t c = col + 16 * q;
   pdl_wait();
   pdl_launch_dependents();
   const Found f = find_tile(a.seg, blockIdx.y, TM, warp_sums, &slot);
   if (f.rows == 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, q = lane & 3;
-  const int64_t col = static_cast<int64_t>(blockIdx.x) * kExpandCols + 64 * warp;
   const bool on = f.id >= 0;
-  const float alpha = on ? a.alpha[f.id] : 0.0f;
   const uint16_t *P = a.P + (on ? f.id : 0) * a.stride_p;
 
-  // V of the tile: the K splits added in order, alpha applied, as two terms.
-  for (int i = threadIdx.x; i < TM * 8 * KR; i += kThreads) {
-    const int r = i / (8 * KR), j = 2 * (i - r * 8 * KR);
-    float v0 = 0.0f, v1 = 0.0f;
-    if (on && r < f.rows && j < a.Rp)
-      for (int s = 0; s < a.splits; ++s) {
-        const float2 p = *reinterpret_cast<const float2 *>(
-            a.part + ((static_cast<int64_t>(s) * a.seg.T + f.row0 + r) * a.Rp + j));
-        v0 += p.x;
-        v1 += p.y;
-      }
-    const float w0 = v0 * alpha, w1 = v1 * alpha;
-    if (blockIdx.x == 0 && a.v_out && r < f.rows) {
-      float *o = a.v_out + (f.row0 + static_cast<int64_t>(r)) * a.ldv;
-      if (j < a.R) o[j] = a.scale_v ? w0 : v0;
-      if (j + 1 < a.R) o[j + 1] = a.scale_v ? w1 : v1;
-    }
-    uint32_t t[2];
-    split_pair<2>(w0, w1, t);
-    *reinterpret_cast<uint32_t *>(&sv[0][r][j]) = t[0];
-    *reinterpret_cast<uint32_t *>(&sv[1][r][j]) = t[1];
-  }
+  // The factor's fragments and the first rows of base are on their way while
+  // V is split.
   uint32_t b[kHold ? KR : 1][8][2];
   if (kHold && on && col < a.N)
 #pragma unroll
     for (int k = 0; k < KR; ++k)
       load_rank_block(a, P, 16 * k, q, col + 8 * g, b[kHold ? k : 0]);
-  __syncthreads();
-  if (col >= a.N) return;
-  for (int m = 0; m < TM / 16 && 16 * m < f.rows; ++m) {
-    const int64_t c = col + 16 * q;
-    uint32_t w[2][8];
+  uint32_t next[2][8];
+  auto load_base = [&](int m) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int r = 16 * m + 8 * h + g;
-      load_bf16x16(r < f.rows ? a.base + (f.row0 + static_cast<int64_t>(r)) * a.ld_base
-                              : nullptr,
-                   c, a.N, a.base_vec, w[h]);
+      load_bf16x16(r < f.rows && col < a.N
+                       ? a.base + (f.row0 + static_cast<int64_t>(r)) * a.ld_base
+                       : nullptr,
+                   c, a.N, a.base_vec, next[h]);
     }
+  };
+  load_base(0);
+  const float alpha = !on ? 0.0f : a.alpha ? a.alpha[f.id] : 1.0f;
+  const int vrows = min(TM, (f.rows + 15) / 16 * 16);
+  if (on)
+    for (int i = threadIdx.x; i < vrows * 8 * KR; i += kThreads) {
+      const int r = i / (8 * KR), j = 2 * (i - r * 8 * KR);
+      const float *v = a.V + (f.row0 + static_cast<int64_t>(r)) * a.ldv + j;
+      const float v0 = r < f.rows && j < a.R ? __ldcg(v) * alpha : 0.0f;
+      const float v1 = r < f.rows && j + 1 < a.R ? __ldcg(v + 1) * alpha : 0.0f;
+      uint32_t t[2];
+      split_pair<2>(v0, v1, t);
+      *reinterpret_cast<uint32_t *>(sv + r * kLd + j) = t[0];
+      *reinterpret_cast<uint32_t *>(sv + (TM + r) * kLd + j) = t[1];
+    }
+  __syncthreads();
+  if (col >= a.N) return;
+  const uint32_t sv_lane = smem_addr(sv) + ((lane & 15) * kLd + 8 * (lane >> 4)) * 2;
+  for (int m = 0; 16 * m < f.rows; ++m) {
+    uint32_t w[2][8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[h][i] = next[h][i];
+    if (16 * (m + 1) < f.rows) load_base(m + 1);
     float acc[8][4];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -437,15 +598,11 @@ __global__ void __launch_bounds__(kThreads)
         if (!kHold) load_rank_block(a, P, 16 * k, q, col + 8 * g, b[0]);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const int j = 16 * k + 2 * q;
-          const uint32_t a0 = *reinterpret_cast<const uint32_t *>(&sv[t][16 * m + g][j]);
-          const uint32_t a1 = *reinterpret_cast<const uint32_t *>(&sv[t][16 * m + g + 8][j]);
-          const uint32_t a2 = *reinterpret_cast<const uint32_t *>(&sv[t][16 * m + g][j + 8]);
-          const uint32_t a3 =
-              *reinterpret_cast<const uint32_t *>(&sv[t][16 * m + g + 8][j + 8]);
+          uint32_t v[4];
+          ldmatrix4(sv_lane + ((t * TM + 16 * m) * kLd + 16 * k) * 2, v);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            mma16816(acc[i], a0, a1, a2, a3, b[kHold ? k : 0][i][0],
+            mma16816(acc[i], v[0], v[1], v[2], v[3], b[kHold ? k : 0][i][0],
                      b[kHold ? k : 0][i][1]);
         }
       }
@@ -486,30 +643,44 @@ struct OuterArgs {
   Segments seg;
   OuterSide side[2];    // dA (dv, x) and dB (v, dy)
   const float *alpha;
-  int32_t R, rank_blocks;
+  int32_t R;
 };
 
-constexpr int kColWarps = 4;                    // warps side by side
-constexpr int kRowWarps = kWarps / kColWarps;   // warps that share out rows
-constexpr int kOuterCols = 64 * kColWarps;
+constexpr int kOuterCols = 32 * kWarps;  // a warp has 32 columns
 
-// MR fragments of 16 ranks.  A cluster of CTAs shares out the rows of one
-// (adapter, 16 MR ranks, 256 columns) and adds its parts in rank order.
+// MR fragments of 16 ranks.  A stage is up to TS rows of one segment.
+template <bool F32, int MR>
+struct OuterCfg {
+  static constexpr int TS = F32 ? 32 : 64;
+  static constexpr int XT = F32 ? 3 : 1;    // terms of X; V has three
+  // Padded rows: fragment loads touch every bank once.
+  static constexpr int kLdX = kOuterCols * (F32 ? 4 : 2) + 16;
+  static constexpr int kX = TS * kLdX;
+  static constexpr int STAGES = MR <= 4 ? 4 : 3;
+  static constexpr int kLdW = 16 * MR + 8;  // row of a term of V, in BF16
+  static constexpr int kTerm = TS * kLdW * 2;
+  static constexpr int kW = STAGES * kX;    // [2 buffers][3 terms]
+  static constexpr int kLdR = kOuterCols + 4;
+  static constexpr int kRed = 16 * MR * kLdR * 4;
+  static constexpr int kSmem = kW + 6 * kTerm > kRed ? kW + 6 * kTerm : kRed;
+  // Words of V (pairs of ranks) that a thread splits for a stage.
+  static constexpr int kPairs = TS * 8 * MR / kThreads;
+  static_assert(kPairs * kThreads == TS * 8 * MR, "pairs");
+  static_assert(kSmem <= 212 * 1024, "shared memory");
+};
+
+// A cluster of CTAs shares out the rows of one (adapter, 256 columns).
 template <bool F32, int MR>
 __device__ __forceinline__ void outer_body(const OuterArgs &a, const OuterSide &o,
-                                           int adapter, int rank0, int64_t col0,
-                                           float *red, int *seg_lo, int *seg_hi,
-                                           int *seg_step, int *warp_sums) {
-  constexpr int XT = F32 ? 3 : 1;           // terms of X
-  constexpr int WT = 3;                     // terms of W
+                                           int adapter, int64_t col0, char *smem,
+                                           int *seg_lo, int *seg_hi, int *seg_step,
+                                           int *warp_sums) {
+  using C = OuterCfg<F32, MR>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, q = lane & 3;
-  const int cw = warp % kColWarps, rw = warp / kColWarps;
-  const uint32_t crank = cluster_ctarank();
-  uint32_t csize;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
+  const uint32_t crank = cluster_ctarank(), csize = cluster_size();
 
-  // The adapter's segments, in order, with the steps of 16 rows before each.
+  // The adapter's segments, in order, with the stages before each.
   constexpr int kPer = kMaxSegments / kThreads;
   const int per = (a.seg.S + kThreads - 1) / kThreads;
   int lo[kPer], hi[kPer], mine = 0, steps = 0;
@@ -527,7 +698,7 @@ __device__ __forceinline__ void outer_body(const OuterArgs &a, const OuterSide &
         lo[i] = l;
         hi[i] = h;
         ++mine;
-        steps += (h - l + 15) / 16;
+        steps += (h - l + C::TS - 1) / C::TS;
       }
     }
   }
@@ -538,118 +709,168 @@ __device__ __forceinline__ void outer_body(const OuterArgs &a, const OuterSide &
   }
   int nseg, nstep;
   int at = block_exclusive(mine, warp_sums, &nseg);
-  int st = block_exclusive(steps, warp_sums, &nstep);
+  int before = block_exclusive(steps, warp_sums, &nstep);
 #pragma unroll
   for (int i = 0; i < kPer; ++i)
     if (hi[i] > lo[i]) {
       seg_lo[at] = lo[i];
       seg_hi[at] = hi[i];
-      seg_step[at] = st;
+      seg_step[at] = before;
       ++at;
-      st += (hi[i] - lo[i] + 15) / 16;
+      before += (hi[i] - lo[i] + C::TS - 1) / C::TS;
     }
   __syncthreads();
 
-  float acc[MR][8][4];
+  const int s0 = static_cast<int>(static_cast<int64_t>(nstep) * crank / csize);
+  const int s1 = static_cast<int>(static_cast<int64_t>(nstep) * (crank + 1) / csize);
+  constexpr int kSize = F32 ? 4 : 2;
+  const uint32_t base = smem_addr(smem);
+  // First row and number of rows of stage s; `at` follows s upwards.
+  auto rows_of = [&](int s, int &at, int &t0) {
+    while (at + 1 < nseg && seg_step[at + 1] <= s) ++at;
+    t0 = seg_lo[at] + C::TS * (s - seg_step[at]);
+    return min(C::TS, seg_hi[at] - t0);
+  };
+  int at_x = 0, at_w = 0, at_m = 0;
+  auto fill = [&](int s) {
+    if (s < s1) {
+      int t0;
+      const int n = rows_of(s, at_x, t0);
+      copy_tile<kOuterCols, kSize, C::kLdX>(
+          base + (s - s0) % C::STAGES * C::kX,
+          static_cast<const char *>(o.X) + t0 * o.ldx * kSize, o.ldx,
+          (n + 15) / 16 * 16, n, col0, o.N, o.x_vec);
+    }
+    cp_async_commit();
+  };
+  // V of a stage: loaded while the stage before is multiplied, split after it.
+  float w[C::kPairs][2];
+  auto load_v = [&](int s) {
+    int t0 = 0;
+    const int n = s < s1 ? rows_of(s, at_w, t0) : 0;
+#pragma unroll
+    for (int i = 0; i < C::kPairs; ++i) {
+      const int e = threadIdx.x + i * kThreads;
+      const int r = e / (8 * MR), j = 2 * (e % (8 * MR));
+      const float *p = o.W + (t0 + static_cast<int64_t>(r)) * o.ldw + j;
+      w[i][0] = r < n && j < a.R ? __ldcg(p) : 0.0f;
+      w[i][1] = r < n && j + 1 < a.R ? __ldcg(p + 1) : 0.0f;
+    }
+  };
+  auto store_v = [&](int s) {
+    char *d = smem + C::kW + ((s - s0) & 1) * 3 * C::kTerm;
+#pragma unroll
+    for (int i = 0; i < C::kPairs; ++i) {
+      const int e = threadIdx.x + i * kThreads;
+      const int r = e / (8 * MR), j = 2 * (e % (8 * MR));
+      uint32_t t[3];
+      split_pair<3>(w[i][0], w[i][1], t);
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        *reinterpret_cast<uint32_t *>(d + k * C::kTerm + (r * C::kLdW + j) * 2) = t[k];
+    }
+  };
+  float acc[MR][4][4];
 #pragma unroll
   for (int m = 0; m < MR; ++m)
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[m][i][e] = 0.0f;
-  const int s0 = static_cast<int>(static_cast<int64_t>(nstep) * crank / csize);
-  const int s1 = static_cast<int>(static_cast<int64_t>(nstep) * (crank + 1) / csize);
-  const int64_t c = col0 + 64 * cw + 8 * g;
-  int at_seg = 0;
-  for (int s = s0 + rw; s < s1; s += kRowWarps) {
-    while (at_seg + 1 < nseg && seg_step[at_seg + 1] <= s) ++at_seg;
-    const int t0 = seg_lo[at_seg] + 16 * (s - seg_step[at_seg]);
-    const int t1 = seg_hi[at_seg];
-    // X rows 2q, 2q+1, 2q+8, 2q+9 of the step, columns c..c+7.
-    uint32_t x[4][XT][4];
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      const int t = t0 + 2 * q + (h & 1) + 8 * (h >> 1);
-      const char *p = static_cast<const char *>(o.X) +
-                      static_cast<int64_t>(t) * o.ldx * (F32 ? 4 : 2);
-      load_pairs<F32, 4, XT>(t < t1 ? p : nullptr, c, o.N, o.x_vec, x[h]);
-    }
+  for (int s = 0; s < C::STAGES - 1; ++s) fill(s0 + s);
+  load_v(s0);
+  store_v(s0);
+  for (int s = s0; s < s1; ++s) {
+    cp_async_wait<C::STAGES - 2>();
+    __syncthreads();
+    fill(s + C::STAGES - 1);
+    load_v(s + 1);
+    int t0;
+    const int n = rows_of(s, at_m, t0);
+    const char *sx = smem + (s - s0) % C::STAGES * C::kX;
+    const uint32_t st = smem_addr(sx);
+    const uint32_t sw = base + C::kW + ((s - s0) & 1) * 3 * C::kTerm;
+#pragma unroll 1
+    for (int k = 0; k < n; k += 16) {
+      // B: rows k.. of X, the warp's four fragments of 8 columns.
+      uint32_t b[C::XT][4][2];
+      if (F32) {
 #pragma unroll
-    for (int m = 0; m < MR; ++m) {
-      // W of the same rows, ranks g and g + 8 of the block.
-      uint32_t wa[4][WT];  // A registers 0..3
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        const int t = t0 + 2 * q + 8 * (h >> 1);
-        const int j = rank0 + 16 * m + g + 8 * (h & 1);
-        const float *p = o.W + static_cast<int64_t>(t) * o.ldw + j;
-        const float w0 = t < t1 && j < a.R ? p[0] : 0.0f;
-        const float w1 = t + 1 < t1 && j < a.R ? p[o.ldw] : 0.0f;
-        split_pair<WT>(w0, w1, wa[h]);
-      }
+          for (int h = 0; h < 2; ++h) {
+            const float *p = reinterpret_cast<const float *>(
+                sx + (k + 2 * q + 8 * h) * C::kLdX + (32 * warp + 8 * i + g) * 4);
+            uint32_t t[C::XT];
+            split_pair<C::XT>(p[0], p[C::kLdX / 4], t);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t sel = i & 1 ? 0x7632u : 0x5410u;
+            for (int x = 0; x < C::XT; ++x) b[x][i][h] = t[x];
+          }
+      } else {
 #pragma unroll
-        for (int tx = 0; tx < XT; ++tx) {
-          const uint32_t b0 = __byte_perm(x[0][tx][i >> 1], x[1][tx][i >> 1], sel);
-          const uint32_t b1 = __byte_perm(x[2][tx][i >> 1], x[3][tx][i >> 1], sel);
-#pragma unroll
-          for (int tw = 0; tw < WT; ++tw)
-            if (tx + tw < WT)
-              mma16816(acc[m][i], wa[0][tw], wa[1][tw], wa[2][tw], wa[3][tw], b0,
-                       b1);
+        for (int i = 0; i < 2; ++i) {
+          uint32_t r[4];
+          ldmatrix4_trans(st + (k + (lane & 15)) * C::kLdX +
+                              (32 * warp + 16 * i + 8 * (lane >> 4)) * 2,
+                          r);
+          b[0][2 * i][0] = r[0];
+          b[0][2 * i][1] = r[1];
+          b[0][2 * i + 1][0] = r[2];
+          b[0][2 * i + 1][1] = r[3];
         }
       }
-    }
-  }
-
-  // Sums of the CTA's row warps, then of the cluster's CTAs, in order.
-  constexpr int kLd = kOuterCols + 4;
-  for (int w = 0; w < kRowWarps; ++w) {
-    if (rw == w) {
 #pragma unroll
       for (int m = 0; m < MR; ++m)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int t = 0; t < 3; ++t) {
+          uint32_t v[4];
+          ldmatrix4_trans(sw + t * C::kTerm +
+                              ((k + (lane & 7) + 8 * (lane >> 4)) * C::kLdW + 16 * m +
+                               8 * ((lane >> 3) & 1)) * 2,
+                          v);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            // Fragment i's column n is column 8 n + i of the warp's 64.
-            float *d = red + (16 * m + g + 8 * (e >> 1)) * kLd + 64 * cw +
-                       8 * (2 * q + (e & 1)) + i;
-            *d = w == 0 ? acc[m][i][e] : *d + acc[m][i][e];
-          }
+          for (int x = 0; x < C::XT; ++x)
+            if (x + t < 3)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                mma16816(acc[m][i], v[0], v[1], v[2], v[3], b[x][i][0], b[x][i][1]);
+        }
     }
-    __syncthreads();
+    if (s + 1 < s1) store_v(s + 1);
   }
+
+  // Sums of the cluster's CTAs, in order.
+  cp_async_wait<0>();
+  __syncthreads();
+  float *red = reinterpret_cast<float *>(smem);
+#pragma unroll
+  for (int m = 0; m < MR; ++m)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; e += 2)
+        *reinterpret_cast<float2 *>(red + (16 * m + g + 4 * e) * C::kLdR + 32 * warp +
+                                    8 * i + 2 * q) =
+            make_float2(acc[m][i][e], acc[m][i][e + 1]);
   cluster_sync_all();
   const float scale = o.use_alpha ? a.alpha[adapter] : 1.0f;
-  const uint32_t red_addr = smem_addr(red);
-  constexpr int kCells = 16 * MR * kOuterCols;
-  for (int i = static_cast<int>(crank) * kThreads + threadIdx.x; i < kCells;
+  const int cells = a.R * kOuterCols;
+  for (int i = static_cast<int>(crank) * kThreads + threadIdx.x; i < cells;
        i += static_cast<int>(csize) * kThreads) {
     const int r = i / kOuterCols, cc = i % kOuterCols;
-    if (rank0 + r >= a.R || col0 + cc >= o.N) continue;
-    float s = 0.0f;
-    for (uint32_t p = 0; p < csize; ++p) {
-      float v;
-      asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                   : "=f"(v)
-                   : "r"(mapa_shared(red_addr + 4u * (r * kLd + cc), p)));
-      s += v;
-    }
-    o.G[(static_cast<int64_t>(adapter) * a.R + rank0 + r) * o.N + col0 + cc] =
-        s * scale;
+    if (col0 + cc >= o.N) continue;
+    o.G[(static_cast<int64_t>(adapter) * a.R + r) * o.N + col0 + cc] =
+        cluster_sum(base + 4u * (r * C::kLdR + cc), csize) * scale;
   }
-  cluster_sync_all();  // no CTA leaves while its parts are read
+  cluster_sync_all();  // no CTA leaves while its sums are read
 }
 
-// grid: x = cluster rank, y = column block of either side, z = adapter and
-// rank block.
+// grid: x = cluster rank, y = column block of either side, z = adapter.
 template <int MR>
 __global__ void __launch_bounds__(kThreads)
     lora_outer_kernel(const OuterArgs a) {
-  extern __shared__ float red[];  // [16 MR][kOuterCols + 4]
+  extern __shared__ __align__(16) char smem[];
   __shared__ int seg_lo[kMaxSegments], seg_hi[kMaxSegments], seg_step[kMaxSegments];
   __shared__ int warp_sums[kWarps];
   pdl_wait();
@@ -659,14 +880,12 @@ __global__ void __launch_bounds__(kThreads)
   const OuterSide &o = a.side[second];
   const int64_t col0 =
       static_cast<int64_t>(blockIdx.y - (second ? blocks0 : 0)) * kOuterCols;
-  const int adapter = blockIdx.z / a.rank_blocks;
-  const int rank0 = (blockIdx.z % a.rank_blocks) * 16 * MR;
   if (o.x_f32)
-    outer_body<true, MR>(a, o, adapter, rank0, col0, red, seg_lo, seg_hi,
-                         seg_step, warp_sums);
+    outer_body<true, MR>(a, o, blockIdx.z, col0, smem, seg_lo, seg_hi, seg_step,
+                         warp_sums);
   else
-    outer_body<false, MR>(a, o, adapter, rank0, col0, red, seg_lo, seg_hi,
-                          seg_step, warp_sums);
+    outer_body<false, MR>(a, o, blockIdx.z, col0, smem, seg_lo, seg_hi, seg_step,
+                          warp_sums);
 }
 
 // --------------------------------------------------------------------- host
@@ -681,22 +900,6 @@ bool short_segments(int64_t T, int64_t S) { return T <= 16 * S; }
 int64_t tile_bound(int64_t T, int64_t S, int64_t TM) {
   const int64_t most = T / TM + S + 1;
   return most < T ? most : T;
-}
-
-int shrink_mt(int64_t T, int64_t S, int R) {
-  if (short_segments(T, S)) return 1;
-  return R <= 32 ? 4 : R <= 64 ? 2 : 1;
-}
-
-// K splits of the shrink kernel: about two CTAs for each SM, each with at
-// least one 64-wide block per warp.
-int shrink_splits(int64_t T, int64_t S, int64_t K, int R) {
-  const int64_t tiles = T / (16 * shrink_mt(T, S, R)) + (S < T ? S : T);
-  const int64_t want = (304 + tiles - 1) / (tiles > 0 ? tiles : 1);
-  const int64_t most = (K + 64 * kWarps - 1) / (64 * kWarps);
-  int64_t s = want < most ? want : most;
-  if (s > kMaxSplitK) s = kMaxSplitK;
-  return s < 1 ? 1 : static_cast<int>(s);
 }
 
 template <typename Kern, typename Args>
@@ -720,84 +923,111 @@ fp8la_status launch(Kern kern, dim3 grid, size_t smem, int cluster,
                                                           : FP8LA_ERR_CUDA;
 }
 
-template <bool F32, int MT, int NJ>
-fp8la_status launch_shrink_one(const ShrinkArgs &a, dim3 grid, cudaStream_t s) {
-  constexpr int kSmem = kWarps * 16 * MT * 8 * NJ * 4;
-  auto kern = lora_shrink_kernel<F32, MT, NJ>;
-  constexpr int slot = 16 + (F32 ? 12 : 0) + (NJ == 1 ? 0 : NJ == 2 ? 1 : NJ == 4 ? 2 : NJ == 8 ? 3 : 4) * 2 + (MT > 1 ? 1 : 0);
+// K split of the shrink kernel over a cluster: until every SM has a CTA (two
+// where they are small), each with at least two stages.
+template <bool F32, int MW, int MF, int NJ>
+fp8la_status launch_shrink_one(const ShrinkArgs &a, int slot, cudaStream_t s) {
+  using C = ShrinkCfg<F32, MW, MF, NJ>;
+  auto kern = lora_shrink_kernel<F32, MW, MF, NJ>;
+  if (once_per_device(slot, [&] {
+        return cudaFuncSetAttribute(
+            kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+      }) != cudaSuccess)
+    return FP8LA_ERR_CUDA;
+  const int64_t T = a.seg.T, S = a.seg.S;
+  const int64_t tiles = T / C::TM + (S < T ? S : T);
+  const int64_t want = C::kSmem > 100 * 1024 ? 152 : 304;
+  const int64_t stages = (a.K + C::KS - 1) / C::KS;
+  int cluster = 1;
+  while (cluster < kMaxCluster && tiles * cluster < want && stages >= 4 * cluster)
+    cluster *= 2;
+  return launch(kern,
+                dim3(cluster, static_cast<unsigned>(tile_bound(T, S, C::TM)), 1),
+                C::kSmem, cluster, a, s);
+}
+
+template <bool F32, int NJ>
+fp8la_status launch_shrink_nj(const ShrinkArgs &a, int slot, cudaStream_t s) {
+  // Rows of a tile: 16 for short segments, else 128, or 64 where that leaves
+  // too few tiles for the SMs even with K split over whole clusters.
+  if (short_segments(a.seg.T, a.seg.S))
+    return launch_shrink_one<F32, 1, 1, NJ>(a, slot, s);
+  if (a.seg.T < 152 * 128 / kMaxCluster)
+    return launch_shrink_one<F32, 4, 1, NJ>(a, slot + 1, s);
+  return launch_shrink_one<F32, 4, 2, NJ>(a, slot + 2, s);
+}
+
+template <bool F32>
+fp8la_status launch_shrink(const ShrinkArgs &a, cudaStream_t s) {
+  constexpr int slot = 16 + (F32 ? 15 : 0);
+  if (a.R <= 8) return launch_shrink_nj<F32, 1>(a, slot, s);
+  if (a.R <= 16) return launch_shrink_nj<F32, 2>(a, slot + 3, s);
+  if (a.R <= 32) return launch_shrink_nj<F32, 4>(a, slot + 6, s);
+  if (a.R <= 64) return launch_shrink_nj<F32, 8>(a, slot + 9, s);
+  return launch_shrink_nj<F32, 16>(a, slot + 12, s);
+}
+
+template <int TM, int KR>
+fp8la_status launch_expand_one(const ExpandArgs &a, int slot, cudaStream_t s) {
+  constexpr int kSmem = 2 * TM * (16 * KR + 8) * 2;
+  auto kern = lora_expand_kernel<TM, KR>;
   if (once_per_device(slot, [&] {
         return cudaFuncSetAttribute(
             kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
       }) != cudaSuccess)
     return FP8LA_ERR_CUDA;
+  const dim3 grid(static_cast<unsigned>((a.N + kExpandCols - 1) / kExpandCols),
+                  static_cast<unsigned>(tile_bound(a.seg.T, a.seg.S, TM)), 1);
   return launch(kern, grid, kSmem, 0, a, s);
 }
 
-template <bool F32>
-fp8la_status launch_shrink(const ShrinkArgs &a, int mt, int splits, int64_t T,
-                           int64_t S, cudaStream_t s) {
-  const dim3 grid(splits, static_cast<unsigned>(tile_bound(T, S, 16 * mt)), 1);
-  if (a.R <= 8)
-    return mt == 1 ? launch_shrink_one<F32, 1, 1>(a, grid, s)
-                   : launch_shrink_one<F32, 4, 1>(a, grid, s);
-  if (a.R <= 16)
-    return mt == 1 ? launch_shrink_one<F32, 1, 2>(a, grid, s)
-                   : launch_shrink_one<F32, 4, 2>(a, grid, s);
-  if (a.R <= 32)
-    return mt == 1 ? launch_shrink_one<F32, 1, 4>(a, grid, s)
-                   : launch_shrink_one<F32, 4, 4>(a, grid, s);
-  if (a.R <= 64)
-    return mt == 1 ? launch_shrink_one<F32, 1, 8>(a, grid, s)
-                   : launch_shrink_one<F32, 2, 8>(a, grid, s);
-  return launch_shrink_one<F32, 1, 16>(a, grid, s);
-}
-
 template <int TM>
-fp8la_status launch_expand_tm(const ExpandArgs &a, int64_t T, int64_t S,
-                              cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>((a.N + kExpandCols - 1) / kExpandCols),
-                  static_cast<unsigned>(tile_bound(T, S, TM)), 1);
-  if (a.R <= 16) return launch(lora_expand_kernel<TM, 1>, grid, 0, 0, a, s);
-  if (a.R <= 32) return launch(lora_expand_kernel<TM, 2>, grid, 0, 0, a, s);
-  if (a.R <= 64) return launch(lora_expand_kernel<TM, 4>, grid, 0, 0, a, s);
-  return launch(lora_expand_kernel<TM, 8>, grid, 0, 0, a, s);
+fp8la_status launch_expand_tm(const ExpandArgs &a, int slot, cudaStream_t s) {
+  if (a.R <= 16) return launch_expand_one<TM, 1>(a, slot, s);
+  if (a.R <= 32) return launch_expand_one<TM, 2>(a, slot + 1, s);
+  if (a.R <= 64) return launch_expand_one<TM, 4>(a, slot + 2, s);
+  return launch_expand_one<TM, 8>(a, slot + 3, s);
 }
 
-fp8la_status launch_expand(const ExpandArgs &a, int64_t T, int64_t S,
-                           cudaStream_t s) {
-  return short_segments(T, S) ? launch_expand_tm<16>(a, T, S, s)
-                              : launch_expand_tm<64>(a, T, S, s);
+fp8la_status launch_expand(const ExpandArgs &a, cudaStream_t s) {
+  return short_segments(a.seg.T, a.seg.S) ? launch_expand_tm<16>(a, 46, s)
+                                          : launch_expand_tm<128>(a, 50, s);
 }
 
 template <int MR>
-fp8la_status launch_outer(const OuterArgs &a, int cluster, cudaStream_t s) {
-  constexpr int kSmem = 16 * MR * (kOuterCols + 4) * 4;
+fp8la_status launch_outer(const OuterArgs &a, int slot, cudaStream_t s) {
+  constexpr int kSmem = OuterCfg<true, MR>::kSmem > OuterCfg<false, MR>::kSmem
+                            ? OuterCfg<true, MR>::kSmem : OuterCfg<false, MR>::kSmem;
   auto kern = lora_outer_kernel<MR>;
-  if (once_per_device(12 + MR, [&] {
+  if (once_per_device(slot, [&] {
         return cudaFuncSetAttribute(
             kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
       }) != cudaSuccess)
     return FP8LA_ERR_CUDA;
   const int64_t blocks = (a.side[0].N + kOuterCols - 1) / kOuterCols +
                          (a.side[1].N + kOuterCols - 1) / kOuterCols;
+  // CTAs that share out an adapter's rows: until every SM has one, each with
+  // two stages or more on average.
+  int cluster = 1;
+  while (cluster < kMaxCluster && blocks * a.seg.n * cluster < 152 &&
+         a.seg.T / a.seg.n >= 256 * cluster)
+    cluster *= 2;
   return launch(kern, dim3(cluster, static_cast<unsigned>(blocks),
-                           static_cast<unsigned>(a.seg.n * a.rank_blocks)),
+                           static_cast<unsigned>(a.seg.n)),
                 kSmem, cluster, a, s);
 }
 
 constexpr int64_t kMaxWidth = int64_t(1) << 22;  // grid limits
 
-int64_t part_bytes(int64_t T, int64_t S, int64_t width, int R) {
-  return (shrink_splits(T, S, width, R) * T * ((R + 15) / 16 * 16) * 4 + 255) /
-         256 * 256;
-}
+// V (or dv) of every row, FP32.
+int64_t v_bytes(int64_t T, int R) { return T * ((R + 3) / 4 * 4) * 4; }
 
 fp8la_status check_common(int64_t T, int32_t S, int32_t n, int32_t R, int64_t K,
                           int64_t N) {
   if (T < 0 || S < 0 || n < 1 || R < 1 || K < 1 || N < 1)
     return FP8LA_ERR_INVALID_ARG;
   if (S > kMaxSegments || R > kMaxRank || T > (int64_t(1) << 19) ||
-      K > kMaxWidth || N > kMaxWidth || n > 16383)
+      K > kMaxWidth || N > kMaxWidth || n > 65535)
     return FP8LA_ERR_UNSUPPORTED;
   return FP8LA_OK;
 }
@@ -816,8 +1046,8 @@ bool aligned_to(const void *p, int size) {
 
 fp8la_status run_shrink(const Segments &seg, const void *X, int32_t dtype,
                         int64_t ldx, const uint16_t *P, int64_t ldp,
-                        int64_t stride, int64_t K, int32_t R, float *part,
-                        cudaStream_t s) {
+                        int64_t stride, int64_t K, int32_t R, const float *alpha,
+                        float *V, int64_t ldv, cudaStream_t s) {
   ShrinkArgs a{};
   a.seg = seg;
   a.X = X;
@@ -827,33 +1057,26 @@ fp8la_status run_shrink(const Segments &seg, const void *X, int32_t dtype,
   a.stride_p = stride;
   a.K = K;
   a.R = R;
-  a.Rp = (R + 15) / 16 * 16;
   a.x_vec = vec_ok(X, ldx, dtype == FP8LA_TYPE_BF16 ? 2 : 4);
   a.p_vec = vec_ok(P, ldp, 2, stride);
-  a.part = part;
-  const int mt = shrink_mt(seg.T, seg.S, R);
-  const int splits = shrink_splits(seg.T, seg.S, K, R);
-  return dtype == FP8LA_TYPE_BF16
-             ? launch_shrink<false>(a, mt, splits, seg.T, seg.S, s)
-             : launch_shrink<true>(a, mt, splits, seg.T, seg.S, s);
+  a.alpha = alpha;
+  a.V = V;
+  a.ldv = ldv;
+  return dtype == FP8LA_TYPE_BF16 ? launch_shrink<false>(a, s)
+                                  : launch_shrink<true>(a, s);
 }
 
-fp8la_status run_expand(const Segments &seg, const float *part, int splits,
-                        int32_t R, const float *alpha, bool scale_v, float *v,
-                        int64_t ldv, const uint16_t *P, int64_t ldp,
+fp8la_status run_expand(const Segments &seg, const float *V, int64_t ldv, int32_t R,
+                        const float *alpha, const uint16_t *P, int64_t ldp,
                         int64_t stride, int64_t N, const uint16_t *base,
                         int64_t ld_base, uint16_t *out, int64_t ld_out,
                         cudaStream_t s) {
   ExpandArgs a{};
   a.seg = seg;
-  a.part = part;
-  a.splits = splits;
-  a.R = R;
-  a.Rp = (R + 15) / 16 * 16;
-  a.alpha = alpha;
-  a.scale_v = scale_v;
-  a.v_out = v;
+  a.V = V;
   a.ldv = ldv;
+  a.R = R;
+  a.alpha = alpha;
   a.P = P;
   a.ldp = ldp;
   a.stride_p = stride;
@@ -865,7 +1088,7 @@ fp8la_status run_expand(const Segments &seg, const float *part, int splits,
   a.p_vec = vec_ok(P, ldp, 2, stride);
   a.base_vec = vec_ok(base, ld_base, 2);
   a.out_vec = vec_ok(out, ld_out, 2);
-  return launch_expand(a, seg.T, seg.S, s);
+  return launch_expand(a, s);
 }
 
 }  // namespace
@@ -873,18 +1096,9 @@ fp8la_status run_expand(const Segments &seg, const float *part, int splits,
 
 using namespace fp8la;
 
-extern "C" int64_t fp8la_lora_apply_workspace_bytes(int64_t rows, int32_t segments,
-                                                    int64_t K, int32_t rank) {
-  const fp8la_status st = check_common(rows, segments, 1, rank, K, 1);
-  return st != FP8LA_OK ? st : part_bytes(rows, segments, K, rank);
-}
-
-extern "C" int64_t fp8la_lora_backward_workspace_bytes(int64_t rows,
-                                                       int32_t segments,
-                                                       int64_t N, int32_t rank) {
-  const fp8la_status st = check_common(rows, segments, 1, rank, 1, N);
-  if (st != FP8LA_OK) return st;
-  return part_bytes(rows, segments, N, rank) + rows * ((rank + 15) / 16 * 16) * 4;
+extern "C" int64_t fp8la_lora_workspace_bytes(int64_t rows, int32_t rank) {
+  const fp8la_status st = check_common(rows, 0, 1, rank, 1, 1);
+  return st != FP8LA_OK ? st : v_bytes(rows, rank);
 }
 
 extern "C" fp8la_status fp8la_lora_apply(
@@ -893,23 +1107,20 @@ extern "C" fp8la_status fp8la_lora_apply(
     const uint16_t *B, int64_t ldb, int64_t stride_b, const float *alpha,
     int32_t num_adapters, int32_t rank, int64_t K, int64_t N,
     int32_t num_segments, const int32_t *m_offsets, const int32_t *adapter_ids,
-    uint16_t *out, int64_t ld_out, float *v, int64_t ldv, void *workspace,
-    int64_t workspace_bytes, fp8la_stream_t stream) {
+    uint16_t *out, int64_t ld_out, float *v, int64_t ldv,
+    fp8la_stream_t stream) {
   if (x_dtype != FP8LA_TYPE_F32 && x_dtype != FP8LA_TYPE_BF16)
     return FP8LA_ERR_INVALID_ARG;
   fp8la_status st = check_common(rows, num_segments, num_adapters, rank, K, N);
   if (st != FP8LA_OK) return st;
   if (rows == 0) return FP8LA_OK;
   if (!base || !x || !alpha || !m_offsets || (num_segments > 0 && !adapter_ids) ||
-      !out || ld_base < N || ldx < K || ld_out < N || (v && ldv < rank))
-    return FP8LA_ERR_INVALID_ARG;
-  if (!workspace ||
-      workspace_bytes < part_bytes(rows, num_segments, K, rank))
+      !out || !v || ld_base < N || ldx < K || ld_out < N || ldv < rank)
     return FP8LA_ERR_INVALID_ARG;
   if ((st = check_factor(A, lda, stride_a, K, num_adapters, rank)) != FP8LA_OK ||
       (st = check_factor(B, ldb, stride_b, N, num_adapters, rank)) != FP8LA_OK)
     return st;
-  if (!aligned_to(base, 2) || !aligned_to(out, 2) || !aligned16(workspace) ||
+  if (!aligned_to(base, 2) || !aligned_to(out, 2) ||
       !aligned_to(x, x_dtype == FP8LA_TYPE_BF16 ? 2 : 4) || !aligned_to(alpha, 4) ||
       !aligned_to(v, 4))
     return FP8LA_ERR_ALIGNMENT;
@@ -918,12 +1129,10 @@ extern "C" fp8la_status fp8la_lora_apply(
                num_adapters, status_word_ptr()};
   if (!seg.status) return FP8LA_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  float *part = static_cast<float *>(workspace);
-  st = run_shrink(seg, x, x_dtype, ldx, A, lda, stride_a, K, rank, part, s);
+  st = run_shrink(seg, x, x_dtype, ldx, A, lda, stride_a, K, rank, nullptr, v, ldv, s);
   if (st == FP8LA_OK)
-    st = run_expand(seg, part, shrink_splits(rows, num_segments, K, rank), rank,
-                    alpha, false, v, ldv, B, ldb, stride_b, N, base, ld_base, out,
-                    ld_out, s);
+    st = run_expand(seg, v, ldv, rank, alpha, B, ldb, stride_b, N, base, ld_base,
+                    out, ld_out, s);
   return st == FP8LA_OK ? launch_status() : st;
 }
 
@@ -944,12 +1153,10 @@ extern "C" fp8la_status fp8la_lora_backward(
   if (st != FP8LA_OK) return st;
   if (!dA || !dB || !alpha || !m_offsets || (num_segments > 0 && !adapter_ids))
     return FP8LA_ERR_INVALID_ARG;
-  const int Rp = (rank + 15) / 16 * 16;
-  const int64_t part = part_bytes(rows, num_segments, N, rank);
   if (rows > 0) {
     if (!dy || !x || !v || !dx_base || !dx || ld_dy < N || ldx < K || ldv < rank ||
         ld_dx_base < K || ld_dx < K || !workspace ||
-        workspace_bytes < part + rows * Rp * 4)
+        workspace_bytes < v_bytes(rows, rank))
       return FP8LA_ERR_INVALID_ARG;
   }
   if ((st = check_factor(A, lda, stride_a, K, num_adapters, rank)) != FP8LA_OK ||
@@ -965,31 +1172,29 @@ extern "C" fp8la_status fp8la_lora_backward(
                num_adapters, status_word_ptr()};
   if (!seg.status) return FP8LA_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  float *parts = static_cast<float *>(workspace);
-  float *dv = reinterpret_cast<float *>(static_cast<char *>(workspace) + part);
+  float *dv = static_cast<float *>(workspace);
+  const int64_t ld_dv = (rank + 3) / 4 * 4;
   if (rows > 0) {
-    st = run_shrink(seg, dy, dy_dtype, ld_dy, B, ldb, stride_b, N, rank, parts, s);
+    st = run_shrink(seg, dy, dy_dtype, ld_dy, B, ldb, stride_b, N, rank, alpha, dv,
+                    ld_dv, s);
     if (st == FP8LA_OK)
-      st = run_expand(seg, parts, shrink_splits(rows, num_segments, N, rank), rank,
-                      alpha, true, dv, Rp, A, lda, stride_a, K, dx_base,
+      st = run_expand(seg, dv, ld_dv, rank, nullptr, A, lda, stride_a, K, dx_base,
                       ld_dx_base, dx, ld_dx, s);
     if (st != FP8LA_OK) return st;
   }
   OuterArgs o{};
   o.seg = seg;
-  o.side[0] = {dv, Rp, x, ldx, K, dA, vec_ok(x, ldx, x_dtype == FP8LA_TYPE_BF16 ? 2 : 4),
+  o.side[0] = {dv, ld_dv, x, ldx, K, dA,
+               vec_ok(x, ldx, x_dtype == FP8LA_TYPE_BF16 ? 2 : 4),
                x_dtype == FP8LA_TYPE_F32, 0};
   o.side[1] = {v, ldv, dy, ld_dy, N, dB,
                vec_ok(dy, ld_dy, dy_dtype == FP8LA_TYPE_BF16 ? 2 : 4),
                dy_dtype == FP8LA_TYPE_F32, 1};
   o.alpha = alpha;
   o.R = rank;
-  const int mr = rank <= 16 ? 1 : 2;
-  o.rank_blocks = (rank + 16 * mr - 1) / (16 * mr);
-  // CTAs that share out an adapter's rows: 32 rows or more for each of a
-  // CTA's row warps.
-  int cluster = 1;
-  while (cluster < 8 && rows / num_adapters >= 128 * cluster) cluster *= 2;
-  st = mr == 1 ? launch_outer<1>(o, cluster, s) : launch_outer<2>(o, cluster, s);
+  st = rank <= 16   ? launch_outer<1>(o, 12, s)
+       : rank <= 32 ? launch_outer<2>(o, 13, s)
+       : rank <= 64 ? launch_outer<4>(o, 14, s)
+                    : launch_outer<8>(o, 15, s);
   return st == FP8LA_OK ? launch_status() : st;
 }

@@ -294,18 +294,16 @@ def test_repeatable_graph_and_streams():
         got = fl.lora_apply(*fa) + fl.lora_backward(*ba)
         assert all(torch.equal(a, b) for a, b in zip(want, got))
     mine = [torch.zeros_like(t) for t in want]
-    w1 = torch.full((fl.fp8la_lora_apply_workspace_bytes(300, 4, 640, 32),), 0xFF,
-                    dtype=torch.uint8, device="cuda")
-    w2 = torch.full((fl.fp8la_lora_backward_workspace_bytes(300, 4, 384, 32),), 0xFF,
-                    dtype=torch.uint8, device="cuda")
+    w2 = torch.full((fl.fp8la_lora_workspace_bytes(300, 32),), 0xFF, dtype=torch.uint8,
+                    device="cuda")
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(s):
-        fl.lora_apply(*fa, out=mine[0], v=mine[1], workspace=w1)
+        fl.lora_apply(*fa, out=mine[0], v=mine[1])
     s.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        fl.lora_apply(*fa, out=mine[0], v=mine[1], workspace=w1)
+        fl.lora_apply(*fa, out=mine[0], v=mine[1])
         ba[2] = mine[1]
         fl.lora_backward(*ba, dx=mine[2], dA=mine[3], dB=mine[4], workspace=w2)
     for _ in range(2):
@@ -369,7 +367,8 @@ def test_refusals():
     c = make(20, [20], [0], 1, 16, 64, 64)
     fa = [c[k] for k in ("base", "x", "A", "B", "alpha", "m_offsets", "adapter_ids")]
     with pytest.raises(fl.Fp8laError) as e:
-        fl.lora_apply(*fa, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+        fl.lora_backward(c["dy"], c["x"], random_v(c), *fa[2:], c["dx_base"],
+                         workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
     assert e.value.status == fl.FP8LA_ERR_INVALID_ARG
     with pytest.raises(AssertionError):
         fl.lora_apply(*fa[:2], c["A"].float(), *fa[3:])
