@@ -17,7 +17,7 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 OBJ_DIR = os.path.join(PKG_DIR, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libfp8la.so")
 SOURCES = ["common.cu", "quantize.cu", "gemm.cu", "gemm_block32.cu",
-           "moe_route.cu", "moe_layer.cu", "lora.cu"]
+           "moe_route.cu", "moe_layer.cu", "lora.cu", "lora_tma.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr"]

@@ -32,52 +32,15 @@
 // rounded to BF16.  base + delta is added in FP32 and rounded once.
 #include <cuda_bf16.h>
 
-#include "internal.h"
-#include "ptx.cuh"
+#include "lora.cuh"
 
 namespace fp8la {
 namespace {
 
+using namespace lora;
+
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxSegments = 1024;
-constexpr int kMaxRank = 128;
-constexpr int kMaxCluster = 8;
-
-struct Segments {
-  const int32_t *offsets;   // [S + 1]
-  const int32_t *ids;       // [S], -1: no adapter
-  int32_t S, T, n;
-  unsigned *status;
-};
-
-// ------------------------------------------------------------ small helpers
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t *>(&b);
-}
-__device__ __forceinline__ float bf_lo(uint32_t w) {
-  return __uint_as_float(w << 16);
-}
-__device__ __forceinline__ float bf_hi(uint32_t w) {
-  return __uint_as_float(w & 0xffff0000u);
-}
-
-// (a, b) as NT BF16 pairs whose sum is the pair to 8 NT significant bits.
-// A non-finite value is carried by the first term alone.
-template <int NT>
-__device__ __forceinline__ void split_pair(float a, float b, uint32_t (&w)[NT]) {
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    w[t] = pack_bf16(a, b);
-    if (t + 1 < NT) {
-      a -= bf_lo(w[t]);
-      b -= bf_hi(w[t]);
-      if (!(fabsf(a) < 3.0e38f)) a = 0.0f;
-      if (!(fabsf(b) < 3.0e38f)) b = 0.0f;
-    }
-  }
-}
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1,
                                          uint32_t a2, uint32_t a3, uint32_t b0,
@@ -199,115 +162,7 @@ __device__ __forceinline__ void copy_tile(uint32_t dst, const char *src, int64_t
   }
 }
 
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t n;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
-  return n;
-}
-
-// Sum over the cluster's CTAs, in rank order, of the float at address `addr`
-// of each one's shared memory.
-__device__ __forceinline__ float cluster_sum(uint32_t addr, uint32_t n) {
-  float s = 0.0f;
-  for (uint32_t p = 0; p < n; ++p) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                 : "=f"(v)
-                 : "r"(mapa_shared(addr, p)));
-    s += v;
-  }
-  return s;
-}
-
-// Exclusive prefix sum over the CTA; total in *all.
-__device__ __forceinline__ int block_exclusive(int v, int *warp_sums, int *all) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int s = v;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int o = __shfl_up_sync(0xffffffffu, s, d);
-    if (lane >= d) s += o;
-  }
-  if (lane == 31) warp_sums[warp] = s;
-  __syncthreads();
-  int before = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const int x = warp_sums[w];
-    if (w < warp) before += x;
-    total += x;
-  }
-  __syncthreads();
-  *all = total;
-  return before + s - v;
-}
-
-struct Found {
-  int id, row0, rows;  // rows 0: no such tile
-};
-
-// Row tile `tile` of the segments cut into tiles of up to TM rows, the rows
-// after the last segment counting as one more without an adapter.  Offsets
-// that decrease, leave 0..T or ids outside -1..n-1 are recorded and no tile
-// is found.
-__device__ __forceinline__ Found find_tile(const Segments &g, int tile, int TM,
-                                           int *warp_sums, Found *slot) {
-  constexpr int kPer = (kMaxSegments + 1 + kThreads - 1) / kThreads;
-  // Threads share out the segments evenly, so that few need one round.
-  const int per = (g.S + 1 + kThreads - 1) / kThreads;
-  int lo[kPer], hi[kPer], sum = 0;
-  bool bad = false;
-  if (threadIdx.x == 0) *slot = {-1, 0, 0};
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int s = threadIdx.x * per + i;
-    lo[i] = hi[i] = 0;
-    if (i < per && s <= g.S) {
-      lo[i] = g.offsets[s];
-      hi[i] = s < g.S ? g.offsets[s + 1] : g.T;
-      bad |= lo[i] < 0 || hi[i] < lo[i] || hi[i] > g.T || (s == 0 && lo[i] != 0);
-      if (s < g.S) bad |= g.ids[s] < -1 || g.ids[s] >= g.n;
-      sum += (hi[i] - lo[i] + TM - 1) / TM;
-    }
-  }
-  bad = __syncthreads_or(bad);
-  if (bad) {
-    if (threadIdx.x == 0) atomicOr(g.status, kStatusBadDeviceArg);
-    return {-1, 0, 0};
-  }
-  int all;
-  int at = block_exclusive(sum, warp_sums, &all);
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int s = threadIdx.x * per + i;
-    if (i < per && s <= g.S) {
-      const int tiles = (hi[i] - lo[i] + TM - 1) / TM;
-      if (tile >= at && tile < at + tiles) {
-        const int r0 = lo[i] + (tile - at) * TM;
-        *slot = {s < g.S ? g.ids[s] : -1, r0, min(TM, hi[i] - r0)};
-      }
-      at += tiles;
-    }
-  }
-  __syncthreads();
-  return *slot;
-}
-
 // ------------------------------------------------------------------- shrink
-struct ShrinkArgs {
-  Segments seg;
-  const void *X;
-  int64_t ldx;
-  const uint16_t *P;
-  int64_t ldp, stride_p;
-  int64_t K;
-  int32_t R;
-  int32_t x_vec, p_vec;
-  const float *alpha;  // null: 1
-  float *V;            // [T][ldv]
-  int64_t ldv;
-};
-
 // MW groups of warps share out the rows (MF fragments of 16 each), KW = 8 / MW
 // the K of a stage; NJ rank fragments of 8 (even where more than one).
 template <bool F32, int MW, int MF, int NJ>
@@ -342,7 +197,7 @@ __global__ void __launch_bounds__(kThreads)
   __shared__ Found slot;
   pdl_wait();
   pdl_launch_dependents();
-  const Found f = find_tile(a.seg, blockIdx.y, C::TM, warp_sums, &slot);
+  const Found f = find_tile<kThreads>(a.seg, blockIdx.y, C::TM, warp_sums, &slot);
   if (f.rows == 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t crank = cluster_ctarank(), csize = cluster_size();
@@ -475,6 +330,7 @@ struct ExpandArgs {
   uint16_t *out;
   int64_t ld_base, ld_out;
   int32_t p_vec, base_vec, out_vec;
+  int32_t tm;            // rows of a tile
 };
 
 constexpr int kExpandCols = 64 * kWarps;
@@ -525,13 +381,28 @@ __device__ __forceinline__ void load_rank_block(const ExpandArgs &a,
     }
 }
 
-// One warp per 64 columns; KR blocks of 16 ranks; tiles of TM rows.
+// One warp per 64 columns; KR blocks of 16 ranks; tiles of tm <= TM rows (a
+// multiple of 16).  Each warp
+// streams its own 16-row pieces of base through a ring in shared memory, kRing
+// deep, with nothing to wait for but its own copies.
+constexpr int kRing = 4;
+constexpr int kPiece = 16 * 128;  // bytes: 16 rows of 64 columns
+
+template <int TM, int KR>
+struct ExpandCfg {
+  static constexpr int kLd = 16 * KR + 8;  // padded row of a term, in BF16
+  static constexpr int kV = 2 * TM * kLd * 2;
+  static constexpr int kSmem = kV + kWarps * kRing * kPiece;
+  static_assert(kV % 16 == 0 && kSmem <= 226 * 1024, "shared memory");
+};
+
 template <int TM, int KR>
 __global__ void __launch_bounds__(kThreads)
     lora_expand_kernel(const ExpandArgs a) {
-  constexpr int kLd = 16 * KR + 8;  // padded row of a term, in BF16
+  using C = ExpandCfg<TM, KR>;
   constexpr bool kHold = KR <= 4;   // the factor stays in registers
-  extern __shared__ __align__(16) uint16_t sv[];  // [2][TM][kLd]
+  extern __shared__ __align__(16) char smem[];
+  uint16_t *sv = reinterpret_cast<uint16_t *>(smem);  // [2][TM][kLd]
   __shared__ int warp_sums[kWarps];
   __shared__ Found slot;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -540,53 +411,61 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t c = col + 16 * q;
   pdl_wait();
   pdl_launch_dependents();
-  const Found f = find_tile(a.seg, blockIdx.y, TM, warp_sums, &slot);
+  const Found f = find_tile<kThreads>(a.seg, blockIdx.y, a.tm, warp_sums, &slot);
   if (f.rows == 0) return;
   const bool on = f.id >= 0;
   const uint16_t *P = a.P + (on ? f.id : 0) * a.stride_p;
+  const uint16_t *base = a.base + static_cast<int64_t>(f.row0) * a.ld_base;
+  uint16_t *out = a.out + static_cast<int64_t>(f.row0) * a.ld_out;
+  if (!on && base == out) return;
 
-  // The factor's fragments and the first rows of base are on their way while
-  // V is split.
+  // The factor's fragments and the first pieces of base are on their way
+  // while V is split.
   uint32_t b[kHold ? KR : 1][8][2];
   if (kHold && on && col < a.N)
 #pragma unroll
     for (int k = 0; k < KR; ++k)
       load_rank_block(a, P, 16 * k, q, col + 8 * g, b[kHold ? k : 0]);
-  uint32_t next[2][8];
-  auto load_base = [&](int m) {
+  const int pieces = (f.rows + 15) / 16;
+  const uint32_t ring = smem_addr(smem) + C::kV + warp * kRing * kPiece;
+  // Rows of 128 bytes; a row's 16-byte units are permuted by its number, so
+  // that eight lanes with as many rows and units meet different banks.
+  auto fetch = [&](int m) {
+    if (a.base_vec && m < pieces && col < a.N) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = 16 * m + 8 * h + g;
-      load_bf16x16(r < f.rows && col < a.N
-                       ? a.base + (f.row0 + static_cast<int64_t>(r)) * a.ld_base
-                       : nullptr,
-                   c, a.N, a.base_vec, next[h]);
+      for (int i = 0; i < 4; ++i) {
+        const int r = (lane >> 3) + 4 * i, u = lane & 7;
+        const int64_t cc = col + 8 * u;
+        const int n = 16 * m + r < f.rows && cc < a.N
+                          ? static_cast<int>(min(static_cast<int64_t>(8), a.N - cc)) : 0;
+        const uint16_t *p = base + (n > 0 ? (16 * m + r) * a.ld_base + cc : 0);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         ring + (m % kRing) * kPiece + r * 128 + ((u ^ (r & 7)) << 4)),
+                     "l"(p), "r"(2 * n)
+                     : "memory");
+      }
     }
+    cp_async_commit();
   };
-  load_base(0);
+#pragma unroll
+  for (int m = 0; m < kRing - 1; ++m) fetch(m);
   const float alpha = !on ? 0.0f : a.alpha ? a.alpha[f.id] : 1.0f;
-  const int vrows = min(TM, (f.rows + 15) / 16 * 16);
   if (on)
-    for (int i = threadIdx.x; i < vrows * 8 * KR; i += kThreads) {
+    for (int i = threadIdx.x; i < pieces * 16 * 8 * KR; i += kThreads) {
       const int r = i / (8 * KR), j = 2 * (i - r * 8 * KR);
       const float *v = a.V + (f.row0 + static_cast<int64_t>(r)) * a.ldv + j;
       const float v0 = r < f.rows && j < a.R ? __ldcg(v) * alpha : 0.0f;
       const float v1 = r < f.rows && j + 1 < a.R ? __ldcg(v + 1) * alpha : 0.0f;
       uint32_t t[2];
       split_pair<2>(v0, v1, t);
-      *reinterpret_cast<uint32_t *>(sv + r * kLd + j) = t[0];
-      *reinterpret_cast<uint32_t *>(sv + (TM + r) * kLd + j) = t[1];
+      *reinterpret_cast<uint32_t *>(sv + r * C::kLd + j) = t[0];
+      *reinterpret_cast<uint32_t *>(sv + (TM + r) * C::kLd + j) = t[1];
     }
   __syncthreads();
   if (col >= a.N) return;
-  const uint32_t sv_lane = smem_addr(sv) + ((lane & 15) * kLd + 8 * (lane >> 4)) * 2;
-  for (int m = 0; 16 * m < f.rows; ++m) {
-    uint32_t w[2][8];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[h][i] = next[h][i];
-    if (16 * (m + 1) < f.rows) load_base(m + 1);
+  const uint32_t sv_lane =
+      smem_addr(sv) + ((lane & 15) * C::kLd + 8 * (lane >> 4)) * 2;
+  for (int m = 0; m < pieces; ++m) {
     float acc[8][4];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -599,7 +478,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           uint32_t v[4];
-          ldmatrix4(sv_lane + ((t * TM + 16 * m) * kLd + 16 * k) * 2, v);
+          ldmatrix4(sv_lane + ((t * TM + 16 * m) * C::kLd + 16 * k) * 2, v);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             mma16816(acc[i], v[0], v[1], v[2], v[3], b[kHold ? k : 0][i][0],
@@ -607,56 +486,57 @@ __global__ void __launch_bounds__(kThreads)
         }
       }
     }
+    cp_async_wait<kRing - 2>();
+    __syncwarp();  // the piece is whole, and the one before it has been read
+    fetch(m + kRing - 1);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int r = 16 * m + 8 * h + g;
       if (r >= f.rows) continue;
+      uint32_t w[8];
+      if (a.base_vec) {
+        const char *p = smem + C::kV + (warp * kRing + m % kRing) * kPiece +
+                        (8 * h + g) * 128;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint4 x = *reinterpret_cast<const uint4 *>(
+              p + (((2 * q + i) ^ (g & 7)) << 4));
+          w[4 * i] = x.x;
+          w[4 * i + 1] = x.y;
+          w[4 * i + 2] = x.z;
+          w[4 * i + 3] = x.w;
+        }
+      } else {
+        load_bf16x16(base + r * a.ld_base, c, a.N, false, w);
+      }
       if (on) {
         // Fragment i's columns 2q and 2q + 1 are columns i and 8 + i of the
         // lane's 16.
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          w[h][i] = pack_bf16(bf_lo(w[h][i]) + acc[2 * i][2 * h],
-                              bf_hi(w[h][i]) + acc[2 * i + 1][2 * h]);
-          w[h][4 + i] = pack_bf16(bf_lo(w[h][4 + i]) + acc[2 * i][2 * h + 1],
-                                  bf_hi(w[h][4 + i]) + acc[2 * i + 1][2 * h + 1]);
+          w[i] = pack_bf16(bf_lo(w[i]) + acc[2 * i][2 * h],
+                           bf_hi(w[i]) + acc[2 * i + 1][2 * h]);
+          w[4 + i] = pack_bf16(bf_lo(w[4 + i]) + acc[2 * i][2 * h + 1],
+                               bf_hi(w[4 + i]) + acc[2 * i + 1][2 * h + 1]);
         }
       }
-      store_bf16x16(a.out + (f.row0 + static_cast<int64_t>(r)) * a.ld_out, c, a.N,
-                    a.out_vec, w[h]);
+      store_bf16x16(out + r * a.ld_out, c, a.N, a.out_vec, w);
     }
   }
 }
 
 // -------------------------------------------------------------------- outer
-struct OuterSide {
-  const float *W;       // [T][ldw]
-  int64_t ldw;
-  const void *X;        // [T][ldx]
-  int64_t ldx;
-  int64_t N;
-  float *G;             // [n][R][N]
-  int32_t x_vec, x_f32;
-  int32_t use_alpha;
-};
-struct OuterArgs {
-  Segments seg;
-  OuterSide side[2];    // dA (dv, x) and dB (v, dy)
-  const float *alpha;
-  int32_t R;
-};
-
 constexpr int kOuterCols = 32 * kWarps;  // a warp has 32 columns
 
 // MR fragments of 16 ranks.  A stage is up to TS rows of one segment.
 template <bool F32, int MR>
 struct OuterCfg {
-  static constexpr int TS = F32 ? 32 : 64;
+  static constexpr int TS = 32;
   static constexpr int XT = F32 ? 3 : 1;    // terms of X; V has three
   // Padded rows: fragment loads touch every bank once.
   static constexpr int kLdX = kOuterCols * (F32 ? 4 : 2) + 16;
   static constexpr int kX = TS * kLdX;
-  static constexpr int STAGES = MR <= 4 ? 4 : 3;
+  static constexpr int STAGES = F32 ? 3 : 4;
   static constexpr int kLdW = 16 * MR + 8;  // row of a term of V, in BF16
   static constexpr int kTerm = TS * kLdW * 2;
   static constexpr int kW = STAGES * kX;    // [2 buffers][3 terms]
@@ -668,6 +548,9 @@ struct OuterCfg {
   static_assert(kPairs * kThreads == TS * 8 * MR, "pairs");
   static_assert(kSmem <= 212 * 1024, "shared memory");
 };
+// CTAs that fit on an SM with either type of X.
+template <int MR>
+constexpr int kOuterCtas = MR <= 2 ? 2 : 1;
 
 // A cluster of CTAs shares out the rows of one (adapter, 256 columns).
 template <bool F32, int MR>
@@ -708,8 +591,8 @@ __device__ __forceinline__ void outer_body(const OuterArgs &a, const OuterSide &
     return;  // every CTA of the grid sees the same
   }
   int nseg, nstep;
-  int at = block_exclusive(mine, warp_sums, &nseg);
-  int before = block_exclusive(steps, warp_sums, &nstep);
+  int at = block_exclusive<kThreads>(mine, warp_sums, &nseg);
+  int before = block_exclusive<kThreads>(steps, warp_sums, &nstep);
 #pragma unroll
   for (int i = 0; i < kPer; ++i)
     if (hi[i] > lo[i]) {
@@ -868,7 +751,7 @@ __device__ __forceinline__ void outer_body(const OuterArgs &a, const OuterSide &
 
 // grid: x = cluster rank, y = column block of either side, z = adapter.
 template <int MR>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kOuterCtas<MR>)
     lora_outer_kernel(const OuterArgs a) {
   extern __shared__ __align__(16) char smem[];
   __shared__ int seg_lo[kMaxSegments], seg_hi[kMaxSegments], seg_step[kMaxSegments];
@@ -893,38 +776,6 @@ bool vec_ok(const void *p, int64_t ld, int size, int64_t stride = 0) {
   return aligned16(p) && ld * size % 16 == 0 && stride * size % 16 == 0;
 }
 
-// Rows of a tile: short segments get the shortest tile, so that one-token
-// requests waste least of a fragment.
-bool short_segments(int64_t T, int64_t S) { return T <= 16 * S; }
-
-int64_t tile_bound(int64_t T, int64_t S, int64_t TM) {
-  const int64_t most = T / TM + S + 1;
-  return most < T ? most : T;
-}
-
-template <typename Kern, typename Args>
-fp8la_status launch(Kern kern, dim3 grid, size_t smem, int cluster,
-                    const Args &a, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 0 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? FP8LA_OK
-                                                          : FP8LA_ERR_CUDA;
-}
-
-// K split of the shrink kernel over a cluster: until every SM has a CTA (two
-// where they are small), each with at least two stages.
 template <bool F32, int MW, int MF, int NJ>
 fp8la_status launch_shrink_one(const ShrinkArgs &a, int slot, cudaStream_t s) {
   using C = ShrinkCfg<F32, MW, MF, NJ>;
@@ -935,15 +786,13 @@ fp8la_status launch_shrink_one(const ShrinkArgs &a, int slot, cudaStream_t s) {
       }) != cudaSuccess)
     return FP8LA_ERR_CUDA;
   const int64_t T = a.seg.T, S = a.seg.S;
-  const int64_t tiles = T / C::TM + (S < T ? S : T);
-  const int64_t want = C::kSmem > 100 * 1024 ? 152 : 304;
-  const int64_t stages = (a.K + C::KS - 1) / C::KS;
-  int cluster = 1;
-  while (cluster < kMaxCluster && tiles * cluster < want && stages >= 4 * cluster)
-    cluster *= 2;
+  // Half of the segments, about, end in a tile of their own.
+  const int64_t tiles = T / C::TM + ((S < T ? S : T) + 1) / 2;
+  const int64_t slots = 152 * (C::kSmem > 110 * 1024 ? 1 : C::kSmem > 50 * 1024 ? 2 : 4);
+  const int cluster = choose_cluster(tiles, (a.K + C::KS - 1) / C::KS, slots, 4);
   return launch(kern,
                 dim3(cluster, static_cast<unsigned>(tile_bound(T, S, C::TM)), 1),
-                C::kSmem, cluster, a, s);
+                kThreads, C::kSmem, cluster, s, a);
 }
 
 template <bool F32, int NJ>
@@ -968,17 +817,31 @@ fp8la_status launch_shrink(const ShrinkArgs &a, cudaStream_t s) {
 }
 
 template <int TM, int KR>
-fp8la_status launch_expand_one(const ExpandArgs &a, int slot, cudaStream_t s) {
-  constexpr int kSmem = 2 * TM * (16 * KR + 8) * 2;
+fp8la_status launch_expand_one(ExpandArgs a, int slot, cudaStream_t s) {
+  constexpr int kSmem = ExpandCfg<TM, KR>::kSmem;
   auto kern = lora_expand_kernel<TM, KR>;
   if (once_per_device(slot, [&] {
         return cudaFuncSetAttribute(
             kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
       }) != cudaSuccess)
     return FP8LA_ERR_CUDA;
-  const dim3 grid(static_cast<unsigned>((a.N + kExpandCols - 1) / kExpandCols),
-                  static_cast<unsigned>(tile_bound(a.seg.T, a.seg.S, TM)), 1);
-  return launch(kern, grid, kSmem, 0, a, s);
+  // Rows of a tile: the least time, with two CTAs on an SM that each take
+  // about as long to start as four 16-row pieces take to stream.
+  const int64_t T = a.seg.T, S = a.seg.S;
+  const int64_t blocks = (a.N + kExpandCols - 1) / kExpandCols;
+  int64_t cost = INT64_MAX;
+  for (int tm = 16; tm <= TM; tm += 16) {
+    const int64_t tiles = T / tm + ((S < T ? S : T) + 1) / 2;
+    const int64_t waves = (tiles * blocks + 303) / 304;
+    const int64_t t = waves * (tm / 16 + 4);
+    if (t <= cost) {
+      cost = t;
+      a.tm = tm;
+    }
+  }
+  const dim3 grid(static_cast<unsigned>(blocks),
+                  static_cast<unsigned>(tile_bound(T, S, a.tm)), 1);
+  return launch(kern, grid, kThreads, kSmem, 0, s, a);
 }
 
 template <int TM>
@@ -1006,16 +869,16 @@ fp8la_status launch_outer(const OuterArgs &a, int slot, cudaStream_t s) {
     return FP8LA_ERR_CUDA;
   const int64_t blocks = (a.side[0].N + kOuterCols - 1) / kOuterCols +
                          (a.side[1].N + kOuterCols - 1) / kOuterCols;
-  // CTAs that share out an adapter's rows: until every SM has one, each with
-  // two stages or more on average.
-  int cluster = 1;
-  while (cluster < kMaxCluster && blocks * a.seg.n * cluster < 152 &&
-         a.seg.T / a.seg.n >= 256 * cluster)
-    cluster *= 2;
+  const int cluster = choose_cluster(
+      blocks * a.seg.n, (a.seg.T + 32 * a.seg.n - 1) / (32 * a.seg.n),
+      152 * kOuterCtas<MR>, 6);
   return launch(kern, dim3(cluster, static_cast<unsigned>(blocks),
                            static_cast<unsigned>(a.seg.n)),
-                kSmem, cluster, a, s);
+                kThreads, kSmem, cluster, s, a);
 }
+
+constexpr bool kUseTma = true;
+constexpr int64_t kTmaRows = 256;
 
 constexpr int64_t kMaxWidth = int64_t(1) << 22;  // grid limits
 
@@ -1062,6 +925,10 @@ fp8la_status run_shrink(const Segments &seg, const void *X, int32_t dtype,
   a.alpha = alpha;
   a.V = V;
   a.ldv = ldv;
+  // Long segments of BF16 rows that TMA can read go to tcgen05.
+  if (dtype == FP8LA_TYPE_BF16 && a.x_vec && a.p_vec && kUseTma &&
+      !short_segments(seg.T, seg.S) && seg.T >= kTmaRows)
+    return launch_shrink_tma(a, s);
   return dtype == FP8LA_TYPE_BF16 ? launch_shrink<false>(a, s)
                                   : launch_shrink<true>(a, s);
 }
@@ -1192,6 +1059,11 @@ extern "C" fp8la_status fp8la_lora_backward(
                dy_dtype == FP8LA_TYPE_F32, 1};
   o.alpha = alpha;
   o.R = rank;
+  if (kUseTma && !o.side[0].x_f32 && !o.side[1].x_f32 && o.side[0].x_vec &&
+      o.side[1].x_vec && !short_segments(rows, num_segments) && rows >= kTmaRows) {
+    st = launch_outer_tma(o, s);
+    return st == FP8LA_OK ? launch_status() : st;
+  }
   st = rank <= 16   ? launch_outer<1>(o, 12, s)
        : rank <= 32 ? launch_outer<2>(o, 13, s)
        : rank <= 64 ? launch_outer<4>(o, 14, s)

@@ -1,0 +1,621 @@
+// The adapters' long sums for BF16 operands on the 5th-generation tensor cores:
+// V of rows (shrink) and the factors' gradients (outer); see lora.cu for the
+// formulas.
+//
+// Bound: X (x or dy) once from HBM.  mma.sync reaches 600 TFLOP/s here and its
+// fragments cost issue slots, which at ranks above 16 is more than the memory
+// time; tcgen05.mma takes both operands from shared memory as TMA left them.
+//
+// shrink: D[128 rows][R] += X[128][64 k] P[R][64 k]^T, both K-major.  K is
+// shared out over a cluster, whose CTAs' sums are added through distributed
+// shared memory in rank order.
+//
+// outer: D[128 columns][R] += X[t][128 columns]^T V[t][R], t being the MMA's
+// K.  X is the transposed (MN-major) operand, just as TMA writes a box of 64
+// columns x 64 rows.  V (FP32) enters as three BF16 terms, which converter
+// warps write K-major ([R][64 t]); all three are accumulated into the same
+// columns.  Rows past a segment's end belong to other requests and may hold
+// anything, so the converters overwrite those that a 16-row MMA step would
+// touch with zeros.
+#include "lora.cuh"
+
+namespace fp8la {
+namespace lora {
+namespace {
+
+// D[tmem] (+)= A[smem] * B[smem]^T, BF16 x BF16 -> F32, one elected thread.
+__device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t adesc,
+                                          uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(
+          d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor for kind::f16: BF16 A and B, F32 accumulator.
+//   bits 4-5 D format (1 = F32)    bits 7-9, 10-12 A, B format (1 = BF16)
+//   bit 15 A is MN-major           bits 17-22 N >> 3, 24-28 M >> 4
+__host__ __device__ constexpr uint32_t idesc_bf16_f32(uint32_t M, uint32_t N,
+                                                      bool a_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) |
+         ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+// Descriptor of an MN-major operand of 64-element (128-byte) swizzled rows, a
+// row for each K: 8-row groups 1024 bytes apart, 64-element blocks
+// `block_bytes` apart.
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr,
+                                                       uint32_t block_bytes) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(block_bytes >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+// 16 TMEM columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&u)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, "
+      "%8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(u[0]), "=f"(u[1]), "=f"(u[2]), "=f"(u[3]), "=f"(u[4]), "=f"(u[5]),
+        "=f"(u[6]), "=f"(u[7]), "=f"(u[8]), "=f"(u[9]), "=f"(u[10]),
+        "=f"(u[11]), "=f"(u[12]), "=f"(u[13]), "=f"(u[14]), "=f"(u[15])
+      : "r"(addr)
+      : "memory");
+}
+
+// ------------------------------------------------------------------- shrink
+constexpr int kSThreads = 192;      // warps 0-3 epilogue, 4 producer, 5 MMA
+constexpr int kSRows = 128;
+constexpr int kSK = 128;            // K of a stage: two boxes of 64
+
+// RP ranks, a multiple of 16.
+template <int RP>
+struct ShrinkTma {
+  static constexpr int kX = kSRows * kSK * 2;
+  static constexpr int kP = RP * kSK * 2;
+  static constexpr int kStage = kX + kP;
+  static constexpr int STAGES = 4 * kStage <= 200 * 1024 ? 4 : 3;
+  static constexpr int kTmemCols = RP < 32 ? 32 : RP;
+  static constexpr int kLdR = RP + 1;  // of the sums, in floats
+  static constexpr int kBar = STAGES * kStage;
+  static constexpr int kMisc = kBar + (2 * STAGES + 1) * 8;
+  static constexpr int kAlloc = kMisc + 32 + 1024;
+  static_assert(kSRows * kLdR * 4 <= STAGES * kStage, "the sums overlay the ring");
+  static_assert(kP % 1024 == 0 && kAlloc <= 226 * 1024, "shared memory");
+};
+
+template <int RP>
+__global__ void __launch_bounds__(kSThreads)
+    lora_shrink_tma_kernel(const __grid_constant__ CUtensorMap tmX,
+                           const __grid_constant__ CUtensorMap tmP,
+                           const ShrinkArgs a, const uint64_t timeout_ns) {
+  using C = ShrinkTma<RP>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int warp_sums[kSThreads / 32];
+  __shared__ Found slot;
+  const uint32_t raw_addr = smem_addr(smem_raw);
+  const uint32_t base = (raw_addr + 1023u) & ~1023u;
+  uint8_t *sbase = smem_raw + (base - raw_addr);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_launch_dependents();
+  const Found f = find_tile<kSThreads>(a.seg, blockIdx.y, kSRows, warp_sums, &slot);
+  if (f.rows == 0) return;
+  const uint32_t crank = cluster_ctarank(), csize = cluster_size();
+  if (f.id < 0) {  // rows without an adapter
+    if (crank == 0)
+      for (int i = threadIdx.x; i < f.rows * a.R; i += kSThreads)
+        a.V[(f.row0 + static_cast<int64_t>(i / a.R)) * a.ldv + i % a.R] = 0.0f;
+    return;
+  }
+  const uint32_t bar0 = base + C::kBar;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (C::STAGES + s); };
+  const uint32_t done_bar = bar0 + 8u * (2 * C::STAGES);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sbase + C::kMisc);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(sbase + C::kMisc + 4);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    mbar_init(done_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 5) {
+    tmem_alloc(smem_addr(tmem_slot), C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int nst = static_cast<int>((a.K + kSK - 1) / kSK);
+  const int s0 = static_cast<int>(static_cast<int64_t>(nst) * crank / csize);
+  const int s1 = static_cast<int>(static_cast<int64_t>(nst) * (crank + 1) / csize);
+  float *red = reinterpret_cast<float *>(sbase);
+
+  if (warp == 4) {
+    if (lane == 0) {
+      uint32_t s = 0, ph = 0, issued = 0;
+      for (int c = s0; c < s1; ++c) {
+        if (!mbar_wait(empty_bar(s), ph ^ 1u, timeout_ns, a.seg.status, abort_flag))
+          break;
+        const uint32_t d = base + s * C::kStage;
+        mbar_arrive_expect_tx(full_bar(s), C::kStage);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          tma_load_2d(d + h * (C::kX / 2), &tmX, full_bar(s), c * kSK + 64 * h, f.row0);
+          tma_load_3d(d + C::kX + h * (C::kP / 2), &tmP, full_bar(s),
+                      c * kSK + 64 * h, 0, f.id);
+        }
+        ++issued;
+        if (++s == C::STAGES) { s = 0; ph ^= 1u; }
+      }
+      for (uint32_t st = 0; st < C::STAGES; ++st) {
+        if (issued <= st) break;
+        const uint32_t arms = (issued - 1 - st) / C::STAGES + 1;
+        mbar_wait_drain(full_bar(st), (arms - 1) & 1u, timeout_ns, a.seg.status);
+      }
+    }
+  } else if (warp == 5) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(kSRows, RP, false);
+      uint32_t s = 0, ph = 0;
+      for (int c = s0; c < s1; ++c) {
+        if (!mbar_wait(full_bar(s), ph, timeout_ns, a.seg.status, abort_flag)) break;
+        tc_fence_after();
+        const uint32_t d = base + s * C::kStage;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint64_t ad = smem_desc_k128_sw128(d + h * (C::kX / 2));
+          const uint64_t bd = smem_desc_k128_sw128(d + C::kX + h * (C::kP / 2));
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_bf16(tmem_base, ad + 2u * k, bd + 2u * k, idesc,
+                      (c > s0 || h > 0 || k > 0) ? 1u : 0u);
+        }
+        umma_commit(empty_bar(s));
+        if (++s == C::STAGES) { s = 0; ph ^= 1u; }
+      }
+      umma_commit(done_bar);
+      mbar_wait_drain(done_bar, 0, timeout_ns, a.seg.status);
+    }
+  } else {
+    // The ring is free once the last MMA is done: the sums go there.
+    const bool ready = mbar_wait(done_bar, 0, timeout_ns, a.seg.status, abort_flag);
+    if (__all_sync(0xffffffffu, ready)) {
+      tc_fence_after();
+      const int row = 32 * warp + lane;
+      const uint32_t col0 = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
+#pragma unroll
+      for (int j = 0; j < RP; j += 16) {
+        float v[16];
+        tmem_ld16(col0 + j, v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) red[row * C::kLdR + j + i] = s1 > s0 ? v[i] : 0.0f;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem_base, C::kTmemCols);
+  }
+  __syncwarp();
+  const float alpha = a.alpha ? a.alpha[f.id] : 1.0f;
+  const int cells = f.rows * a.R;
+  if (csize > 1) cluster_sync_all();
+  for (int i = static_cast<int>(crank) * kSThreads + threadIdx.x; i < cells;
+       i += static_cast<int>(csize) * kSThreads) {
+    const int r = i / a.R, j = i - r * a.R;
+    const float v = csize > 1 ? cluster_sum(base + 4u * (r * C::kLdR + j), csize)
+                              : red[r * C::kLdR + j];
+    a.V[(f.row0 + static_cast<int64_t>(r)) * a.ldv + j] = v * alpha;
+  }
+  if (csize > 1) cluster_sync_all();  // no CTA leaves while its sums are read
+}
+
+// -------------------------------------------------------------------- outer
+constexpr int kOConv = 8;           // converter and epilogue warps
+constexpr int kOThreads = 32 * (kOConv + 2);
+constexpr int kOCols = 256;         // two MMA blocks of 128
+constexpr int kORows = 64;          // of a stage
+
+template <int RP>
+struct OuterTma {
+  static constexpr int kBox = 64 * 128;             // 64 rows x 64 columns
+  static constexpr int kX = 4 * kBox;
+  static constexpr int kTerm = RP * 128;            // [RP][64 t]
+  static constexpr int kV = 3 * kTerm;
+  // Two CTAs on an SM for the smallest ranks, so that one streams while the
+  // other starts or adds up.
+  static constexpr int STAGES = RP <= 32 ? 2 : 3;
+  static constexpr int kTmemCols = 2 * RP < 32 ? 32 : 2 * RP;
+  static constexpr int kVBuf = STAGES * kX;         // [2][3 terms]
+  static constexpr int kLdR = kOCols + 4;
+  static constexpr int kBar = kVBuf + 2 * kV;
+  static constexpr int kMisc = kBar + (3 * STAGES + 4 + 1) * 8;
+  static constexpr int kSegs = kMisc + 32;          // three lists
+  static constexpr int kAlloc = kSegs + 3 * kMaxSegments * 4 + 1024;
+  static_assert(RP * kLdR * 4 <= kBar, "the sums overlay the ring");
+  static_assert(kVBuf % 1024 == 0 && kTerm % 1024 == 0, "swizzle atoms");
+  static_assert(kAlloc <= 226 * 1024, "shared memory");
+};
+
+// grid: x = cluster rank (rows), y = column block of either side, z = adapter.
+template <int RP>
+__global__ void __launch_bounds__(kOThreads, RP <= 32 ? 2 : 1)
+    lora_outer_tma_kernel(const __grid_constant__ CUtensorMap tm0,
+                          const __grid_constant__ CUtensorMap tm1,
+                          const OuterArgs a, const uint64_t timeout_ns) {
+  using C = OuterTma<RP>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int warp_sums[kOThreads / 32];
+  const uint32_t raw_addr = smem_addr(smem_raw);
+  const uint32_t base = (raw_addr + 1023u) & ~1023u;
+  uint8_t *sbase = smem_raw + (base - raw_addr);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int *seg_lo = reinterpret_cast<int *>(sbase + C::kSegs);
+  int *seg_hi = seg_lo + kMaxSegments, *seg_step = seg_hi + kMaxSegments;
+  const uint32_t bar0 = base + C::kBar;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (C::STAGES + s); };
+  auto vready_bar = [&](int b) { return bar0 + 8u * (2 * C::STAGES + b); };
+  auto vfree_bar = [&](int b) { return bar0 + 8u * (2 * C::STAGES + 2 + b); };
+  const uint32_t done_bar = bar0 + 8u * (2 * C::STAGES + 4);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sbase + C::kMisc);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(sbase + C::kMisc + 4);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(vready_bar(b), kOConv);
+      mbar_init(vfree_bar(b), 1);
+    }
+    mbar_init(done_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  const int adapter = blockIdx.z;
+  const uint32_t crank = cluster_ctarank(), csize = cluster_size();
+
+  // The adapter's segments, in order, with the stages before each.
+  constexpr int kPer = (kMaxSegments + kOThreads - 1) / kOThreads;
+  const int per = (a.seg.S + kOThreads - 1) / kOThreads;
+  int lo[kPer], hi[kPer], mine = 0, steps = 0;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int s = threadIdx.x * per + i;
+    lo[i] = hi[i] = 0;
+    if (i < per && s < a.seg.S) {
+      const int l = a.seg.offsets[s], h = a.seg.offsets[s + 1];
+      const int id = a.seg.ids[s];
+      bad |= l < 0 || h < l || h > a.seg.T || (s == 0 && l != 0) || id < -1 ||
+             id >= a.seg.n;
+      if (id == adapter && h > l) {
+        lo[i] = l;
+        hi[i] = h;
+        ++mine;
+        steps += (h - l + kORows - 1) / kORows;
+      }
+    }
+  }
+  bad = __syncthreads_or(bad);
+  if (bad) {
+    if (threadIdx.x == 0) atomicOr(a.seg.status, kStatusBadDeviceArg);
+    return;  // every CTA of the grid sees the same
+  }
+  int nseg, nstep;
+  int at = block_exclusive<kOThreads>(mine, warp_sums, &nseg);
+  int before = block_exclusive<kOThreads>(steps, warp_sums, &nstep);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (hi[i] > lo[i]) {
+      seg_lo[at] = lo[i];
+      seg_hi[at] = hi[i];
+      seg_step[at] = before;
+      ++at;
+      before += (hi[i] - lo[i] + kORows - 1) / kORows;
+    }
+  if (warp == kOConv + 1) {
+    tmem_alloc(smem_addr(tmem_slot), C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int s0 = static_cast<int>(static_cast<int64_t>(nstep) * crank / csize);
+  const int s1 = static_cast<int>(static_cast<int64_t>(nstep) * (crank + 1) / csize);
+  const int blocks0 = static_cast<int>((a.side[0].N + kOCols - 1) / kOCols);
+  const bool second = static_cast<int>(blockIdx.y) >= blocks0;
+  const OuterSide &o = a.side[second];
+  const CUtensorMap *tm = second ? &tm1 : &tm0;
+  const int col0 = (blockIdx.y - (second ? blocks0 : 0)) * kOCols;
+  // First row and number of rows of stage s; `i` follows s upwards.
+  auto rows_of = [&](int s, int &i, int &t0) {
+    while (i + 1 < nseg && seg_step[i + 1] <= s) ++i;
+    t0 = seg_lo[i] + kORows * (s - seg_step[i]);
+    return min(kORows, seg_hi[i] - t0);
+  };
+
+  if (warp == kOConv) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      uint32_t s = 0, ph = 0, issued = 0;
+      int i = 0;
+      for (int c = s0; c < s1; ++c) {
+        if (!mbar_wait(empty_bar(s), ph ^ 1u, timeout_ns, a.seg.status, abort_flag))
+          break;
+        int t0;
+        rows_of(c, i, t0);
+        mbar_arrive_expect_tx(full_bar(s), C::kX);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          tma_load_2d(base + s * C::kX + j * C::kBox, tm, full_bar(s), col0 + 64 * j, t0);
+        ++issued;
+        if (++s == C::STAGES) { s = 0; ph ^= 1u; }
+      }
+      for (uint32_t st = 0; st < C::STAGES; ++st) {
+        if (issued <= st) break;
+        const uint32_t arms = (issued - 1 - st) / C::STAGES + 1;
+        mbar_wait_drain(full_bar(st), (arms - 1) & 1u, timeout_ns, a.seg.status);
+      }
+    }
+  } else if (warp == kOConv + 1) {
+    // ----------------------------------------------------------------- MMA
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(128, RP, true);
+      uint32_t s = 0, ph = 0;
+      int i = 0;
+      for (int c = s0; c < s1; ++c) {
+        const uint32_t b = (c - s0) & 1u, use = (c - s0) >> 1;
+        // The converters of a stage have seen its X.
+        if (!mbar_wait(full_bar(s), ph, timeout_ns, a.seg.status, abort_flag) ||
+            !mbar_wait(vready_bar(b), use & 1u, timeout_ns, a.seg.status, abort_flag))
+          break;
+        tc_fence_after();
+        int t0;
+        const int n = rows_of(c, i, t0);
+        const uint32_t x = base + s * C::kX;
+        const uint32_t v = base + C::kVBuf + b * C::kV;
+        for (int k = 0; 16 * k < n; ++k)
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            const uint64_t ad =
+                smem_desc_mn_sw128(x + 2 * m * C::kBox + k * 2048, C::kBox);
+#pragma unroll
+            for (int t = 0; t < 3; ++t)
+              umma_bf16(tmem_base + m * RP, ad,
+                        smem_desc_k128_sw128(v + t * C::kTerm) + 2u * k, idesc,
+                        (c > s0 || k > 0 || t > 0) ? 1u : 0u);
+          }
+        umma_commit(empty_bar(s));
+        umma_commit(vfree_bar(b));
+        if (++s == C::STAGES) { s = 0; ph ^= 1u; }
+      }
+      umma_commit(done_bar);
+      mbar_wait_drain(done_bar, 0, timeout_ns, a.seg.status);
+    }
+  } else {
+    // -------------------------------------------- converters, then epilogue
+    // A unit is one rank's 8 rows: 16 bytes of each term.
+    constexpr int kUnits = RP * 8 / (32 * kOConv);
+    static_assert(RP * 8 >= 32 * kOConv || RP == 16, "units");
+    constexpr int kU = kUnits > 0 ? kUnits : 1;
+    uint32_t s = 0, ph = 0;
+    int i_load = 0, i_fix = 0;
+    float w[kU][8];
+    auto load_v = [&](int c) {
+      int t0 = 0;
+      const int n = c < s1 ? rows_of(c, i_load, t0) : 0;
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int e = threadIdx.x + u * 32 * kOConv;
+        const int j = e % RP, t = 8 * (e / RP);
+        const float *p = o.W + (t0 + static_cast<int64_t>(t)) * o.ldw + j;
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          w[u][q] = t + q < n && j < a.R && e < RP * 8 ? __ldcg(p + q * o.ldw) : 0.0f;
+      }
+    };
+    load_v(s0);
+    bool ok = true;
+    for (int c = s0; c < s1; ++c) {
+      const uint32_t b = (c - s0) & 1u, use = (c - s0) >> 1;
+      const bool ready = mbar_wait(vfree_bar(b), (use & 1u) ^ 1u, timeout_ns,
+                                   a.seg.status, abort_flag);
+      if (!__all_sync(0xffffffffu, ready)) {
+        ok = false;
+        break;
+      }
+      const uint32_t v = base + C::kVBuf + b * C::kV;
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int e = threadIdx.x + u * 32 * kOConv;
+        const uint32_t j = e % RP, unit = e / RP;
+        uint32_t t[3][4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t p[3];
+          split_pair<3>(w[u][2 * q], w[u][2 * q + 1], p);
+#pragma unroll
+          for (int k = 0; k < 3; ++k) t[k][q] = p[k];
+        }
+        if (e < RP * 8)
+#pragma unroll
+          for (int k = 0; k < 3; ++k)
+            st_shared_v4(v + k * C::kTerm + j * 128 + ((unit ^ (j & 7u)) << 4), t[k][0],
+                         t[k][1], t[k][2], t[k][3]);
+      }
+      load_v(c + 1);
+      int t0;
+      const int n = rows_of(c, i_fix, t0);
+      if (n % 16 != 0) {
+        // Rows n.. of the last MMA step are other requests': zeros instead.
+        const bool full = mbar_wait(full_bar(s), ph, timeout_ns, a.seg.status, abort_flag);
+        if (!__all_sync(0xffffffffu, full)) {
+          ok = false;
+          break;
+        }
+        const int rows = 16 - n % 16;
+        for (int e = threadIdx.x; e < rows * 32; e += 32 * kOConv)
+          st_shared_v4(base + s * C::kX + (e & 3) * C::kBox + (n + (e >> 5)) * 128 +
+                           ((e >> 2) & 7) * 16,
+                       0, 0, 0, 0);
+      }
+      if (++s == C::STAGES) { s = 0; ph ^= 1u; }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(vready_bar(b));
+    }
+    // Thread = column of X; the two halves of the warps have a block each.
+    const bool ready =
+        ok && mbar_wait(done_bar, 0, timeout_ns, a.seg.status, abort_flag);
+    if (__all_sync(0xffffffffu, ready)) {
+      tc_fence_after();
+      const int m = warp >> 2;
+      const int cc = 128 * m + 32 * (warp & 3) + lane;
+      const uint32_t t = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16) + m * RP;
+      float *red = reinterpret_cast<float *>(sbase);
+      const float scale = o.use_alpha ? a.alpha[adapter] : 1.0f;
+#pragma unroll
+      for (int j = 0; j < RP; j += 16) {
+        float v[16];
+        tmem_ld16(t + j, v);
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          const float g = s1 > s0 ? v[q] : 0.0f;
+          if (csize > 1)
+            red[(j + q) * C::kLdR + cc] = g;
+          else if (j + q < a.R && col0 + cc < o.N)
+            o.G[(static_cast<int64_t>(adapter) * a.R + j + q) * o.N + col0 + cc] =
+                g * scale;
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kOConv + 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem_base, C::kTmemCols);
+  }
+  __syncwarp();
+  if (csize == 1) return;
+  cluster_sync_all();
+  const float scale = o.use_alpha ? a.alpha[adapter] : 1.0f;
+  const int cells = a.R * kOCols;
+  for (int i = static_cast<int>(crank) * kOThreads + threadIdx.x; i < cells;
+       i += static_cast<int>(csize) * kOThreads) {
+    const int r = i / kOCols, cc = i % kOCols;
+    if (col0 + cc >= o.N) continue;
+    o.G[(static_cast<int64_t>(adapter) * a.R + r) * o.N + col0 + cc] =
+        cluster_sum(base + 4u * (r * C::kLdR + cc), csize) * scale;
+  }
+  cluster_sync_all();  // no CTA leaves while its sums are read
+}
+
+// --------------------------------------------------------------------- host
+// BF16 matrices [outer][rows][width] as swizzled boxes of 64 columns.
+bool encode_bf16(CUtensorMap *m, const void *p, int64_t width, int64_t rows,
+                 int64_t outer, int64_t ld, int64_t stride, uint32_t box_rows,
+                 int dims_n) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(width),
+                              static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(outer)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2,
+                                 static_cast<cuuint64_t>(stride) * 2};
+  const cuuint32_t box[3] = {64, box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims_n, const_cast<void *>(p), dims,
+             strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int RP>
+fp8la_status shrink_one(const ShrinkArgs &a, int slot, cudaStream_t s) {
+  using C = ShrinkTma<RP>;
+  auto kern = lora_shrink_tma_kernel<RP>;
+  if (once_per_device(slot, [&] {
+        return cudaFuncSetAttribute(
+            kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kAlloc);
+      }) != cudaSuccess)
+    return FP8LA_ERR_CUDA;
+  CUtensorMap tmX, tmP;
+  const int64_t stride = a.seg.n > 1 ? a.stride_p : a.R * a.ldp;
+  if (!encode_bf16(&tmX, a.X, a.K, a.seg.T, 1, a.ldx, 0, kSRows, 2) ||
+      !encode_bf16(&tmP, a.P, a.K, a.R, a.seg.n, a.ldp, stride, RP, 3))
+    return FP8LA_ERR_CUDA;
+  const int64_t T = a.seg.T, S = a.seg.S;
+  const int64_t tiles = T / kSRows + ((S < T ? S : T) + 1) / 2;
+  const int cluster = choose_cluster(tiles, (a.K + kSK - 1) / kSK, 152, 6);
+  return launch(kern, dim3(cluster, static_cast<unsigned>(tile_bound(T, S, kSRows)), 1),
+                kSThreads, C::kAlloc, cluster, s, tmX, tmP, a, wait_timeout_ns());
+}
+
+template <int RP>
+fp8la_status outer_one(const OuterArgs &a, int slot, cudaStream_t s) {
+  using C = OuterTma<RP>;
+  auto kern = lora_outer_tma_kernel<RP>;
+  if (once_per_device(slot, [&] {
+        return cudaFuncSetAttribute(
+            kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kAlloc);
+      }) != cudaSuccess)
+    return FP8LA_ERR_CUDA;
+  CUtensorMap tm[2];
+  int64_t blocks = 0;
+  for (int i = 0; i < 2; ++i) {
+    const OuterSide &o = a.side[i];
+    if (!encode_bf16(&tm[i], o.X, o.N, a.seg.T, 1, o.ldx, 0, kORows, 2))
+      return FP8LA_ERR_CUDA;
+    blocks += (o.N + kOCols - 1) / kOCols;
+  }
+  const int64_t n = a.seg.n;
+  const int cluster =
+      choose_cluster(blocks * n, (a.seg.T + kORows * n - 1) / (kORows * n), 152, 6);
+  return launch(kern, dim3(cluster, static_cast<unsigned>(blocks),
+                           static_cast<unsigned>(n)),
+                kOThreads, C::kAlloc, cluster, s, tm[0], tm[1], a, wait_timeout_ns());
+}
+
+}  // namespace
+
+fp8la_status launch_shrink_tma(const ShrinkArgs &a, cudaStream_t s) {
+  return a.R <= 16   ? shrink_one<16>(a, 54, s)
+         : a.R <= 32 ? shrink_one<32>(a, 55, s)
+         : a.R <= 64 ? shrink_one<64>(a, 56, s)
+                     : shrink_one<128>(a, 57, s);
+}
+
+fp8la_status launch_outer_tma(const OuterArgs &a, cudaStream_t s) {
+  return a.R <= 16   ? outer_one<16>(a, 58, s)
+         : a.R <= 32 ? outer_one<32>(a, 59, s)
+         : a.R <= 64 ? outer_one<64>(a, 60, s)
+                     : outer_one<128>(a, 61, s);
+}
+
+}  // namespace lora
+}  // namespace fp8la

@@ -143,6 +143,11 @@ CASES = [
     (2048, [512, 1024, 512], [1, 0, 1], 2, 16, 512, 1024),
     (1024, [1] * 1000, [(7 * i) % 11 - 1 for i in range(1000)], 10, 4, 64, 64),
     (100, [], [], 1, 8, 64, 64),                                     # no segment at all
+    (700, [130, 63, 1, 64, 300, 129], [0, 1, 0, 2, 1, 0], 3, 32, 640, 1096),
+    (900, [257, 0, 500, 100], [1, 0, -1, 1], 2, 64, 8, 2056),
+    (600, [17, 583], [0, 0], 1, 128, 1992, 264),
+    (5000, [1500, 2100, 1400], [0, 1, 0], 2, 48, 264, 520),          # long sums over rows
+    (300, [299], [0], 1, 20, 8192, 64),                              # long sums over K
 ]
 
 
@@ -220,8 +225,8 @@ def test_non_finite_stays_in_its_rows():
     and its adapter's gradients, no others."""
     import torch
     fl = lib()
-    for xt in ("bfloat16", "float32"):
-        c = make(60, [20, 25, 15], [0, 1, -1], 2, 16, 192, 256, xt=xt)
+    for xt, more in (("bfloat16", 0), ("float32", 0), ("bfloat16", 400)):
+        c = make(60 + more, [20, 25, 15, more], [0, 1, -1, 0], 2, 16, 192, 256, xt=xt)
         out, v = fl.lora_apply(c["base"], c["x"], c["A"], c["B"], c["alpha"], c["m_offsets"],
                                c["adapter_ids"])
         c["x"][22, 5] = float("nan")
@@ -232,14 +237,14 @@ def test_non_finite_stays_in_its_rows():
                                c["adapter_ids"])
         assert torch.isnan(o2[22].float()).all() and torch.isnan(v2[22]).all()
         assert not torch.isfinite(v2[23]).any()
-        keep = [t for t in range(60) if t not in (22, 23)]
+        keep = [t for t in range(60 + more) if t not in (22, 23)]
         assert torch.equal(out[keep], o2[keep]) and torch.equal(v[keep], v2[keep])
         dx, dA, dB = fl.lora_backward(c["dy"], c["x"], v, c["A"], c["B"], c["alpha"],
                                       c["m_offsets"], c["adapter_ids"], c["dx_base"])
         assert torch.isfinite(dA[0]).all() and torch.isfinite(dB[0]).all()
         assert torch.isnan(dA[1]).any() and torch.isnan(dB[1, :, 9]).all()
         assert torch.isnan(dx[22].float()).all()
-        keep = [t for t in range(60) if t != 22]
+        keep = [t for t in range(60 + more) if t != 22]
         assert torch.isfinite(dx[keep].float()).all()
 
 
