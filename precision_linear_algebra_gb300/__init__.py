@@ -412,31 +412,38 @@ def grouped_gemm(m_offsets, A, B, scale_a, scale_b, C=None):
     return C
 
 
-def _dtype_code(t):
+# The calls below run in the microseconds of a decoding step, so they look at
+# each tensor's shape and strides once and pass them straight to the library.
+def _rows(t, rows, cols, dtype=None):
+    """Row stride of a [rows][cols] tensor whose rows are contiguous."""
+    assert t.shape == (rows, cols) and (dtype is None or t.dtype is dtype)
+    s0, s1 = t.stride()
+    assert s1 == 1 or cols == 1
+    return s0 if rows > 1 else max(cols, 1)
+
+
+def _dense(t, shape, dtype):
+    assert t.dtype is dtype and t.shape == shape and t.is_contiguous()
+
+
+def _type(t):
     import torch
     dt = t.dtype
-    assert dt == torch.bfloat16 or dt == torch.float32
-    return FP8LA_TYPE_BF16 if dt == torch.bfloat16 else FP8LA_TYPE_F32
-
-
-def _out(t, shape, dtype, device, dense=True):
-    """An output: the caller's tensor, checked, or a new one."""
-    import torch
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    assert t.dtype == dtype and t.shape == shape
-    assert t.is_contiguous() if dense else t.stride(-1) == 1
-    return t
+    if dt is torch.bfloat16:
+        return FP8LA_TYPE_BF16
+    assert dt is torch.float32
+    return FP8LA_TYPE_F32
 
 
 def _workspace(workspace, need, device):
-    """The caller's workspace, or a fresh one from torch's allocator."""
+    """(pointer, bytes, tensor): the caller's workspace, or a fresh one."""
     import torch
     if need == 0:
-        return None, 0
+        return None, 0, None
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device), need
-    return workspace, workspace.numel() * workspace.element_size()
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        return workspace.data_ptr(), need, workspace
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 def moe_route(logits, top_k, renormalise=True, sort=True, ids=None, weights=None,
@@ -450,21 +457,33 @@ def moe_route(logits, top_k, renormalise=True, sort=True, ids=None, weights=None
     synchronised.
     """
     import torch
-    assert logits.dim() == 2 and logits.stride(1) == 1
     T, E = logits.shape
     dev = logits.device
-    ids = _out(ids, (T, top_k), torch.int32, dev)
-    weights = _out(weights, (T, top_k), torch.float32, dev)
+    if ids is None:
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    else:
+        _dense(ids, (T, top_k), torch.int32)
+    if weights is None:
+        weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    else:
+        _dense(weights, (T, top_k), torch.float32)
+    po = pr = pw = ws = None
     nbytes = 0
     if sort:
-        m_offsets = _out(m_offsets, (E + 1,), torch.int32, dev)
-        order = _out(order, (T * top_k,), torch.int32, dev)
-        workspace, nbytes = _workspace(workspace, fp8_moe_route_workspace_bytes(T, E), dev)
+        if m_offsets is None:
+            m_offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        else:
+            _dense(m_offsets, (E + 1,), torch.int32)
+        if order is None:
+            order = torch.empty(T * top_k, dtype=torch.int32, device=dev)
+        else:
+            _dense(order, (T * top_k,), torch.int32)
+        po, pr = m_offsets.data_ptr(), order.data_ptr()
+        pw, nbytes, ws = _workspace(workspace, fp8_moe_route_workspace_bytes(T, E), dev)
     else:
-        m_offsets = order = workspace = None
-    fp8_moe_route(_ptr(logits), _dtype_code(logits), T, E, _ld(logits), top_k,
-                  int(renormalise), _ptr(ids), _ptr(weights), _ptr(m_offsets), _ptr(order),
-                  _ptr(workspace), nbytes, _stream())
+        m_offsets = order = None
+    _call("fp8_moe_route", logits.data_ptr(), _type(logits), T, E, _rows(logits, T, E), top_k,
+          renormalise, ids.data_ptr(), weights.data_ptr(), po, pr, pw, nbytes, _stream())
     return ids, weights, m_offsets, order
 
 
@@ -480,37 +499,43 @@ def moe_layer(x, ids, weights, w13, scale13, w2, scale2, y=None, workspace=None,
     """
     import torch
     T, D = x.shape
-    E, F = w13.shape[0], w2.shape[2]
+    E, _, F = w2.shape
     top_k = ids.shape[1]
-    assert x.stride(1) == 1 and w13.shape == (E, 2 * F, D) and w2.shape == (E, D, F)
-    assert w13.dtype == torch.uint8 and w2.dtype == torch.uint8
-    assert w13.stride(2) == 1 and w2.stride(2) == 1
-    assert ids.dtype == torch.int32 and ids.shape == (T, top_k) and ids.is_contiguous()
-    assert (weights.dtype == torch.float32 and weights.shape == (T, top_k)
-            and weights.is_contiguous())
-    assert scale13.dtype == torch.float32 and scale13.numel() == E and scale13.is_contiguous()
-    assert scale2.dtype == torch.float32 and scale2.numel() == E and scale2.is_contiguous()
-    y = _out(y, (T, D), torch.bfloat16, x.device, dense=False)
-    workspace, nbytes = _workspace(workspace,
-                                   fp8_moe_layer_workspace_bytes(T, top_k, E, D, F), x.device)
-    fp8_moe_layer(_ptr(x), _dtype_code(x), T, D, _ld(x), _ptr(ids), _ptr(weights), top_k, E,
-                  _ptr(w13), w13.stride(1), w13.stride(0), _ptr(scale13), _ptr(w2),
-                  w2.stride(1), w2.stride(0), _ptr(scale2), F, _FORMATS[fmt],
-                  _ACTIVATIONS[activation], _ptr(y), _ld(y), _ptr(workspace), nbytes, _stream())
+    assert w13.shape == (E, 2 * F, D) and w2.shape[1] == D
+    assert w13.dtype is torch.uint8 and w2.dtype is torch.uint8
+    e13, ld13, one13 = w13.stride()
+    e2, ld2, one2 = w2.stride()
+    assert (one13 == 1 or D == 1) and (one2 == 1 or F == 1)
+    _dense(ids, (T, top_k), torch.int32)
+    _dense(weights, (T, top_k), torch.float32)
+    _dense(scale13, (E,), torch.float32)
+    _dense(scale2, (E,), torch.float32)
+    if y is None:
+        y, ldy = torch.empty((T, D), dtype=torch.bfloat16, device=x.device), D
+    else:
+        ldy = _rows(y, T, D, torch.bfloat16)
+    pw, nbytes, ws = _workspace(workspace, fp8_moe_layer_workspace_bytes(T, top_k, E, D, F),
+                                x.device)
+    _call("fp8_moe_layer", x.data_ptr(), _type(x), T, D, _rows(x, T, D), ids.data_ptr(),
+          weights.data_ptr(), top_k, E, w13.data_ptr(), ld13, e13, scale13.data_ptr(),
+          w2.data_ptr(), ld2, e2, scale2.data_ptr(), F, _FORMATS[fmt],
+          _ACTIVATIONS[activation], y.data_ptr(), ldy, pw, nbytes, _stream())
     return y
 
 
-def _check_adapters(x, A, B, alpha, m_offsets, adapter_ids, N):
+def _adapters(A, B, alpha, m_offsets, adapter_ids, N):
+    """Sizes and strides of a set of adapters and its segments."""
     import torch
     n, R, K = A.shape
-    assert x.dim() == 2 and x.shape[1] == K and x.stride(1) == 1
-    assert A.dtype == torch.bfloat16 and B.dtype == torch.bfloat16
-    assert B.shape == (n, R, N) and A.stride(2) == 1 and B.stride(2) == 1
-    assert alpha.dtype == torch.float32 and alpha.shape == (n,) and alpha.is_contiguous()
-    assert m_offsets.dtype == torch.int32 and adapter_ids.dtype == torch.int32
-    assert m_offsets.is_contiguous() and adapter_ids.is_contiguous()
-    assert m_offsets.numel() == adapter_ids.numel() + 1
-    return n, R, K
+    assert A.dtype is torch.bfloat16 and B.dtype is torch.bfloat16 and B.shape == (n, R, N)
+    sa, lda, onea = A.stride()
+    sb, ldb, oneb = B.stride()
+    assert (onea == 1 or K == 1) and (oneb == 1 or N == 1)
+    _dense(alpha, (n,), torch.float32)
+    S = adapter_ids.numel()
+    _dense(adapter_ids, (S,), torch.int32)
+    _dense(m_offsets, (S + 1,), torch.int32)
+    return n, R, K, S, lda, sa, ldb, sb
 
 
 def lora_apply(base, x, A, B, alpha, m_offsets, adapter_ids, out=None, v=None):
@@ -524,14 +549,19 @@ def lora_apply(base, x, A, B, alpha, m_offsets, adapter_ids, out=None, v=None):
     """
     import torch
     T, N = base.shape
-    n, R, K = _check_adapters(x, A, B, alpha, m_offsets, adapter_ids, N)
-    assert base.dtype == torch.bfloat16 and base.stride(1) == 1 and x.shape[0] == T
-    out = _out(out, (T, N), torch.bfloat16, x.device, dense=False)
-    v = _out(v, (T, R), torch.float32, x.device, dense=False)
-    fp8la_lora_apply(_ptr(base), _ld(base), _ptr(x), _dtype_code(x), _ld(x), T, _ptr(A),
-                     A.stride(1), A.stride(0), _ptr(B), B.stride(1), B.stride(0), _ptr(alpha),
-                     n, R, K, N, adapter_ids.numel(), _ptr(m_offsets), _ptr(adapter_ids),
-                     _ptr(out), _ld(out), _ptr(v), _ld(v), _stream())
+    n, R, K, S, lda, sa, ldb, sb = _adapters(A, B, alpha, m_offsets, adapter_ids, N)
+    if out is None:
+        out, ldo = torch.empty((T, N), dtype=torch.bfloat16, device=x.device), N
+    else:
+        ldo = _rows(out, T, N, torch.bfloat16)
+    if v is None:
+        v, ldv = torch.empty((T, R), dtype=torch.float32, device=x.device), R
+    else:
+        ldv = _rows(v, T, R, torch.float32)
+    _call("fp8la_lora_apply", base.data_ptr(), _rows(base, T, N, torch.bfloat16), x.data_ptr(),
+          _type(x), _rows(x, T, K), T, A.data_ptr(), lda, sa, B.data_ptr(), ldb, sb,
+          alpha.data_ptr(), n, R, K, N, S, m_offsets.data_ptr(), adapter_ids.data_ptr(),
+          out.data_ptr(), ldo, v.data_ptr(), ldv, _stream())
     return out, v
 
 
@@ -546,20 +576,27 @@ def lora_backward(dy, x, v, A, B, alpha, m_offsets, adapter_ids, dx_base, dx=Non
     """
     import torch
     T, N = dy.shape
-    n, R, K = _check_adapters(x, A, B, alpha, m_offsets, adapter_ids, N)
-    assert dy.stride(1) == 1 and x.shape[0] == T
-    assert dx_base.dtype == torch.bfloat16 and dx_base.shape == (T, K)
-    assert dx_base.stride(1) == 1
-    assert v.dtype == torch.float32 and v.shape == (T, R) and v.stride(1) == 1
-    dx = _out(dx, (T, K), torch.bfloat16, x.device, dense=False)
-    dA = _out(dA, (n, R, K), torch.float32, x.device)
-    dB = _out(dB, (n, R, N), torch.float32, x.device)
-    workspace, nbytes = _workspace(workspace, fp8la_lora_workspace_bytes(T, R), x.device)
-    fp8la_lora_backward(_ptr(dy), _dtype_code(dy), _ld(dy), _ptr(x), _dtype_code(x), _ld(x),
-                        _ptr(v), _ld(v), T, _ptr(A), A.stride(1), A.stride(0), _ptr(B),
-                        B.stride(1), B.stride(0), _ptr(alpha), n, R, K, N,
-                        adapter_ids.numel(), _ptr(m_offsets), _ptr(adapter_ids), _ptr(dx_base), _ld(dx_base), _ptr(dx), _ld(dx),
-                        _ptr(dA), _ptr(dB), _ptr(workspace), nbytes, _stream())
+    n, R, K, S, lda, sa, ldb, sb = _adapters(A, B, alpha, m_offsets, adapter_ids, N)
+    dev = x.device
+    if dx is None:
+        dx, lddx = torch.empty((T, K), dtype=torch.bfloat16, device=dev), K
+    else:
+        lddx = _rows(dx, T, K, torch.bfloat16)
+    if dA is None:
+        dA = torch.empty((n, R, K), dtype=torch.float32, device=dev)
+    else:
+        _dense(dA, (n, R, K), torch.float32)
+    if dB is None:
+        dB = torch.empty((n, R, N), dtype=torch.float32, device=dev)
+    else:
+        _dense(dB, (n, R, N), torch.float32)
+    pw, nbytes, ws = _workspace(workspace, fp8la_lora_workspace_bytes(T, R), dev)
+    _call("fp8la_lora_backward", dy.data_ptr(), _type(dy), _rows(dy, T, N), x.data_ptr(),
+          _type(x), _rows(x, T, K), v.data_ptr(), _rows(v, T, R, torch.float32), T,
+          A.data_ptr(), lda, sa, B.data_ptr(), ldb, sb, alpha.data_ptr(), n, R, K, N, S,
+          m_offsets.data_ptr(), adapter_ids.data_ptr(), dx_base.data_ptr(),
+          _rows(dx_base, T, K, torch.bfloat16), dx.data_ptr(), lddx, dA.data_ptr(),
+          dB.data_ptr(), pw, nbytes, _stream())
     return dx, dA, dB
 
 

@@ -270,11 +270,19 @@ __global__ void __launch_bounds__(kThreads)
           for (int h = 0; h < 4; ++h) x[h][0] = w[h];
         }
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
+        for (int j = 0; j < NJ; ++j) {
+          // mma.sync cuts off a little of the sum that it adds to.  With three
+          // terms that made V's error three times an FP32 product's, so a
+          // step's terms are added up apart, the small ones first.
+          float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
-            mma16816(acc[m][j], x[0][t], x[1][t], x[2][t], x[3][t],
+          for (int t = NT - 1; t >= 0; --t)
+            mma16816(NT > 1 ? part : acc[m][j], x[0][t], x[1][t], x[2][t], x[3][t],
                      b[j >> 1][2 * (j & 1)], b[j >> 1][2 * (j & 1) + 1]);
+          if (NT > 1)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[m][j][e] += part[e];
+        }
       }
     }
   }
@@ -704,21 +712,34 @@ __device__ __forceinline__ void outer_body(const OuterArgs &a, const OuterSide &
         }
       }
 #pragma unroll
-      for (int m = 0; m < MR; ++m)
+      for (int m = 0; m < MR; ++m) {
+        // mma.sync cuts off a little of the sum that it adds to: over the
+        // thousands of rows of an adapter that came to an error of 2e-5.  So
+        // 16 rows are added up apart, the small terms first.
+        float part[4][4];
 #pragma unroll
-        for (int t = 0; t < 3; ++t) {
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) part[i][e] = 0.0f;
+#pragma unroll
+        for (int t = 2; t >= 0; --t) {
           uint32_t v[4];
           ldmatrix4_trans(sw + t * C::kTerm +
                               ((k + (lane & 7) + 8 * (lane >> 4)) * C::kLdW + 16 * m +
                                8 * ((lane >> 3) & 1)) * 2,
                           v);
 #pragma unroll
-          for (int x = 0; x < C::XT; ++x)
+          for (int x = C::XT - 1; x >= 0; --x)
             if (x + t < 3)
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                mma16816(acc[m][i], v[0], v[1], v[2], v[3], b[x][i][0], b[x][i][1]);
+                mma16816(part[i], v[0], v[1], v[2], v[3], b[x][i][0], b[x][i][1]);
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[m][i][e] += part[i][e];
+      }
     }
     if (s + 1 < s1) store_v(s + 1);
   }

@@ -76,6 +76,11 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&u)[16]) {
 constexpr int kSThreads = 192;      // warps 0-3 epilogue, 4 producer, 5 MMA
 constexpr int kSRows = 128;
 constexpr int kSK = 128;            // K of a stage: two boxes of 64
+// Accumulators that stages take in turn.  The tensor core cuts off a little of
+// the running sum with each addition, so a sum is kept in several shorter
+// ones, which the epilogue adds with rounding: with one accumulator, 2048
+// products in it left a relative error of 2e-6 in V, more than FP32 has.
+constexpr int kAcc = 4;
 
 // RP ranks, a multiple of 16.
 template <int RP>
@@ -84,7 +89,7 @@ struct ShrinkTma {
   static constexpr int kP = RP * kSK * 2;
   static constexpr int kStage = kX + kP;
   static constexpr int STAGES = 4 * kStage <= 200 * 1024 ? 4 : 3;
-  static constexpr int kTmemCols = RP < 32 ? 32 : RP;
+  static constexpr int kTmemCols = kAcc * RP;
   static constexpr int kLdR = RP + 1;  // of the sums, in floats
   static constexpr int kBar = STAGES * kStage;
   static constexpr int kMisc = kBar + (2 * STAGES + 1) * 8;
@@ -182,8 +187,8 @@ __global__ void __launch_bounds__(kSThreads)
           const uint64_t bd = smem_desc_k128_sw128(d + C::kX + h * (C::kP / 2));
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            umma_bf16(tmem_base, ad + 2u * k, bd + 2u * k, idesc,
-                      (c > s0 || h > 0 || k > 0) ? 1u : 0u);
+            umma_bf16(tmem_base + (c - s0) % kAcc * RP, ad + 2u * k, bd + 2u * k,
+                      idesc, (c - s0 >= kAcc || h > 0 || k > 0) ? 1u : 0u);
         }
         umma_commit(empty_bar(s));
         if (++s == C::STAGES) { s = 0; ph ^= 1u; }
@@ -200,10 +205,17 @@ __global__ void __launch_bounds__(kSThreads)
       const uint32_t col0 = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
 #pragma unroll
       for (int j = 0; j < RP; j += 16) {
-        float v[16];
-        tmem_ld16(col0 + j, v);
+        float sum[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) red[row * C::kLdR + j + i] = s1 > s0 ? v[i] : 0.0f;
+        for (int i = 0; i < 16; ++i) sum[i] = 0.0f;
+        for (int q = 0; q < min(kAcc, s1 - s0); ++q) {
+          float v[16];
+          tmem_ld16(col0 + q * RP + j, v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) sum[i] += v[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) red[row * C::kLdR + j + i] = sum[i];
       }
     }
   }
@@ -243,7 +255,10 @@ struct OuterTma {
   // Two CTAs on an SM for the smallest ranks, so that one streams while the
   // other starts or adds up.
   static constexpr int STAGES = RP <= 32 ? 2 : 3;
-  static constexpr int kTmemCols = 2 * RP < 32 ? 32 : 2 * RP;
+  // Accumulators: NACC that stages take in turn for V's first term, and one
+  // for the other two, which are 2^-8 of it or less; all of TMEM, at most.
+  static constexpr int NACC = RP <= 64 ? kAcc - 1 : 1;
+  static constexpr int kTmemCols = 2 * RP * (NACC + 1);
   static constexpr int kVBuf = STAGES * kX;         // [2][3 terms]
   static constexpr int kLdR = kOCols + 4;
   static constexpr int kBar = kVBuf + 2 * kV;
@@ -404,9 +419,11 @@ __global__ void __launch_bounds__(kOThreads, RP <= 32 ? 2 : 1)
                 smem_desc_mn_sw128(x + 2 * m * C::kBox + k * 2048, C::kBox);
 #pragma unroll
             for (int t = 0; t < 3; ++t)
-              umma_bf16(tmem_base + m * RP, ad,
-                        smem_desc_k128_sw128(v + t * C::kTerm) + 2u * k, idesc,
-                        (c > s0 || k > 0 || t > 0) ? 1u : 0u);
+              umma_bf16(tmem_base +
+                            ((t == 0 ? (c - s0) % C::NACC : C::NACC) * 2 + m) * RP,
+                        ad, smem_desc_k128_sw128(v + t * C::kTerm) + 2u * k, idesc,
+                        (k > 0 || t > 1 || c - s0 >= (t == 0 ? C::NACC : 1)) ? 1u
+                                                                            : 0u);
           }
         umma_commit(empty_bar(s));
         umma_commit(vfree_bar(b));
@@ -499,11 +516,19 @@ __global__ void __launch_bounds__(kOThreads, RP <= 32 ? 2 : 1)
       const float scale = o.use_alpha ? a.alpha[adapter] : 1.0f;
 #pragma unroll
       for (int j = 0; j < RP; j += 16) {
-        float v[16];
-        tmem_ld16(t + j, v);
+        float sum[16];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) sum[q] = 0.0f;
+        // The small terms first.
+        for (int n = min(C::NACC, s1 - s0); s1 > s0 && n >= 0; --n) {
+          float v[16];
+          tmem_ld16(t + (n == min(C::NACC, s1 - s0) ? C::NACC : n) * 2 * RP + j, v);
+#pragma unroll
+          for (int q = 0; q < 16; ++q) sum[q] += v[q];
+        }
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
-          const float g = s1 > s0 ? v[q] : 0.0f;
+          const float g = sum[q];
           if (csize > 1)
             red[(j + q) * C::kLdR + cc] = g;
           else if (j + q < a.R && col0 + cc < o.N)
