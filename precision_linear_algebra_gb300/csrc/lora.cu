@@ -29,7 +29,8 @@
 // operand (x or dy given as FP32, v and dv always) enters as a sum of BF16
 // terms: three (24 significant bits) where the output is FP32, so that it is
 // as good as an FP32 product's, two (relative error 2^-17) where it is
-// rounded to BF16.  base + delta is added in FP32 and rounded once.
+// rounded to BF16.  base is the first term of its sum, which is rounded
+// once.
 #include <cuda_bf16.h>
 
 #include "lora.cuh"
@@ -52,52 +53,38 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// 2 E consecutive elements from column c on of a row of `width` elements, as
-// E pairs of BF16 in NT terms; zeros outside the row (p null: all zeros).
-template <bool F32, int E, int NT>
-__device__ __forceinline__ void load_pairs(const void *p, int64_t c, int64_t width,
-                                           bool vec, uint32_t (&w)[NT][E]) {
-  if (!F32) {
-    const uint16_t *q = static_cast<const uint16_t *>(p) + c;
-    if (p && vec && c + 2 * E <= width) {
+// Rows of a matrix are read in units of 16, 8, 4 or 2 bytes, as its address and
+// strides allow.
+//
+// 2 E consecutive BF16 from column c on of a row of `width`, as E pairs; zeros
+// outside the row (p null: all zeros).
+template <int E>
+__device__ __forceinline__ void load_pairs(const uint16_t *p, int64_t c,
+                                           int64_t width, int unit,
+                                           uint32_t (&w)[E]) {
+  const uint16_t *q = p + c;
+  if (p && unit == 16 && c + 2 * E <= width) {
 #pragma unroll
-      for (int i = 0; i < E / 4; ++i) {
-        const uint4 v = *(reinterpret_cast<const uint4 *>(q) + i);
-        w[0][4 * i] = v.x;
-        w[0][4 * i + 1] = v.y;
-        w[0][4 * i + 2] = v.z;
-        w[0][4 * i + 3] = v.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const uint32_t lo = p && c + 2 * i < width ? q[2 * i] : 0;
-        const uint32_t hi = p && c + 2 * i + 1 < width ? q[2 * i + 1] : 0;
-        w[0][i] = lo | hi << 16;
-      }
+    for (int i = 0; i < E / 4; ++i) {
+      const uint4 v = *(reinterpret_cast<const uint4 *>(q) + i);
+      w[4 * i] = v.x;
+      w[4 * i + 1] = v.y;
+      w[4 * i + 2] = v.z;
+      w[4 * i + 3] = v.w;
     }
+  } else if (E == 2 && p && unit == 8 && c + 2 * E <= width) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(q);
+    w[0] = v.x;
+    w[1] = v.y;
+  } else if (p && unit >= 4 && c + 2 * E <= width) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) w[i] = *(reinterpret_cast<const uint32_t *>(q) + i);
   } else {
-    const float *q = static_cast<const float *>(p) + c;
-    float v[2 * E];
-    if (p && vec && c + 2 * E <= width) {
-#pragma unroll
-      for (int i = 0; i < E / 2; ++i) {
-        const float4 f = *(reinterpret_cast<const float4 *>(q) + i);
-        v[4 * i] = f.x;
-        v[4 * i + 1] = f.y;
-        v[4 * i + 2] = f.z;
-        v[4 * i + 3] = f.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 2 * E; ++i) v[i] = p && c + i < width ? q[i] : 0.0f;
-    }
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      uint32_t t[NT];
-      split_pair<NT>(v[2 * i], v[2 * i + 1], t);
-#pragma unroll
-      for (int k = 0; k < NT; ++k) w[k][i] = t[k];
+      const uint32_t lo = p && c + 2 * i < width ? q[2 * i] : 0;
+      const uint32_t hi = p && c + 2 * i + 1 < width ? q[2 * i + 1] : 0;
+      w[i] = lo | hi << 16;
     }
   }
 }
@@ -122,47 +109,64 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Copies `rows` rows of COLS elements of SIZE bytes, from column c of a matrix
-// with `width` columns on, to shared memory (rows LD bytes apart), zeros where
-// the matrix has no element or r >= valid.  Asynchronous where the matrix has
-// 16-byte rows; else at once, by plain loads and stores.
-template <int COLS, int SIZE, int LD>
-__device__ __forceinline__ void copy_tile(uint32_t dst, const char *src, int64_t ld,
-                                          int rows, int valid, int64_t c,
-                                          int64_t width, bool vec) {
-  constexpr int kUnits = COLS * SIZE / 16;  // 16-byte units of a row
-  constexpr int kPer = 16 / SIZE;
+// Copies the U-byte units of `rows` rows of COLS elements of SIZE bytes, see
+// copy_tile.
+template <int U, int COLS, int SIZE, int LD>
+__device__ __forceinline__ void copy_units(uint32_t dst, const char *src, int64_t ld,
+                                           int rows, int valid, int64_t c,
+                                           int64_t width) {
+  constexpr int kUnits = COLS * SIZE / U;
+  constexpr int kPer = U / SIZE;
+#pragma unroll 4
   for (int i = threadIdx.x; i < rows * kUnits; i += kThreads) {
     const int r = i / kUnits, u = i % kUnits;
     const int64_t cc = c + u * kPer;
     const int n = r < valid && cc < width
                       ? static_cast<int>(min(static_cast<int64_t>(kPer), width - cc)) : 0;
     const char *p = src + (n > 0 ? (r * ld + cc) * SIZE : 0);
-    const uint32_t d = dst + r * LD + u * 16;
-    if (vec) {
+    const uint32_t d = dst + r * LD + u * U;
+    if (U == 16)
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(p),
                    "r"(n * SIZE)
                    : "memory");
-    } else {
-      uint32_t w[4] = {0, 0, 0, 0};
-      if (SIZE == 4) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (j < n) w[j] = reinterpret_cast<const uint32_t *>(p)[j];
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j < n)
-            w[j >> 1] |= static_cast<uint32_t>(
-                             reinterpret_cast<const uint16_t *>(p)[j])
-                         << (16 * (j & 1));
-      }
-      st_shared_v4(d, w[0], w[1], w[2], w[3]);
+    else
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(d), "l"(p),
+                   "r"(n * SIZE), "n"(U)
+                   : "memory");
+  }
+}
+
+// Copies `rows` rows of COLS elements of SIZE bytes, from column c of a matrix
+// with `width` columns on, to shared memory (rows LD bytes apart), zeros where
+// the matrix has no element or r >= valid.  Asynchronous, but for BF16 rows at
+// odd addresses, which go through registers, element by element.
+template <int COLS, int SIZE, int LD>
+__device__ __forceinline__ void copy_tile(uint32_t dst, const char *src, int64_t ld,
+                                          int rows, int valid, int64_t c,
+                                          int64_t width, int unit) {
+  if (unit == 16) {
+    copy_units<16, COLS, SIZE, LD>(dst, src, ld, rows, valid, c, width);
+  } else if (unit == 8) {
+    copy_units<8, COLS, SIZE, LD>(dst, src, ld, rows, valid, c, width);
+  } else if (SIZE == 4 || unit == 4) {
+    copy_units<4, COLS, SIZE, LD>(dst, src, ld, rows, valid, c, width);
+  } else {
+    // Neighbouring lanes take neighbouring pairs.
+    constexpr int kPairs = COLS / 2;
+#pragma unroll 8
+    for (int i = threadIdx.x; i < rows * kPairs; i += kThreads) {
+      const int r = i / kPairs, u = i % kPairs;
+      const int64_t cc = c + 2 * u;
+      const uint16_t *p = reinterpret_cast<const uint16_t *>(src) + r * ld + cc;
+      const uint32_t lo = r < valid && cc < width ? p[0] : 0;
+      const uint32_t hi = r < valid && cc + 1 < width ? p[1] : 0;
+      asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + r * LD + u * 4),
+                   "r"(lo | hi << 16)
+                   : "memory");
     }
   }
 }
 
-// ------------------------------------------------------------------- shrink
 // MW groups of warps share out the rows (MF fragments of 16 each), KW = 8 / MW
 // the K of a stage; NJ rank fragments of 8 (even where more than one).
 template <bool F32, int MW, int MF, int NJ>
@@ -222,8 +226,8 @@ __global__ void __launch_bounds__(kThreads)
     if (s < s1) {
       const uint32_t d = base + (s - s0) % C::STAGES * C::kStage;
       const int64_t k = static_cast<int64_t>(s) * C::KS;
-      copy_tile<C::KS, kSize, C::kLdX>(d, X, a.ldx, xrows, f.rows, k, a.K, a.x_vec);
-      copy_tile<C::KS, 2, C::kLdP>(d + C::kX, P, a.ldp, C::RP, a.R, k, a.K, a.p_vec);
+      copy_tile<C::KS, kSize, C::kLdX>(d, X, a.ldx, xrows, f.rows, k, a.K, a.x_unit);
+      copy_tile<C::KS, 2, C::kLdP>(d + C::kX, P, a.ldp, C::RP, a.R, k, a.K, a.p_unit);
     }
     cp_async_commit();
   };
@@ -337,199 +341,292 @@ struct ExpandArgs {
   const uint16_t *base;
   uint16_t *out;
   int64_t ld_base, ld_out;
-  int32_t p_vec, base_vec, out_vec;
-  int32_t tm;            // rows of a tile
+  int32_t p_unit, base_unit, out_unit;
+  int32_t rows;          // of a CTA
 };
 
-constexpr int kExpandCols = 64 * kWarps;
+constexpr int kExpandThreads = 512;
+constexpr int kExpandWarps = kExpandThreads / 32;
+constexpr int kWarpCols = 32;
+constexpr int kExpandCols = kWarpCols * kExpandWarps;
 
-__device__ __forceinline__ void load_bf16x16(const uint16_t *p, int64_t c,
-                                             int64_t width, bool vec,
-                                             uint32_t (&w)[8]) {
-  uint32_t t[1][8];
-  load_pairs<false, 8, 1>(p, c, width, vec, t);
+__device__ __forceinline__ void store_bf16x8(uint16_t *p, int64_t c, int64_t width,
+                                             int unit, const uint32_t (&w)[4]) {
+  if (unit == 16 && c + 8 <= width) {
+    *reinterpret_cast<uint4 *>(p + c) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else if (unit >= 4 && c + 8 <= width) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = t[0][i];
-}
-
-__device__ __forceinline__ void store_bf16x16(uint16_t *p, int64_t c,
-                                              int64_t width, bool vec,
-                                              const uint32_t (&w)[8]) {
-  if (vec && c + 16 <= width) {
-    uint4 *d = reinterpret_cast<uint4 *>(p + c);
-    d[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    for (int i = 0; i < 4; ++i) *(reinterpret_cast<uint32_t *>(p + c) + i) = w[i];
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < 8; ++i)
       if (c + i < width)
         p[c + i] = static_cast<uint16_t>(i & 1 ? w[i >> 1] >> 16 : w[i >> 1]);
   }
 }
 
-// B fragments of one 16-rank block for this lane's share of 64 columns: rows
-// 2q, 2q+1, 2q+8, 2q+9 of the block, columns 8g..8g+7; column i of them is
+// B fragments of one 16-rank block for this lane's share of 32 columns: rows
+// 2q, 2q+1, 2q+8, 2q+9 of the block, columns 4g..4g+3; column i of them is
 // column g of fragment i.
 __device__ __forceinline__ void load_rank_block(const ExpandArgs &a,
                                                 const uint16_t *P, int r0, int q,
-                                                int64_t col, uint32_t (&b)[8][2]) {
-  uint32_t w[4][1][4];
+                                                int64_t col, uint32_t (&b)[4][2]) {
+  uint32_t w[4][2];
 #pragma unroll
   for (int h = 0; h < 4; ++h) {
     const int r = r0 + 2 * q + (h & 1) + 8 * (h >> 1);
-    load_pairs<false, 4, 1>(r < a.R ? P + r * a.ldp : nullptr, col, a.N, a.p_vec,
-                            w[h]);
+    load_pairs<2>(r < a.R ? P + r * a.ldp : nullptr, col, a.N, min(a.p_unit, 8), w[h]);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      b[2 * i][h] = __byte_perm(w[2 * h][0][i], w[2 * h + 1][0][i], 0x5410);
-      b[2 * i + 1][h] = __byte_perm(w[2 * h][0][i], w[2 * h + 1][0][i], 0x7632);
+      b[2 * i][h] = __byte_perm(w[2 * h][i], w[2 * h + 1][i], 0x5410);
+      b[2 * i + 1][h] = __byte_perm(w[2 * h][i], w[2 * h + 1][i], 0x7632);
     }
 }
 
-// One warp per 64 columns; KR blocks of 16 ranks; tiles of tm <= TM rows (a
-// multiple of 16).  Each warp
-// streams its own 16-row pieces of base through a ring in shared memory, kRing
-// deep, with nothing to wait for but its own copies.
-constexpr int kRing = 4;
-constexpr int kPiece = 16 * 128;  // bytes: 16 rows of 64 columns
+// One warp per 32 columns, KR blocks of 16 ranks.  A CTA keeps its 512 columns
+// and walks down its share of all rows, in chunks of up to CH rows of one
+// segment; it fetches the factor's fragments again where the adapter changes.
+// While a chunk is multiplied the next one's V is on its way, and each warp
+// streams 16-row pieces of base through a ring of its own, RING deep, across
+// chunks and segments, with nothing to wait for but its own copies.
+constexpr int kPiece = 16 * 2 * kWarpCols;  // bytes: 16 rows of 32 columns
 
-template <int TM, int KR>
+template <int CH, int KR>
 struct ExpandCfg {
-  static constexpr int kLd = 16 * KR + 8;  // padded row of a term, in BF16
-  static constexpr int kV = 2 * TM * kLd * 2;
-  static constexpr int kSmem = kV + kWarps * kRing * kPiece;
+  static constexpr int RING = CH == 16 ? 2 : 8;
+  static constexpr int kLd = 16 * KR + 8;            // padded row of a term, in BF16
+  static constexpr int kV = 2 * CH * kLd * 2;        // two terms
+  static constexpr int kRingAt = 2 * kV;             // two buffers
+  static constexpr int kSegs = kRingAt + kExpandWarps * RING * kPiece;
+  static constexpr int kSmem = kSegs + (2 * kMaxSegments + 1) * 4;
+  static constexpr int kPairs = (CH * 8 * KR + kExpandThreads - 1) / kExpandThreads;
   static_assert(kV % 16 == 0 && kSmem <= 226 * 1024, "shared memory");
 };
 
-template <int TM, int KR>
-__global__ void __launch_bounds__(kThreads)
+// Walks down rows: n rows of segment s, which uses adapter id, from `row` on.
+struct Walk {
+  int row, n, s, id;
+};
+
+template <int CH, int KR>
+__global__ void __launch_bounds__(kExpandThreads, 1)
     lora_expand_kernel(const ExpandArgs a) {
-  using C = ExpandCfg<TM, KR>;
-  constexpr bool kHold = KR <= 4;   // the factor stays in registers
+  using C = ExpandCfg<CH, KR>;
   extern __shared__ __align__(16) char smem[];
-  uint16_t *sv = reinterpret_cast<uint16_t *>(smem);  // [2][TM][kLd]
-  __shared__ int warp_sums[kWarps];
-  __shared__ Found slot;
+  int *offsets = reinterpret_cast<int *>(smem + C::kSegs);
+  int *ids = offsets + a.seg.S + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, q = lane & 3;
-  const int64_t col = static_cast<int64_t>(blockIdx.x) * kExpandCols + 64 * warp;
-  const int64_t c = col + 16 * q;
+  const int64_t col = static_cast<int64_t>(blockIdx.x) * kExpandCols + kWarpCols * warp;
+  const int64_t c = col + 8 * q;
+  const int r0 = blockIdx.y * a.rows, r1 = min(a.seg.T, r0 + a.rows);
   pdl_wait();
   pdl_launch_dependents();
-  const Found f = find_tile<kThreads>(a.seg, blockIdx.y, a.tm, warp_sums, &slot);
-  if (f.rows == 0) return;
-  const bool on = f.id >= 0;
-  const uint16_t *P = a.P + (on ? f.id : 0) * a.stride_p;
-  const uint16_t *base = a.base + static_cast<int64_t>(f.row0) * a.ld_base;
-  uint16_t *out = a.out + static_cast<int64_t>(f.row0) * a.ld_out;
-  if (!on && base == out) return;
-
-  // The factor's fragments and the first pieces of base are on their way
-  // while V is split.
-  uint32_t b[kHold ? KR : 1][8][2];
-  if (kHold && on && col < a.N)
-#pragma unroll
-    for (int k = 0; k < KR; ++k)
-      load_rank_block(a, P, 16 * k, q, col + 8 * g, b[kHold ? k : 0]);
-  const int pieces = (f.rows + 15) / 16;
-  const uint32_t ring = smem_addr(smem) + C::kV + warp * kRing * kPiece;
-  // Rows of 128 bytes; a row's 16-byte units are permuted by its number, so
-  // that eight lanes with as many rows and units meet different banks.
-  auto fetch = [&](int m) {
-    if (a.base_vec && m < pieces && col < a.N) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = (lane >> 3) + 4 * i, u = lane & 7;
-        const int64_t cc = col + 8 * u;
-        const int n = 16 * m + r < f.rows && cc < a.N
-                          ? static_cast<int>(min(static_cast<int64_t>(8), a.N - cc)) : 0;
-        const uint16_t *p = base + (n > 0 ? (16 * m + r) * a.ld_base + cc : 0);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                         ring + (m % kRing) * kPiece + r * 128 + ((u ^ (r & 7)) << 4)),
-                     "l"(p), "r"(2 * n)
-                     : "memory");
-      }
+  bool bad = false;
+  for (int i = threadIdx.x; i <= a.seg.S; i += kExpandThreads) {
+    const int lo = a.seg.offsets[i];
+    offsets[i] = lo;
+    bad |= lo < 0 || lo > a.seg.T || (i == 0 && lo != 0);
+    if (i < a.seg.S) {
+      const int id = a.seg.ids[i];
+      ids[i] = id;
+      bad |= a.seg.offsets[i + 1] < lo || id < -1 || id >= a.seg.n;
     }
-    cp_async_commit();
+  }
+  if (__syncthreads_or(bad)) {
+    if (threadIdx.x == 0) atomicOr(a.seg.status, kStatusBadDeviceArg);
+    return;
+  }
+  // The rows after the last segment count as one more, without an adapter.
+  auto settle = [&](Walk &w) {
+    while (w.s < a.seg.S && offsets[w.s + 1] <= w.row) ++w.s;
+    const int end = min(r1, w.s < a.seg.S ? offsets[w.s + 1] : r1);
+    w.n = min(CH, end - w.row);
+    w.id = w.s < a.seg.S ? ids[w.s] : -1;
   };
-#pragma unroll
-  for (int m = 0; m < kRing - 1; ++m) fetch(m);
-  const float alpha = !on ? 0.0f : a.alpha ? a.alpha[f.id] : 1.0f;
-  if (on)
-    for (int i = threadIdx.x; i < pieces * 16 * 8 * KR; i += kThreads) {
-      const int r = i / (8 * KR), j = 2 * (i - r * 8 * KR);
-      const float *v = a.V + (f.row0 + static_cast<int64_t>(r)) * a.ldv + j;
-      const float v0 = r < f.rows && j < a.R ? __ldcg(v) * alpha : 0.0f;
-      const float v1 = r < f.rows && j + 1 < a.R ? __ldcg(v + 1) * alpha : 0.0f;
-      uint32_t t[2];
-      split_pair<2>(v0, v1, t);
-      *reinterpret_cast<uint32_t *>(sv + r * C::kLd + j) = t[0];
-      *reinterpret_cast<uint32_t *>(sv + (TM + r) * C::kLd + j) = t[1];
+  Walk w;
+  {
+    // The last segment that begins at or before r0.
+    int lo = 0, hi = a.seg.S;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (offsets[mid] <= r0) lo = mid;
+      else hi = mid - 1;
     }
-  __syncthreads();
-  if (col >= a.N) return;
-  const uint32_t sv_lane =
-      smem_addr(sv) + ((lane & 15) * C::kLd + 8 * (lane >> 4)) * 2;
-  for (int m = 0; m < pieces; ++m) {
-    float acc[8][4];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][e] = 0.0f;
-    if (on) {
-#pragma unroll
-      for (int k = 0; k < KR; ++k) {
-        if (!kHold) load_rank_block(a, P, 16 * k, q, col + 8 * g, b[0]);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          uint32_t v[4];
-          ldmatrix4(sv_lane + ((t * TM + 16 * m) * C::kLd + 16 * k) * 2, v);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            mma16816(acc[i], v[0], v[1], v[2], v[3], b[kHold ? k : 0][i][0],
-                     b[kHold ? k : 0][i][1]);
-        }
-      }
-    }
-    cp_async_wait<kRing - 2>();
-    __syncwarp();  // the piece is whole, and the one before it has been read
-    fetch(m + kRing - 1);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = 16 * m + 8 * h + g;
-      if (r >= f.rows) continue;
-      uint32_t w[8];
-      if (a.base_vec) {
-        const char *p = smem + C::kV + (warp * kRing + m % kRing) * kPiece +
-                        (8 * h + g) * 128;
+    w.row = r0;
+    w.s = lo;
+    settle(w);
+  }
+
+  const bool live = col < a.N;
+  const uint32_t ring = smem_addr(smem) + C::kRingAt + warp * C::RING * kPiece;
+  // Rows of 64 bytes; a row's 16-byte units are permuted by its number, so
+  // that the eight lanes of a phase meet different banks.
+  Walk ahead = w;
+  int ahead_p = 0, slot_f = 0;
+  auto fetch = [&]() {
+    if (a.base_unit >= 4 && live && ahead.row < r1) {
+      const int n = ahead.n - ahead_p;
+      const uint16_t *src =
+          a.base + (ahead.row + static_cast<int64_t>(ahead_p)) * a.ld_base;
+      const uint32_t dst = ring + slot_f * kPiece;
+      if (a.base_unit == 16) {
+        const int u = lane & 3;
+        const int64_t left = a.N - (col + 8 * u);
+        const int most = left >= 8 ? 16 : left > 0 ? 2 * static_cast<int>(left) : 0;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint4 x = *reinterpret_cast<const uint4 *>(
-              p + (((2 * q + i) ^ (g & 7)) << 4));
-          w[4 * i] = x.x;
-          w[4 * i + 1] = x.y;
-          w[4 * i + 2] = x.z;
-          w[4 * i + 3] = x.w;
+          const int r = (lane >> 2) + 8 * i;
+          const int k = r < n ? most : 0;
+          const uint16_t *p = k > 0 ? src + r * a.ld_base + col + 8 * u : a.base;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                           dst + r * 64 + ((u ^ ((r >> 1) & 3)) << 4)),
+                       "l"(p), "r"(k)
+                       : "memory");
         }
       } else {
-        load_bf16x16(base + r * a.ld_base, c, a.N, false, w);
-      }
-      if (on) {
-        // Fragment i's columns 2q and 2q + 1 are columns i and 8 + i of the
-        // lane's 16.
+        const int u = lane & 15;
+        const int64_t left = a.N - (col + 2 * u);
+        const int most = left >= 2 ? 4 : left > 0 ? 2 : 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          w[i] = pack_bf16(bf_lo(w[i]) + acc[2 * i][2 * h],
-                           bf_hi(w[i]) + acc[2 * i + 1][2 * h]);
-          w[4 + i] = pack_bf16(bf_lo(w[4 + i]) + acc[2 * i][2 * h + 1],
-                               bf_hi(w[4 + i]) + acc[2 * i + 1][2 * h + 1]);
+        for (int i = 0; i < 8; ++i) {
+          const int r = (lane >> 4) + 2 * i;
+          const int k = r < n ? most : 0;
+          const uint16_t *p = k > 0 ? src + r * a.ld_base + col + 2 * u : a.base;
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
+                           dst + r * 64 + (((u >> 2) ^ ((r >> 1) & 3)) << 4) +
+                           4 * (u & 3)),
+                       "l"(p), "r"(k)
+                       : "memory");
         }
       }
-      store_bf16x16(out + r * a.ld_out, c, a.N, a.out_vec, w);
+      ahead_p += 16;
+      if (ahead_p >= ahead.n) {
+        ahead.row += ahead.n;
+        ahead_p = 0;
+        if (ahead.row < r1) settle(ahead);
+      }
     }
+    if (++slot_f == C::RING) slot_f = 0;
+    cp_async_commit();
+  };
+  // Loads only: nothing here waits for them.
+  float v[C::kPairs][2], alpha = 1.0f;
+  auto load_v = [&](const Walk &w) {
+    if (a.alpha && w.row < r1 && w.id >= 0) alpha = __ldg(a.alpha + w.id);
+#pragma unroll
+    for (int i = 0; i < C::kPairs; ++i) {
+      const int e = threadIdx.x + i * kExpandThreads;
+      const int r = e / (8 * KR), j = 2 * (e % (8 * KR));
+      const bool in = w.row < r1 && w.id >= 0 && r < w.n;
+      const float *p = a.V + (w.row + static_cast<int64_t>(r)) * a.ldv + j;
+      v[i][0] = in && j < a.R ? __ldcg(p) : 0.0f;
+      v[i][1] = in && j + 1 < a.R ? __ldcg(p + 1) : 0.0f;
+    }
+  };
+  auto store_v = [&](int buf) {
+    uint16_t *sv = reinterpret_cast<uint16_t *>(smem + buf * C::kV);
+#pragma unroll
+    for (int i = 0; i < C::kPairs; ++i) {
+      const int e = threadIdx.x + i * kExpandThreads;
+      const int r = e / (8 * KR), j = 2 * (e % (8 * KR));
+      uint32_t t[2];
+      split_pair<2>(v[i][0] * alpha, v[i][1] * alpha, t);
+      if (r < CH) {
+        *reinterpret_cast<uint32_t *>(sv + r * C::kLd + j) = t[0];
+        *reinterpret_cast<uint32_t *>(sv + (CH + r) * C::kLd + j) = t[1];
+      }
+    }
+  };
+
+  uint32_t b[KR][4][2];
+  int held = -1;
+  auto load_factor = [&](int id) {
+    if (live && id >= 0 && id != held) {
+      held = id;
+#pragma unroll
+      for (int k = 0; k < KR; ++k)
+        load_rank_block(a, a.P + id * a.stride_p, 16 * k, q, col + 4 * g, b[k]);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < C::RING - 1; ++i) fetch();
+  load_factor(w.id);
+  load_v(w);
+  store_v(0);
+  int buf = 0, slot = 0;
+  while (w.row < r1) {
+    __syncthreads();  // V of this chunk is there, the other buffer is free
+    Walk next = w;
+    next.row += w.n;
+    if (next.row < r1) settle(next);
+    load_v(next);
+    load_factor(w.id);
+    const uint32_t sv_lane = smem_addr(smem) + buf * C::kV +
+                             ((lane & 15) * C::kLd + 8 * (lane >> 4)) * 2;
+    uint16_t *dst = a.out + (w.row + static_cast<int64_t>(g)) * a.ld_out;
+    for (int m = 0; m < w.n && live; m += 16, dst += 16 * a.ld_out) {
+      cp_async_wait<C::RING - 2>();
+      __syncwarp();  // the piece is whole, and the one before it has been read
+      // The sums begin with base.  Fragment i's columns 2q and 2q + 1 are
+      // columns i and 4 + i of the lane's 8.
+      float acc[4][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t x[4];
+        if (a.base_unit >= 4) {
+          const uint4 y = *reinterpret_cast<const uint4 *>(
+              smem + C::kRingAt + (warp * C::RING + slot) * kPiece + (8 * h + g) * 64 +
+              ((q ^ ((g >> 1) & 3)) << 4));
+          x[0] = y.x;
+          x[1] = y.y;
+          x[2] = y.z;
+          x[3] = y.w;
+        } else {
+          const bool in = m + 8 * h + g < w.n;
+          load_pairs<4>(in ? a.base + (w.row + m + 8 * h + g) * a.ld_base : nullptr, c,
+                        a.N, 2, x);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          acc[2 * i][2 * h] = bf_lo(x[i]);
+          acc[2 * i + 1][2 * h] = bf_hi(x[i]);
+          acc[2 * i][2 * h + 1] = bf_lo(x[2 + i]);
+          acc[2 * i + 1][2 * h + 1] = bf_hi(x[2 + i]);
+        }
+      }
+      fetch();
+      if (w.id >= 0) {
+#pragma unroll
+        for (int k = 0; k < KR; ++k)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            uint32_t f[4];
+            ldmatrix4(sv_lane + ((t * CH + m) * C::kLd + 16 * k) * 2, f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              mma16816(acc[i], f[0], f[1], f[2], f[3], b[k][i][0], b[k][i][1]);
+          }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (m + 8 * h + g >= w.n) continue;
+        uint32_t x[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          x[i] = pack_bf16(acc[2 * i][2 * h], acc[2 * i + 1][2 * h]);
+          x[2 + i] = pack_bf16(acc[2 * i][2 * h + 1], acc[2 * i + 1][2 * h + 1]);
+        }
+        store_bf16x8(dst + 8 * h * a.ld_out, c, a.N, a.out_unit, x);
+      }
+      if (++slot == C::RING) slot = 0;
+    }
+    buf ^= 1;
+    store_v(buf);
+    w = next;
   }
 }
 
@@ -630,7 +727,7 @@ __device__ __forceinline__ void outer_body(const OuterArgs &a, const OuterSide &
       copy_tile<kOuterCols, kSize, C::kLdX>(
           base + (s - s0) % C::STAGES * C::kX,
           static_cast<const char *>(o.X) + t0 * o.ldx * kSize, o.ldx,
-          (n + 15) / 16 * 16, n, col0, o.N, o.x_vec);
+          (n + 15) / 16 * 16, n, col0, o.N, o.x_unit);
     }
     cp_async_commit();
   };
@@ -793,8 +890,12 @@ __global__ void __launch_bounds__(kThreads, kOuterCtas<MR>)
 }
 
 // --------------------------------------------------------------------- host
-bool vec_ok(const void *p, int64_t ld, int size, int64_t stride = 0) {
-  return aligned16(p) && ld * size % 16 == 0 && stride * size % 16 == 0;
+// Largest unit, in bytes, that every row of a matrix can be read in.
+int unit_of(const void *p, int64_t ld, int size, int64_t stride = 0) {
+  const uint64_t all = reinterpret_cast<uintptr_t>(p) |
+                       static_cast<uint64_t>(ld * size) |
+                       static_cast<uint64_t>(stride * size);
+  return all % 16 == 0 ? 16 : all % 8 == 0 ? 8 : all % 4 == 0 ? 4 : 2;
 }
 
 template <bool F32, int MW, int MF, int NJ>
@@ -837,45 +938,46 @@ fp8la_status launch_shrink(const ShrinkArgs &a, cudaStream_t s) {
   return launch_shrink_nj<F32, 16>(a, slot + 12, s);
 }
 
-template <int TM, int KR>
+template <int CH, int KR>
 fp8la_status launch_expand_one(ExpandArgs a, int slot, cudaStream_t s) {
-  constexpr int kSmem = ExpandCfg<TM, KR>::kSmem;
-  auto kern = lora_expand_kernel<TM, KR>;
+  using C = ExpandCfg<CH, KR>;
+  auto kern = lora_expand_kernel<CH, KR>;
   if (once_per_device(slot, [&] {
         return cudaFuncSetAttribute(
-            kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+            kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
       }) != cudaSuccess)
     return FP8LA_ERR_CUDA;
-  // Rows of a tile: the least time, with two CTAs on an SM that each take
-  // about as long to start as four 16-row pieces take to stream.
+  // Rows of a CTA: one wave, or a segment or so where those are short, since
+  // each brings its own factor.
   const int64_t T = a.seg.T, S = a.seg.S;
   const int64_t blocks = (a.N + kExpandCols - 1) / kExpandCols;
-  int64_t cost = INT64_MAX;
-  for (int tm = 16; tm <= TM; tm += 16) {
-    const int64_t tiles = T / tm + ((S < T ? S : T) + 1) / 2;
-    const int64_t waves = (tiles * blocks + 303) / 304;
-    const int64_t t = waves * (tm / 16 + 4);
-    if (t <= cost) {
-      cost = t;
-      a.tm = tm;
-    }
+  const int64_t ranges = blocks < 152 ? 152 / blocks : 1;
+  int64_t rows = (T + ranges - 1) / ranges;
+  if (CH == 16) {
+    const int64_t mean = (T + S - 1) / S;
+    if (rows > mean) rows = mean;
+  } else {
+    rows = (rows + 15) / 16 * 16;
   }
-  const dim3 grid(static_cast<unsigned>(blocks),
-                  static_cast<unsigned>(tile_bound(T, S, a.tm)), 1);
-  return launch(kern, grid, kThreads, kSmem, 0, s, a);
+  a.rows = static_cast<int32_t>(rows < 1 ? 1 : rows);
+  return launch(kern,
+                dim3(static_cast<unsigned>(blocks),
+                     static_cast<unsigned>((T + a.rows - 1) / a.rows), 1),
+                kExpandThreads, C::kSmem, 0, s, a);
 }
 
-template <int TM>
-fp8la_status launch_expand_tm(const ExpandArgs &a, int slot, cudaStream_t s) {
-  if (a.R <= 16) return launch_expand_one<TM, 1>(a, slot, s);
-  if (a.R <= 32) return launch_expand_one<TM, 2>(a, slot + 1, s);
-  if (a.R <= 64) return launch_expand_one<TM, 4>(a, slot + 2, s);
-  return launch_expand_one<TM, 8>(a, slot + 3, s);
+// CH: rows of a chunk.  V of the largest ranks takes twice the room.
+template <int CH>
+fp8la_status launch_expand_ch(const ExpandArgs &a, int slot, cudaStream_t s) {
+  if (a.R <= 16) return launch_expand_one<CH, 1>(a, slot, s);
+  if (a.R <= 32) return launch_expand_one<CH, 2>(a, slot + 1, s);
+  if (a.R <= 64) return launch_expand_one<CH, 4>(a, slot + 2, s);
+  return launch_expand_one<(CH < 64 ? CH : 64), 8>(a, slot + 3, s);
 }
 
 fp8la_status launch_expand(const ExpandArgs &a, cudaStream_t s) {
-  return short_segments(a.seg.T, a.seg.S) ? launch_expand_tm<16>(a, 46, s)
-                                          : launch_expand_tm<128>(a, 50, s);
+  return short_segments(a.seg.T, a.seg.S) ? launch_expand_ch<16>(a, 46, s)
+                                          : launch_expand_ch<128>(a, 50, s);
 }
 
 template <int MR>
@@ -898,7 +1000,7 @@ fp8la_status launch_outer(const OuterArgs &a, int slot, cudaStream_t s) {
                 kThreads, kSmem, cluster, s, a);
 }
 
-constexpr bool kUseTma = true;
+// Fewest rows for the tcgen05 kernels.
 constexpr int64_t kTmaRows = 256;
 
 constexpr int64_t kMaxWidth = int64_t(1) << 22;  // grid limits
@@ -941,13 +1043,13 @@ fp8la_status run_shrink(const Segments &seg, const void *X, int32_t dtype,
   a.stride_p = stride;
   a.K = K;
   a.R = R;
-  a.x_vec = vec_ok(X, ldx, dtype == FP8LA_TYPE_BF16 ? 2 : 4);
-  a.p_vec = vec_ok(P, ldp, 2, stride);
+  a.x_unit = unit_of(X, ldx, dtype == FP8LA_TYPE_BF16 ? 2 : 4);
+  a.p_unit = unit_of(P, ldp, 2, stride);
   a.alpha = alpha;
   a.V = V;
   a.ldv = ldv;
   // Long segments of BF16 rows that TMA can read go to tcgen05.
-  if (dtype == FP8LA_TYPE_BF16 && a.x_vec && a.p_vec && kUseTma &&
+  if (dtype == FP8LA_TYPE_BF16 && a.x_unit == 16 && a.p_unit == 16 &&
       !short_segments(seg.T, seg.S) && seg.T >= kTmaRows)
     return launch_shrink_tma(a, s);
   return dtype == FP8LA_TYPE_BF16 ? launch_shrink<false>(a, s)
@@ -973,9 +1075,9 @@ fp8la_status run_expand(const Segments &seg, const float *V, int64_t ldv, int32_
   a.out = out;
   a.ld_base = ld_base;
   a.ld_out = ld_out;
-  a.p_vec = vec_ok(P, ldp, 2, stride);
-  a.base_vec = vec_ok(base, ld_base, 2);
-  a.out_vec = vec_ok(out, ld_out, 2);
+  a.p_unit = unit_of(P, ldp, 2, stride);
+  a.base_unit = unit_of(base, ld_base, 2);
+  a.out_unit = unit_of(out, ld_out, 2);
   return launch_expand(a, s);
 }
 
@@ -1073,15 +1175,15 @@ extern "C" fp8la_status fp8la_lora_backward(
   OuterArgs o{};
   o.seg = seg;
   o.side[0] = {dv, ld_dv, x, ldx, K, dA,
-               vec_ok(x, ldx, x_dtype == FP8LA_TYPE_BF16 ? 2 : 4),
+               unit_of(x, ldx, x_dtype == FP8LA_TYPE_BF16 ? 2 : 4),
                x_dtype == FP8LA_TYPE_F32, 0};
   o.side[1] = {v, ldv, dy, ld_dy, N, dB,
-               vec_ok(dy, ld_dy, dy_dtype == FP8LA_TYPE_BF16 ? 2 : 4),
+               unit_of(dy, ld_dy, dy_dtype == FP8LA_TYPE_BF16 ? 2 : 4),
                dy_dtype == FP8LA_TYPE_F32, 1};
   o.alpha = alpha;
   o.R = rank;
-  if (kUseTma && !o.side[0].x_f32 && !o.side[1].x_f32 && o.side[0].x_vec &&
-      o.side[1].x_vec && !short_segments(rows, num_segments) && rows >= kTmaRows) {
+  if (!o.side[0].x_f32 && !o.side[1].x_f32 && o.side[0].x_unit == 16 &&
+      o.side[1].x_unit == 16 && !short_segments(rows, num_segments) && rows >= kTmaRows) {
     st = launch_outer_tma(o, s);
     return st == FP8LA_OK ? launch_status() : st;
   }

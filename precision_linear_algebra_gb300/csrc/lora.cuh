@@ -153,7 +153,7 @@ struct ShrinkArgs {
   int64_t ldp, stride_p;
   int64_t K;
   int32_t R;
-  int32_t x_vec, p_vec;
+  int32_t x_unit, p_unit;  // bytes that rows can be read in
   const float *alpha;  // null: 1
   float *V;            // [T][ldv]
   int64_t ldv;
@@ -166,7 +166,7 @@ struct OuterSide {
   int64_t ldx;
   int64_t N;
   float *G;             // [n][R][N]
-  int32_t x_vec, x_f32;
+  int32_t x_unit, x_f32;
   int32_t use_alpha;
 };
 struct OuterArgs {
