@@ -69,7 +69,7 @@ inline fp8la_status launch_status() {
 }
 
 namespace detail {
-constexpr int kSlots = 64;
+constexpr int kSlots = 80;
 constexpr int kDevs = 64;
 bool setup_done(int slot, int dev);
 void mark_setup_done(int slot, int dev);

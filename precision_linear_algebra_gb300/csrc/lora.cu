@@ -329,22 +329,6 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // ------------------------------------------------------------------- expand
-struct ExpandArgs {
-  Segments seg;
-  const float *V;        // [T][ldv]
-  int64_t ldv;
-  int32_t R;
-  const float *alpha;    // null: 1
-  const uint16_t *P;     // [n][R][ldp]
-  int64_t ldp, stride_p;
-  int64_t N;
-  const uint16_t *base;
-  uint16_t *out;
-  int64_t ld_base, ld_out;
-  int32_t p_unit, base_unit, out_unit;
-  int32_t rows;          // of a CTA
-};
-
 constexpr int kExpandThreads = 512;
 constexpr int kExpandWarps = kExpandThreads / 32;
 constexpr int kWarpCols = 32;
@@ -406,11 +390,6 @@ struct ExpandCfg {
   static_assert(kV % 16 == 0 && kSmem <= 226 * 1024, "shared memory");
 };
 
-// Walks down rows: n rows of segment s, which uses adapter id, from `row` on.
-struct Walk {
-  int row, n, s, id;
-};
-
 template <int CH, int KR>
 __global__ void __launch_bounds__(kExpandThreads, 1)
     lora_expand_kernel(const ExpandArgs a) {
@@ -425,41 +404,11 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
   const int r0 = blockIdx.y * a.rows, r1 = min(a.seg.T, r0 + a.rows);
   pdl_wait();
   pdl_launch_dependents();
-  bool bad = false;
-  for (int i = threadIdx.x; i <= a.seg.S; i += kExpandThreads) {
-    const int lo = a.seg.offsets[i];
-    offsets[i] = lo;
-    bad |= lo < 0 || lo > a.seg.T || (i == 0 && lo != 0);
-    if (i < a.seg.S) {
-      const int id = a.seg.ids[i];
-      ids[i] = id;
-      bad |= a.seg.offsets[i + 1] < lo || id < -1 || id >= a.seg.n;
-    }
-  }
-  if (__syncthreads_or(bad)) {
-    if (threadIdx.x == 0) atomicOr(a.seg.status, kStatusBadDeviceArg);
-    return;
-  }
-  // The rows after the last segment count as one more, without an adapter.
-  auto settle = [&](Walk &w) {
-    while (w.s < a.seg.S && offsets[w.s + 1] <= w.row) ++w.s;
-    const int end = min(r1, w.s < a.seg.S ? offsets[w.s + 1] : r1);
-    w.n = min(CH, end - w.row);
-    w.id = w.s < a.seg.S ? ids[w.s] : -1;
-  };
+  if (!load_segments<kExpandThreads>(a.seg, offsets, ids)) return;
+  auto settle = [&](Walk &w) { settle_walk<CH>(w, a.seg.S, offsets, ids, r1); };
   Walk w;
-  {
-    // The last segment that begins at or before r0.
-    int lo = 0, hi = a.seg.S;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (offsets[mid] <= r0) lo = mid;
-      else hi = mid - 1;
-    }
-    w.row = r0;
-    w.s = lo;
-    settle(w);
-  }
+  begin_walk(w, r0, a.seg.S, offsets);
+  settle(w);
 
   const bool live = col < a.N;
   const uint32_t ring = smem_addr(smem) + C::kRingAt + warp * C::RING * kPiece;
@@ -1000,8 +949,10 @@ fp8la_status launch_outer(const OuterArgs &a, int slot, cudaStream_t s) {
                 kThreads, kSmem, cluster, s, a);
 }
 
-// Fewest rows for the tcgen05 kernels.
-constexpr int64_t kTmaRows = 256;
+// Fewest rows for the tcgen05 kernels; fewest elements for that of expand,
+// whose CTAs take 64 rows x 256 columns at a time: below, it has work for few
+// SMs (256 x 1024: 26 us for a backward pass that takes 19 with mma.sync).
+constexpr int64_t kTmaRows = 256, kTmaExpand = 152 * 64 * 256;
 
 constexpr int64_t kMaxWidth = int64_t(1) << 22;  // grid limits
 
@@ -1078,6 +1029,10 @@ fp8la_status run_expand(const Segments &seg, const float *V, int64_t ldv, int32_
   a.p_unit = unit_of(P, ldp, 2, stride);
   a.base_unit = unit_of(base, ld_base, 2);
   a.out_unit = unit_of(out, ld_out, 2);
+  a.v_vec = unit_of(V, ldv, 4) == 16;
+  if (a.base_unit == 16 && a.out_unit == 16 && a.p_unit == 16 && R <= 64 &&
+      !short_segments(seg.T, seg.S) && seg.T * N >= kTmaExpand)
+    return launch_expand_tma(a, s);
   return launch_expand(a, s);
 }
 

@@ -159,6 +159,77 @@ struct ShrinkArgs {
   int64_t ldv;
 };
 
+struct ExpandArgs {
+  Segments seg;
+  const float *V;        // [T][ldv]
+  int64_t ldv;
+  int32_t R;
+  const float *alpha;    // null: 1
+  const uint16_t *P;     // [n][R][ldp]
+  int64_t ldp, stride_p;
+  int64_t N;
+  const uint16_t *base;
+  uint16_t *out;
+  int64_t ld_base, ld_out;
+  int32_t p_unit, base_unit, out_unit;
+  int32_t v_vec;         // V's rows can be read in 16-byte units
+  int32_t rows;          // of a CTA
+};
+
+
+// Walks down rows: n rows of segment s, which uses adapter id, from `row` on.
+struct Walk {
+  int row, n, s, id;
+};
+
+// Copies the segments to shared memory; false, and recorded, where offsets
+// decrease or leave 0..T or ids leave -1..n-1.  Ends with a barrier.
+template <int THREADS>
+__device__ __forceinline__ bool load_segments(const Segments &g, int *offsets,
+                                              int *ids) {
+  bool bad = false;
+  for (int i = threadIdx.x; i <= g.S; i += THREADS) {
+    const int lo = g.offsets[i];
+    offsets[i] = lo;
+    bad |= lo < 0 || lo > g.T || (i == 0 && lo != 0);
+    if (i < g.S) {
+      const int id = g.ids[i];
+      ids[i] = id;
+      bad |= g.offsets[i + 1] < lo || id < -1 || id >= g.n;
+    }
+  }
+  if (__syncthreads_or(bad)) {
+    if (threadIdx.x == 0) atomicOr(g.status, kStatusBadDeviceArg);
+    return false;
+  }
+  return true;
+}
+
+// A walk from row r0 on (to be settled): the last segment that begins at or
+// before it.
+__device__ __forceinline__ void begin_walk(Walk &w, int r0, int S, const int *offsets) {
+  int lo = 0, hi = S;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (offsets[mid] <= r0) lo = mid;
+    else hi = mid - 1;
+  }
+  w.row = r0;
+  w.s = lo;
+}
+
+// Finds the segment of w.row (< end) and the rows of it that come next, at
+// most CH.  The rows after the last segment count as one more, without an
+// adapter.
+template <int CH>
+__device__ __forceinline__ void settle_walk(Walk &w, int S, const int *offsets,
+                                            const int *ids, int end) {
+  while (w.s < S && offsets[w.s + 1] <= w.row) ++w.s;
+  const int last = min(end, w.s < S ? offsets[w.s + 1] : end);
+  w.n = min(CH, last - w.row);
+  w.id = w.s < S ? ids[w.s] : -1;
+}
+
 struct OuterSide {
   const float *W;       // [T][ldw]
   int64_t ldw;
@@ -227,8 +298,9 @@ inline int choose_cluster(int64_t items, int64_t stages, int64_t slots, int fixe
 }
 
 // The same sums for BF16 operands that TMA can read, on tcgen05 (lora_tma.cu).
-// V of tiles of 128 rows; and both sides' gradients.
+// V of tiles of 128 rows; base + V P at ranks up to 64; both sides' gradients.
 fp8la_status launch_shrink_tma(const ShrinkArgs &a, cudaStream_t s);
+fp8la_status launch_expand_tma(const ExpandArgs &a, cudaStream_t s);
 fp8la_status launch_outer_tma(const OuterArgs &a, cudaStream_t s);
 
 }  // namespace lora

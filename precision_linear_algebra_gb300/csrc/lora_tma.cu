@@ -10,6 +10,13 @@
 // shared out over a cluster, whose CTAs' sums are added through distributed
 // shared memory in rank order.
 //
+// expand: D[128 rows][256 columns] = V[128][R] P[R][256 columns], V split into
+// two BF16 terms by converter warps (K-major), P as TMA writes it (MN-major).
+// base comes by TMA, the epilogue adds to it in shared memory and TMA stores
+// the sum from there, so nothing but the sum itself takes an instruction for
+// each element: the mma.sync form needs 22 of them and is bound by that.  The
+// CTAs get equal shares of the rows of all column blocks.
+//
 // outer: D[128 columns][R] += X[t][128 columns]^T V[t][R], t being the MMA's
 // K.  X is the transposed (MN-major) operand, just as TMA writes a box of 64
 // columns x 64 rows.  V (FP32) enters as three BF16 terms, which converter
@@ -238,6 +245,363 @@ __global__ void __launch_bounds__(kSThreads)
     a.V[(f.row0 + static_cast<int64_t>(r)) * a.ldv + j] = v * alpha;
   }
   if (csize > 1) cluster_sync_all();  // no CTA leaves while its sums are read
+}
+
+// ------------------------------------------------------------------- expand
+constexpr int kEEpi = 8;            // epilogue warps
+constexpr int kEConv = 4;           // warps that split V
+constexpr int kEProducer = kEEpi + kEConv;
+constexpr int kEMma = kEProducer + 1;
+constexpr int kEStore = kEProducer + 2;
+constexpr int kEThreads = 32 * (kEStore + 1);
+constexpr int kECols = 256;
+constexpr int kERows = 128;         // of a tile
+constexpr int kEGrain = 64;         // rows by which the CTAs' shares are cut
+
+template <int RP>
+struct ExpandTma {
+  static constexpr int kBox = kERows * 128;         // 128 rows x 64 columns
+  static constexpr int kStage = 4 * kBox;
+  static constexpr int kPBox = RP * 128;            // RP ranks x 64 columns
+  static constexpr int kVTerm = kERows * 128;       // 128 rows x up to 64 ranks
+  static constexpr int kP = 2 * kStage;
+  static constexpr int kV = kP + 4 * kPBox;
+  static constexpr int kBar = kV + 2 * kVTerm;
+  static constexpr int kNumBars = 15;
+  static constexpr int kMisc = kBar + kNumBars * 8;
+  static constexpr int kSegs = kMisc + 16;
+  static constexpr int kAlloc = kSegs + (2 * kMaxSegments + 1) * 4 + 1024;
+  static constexpr int kUnits = kERows * (RP / 8) / (32 * kEConv);
+  static_assert(kPBox % 1024 == 0 && kBar % 8 == 0, "swizzle atoms");
+  static_assert(kAlloc <= 226 * 1024, "shared memory");
+};
+
+template <int RP>
+__global__ void __launch_bounds__(kEThreads, 1)
+    lora_expand_tma_kernel(const __grid_constant__ CUtensorMap tmBase,
+                           const __grid_constant__ CUtensorMap tmOut,
+                           const __grid_constant__ CUtensorMap tmP,
+                           const ExpandArgs a, const uint64_t timeout_ns) {
+  using C = ExpandTma<RP>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_addr(smem_raw);
+  const uint32_t base = (raw_addr + 1023u) & ~1023u;
+  uint8_t *sbase = smem_raw + (base - raw_addr);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int *offsets = reinterpret_cast<int *>(sbase + C::kSegs);
+  int *ids = offsets + a.seg.S + 1;
+  const uint32_t bar0 = base + C::kBar;
+  auto full_bar = [&](int b) { return bar0 + 8u * b; };          // base is there
+  auto empty_bar = [&](int b) { return bar0 + 8u * (2 + b); };   // and stored
+  auto done_bar = [&](int b) { return bar0 + 8u * (4 + b); };    // out is staged
+  auto accfull_bar = [&](int b) { return bar0 + 8u * (6 + b); };
+  auto accfree_bar = [&](int b) { return bar0 + 8u * (8 + b); };
+  const uint32_t pfull_bar = bar0 + 80, pfree_bar = bar0 + 88;
+  const uint32_t vready_bar = bar0 + 96, vfree_bar = bar0 + 104;
+  const uint32_t final_bar = bar0 + 112;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sbase + C::kMisc);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(sbase + C::kMisc + 4);
+  if (threadIdx.x == 0) {
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(full_bar(b), 1);
+      mbar_init(empty_bar(b), 1);
+      mbar_init(done_bar(b), kEEpi);
+      mbar_init(accfull_bar(b), 1);
+      mbar_init(accfree_bar(b), kEEpi);
+    }
+    mbar_init(pfull_bar, 1);
+    mbar_init(pfree_bar, 1);
+    mbar_init(vready_bar, kEConv);
+    mbar_init(vfree_bar, 1);
+    mbar_init(final_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  if (!load_segments<kEThreads>(a.seg, offsets, ids)) return;
+  if (warp == kEMma) {
+    tmem_alloc(smem_addr(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const bool in_place = a.base == a.out;
+
+  // Every role goes through the same tiles: visit(tile, n) for each, in order;
+  // false ends the walk.
+  auto tiles = [&](auto &&visit) {
+    const int groups = (a.seg.T + kEGrain - 1) / kEGrain;
+    const int64_t blocks = (a.N + kECols - 1) / kECols, all = groups * blocks;
+    int64_t u = all * blockIdx.x / gridDim.x;
+    const int64_t u1 = all * (blockIdx.x + 1) / gridDim.x;
+    int n = 0;
+    while (u < u1) {
+      const int block = static_cast<int>(u / groups);
+      const int g0 = static_cast<int>(u - static_cast<int64_t>(block) * groups);
+      const int g1 = static_cast<int>(min(static_cast<int64_t>(groups), g0 + u1 - u));
+      const int end = min(a.seg.T, g1 * kEGrain);
+      Walk w;
+      begin_walk(w, g0 * kEGrain, a.seg.S, offsets);
+      while (w.row < end) {
+        settle_walk<kERows>(w, a.seg.S, offsets, ids, end);
+        // Rows without an adapter are where they should be already, in place.
+        if (w.id >= 0 || !in_place)
+          if (!visit(w, block * kECols, n++)) return;
+        w.row += w.n;
+      }
+      u += g1 - g0;
+    }
+  };
+  // Runs of tiles with one factor: its adapter and column block.
+  struct Run {
+    int id = -1, col = -1, count = 0;
+    __device__ bool next(const Walk &w, int c) {
+      if (w.id < 0 || (w.id == id && c == col)) return false;
+      id = w.id;
+      col = c;
+      ++count;
+      return true;
+    }
+  };
+
+  if (warp == kEProducer) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      Run run;
+      int issued = 0;
+      tiles([&](const Walk &w, int col, int n) {
+        const int b = n & 1;
+        if (run.next(w, col)) {
+          if (run.count > 1 && !mbar_wait(pfree_bar, run.count & 1u, timeout_ns,
+                                          a.seg.status, abort_flag))
+            return false;
+          mbar_arrive_expect_tx(pfull_bar, 4 * C::kPBox);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            tma_load_3d(base + C::kP + j * C::kPBox, &tmP, pfull_bar, col + 64 * j, 0,
+                        w.id);
+        }
+        if (!mbar_wait(empty_bar(b), ((n >> 1) & 1u) ^ 1u, timeout_ns, a.seg.status,
+                       abort_flag))
+          return false;
+        mbar_arrive_expect_tx(full_bar(b), C::kStage);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          tma_load_2d(base + b * C::kStage + j * C::kBox, &tmBase, full_bar(b),
+                      col + 64 * j, w.row);
+        ++issued;
+        return true;
+      });
+      for (int b = 0; b < 2; ++b)
+        if (issued > b)
+          mbar_wait_drain(full_bar(b), ((issued - 1 - b) / 2) & 1u, timeout_ns,
+                          a.seg.status);
+      if (run.count > 0)
+        mbar_wait_drain(pfull_bar, (run.count - 1) & 1u, timeout_ns, a.seg.status);
+    }
+  } else if (warp == kEMma) {
+    // ----------------------------------------------------------------- MMA
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(kERows, kECols, false) | (1u << 16);
+      Run run;
+      int m = 0;  // tiles with an adapter
+      tiles([&](const Walk &w, int col, int n) {
+        if (w.id < 0) return true;
+        const int b = m & 1;
+        if (run.next(w, col)) {
+          // All MMAs with the factor before this one have been issued.
+          if (run.count > 1) umma_commit(pfree_bar);
+          if (!mbar_wait(pfull_bar, (run.count - 1) & 1u, timeout_ns, a.seg.status,
+                         abort_flag))
+            return false;
+        }
+        if (!mbar_wait(accfree_bar(b), ((m >> 1) & 1u) ^ 1u, timeout_ns, a.seg.status,
+                       abort_flag) ||
+            !mbar_wait(vready_bar, m & 1u, timeout_ns, a.seg.status, abort_flag))
+          return false;
+        tc_fence_after();
+        // V [128 rows][ranks] is K-major; the factor [ranks][columns] MN-major.
+#pragma unroll
+        for (int k = 0; k < RP / 16; ++k)
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            umma_bf16(tmem_base + b * kECols,
+                      smem_desc_k128_sw128(base + C::kV + t * C::kVTerm) + 2u * k,
+                      smem_desc_mn_sw128(base + C::kP + k * 2048, C::kPBox), idesc,
+                      (k > 0 || t > 0) ? 1u : 0u);
+        umma_commit(vfree_bar);
+        umma_commit(accfull_bar(b));
+        ++m;
+        return true;
+      });
+      umma_commit(final_bar);
+      mbar_wait_drain(final_bar, 0, timeout_ns, a.seg.status);
+    }
+  } else if (warp == kEStore) {
+    // --------------------------------------------------------------- store
+    if (lane == 0) {
+      tiles([&](const Walk &w, int col, int n) {
+        const int b = n & 1;
+        if (!mbar_wait(done_bar(b), (n >> 1) & 1u, timeout_ns, a.seg.status, abort_flag))
+          return false;
+        if (w.n == kERows) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (col + 64 * j < a.N)
+              tma_store_2d(&tmOut, base + b * C::kStage + j * C::kBox, col + 64 * j,
+                           w.row);
+          bulk_commit_group();
+          bulk_wait_read_all();
+        }
+        mbar_arrive(empty_bar(b));
+        return true;
+      });
+      bulk_wait_all();
+    }
+  } else if (warp >= kEEpi) {
+    // ---------------------------------------------------------- converters
+    const int ct = threadIdx.x - 32 * kEEpi;
+    float v[C::kUnits][8], alpha = 1.0f;
+    // A tile's V is loaded while the one before is multiplied: the buffer is
+    // waited for after the loads.
+    auto load_v = [&](const Walk &w) {
+      alpha = a.alpha ? __ldg(a.alpha + w.id) : 1.0f;
+#pragma unroll
+      for (int u = 0; u < C::kUnits; ++u) {
+        const int e = ct + u * 32 * kEConv;
+        const int r = e / (RP / 8), j = 8 * (e % (RP / 8));
+        const float *p = a.V + (w.row + static_cast<int64_t>(r)) * a.ldv + j;
+        if (a.v_vec && j + 8 <= a.R) {
+          float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f), y = x;
+          if (r < w.n) {
+            x = __ldcg(reinterpret_cast<const float4 *>(p));
+            y = __ldcg(reinterpret_cast<const float4 *>(p) + 1);
+          }
+          v[u][0] = x.x;
+          v[u][1] = x.y;
+          v[u][2] = x.z;
+          v[u][3] = x.w;
+          v[u][4] = y.x;
+          v[u][5] = y.y;
+          v[u][6] = y.z;
+          v[u][7] = y.w;
+        } else {
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            v[u][q] = r < w.n && j + q < a.R ? __ldcg(p + q) : 0.0f;
+        }
+      }
+    };
+    auto store_v = [&](int m) {
+      const bool ready = mbar_wait(vfree_bar, (m & 1u) ^ 1u, timeout_ns, a.seg.status,
+                                   abort_flag);
+      if (!__all_sync(0xffffffffu, ready)) return false;
+#pragma unroll
+      for (int u = 0; u < C::kUnits; ++u) {
+        const int e = ct + u * 32 * kEConv;
+        const uint32_t r = e / (RP / 8), unit = e % (RP / 8);
+        uint32_t t[2][4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t x[2];
+          split_pair<2>(v[u][2 * q] * alpha, v[u][2 * q + 1] * alpha, x);
+          t[0][q] = x[0];
+          t[1][q] = x[1];
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          st_shared_v4(base + C::kV + k * C::kVTerm + r * 128 +
+                           ((unit ^ (r & 7u)) << 4),
+                       t[k][0], t[k][1], t[k][2], t[k][3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(vready_bar);
+      return true;
+    };
+    int m = 0;
+    tiles([&](const Walk &w, int col, int n) {
+      if (w.id < 0) return true;
+      load_v(w);
+      return store_v(m++);
+    });
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int quarter = warp & 3, half = warp >> 2;
+    const int row = 32 * quarter + lane;
+    const uint32_t lane_base =
+        tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + 128 * half;
+    int m = 0;
+    tiles([&](const Walk &w, int col, int n) {
+      const int b = n & 1, t = m & 1;
+      bool ready = mbar_wait(full_bar(b), (n >> 1) & 1u, timeout_ns, a.seg.status,
+                             abort_flag);
+      if (w.id >= 0)
+        ready = ready && mbar_wait(accfull_bar(t), (m >> 1) & 1u, timeout_ns,
+                                   a.seg.status, abort_flag);
+      if (!__all_sync(0xffffffffu, ready)) return false;
+      tc_fence_after();
+      uint16_t *dst = a.out + (w.row + static_cast<int64_t>(row)) * a.ld_out;
+#pragma unroll 1
+      for (int j = 0; j < 4; ++j) {  // 32 columns
+        uint8_t *src = sbase + b * C::kStage + (2 * half + (j >> 1)) * C::kBox + row * 128;
+        uint32_t acc[32];
+        if (w.id >= 0) tmem_ld32(lane_base + t * kECols + 32 * j, acc);
+        const int64_t c0 = col + 128 * half + 32 * j;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // 8 columns
+          uint4 *at = reinterpret_cast<uint4 *>(
+              src + (((4 * (j & 1) + i) ^ (row & 7)) << 4));
+          uint4 x = *at;
+          if (w.id >= 0) {
+            uint32_t *y = &x.x;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const __nv_bfloat162 s = __floats2bfloat162_rn(
+                  bf_lo(y[q]) + __uint_as_float(acc[8 * i + 2 * q]),
+                  bf_hi(y[q]) + __uint_as_float(acc[8 * i + 2 * q + 1]));
+              y[q] = *reinterpret_cast<const uint32_t *>(&s);
+            }
+          }
+          if (w.n == kERows) {
+            *at = x;
+          } else if (row < w.n) {
+            // A tile that ends inside the 128 rows: what follows belongs to
+            // another segment or share.
+            const int64_t c = c0 + 8 * i;
+            if (c + 8 <= a.N) {
+              *reinterpret_cast<uint4 *>(dst + c) = x;
+            } else {
+              const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                if (c + q < a.N)
+                  dst[c + q] = static_cast<uint16_t>(q & 1 ? y[q >> 1] >> 16 : y[q >> 1]);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (w.id >= 0) mbar_arrive(accfree_bar(t));
+        mbar_arrive(done_bar(b));
+      }
+      if (w.id >= 0) ++m;
+      return true;
+    });
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kEMma) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
+  }
 }
 
 // -------------------------------------------------------------------- outer
@@ -602,6 +966,27 @@ fp8la_status shrink_one(const ShrinkArgs &a, int slot, cudaStream_t s) {
 }
 
 template <int RP>
+fp8la_status expand_one(const ExpandArgs &a, int slot, cudaStream_t s) {
+  using C = ExpandTma<RP>;
+  auto kern = lora_expand_tma_kernel<RP>;
+  if (once_per_device(slot, [&] {
+        return cudaFuncSetAttribute(
+            kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kAlloc);
+      }) != cudaSuccess)
+    return FP8LA_ERR_CUDA;
+  CUtensorMap tmBase, tmOut, tmP;
+  const int64_t stride = a.seg.n > 1 ? a.stride_p : a.R * a.ldp;
+  const int sms = sm_count();
+  if (sms <= 0 ||
+      !encode_bf16(&tmBase, a.base, a.N, a.seg.T, 1, a.ld_base, 0, kERows, 2) ||
+      !encode_bf16(&tmOut, a.out, a.N, a.seg.T, 1, a.ld_out, 0, kERows, 2) ||
+      !encode_bf16(&tmP, a.P, a.N, a.R, a.seg.n, a.ldp, stride, RP, 3))
+    return FP8LA_ERR_CUDA;
+  return launch(kern, dim3(sms, 1, 1), kEThreads, C::kAlloc, 0, s, tmBase, tmOut, tmP, a,
+                wait_timeout_ns());
+}
+
+template <int RP>
 fp8la_status outer_one(const OuterArgs &a, int slot, cudaStream_t s) {
   using C = OuterTma<RP>;
   auto kern = lora_outer_tma_kernel<RP>;
@@ -633,6 +1018,12 @@ fp8la_status launch_shrink_tma(const ShrinkArgs &a, cudaStream_t s) {
          : a.R <= 32 ? shrink_one<32>(a, 55, s)
          : a.R <= 64 ? shrink_one<64>(a, 56, s)
                      : shrink_one<128>(a, 57, s);
+}
+
+fp8la_status launch_expand_tma(const ExpandArgs &a, cudaStream_t s) {
+  return a.R <= 16   ? expand_one<16>(a, 62, s)
+         : a.R <= 32 ? expand_one<32>(a, 63, s)
+                     : expand_one<64>(a, 64, s);
 }
 
 fp8la_status launch_outer_tma(const OuterArgs &a, cudaStream_t s) {
