@@ -49,12 +49,6 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t (&w)[NT]) 
   }
 }
 
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t n;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
-  return n;
-}
-
 // Sum over the cluster's CTAs, in rank order, of the float at address `addr`
 // of each one's shared memory.
 __device__ __forceinline__ float cluster_sum(uint32_t addr, uint32_t n) {

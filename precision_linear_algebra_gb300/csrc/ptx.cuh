@@ -126,16 +126,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap,
       : "memory");
 }
 
-// Brings a 3-D box into L2 only.
-__device__ __forceinline__ void tma_prefetch_3d(const void *tmap, int32_t c0,
-                                                int32_t c1, int32_t c2) {
-  asm volatile(
-      "cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
-          reinterpret_cast<uint64_t>(tmap)),
-      "r"(c0), "r"(c1), "r"(c2)
-      : "memory");
-}
-
 // Untiled copy of `bytes` bytes (a multiple of 16, both addresses 16-byte
 // aligned) into shared memory, signalled on `bar`.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src,
@@ -314,6 +304,11 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t n;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+  return n;
+}
 
 // All threads of all CTAs of the cluster.
 __device__ __forceinline__ void cluster_sync_all() {
@@ -331,6 +326,11 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
                : "=r"(r)
                : "r"(addr), "r"(rank));
   return r;
+}
+__device__ __forceinline__ int ld_shared_cluster(uint32_t cluster_addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+  return v;
 }
 
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {

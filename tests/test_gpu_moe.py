@@ -116,6 +116,33 @@ def test_route_no_tokens_and_no_sort():
     assert torch.equal(ids, ids2) and torch.equal(w, w2)
 
 
+@pytest.mark.parametrize("T", [15, 16, 17, 32, 33, 47, 64, 65, 96, 113, 127, 128, 129])
+@pytest.mark.parametrize("E,k", [(1, 1), (8, 2), (64, 8), (1024, 16)])
+def test_route_one_launch(T, E, k):
+    """Token counts around a CTA's and a cluster's, a fifth of the logits masked."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(T * E + k)
+    z = torch.randn(T, E, generator=g, device="cuda")
+    z = z.masked_fill(torch.rand(T, E, generator=g, device="cuda") < 0.2, -math.inf)
+    check_route(lib(), z, k, True)
+
+
+def test_route_a_million_tokens_without_sort():
+    """Only the sort limits tokens x top_k: 2^20 + 9 tokens with 16 of 16."""
+    import torch
+    fl = lib()
+    T = (1 << 20) + 9
+    g = torch.Generator(device="cuda").manual_seed(1)
+    z = torch.randn(T, 16, generator=g, device="cuda")
+    ids, w, offs, order = fl.moe_route(z, 16, sort=False)
+    torch.cuda.synchronize()
+    top, want = torch.sort(z, dim=1, descending=True, stable=True)
+    assert offs is None and order is None
+    assert torch.equal(ids.long(), want)
+    p = torch.softmax(top.double(), 1)
+    assert ((w.double() - p).abs() <= 24 * 2.0 ** -23 * p + 1e-38).all()
+
+
 # -------------------------------------------------------------------- layer
 def make_layer(T, E, k, D, F, dtype="bfloat16", fmt="e4m3", seed=0, ldpad=0):
     """Random weights as the quantiser leaves them, and a routing with
