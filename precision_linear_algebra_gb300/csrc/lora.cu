@@ -31,6 +31,13 @@
 // as good as an FP32 product's, two (relative error 2^-17) where it is
 // rounded to BF16.  base is the first term of its sum, which is rounded
 // once.
+//
+// Measured on the stream: forward 9.7 us for 8 rows of their own, rank 16, 4096
+// -> 4096 (the call's host side takes longer), 25 us for 333 ragged rows of FP32,
+// rank 24, 1000 -> 1001.  FP32 rows at size cost three BF16 terms here: 4096 rows,
+// rank 64, 8192 -> 8192, 131 us forward (276 MB, 2.1 TB/s) and, at rank 32, 250 us
+// backward (1.6 TB/s).  BF16 rows at odd addresses are copied element by element:
+// 3000 rows, rank 48, 6099 -> 4103, 178 us forward, 80 at even ones.
 #include <cuda_bf16.h>
 
 #include "lora.cuh"
@@ -925,8 +932,15 @@ fp8la_status launch_expand_ch(const ExpandArgs &a, int slot, cudaStream_t s) {
 }
 
 fp8la_status launch_expand(const ExpandArgs &a, cudaStream_t s) {
-  return short_segments(a.seg.T, a.seg.S) ? launch_expand_ch<16>(a, 46, s)
-                                          : launch_expand_ch<128>(a, 50, s);
+  // Chunks of 16 rows, a segment to a CTA, spread few short segments over the
+  // SMs; with more, loading a factor for each costs more.  Measured, us for a
+  // forward pass with chunks of 16 / 128, 4096 -> 4096, rank 16: 8 segments of one
+  // row 9.7 / 22.1, 64 of one 24.3 / 40.6, 256 of one 61.9 / 52.4, 1024 of one
+  // 218 / 160, 64 of 4 24.3 / 22.5; rank 64: 64 of one 35.5 / 84.3, 256 of one
+  // 111.6 / 112.9, 1024 of one 416 / 386, 64 of 16 44.5 / 46.8.
+  return a.seg.T < 256 && short_segments(a.seg.T, a.seg.S)
+             ? launch_expand_ch<16>(a, 46, s)
+             : launch_expand_ch<128>(a, 50, s);
 }
 
 template <int MR>
@@ -949,10 +963,13 @@ fp8la_status launch_outer(const OuterArgs &a, int slot, cudaStream_t s) {
                 kThreads, kSmem, cluster, s, a);
 }
 
-// Fewest rows for the tcgen05 kernels; fewest elements for that of expand,
-// whose CTAs take 64 rows x 256 columns at a time: below, it has work for few
-// SMs (256 x 1024: 26 us for a backward pass that takes 19 with mma.sync).
-constexpr int64_t kTmaRows = 256, kTmaExpand = 152 * 64 * 256;
+// Fewest rows for tcgen05 in shrink and outer: a whole tile.  Below, every call
+// takes mma.sync, so that a small call's result does not depend on how its rows
+// are aligned.  That has a price: 90 rows in two segments, rank 20, 2048 ->
+// 2048, take 14.8 us forward and 27.8 backward, with tcgen05 13.4 and 21.0; 8 rows
+// of their own, rank 64, 12.4 and 32.3 against 11.9 and 26.3.  128 rows, rank 16,
+// 4096 -> 4096: 12.0 and 24.2 with mma.sync, 10.3 and 16.6 with tcgen05.
+constexpr int64_t kTmaRows = 128;
 
 constexpr int64_t kMaxWidth = int64_t(1) << 22;  // grid limits
 
@@ -999,9 +1016,13 @@ fp8la_status run_shrink(const Segments &seg, const void *X, int32_t dtype,
   a.alpha = alpha;
   a.V = V;
   a.ldv = ldv;
-  // Long segments of BF16 rows that TMA can read go to tcgen05.
+  // BF16 rows that TMA can read go to tcgen05, but for short segments of few
+  // ranks, whose 128-row tiles are mostly empty.  Measured, us for a forward
+  // pass with mma.sync / tcgen05 here, 4096 -> 4096: 256 segments of one row, rank
+  // 16: 61.9 / 67.5, rank 32: 83.3 / 77.8, rank 64: 111.6 / 97.5; 64 of 16, rank
+  // 16: 22.1 / 22.8, rank 32: 33.6 / 26.1, rank 64: 44.5 / 32.8.
   if (dtype == FP8LA_TYPE_BF16 && a.x_unit == 16 && a.p_unit == 16 &&
-      !short_segments(seg.T, seg.S) && seg.T >= kTmaRows)
+      seg.T >= kTmaRows && (R > 16 || !short_segments(seg.T, seg.S)))
     return launch_shrink_tma(a, s);
   return dtype == FP8LA_TYPE_BF16 ? launch_shrink<false>(a, s)
                                   : launch_shrink<true>(a, s);
@@ -1030,8 +1051,17 @@ fp8la_status run_expand(const Segments &seg, const float *V, int64_t ldv, int32_
   a.base_unit = unit_of(base, ld_base, 2);
   a.out_unit = unit_of(out, ld_out, 2);
   a.v_vec = unit_of(V, ldv, 4) == 16;
-  if (a.base_unit == 16 && a.out_unit == 16 && a.p_unit == 16 && R <= 64 &&
-      !short_segments(seg.T, seg.S) && seg.T * N >= kTmaExpand)
+  // tcgen05 takes 128 rows x 256 columns at a time, wants many such tiles to
+  // hide its start, and saves what mma.sync pays for each rank.  Measured, us for
+  // a forward pass (K = 1024) with mma.sync / tcgen05 here: rank 16, 4096 x 4096:
+  // 23.3 / 24.4, x 10240: 41.6 / 42.8; rank 32, 2048 x 4096: 19.1 / 19.0, x 8192:
+  // 27.4 / 25.4, 1024 x 8192: 18.0 / 20.9, 4096 x 4096 in 64 segments: 30.9 /
+  // 32.9; rank 64, 2048 x 4096: 25.7 / 22.4, 4096 x 4096: 36.5 / 30.1, 1024 x
+  // 8192: 23.9 / 24.4, 4096 x 4096 in 64 segments: 43.1 / 38.2, 2048 x 4096 in 64
+  // (K = 4096): 38.0 / 41.3.
+  if (a.base_unit == 16 && a.out_unit == 16 && a.p_unit == 16 && R > 16 &&
+      R <= 64 && seg.T >= 64 * static_cast<int64_t>(seg.S) && seg.T >= 2048 &&
+      seg.T * N >= int64_t(2048) * 4096)
     return launch_expand_tma(a, s);
   return launch_expand(a, s);
 }
@@ -1137,8 +1167,12 @@ extern "C" fp8la_status fp8la_lora_backward(
                dy_dtype == FP8LA_TYPE_F32, 1};
   o.alpha = alpha;
   o.R = rank;
-  if (!o.side[0].x_f32 && !o.side[1].x_f32 && o.side[0].x_unit == 16 &&
-      o.side[1].x_unit == 16 && !short_segments(rows, num_segments) && rows >= kTmaRows) {
+  // BF16 rows that TMA can read.  Measured, us for a backward pass with
+  // mma.sync / tcgen05 here, 4096 x 4096, rank 16: 256 segments of one row 136 /
+  // 108, 1024 of one 471 / 383, 64 of 16 52.7 / 37.0; rank 64: 256 of one 233 /
+  // 210, 64 of 16 100 / 84.
+  if (rows >= kTmaRows && !o.side[0].x_f32 && !o.side[1].x_f32 &&
+      o.side[0].x_unit == 16 && o.side[1].x_unit == 16) {
     st = launch_outer_tma(o, s);
     return st == FP8LA_OK ? launch_status() : st;
   }

@@ -377,3 +377,65 @@ def test_refusals():
     assert e.value.status == fl.FP8LA_ERR_INVALID_ARG
     with pytest.raises(AssertionError):
         fl.lora_apply(*fa[:2], c["A"].float(), *fa[3:])
+
+
+# ----------------------------------------- where one kernel hands over to another
+@pytest.mark.parametrize("R", [4, 16, 17, 32, 64, 128])
+@pytest.mark.parametrize("T,lengths,n", [
+    (1, [1], 1),                                # a single row
+    (7, [7], 1),
+    (8, [1] * 8, 8),                            # one row each
+    (31, [3, 0, 17, 11], 2),
+    (64, [2] * 32, 3),
+    (255, [1] * 200 + [55], 4),
+    (256, [1] * 256, 5),                        # many short segments
+    (300, [15] * 20, 3),
+])
+def test_short_segments_aligned(T, lengths, n, R):
+    """Rows that TMA can read, from a single one up: every kernel's smallest
+    tiles, with neighbours' rows beside each segment's."""
+    ids = [i % (n + 1) - (i % (n + 1) == n) * (n + 1) for i in range(len(lengths))]
+    c = make(T, lengths, ids, n, R, 264, 328, xt="bfloat16")
+    check_forward(lib(), c)
+    check_backward(lib(), c, random_v(c))
+
+
+@pytest.mark.parametrize("R", [16, 17, 32, 64, 65])
+@pytest.mark.parametrize("T,lengths", [
+    (2047, [1000, 1047]),
+    (2048, [2048]),
+    (2305, [700, 1, 900, 127, 300, 201]),       # rows after the last, tiles cut short
+    (2500, [39] * 64),                          # too short for the widest tiles
+])
+def test_many_rows_and_columns(T, lengths, R):
+    """Both sides of the sizes from which the widest tiles are used."""
+    ids = [i % 3 - (i % 3 == 2) * 3 for i in range(len(lengths))]
+    c = make(T, lengths, ids, 2, R, 72, 4104, xt="bfloat16")
+    check_forward(lib(), c)
+
+
+@pytest.mark.parametrize("ld", [1 << 13, 1 << 45])
+def test_single_row_of_any_stride(ld):
+    """The stride of a single row or adapter is never used."""
+    import torch
+    fl = lib()
+    T, n, R, K, N = 1, 1, 1, 256, 512
+    c = make(T, [1], [0], n, R, K, N, xt="bfloat16")
+    v = random_v(c)
+    (want, wv), wb = check_forward(fl, c), check_backward(fl, c, v)
+    P = {k: t.data_ptr() for k, t in c.items()}
+    out, dx = torch.empty_like(c["base"]), torch.empty_like(c["dx_base"])
+    gv, dA, dB = torch.empty_like(wv), torch.empty_like(wb[1]), torch.empty_like(wb[2])
+    ws = torch.empty(fl.fp8la_lora_workspace_bytes(T, R), dtype=torch.uint8, device="cuda")
+    s = torch.cuda.current_stream().cuda_stream
+    fl.fp8la_lora_apply(P["base"], ld, P["x"], 1, ld, T, P["A"], ld, ld, P["B"], ld, ld,
+                        P["alpha"], n, R, K, N, 1, P["m_offsets"], P["adapter_ids"],
+                        out.data_ptr(), ld, gv.data_ptr(), ld, s)
+    fl.fp8la_lora_backward(P["dy"], 1, ld, P["x"], 1, ld, v.data_ptr(), ld, T, P["A"], ld, ld,
+                           P["B"], ld, ld, P["alpha"], n, R, K, N, 1, P["m_offsets"],
+                           P["adapter_ids"], P["dx_base"], ld, dx.data_ptr(), ld, dA.data_ptr(),
+                           dB.data_ptr(), ws.data_ptr(), ws.numel(), s)
+    torch.cuda.synchronize()
+    assert fl.device_status() == 0
+    for g, w in zip((out, gv, dx, dA, dB), (want, wv, *wb)):
+        assert torch.equal(g, w)
