@@ -329,8 +329,9 @@ FP8LA_API fp8la_status fp8_grouped_gemm(int32_t num_groups, const int32_t *m_off
  * int32 and weights: fp32 [tokens][top_k]; m_offsets: int32 [E + 1]; order:
  * int32 [tokens * top_k].  1 <= top_k <= min(E, 16), E <= 1024 (beyond:
  * FP8LA_ERR_UNSUPPORTED).  workspace: fp8_moe_route_workspace_bytes(tokens,
- * E) bytes, 4-byte aligned, needed only for the sort; it keeps nothing
- * between calls.  One launch, or two for a sort of more than 128 tokens.
+ * E) bytes, 4-byte aligned, needed only for the sort, which takes up to 2^23
+ * pairs (beyond: FP8LA_ERR_UNSUPPORTED may follow); it keeps nothing between
+ * calls.  One launch, or two for a sort of more than 128 tokens.
  */
 FP8LA_API int64_t fp8_moe_route_workspace_bytes(int64_t tokens, int32_t num_experts);
 FP8LA_API fp8la_status fp8_moe_route(const void *logits, int32_t dtype, int64_t tokens,
@@ -403,11 +404,14 @@ FP8LA_API fp8la_status fp8_moe_layer(
  * stride_b elements apart; alpha: fp32 [num_adapters]; m_offsets: int32
  * [num_segments + 1], starting at 0, non-decreasing, at most rows;
  * adapter_ids: int32 [num_segments], -1 .. num_adapters-1.  v: fp32
- * [rows][ldv], ldv >= rank (the backward pass wants it).  All device; the host reads none of it.  Offsets or ids that break these rules
- * make the call write no output and record FP8LA_ERR_DEVICE_ARG.
+ * [rows][ldv], ldv >= rank (the backward pass wants it).  All device; the
+ * host reads none of it.  Offsets or ids that break these rules make the call
+ * write no output and record FP8LA_ERR_DEVICE_ARG.
  * fp32 operands enter the tensor cores as sums of bf16 terms: three (24
- * significant bits) for v, two (16) for out; sums are fp32, in a fixed order.  Pointers need their
- * type's alignment; 16-byte rows are read and written fastest.
+ * significant bits) for v, two (16) for out; sums are fp32, in a fixed order.
+ * Pointers need their type's alignment; 16-byte rows are read and written
+ * fastest.  Below 128 rows the result does not depend on the alignment; from
+ * there on rows at other addresses are added in another order.
  * Limits (FP8LA_ERR_UNSUPPORTED): rank <= 128, num_segments <= 1024, rows
  * <= 2^19, K and N <= 2^22, num_adapters <= 65535.  Two launches.
  */
