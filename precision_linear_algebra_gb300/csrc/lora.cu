@@ -33,10 +33,9 @@
 // once.
 //
 // Measured on the stream: forward 9.7 us for 8 rows of their own, rank 16, 4096
-// -> 4096 (the call's host side takes longer), 25 us for 333 ragged rows of FP32,
-// rank 24, 1000 -> 1001.  FP32 rows at size cost three BF16 terms here: 4096 rows,
-// rank 64, 8192 -> 8192, 131 us forward (276 MB, 2.1 TB/s) and, at rank 32, 250 us
-// backward (1.6 TB/s).  BF16 rows at odd addresses are copied element by element:
+// -> 4096 (the call's host side takes longer).  The outer sums of FP32 rows
+// cost six MMAs a step here: 4096 rows, rank 32, 8192 -> 8192, 219 us backward
+// (413 MB, 1.9 TB/s).  BF16 rows at odd addresses are copied element by element:
 // 3000 rows, rank 48, 6099 -> 4103, 178 us forward, 80 at even ones.
 #include <cuda_bf16.h>
 
@@ -1024,6 +1023,14 @@ fp8la_status run_shrink(const Segments &seg, const void *X, int32_t dtype,
   if (dtype == FP8LA_TYPE_BF16 && a.x_unit == 16 && a.p_unit == 16 &&
       seg.T >= kTmaRows && (R > 16 || !short_segments(seg.T, seg.S)))
     return launch_shrink_tma(a, s);
+  // FP32 rows: splitting a tile costs the same however few of its rows count.
+  // mma.sync / tcgen05, 4096 -> 4096: 4 segments, 1024 rows, rank 16: 22.2 / 19.2,
+  // rank 64: 39.2 / 25.1, 4096 rows, rank 16: 49.2 / 39.1, rank 64: 82.1 / 46.5;
+  // 128 rows, rank 16: 16.4 / 16.5, rank 64: 29.7 / 21.5; rank 64, 64 segments of
+  // 16: 55.4 / 52.9, 256 of one: 125 / 175.
+  if (dtype == FP8LA_TYPE_F32 && a.x_unit == 16 && a.p_unit == 16 &&
+      seg.T >= kTmaRows && !short_segments(seg.T, seg.S))
+    return launch_shrink_f32(a, s);
   return dtype == FP8LA_TYPE_BF16 ? launch_shrink<false>(a, s)
                                   : launch_shrink<true>(a, s);
 }

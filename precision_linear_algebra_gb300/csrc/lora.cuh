@@ -294,6 +294,7 @@ inline int choose_cluster(int64_t items, int64_t stages, int64_t slots, int fixe
 // The same sums for BF16 operands that TMA can read, on tcgen05 (lora_tma.cu).
 // V of tiles of 128 rows; base + V P at ranks up to 64; both sides' gradients.
 fp8la_status launch_shrink_tma(const ShrinkArgs &a, cudaStream_t s);
+fp8la_status launch_shrink_f32(const ShrinkArgs &a, cudaStream_t s);
 fp8la_status launch_expand_tma(const ExpandArgs &a, cudaStream_t s);
 fp8la_status launch_outer_tma(const OuterArgs &a, cudaStream_t s);
 

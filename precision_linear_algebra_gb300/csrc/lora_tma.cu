@@ -1,4 +1,5 @@
-// The adapters' long sums for BF16 operands on the 5th-generation tensor cores:
+// The adapters' long sums on the 5th-generation tensor cores, BF16 operands and,
+// in shrink, FP32 ones too:
 // V of rows (shrink) and the factors' gradients (outer); see lora.cu for the
 // formulas.
 //
@@ -99,6 +100,24 @@ constexpr int kSK = 128;            // K of a stage: two boxes of 64
 // ones, which the epilogue adds with rounding: with one accumulator, 2048
 // products in it left a relative error of 2e-6 in V, more than FP32 has.
 constexpr int kAcc = 4;
+
+// Tile row sums of a shrink CTA, `red` in every CTA of the cluster, to V.
+template <int THREADS>
+__device__ __forceinline__ void store_v(const ShrinkArgs &a, const Found &f,
+                                        const float *red, uint32_t red_addr, int ld) {
+  const uint32_t crank = cluster_ctarank(), csize = cluster_size();
+  const float alpha = a.alpha ? a.alpha[f.id] : 1.0f;
+  const int cells = f.rows * a.R;
+  if (csize > 1) cluster_sync_all();
+  for (int i = static_cast<int>(crank) * THREADS + threadIdx.x; i < cells;
+       i += static_cast<int>(csize) * THREADS) {
+    const int r = i / a.R, j = i - r * a.R;
+    const float v = csize > 1 ? cluster_sum(red_addr + 4u * (r * ld + j), csize)
+                              : red[r * ld + j];
+    a.V[(f.row0 + static_cast<int64_t>(r)) * a.ldv + j] = v * alpha;
+  }
+  if (csize > 1) cluster_sync_all();  // no CTA leaves while its sums are read
+}
 
 // RP ranks, a multiple of 16.
 template <int RP>
@@ -245,17 +264,227 @@ __global__ void __launch_bounds__(kSThreads)
     tmem_dealloc(tmem_base, C::kTmemCols);
   }
   __syncwarp();
-  const float alpha = a.alpha ? a.alpha[f.id] : 1.0f;
-  const int cells = f.rows * a.R;
-  if (csize > 1) cluster_sync_all();
-  for (int i = static_cast<int>(crank) * kSThreads + threadIdx.x; i < cells;
-       i += static_cast<int>(csize) * kSThreads) {
-    const int r = i / a.R, j = i - r * a.R;
-    const float v = csize > 1 ? cluster_sum(base + 4u * (r * C::kLdR + j), csize)
-                              : red[r * C::kLdR + j];
-    a.V[(f.row0 + static_cast<int64_t>(r)) * a.ldv + j] = v * alpha;
+  store_v<kSThreads>(a, f, red, base, C::kLdR);
+}
+
+// ------------------------------------------------------------- FP32 shrink
+// X in FP32: converter warps split each stage into three BF16 terms, as TMA
+// would have written them (K-major, swizzled), and the MMA adds all three.
+//
+// Bound: X once from HBM; 300 instructions of a converter thread for a stage of
+// 32 KB and twelve MMAs stay below the stage's share of memory time.  With a
+// forward pass of 4096 rows, rank 64, 8192 -> 8192 it takes 73 us on the stream
+// (276 MB, 3.8 TB/s), with the mma.sync form 131.
+constexpr int kFConv = 8;           // converter warps, 0-3 also epilogue
+constexpr int kFThreads = 32 * (kFConv + 2);
+constexpr int kFK = 64;             // K of a stage: two boxes of 32 floats
+
+template <int RP>
+struct ShrinkF32 {
+  static constexpr int kBox = kSRows * 128;
+  static constexpr int kX = 2 * kBox;
+  static constexpr int kP = RP * 128;
+  static constexpr int kStage = kX + kP;
+  static constexpr int kTerm = kSRows * 128;
+  static constexpr int STAGES = RP <= 64 ? 3 : 2;
+  // Accumulators as in the outer kernel: NACC for the first term, in turn, and
+  // one for the other two; all of TMEM, at most.
+  static constexpr int NACC = RP <= 64 ? 7 : 3;
+  static constexpr int kTmemCols = (NACC + 1) * RP;
+  static constexpr int kLdR = RP + 1;
+  static constexpr int kT = STAGES * kStage;        // [2][3 terms]
+  static constexpr int kBar = kT + 6 * kTerm;
+  static constexpr int kMisc = kBar + (2 * STAGES + 5) * 8;
+  static constexpr int kAlloc = kMisc + 32 + 1024;
+  static_assert(kSRows * kLdR * 4 <= kT, "the sums overlay the ring");
+  static_assert(kP % 1024 == 0 && kAlloc <= 226 * 1024, "shared memory");
+  static_assert(kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "TMEM");
+};
+
+template <int RP>
+__global__ void __launch_bounds__(kFThreads, 1)
+    lora_shrink_f32_kernel(const __grid_constant__ CUtensorMap tmX,
+                           const __grid_constant__ CUtensorMap tmP,
+                           const ShrinkArgs a, const uint64_t timeout_ns) {
+  using C = ShrinkF32<RP>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int warp_sums[kFThreads / 32];
+  __shared__ Found slot;
+  const uint32_t raw_addr = smem_addr(smem_raw);
+  const uint32_t base = (raw_addr + 1023u) & ~1023u;
+  uint8_t *sbase = smem_raw + (base - raw_addr);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_launch_dependents();
+  const Found f = find_tile<kFThreads>(a.seg, blockIdx.y, kSRows, warp_sums, &slot);
+  if (f.rows == 0) return;
+  const uint32_t crank = cluster_ctarank(), csize = cluster_size();
+  if (f.id < 0) {  // rows without an adapter
+    if (crank == 0)
+      for (int i = threadIdx.x; i < f.rows * a.R; i += kFThreads)
+        a.V[(f.row0 + static_cast<int64_t>(i / a.R)) * a.ldv + i % a.R] = 0.0f;
+    return;
   }
-  if (csize > 1) cluster_sync_all();  // no CTA leaves while its sums are read
+  const uint32_t bar0 = base + C::kBar;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (C::STAGES + s); };
+  auto tready_bar = [&](int b) { return bar0 + 8u * (2 * C::STAGES + b); };
+  auto tfree_bar = [&](int b) { return bar0 + 8u * (2 * C::STAGES + 2 + b); };
+  const uint32_t done_bar = bar0 + 8u * (2 * C::STAGES + 4);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sbase + C::kMisc);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(sbase + C::kMisc + 4);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tready_bar(b), kFConv);
+      mbar_init(tfree_bar(b), 1);
+    }
+    mbar_init(done_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kFConv + 1) {
+    tmem_alloc(smem_addr(tmem_slot), C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int nst = static_cast<int>((a.K + kFK - 1) / kFK);
+  const int s0 = static_cast<int>(static_cast<int64_t>(nst) * crank / csize);
+  const int s1 = static_cast<int>(static_cast<int64_t>(nst) * (crank + 1) / csize);
+  float *red = reinterpret_cast<float *>(sbase);
+
+  if (warp == kFConv) {
+    if (lane == 0) {
+      uint32_t s = 0, ph = 0, issued = 0;
+      for (int c = s0; c < s1; ++c) {
+        if (!mbar_wait(empty_bar(s), ph ^ 1u, timeout_ns, a.seg.status, abort_flag))
+          break;
+        const uint32_t d = base + s * C::kStage;
+        mbar_arrive_expect_tx(full_bar(s), C::kStage);
+        tma_load_2d(d, &tmX, full_bar(s), c * kFK, f.row0);
+        tma_load_2d(d + C::kBox, &tmX, full_bar(s), c * kFK + 32, f.row0);
+        tma_load_3d(d + C::kX, &tmP, full_bar(s), c * kFK, 0, f.id);
+        ++issued;
+        if (++s == C::STAGES) { s = 0; ph ^= 1u; }
+      }
+      for (uint32_t st = 0; st < C::STAGES; ++st) {
+        if (issued <= st) break;
+        const uint32_t arms = (issued - 1 - st) / C::STAGES + 1;
+        mbar_wait_drain(full_bar(st), (arms - 1) & 1u, timeout_ns, a.seg.status);
+      }
+    }
+  } else if (warp == kFConv + 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(kSRows, RP, false);
+      uint32_t s = 0, ph = 0;
+      for (int c = s0; c < s1; ++c) {
+        const uint32_t b = (c - s0) & 1u, use = (c - s0) >> 1;
+        if (!mbar_wait(full_bar(s), ph, timeout_ns, a.seg.status, abort_flag) ||
+            !mbar_wait(tready_bar(b), use & 1u, timeout_ns, a.seg.status, abort_flag))
+          break;
+        tc_fence_after();
+        const uint64_t bd = smem_desc_k128_sw128(base + s * C::kStage + C::kX);
+        const uint32_t terms = base + C::kT + 3 * b * C::kTerm;
+#pragma unroll
+        for (int t = 0; t < 3; ++t) {
+          const uint64_t ad = smem_desc_k128_sw128(terms + t * C::kTerm);
+          const uint32_t d =
+              tmem_base + (t == 0 ? (c - s0) % C::NACC : C::NACC) * RP;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_bf16(d, ad + 2u * k, bd + 2u * k, idesc,
+                      (k > 0 || t > 1 || c - s0 >= (t == 0 ? C::NACC : 1)) ? 1u : 0u);
+        }
+        umma_commit(empty_bar(s));
+        umma_commit(tfree_bar(b));
+        if (++s == C::STAGES) { s = 0; ph ^= 1u; }
+      }
+      umma_commit(done_bar);
+      mbar_wait_drain(done_bar, 0, timeout_ns, a.seg.status);
+    }
+  } else {
+    // A unit is 8 values of a row: 32 bytes in, 16 bytes of each term out.  A
+    // warp takes the same unit of 32 rows, which the swizzle spreads over the
+    // banks.
+    uint32_t s = 0, ph = 0;
+    bool ok = true;
+    for (int c = s0; c < s1; ++c) {
+      const uint32_t b = (c - s0) & 1u, use = (c - s0) >> 1;
+      const bool ready =
+          mbar_wait(tfree_bar(b), (use & 1u) ^ 1u, timeout_ns, a.seg.status,
+                    abort_flag) &&
+          mbar_wait(full_bar(s), ph, timeout_ns, a.seg.status, abort_flag);
+      if (!__all_sync(0xffffffffu, ready)) {
+        ok = false;
+        break;
+      }
+      const uint32_t row = threadIdx.x % kSRows, first = threadIdx.x / kSRows;
+      const uint8_t *x = sbase + s * C::kStage + row * 128;
+      const uint32_t out = base + C::kT + 3 * b * C::kTerm + row * 128;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t unit = first + 2 * u;   // of 8 in a row
+        const uint8_t *p = x + (unit >> 2) * C::kBox;
+        const uint32_t q = 2 * (unit & 3u);
+        const float4 lo = *reinterpret_cast<const float4 *>(p + ((q ^ (row & 7u)) << 4));
+        const float4 hi =
+            *reinterpret_cast<const float4 *>(p + (((q + 1) ^ (row & 7u)) << 4));
+        uint32_t w[4][3];
+        split_pair<3>(lo.x, lo.y, w[0]);
+        split_pair<3>(lo.z, lo.w, w[1]);
+        split_pair<3>(hi.x, hi.y, w[2]);
+        split_pair<3>(hi.z, hi.w, w[3]);
+#pragma unroll
+        for (int t = 0; t < 3; ++t)
+          st_shared_v4(out + t * C::kTerm + ((unit ^ (row & 7u)) << 4), w[0][t], w[1][t],
+                       w[2][t], w[3][t]);
+      }
+      if (++s == C::STAGES) { s = 0; ph ^= 1u; }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tready_bar(b));
+    }
+    if (warp < 4) {
+      // The ring is free once the last MMA is done: the sums go there.
+      const bool ready =
+          ok && mbar_wait(done_bar, 0, timeout_ns, a.seg.status, abort_flag);
+      if (__all_sync(0xffffffffu, ready)) {
+        tc_fence_after();
+        const int row = 32 * warp + lane, used = min(C::NACC, s1 - s0);
+        const uint32_t col0 = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
+#pragma unroll
+        for (int j = 0; j < RP; j += 16) {
+          float sum[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) sum[i] = 0.0f;
+          // The small terms first.
+          for (int n = used; used > 0 && n >= 0; --n) {
+            float v[16];
+            tmem_ld16(col0 + (n == used ? C::NACC : n) * RP + j, v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sum[i] += v[i];
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) red[row * C::kLdR + j + i] = sum[i];
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kFConv + 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem_base, C::kTmemCols);
+  }
+  __syncwarp();
+  store_v<kFThreads>(a, f, red, base, C::kLdR);
 }
 
 // ------------------------------------------------------------------- expand
@@ -958,6 +1187,22 @@ bool encode_bf16(CUtensorMap *m, const void *p, int64_t width, int64_t rows,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// FP32 matrix [rows][width] as swizzled boxes of 32 columns.
+bool encode_f32(CUtensorMap *m, const void *p, int64_t width, int64_t rows, int64_t ld,
+                uint32_t box_rows) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width),
+                              static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 4};
+  const cuuint32_t box[2] = {32, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void *>(p), dims, strides,
+             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int RP>
 fp8la_status shrink_one(const ShrinkArgs &a, int slot, cudaStream_t s) {
   using C = ShrinkTma<RP>;
@@ -976,6 +1221,26 @@ fp8la_status shrink_one(const ShrinkArgs &a, int slot, cudaStream_t s) {
   const int cluster = choose_cluster(tiles, (a.K + kSK - 1) / kSK, 152, 6);
   return launch(kern, dim3(cluster, static_cast<unsigned>(tile_bound(T, S, kSRows)), 1),
                 kSThreads, C::kAlloc, cluster, s, tmX, tmP, a, wait_timeout_ns());
+}
+
+template <int RP>
+fp8la_status shrink_f32_one(const ShrinkArgs &a, int slot, cudaStream_t s) {
+  using C = ShrinkF32<RP>;
+  auto kern = lora_shrink_f32_kernel<RP>;
+  if (once_per_device(slot, [&] {
+        return cudaFuncSetAttribute(
+            kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kAlloc);
+      }) != cudaSuccess)
+    return FP8LA_ERR_CUDA;
+  CUtensorMap tmX, tmP;
+  if (!encode_f32(&tmX, a.X, a.K, a.seg.T, a.ldx, kSRows) ||
+      !encode_bf16(&tmP, a.P, a.K, a.R, a.seg.n, a.ldp, a.stride_p, RP, 3))
+    return FP8LA_ERR_CUDA;
+  const int64_t T = a.seg.T, S = a.seg.S;
+  const int64_t tiles = T / kSRows + ((S < T ? S : T) + 1) / 2;
+  const int cluster = choose_cluster(tiles, (a.K + kFK - 1) / kFK, 152, 6);
+  return launch(kern, dim3(cluster, static_cast<unsigned>(tile_bound(T, S, kSRows)), 1),
+                kFThreads, C::kAlloc, cluster, s, tmX, tmP, a, wait_timeout_ns());
 }
 
 template <int RP>
@@ -1030,6 +1295,13 @@ fp8la_status launch_shrink_tma(const ShrinkArgs &a, cudaStream_t s) {
          : a.R <= 32 ? shrink_one<32>(a, 55, s)
          : a.R <= 64 ? shrink_one<64>(a, 56, s)
                      : shrink_one<128>(a, 57, s);
+}
+
+fp8la_status launch_shrink_f32(const ShrinkArgs &a, cudaStream_t s) {
+  return a.R <= 16   ? shrink_f32_one<16>(a, 65, s)
+         : a.R <= 32 ? shrink_f32_one<32>(a, 66, s)
+         : a.R <= 64 ? shrink_f32_one<64>(a, 67, s)
+                     : shrink_f32_one<128>(a, 68, s);
 }
 
 fp8la_status launch_expand_tma(const ExpandArgs &a, cudaStream_t s) {

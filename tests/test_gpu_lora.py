@@ -12,6 +12,8 @@ magnitudes.  So, with |.| the sum of the magnitudes of the products:
 and in the norm, where independent errors do not add up like magnitudes: the
 same relative terms against the norm of the result (for out: the rounding)."""
 
+import math
+
 import pytest
 
 from _helpers import lib
@@ -439,3 +441,38 @@ def test_single_row_of_any_stride(ld):
     assert fl.device_status() == 0
     for g, w in zip((out, gv, dx, dA, dB), (want, wv, *wb)):
         assert torch.equal(g, w)
+
+
+@pytest.mark.parametrize("R", [8, 17, 48, 128])
+@pytest.mark.parametrize("T,lengths,K", [
+    (128, [128], 64),
+    (130, [1] * 130, 100),                      # one row each, K short of a stage
+    (300, [15] * 20, 264),
+    (1000, [400, 129, 0, 471], 1996),
+])
+def test_fp32_rows_aligned(T, lengths, K, R):
+    """FP32 rows that TMA can read, K ending inside a stage."""
+    ids = [i % 3 - (i % 3 == 2) * 3 for i in range(len(lengths))]
+    c = make(T, lengths, ids, 2, R, K, 328, xt="float32")
+    check_forward(lib(), c)
+    check_backward(lib(), c, random_v(c))
+
+
+@pytest.mark.parametrize("xt", ["bfloat16", "float32"])
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+def test_non_finite_rows_stay_their_own(xt, value):
+    """A non-finite input makes its own row of V and out non-finite, no other."""
+    import torch
+    fl = lib()
+    c = make(300, [170, 130], [1, 0], 2, 24, 264, 328, xt=xt)
+    names = ("base", "x", "A", "B", "alpha", "m_offsets", "adapter_ids")
+    out0, v0 = fl.lora_apply(*[c[k] for k in names])
+    c["x"][131, 77] = value
+    c["x"][299, 263] = value
+    out, v = fl.lora_apply(*[c[k] for k in names])
+    torch.cuda.synchronize()
+    assert fl.device_status() == 0
+    keep = torch.ones(300, dtype=torch.bool, device="cuda")
+    keep[[131, 299]] = False
+    assert torch.equal(v[keep], v0[keep]) and torch.equal(out[keep], out0[keep])
+    assert not torch.isfinite(v[~keep]).any() and not torch.isfinite(out[~keep]).any()
