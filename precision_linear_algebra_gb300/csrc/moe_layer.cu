@@ -11,17 +11,22 @@
 //
 // Weights are the M side of the MMA, tokens the N side, which may be as narrow
 // as 16 columns.  kind::f8f6f4 wants FP8 on both sides, so an activation
-// enters as the sum of two E4M3 values,
-//   v * 2^(7-e) = hi + lo / 32,   2^e <= the largest |v| < 2^(e+1),
-// two columns of the MMA whose results the epilogue adds.  hi and lo keep 8
-// significant bits: exact for BF16 activations down to 2^-15 of the largest
-// (below that the error is under 2^-22 of the largest), and for FP32 ones no
-// worse than a rounding to BF16.  A power of two as scale rounds nothing.  x
-// has one scale for each token, h one for each token and 128 elements.
+// enters as a sum of E4M3 values under a power of two, which rounds nothing:
+//   BF16 x     v * 2^(7-e) = t0 + t1 / 32
+//   FP32 x, h  v * 2^(7-e) = t0 + t1 + (t2 + t3) / 1024
+// with 2^e <= the largest |v| < 2^(e+1) of the token (x), or of the token's 128
+// neighbours (h).  Each term keeps what the ones before left to 2^-5, the first
+// v to 2^-4.  So two terms hold BF16's 8 bits (exact down to 2^-15 of the
+// largest, off by at most 2^-22 of the largest below), and four hold 2^-19 of
+// v, or 2^-27 of the largest where that is more: with two, h alone would put
+// one output in five beside its BF16 neighbour.  Terms of the same scale are
+// added into the same columns of the MMA, so four terms take no more of TMEM
+// than two; the epilogue adds the two scales' sums.
 //
 // Four launches, each with its set-up under the one before:
 //   prepare  sorts the pairs by expert into tiles of up to TT and splits the
-//            tokens' x into codes, one row for each pair, in that order
+//            tokens' x into codes, a row of each term for each pair, in that
+//            order
 //   gate/up  one item = a tile x (128 gate + the same 128 up rows).  Its
 //            epilogue has all 128 h of a down K block at hand, so it writes h
 //            as codes with their scale.
@@ -75,11 +80,18 @@ constexpr int kSlack = 64;          // positions past the last pair that are rea
 // Starts: three 16-bit words for each expert, and warp sums.
 constexpr int kStartsBytes = kMaxExperts * 6 + 256;
 
+// Terms of an activation, and the factor of those with the smaller scale.
+constexpr int kBf16Terms = 2, kTerms = 4;
+template <int TERMS>
+constexpr float kSmall = TERMS == 2 ? 1.0f / 32 : 1.0f / 1024;
+
 // TT: most tokens of a tile.
-template <int TT>
+template <int TT, int TERMS>
 struct Cfg {
-  static constexpr int STAGES = TT == 16 ? 6 : 4;
-  static constexpr int kBBytes = 2 * TT * BK;      // hi and lo rows
+  // As many as fit: 32 KB of weights each, beside the codes.
+  static constexpr int STAGES = TERMS == 2 ? (TT == 16 ? 6 : 4) : (TT == 16 ? 5 : 3);
+  static constexpr int kPairBytes = 2 * TT * BK;   // rows of a term of each scale
+  static constexpr int kBBytes = TERMS / 2 * kPairBytes;
   static constexpr int kScaleBytes = 4 * TT;       // h's scales (down kernel)
   static constexpr int kTmemCols = 8 * TT;         // 2 buffers x 2 blocks x 2 TT
   static constexpr int kA = 0;
@@ -92,7 +104,7 @@ struct Cfg {
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kEnd = kMisc + 32;
   static constexpr int kAlloc = kEnd + 1024;
-  static_assert(kB % 1024 == 0 && kBBytes % 1024 == 0, "swizzle atoms");
+  static_assert(kB % 1024 == 0 && kPairBytes % 1024 == 0, "swizzle atoms");
   static_assert(kMaxExperts * 4 <= STAGES * kBBytes, "the starts' counters");
   static_assert(kScale % 16 == 0 && kBar % 8 == 0, "alignment");
   static_assert(kAlloc <= 227 * 1024, "shared memory");
@@ -111,9 +123,9 @@ struct Plan {
   int32_t *pos;          // [pairs], -1: no expert
   int32_t *tile_of;      // [pairs]
   unsigned *arrived;     // [tiles][row blocks]: parts of a shared h item
-  uint8_t *xc;           // [2][positions][Dc] codes of x
+  uint8_t *xc;           // [terms][positions][Dc] codes of x, see split_codes
   float *xs;             // [positions]
-  uint8_t *hc;           // [2][positions][Fc] codes of h
+  uint8_t *hc;           // [terms][positions][Fc] codes of h
   float *hs;             // [128-blocks of F][positions]
   float *parts;          // [CTAs][2][TT][256] parts of shared items
   float *out;            // [positions][Dc] sums of whole down items
@@ -123,7 +135,7 @@ struct LayerArgs {
   Plan p;
   const void *x;
   int64_t ldx;
-  int32_t x_bf16, x_vec;
+  int32_t x_vec;
   int32_t T, E, k, D, F;
   int32_t P;             // positions, as allocated
   int64_t Dc, Fc;        // D and F rounded up to 16
@@ -177,15 +189,29 @@ __device__ __forceinline__ void group_scale(uint32_t top, float &inv, float &sca
   scale = eb == 255u ? 1.0f : __uint_as_float((eb - 7u) << 23);
 }
 
-// (a, b) scaled -> their hi codes and their lo codes (two in 16 bits each).
-__device__ __forceinline__ void split_codes(float a, float b, uint32_t &hi,
-                                            uint32_t &lo) {
-  hi = cvt_e4m3x2(a, b);
-  const float2 back = decode_e4m3x2(hi);
-  lo = cvt_e4m3x2((a - back.x) * 32.0f, (b - back.y) * 32.0f);
+// (a, b) scaled -> the codes of their terms (two in 16 bits each), in the order
+// of the planes in memory: t0, t1, or t0, t2, t1, t3, so that each two planes
+// hold a term of either scale.
+template <int TERMS>
+__device__ __forceinline__ void split_codes(float a, float b, uint32_t (&c)[TERMS]) {
+  auto take = [&](uint32_t &code) {
+    code = cvt_e4m3x2(a, b);
+    const float2 back = decode_e4m3x2(code);
+    a -= back.x;
+    b -= back.y;
+  };
+  auto grow = [&]() {
+    a *= 1.0f / kSmall<TERMS>;
+    b *= 1.0f / kSmall<TERMS>;
+  };
+  take(c[0]);
+  if (TERMS > 2) take(c[TERMS - 2]);
+  grow();
+  take(c[1]);
+  if (TERMS > 2) take(c[TERMS - 1]);
 }
 
-// 16 TMEM columns: the hi and the lo sums of 8 tokens.
+// 16 TMEM columns: 8 tokens' sums of the terms of either scale.
 __device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&u)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, "
@@ -384,33 +410,35 @@ __global__ void __launch_bounds__(kPrepThreads)
   // a row's padded end becomes zeros.
   for (int d = 16 * threadIdx.x; d < a.D; d += kRound) {
     if (a.D > kRound) load_x16<F32>(a, t, d, xw);
-    uint32_t hi[4], lo[4];
+    constexpr int kT = F32 ? kTerms : kBf16Terms;
+    uint32_t w[kT][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      uint32_t h0, h1, l0, l1;
-      split_codes(x_value<F32>(xw, 4 * i) * inv, x_value<F32>(xw, 4 * i + 1) * inv,
-                  h0, l0);
-      split_codes(x_value<F32>(xw, 4 * i + 2) * inv,
-                  x_value<F32>(xw, 4 * i + 3) * inv, h1, l1);
-      hi[i] = h0 | h1 << 16;
-      lo[i] = l0 | l1 << 16;
+      uint32_t c0[kT], c1[kT];
+      split_codes<kT>(x_value<F32>(xw, 4 * i) * inv, x_value<F32>(xw, 4 * i + 1) * inv,
+                      c0);
+      split_codes<kT>(x_value<F32>(xw, 4 * i + 2) * inv,
+                      x_value<F32>(xw, 4 * i + 3) * inv, c1);
+#pragma unroll
+      for (int p = 0; p < kT; ++p) w[p][i] = c0[p] | c1[p] << 16;
     }
     for (int j = 0; j < a.k; ++j) {
       if (pos_of[j] < 0) continue;
-      uint8_t *row = a.p.xc + static_cast<int64_t>(pos_of[j]) * a.Dc + d;
-      *reinterpret_cast<uint4 *>(row) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      *reinterpret_cast<uint4 *>(row + static_cast<int64_t>(a.P) * a.Dc) =
-          make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+      for (int p = 0; p < kT; ++p)
+        *reinterpret_cast<uint4 *>(
+            a.p.xc + (static_cast<int64_t>(p) * a.P + pos_of[j]) * a.Dc + d) =
+            make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
     }
   }
 }
 
 // ------------------------------------------------------------ gate/up, down
-template <int TT, bool UP>
+template <int TT, int TERMS, bool UP>
 __global__ void __launch_bounds__(kThreads, 1)
     moe_gemm_kernel(const __grid_constant__ CUtensorMap tmW,
                     const __grid_constant__ CUtensorMap tmC, const LayerArgs a) {
-  using C = Cfg<TT>;
+  using C = Cfg<TT, TERMS>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_addr(smem_raw);
   const uint32_t base = (raw_addr + 1023u) & ~1023u;
@@ -519,18 +547,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       auto load_w = [&](const Item &w, int c, uint32_t s) {
         const uint32_t dst = base + C::kA + s * kABytes;
-        const uint32_t bytes = kABytes + 2 * w.npad * BK + (UP ? 0 : 4 * w.npad);
+        const uint32_t bytes = kABytes + TERMS * w.npad * BK + (UP ? 0 : 4 * w.npad);
         mbar_arrive_expect_tx(full_bar(s), bytes);
         const int r0 = w.r * kRows;
         tma_load_3d(dst, &tmW, full_bar(s), c * BK, r0, w.t.expert);
         tma_load_3d(dst + kABytes / 2, &tmW, full_bar(s), c * BK,
                     UP ? a.F + r0 : r0 + BM, w.t.expert);
       };
-      // Codes of the tile, 8 positions at a time: 8 hi rows, 8 lo rows.
+      // Codes of the tile, 8 positions and two planes at a time: 8 rows of the
+      // one, 8 of the other.
       auto load_codes = [&](const Item &w, int c, uint32_t s) {
-        for (int j = 0; j < w.npad; j += 8)
-          tma_load_3d(base + C::kB + s * C::kBBytes + 2 * j * BK, &tmC,
-                      full_bar(s), c * BK, w.t.first + j, 0);
+#pragma unroll
+        for (int p = 0; p < TERMS; p += 2)
+          for (int j = 0; j < w.npad; j += 8)
+            tma_load_3d(base + C::kB + s * C::kBBytes + p / 2 * C::kPairBytes + 2 * j * BK,
+                        &tmC, full_bar(s), c * BK, w.t.first + j, p);
         if (!UP)
           bulk_load(base + C::kScale + s * C::kScaleBytes,
                     a.p.hs + static_cast<int64_t>(c) * a.P + w.t.first,
@@ -594,9 +625,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int q = 0; q < BK / 32; ++q)
-              umma_f8f6f4(tmem_base + (b * 2 + m) * 2 * TT,
-                          adesc + m * (kABytes / 2 / 16) + 2u * q, bdesc + 2u * q,
-                          idesc, (q > 0 || (UP && c > w.c0)) ? 1u : 0u);
+#pragma unroll
+              for (int p = 0; p < TERMS / 2; ++p)
+                umma_f8f6f4(tmem_base + (b * 2 + m) * 2 * TT,
+                            adesc + m * (kABytes / 2 / 16) + 2u * q,
+                            bdesc + p * (C::kPairBytes / 16) + 2u * q, idesc,
+                            (p > 0 || q > 0 || (UP && c > w.c0)) ? 1u : 0u);
           umma_commit(empty_bar(s));
           if (++s == C::STAGES) { s = 0; ph ^= 1u; }
           if (!UP || c + 1 == w.c1) {
@@ -662,8 +696,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld16(lane_base + b * 4 * TT + 2 * TT + 2 * j0, vu);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              us[q][j] = fmaf(vu[8 + j], 0.03125f, vu[j]) * gs[q][j] * ws;
-              gs[q][j] = fmaf(vg[8 + j], 0.03125f, vg[j]) * gs[q][j] * ws;
+              us[q][j] = fmaf(vu[8 + j], kSmall<TERMS>, vu[j]) * gs[q][j] * ws;
+              gs[q][j] = fmaf(vg[8 + j], kSmall<TERMS>, vg[j]) * gs[q][j] * ws;
             }
           }
         }
@@ -746,17 +780,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 group_scale(top, inv, scale[e]);
                 v[e] = gs[q][j + e] * inv;
               }
-              uint32_t hi, lo;
-              split_codes(v[0], v[1], hi, lo);
+              uint32_t code[kTerms];
+              split_codes<kTerms>(v[0], v[1], code);
 #pragma unroll
               for (int e = 0; e < 2; ++e)
                 if (col + e < w.t.count) {
-                  const int64_t at = static_cast<int64_t>(w.t.first + col + e) * a.Fc + f;
-                  if (f < a.F) {
-                    a.p.hc[at] = static_cast<uint8_t>(hi >> (8 * e));
-                    a.p.hc[static_cast<int64_t>(a.P) * a.Fc + at] =
-                        static_cast<uint8_t>(lo >> (8 * e));
-                  }
+                  if (f < a.F)
+#pragma unroll
+                    for (int p = 0; p < kTerms; ++p)
+                      a.p.hc[(static_cast<int64_t>(p) * a.P + w.t.first + col + e) * a.Fc +
+                             f] = static_cast<uint8_t>(code[p] >> (8 * e));
                   if (row == 0)
                     a.p.hs[static_cast<int64_t>(w.r) * a.P + w.t.first + col + e] =
                         scale[e];
@@ -786,8 +819,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_ld16(lane_base + (b * 2 + half) * 2 * TT + 16 * q, v);
 #pragma unroll
               for (int j = 0; j < 8; ++j)
-                acc[8 * q + j] = fmaf(fmaf(v[8 + j], 0.03125f, v[j]), sc[8 * q + j],
-                                      acc[8 * q + j]);
+                acc[8 * q + j] = fmaf(fmaf(v[8 + j], kSmall<TERMS>, v[j]),
+                                      sc[8 * q + j], acc[8 * q + j]);
             }
           tc_fence_before();
           // The scales were read by generic loads; their next fill is TMA's.
@@ -934,9 +967,9 @@ Layout layout(int64_t T, int64_t k, int64_t E, int64_t D, int64_t F, int grid) {
   l.pos = take(pairs * 4);
   l.tile_of = take(pairs * 4);
   l.arrived = take(tiles * ((F + BM - 1) / BM) * 4);
-  l.xc = take(2 * l.P * Dc);
+  l.xc = take(kTerms * l.P * Dc);
   l.xs = take(l.P * 4);
-  l.hc = take(2 * l.P * Fc);
+  l.hc = take(kTerms * l.P * Fc);
   l.hs = take((F + BK - 1) / BK * l.P * 4);
   l.parts = take(static_cast<int64_t>(grid) * 2 * tile_tokens(T, k, E) * 256 * 4);
   l.out = take(l.P * Dc * 4);
@@ -966,29 +999,29 @@ bool launch_pdl(Kern kern, dim3 grid, int threads, int smem, cudaStream_t s,
   return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess;
 }
 
-template <int TT>
+template <int TT, int XTERMS>
 fp8la_status launch_layer(const CUtensorMap &tm13, const CUtensorMap &tmx,
                           const CUtensorMap &tm2, const CUtensorMap &tmh,
-                          const LayerArgs &a, cudaStream_t s) {
-  using C = Cfg<TT>;
-  auto up = moe_gemm_kernel<TT, true>;
-  auto down = moe_gemm_kernel<TT, false>;
-  if (once_per_device(TT == 16 ? 8 : 9, [&] {
+                          const LayerArgs &a, int slot, cudaStream_t s) {
+  using CU = Cfg<TT, XTERMS>;
+  using CD = Cfg<TT, kTerms>;
+  auto up = moe_gemm_kernel<TT, XTERMS, true>;
+  auto down = moe_gemm_kernel<TT, kTerms, false>;
+  if (once_per_device(slot, [&] {
         const cudaError_t e = cudaFuncSetAttribute(
-            up, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kAlloc);
+            up, cudaFuncAttributeMaxDynamicSharedMemorySize, CU::kAlloc);
         return e != cudaSuccess
                    ? e
                    : cudaFuncSetAttribute(
                          down, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         C::kAlloc);
+                         CD::kAlloc);
       }) != cudaSuccess)
     return FP8LA_ERR_CUDA;
   const dim3 combine(a.T, (a.D + 2 * BM - 1) / (2 * BM), 1);
-  if (!launch_pdl(a.x_bf16 ? moe_prepare_kernel<TT, false>
-                           : moe_prepare_kernel<TT, true>,
-                  a.T, kPrepThreads, 0, s, a) ||
-      !launch_pdl(up, a.grid, kThreads, C::kAlloc, s, tm13, tmx, a) ||
-      !launch_pdl(down, a.grid, kThreads, C::kAlloc, s, tm2, tmh, a) ||
+  if (!launch_pdl(moe_prepare_kernel<TT, XTERMS == kTerms>, a.T, kPrepThreads, 0, s,
+                  a) ||
+      !launch_pdl(up, a.grid, kThreads, CU::kAlloc, s, tm13, tmx, a) ||
+      !launch_pdl(down, a.grid, kThreads, CD::kAlloc, s, tm2, tmh, a) ||
       !launch_pdl(moe_combine_kernel<TT>, combine, 2 * BM, 0, s, a))
     return FP8LA_ERR_CUDA;
   return launch_status();
@@ -1053,11 +1086,12 @@ extern "C" fp8la_status fp8_moe_layer(
   const int64_t st2 = num_experts > 1 ? expert_stride2 : D * ld2;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   const int64_t Dc = round16(D), Fc = round16(F);
+  const bool bf16 = x_dtype == FP8LA_TYPE_BF16;
   CUtensorMap tm13, tm2, tmx, tmh;
   if (!encode_codes(&tm13, w13, D, 2 * F, num_experts, ld13, st13, BM, 1) ||
       !encode_codes(&tm2, w2, F, D, num_experts, ld2, st2, BM, 1) ||
-      !encode_codes(&tmx, ws + l.xc, D, l.P, 2, Dc, l.P * Dc, 8, 2) ||
-      !encode_codes(&tmh, ws + l.hc, F, l.P, 2, Fc, l.P * Fc, 8, 2))
+      !encode_codes(&tmx, ws + l.xc, D, l.P, bf16 ? kBf16Terms : kTerms, Dc, l.P * Dc, 8, 2) ||
+      !encode_codes(&tmh, ws + l.hc, F, l.P, kTerms, Fc, l.P * Fc, 8, 2))
     return FP8LA_ERR_CUDA;
   unsigned *status = status_word_ptr();
   if (!status) return FP8LA_ERR_CUDA;
@@ -1075,7 +1109,6 @@ extern "C" fp8la_status fp8_moe_layer(
   a.p.out = reinterpret_cast<float *>(ws + l.out);
   a.x = x;
   a.ldx = ldx;
-  a.x_bf16 = x_dtype == FP8LA_TYPE_BF16;
   a.x_vec = aligned16(x) && ldx * xs % 16 == 0;
   a.T = static_cast<int32_t>(tokens);
   a.E = num_experts;
@@ -1097,7 +1130,9 @@ extern "C" fp8la_status fp8_moe_layer(
   a.status = status;
   a.timeout_ns = wait_timeout_ns();
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return tile_tokens(tokens, top_k, num_experts) == 16
-             ? launch_layer<16>(tm13, tmx, tm2, tmh, a, s)
-                                   : launch_layer<64>(tm13, tmx, tm2, tmh, a, s);
+  if (tile_tokens(tokens, top_k, num_experts) == 16)
+    return bf16 ? launch_layer<16, kBf16Terms>(tm13, tmx, tm2, tmh, a, 8, s)
+                : launch_layer<16, kTerms>(tm13, tmx, tm2, tmh, a, 10, s);
+  return bf16 ? launch_layer<64, kBf16Terms>(tm13, tmx, tm2, tmh, a, 9, s)
+              : launch_layer<64, kTerms>(tm13, tmx, tm2, tmh, a, 11, s);
 }
