@@ -657,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       gph ^= 1u;
       return __all_sync(0xffffffffu, ok) != 0;
     };
-    uint32_t g = 0, s = 0;
+    uint32_t g = 0, s = 0, ph = 0;
     bool ok = true;
     for (int n = 0; ok && n < items; ++n) {
       const Item w = item(n);
@@ -803,7 +803,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < TT; ++j) acc[j] = 0.0f;
         for (int c = w.c0; c < w.c1; ++c, ++g) {
           const uint32_t b = g & 1u;
-          const bool ready = mbar_wait(accfull_bar(b), (g >> 1) & 1u, a.timeout_ns,
+          // The accumulators were signalled by the MMA; the scales, which these
+          // threads read themselves, by their copy.
+          const bool ready = mbar_wait(full_bar(s), ph, a.timeout_ns, a.status,
+                                       abort_flag) &&
+                             mbar_wait(accfull_bar(b), (g >> 1) & 1u, a.timeout_ns,
                                        a.status, abort_flag);
           if (!__all_sync(0xffffffffu, ready)) {
             ok = false;
@@ -830,7 +834,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(accfree_bar(b));
             mbar_arrive(empty_bar(s));
           }
-          if (++s == C::STAGES) s = 0;
+          if (++s == C::STAGES) { s = 0; ph ^= 1u; }
         }
         if (!ok) break;
         const float ws = __ldg(a.s2 + w.t.expert);
