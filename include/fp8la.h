@@ -346,19 +346,23 @@ FP8LA_API fp8la_status fp8_moe_route(const void *logits, int32_t dtype, int64_t 
 
 /*
  * Mixture-of-experts layer for up to 128 tokens, all of it in four
- * launches, with FP8 weights and full-precision activations:
+ * launches, with FP8 weights and activations that are not quantised to FP8:
  *
  *   [g; u] = scale13[e] * dec(W13[e]) x_t        (rows 0..F-1 are g)
  *   h      = act(g) * u
  *   y_t    = bf16_rn( sum_j weights[t][j] * scale2[e_j] * dec(W2[e_j]) h ),
  *            e_j = ids[t][j], slots with id -1 left out
  *
- * Sums are FP32.  x and h enter the tensor cores as the sum of two E4M3
- * values under a power-of-two scale (of a token, or of 128 elements of h): 8
- * significant bits, which is exact for bf16 x except for elements below 2^-15
- * of the token's largest, and for fp32 x and for h no worse than a rounding to
- * bf16.  A token whose x holds an infinity or NaN gets a NaN row.  Tokens
- * with no expert get a zero row.  The result does not depend on timing.
+ * Sums are FP32.  x and h enter the tensor cores as sums of E4M3 values under
+ * a power-of-two scale, that of the token (x) or of 128 elements of h.  bf16 x
+ * is the sum of two, exact except for elements below 2^-15 of the token's
+ * largest, which are off by at most 2^-22 of it.  fp32 x and h are the sum of
+ * four: off by at most 2^-19 of the element or 2^-27 of the largest under the
+ * same scale, whichever is more.  A token whose x holds an infinity or NaN gets
+ * a NaN row, and so does one with an h that is not finite in FP32.  Weight codes
+ * that are infinite (E5M2) or NaN make the outputs that they reach infinite or
+ * NaN, and no others; which of the two is not specified.  Tokens with no expert
+ * get a zero row.  The result does not depend on timing.
  *
  * x: fp32 or bf16 [tokens][ldx]; ids: int32, weights: fp32 [tokens][top_k]
  * (from fp8_moe_route or any other router; an id twice in a token counts

@@ -1,5 +1,5 @@
 // Mixture-of-experts layer for a few tokens, with the expert weights in FP8
-// and the activations at full precision.
+// and the activations at 8 (BF16 x) and 18 bits (FP32 x, and h).
 //
 //   gate/up kernel:  [g; u] = s13[e] * W13[e] x_t,  h = act(g) * u
 //   down kernel:     y_t = sum_j w_tj * s2[e_j] * (W2[e_j] h_tj)

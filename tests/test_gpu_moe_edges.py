@@ -29,3 +29,67 @@ def test_every_block_has_its_own_scale(T):
     y = check_layer(fl, c)
     for _ in range(20):
         assert torch.equal(y, fl.moe_layer(**c))
+
+
+def users(c, e):
+    """Tokens that have expert e."""
+    return (c["ids"] == e).any(1)
+
+
+@pytest.mark.parametrize("T", [6, 40])
+def test_weight_codes_that_are_not_finite(T):
+    """An infinite or NaN E5M2 code of the gate or up weights reaches every
+    output of its expert's tokens, one of the down weights their output of its
+    row; nothing else changes by a bit."""
+    import torch
+    fl = lib()
+    for code in (0x7C, 0xFC, 0x7F):
+        c = make_layer(T, 5, 2, 200, 150, fmt="e5m2")
+        y0 = fl.moe_layer(**c)
+        hit = users(c, 3)
+        assert hit.any() and not hit.all()
+        for row in (17, 150 + 149):
+            d = dict(c, w13=c["w13"].clone())
+            d["w13"][3, row, 199] = code
+            y = fl.moe_layer(**pad16(d))
+            assert not torch.isfinite(y[hit].float()).any()
+            assert torch.equal(y[~hit], y0[~hit])
+        d = dict(c, w2=c["w2"].clone())
+        d["w2"][3, 177, 149] = code
+        y = fl.moe_layer(**pad16(d))
+        assert not torch.isfinite(y[hit, 177].float()).any()
+        y[:, 177] = y0[:, 177]
+        assert torch.equal(y, y0)
+    assert fl.device_status() == 0
+
+
+def pad16(c):
+    """Weights with rows of a multiple of 16 bytes."""
+    import torch
+    out = dict(c)
+    for k in ("w13", "w2"):
+        t = c[k]
+        wide = torch.zeros((*t.shape[:2], (t.shape[2] + 15) // 16 * 16), dtype=torch.uint8,
+                           device="cuda")
+        wide[:, :, :t.shape[2]] = t
+        out[k] = wide[:, :, :t.shape[2]]
+    return out
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("T", [6, 40])
+def test_h_beyond_fp32(T, dtype):
+    """Gate and up sums near 1e30 whose product is no FP32 number make NaN rows
+    of the expert's tokens, and of no others."""
+    import torch
+    fl = lib()
+    c = make_layer(T, 5, 2, 200, 150, dtype)
+    y0 = fl.moe_layer(**c)
+    hit = users(c, 2)
+    assert hit.any() and not hit.all()
+    c["scale13"][2] *= 1e30
+    y = fl.moe_layer(**c)
+    torch.cuda.synchronize()
+    assert fl.device_status() == 0
+    assert torch.isnan(y[hit].float()).all()
+    assert torch.equal(y[~hit], y0[~hit])
