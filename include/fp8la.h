@@ -75,7 +75,8 @@ typedef struct CUstream_st *fp8la_stream_t;
 typedef int fp8la_status;
 #define FP8LA_OK                  0
 #define FP8LA_ERR_INVALID_ARG    -1  /* NULL pointer, negative size, ld < width, ... */
-#define FP8LA_ERR_ALIGNMENT      -2  /* pointer or stride breaks the 16-byte TMA rule */
+#define FP8LA_ERR_ALIGNMENT      -2  /* pointer or stride breaks the 16-byte TMA rule,
+                                        or a pointer its element type's alignment */
 #define FP8LA_ERR_UNSUPPORTED    -3  /* size beyond a TMA or kernel limit; no sm_10x GPU */
 #define FP8LA_ERR_CUDA           -4  /* a CUDA runtime or driver call failed */
 #define FP8LA_ERR_DEVICE_TIMEOUT -5  /* a bounded wait inside a kernel ran out */

@@ -64,6 +64,11 @@ inline bool aligned16(const void *p) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
 }
 
+// Whether p is aligned to `size` bytes, a power of two.
+inline bool aligned_to(const void *p, int size) {
+  return (reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(size - 1)) == 0;
+}
+
 inline fp8la_status launch_status() {
   return cudaGetLastError() == cudaSuccess ? FP8LA_OK : FP8LA_ERR_CUDA;
 }

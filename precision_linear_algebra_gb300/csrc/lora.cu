@@ -993,10 +993,6 @@ fp8la_status check_factor(const uint16_t *p, int64_t ld, int64_t stride,
   return FP8LA_OK;
 }
 
-bool aligned_to(const void *p, int size) {
-  return reinterpret_cast<uintptr_t>(p) % size == 0;
-}
-
 fp8la_status run_shrink(const Segments &seg, const void *X, int32_t dtype,
                         int64_t ldx, const uint16_t *P, int64_t ldp,
                         int64_t stride, int64_t K, int32_t R, const float *alpha,
@@ -1104,7 +1100,7 @@ extern "C" fp8la_status fp8la_lora_apply(
     return st;
   if (!aligned_to(base, 2) || !aligned_to(out, 2) ||
       !aligned_to(x, x_dtype == FP8LA_TYPE_BF16 ? 2 : 4) || !aligned_to(alpha, 4) ||
-      !aligned_to(v, 4))
+      !aligned_to(v, 4) || !aligned_to(m_offsets, 4) || !aligned_to(adapter_ids, 4))
     return FP8LA_ERR_ALIGNMENT;
   if (!device_is_sm10x()) return FP8LA_ERR_UNSUPPORTED;
   Segments seg{m_offsets, adapter_ids, num_segments, static_cast<int32_t>(rows),
@@ -1147,7 +1143,8 @@ extern "C" fp8la_status fp8la_lora_backward(
   if (!aligned_to(dy, dy_dtype == FP8LA_TYPE_BF16 ? 2 : 4) ||
       !aligned_to(x, x_dtype == FP8LA_TYPE_BF16 ? 2 : 4) || !aligned_to(v, 4) ||
       !aligned_to(alpha, 4) || !aligned_to(dA, 4) || !aligned_to(dB, 4) ||
-      !aligned_to(dx_base, 2) || !aligned_to(dx, 2) || !aligned16(workspace))
+      !aligned_to(dx_base, 2) || !aligned_to(dx, 2) || !aligned_to(m_offsets, 4) ||
+      !aligned_to(adapter_ids, 4) || !aligned16(workspace))
     return FP8LA_ERR_ALIGNMENT;
   if (!device_is_sm10x()) return FP8LA_ERR_UNSUPPORTED;
   Segments seg{m_offsets, adapter_ids, num_segments, static_cast<int32_t>(rows),

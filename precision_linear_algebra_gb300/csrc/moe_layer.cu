@@ -1081,8 +1081,9 @@ extern "C" fp8la_status fp8_moe_layer(
   const int xs = x_dtype == FP8LA_TYPE_BF16 ? 2 : 4;
   if (!aligned16(w13) || !aligned16(w2) || ld13 % 16 != 0 || ld2 % 16 != 0 ||
       (num_experts > 1 && (expert_stride13 % 16 != 0 || expert_stride2 % 16 != 0)) ||
-      !aligned16(workspace) || reinterpret_cast<uintptr_t>(x) % xs != 0 ||
-      reinterpret_cast<uintptr_t>(y) % 2 != 0)
+      !aligned16(workspace) || !aligned_to(x, xs) || !aligned_to(y, 2) ||
+      !aligned_to(ids, 4) || !aligned_to(weights, 4) || !aligned_to(scale13, 4) ||
+      !aligned_to(scale2, 4))
     return FP8LA_ERR_ALIGNMENT;
   if (!device_is_sm10x()) return FP8LA_ERR_UNSUPPORTED;
   // A single expert's stride addresses nothing, but the tensor map wants one.

@@ -355,6 +355,10 @@ extern "C" fp8la_status fp8_moe_route(
   if (sort && need > 0 && (!workspace || workspace_bytes < need))
     return FP8LA_ERR_INVALID_ARG;
   if (tokens == 0 && !sort) return FP8LA_OK;
+  if (!aligned_to(logits, dtype == FP8LA_TYPE_BF16 ? 2 : 4) || !aligned_to(ids, 4) ||
+      !aligned_to(weights, 4) || !aligned_to(m_offsets, 4) || !aligned_to(order, 4) ||
+      (need > 0 && sort && !aligned_to(workspace, 4)))
+    return FP8LA_ERR_ALIGNMENT;
   if (!device_is_sm10x()) return FP8LA_ERR_UNSUPPORTED;
   // A sorting CTA's pairs are counted in 16 bits.
   const int64_t per = tokens_per_cta(tokens);
