@@ -414,16 +414,17 @@ def grouped_gemm(m_offsets, A, B, scale_a, scale_b, C=None):
 
 # The calls below run in the microseconds of a decoding step, so they look at
 # each tensor's shape and strides once and pass them straight to the library.
+# A tensor of the host is refused here: its pointer would reach a kernel.
 def _rows(t, rows, cols, dtype=None):
-    """Row stride of a [rows][cols] tensor whose rows are contiguous."""
-    assert t.shape == (rows, cols) and (dtype is None or t.dtype is dtype)
+    """Row stride of a CUDA [rows][cols] tensor whose rows are contiguous."""
+    assert t.is_cuda and t.shape == (rows, cols) and (dtype is None or t.dtype is dtype)
     s0, s1 = t.stride()
     assert s1 == 1 or cols == 1
     return s0 if rows > 1 else max(cols, 1)
 
 
 def _dense(t, shape, dtype):
-    assert t.dtype is dtype and t.shape == shape and t.is_contiguous()
+    assert t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous()
 
 
 def _type(t):
@@ -443,6 +444,7 @@ def _workspace(workspace, need, device):
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
         return workspace.data_ptr(), need, workspace
+    assert workspace.is_cuda and workspace.is_contiguous()
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
@@ -503,6 +505,7 @@ def moe_layer(x, ids, weights, w13, scale13, w2, scale2, y=None, workspace=None,
     top_k = ids.shape[1]
     assert w13.shape == (E, 2 * F, D) and w2.shape[1] == D
     assert w13.dtype is torch.uint8 and w2.dtype is torch.uint8
+    assert w13.is_cuda and w2.is_cuda
     e13, ld13, one13 = w13.stride()
     e2, ld2, one2 = w2.stride()
     assert (one13 == 1 or D == 1) and (one2 == 1 or F == 1)
@@ -528,6 +531,7 @@ def _adapters(A, B, alpha, m_offsets, adapter_ids, N):
     import torch
     n, R, K = A.shape
     assert A.dtype is torch.bfloat16 and B.dtype is torch.bfloat16 and B.shape == (n, R, N)
+    assert A.is_cuda and B.is_cuda
     sa, lda, onea = A.stride()
     sb, ldb, oneb = B.stride()
     assert (onea == 1 or K == 1) and (oneb == 1 or N == 1)
