@@ -810,7 +810,8 @@ __device__ __forceinline__ void outer_body(const OuterArgs &a, const OuterSide &
                                     8 * i + 2 * q) =
             make_float2(acc[m][i][e], acc[m][i][e + 1]);
   cluster_sync_all();
-  const float scale = o.use_alpha ? a.alpha[adapter] : 1.0f;
+  // Without rows the gradient is 0 whatever alpha is.
+  const float scale = o.use_alpha && nstep > 0 ? a.alpha[adapter] : 1.0f;
   const int cells = a.R * kOuterCols;
   for (int i = static_cast<int>(crank) * kThreads + threadIdx.x; i < cells;
        i += static_cast<int>(csize) * kThreads) {

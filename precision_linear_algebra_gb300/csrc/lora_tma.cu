@@ -968,6 +968,8 @@ __global__ void __launch_bounds__(kOThreads, RP <= 32 ? 2 : 1)
   const bool second = static_cast<int>(blockIdx.y) >= blocks0;
   const OuterSide &o = a.side[second];
   const CUtensorMap *tm = second ? &tm1 : &tm0;
+  // Without rows the gradient is 0 whatever alpha is.
+  const float scale = o.use_alpha && nstep > 0 ? a.alpha[adapter] : 1.0f;
   const int col0 = (blockIdx.y - (second ? blocks0 : 0)) * kOCols;
   // First row and number of rows of stage s; `i` follows s upwards.
   auto rows_of = [&](int s, int &i, int &t0) {
@@ -1117,7 +1119,6 @@ __global__ void __launch_bounds__(kOThreads, RP <= 32 ? 2 : 1)
       const int cc = 128 * m + 32 * (warp & 3) + lane;
       const uint32_t t = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16) + m * RP;
       float *red = reinterpret_cast<float *>(sbase);
-      const float scale = o.use_alpha ? a.alpha[adapter] : 1.0f;
 #pragma unroll
       for (int j = 0; j < RP; j += 16) {
         float sum[16];
@@ -1152,7 +1153,6 @@ __global__ void __launch_bounds__(kOThreads, RP <= 32 ? 2 : 1)
   __syncwarp();
   if (csize == 1) return;
   cluster_sync_all();
-  const float scale = o.use_alpha ? a.alpha[adapter] : 1.0f;
   const int cells = a.R * kOCols;
   for (int i = static_cast<int>(crank) * kOThreads + threadIdx.x; i < cells;
        i += static_cast<int>(csize) * kOThreads) {
