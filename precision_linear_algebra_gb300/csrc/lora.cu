@@ -866,7 +866,7 @@ fp8la_status launch_shrink_one(const ShrinkArgs &a, int slot, cudaStream_t s) {
   const int64_t T = a.seg.T, S = a.seg.S;
   // Half of the segments, about, end in a tile of their own.
   const int64_t tiles = T / C::TM + ((S < T ? S : T) + 1) / 2;
-  const int64_t slots = 152 * (C::kSmem > 110 * 1024 ? 1 : C::kSmem > 50 * 1024 ? 2 : 4);
+  const int64_t slots = sms() * (C::kSmem > 110 * 1024 ? 1 : C::kSmem > 50 * 1024 ? 2 : 4);
   const int cluster = choose_cluster(tiles, (a.K + C::KS - 1) / C::KS, slots, 4);
   return launch(kern,
                 dim3(cluster, static_cast<unsigned>(tile_bound(T, S, C::TM)), 1),
@@ -879,7 +879,7 @@ fp8la_status launch_shrink_nj(const ShrinkArgs &a, int slot, cudaStream_t s) {
   // too few tiles for the SMs even with K split over whole clusters.
   if (short_segments(a.seg.T, a.seg.S))
     return launch_shrink_one<F32, 1, 1, NJ>(a, slot, s);
-  if (a.seg.T < 152 * 128 / kMaxCluster)
+  if (a.seg.T < sms() * 128 / kMaxCluster)
     return launch_shrink_one<F32, 4, 1, NJ>(a, slot + 1, s);
   return launch_shrink_one<F32, 4, 2, NJ>(a, slot + 2, s);
 }
@@ -907,7 +907,7 @@ fp8la_status launch_expand_one(ExpandArgs a, int slot, cudaStream_t s) {
   // each brings its own factor.
   const int64_t T = a.seg.T, S = a.seg.S;
   const int64_t blocks = (a.N + kExpandCols - 1) / kExpandCols;
-  const int64_t ranges = blocks < 152 ? 152 / blocks : 1;
+  const int64_t ranges = blocks < sms() ? sms() / blocks : 1;
   int64_t rows = (T + ranges - 1) / ranges;
   if (CH == 16) {
     const int64_t mean = (T + S - 1) / S;
@@ -957,7 +957,7 @@ fp8la_status launch_outer(const OuterArgs &a, int slot, cudaStream_t s) {
                          (a.side[1].N + kOuterCols - 1) / kOuterCols;
   const int cluster = choose_cluster(
       blocks * a.seg.n, (a.seg.T + 32 * a.seg.n - 1) / (32 * a.seg.n),
-      152 * kOuterCtas<MR>, 6);
+      sms() * kOuterCtas<MR>, 6);
   return launch(kern, dim3(cluster, static_cast<unsigned>(blocks),
                            static_cast<unsigned>(a.seg.n)),
                 kThreads, kSmem, cluster, s, a);

@@ -271,6 +271,12 @@ inline fp8la_status launch(Kern kern, dim3 grid, int threads, size_t smem,
                                                           : FP8LA_ERR_CUDA;
 }
 
+// SMs of the current device (the launch itself fails where there is none).
+inline int64_t sms() {
+  const int n = sm_count();
+  return n > 0 ? n : 1;
+}
+
 // CTAs of a cluster that share out a long axis: the least time for `items`
 // clusters of `stages` stages each, where a CTA takes about `fixed` stages'
 // time to start and to add up, and the SMs hold `slots` CTAs at once (a

@@ -1218,7 +1218,7 @@ fp8la_status shrink_one(const ShrinkArgs &a, int slot, cudaStream_t s) {
     return FP8LA_ERR_CUDA;
   const int64_t T = a.seg.T, S = a.seg.S;
   const int64_t tiles = T / kSRows + ((S < T ? S : T) + 1) / 2;
-  const int cluster = choose_cluster(tiles, (a.K + kSK - 1) / kSK, 152, 6);
+  const int cluster = choose_cluster(tiles, (a.K + kSK - 1) / kSK, sms(), 6);
   return launch(kern, dim3(cluster, static_cast<unsigned>(tile_bound(T, S, kSRows)), 1),
                 kSThreads, C::kAlloc, cluster, s, tmX, tmP, a, wait_timeout_ns());
 }
@@ -1238,7 +1238,7 @@ fp8la_status shrink_f32_one(const ShrinkArgs &a, int slot, cudaStream_t s) {
     return FP8LA_ERR_CUDA;
   const int64_t T = a.seg.T, S = a.seg.S;
   const int64_t tiles = T / kSRows + ((S < T ? S : T) + 1) / 2;
-  const int cluster = choose_cluster(tiles, (a.K + kFK - 1) / kFK, 152, 6);
+  const int cluster = choose_cluster(tiles, (a.K + kFK - 1) / kFK, sms(), 6);
   return launch(kern, dim3(cluster, static_cast<unsigned>(tile_bound(T, S, kSRows)), 1),
                 kFThreads, C::kAlloc, cluster, s, tmX, tmP, a, wait_timeout_ns());
 }
@@ -1282,7 +1282,7 @@ fp8la_status outer_one(const OuterArgs &a, int slot, cudaStream_t s) {
   }
   const int64_t n = a.seg.n;
   const int cluster =
-      choose_cluster(blocks * n, (a.seg.T + kORows * n - 1) / (kORows * n), 152, 6);
+      choose_cluster(blocks * n, (a.seg.T + kORows * n - 1) / (kORows * n), sms(), 6);
   return launch(kern, dim3(cluster, static_cast<unsigned>(blocks),
                            static_cast<unsigned>(n)),
                 kOThreads, C::kAlloc, cluster, s, tm[0], tm[1], a, wait_timeout_ns());
