@@ -1281,6 +1281,12 @@ fp8la_status outer_one(const OuterArgs &a, int slot, cudaStream_t s) {
     blocks += (o.N + kOCols - 1) / kOCols;
   }
   const int64_t n = a.seg.n;
+  // Two CTAs fit on an SM at ranks up to 32, but one is counted: two lead to
+  // smaller clusters, which most of the sizes tried do not like.  Measured, us for a
+  // backward pass counting one / two: rank 32, 4096 x 8192 with 3 adapters 97.4 /
+  // 99.8, 1024 x 4096 with 4 27.7 / 30.5, 4096 x 2048 with 8 43.3 / 44.7, 4096 x
+  // 4096 with 4 58.7 / 57.5; rank 8, 2048 x 2048 with 8 23.1 / 24.2; rank 16, 4096
+  // x 4096 with 2 55.3 / 50.0, 4096 x 8192 with 1 90.4 / 79.9.
   const int cluster =
       choose_cluster(blocks * n, (a.seg.T + kORows * n - 1) / (kORows * n), sms(), 6);
   return launch(kern, dim3(cluster, static_cast<unsigned>(blocks),
