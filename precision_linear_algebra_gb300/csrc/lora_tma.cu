@@ -595,6 +595,13 @@ __global__ void __launch_bounds__(kEThreads, 1)
       u += g1 - g0;
     }
   };
+  // Whether a tile's sums are stored by TMA.  Not those of a tile that ends inside
+  // the 128 rows: what follows belongs to another segment or share.  Nor where the
+  // matrix ends inside a 16-byte unit: TMA stores whole units, and what follows a
+  // row's last column belongs to the caller.
+  auto by_tma = [&](const Walk &w, int col) {
+    return w.n == kERows && (col + kECols <= a.N || a.N % 8 == 0);
+  };
   // Runs of tiles with one factor: its adapter and column block.
   struct Run {
     int id = -1, col = -1, count = 0;
@@ -687,7 +694,7 @@ __global__ void __launch_bounds__(kEThreads, 1)
         const int b = n & 1;
         if (!mbar_wait(done_bar(b), (n >> 1) & 1u, timeout_ns, a.seg.status, abort_flag))
           return false;
-        if (w.n == kERows) {
+        if (by_tma(w, col)) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             if (col + 64 * j < a.N)
@@ -785,6 +792,7 @@ __global__ void __launch_bounds__(kEThreads, 1)
       if (!__all_sync(0xffffffffu, ready)) return false;
       tc_fence_after();
       uint16_t *dst = a.out + (w.row + static_cast<int64_t>(row)) * a.ld_out;
+      const bool stage = by_tma(w, col);
 #pragma unroll 1
       for (int j = 0; j < 4; ++j) {  // 32 columns
         uint8_t *src = sbase + b * C::kStage + (2 * half + (j >> 1)) * C::kBox + row * 128;
@@ -806,11 +814,9 @@ __global__ void __launch_bounds__(kEThreads, 1)
               y[q] = *reinterpret_cast<const uint32_t *>(&s);
             }
           }
-          if (w.n == kERows) {
+          if (stage) {
             *at = x;
           } else if (row < w.n) {
-            // A tile that ends inside the 128 rows: what follows belongs to
-            // another segment or share.
             const int64_t c = c0 + 8 * i;
             if (c + 8 <= a.N) {
               *reinterpret_cast<uint4 *>(dst + c) = x;

@@ -139,7 +139,8 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src,
 
 // TMA store of a 2-D box from shared memory (bulk-group completion).  The
 // innermost coordinate times the element size must be a multiple of 16
-// bytes; elements outside the tensor are not written.
+// bytes.  Nothing is written outside the tensor but for this: where a row ends
+// inside a 16-byte unit, the whole unit is.
 __device__ __forceinline__ void tma_store_2d(const void *tmap, uint32_t src,
                                              int32_t c0, int32_t c1) {
   asm volatile(
