@@ -1,0 +1,85 @@
+"""GPU: V and the factors' gradients are as good as sums of FP32 values.
+
+An FP32 operand is exactly the sum of three BF16 terms, and products of BF16
+numbers are exact, so the sums alone lose something.  A tensor core's addition
+cuts off what lies below the running sum's last bits, always towards zero: each
+of m additions into one accumulator leaves a share of the running sum, which in a
+sum of random signs comes to something like m of the result.  So accumulators
+have to stay short, whatever the sizes, and be added up in FP32.  Measured on
+chains of known length: 43 steps of 16 rows leave 1.0e-6 in dA (rank 64, 4096
+rows), 32 steps 4.8e-7 in V (8192 products).  Twice that is allowed at every
+size, 2^-19 and 2^-20, but for ranks above 64, where the first version of the
+gradients had one accumulator of 128 steps at 4096 rows: 2^-18 there.
+
+With two terms instead of three the operand alone would be off by 2.5e-6, and one
+accumulator for all steps was measured at 2e-6 in V and more than 1e-5 in the
+gradients: up to rank 64 either breaks these bounds, where test_gpu_lora.py's,
+made for any two terms, would let it pass."""
+
+import pytest
+
+from _helpers import lib
+from test_gpu_lora import make, random_v
+
+pytestmark = pytest.mark.gpu
+
+V_NORM = 2.0 ** -20
+
+
+def gradient_norm(R):
+    return 2.0 ** (-19 if R <= 64 else -18)
+
+
+def off(got, want):
+    return ((got.double() - want).norm() / want.norm()).item()
+
+
+@pytest.mark.parametrize("xt", ["bfloat16", "float32"])
+@pytest.mark.parametrize("T,R,K,N", [
+    (4096, 16, 8192, 1024),
+    (4096, 64, 8192, 1024),
+    (4096, 128, 8192, 1024),
+    (100, 16, 8192, 1000),          # below a tile of 128 rows
+    (100, 64, 8192, 1000),
+    (300, 32, 8190, 1002),          # rows that TMA cannot read
+    (5000, 8, 8190, 70),
+])
+def test_one_long_segment(T, R, K, N, xt):
+    import torch
+    fl = lib()
+    c = make(T, [T], [0], 1, R, K, N, xt=xt)
+    x, dy, A, B, al = (c[k].double() for k in ("x", "dy", "A", "B", "alpha"))
+    _, v = fl.lora_apply(*[c[k] for k in ("base", "x", "A", "B", "alpha", "m_offsets",
+                                          "adapter_ids")])
+    assert off(v, x @ A[0].t()) <= V_NORM
+    v = random_v(c)
+    _, dA, dB = fl.lora_backward(c["dy"], c["x"], v, *[c[k] for k in (
+        "A", "B", "alpha", "m_offsets", "adapter_ids", "dx_base")])
+    assert off(dA[0], (al[0] * (dy @ B[0].t())).t() @ x) <= gradient_norm(R)
+    assert off(dB[0], al[0] * (v.double().t() @ dy)) <= gradient_norm(R)
+    assert fl.device_status() == 0
+
+
+@pytest.mark.parametrize("xt", ["bfloat16", "float32"])
+@pytest.mark.parametrize("R", [16])
+def test_short_segments(R, xt):
+    """512 segments of 1 or 3 rows, two adapters."""
+    import torch
+    fl = lib()
+    lengths = [1, 3] * 256
+    ids = [(i // 2) % 2 for i in range(512)]
+    c = make(1024, lengths, ids, 2, R, 8192, 1024, xt=xt)
+    x, dy, A, B, al = (c[k].double() for k in ("x", "dy", "A", "B", "alpha"))
+    who = torch.repeat_interleave(c["adapter_ids"], torch.tensor(lengths, device="cuda"))
+    _, v = fl.lora_apply(*[c[k] for k in ("base", "x", "A", "B", "alpha", "m_offsets",
+                                          "adapter_ids")])
+    w = random_v(c)
+    _, dA, dB = fl.lora_backward(c["dy"], c["x"], w, *[c[k] for k in (
+        "A", "B", "alpha", "m_offsets", "adapter_ids", "dx_base")])
+    for i in range(2):
+        mine = who == i
+        assert off(v[mine], x[mine] @ A[i].t()) <= V_NORM
+        dv = al[i] * (dy[mine] @ B[i].t())
+        assert off(dA[i], dv.t() @ x[mine]) <= gradient_norm(R)
+        assert off(dB[i], al[i] * (w[mine].double().t() @ dy[mine])) <= gradient_norm(R)
+    assert fl.device_status() == 0
