@@ -95,10 +95,11 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&u)[16]) {
 constexpr int kSThreads = 192;      // warps 0-3 epilogue, 4 producer, 5 MMA
 constexpr int kSRows = 128;
 constexpr int kSK = 128;            // K of a stage: two boxes of 64
-// Accumulators that stages take in turn.  The tensor core cuts off a little of
-// the running sum with each addition, so a sum is kept in several shorter
-// ones, which the epilogue adds with rounding: with one accumulator, 2048
-// products in it left a relative error of 2e-6 in V, more than FP32 has.
+// Stages of one accumulator.  The tensor core cuts off a little of the running
+// sum with each addition, always towards zero, so long sums are kept in short
+// ones, which the epilogue adds with rounding while the next is made: after 128
+// steps of 16 products V's relative error was 2e-6, more than FP32 has.
+constexpr int kChain = 2;
 constexpr int kAcc = 4;
 
 // Tile row sums of a shrink CTA, `red` in every CTA of the cluster, to V.
@@ -126,10 +127,10 @@ struct ShrinkTma {
   static constexpr int kP = RP * kSK * 2;
   static constexpr int kStage = kX + kP;
   static constexpr int STAGES = 4 * kStage <= 200 * 1024 ? 4 : 3;
-  static constexpr int kTmemCols = kAcc * RP;
+  static constexpr int kTmemCols = 2 * RP;  // two accumulators
   static constexpr int kLdR = RP + 1;  // of the sums, in floats
   static constexpr int kBar = STAGES * kStage;
-  static constexpr int kMisc = kBar + (2 * STAGES + 1) * 8;
+  static constexpr int kMisc = kBar + (2 * STAGES + 5) * 8;
   static constexpr int kAlloc = kMisc + 32 + 1024;
   static_assert(kSRows * kLdR * 4 <= STAGES * kStage, "the sums overlay the ring");
   static_assert(kP % 1024 == 0 && kAlloc <= 226 * 1024, "shared memory");
@@ -162,13 +163,19 @@ __global__ void __launch_bounds__(kSThreads)
   const uint32_t bar0 = base + C::kBar;
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (C::STAGES + s); };
-  const uint32_t done_bar = bar0 + 8u * (2 * C::STAGES);
+  auto accfull_bar = [&](int b) { return bar0 + 8u * (2 * C::STAGES + b); };
+  auto accfree_bar = [&](int b) { return bar0 + 8u * (2 * C::STAGES + 2 + b); };
+  const uint32_t done_bar = bar0 + 8u * (2 * C::STAGES + 4);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sbase + C::kMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sbase + C::kMisc + 4);
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(accfull_bar(b), 1);
+      mbar_init(accfree_bar(b), 4);
     }
     mbar_init(done_bar, 1);
     *abort_flag = 0;
@@ -215,7 +222,12 @@ __global__ void __launch_bounds__(kSThreads)
       constexpr uint32_t idesc = idesc_bf16_f32(kSRows, RP, false);
       uint32_t s = 0, ph = 0;
       for (int c = s0; c < s1; ++c) {
-        if (!mbar_wait(full_bar(s), ph, timeout_ns, a.seg.status, abort_flag)) break;
+        const int g = (c - s0) / kChain, b = g & 1;
+        const bool first = (c - s0) % kChain == 0;
+        if ((first && !mbar_wait(accfree_bar(b), ((g >> 1) & 1u) ^ 1u, timeout_ns,
+                                 a.seg.status, abort_flag)) ||
+            !mbar_wait(full_bar(s), ph, timeout_ns, a.seg.status, abort_flag))
+          break;
         tc_fence_after();
         const uint32_t d = base + s * C::kStage;
 #pragma unroll
@@ -224,36 +236,48 @@ __global__ void __launch_bounds__(kSThreads)
           const uint64_t bd = smem_desc_k128_sw128(d + C::kX + h * (C::kP / 2));
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            umma_bf16(tmem_base + (c - s0) % kAcc * RP, ad + 2u * k, bd + 2u * k,
-                      idesc, (c - s0 >= kAcc || h > 0 || k > 0) ? 1u : 0u);
+            umma_bf16(tmem_base + b * RP, ad + 2u * k, bd + 2u * k, idesc,
+                      (!first || h > 0 || k > 0) ? 1u : 0u);
         }
         umma_commit(empty_bar(s));
+        if ((c - s0) % kChain == kChain - 1 || c + 1 == s1) umma_commit(accfull_bar(b));
         if (++s == C::STAGES) { s = 0; ph ^= 1u; }
       }
       umma_commit(done_bar);
       mbar_wait_drain(done_bar, 0, timeout_ns, a.seg.status);
     }
   } else {
-    // The ring is free once the last MMA is done: the sums go there.
-    const bool ready = mbar_wait(done_bar, 0, timeout_ns, a.seg.status, abort_flag);
-    if (__all_sync(0xffffffffu, ready)) {
+    const int row = 32 * warp + lane;
+    const uint32_t col0 = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
+    float sum[RP];
+#pragma unroll
+    for (int j = 0; j < RP; ++j) sum[j] = 0.0f;
+    const int chains = (s1 - s0 + kChain - 1) / kChain;
+    bool ok = true;
+    for (int g = 0; g < chains; ++g) {
+      const int b = g & 1;
+      const bool ready = mbar_wait(accfull_bar(b), (g >> 1) & 1u, timeout_ns,
+                                   a.seg.status, abort_flag);
+      if (!__all_sync(0xffffffffu, ready)) {
+        ok = false;
+        break;
+      }
       tc_fence_after();
-      const int row = 32 * warp + lane;
-      const uint32_t col0 = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
 #pragma unroll
       for (int j = 0; j < RP; j += 16) {
-        float sum[16];
+        float v[16];
+        tmem_ld16(col0 + b * RP + j, v);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) sum[i] = 0.0f;
-        for (int q = 0; q < min(kAcc, s1 - s0); ++q) {
-          float v[16];
-          tmem_ld16(col0 + q * RP + j, v);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) sum[i] += v[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) red[row * C::kLdR + j + i] = sum[i];
+        for (int i = 0; i < 16; ++i) sum[j + i] += v[i];
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(accfree_bar(b));
+    }
+    // The ring is free, as the last MMA is done: the sums go there.
+    if (ok) {
+#pragma unroll
+      for (int j = 0; j < RP; ++j) red[row * C::kLdR + j] = sum[j];
     }
   }
   tc_fence_before();

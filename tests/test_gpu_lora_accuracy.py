@@ -43,6 +43,7 @@ def off(got, want):
     (100, 64, 8192, 1000),
     (300, 32, 8190, 1002),          # rows that TMA cannot read
     (5000, 8, 8190, 70),
+    (20480, 24, 8192, 64),          # tiles enough for the SMs: K in one piece
 ])
 def test_one_long_segment(T, R, K, N, xt):
     import torch
@@ -61,7 +62,7 @@ def test_one_long_segment(T, R, K, N, xt):
 
 
 @pytest.mark.parametrize("xt", ["bfloat16", "float32"])
-@pytest.mark.parametrize("R", [16])
+@pytest.mark.parametrize("R", [16, 48])
 def test_short_segments(R, xt):
     """512 segments of 1 or 3 rows, two adapters."""
     import torch
