@@ -299,9 +299,10 @@ __global__ void __launch_bounds__(kSThreads)
 // 32 KB and twelve MMAs stay below the stage's share of memory time.  With a
 // forward pass of 4096 rows, rank 64, 8192 -> 8192 it takes 73 us on the stream
 // (276 MB, 3.8 TB/s), with the mma.sync form 131.
-constexpr int kFConv = 8;           // converter warps, 0-3 also epilogue
+constexpr int kFConv = 8;           // converter and epilogue warps
 constexpr int kFThreads = 32 * (kFConv + 2);
 constexpr int kFK = 64;             // K of a stage: two boxes of 32 floats
+constexpr int kFChain = 4;          // stages of an accumulator, see kChain
 
 template <int RP>
 struct ShrinkF32 {
@@ -311,14 +312,16 @@ struct ShrinkF32 {
   static constexpr int kStage = kX + kP;
   static constexpr int kTerm = kSRows * 128;
   static constexpr int STAGES = RP <= 64 ? 3 : 2;
-  // Accumulators as in the outer kernel: NACC for the first term, in turn, and
-  // one for the other two; all of TMEM, at most.
-  static constexpr int NACC = RP <= 64 ? 7 : 3;
-  static constexpr int kTmemCols = (NACC + 1) * RP;
+  // Two accumulators for the first term, and one for all of the other two, which
+  // are 2^-8 of it or less.
+  static constexpr int kTmemCols = 4 * RP;          // a power of two
+  // Warps that add them up, and the columns of each: half, but no less than a load.
+  static constexpr int kAddWarps = RP >= 32 ? kFConv : kFConv / 2;
+  static constexpr int kAddCols = RP >= 32 ? RP / 2 : RP;
   static constexpr int kLdR = RP + 1;
   static constexpr int kT = STAGES * kStage;        // [2][3 terms]
   static constexpr int kBar = kT + 6 * kTerm;
-  static constexpr int kMisc = kBar + (2 * STAGES + 5) * 8;
+  static constexpr int kMisc = kBar + (2 * STAGES + 9) * 8;
   static constexpr int kAlloc = kMisc + 32 + 1024;
   static_assert(kSRows * kLdR * 4 <= kT, "the sums overlay the ring");
   static_assert(kP % 1024 == 0 && kAlloc <= 226 * 1024, "shared memory");
@@ -354,7 +357,9 @@ __global__ void __launch_bounds__(kFThreads, 1)
   auto empty_bar = [&](int s) { return bar0 + 8u * (C::STAGES + s); };
   auto tready_bar = [&](int b) { return bar0 + 8u * (2 * C::STAGES + b); };
   auto tfree_bar = [&](int b) { return bar0 + 8u * (2 * C::STAGES + 2 + b); };
-  const uint32_t done_bar = bar0 + 8u * (2 * C::STAGES + 4);
+  auto accfull_bar = [&](int b) { return bar0 + 8u * (2 * C::STAGES + 4 + b); };
+  auto accfree_bar = [&](int b) { return bar0 + 8u * (2 * C::STAGES + 6 + b); };
+  const uint32_t done_bar = bar0 + 8u * (2 * C::STAGES + 8);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sbase + C::kMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sbase + C::kMisc + 4);
   if (threadIdx.x == 0) {
@@ -365,6 +370,8 @@ __global__ void __launch_bounds__(kFThreads, 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(tready_bar(b), kFConv);
       mbar_init(tfree_bar(b), 1);
+      mbar_init(accfull_bar(b), 1);
+      mbar_init(accfree_bar(b), C::kAddWarps);
     }
     mbar_init(done_bar, 1);
     *abort_flag = 0;
@@ -409,7 +416,11 @@ __global__ void __launch_bounds__(kFThreads, 1)
       uint32_t s = 0, ph = 0;
       for (int c = s0; c < s1; ++c) {
         const uint32_t b = (c - s0) & 1u, use = (c - s0) >> 1;
-        if (!mbar_wait(full_bar(s), ph, timeout_ns, a.seg.status, abort_flag) ||
+        const int g = (c - s0) / kFChain;
+        const bool first = (c - s0) % kFChain == 0;
+        if ((first && !mbar_wait(accfree_bar(g & 1), ((g >> 1) & 1u) ^ 1u, timeout_ns,
+                                 a.seg.status, abort_flag)) ||
+            !mbar_wait(full_bar(s), ph, timeout_ns, a.seg.status, abort_flag) ||
             !mbar_wait(tready_bar(b), use & 1u, timeout_ns, a.seg.status, abort_flag))
           break;
         tc_fence_after();
@@ -418,15 +429,16 @@ __global__ void __launch_bounds__(kFThreads, 1)
 #pragma unroll
         for (int t = 0; t < 3; ++t) {
           const uint64_t ad = smem_desc_k128_sw128(terms + t * C::kTerm);
-          const uint32_t d =
-              tmem_base + (t == 0 ? (c - s0) % C::NACC : C::NACC) * RP;
+          const uint32_t d = tmem_base + (t == 0 ? g & 1 : 2) * RP;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             umma_bf16(d, ad + 2u * k, bd + 2u * k, idesc,
-                      (k > 0 || t > 1 || c - s0 >= (t == 0 ? C::NACC : 1)) ? 1u : 0u);
+                      (k > 0 || t > 1 || (t == 0 ? !first : c > s0)) ? 1u : 0u);
         }
         umma_commit(empty_bar(s));
         umma_commit(tfree_bar(b));
+        if ((c - s0) % kFChain == kFChain - 1 || c + 1 == s1)
+          umma_commit(accfull_bar(g & 1));
         if (++s == C::STAGES) { s = 0; ph ^= 1u; }
       }
       umma_commit(done_bar);
@@ -436,6 +448,35 @@ __global__ void __launch_bounds__(kFThreads, 1)
     // A unit is 8 values of a row: 32 bytes in, 16 bytes of each term out.  A
     // warp takes the same unit of 32 rows, which the swizzle spreads over the
     // banks.
+    // They also add the accumulators up, thread = row: a chain's while the second
+    // stage after it is multiplied, so that they rarely wait for it.
+    float sum[C::kAddCols];
+#pragma unroll
+    for (int j = 0; j < C::kAddCols; ++j) sum[j] = 0.0f;
+    const int first_col = (warp >> 2) * C::kAddCols;
+    const uint32_t col0 =
+        tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16) + first_col;
+    auto add = [&](int acc) {
+#pragma unroll
+      for (int j = 0; j < C::kAddCols; j += 16) {
+        float v[16];
+        tmem_ld16(col0 + acc * RP + j, v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum[j + i] += v[i];
+      }
+    };
+    auto add_chain = [&](int g) {
+      const bool ready = mbar_wait(accfull_bar(g & 1), (g >> 1) & 1u, timeout_ns,
+                                   a.seg.status, abort_flag);
+      if (!__all_sync(0xffffffffu, ready)) return false;
+      tc_fence_after();
+      add(g & 1);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(accfree_bar(g & 1));
+      return true;
+    };
+    int added = 0;
     uint32_t s = 0, ph = 0;
     bool ok = true;
     for (int c = s0; c < s1; ++c) {
@@ -473,30 +514,24 @@ __global__ void __launch_bounds__(kFThreads, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(tready_bar(b));
-    }
-    if (warp < 4) {
-      // The ring is free once the last MMA is done: the sums go there.
-      const bool ready =
-          ok && mbar_wait(done_bar, 0, timeout_ns, a.seg.status, abort_flag);
-      if (__all_sync(0xffffffffu, ready)) {
-        tc_fence_after();
-        const int row = 32 * warp + lane, used = min(C::NACC, s1 - s0);
-        const uint32_t col0 = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
-#pragma unroll
-        for (int j = 0; j < RP; j += 16) {
-          float sum[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) sum[i] = 0.0f;
-          // The small terms first.
-          for (int n = used; used > 0 && n >= 0; --n) {
-            float v[16];
-            tmem_ld16(col0 + (n == used ? C::NACC : n) * RP + j, v);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) sum[i] += v[i];
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) red[row * C::kLdR + j + i] = sum[i];
+      if (warp < C::kAddWarps && c - s0 == (added + 1) * kFChain + 1) {
+        if (!add_chain(added)) {
+          ok = false;
+          break;
         }
+        ++added;
+      }
+    }
+    if (warp < C::kAddWarps) {
+      const int chains = (s1 - s0 + kFChain - 1) / kFChain;
+      for (; ok && added < chains; ++added) ok = add_chain(added);
+      // The ring is free, as the last MMA is done: the sums go there.
+      if (ok) {
+        if (chains > 0) add(2);
+        const int row = 32 * (warp & 3) + lane;
+#pragma unroll
+        for (int j = 0; j < C::kAddCols; ++j)
+          red[row * C::kLdR + first_col + j] = sum[j];
       }
     }
   }

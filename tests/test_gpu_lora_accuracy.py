@@ -43,7 +43,7 @@ def off(got, want):
     (100, 64, 8192, 1000),
     (300, 32, 8190, 1002),          # rows that TMA cannot read
     (5000, 8, 8190, 70),
-    (20480, 24, 8192, 64),          # tiles enough for the SMs: K in one piece
+    (20480, 24, 8192, 64),
 ])
 def test_one_long_segment(T, R, K, N, xt):
     import torch
@@ -83,4 +83,16 @@ def test_short_segments(R, xt):
         dv = al[i] * (dy[mine] @ B[i].t())
         assert off(dA[i], dv.t() @ x[mine]) <= gradient_norm(R)
         assert off(dB[i], al[i] * (w[mine].double().t() @ dy[mine])) <= gradient_norm(R)
+    assert fl.device_status() == 0
+
+
+@pytest.mark.parametrize("xt", ["bfloat16", "float32"])
+@pytest.mark.parametrize("T,R,K", [(32768, 128, 8192), (20480, 16, 16384), (20480, 64, 16384)])
+def test_v_of_rows_for_every_sm(T, R, K, xt):
+    """Tiles enough for the SMs, so that each has K in one piece."""
+    fl = lib()
+    c = make(T, [T], [0], 1, R, K, 16, xt=xt)
+    _, v = fl.lora_apply(*[c[k] for k in ("base", "x", "A", "B", "alpha", "m_offsets",
+                                          "adapter_ids")])
+    assert off(v, c["x"].double() @ c["A"][0].double().t()) <= V_NORM
     assert fl.device_status() == 0
