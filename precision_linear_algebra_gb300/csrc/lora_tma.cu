@@ -100,7 +100,6 @@ constexpr int kSK = 128;            // K of a stage: two boxes of 64
 // ones, which the epilogue adds with rounding while the next is made: after 128
 // steps of 16 products V's relative error was 2e-6, more than FP32 has.
 constexpr int kChain = 2;
-constexpr int kAcc = 4;
 
 // Tile row sums of a shrink CTA, `red` in every CTA of the cluster, to V.
 template <int THREADS>
@@ -914,6 +913,9 @@ constexpr int kOConv = 8;           // converter and epilogue warps
 constexpr int kOThreads = 32 * (kOConv + 2);
 constexpr int kOCols = 256;         // two MMA blocks of 128
 constexpr int kORows = 64;          // of a stage
+// Stages of an accumulator, see kChain.  4, 8 and 16 take 102.3, 101.8 and 101.5 us
+// for the backward pass named above and leave 4.3e-7, 6.6e-7 and more of dA.
+constexpr int kOChain = 4;
 
 template <int RP>
 struct OuterTma {
@@ -924,14 +926,14 @@ struct OuterTma {
   // Two CTAs on an SM for the smallest ranks, so that one streams while the
   // other starts or adds up.
   static constexpr int STAGES = RP <= 32 ? 2 : 3;
-  // Accumulators: NACC that stages take in turn for V's first term, and one
-  // for the other two, which are 2^-8 of it or less; all of TMEM, at most.
-  static constexpr int NACC = RP <= 64 ? kAcc - 1 : 1;
-  static constexpr int kTmemCols = 2 * RP * (NACC + 1);
+  // NACC accumulators for V's first term, and one for all of the other two, which
+  // are 2^-8 of it or less.  With one the MMA waits until it has been added up.
+  static constexpr int NACC = RP <= 64 ? 2 : 1;
+  static constexpr int kTmemCols = RP <= 64 ? 8 * RP : 4 * RP;  // a power of two
   static constexpr int kVBuf = STAGES * kX;         // [2][3 terms]
   static constexpr int kLdR = kOCols + 4;
   static constexpr int kBar = kVBuf + 2 * kV;
-  static constexpr int kMisc = kBar + (3 * STAGES + 4 + 1) * 8;
+  static constexpr int kMisc = kBar + (2 * STAGES + 9) * 8;
   static constexpr int kSegs = kMisc + 32;          // three lists
   static constexpr int kAlloc = kSegs + 3 * kMaxSegments * 4 + 1024;
   static_assert(RP * kLdR * 4 <= kBar, "the sums overlay the ring");
@@ -959,7 +961,9 @@ __global__ void __launch_bounds__(kOThreads, RP <= 32 ? 2 : 1)
   auto empty_bar = [&](int s) { return bar0 + 8u * (C::STAGES + s); };
   auto vready_bar = [&](int b) { return bar0 + 8u * (2 * C::STAGES + b); };
   auto vfree_bar = [&](int b) { return bar0 + 8u * (2 * C::STAGES + 2 + b); };
-  const uint32_t done_bar = bar0 + 8u * (2 * C::STAGES + 4);
+  auto accfull_bar = [&](int b) { return bar0 + 8u * (2 * C::STAGES + 4 + b); };
+  auto accfree_bar = [&](int b) { return bar0 + 8u * (2 * C::STAGES + 6 + b); };
+  const uint32_t done_bar = bar0 + 8u * (2 * C::STAGES + 8);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sbase + C::kMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sbase + C::kMisc + 4);
   if (threadIdx.x == 0) {
@@ -970,6 +974,8 @@ __global__ void __launch_bounds__(kOThreads, RP <= 32 ? 2 : 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(vready_bar(b), kOConv);
       mbar_init(vfree_bar(b), 1);
+      mbar_init(accfull_bar(b), 1);
+      mbar_init(accfree_bar(b), kOConv);
     }
     mbar_init(done_bar, 1);
     *abort_flag = 0;
@@ -1074,8 +1080,12 @@ __global__ void __launch_bounds__(kOThreads, RP <= 32 ? 2 : 1)
       int i = 0;
       for (int c = s0; c < s1; ++c) {
         const uint32_t b = (c - s0) & 1u, use = (c - s0) >> 1;
+        const int g = (c - s0) / kOChain, acc = g % C::NACC;
+        const bool first = (c - s0) % kOChain == 0;
         // The converters of a stage have seen its X.
-        if (!mbar_wait(full_bar(s), ph, timeout_ns, a.seg.status, abort_flag) ||
+        if ((first && !mbar_wait(accfree_bar(acc), ((g / C::NACC) & 1u) ^ 1u, timeout_ns,
+                                 a.seg.status, abort_flag)) ||
+            !mbar_wait(full_bar(s), ph, timeout_ns, a.seg.status, abort_flag) ||
             !mbar_wait(vready_bar(b), use & 1u, timeout_ns, a.seg.status, abort_flag))
           break;
         tc_fence_after();
@@ -1090,21 +1100,21 @@ __global__ void __launch_bounds__(kOThreads, RP <= 32 ? 2 : 1)
                 smem_desc_mn_sw128(x + 2 * m * C::kBox + k * 2048, C::kBox);
 #pragma unroll
             for (int t = 0; t < 3; ++t)
-              umma_bf16(tmem_base +
-                            ((t == 0 ? (c - s0) % C::NACC : C::NACC) * 2 + m) * RP,
-                        ad, smem_desc_k128_sw128(v + t * C::kTerm) + 2u * k, idesc,
-                        (k > 0 || t > 1 || c - s0 >= (t == 0 ? C::NACC : 1)) ? 1u
-                                                                            : 0u);
+              umma_bf16(tmem_base + ((t == 0 ? acc : C::NACC) * 2 + m) * RP, ad,
+                        smem_desc_k128_sw128(v + t * C::kTerm) + 2u * k, idesc,
+                        (k > 0 || t > 1 || (t == 0 ? !first : c > s0)) ? 1u : 0u);
           }
         umma_commit(empty_bar(s));
         umma_commit(vfree_bar(b));
+        if ((c - s0) % kOChain == kOChain - 1 || c + 1 == s1)
+          umma_commit(accfull_bar(acc));
         if (++s == C::STAGES) { s = 0; ph ^= 1u; }
       }
       umma_commit(done_bar);
       mbar_wait_drain(done_bar, 0, timeout_ns, a.seg.status);
     }
   } else {
-    // -------------------------------------------- converters, then epilogue
+    // --------------------------------------------- converters and epilogue
     // A unit is one rank's 8 rows: 16 bytes of each term.
     constexpr int kUnits = RP * 8 / (32 * kOConv);
     static_assert(RP * 8 >= 32 * kOConv || RP == 16, "units");
@@ -1125,6 +1135,37 @@ __global__ void __launch_bounds__(kOThreads, RP <= 32 ? 2 : 1)
           w[u][q] = t + q < n && j < a.R && e < RP * 8 ? __ldcg(p + q * o.ldw) : 0.0f;
       }
     };
+    // Thread = column of X; the two halves of the warps have a block each.  A chain
+    // is added up while the second stage after it is multiplied, so that they
+    // rarely wait for it, or the first, where the MMA waits for them.
+    float sum[RP];
+#pragma unroll
+    for (int j = 0; j < RP; ++j) sum[j] = 0.0f;
+    const int m = warp >> 2;
+    const uint32_t t_addr =
+        tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16) + m * RP;
+    auto add = [&](int acc) {
+#pragma unroll
+      for (int j = 0; j < RP; j += 16) {
+        float v[16];
+        tmem_ld16(t_addr + acc * 2 * RP + j, v);
+#pragma unroll
+        for (int q = 0; q < 16; ++q) sum[j + q] += v[q];
+      }
+    };
+    auto add_chain = [&](int g) {
+      const int acc = g % C::NACC;
+      const bool ready = mbar_wait(accfull_bar(acc), (g / C::NACC) & 1u, timeout_ns,
+                                   a.seg.status, abort_flag);
+      if (!__all_sync(0xffffffffu, ready)) return false;
+      tc_fence_after();
+      add(acc);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(accfree_bar(acc));
+      return true;
+    };
+    int added = 0;
     load_v(s0);
     bool ok = true;
     for (int c = s0; c < s1; ++c) {
@@ -1174,37 +1215,28 @@ __global__ void __launch_bounds__(kOThreads, RP <= 32 ? 2 : 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(vready_bar(b));
+      if (c - s0 == (added + 1) * kOChain + C::NACC - 1) {
+        if (!add_chain(added)) {
+          ok = false;
+          break;
+        }
+        ++added;
+      }
     }
-    // Thread = column of X; the two halves of the warps have a block each.
-    const bool ready =
-        ok && mbar_wait(done_bar, 0, timeout_ns, a.seg.status, abort_flag);
-    if (__all_sync(0xffffffffu, ready)) {
-      tc_fence_after();
-      const int m = warp >> 2;
+    const int chains = (s1 - s0 + kOChain - 1) / kOChain;
+    for (; ok && added < chains; ++added) ok = add_chain(added);
+    // The ring is free, as the last MMA is done: the sums go there.
+    if (ok) {
+      if (chains > 0) add(C::NACC);
       const int cc = 128 * m + 32 * (warp & 3) + lane;
-      const uint32_t t = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16) + m * RP;
       float *red = reinterpret_cast<float *>(sbase);
 #pragma unroll
-      for (int j = 0; j < RP; j += 16) {
-        float sum[16];
-#pragma unroll
-        for (int q = 0; q < 16; ++q) sum[q] = 0.0f;
-        // The small terms first.
-        for (int n = min(C::NACC, s1 - s0); s1 > s0 && n >= 0; --n) {
-          float v[16];
-          tmem_ld16(t + (n == min(C::NACC, s1 - s0) ? C::NACC : n) * 2 * RP + j, v);
-#pragma unroll
-          for (int q = 0; q < 16; ++q) sum[q] += v[q];
-        }
-#pragma unroll
-        for (int q = 0; q < 16; ++q) {
-          const float g = sum[q];
-          if (csize > 1)
-            red[(j + q) * C::kLdR + cc] = g;
-          else if (j + q < a.R && col0 + cc < o.N)
-            o.G[(static_cast<int64_t>(adapter) * a.R + j + q) * o.N + col0 + cc] =
-                g * scale;
-        }
+      for (int j = 0; j < RP; ++j) {
+        if (csize > 1)
+          red[j * C::kLdR + cc] = sum[j];
+        else if (j < a.R && col0 + cc < o.N)
+          o.G[(static_cast<int64_t>(adapter) * a.R + j) * o.N + col0 + cc] =
+              sum[j] * scale;
       }
     }
   }

@@ -44,6 +44,9 @@ def off(got, want):
     (300, 32, 8190, 1002),          # rows that TMA cannot read
     (5000, 8, 8190, 70),
     (20480, 24, 8192, 64),
+    (32768, 16, 4096, 4096),        # many rows
+    (32768, 128, 4096, 1024),
+    (131072, 32, 256, 64),
 ])
 def test_one_long_segment(T, R, K, N, xt):
     import torch
