@@ -328,8 +328,8 @@ FP8LA_API fp8la_status fp8_grouped_gemm(int32_t num_groups, const int32_t *m_off
  *
  * logits: fp32 or bf16 (dtype, FP8LA_TYPE_*) [tokens][ld], ld >= E; ids:
  * int32 and weights: fp32 [tokens][top_k]; m_offsets: int32 [E + 1]; order:
- * int32 [tokens * top_k].  1 <= top_k <= min(E, 16), E <= 1024 (beyond:
- * FP8LA_ERR_UNSUPPORTED).  workspace: fp8_moe_route_workspace_bytes(tokens,
+ * int32 [tokens * top_k].  1 <= top_k <= min(E, 16), E <= 1024, tokens * top_k
+ * < 2^31 - 2^16 (beyond: FP8LA_ERR_UNSUPPORTED).  workspace: fp8_moe_route_workspace_bytes(tokens,
  * E) bytes, 4-byte aligned, needed only for the sort, which takes up to 2^23
  * pairs (beyond: FP8LA_ERR_UNSUPPORTED may follow); it keeps nothing between
  * calls.  One launch, or two for a sort of more than 128 tokens.

@@ -347,7 +347,8 @@ extern "C" fp8la_status fp8_moe_route(
     return FP8LA_ERR_INVALID_ARG;
   if (num_experts > kMaxExperts || top_k > kMaxTopK)
     return FP8LA_ERR_UNSUPPORTED;
-  if (tokens >= (int64_t(1) << 31) / top_k) return FP8LA_ERR_UNSUPPORTED;
+  // Token and pair numbers, and those that a loop's last step passes, are 32-bit.
+  if (tokens >= ((int64_t(1) << 31) - 65536) / top_k) return FP8LA_ERR_UNSUPPORTED;
   if (tokens > 0 && (!logits || !ids || !weights || (m_offsets && !order)))
     return FP8LA_ERR_INVALID_ARG;
   const bool sort = m_offsets != nullptr;
