@@ -414,6 +414,9 @@ FP8LA_API fp8la_status fp8_moe_layer(
  * write no output and record FP8LA_ERR_DEVICE_ARG.
  * fp32 operands enter the tensor cores as sums of bf16 terms: three (24
  * significant bits) for v, two (16) for out; sums are fp32, in a fixed order.
+ * Values that are not finite, fp32 ones beyond bf16's +-3.39e38 among them, make
+ * the outputs that they reach infinite or NaN, and no others; which of the two
+ * is not specified.
  * Pointers need their type's alignment; 16-byte rows are read and written
  * fastest.  Below 128 rows the result does not depend on the alignment; from
  * there on rows at other addresses are added in another order.

@@ -174,3 +174,71 @@ def test_values_that_are_not_finite(value):
         for got, want in zip((o, w, dx, dA, dB), (o0, v0) + g0):
             assert torch.equal(got, want)
     assert fl.device_status() == 0
+
+
+@pytest.mark.parametrize("xt", ["bfloat16", "float32"])
+@pytest.mark.parametrize("T,lengths,ids,R,K,N", [
+    (70, [3, 0, 17, 16, 30], [1, 0, -1, 1, 0], 8, 72, 96),
+    (ROWS, LENGTHS, IDS, 32, 264, 4104),
+    (ROWS, LENGTHS, IDS, 32, 4104, 264),
+])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_factors_that_are_not_finite(T, lengths, ids, R, K, N, xt, value):
+    """An element of A reaches its rank of V and all of out in its adapter's rows,
+    one of B its column of out and all of dx; other rows, columns and adapters are
+    as before bit for bit."""
+    import torch
+    fl = lib()
+    c = make(T, lengths, ids, 3, R, K, N, xt=xt)
+    v = random_v(c)
+    mine = torch.zeros(T, dtype=torch.bool, device="cuda")
+    for lo, hi, i in segments(c):
+        if i == 1:
+            mine[lo:hi] = True
+    o0, v0 = apply(fl, c)
+    g0 = backward(fl, c, v)
+    d = dict(c, A=c["A"].clone())
+    d["A"][1, 5, 66] = value
+    o, w = apply(fl, d)
+    assert not torch.isfinite(w[mine, 5]).any() and not torch.isfinite(o[mine]).any()
+    assert torch.equal(o[~mine], o0[~mine]) and torch.equal(w[~mine], v0[~mine])
+    w[:, 5] = v0[:, 5]
+    assert torch.equal(w, v0)
+    dx, dA, dB = backward(fl, d, v)
+    assert not torch.isfinite(dx[mine, 66]).any()
+    dx[:, 66] = g0[0][:, 66]
+    for a, b in zip((dx, dA, dB), g0):
+        assert torch.equal(a, b)
+    d = dict(c, B=c["B"].clone())
+    d["B"][1, 5, 66] = value
+    o, w = apply(fl, d)
+    assert not torch.isfinite(o[mine, 66]).any() and torch.equal(w, v0)
+    o[:, 66] = o0[:, 66]
+    assert torch.equal(o, o0)
+    dx, dA, dB = backward(fl, d, v)
+    assert not torch.isfinite(dx[mine]).any() and not torch.isfinite(dA[1, 5]).any()
+    assert torch.equal(dx[~mine], g0[0][~mine]) and torch.equal(dB, g0[2])
+    dA[1, 5] = g0[1][1, 5]
+    assert torch.equal(dA, g0[1])
+    assert fl.device_status() == 0
+
+
+@pytest.mark.parametrize("T,lengths", [(40, [20, 20]), (700, [300, 400])])
+def test_fp32_beyond_bf16(T, lengths):
+    """FP32's largest values are infinite to an adapter; BF16's are not."""
+    import torch
+    fl = lib()
+    c = make(T, lengths, [0, 0], 1, 16, 264, 128, xt="float32")
+    c["A"] *= 2.0 ** -20
+    c["B"] *= 2.0 ** -120
+    top = torch.finfo(torch.float32).max
+    c["x"][3, 7] = top
+    c["x"][4, 7] = -top
+    c["x"][25, 8] = float(torch.finfo(torch.bfloat16).max)
+    out, v = apply(fl, c)
+    assert not torch.isfinite(v[3:5]).any()
+    keep = torch.ones(T, dtype=torch.bool, device="cuda")
+    keep[3:5] = False
+    assert torch.isfinite(v[keep]).all() and torch.isfinite(out[keep].float()).all()
+    want = c["x"][25].double() @ c["A"][0].double().t()
+    assert ((v[25].double() - want).abs() <= 2.0 ** -20 * want.abs()).all()
