@@ -19,9 +19,10 @@
 // FMAs; X and Y are read and written once, and the factors, V and the sums
 // are small enough to stay on the chip.  The products are mma.sync m16n8k16
 // with fragments from shared memory, filled by cp.async several stages ahead
-// (shrink, outer), or straight from registers (expand, where a warp keeps its
-// 64 columns of the factor and streams rows past them: output columns are
-// dealt out so that each lane owns 16 consecutive ones).  Sums over a long
+// (shrink, outer).  In expand a warp keeps its 32 columns of the factor in
+// registers and streams rows past them, V from shared memory and base through a
+// ring of its own; output columns are dealt out so that each lane owns 8
+// consecutive ones.  Sums over a long
 // axis (K in shrink, rows in outer) are shared out over a cluster of CTAs and
 // added through distributed shared memory in rank order.
 //
@@ -29,14 +30,17 @@
 // operand (x or dy given as FP32, v and dv always) enters as a sum of BF16
 // terms: three (24 significant bits) where the output is FP32, so that it is
 // as good as an FP32 product's, two (relative error 2^-17) where it is
-// rounded to BF16.  base is the first term of its sum, which is rounded
-// once.
+// rounded to BF16.  base is a term of that FP32 sum, which is rounded once.
+// The tensor cores cut off a little of a running sum with each addition, always
+// towards zero, so V's and the gradients' sums are made of short ones that are
+// added with rounding, here of 16 products and in lora_tma.cu of 16 steps:
+// whatever the length, they stay as good as an FP32 product's.
 //
-// Measured on the stream: forward 9.7 us for 8 rows of their own, rank 16, 4096
+// Measured on the stream: forward 9.8 us for 8 rows of their own, rank 16, 4096
 // -> 4096 (the call's host side takes longer).  The outer sums of FP32 rows
-// cost six MMAs a step here: 4096 rows, rank 32, 8192 -> 8192, 219 us backward
+// cost six MMAs a step here: 4096 rows, rank 32, 8192 -> 8192, 221 us backward
 // (413 MB, 1.9 TB/s).  BF16 rows at odd addresses are copied element by element:
-// 3000 rows, rank 48, 6099 -> 4103, 178 us forward, 80 at even ones.
+// 3000 rows, rank 48, 6099 -> 4103, 177 us forward, 87 at even ones.
 #include <cuda_bf16.h>
 
 #include "lora.cuh"
@@ -935,9 +939,9 @@ fp8la_status launch_expand(const ExpandArgs &a, cudaStream_t s) {
   // Chunks of 16 rows, a segment to a CTA, spread few short segments over the
   // SMs; with more, loading a factor for each costs more.  Measured, us for a
   // forward pass with chunks of 16 / 128, 4096 -> 4096, rank 16: 8 segments of one
-  // row 9.7 / 22.1, 64 of one 24.3 / 40.6, 256 of one 61.9 / 52.4, 1024 of one
-  // 218 / 160, 64 of 4 24.3 / 22.5; rank 64: 64 of one 35.5 / 84.3, 256 of one
-  // 111.6 / 112.9, 1024 of one 416 / 386, 64 of 16 44.5 / 46.8.
+  // row 9.8 / 22.2, 64 of one 24.1 / 40.5, 256 of one 62.5 / 53.2, 1024 of one
+  // 220 / 162, 64 of 4 24.3 / 23.1; rank 64: 64 of one 35.6 / 84.9, 256 of one
+  // 101.5 / 100.5, 1024 of one 395 / 367, 64 of 16 33.4 / 32.5.
   return a.seg.T < 256 && short_segments(a.seg.T, a.seg.S)
              ? launch_expand_ch<16>(a, 46, s)
              : launch_expand_ch<128>(a, 50, s);
@@ -966,9 +970,10 @@ fp8la_status launch_outer(const OuterArgs &a, int slot, cudaStream_t s) {
 // Fewest rows for tcgen05 in shrink and outer: a whole tile.  Below, every call
 // takes mma.sync, so that a small call's result does not depend on how its rows
 // are aligned.  That has a price: 90 rows in two segments, rank 20, 2048 ->
-// 2048, take 14.8 us forward and 27.8 backward, with tcgen05 13.4 and 21.0; 8 rows
-// of their own, rank 64, 12.4 and 32.3 against 11.9 and 26.3.  128 rows, rank 16,
-// 4096 -> 4096: 12.0 and 24.2 with mma.sync, 10.3 and 16.6 with tcgen05.
+// 2048, take 15.0 us forward and 27.6 backward, with tcgen05 13.3 and 21.1; 8 rows
+// of their own, rank 64, 4096 -> 4096, 15.6 and 46.8 against 12.8 and 34.2.  128
+// rows, rank 16, 4096 -> 4096: 12.3 and 24.4 with mma.sync, 10.7 and 18.2 with
+// tcgen05.
 constexpr int64_t kTmaRows = 128;
 
 constexpr int64_t kMaxWidth = int64_t(1) << 22;  // grid limits
@@ -1015,16 +1020,17 @@ fp8la_status run_shrink(const Segments &seg, const void *X, int32_t dtype,
   // BF16 rows that TMA can read go to tcgen05, but for short segments of few
   // ranks, whose 128-row tiles are mostly empty.  Measured, us for a forward
   // pass with mma.sync / tcgen05 here, 4096 -> 4096: 256 segments of one row, rank
-  // 16: 61.9 / 67.5, rank 32: 83.3 / 77.8, rank 64: 111.6 / 97.5; 64 of 16, rank
-  // 16: 22.1 / 22.8, rank 32: 33.6 / 26.1, rank 64: 44.5 / 32.8.
+  // 16: 52.7 / 61.8, rank 32: 78.5 / 76.0, rank 64: 115.2 / 100.5; 1024 of one, rank
+  // 16: 162 / 220, rank 32: 258 / 274, rank 64: 394 / 367; 64 of 16, rank 16: 20.9 /
+  // 21.5, rank 32: 33.0 / 25.4, rank 64: 47.7 / 32.6.
   if (dtype == FP8LA_TYPE_BF16 && a.x_unit == 16 && a.p_unit == 16 &&
       seg.T >= kTmaRows && (R > 16 || !short_segments(seg.T, seg.S)))
     return launch_shrink_tma(a, s);
   // FP32 rows: splitting a tile costs the same however few of its rows count.
-  // mma.sync / tcgen05, 4096 -> 4096: 4 segments, 1024 rows, rank 16: 22.2 / 19.2,
-  // rank 64: 39.2 / 25.1, 4096 rows, rank 16: 49.2 / 39.1, rank 64: 82.1 / 46.5;
-  // 128 rows, rank 16: 16.4 / 16.5, rank 64: 29.7 / 21.5; rank 64, 64 segments of
-  // 16: 55.4 / 52.9, 256 of one: 125 / 175.
+  // mma.sync / tcgen05, 4096 -> 4096: 4 segments, 1024 rows, rank 16: 22.0 / 19.5,
+  // rank 64: 39.0 / 24.8, 4096 rows, rank 16: 50.5 / 39.2, rank 64: 82.4 / 46.7;
+  // 128 rows, rank 16: 15.6 / 16.5, rank 64: 28.9 / 21.2; rank 64, 64 segments of
+  // 16: 54.9 / 57.0, 256 of one: 128 / 187.
   if (dtype == FP8LA_TYPE_F32 && a.x_unit == 16 && a.p_unit == 16 &&
       seg.T >= kTmaRows && !short_segments(seg.T, seg.S))
     return launch_shrink_f32(a, s);
@@ -1058,11 +1064,11 @@ fp8la_status run_expand(const Segments &seg, const float *V, int64_t ldv, int32_
   // tcgen05 takes 128 rows x 256 columns at a time, wants many such tiles to
   // hide its start, and saves what mma.sync pays for each rank.  Measured, us for
   // a forward pass (K = 1024) with mma.sync / tcgen05 here: rank 16, 4096 x 4096:
-  // 23.3 / 24.4, x 10240: 41.6 / 42.8; rank 32, 2048 x 4096: 19.1 / 19.0, x 8192:
-  // 27.4 / 25.4, 1024 x 8192: 18.0 / 20.9, 4096 x 4096 in 64 segments: 30.9 /
-  // 32.9; rank 64, 2048 x 4096: 25.7 / 22.4, 4096 x 4096: 36.5 / 30.1, 1024 x
-  // 8192: 23.9 / 24.4, 4096 x 4096 in 64 segments: 43.1 / 38.2, 2048 x 4096 in 64
-  // (K = 4096): 38.0 / 41.3.
+  // 23.2 / 25.1, x 10240: 41.9 / 43.4; rank 32, 2048 x 4096: 18.9 / 19.0, x 8192:
+  // 27.2 / 25.1, 1024 x 8192: 17.8 / 20.8, 4096 x 4096 in 64 segments: 31.1 /
+  // 33.2; rank 64, 2048 x 4096: 25.6 / 22.4, 4096 x 4096: 36.3 / 30.5, 1024 x
+  // 8192: 23.7 / 24.3, 4096 x 4096 in 64 segments: 42.9 / 38.5, 2048 x 4096 in 64
+  // (K = 4096): 38.9 / 41.9.
   if (a.base_unit == 16 && a.out_unit == 16 && a.p_unit == 16 && R > 16 &&
       R <= 64 && seg.T >= 64 * static_cast<int64_t>(seg.S) && seg.T >= 2048 &&
       seg.T * N >= int64_t(2048) * 4096)
@@ -1173,9 +1179,9 @@ extern "C" fp8la_status fp8la_lora_backward(
   o.alpha = alpha;
   o.R = rank;
   // BF16 rows that TMA can read.  Measured, us for a backward pass with
-  // mma.sync / tcgen05 here, 4096 x 4096, rank 16: 256 segments of one row 136 /
-  // 108, 1024 of one 471 / 383, 64 of 16 52.7 / 37.0; rank 64: 256 of one 233 /
-  // 210, 64 of 16 100 / 84.
+  // mma.sync / tcgen05 here, 4096 x 4096, rank 16: 256 segments of one row 129 /
+  // 102, 1024 of one 419 / 334, 64 of 16 51.9 / 36.1; rank 64: 256 of one 221 /
+  // 206, 64 of 16 89 / 75.
   if (rows >= kTmaRows && !o.side[0].x_f32 && !o.side[1].x_f32 &&
       o.side[0].x_unit == 16 && o.side[1].x_unit == 16) {
     st = launch_outer_tma(o, s);

@@ -9,7 +9,8 @@
 //
 // shrink: D[128 rows][R] += X[128][64 k] P[R][64 k]^T, both K-major.  K is
 // shared out over a cluster, whose CTAs' sums are added through distributed
-// shared memory in rank order.
+// shared memory in rank order.  A CTA's sum is made of short ones of 16 steps
+// (kChain), in two accumulators in turn.
 //
 // expand: D[128 rows][256 columns] = V[128][R] P[R][256 columns], V split into
 // two BF16 terms by converter warps (K-major), P as TMA writes it (MN-major).
@@ -21,21 +22,22 @@
 // outer: D[128 columns][R] += X[t][128 columns]^T V[t][R], t being the MMA's
 // K.  X is the transposed (MN-major) operand, just as TMA writes a box of 64
 // columns x 64 rows.  V (FP32) enters as three BF16 terms, which converter
-// warps write K-major ([R][64 t]); all three are accumulated into the same
-// columns.  Rows past a segment's end belong to other requests and may hold
-// anything, so the converters overwrite those that a 16-row MMA step would
-// touch with zeros.
+// warps write K-major ([R][64 t]).  The first term's sums are short ones, as in
+// shrink; the other two, 2^-8 of it or less, have an accumulator to themselves.
+// Rows past a segment's end belong to other requests and may hold anything, so
+// the converters overwrite those that a 16-row MMA step would touch with zeros.
 //
 // Measured, caches cold, each kernel by itself: shrink of 4096 x 8192, rank 64,
-// 23.5 us (70 MB read, 3.0 TB/s, tensor pipe 7 %: 148 CTAs, one wave, whose start
-// and join are half of it); expand to 4096 x 10240, rank 64, 38.8 us (168 MB in
-// and out, 4.3 TB/s); outer of 4096 x 8192 twice, rank 32, three adapters, 47.9 us
-// (135 MB, 2.8 TB/s, tensor pipe 11 %): its stages of 32 KB take 1.4 us each, 1.1
-// of it from operands to the commit, because X as the transposed M side of the
-// MMA runs at half rate.  X as the N side and equal shares of all stages for the
-// SMs stream at HBM's rate, but start, drain and join for 5 us each: 105 us
-// against 97 for that backward pass, 139 against 145 at rank 64, 6 to 27 us more
-// for smaller ones, so the simpler form stays.
+// 23.2 us (70 MB read, 3.0 TB/s, tensor pipe 7.5 %: 148 CTAs, one wave, whose start
+// and join are half of it); expand to 4096 x 10240, rank 64, 37.6 us (168 MB in
+// and out, 4.5 TB/s); outer of 4096 x 8192 twice, rank 32, three adapters, 51.9 us
+// (135 MB, 2.6 TB/s, tensor pipe 10 %).  Of outer with one long chain, 47.9 us:
+// its stages of 32 KB took 1.4 us each, 1.1 of it from operands to the commit,
+// because X as the transposed M side of the MMA runs at half rate.  X as the N
+// side and equal shares of all stages for the SMs streamed at HBM's rate, but
+// start, drain and join for 5 us each: 105 us against 97 for that backward pass,
+// 139 against 145 at rank 64, 6 to 27 us more for smaller ones, so the simpler
+// form stays.
 #include "lora.cuh"
 
 namespace fp8la {
@@ -914,7 +916,7 @@ constexpr int kOThreads = 32 * (kOConv + 2);
 constexpr int kOCols = 256;         // two MMA blocks of 128
 constexpr int kORows = 64;          // of a stage
 // Stages of an accumulator, see kChain.  4, 8 and 16 take 102.3, 101.8 and 101.5 us
-// for the backward pass named above and leave 4.3e-7, 6.6e-7 and more of dA.
+// for the backward pass of outer's figure above; 4 leave 4.3e-7 of dA, 8 6.6e-7.
 constexpr int kOChain = 4;
 
 template <int RP>

@@ -46,14 +46,15 @@
 // warp 9 MMA issuer.
 //
 // Measured on the stream, the four launches with the router's, 2 of 8 experts of
-// 4096 x 14336: 78 us for 1 token (352 MB, 4.5 TB/s), 254 us for 128 tokens (1.41
-// GB, 5.5 TB/s); 8 of 64 of 2048 x 1408, 24 tokens: 110 us (4.8 TB/s).  Time
-// stamps in the kernels, 1 / 24 / 128 tokens: first codes at 13 / 12 / 11 us,
-// gate/up's MMAs until 44 / 59 / 152 in the mean CTA (its weights at 7.5, 7.5, 6.7
-// TB/s), down's from 52 / 72 / 165 to 67 / 95 / 237 (the last: 6.6 TB/s), end of
-// combine at 73 / 103 / 243.  So the weights stream at HBM's rate, and what is
-// left over it is the start (cold code and ids) and the gap in which the last
-// parts of h are joined.
+// 4096 x 14336: 80 us for 1 token (352 MB, 4.4 TB/s), 270 us for 128 tokens (1.41
+// GB, 5.2 TB/s); 8 of 64 of 2048 x 1408, 24 tokens of FP32: 115 us (4.6 TB/s).
+// Time stamps in the kernels, 1 / 24 / 128 tokens: first codes at 14 / 12 / 12 us,
+// gate/up's MMAs until 46 / 67 / 153 in the mean CTA (its weights at 7.5, 6.5, 6.7
+// TB/s), down's from 54 / 75 / 167 to 72 / 103 / 252 (6.6, 6.5, 5.5 TB/s), end of
+// combine at 77 / 109 / 258.  What is left over the weights' time is the start
+// (cold code and ids) and the gap in which the last parts of h are joined.  Four
+// terms instead of two cost 77 -> 80, 109 -> 115 and 254 -> 270 us: fewer stages of
+// weights fit beside the codes.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -941,12 +942,13 @@ int64_t positions(int64_t pairs, int64_t E) {
   return round16(pairs + 3 * (E < pairs ? E : pairs) + kSlack);
 }
 
-// Tokens of a tile.  Tiles of 16 leave more of shared memory to the weight
-// ring (6 stages against 4) but read the weights of an expert with more
-// tokens again, from L2.  Measured, us for a layer with tiles of 16 / of 64,
-// by the mean number of tokens of an expert: 3 (24 tokens, 8 of 64 experts)
-// 115 / 130; 8 (64 tokens) 124 / 138; 8 (32 tokens, 2 of 8) 139 / 146; 16 (64
-// tokens, 2 of 8) 185 / 152; 16 (128 tokens, 8 of 64) 147 / 148.
+// Tokens of a tile.  Tiles of 16 leave more of shared memory to the weight ring
+// (5 or 6 stages against 3 or 4) but read the weights of an expert with more
+// tokens again, from L2.  Measured, us for a layer with tiles of 16 / of 64, by the
+// mean number of tokens of an expert, BF16 x, then FP32: 3 (24 tokens, 8 of 64
+// experts) 113 / 122, 116 / 126; 8 (64 tokens) 121 / 131, 124 / 134; 8 (32 tokens, 2
+// of 8) 137 / 139, 139 / 146; 16 (64 tokens, 2 of 8) 188 / 143, 194 / 152; 16 (128
+// tokens, 8 of 64) 154 / 145, 167 / 144.
 int tile_tokens(int64_t T, int64_t k, int64_t E) {
   return T <= 16 || T * k <= 8 * E ? 16 : 64;
 }
