@@ -83,7 +83,8 @@ typedef int fp8la_status;
 #define FP8LA_ERR_DEVICE_ARG     -6  /* a kernel found a device-side argument it
                                         cannot use (m_offsets of fp8_grouped_gemm or
                                         fp8_quantize_pertensor_grouped, ids of
-                                        fp8_moe_layer, segments of fp8la_lora_*) */
+                                        fp8_moe_layer, segments of fp8la_lora_* and
+                                        fp8_kv_*, pages of fp8_kv_*) */
 
 /*
  * Per-tensor E4M3 quantisation ([P1] risks paragraph: E4M3 spans +-448 and
@@ -461,6 +462,122 @@ FP8LA_API fp8la_status fp8la_lora_backward(
     const uint16_t *dx_base, int64_t ld_dx_base, uint16_t *dx, int64_t ld_dx,
     float *dA, float *dB, void *workspace, int64_t workspace_bytes,
     fp8la_stream_t stream);
+
+/*
+ * A paged key/value cache of FP8 codes, owned by the caller.  Token `place` of
+ * page p, head h, has its D codes of K at k + p * page_stride + h * head_stride
+ * + place * token_stride, contiguous, and their scale at k_scale + p *
+ * scale_page_stride + h * scale_head_stride + place * scale_token_stride; V alike.
+ * A value is code * scale.  Strides are in elements (a page may hold its heads
+ * outside its tokens or the other way round), and a dimension of one element may
+ * have any.  k, v 16-byte aligned, with strides that are multiples of 16.
+ * head_dim: a multiple of 16 up to 256; page_size: any, up to 2^30; kv_heads <=
+ * 1024 (beyond these: FP8LA_ERR_UNSUPPORTED).  The struct itself is on the host and
+ * is read during the call only; what it points to is on the device.
+ *
+ * The calls below share how sequences are named.  Their rows come in segments:
+ * segment s, the rows m_offsets[s] .. m_offsets[s+1]-1, are the LAST rows of
+ * sequence s, whose length, with these rows, is kv_lens[s]: row i of n stands at
+ * position kv_lens[s] - n + i.  Position j of sequence s lies in page
+ * page_table[s * ld_table + j / page_size], at place j % page_size.  m_offsets:
+ * int32 [num_segments + 1], starting at 0, non-decreasing, at most `rows`;
+ * kv_lens: int32 [num_segments], at most max_pages * page_size; page_table: int32
+ * [num_segments][ld_table], max_pages entries of a row at most, of which only those
+ * below kv_lens[s] are read.  All on the device; the host reads none of it, so a
+ * captured step can be replayed for other lengths.  Offsets and lengths that break
+ * these rules make the call write nothing and record FP8LA_ERR_DEVICE_ARG; a page
+ * outside 0 .. num_pages-1 records it, too, and nothing is read or written there.
+ * Rows after the last segment are neither read nor written.  Segments may be
+ * empty.  num_segments <= 1024, rows < 2^31.
+ */
+typedef struct fp8la_kv_cache {
+  uint8_t *k, *v;
+  float *k_scale, *v_scale;
+  int64_t num_pages;
+  int32_t page_size, kv_heads, head_dim, format;  /* FP8LA_FORMAT_* */
+  int64_t page_stride, head_stride, token_stride;
+  int64_t scale_page_stride, scale_head_stride, scale_token_stride;
+} fp8la_kv_cache;
+
+/*
+ * Quantises rows of K and V into the cache.  Each (row, head) is quantised as
+ * fp8_quantize_pertensor_ex quantises a tensor: scale = fp32(amax / fmax), codes
+ * RNE and saturating (amax 0 or fmax / amax not finite: scale 1).  k, v: fp32 or
+ * bf16 (dtype) [rows][kv_heads][head_dim], rows ld and heads ld_head elements apart,
+ * e.g. slices of a fused projection; 16-byte rows are read fastest.  Needs
+ * kv_lens[s] >= the segment's rows.  Nothing else in the cache changes.  Rows that
+ * name a page outside the cache are left out.  Two rows that name the same place
+ * leave it undefined.  One launch.
+ */
+FP8LA_API fp8la_status fp8_kv_append(
+    const void *k, int64_t ld_k, int64_t ld_k_head, const void *v, int64_t ld_v,
+    int64_t ld_v_head, int32_t dtype, int64_t rows, int64_t num_segments,
+    const int32_t *m_offsets, const int32_t *kv_lens, const int32_t *page_table,
+    int64_t ld_table, int64_t max_pages, const fp8la_kv_cache *cache,
+    fp8la_stream_t stream);
+
+/*
+ * Reads rows back: k[row][head][i] = fp32(code * scale), rounded to bf16 where
+ * dtype says so.  The rows are those that fp8_kv_append with the same arguments
+ * writes (all of a sequence: a segment of kv_lens[s] rows).  k, v must not overlap
+ * each other or the cache.  Rows whose page is outside the cache are not written.
+ */
+FP8LA_API fp8la_status fp8_kv_read(
+    void *k, int64_t ld_k, int64_t ld_k_head, void *v, int64_t ld_v,
+    int64_t ld_v_head, int32_t dtype, int64_t rows, int64_t num_segments,
+    const int32_t *m_offsets, const int32_t *kv_lens, const int32_t *page_table,
+    int64_t ld_table, int64_t max_pages, const fp8la_kv_cache *cache,
+    fp8la_stream_t stream);
+
+/*
+ * Attention of packed sequences over the cache, from one decoding token a
+ * sequence to whole prompts (append the rows first, then call this):
+ *
+ *   x_j    = scale * sum_i q[t][h][i] K_j[i]
+ *   out[t] = bf16_rn( sum_j exp(x_j) V_j / sum_j exp(x_j) ),
+ *   lse[t] = log sum_j exp(x_j)
+ *
+ * over the positions j of the row's sequence: with causal != 0 those up to its
+ * own, else all kv_lens[s].  Query head h reads K/V head h / (num_heads /
+ * kv_heads).  A row that sees nothing (no tokens, or causal with kv_lens[s] below
+ * the segment's rows) gets out = 0 and lse = -inf.
+ *
+ * With prefix_len (one int32 on the device), every sequence begins with the same
+ * prefix_len tokens, in the pages prefix_table[0 .. prefix_pages-1]; kv_lens and
+ * page_table then name what follows them, and every row sees the whole prefix.
+ * All sequences' rows go through the prefix together, so that it is read once.
+ *
+ * q: fp32 or bf16 [rows][num_heads][head_dim], rows ld_q and heads ld_q_head
+ * elements apart; out: bf16, likewise; lse: fp32 [rows][ld_lse], or NULL.
+ * max_rows: the rows of the longest segment, or more (`rows`, if nothing better is
+ * known): it chooses the kernels, and a segment with more makes the call write
+ * nothing and record FP8LA_ERR_DEVICE_ARG.  num_heads a multiple of kv_heads, rows *
+ * num_heads < 2^31 - 2^20.
+ *
+ * Sums are FP32.  Codes enter the tensor cores exactly, q with an error of at most
+ * 2^-22 of an element (fp32) or none (bf16), but 2^-33 of the row's largest where
+ * that is more; the weights exp(x_j) are rounded to 11 bits (and below 2^-21 of the
+ * row's largest weight times V's scale to 2^-32 of it).  A token makes the rows that
+ * see it NaN if its K or K's scale is not finite (but counts for nothing where its
+ * score is -inf), if its V's scale is not a positive finite number, or if its page is
+ * outside the cache; a V that is not finite makes that element of those rows infinite
+ * or NaN, which of the two is not specified.  No others change.  Places beyond a sequence's
+ * end may hold anything.  The result does not depend on timing.  workspace:
+ * fp8_kv_attention_workspace_bytes(rows, num_heads, head_dim, prefix_len != NULL)
+ * bytes, 16-byte aligned; it keeps nothing between calls, but calls that may run at
+ * the same time need one each.
+ */
+FP8LA_API int64_t fp8_kv_attention_workspace_bytes(int64_t rows, int32_t num_heads,
+                                         int32_t head_dim, int32_t prefix);
+FP8LA_API fp8la_status fp8_kv_attention(
+    const void *q, int32_t q_dtype, int64_t ld_q, int64_t ld_q_head,
+    int32_t num_heads, int64_t rows, int64_t num_segments,
+    const int32_t *m_offsets, const int32_t *kv_lens, const int32_t *page_table,
+    int64_t ld_table, int64_t max_pages, int64_t max_rows,
+    const int32_t *prefix_table, int64_t prefix_pages, const int32_t *prefix_len,
+    const fp8la_kv_cache *cache, float scale, int32_t causal, uint16_t *out,
+    int64_t ld_out, int64_t ld_out_head, float *lse, int64_t ld_lse,
+    void *workspace, int64_t workspace_bytes, fp8la_stream_t stream);
 
 /*
  * Synchronise `stream`, then read and clear the current device's status

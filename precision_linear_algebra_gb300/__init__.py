@@ -38,6 +38,7 @@ _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
 _S = ctypes.c_int
+_F = ctypes.c_float
 SIGNATURES = [
     ("fp8_quantize_pertensor", _S, [_P, _I64, _I64, _I64, _P, _I64, _P, _P, _P]),
     ("fp8_quantize_pertensor_ex", _S, [_P, _I64, _I64, _I64, _P, _I64, _P, _P, _I32, _P]),
@@ -66,6 +67,14 @@ SIGNATURES = [
     ("fp8la_lora_backward", _S,
      [_P, _I32, _I64, _P, _I32, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I32,
       _I32, _I64, _I64, _I32, _P, _P, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P]),
+    ("fp8_kv_append", _S,
+     [_P, _I64, _I64, _P, _I64, _I64, _I32, _I64, _I64, _P, _P, _P, _I64, _I64, _P, _P]),
+    ("fp8_kv_read", _S,
+     [_P, _I64, _I64, _P, _I64, _I64, _I32, _I64, _I64, _P, _P, _P, _I64, _I64, _P, _P]),
+    ("fp8_kv_attention_workspace_bytes", _I64, [_I64, _I32, _I32, _I32]),
+    ("fp8_kv_attention", _S,
+     [_P, _I32, _I64, _I64, _I32, _I64, _I64, _P, _P, _P, _I64, _I64, _I64, _P, _I64, _P, _P, _F,
+      _I32, _P, _I64, _I64, _P, _I64, _P, _I64, _P]),
     ("fp8_get_device_status", _S, [_P]),
     ("fp8la_set_wait_timeout_ns", _S, [_I64]),
     ("fp8la_diag_gemm_withheld_arrival", _S, [_P, _I64, _P, _I64, _P, _I64, _P, _P, _P]),
@@ -77,6 +86,15 @@ SIGNATURES = [
 ]
 
 _lib = None
+
+
+class fp8la_kv_cache(ctypes.Structure):
+    """The C struct of the same name."""
+    _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P), ("num_pages", _I64),
+                ("page_size", _I32), ("kv_heads", _I32), ("head_dim", _I32), ("format", _I32),
+                ("page_stride", _I64), ("head_stride", _I64), ("token_stride", _I64),
+                ("scale_page_stride", _I64), ("scale_head_stride", _I64),
+                ("scale_token_stride", _I64)]
 
 
 class Fp8laError(RuntimeError):
@@ -217,6 +235,32 @@ def fp8la_lora_backward(dy, dy_dtype, ld_dy, x, x_dtype, ldx, v, ldv, rows, A, l
                  lda, stride_a, B, ldb, stride_b, alpha, num_adapters, rank, K, N, num_segments,
                  m_offsets, adapter_ids, dx_base, ld_dx_base, dx, ld_dx, dA, dB, workspace,
                  workspace_bytes, stream)
+
+
+def fp8_kv_append(k, ld_k, ld_k_head, v, ld_v, ld_v_head, dtype, rows, num_segments, m_offsets,
+                  kv_lens, page_table, ld_table, max_pages, cache, stream):
+    return _call("fp8_kv_append", k, ld_k, ld_k_head, v, ld_v, ld_v_head, dtype, rows,
+                 num_segments, m_offsets, kv_lens, page_table, ld_table, max_pages, cache, stream)
+
+
+def fp8_kv_read(k, ld_k, ld_k_head, v, ld_v, ld_v_head, dtype, rows, num_segments, m_offsets,
+                kv_lens, page_table, ld_table, max_pages, cache, stream):
+    return _call("fp8_kv_read", k, ld_k, ld_k_head, v, ld_v, ld_v_head, dtype, rows,
+                 num_segments, m_offsets, kv_lens, page_table, ld_table, max_pages, cache, stream)
+
+
+def fp8_kv_attention_workspace_bytes(rows, num_heads, head_dim, prefix):
+    return _bytes("fp8_kv_attention_workspace_bytes", rows, num_heads, head_dim, prefix)
+
+
+def fp8_kv_attention(q, q_dtype, ld_q, ld_q_head, num_heads, rows, num_segments, m_offsets,
+                     kv_lens, page_table, ld_table, max_pages, max_rows, prefix_table,
+                     prefix_pages, prefix_len, cache, scale, causal, out, ld_out, ld_out_head,
+                     lse, ld_lse, workspace, workspace_bytes, stream):
+    return _call("fp8_kv_attention", q, q_dtype, ld_q, ld_q_head, num_heads, rows, num_segments,
+                 m_offsets, kv_lens, page_table, ld_table, max_pages, max_rows, prefix_table,
+                 prefix_pages, prefix_len, cache, scale, causal, out, ld_out, ld_out_head, lse,
+                 ld_lse, workspace, workspace_bytes, stream)
 
 
 def fp8_get_device_status(stream):
@@ -602,6 +646,144 @@ def lora_backward(dy, x, v, A, B, alpha, m_offsets, adapter_ids, dx_base, dx=Non
           _rows(dx_base, T, K, torch.bfloat16), dx.data_ptr(), lddx, dA.data_ptr(),
           dB.data_ptr(), pw, nbytes, _stream())
     return dx, dA, dB
+
+
+class KVCache:
+    """A paged key/value cache of FP8 codes, one scale for each token and head.
+
+    k, v: uint8 CUDA [pages][heads][page_size][D], D contiguous (D a multiple of
+    16 up to 256), other strides multiples of 16 and the same for both; k_scale,
+    v_scale: fp32 [pages][heads][page_size], strides the same for both.  A view
+    with the heads inside the page's tokens (transpose(1, 2)) is as good.
+    """
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "fmt", "shape", "struct", "ref")
+
+    def __init__(self, k, v, k_scale, v_scale, fmt="e4m3"):
+        import torch
+        P, H, page, D = k.shape
+        st, sst = k.stride(), k_scale.stride()
+        assert k.is_cuda and v.is_cuda and k_scale.is_cuda and v_scale.is_cuda
+        assert k.dtype is torch.uint8 and v.dtype is torch.uint8
+        assert v.shape == k.shape and v.stride() == st and st[3] == 1
+        assert k_scale.dtype is torch.float32 and v_scale.dtype is torch.float32
+        assert k_scale.shape == (P, H, page) and v_scale.shape == (P, H, page)
+        assert v_scale.stride() == sst
+        self.k, self.v, self.k_scale, self.v_scale, self.fmt = k, v, k_scale, v_scale, fmt
+        self.shape = (P, H, page, D)
+        self.struct = fp8la_kv_cache(
+            k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), P, page, H, D,
+            _FORMATS[fmt], st[0], st[1], st[2], sst[0], sst[1], sst[2])
+        self.ref = ctypes.addressof(self.struct)
+
+
+def kv_cache(num_pages, kv_heads, page_size, head_dim, fmt="e4m3", device="cuda"):
+    """A KVCache of zeros."""
+    import torch
+    shape = (num_pages, kv_heads, page_size)
+    codes = [torch.zeros((*shape, head_dim), dtype=torch.uint8, device=device) for _ in "kv"]
+    scales = [torch.ones(shape, dtype=torch.float32, device=device) for _ in "kv"]
+    return KVCache(*codes, *scales, fmt)
+
+
+def _sequences(m_offsets, kv_lens, page_table):
+    """(segments, offsets, lengths, table, its row stride, its width)."""
+    import torch
+    S, pages = page_table.shape
+    _dense(m_offsets, (S + 1,), torch.int32)
+    _dense(kv_lens, (S,), torch.int32)
+    ld = _rows(page_table, S, pages, torch.int32)
+    return S, m_offsets.data_ptr(), kv_lens.data_ptr(), page_table.data_ptr(), ld, pages
+
+
+def _heads(t, shape, dtype=None):
+    """Row and head strides of a CUDA [rows][heads][D] tensor, D contiguous."""
+    assert t.is_cuda and t.shape == shape and (dtype is None or t.dtype is dtype)
+    s0, s1, s2 = t.stride()
+    assert s2 == 1
+    return s0, s1
+
+
+def kv_append(k, v, cache, m_offsets, kv_lens, page_table):
+    """Quantises k and v, fp32 or bf16 CUDA [T][heads][D], into a KVCache.
+
+    Rows m_offsets[s] .. m_offsets[s+1]-1 (int32 [S+1]) are the last ones of
+    sequence s, which has kv_lens[s] tokens with them (int32 [S]); its position j
+    lies in page page_table[s][j // page_size] (int32 [S][pages]).  k and v may be
+    slices of a fused projection.  Nothing is synchronised.
+    """
+    T = k.shape[0]
+    _, H, _, D = cache.shape
+    ldk, ldkh = _heads(k, (T, H, D))
+    ldv, ldvh = _heads(v, (T, H, D), k.dtype)
+    S, po, pl, pt, ldt, pages = _sequences(m_offsets, kv_lens, page_table)
+    _call("fp8_kv_append", k.data_ptr(), ldk, ldkh, v.data_ptr(), ldv, ldvh, _type(k), T, S, po,
+          pl, pt, ldt, pages, cache.ref, _stream())
+
+
+def kv_read(cache, m_offsets, kv_lens, page_table, rows, dtype=None, k=None, v=None):
+    """Reads back the rows that kv_append with the same arguments wrote.
+
+    rows: m_offsets[S], or more (rows beyond are left as they were).  Returns (k,
+    v), each dtype (torch.bfloat16, the default, or float32) [rows][heads][D].
+    """
+    import torch
+    _, H, _, D = cache.shape
+    dtype = dtype or (k.dtype if k is not None else torch.bfloat16)
+    dev = cache.k.device
+    if k is None:
+        k = torch.empty((rows, H, D), dtype=dtype, device=dev)
+    if v is None:
+        v = torch.empty((rows, H, D), dtype=dtype, device=dev)
+    ldk, ldkh = _heads(k, (rows, H, D), dtype)
+    ldv, ldvh = _heads(v, (rows, H, D), dtype)
+    S, po, pl, pt, ldt, pages = _sequences(m_offsets, kv_lens, page_table)
+    _call("fp8_kv_read", k.data_ptr(), ldk, ldkh, v.data_ptr(), ldv, ldvh, _type(k), rows, S, po,
+          pl, pt, ldt, pages, cache.ref, _stream())
+    return k, v
+
+
+def kv_attention(q, cache, m_offsets, kv_lens, page_table, max_rows=None, scale=None,
+                 causal=True, prefix_table=None, prefix_len=None, out=None, lse=None,
+                 workspace=None):
+    """Attention of packed sequences over a KVCache.
+
+    q: fp32 or bf16 CUDA [T][query heads][D]; segments, lengths and pages as for
+    kv_append, whose rows are to be written first.  With causal a row sees the
+    positions up to its own, else all kv_lens[s].  max_rows: rows of the longest
+    segment, or more (default T).  scale: of the scores (default D ** -0.5).
+    prefix_table (int32 [pages]) and prefix_len (int32 [1]): tokens that every
+    sequence begins with, before those of its own page_table and kv_lens.  Returns
+    (out bf16 [T][query heads][D], lse fp32 [T][query heads]); rows that see
+    nothing get 0 and -inf.  Nothing is synchronised.
+    """
+    import torch
+    T, Hq, D = q.shape
+    dev = q.device
+    ldq, ldqh = _heads(q, (T, Hq, cache.shape[3]))
+    if out is None:
+        out, ldo, ldoh = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev), Hq * D, D
+    else:
+        ldo, ldoh = _heads(out, (T, Hq, D), torch.bfloat16)
+    if lse is None:
+        lse, ldl = torch.empty((T, Hq), dtype=torch.float32, device=dev), Hq
+    else:
+        ldl = _rows(lse, T, Hq, torch.float32)
+    S, po, pl, pt, ldt, pages = _sequences(m_offsets, kv_lens, page_table)
+    pp = pn = None
+    shared = 0
+    if prefix_len is not None:
+        _dense(prefix_len, (1,), torch.int32)
+        shared = prefix_table.numel()
+        _dense(prefix_table, (shared,), torch.int32)
+        pp, pn = prefix_table.data_ptr(), prefix_len.data_ptr()
+    pw, nbytes, ws = _workspace(
+        workspace, fp8_kv_attention_workspace_bytes(T, Hq, D, pn is not None), dev)
+    _call("fp8_kv_attention", q.data_ptr(), _type(q), ldq, ldqh, Hq, T, S, po, pl, pt, ldt, pages,
+          T if max_rows is None else max_rows, pp, shared, pn, cache.ref,
+          D ** -0.5 if scale is None else scale, causal, out.data_ptr(), ldo, ldoh,
+          lse.data_ptr(), ldl, pw, nbytes, _stream())
+    return out, lse
 
 
 def device_status():

@@ -1,0 +1,854 @@
+// Attention of few rows of each sequence over the FP8 key/value cache, the join
+// of partial results, and the entry point.
+//
+// A row (token t, query head h) of sequence s has scores x_j = (q . k_j) ks_j
+// scale over the tokens j that it sees, k_j the codes of K's row and ks_j its
+// scale; out = sum_j p_j vs_j v_j / sum_j p_j, p_j = exp(x_j).  V's scales go into
+// the exponent, w_j = 2^(x_j log2 e + log2 vs_j - M) with a running maximum M of
+// those sums, so that the products are w_j times codes, and the denominator is
+// sum_j w_j / vs_j.  One exponential an element, no product with dequantised values.
+//
+// Precision: codes are halves exactly.  A BF16 query row, scaled by a power of
+// two to a maximum of 2^8, is halves exactly but for elements below 2^-22 of its
+// maximum (off by 2^-33 of it at most); an FP32 one is the sum of two halves,
+// 2^-22.  w_j is rounded to a half, 2^-11, at most 2^7 (2^15 between two rescalings),
+// so that only what is 2^-21 of the largest or less loses more.  Sums are FP32.
+//
+// Bound: HBM, K's and V's codes once for all heads of a group.  A warp streams 16
+// tokens at a time through a ring of its own, filled by cp.async four deep: no
+// barrier in the loop.  mma.sync m16n8k16 takes 16 rows, which is what a group of
+// heads of one token needs; the fragments come from codes by one conversion for
+// two of them.  tcgen05 wants 64 rows at least, which kv_attention_tc.cu has.
+#include "kv_attention.cuh"
+
+namespace fp8la {
+namespace kv {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kWarps = 4;
+constexpr int kRows = 16;       // rows of a tile
+constexpr int kGroup = 16;      // tokens of a warp's step
+constexpr int kTile = kWarps * kGroup;
+constexpr int kStages = 4;
+constexpr float kShift = 7.0f;  // w of the running maximum is 2^7
+constexpr float kLazy = 8.0f;   // it is raised where 2^8 is passed
+
+template <bool F32Q, int DP>
+struct Cfg {
+  static constexpr int CH = DP / 16;                  // 16-byte chunks of a row
+  static constexpr int kK = kGroup * DP;
+  static constexpr int kStage = 2 * kK + 3 * kGroup * 4;  // K, V, ks, vs, 1 / vs
+  static constexpr int kRing = kStages * kStage;
+  static constexpr int KS = DP / 16;                  // MMA steps along D
+  static constexpr int TERMS = F32Q ? 2 : 1;
+  static constexpr bool QREG = KS * TERMS <= 8;
+  static constexpr int kQ = kWarps * kRing;           // query fragments
+  static constexpr int kQBytes = QREG ? 0 : KS * TERMS * 32 * 16;
+  static constexpr int kLdO = DP + 4;                 // of the warps' results, floats
+  static constexpr int kRed = kWarps * kRows * (kLdO + 1) * 4;
+  static constexpr int kSmem =
+      kQ + kQBytes > kRed ? kQ + kQBytes : kRed;
+  static constexpr int CTAS = F32Q || DP > 128 ? (DP > 128 ? 1 : 2) : 3;
+  static constexpr int VW = DP == 64 ? 8 : 16;        // V bytes of a lane
+  static constexpr int VH = DP == 256 ? 2 : 1;        // ... times
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(on ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+               "r"(on ? 4 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 lds_f2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float lds_f(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts_f(uint32_t a, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+
+// Bank spreading of the 16-byte chunks: a phase of K's reads takes 4 chunks of 2
+// tokens, one of V's 2 chunks of every other token of 8.
+template <int DP>
+__device__ __forceinline__ int swizzle_k(int token) {
+  return DP == 64 ? 0 : (token & 1) * 4;
+}
+template <int DP>
+__device__ __forceinline__ int swizzle_v(int token) {
+  return DP == 64 ? 2 * ((token >> 1) & 1) : 2 * ((token >> 1) & 3);
+}
+
+// 2^e with the exponent of v (0 where v is not a positive finite number).
+__device__ __forceinline__ int exponent_of(float v) {
+  const uint32_t b = __float_as_uint(v);
+  const int e = static_cast<int>(b >> 23);  // a sign makes it more than 255
+  if (v == 0.0f || e >= 255) return 0;
+  return e > 0 ? e - 127 : -126;
+}
+__device__ __forceinline__ float power_of_two(int e) {  // -126 .. 127
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+// 16 consecutive elements of a query row, from d on, as FP32.
+template <bool F32Q>
+__device__ __forceinline__ void load_q(const AttnArgs &a, int64_t at, bool on, float (&x)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = 0.0f;
+  if (!on) return;
+  if (F32Q) {
+    const float *p = static_cast<const float *>(a.q) + at;
+    if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 v = reinterpret_cast<const float4 *>(p)[i];
+        x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = p[i];
+    }
+  } else {
+    const uint16_t *p = static_cast<const uint16_t *>(a.q) + at;
+    if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint4 v = reinterpret_cast<const uint4 *>(p)[i];
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x[8 * i + 2 * j] = __uint_as_float(u[j] << 16);
+          x[8 * i + 2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(static_cast<uint32_t>(p[i]) << 16);
+    }
+  }
+}
+
+template <bool F32Q, int FMT, int DP>
+__global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
+    kv_attention_kernel(const AttnArgs a) {
+  using C = Cfg<F32Q, DP>;
+  using Fm = Format<FMT>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ Share share_slot;
+  __shared__ int64_t warp_sums[kWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, c = lane & 3;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (threadIdx.x == 0 && a.desc) a.desc[blockIdx.x].parts = 0;
+  const Share sh = share_out<kThreads, kRows, kTile, false>(a, &share_slot, warp_sums);
+  const Cache &kc = a.cache;
+  const uint32_t ring = smem_addr(smem) + warp * C::kRing;
+  const uint32_t qsm = smem_addr(smem) + C::kQ;
+
+  int64_t at = sh.begin, before = sh.before;
+  int s = sh.seq;
+  while (at < sh.end) {
+    // The item that holds unit `at`.
+    Seq q = load_seq(a, s);
+    int64_t units = units_of<kRows, kTile, false>(a, q);
+    while (at >= before + units * kc.heads) {
+      before += units * kc.heads;
+      q = load_seq(a, ++s);
+      units = units_of<kRows, kTile, false>(a, q);
+    }
+    const int NT = tiles_of<kRows, kTile, false>(a, q, 0);
+    const int rts = (q.n * a.G + kRows - 1) / kRows;
+    const int64_t local = at - before;
+    const int64_t item = local / NT;
+    const int tile0 = static_cast<int>(local - item * NT);
+    const int h = static_cast<int>(item / rts), rt = static_cast<int>(item - static_cast<int64_t>(h) * rts);
+    const int count = static_cast<int>(min(static_cast<int64_t>(NT - tile0), sh.end - at));
+    at += count;
+
+    // This lane's rows are rt * 16 + g and that + 8; they see the tokens below
+    // seen[0] and seen[1].  Tokens from `all` on are not seen by every row.
+    const int rows = min(kRows, q.n * a.G - rt * kRows);
+    int tok[2], head[2], seen[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = rt * kRows + min(g + 8 * i, rows - 1);
+      tok[i] = divide(r, a.group);
+      head[i] = h * a.G + r - tok[i] * a.G;
+      seen[i] = g + 8 * i < rows ? tokens_seen(a, q, r) : 0;
+    }
+    const int all = tokens_seen(a, q, rt * kRows);
+    const int most = tokens_seen(a, q, rt * kRows + rows - 1);
+    const int begin = tile0 * kTile, end = min(begin + count * kTile, most);
+
+    // Token `first + lane`'s place in the cache, for lanes below 16, in bytes of
+    // codes and in scales; the table is read one step before it is needed.
+    const int32_t *table = a.rows.table + s * a.rows.ld_table;
+    const uint8_t *kbase = kc.k + h * kc.head_stride, *vbase = kc.v + h * kc.head_stride;
+    const float *ksbase = kc.k_scale + h * kc.scale_head_stride;
+    const float *vsbase = kc.v_scale + h * kc.scale_head_stride;
+    auto page_at = [&](int first) {
+      const int t = first + (lane & 15);
+      return t < end ? table[divide(t, kc.page)] : -1;
+    };
+    auto request = [&](int first, int page, int slot) {
+      const int t = first + (lane & 15);
+      bool on = t < end;
+      if (on && (page < 0 || page >= kc.num_pages)) {
+        atomicOr(a.rows.status, kStatusBadDeviceArg);
+        on = false;
+      }
+      const int place = t - divide(t, kc.page) * kc.page_size;
+      const int64_t code = on ? page * kc.page_stride + place * kc.token_stride : -1;
+      const int64_t sc = on ? page * kc.scale_page_stride + place * kc.scale_token_stride : 0;
+      const uint32_t dst = ring + slot * C::kStage;
+      cp_async4(dst + 2 * C::kK + lane * 4, (lane < 16 ? ksbase : vsbase) + sc, on);
+#pragma unroll
+      for (int i = 0; i < kGroup * C::CH / 32; ++i) {
+        const int id = lane + 32 * i, token = id / C::CH, ch = id % C::CH;
+        const int64_t off = __shfl_sync(0xffffffffu, code, token);
+        const bool ok = off >= 0 && ch * 16 < kc.D;
+        const int64_t from = ok ? off + ch * 16 : 0;
+        cp_async16(dst + token * DP + (ch ^ swizzle_k<DP>(token)) * 16, kbase + from, ok);
+        cp_async16(dst + C::kK + token * DP + (ch ^ swizzle_v<DP>(token)) * 16, vbase + from, ok);
+      }
+    };
+    const int first = begin + warp * kGroup;
+    int page = page_at(first);
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+      if (first + i * kTile < end) {
+        const int p = page;
+        page = page_at(first + (i + 1) * kTile);
+        request(first + i * kTile, p, i);
+      }
+      cp_commit();
+    }
+
+    // Query fragments: k 2c, 2c+1, 2c+8, 2c+9 of step 4 f + j stand for the elements
+    // 64 f + 16 c + 4 j .. + 3, so that a lane's codes are 16 bytes of a row.
+    uint32_t qf[C::QREG ? C::KS * C::TERMS : 1][4];
+    float factor[2];
+    {
+      int e[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int64_t row = (static_cast<int64_t>(q.row0) + tok[i]) * a.ldq + head[i] * a.ldq_head;
+        float m = 0.0f;
+#pragma unroll 1
+        for (int f = 0; f < DP / 64; ++f) {
+          float x[16];
+          load_q<F32Q>(a, row + 64 * f + 16 * c, 64 * f + 16 * c < kc.D, x);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) m = fmaxf(m, fabsf(x[j]));
+        }
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        e[i] = min(max(8 - exponent_of(m), -126), 126);
+        factor[i] = power_of_two(-e[i]) * a.scale_log2;
+      }
+#pragma unroll
+      for (int f = 0; f < DP / 64; ++f) {
+        float x[2][16];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int64_t row = (static_cast<int64_t>(q.row0) + tok[i]) * a.ldq + head[i] * a.ldq_head;
+          load_q<F32Q>(a, row + 64 * f + 16 * c, 64 * f + 16 * c < kc.D, x[i]);
+          const float up = power_of_two(e[i]);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) x[i][j] *= up;
+        }
+#pragma unroll
+        for (int t = 0; t < C::TERMS; ++t) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float *p = &x[k & 1][4 * j + (k >> 1) * 2];
+              w[k] = pack_half(p[0], p[1]);
+              if (t + 1 < C::TERMS) {
+                const float2 r = half2_floats(w[k]);
+                p[0] -= r.x;
+                p[1] -= r.y;
+              }
+            }
+            const int step = (4 * f + j) * C::TERMS + t;
+            if (C::QREG) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) qf[step][k] = w[k];
+            } else if (warp == 0) {
+              st_shared_v4(qsm + (step * 32 + lane) * 16, w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+      }
+      if (!C::QREG) __syncthreads();
+    }
+
+    float o[C::VH * C::VW][4];
+#pragma unroll
+    for (int j = 0; j < C::VH * C::VW; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[j][i] = 0.0f;
+    float M[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    int e0 = 0;
+    bool poison = false;
+    int slot = 0;
+#pragma unroll 1
+    for (int base = first; base < end; base += kTile) {
+      cp_wait<kStages - 2>();
+      __syncwarp();
+      {
+        const int ahead = base + (kStages - 1) * kTile;
+        if (ahead < end) {
+          const int p = page;
+          page = page_at(ahead + kTile);
+          request(ahead, p, (slot + kStages - 1) % kStages);
+        }
+        cp_commit();
+      }
+      const uint32_t st = ring + slot * C::kStage, scales = st + 2 * C::kK;
+      // V's scales: logarithm and reciprocal, relative to a power of two near the first.
+      if (base == first) {
+        e0 = exponent_of(lds_f(scales + 64));
+        __syncwarp();
+      }
+      if (lane < 16) {
+        const float v = lds_f(scales + 64 + 4 * lane);
+        const bool fine = v > 0.0f && v < INFINITY;
+        const bool in = base + lane < end;
+        sts_f(scales + 64 + 4 * lane, !in ? 0.0f : fine ? log2f(v) - e0 : NAN);
+        sts_f(scales + 128 + 4 * lane, !in ? 0.0f : fine ? __fdiv_rn(power_of_two(e0), v) : NAN);
+      }
+      // Scores of tokens g and 8 + g against the 16 rows.
+      float sc[2][4] = {};
+#pragma unroll
+      for (int f = 0; f < DP / 64; ++f) {
+        uint32_t kw[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int token = g + 8 * i;
+          const uint4 w = lds128(st + token * DP + ((4 * f + c) ^ swizzle_k<DP>(token)) * 16);
+          kw[i][0] = w.x; kw[i][1] = w.y; kw[i][2] = w.z; kw[i][3] = w.w;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t b[2][2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            b[i][0] = decode2<FMT>(kw[i][j] & 0xffffu);
+            b[i][1] = decode2<FMT>(kw[i][j] >> 16);
+          }
+#pragma unroll
+          for (int t = 0; t < C::TERMS; ++t) {
+            const int step = (4 * f + j) * C::TERMS + t;
+            if (C::QREG) {
+              mma_f16(sc[0], qf[step], b[0][0], b[0][1]);
+              mma_f16(sc[1], qf[step], b[1][0], b[1][1]);
+            } else {
+              const uint4 w = lds128(qsm + (step * 32 + lane) * 16);
+              const uint32_t qw[4] = {w.x, w.y, w.z, w.w};
+              mma_f16(sc[0], qw, b[0][0], b[0][1]);
+              mma_f16(sc[1], qw, b[1][0], b[1][1]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      // Exponents and weights of tokens 2c, 2c+1, 8+2c, 9+2c.
+      float iv[2][2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 ks = lds_f2(scales + 32 * i + 8 * c);
+        const float2 lv = lds_f2(scales + 64 + 32 * i + 8 * c);
+        const float2 r = lds_f2(scales + 128 + 32 * i + 8 * c);
+        iv[i][0] = r.x;
+        iv[i][1] = r.y;
+        sc[i][0] = fmaf(sc[i][0] * ks.x, factor[0], lv.x);
+        sc[i][1] = fmaf(sc[i][1] * ks.y, factor[0], lv.y);
+        sc[i][2] = fmaf(sc[i][2] * ks.x, factor[1], lv.x);
+        sc[i][3] = fmaf(sc[i][3] * ks.y, factor[1], lv.y);
+      }
+      const bool edge = base + kGroup > min(all, end);
+      if (edge) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (base + 8 * i + 2 * c + (k & 1) >= min(seen[k >> 1], end)) {
+              sc[i][k] = -INFINITY;
+            }
+      }
+      float mx[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        mx[k] = fmaxf(fmaxf(sc[0][2 * k], sc[0][2 * k + 1]),
+                      fmaxf(sc[1][2 * k], sc[1][2 * k + 1]));
+      if (__any_sync(0xffffffffu, mx[0] > M[0] + kLazy || mx[1] > M[1] + kLazy)) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float m = mx[k];
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+          m = fmaxf(m, M[k]);
+          const float down = m == -INFINITY ? 1.0f : ex2(M[k] - m);
+          M[k] = m;
+          l[k] *= down;
+#pragma unroll
+          for (int j = 0; j < C::VH * C::VW; ++j) {
+            o[j][2 * k] *= down;
+            o[j][2 * k + 1] *= down;
+          }
+        }
+      }
+      const float top[2] = {M[0] == -INFINITY ? 0.0f : M[0] - kShift,
+                            M[1] == -INFINITY ? 0.0f : M[1] - kShift};
+      float w[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          w[i][k] = ex2(sc[i][k] - top[k >> 1]);
+          float p = w[i][k] * iv[i][k & 1];
+          // 1 / vs of a token that the row does not see may be anything.
+          if (edge && sc[i][k] == -INFINITY) p = 0.0f;
+          l[k >> 1] += p;
+        }
+      const uint32_t pf[4] = {pack_half(w[0][0], w[0][1]), pack_half(w[0][2], w[0][3]),
+                              pack_half(w[1][0], w[1][1]), pack_half(w[1][2], w[1][3])};
+      // Values.  Where some rows do not see a token (weight 0), its codes that are not
+      // finite must not reach them: they are taken out here and put in at the end.
+      const bool partial = all < most && base + kGroup > all;
+#pragma unroll
+      for (int f = 0; f < C::VH; ++f) {
+        uint32_t vw[4][C::VW / 4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int token = 2 * c + (i & 1) + 8 * (i >> 1);
+          const uint32_t row = st + C::kK + token * DP;
+          if (C::VW == 16) {
+            const uint4 v = lds128(row + ((8 * f + g) ^ swizzle_v<DP>(token)) * 16);
+            vw[i][0] = v.x; vw[i][1] = v.y; vw[i][C::VW / 8] = v.z; vw[i][C::VW / 4 - 1] = v.w;
+          } else {
+            const uint2 v = lds64(row + ((g >> 1) ^ swizzle_v<DP>(token)) * 16 + (g & 1) * 8);
+            vw[i][0] = v.x; vw[i][1] = v.y;
+          }
+          if (partial) {
+#pragma unroll
+            for (int j = 0; j < C::VW / 4; ++j)
+#pragma unroll
+              for (int b = 0; b < 4; ++b)
+                if (!Fm::finite(vw[i][j] >> (8 * b))) {
+                  vw[i][j] &= ~(0xffu << (8 * b));
+                  poison = true;
+                }
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < C::VW / 4; ++j) {
+          const uint32_t a0 = __byte_perm(vw[0][j], vw[1][j], 0x5140);
+          const uint32_t a1 = __byte_perm(vw[0][j], vw[1][j], 0x7362);
+          const uint32_t b0 = __byte_perm(vw[2][j], vw[3][j], 0x5140);
+          const uint32_t b1 = __byte_perm(vw[2][j], vw[3][j], 0x7362);
+          float(&oo)[4] = o[f * C::VW + 4 * j];
+          mma_f16(oo, pf, decode2<FMT>(a0 & 0xffffu), decode2<FMT>(b0 & 0xffffu));
+          mma_f16(o[f * C::VW + 4 * j + 1], pf, decode2<FMT>(a0 >> 16), decode2<FMT>(b0 >> 16));
+          mma_f16(o[f * C::VW + 4 * j + 2], pf, decode2<FMT>(a1 & 0xffffu),
+                  decode2<FMT>(b1 & 0xffffu));
+          mma_f16(o[f * C::VW + 4 * j + 3], pf, decode2<FMT>(a1 >> 16), decode2<FMT>(b1 >> 16));
+        }
+      }
+      if (++slot == kStages) slot = 0;
+    }
+    cp_wait<0>();
+    if (__any_sync(0xffffffffu, poison)) {
+      for (int base = first; base < end; base += kTile) {
+        if (base + kGroup <= all) continue;
+        for (int t = base; t < min(base + kGroup, end); ++t) {
+          const int p = table[divide(t, kc.page)];
+          if (p < 0 || p >= kc.num_pages) continue;
+          const uint8_t *row = vbase + p * kc.page_stride +
+                               (t - divide(t, kc.page) * kc.page_size) * kc.token_stride;
+#pragma unroll
+          for (int j = 0; j < C::VH * C::VW; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int d = j / C::VW * 128 + (2 * c + i) * C::VW + j % C::VW;
+              if (d < kc.D && !Fm::finite(row[d])) {
+                if (t < seen[0]) o[j][i] = NAN;
+                if (t < seen[1]) o[j][2 + i] = NAN;
+              }
+            }
+        }
+      }
+    }
+
+    // Each warp's result, normalised, with its logarithm (base 2); then all four's.
+    __syncthreads();
+    float *red = reinterpret_cast<float *>(smem);
+    float *red_lse = red + kWarps * kRows * C::kLdO;
+    const float back = power_of_two(e0);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float sum = l[k];
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+      float *row = red + (warp * kRows + g + 8 * k) * C::kLdO;
+#pragma unroll
+      for (int j = 0; j < C::VH * C::VW; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          row[j / C::VW * 128 + (2 * c + i) * C::VW + j % C::VW] =
+              o[j][2 * k + i] * inv * back;
+      if (c == 0)
+        red_lse[warp * kRows + g + 8 * k] =
+            sum > 0.0f || sum != sum ? M[k] - kShift + log2f(sum) : -INFINITY;
+    }
+    __syncthreads();
+    const bool whole = count == NT;
+    const int part = 2 * blockIdx.x + (tile0 > 0 ? 0 : 1);
+    constexpr int kPieces = DP / 8;
+    for (int i = threadIdx.x; i < rows * kPieces; i += kThreads) {
+      const int r = i / kPieces, d = i % kPieces * 8;
+      float lse[kWarps], best = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        lse[w] = red_lse[w * kRows + r];
+        best = fmaxf(best, lse[w]);
+      }
+      // A NaN is in no maximum, but in its weight.
+      float weight[kWarps], sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        weight[w] = lse[w] == -INFINITY ? 0.0f : exp2f(lse[w] - best);
+        sum += weight[w];
+      }
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      const float joined = sum == 0.0f ? -INFINITY : best + log2f(sum);
+      float x[8] = {};
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (weight[w] == 0.0f) continue;
+        const float *p = red + (w * kRows + r) * C::kLdO + d;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = fmaf(weight[w] * inv, p[j], x[j]);
+      }
+      if (d >= kc.D) continue;
+      if (whole) {
+        const int rr = rt * kRows + r, t = divide(rr, a.group);
+        const int64_t row = static_cast<int64_t>(q.row0) + t;
+        const int hq = h * a.G + rr - t * a.G;
+        emit<8>(a, row, hq, d, x, joined, weigh(a, row, hq, joined));
+      } else {
+        float *p = a.part_o + (static_cast<int64_t>(part) * kRows + r) * DP + d;
+        *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<float4 *>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+        if (d == 0) a.part_lse[part * kRows + r] = joined;
+      }
+    }
+    if (threadIdx.x == 0 && !whole && tile0 == 0)
+      a.desc[blockIdx.x] = {s, h, rt, owner_of(sh, at - count + NT - 1) - static_cast<int>(blockIdx.x) + 1};
+    __syncthreads();  // the results overlay the rings
+  }
+}
+
+// ---------------------------------------------------------------------- join
+// Joins the partial results of an item that several CTAs shared: CTA b began it
+// (its second partial result), the next parts - 1 went on (their first ones).  A
+// block takes four rows, two warps each; rows are added in the CTAs' order.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = 4;
+
+template <int DP>
+__global__ void __launch_bounds__(kJoinThreads)
+    kv_join_kernel(const AttnArgs a, const int BM) {
+  constexpr int V = DP / 32;
+  __shared__ float sums[kJoinRows][DP + 2];
+  pdl_wait();
+  pdl_launch_dependents();
+  const Desc d = a.desc[blockIdx.x];
+  if (d.parts == 0) return;
+  const Seq q = load_seq(a, d.s);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int side = warp & 1, slot = warp >> 1;
+  const int r = blockIdx.y * kJoinRows + slot;
+  const int rr = d.rt * BM + r;
+  const bool on = r < BM && rr < q.n * a.G;
+  auto part = [&](int i) {
+    return static_cast<int64_t>(2 * (static_cast<int>(blockIdx.x) + i) + (i == 0 ? 1 : 0)) * BM + r;
+  };
+  float best = -INFINITY, x[V] = {}, sum = 0.0f;
+  const int half = (d.parts + 1) / 2;
+  const int i0 = side * half, i1 = min(d.parts, i0 + half);
+  if (on) {
+    for (int i = lane; i < d.parts; i += 32) best = fmaxf(best, a.part_lse[part(i)]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
+#pragma unroll 4
+    for (int i = i0; i < i1; ++i) {
+      const float lse = a.part_lse[part(i)];
+      const float w = lse == -INFINITY ? 0.0f : exp2f(lse - best);
+      const float *p = a.part_o + part(i) * DP + lane * V;
+      float y[V];
+      if (V >= 4) {
+#pragma unroll
+        for (int j = 0; j < V; j += 4)
+          *reinterpret_cast<float4 *>(&y[j]) = *reinterpret_cast<const float4 *>(p + j);
+      } else {
+        *reinterpret_cast<float2 *>(&y[0]) = *reinterpret_cast<const float2 *>(p);
+      }
+      sum += w;
+      if (w != 0.0f) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[j] = fmaf(w, y[j], x[j]);
+      }
+    }
+  }
+  if (side == 1) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) sums[slot][lane * V + j] = x[j];
+    if (lane == 0) sums[slot][DP] = sum;
+  }
+  __syncthreads();
+  if (!on || side == 1 || lane * V >= a.cache.D) return;
+  sum += sums[slot][DP];
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+  for (int j = 0; j < V; ++j) x[j] = (x[j] + sums[slot][lane * V + j]) * inv;
+  const float lse = sum == 0.0f ? -INFINITY : best + log2f(sum);
+  const int t = divide(rr, a.group);
+  const int64_t row = static_cast<int64_t>(q.row0) + t;
+  const int hq = d.h * a.G + rr - t * a.G;
+  emit<V>(a, row, hq, lane * V, x, lse, weigh(a, row, hq, lse));
+}
+
+template <typename Kern, typename... Args>
+fp8la_status launch(Kern kern, dim3 grid, int threads, size_t smem, cudaStream_t s,
+                    const Args &...a) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a...) == cudaSuccess ? FP8LA_OK : FP8LA_ERR_CUDA;
+}
+
+template <bool F32Q, int FMT, int DP>
+fp8la_status launch_few_one(const AttnArgs &a, int slot, int ctas, cudaStream_t s) {
+  using C = Cfg<F32Q, DP>;
+  auto kern = kv_attention_kernel<F32Q, FMT, DP>;
+  if (once_per_device(slot, [&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    C::kSmem);
+      }) != cudaSuccess)
+    return FP8LA_ERR_CUDA;
+  return launch(kern, dim3(ctas), kThreads, C::kSmem, s, a);
+}
+
+int padded_dim(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+
+// CTAs of the few-row kernel on the device.
+int few_ctas(bool f32, int DP) {
+  const int n = sm_count();
+  const int per = DP == 64 ? (f32 ? Cfg<true, 64>::CTAS : Cfg<false, 64>::CTAS)
+                  : DP == 128 ? (f32 ? Cfg<true, 128>::CTAS : Cfg<false, 128>::CTAS)
+                              : (f32 ? Cfg<true, 256>::CTAS : Cfg<false, 256>::CTAS);
+  return (n > 0 ? n : 1) * per;
+}
+
+template <bool F32Q, int FMT>
+fp8la_status launch_few_fmt(const AttnArgs &a, int DP, int slot, int ctas, cudaStream_t s) {
+  if (DP == 64) return launch_few_one<F32Q, FMT, 64>(a, slot, ctas, s);
+  if (DP == 128) return launch_few_one<F32Q, FMT, 128>(a, slot + 1, ctas, s);
+  return launch_few_one<F32Q, FMT, 256>(a, slot + 2, ctas, s);
+}
+
+fp8la_status launch_few(const AttnArgs &a, bool f32, int format, int ctas, cudaStream_t s) {
+  const int DP = padded_dim(a.cache.D);
+  if (f32)
+    return format == FP8LA_FORMAT_E4M3 ? launch_few_fmt<true, 0>(a, DP, 80, ctas, s)
+                                       : launch_few_fmt<true, 1>(a, DP, 83, ctas, s);
+  return format == FP8LA_FORMAT_E4M3 ? launch_few_fmt<false, 0>(a, DP, 86, ctas, s)
+                                     : launch_few_fmt<false, 1>(a, DP, 89, ctas, s);
+}
+
+// Workspace: partial results and their descriptions, then the prefix's results.
+struct Layout {
+  int64_t part_o, part_lse, desc, raw_o, raw_lse, bytes;
+};
+Layout layout_of(int64_t T, int Hq, int D, int ctas, int BM, bool prefix) {
+  Layout l;
+  auto up = [](int64_t n) { return (n + 255) / 256 * 256; };
+  const int DP = padded_dim(D);
+  l.part_o = 0;
+  l.part_lse = up(static_cast<int64_t>(2 * ctas) * BM * DP * 4);
+  l.desc = l.part_lse + up(static_cast<int64_t>(2 * ctas) * BM * 4);
+  l.raw_o = l.desc + up(static_cast<int64_t>(ctas) * sizeof(Desc));
+  l.raw_lse = l.raw_o + (prefix ? up(T * Hq * D * 4) : 0);
+  l.bytes = l.raw_lse + (prefix ? up(T * Hq * 4) : 0);
+  return l;
+}
+
+constexpr int64_t kMaxRowHeads = (int64_t(1) << 31) - (int64_t(1) << 20);
+
+}  // namespace
+
+fp8la_status launch_join(const AttnArgs &a, int BM, int DP, int ctas, int rows, cudaStream_t s) {
+  const dim3 grid(ctas, ((rows < BM ? rows : BM) + kJoinRows - 1) / kJoinRows);
+  if (DP == 64) return launch(kv_join_kernel<64>, grid, kJoinThreads, 0, s, a, BM);
+  if (DP == 128) return launch(kv_join_kernel<128>, grid, kJoinThreads, 0, s, a, BM);
+  return launch(kv_join_kernel<256>, grid, kJoinThreads, 0, s, a, BM);
+}
+
+}  // namespace kv
+}  // namespace fp8la
+
+using namespace fp8la;
+using namespace fp8la::kv;
+
+extern "C" {
+
+int64_t fp8_kv_attention_workspace_bytes(int64_t rows, int32_t num_heads, int32_t head_dim,
+                                         int32_t prefix) {
+  if (rows < 0 || num_heads < 1 || head_dim < 1) return FP8LA_ERR_INVALID_ARG;
+  if (head_dim % 16 != 0 || head_dim > kMaxHeadDim || rows * num_heads >= kMaxRowHeads ||
+      rows > INT32_MAX)
+    return FP8LA_ERR_UNSUPPORTED;
+  const int ctas = few_ctas(false, padded_dim(head_dim));
+  return layout_of(rows, num_heads, head_dim, ctas, kRows, prefix != 0).bytes;
+}
+
+fp8la_status fp8_kv_attention(const void *q, int32_t q_dtype, int64_t ld_q, int64_t ld_q_head,
+                              int32_t num_heads, int64_t rows, int64_t num_segments,
+                              const int32_t *m_offsets, const int32_t *kv_lens,
+                              const int32_t *page_table, int64_t ld_table, int64_t max_pages,
+                              int64_t max_rows, const int32_t *prefix_table,
+                              int64_t prefix_pages, const int32_t *prefix_len,
+                              const fp8la_kv_cache *cache, float scale, int32_t causal,
+                              uint16_t *out, int64_t ld_out, int64_t ld_out_head, float *lse,
+                              int64_t ld_lse, void *workspace, int64_t workspace_bytes,
+                              fp8la_stream_t stream) {
+  AttnArgs a = {};
+  fp8la_status st = check_cache(cache, &a.cache);
+  if (st != FP8LA_OK) return st;
+  const int H = a.cache.heads, D = a.cache.D;
+  if (q_dtype != FP8LA_TYPE_F32 && q_dtype != FP8LA_TYPE_BF16) return FP8LA_ERR_INVALID_ARG;
+  if (num_heads < 1 || num_heads % H != 0 || max_rows < 0 || prefix_pages < 0 ||
+      !(scale > -INFINITY && scale < INFINITY))
+    return FP8LA_ERR_INVALID_ARG;
+  if (rows > INT32_MAX || rows * num_heads >= kMaxRowHeads) return FP8LA_ERR_UNSUPPORTED;
+  st = check_rows(a.cache, m_offsets, kv_lens, page_table, ld_table, max_pages, num_segments,
+                  rows, &a.rows);
+  if (st != FP8LA_OK || rows == 0 || num_segments == 0) return st;
+  const int size = q_dtype == FP8LA_TYPE_F32 ? 4 : 2;
+  if (!q || !out || !workspace || (prefix_len && !prefix_table && prefix_pages > 0) ||
+      (!prefix_len && prefix_pages > 0))
+    return FP8LA_ERR_INVALID_ARG;
+  if ((rows > 1 && ld_q < 0) || (num_heads > 1 && ld_q_head < 0)) return FP8LA_ERR_INVALID_ARG;
+  const int64_t Hq = num_heads;
+  if (!((rows == 1 || ld_out >= (Hq - 1) * ld_out_head + D) && (Hq == 1 || ld_out_head >= D)) &&
+      !((Hq == 1 || ld_out_head >= (rows - 1) * ld_out + D) && (rows == 1 || ld_out >= D)))
+    return FP8LA_ERR_INVALID_ARG;
+  if (lse && rows > 1 && ld_lse < Hq) return FP8LA_ERR_INVALID_ARG;
+  const bool prefix = prefix_len != nullptr;
+  if (workspace_bytes < fp8_kv_attention_workspace_bytes(rows, num_heads, D, prefix))
+    return FP8LA_ERR_INVALID_ARG;
+  if (!aligned_to(q, size) || !aligned_to(out, 2) || !aligned_to(lse, 4) ||
+      !aligned_to(prefix_table, 4) || !aligned_to(prefix_len, 4) || !aligned16(workspace))
+    return FP8LA_ERR_ALIGNMENT;
+  if (prefix_pages > INT32_MAX) return FP8LA_ERR_UNSUPPORTED;
+  if (!device_is_sm10x()) return FP8LA_ERR_UNSUPPORTED;
+  a.rows.status = status_word_ptr();
+  if (!a.rows.status) return FP8LA_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool f32 = q_dtype == FP8LA_TYPE_F32;
+  const int DP = padded_dim(D);
+  const int ctas = few_ctas(f32, DP);
+  const Layout l = layout_of(rows, num_heads, D, few_ctas(false, DP), kRows, prefix);
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  a.q = q;
+  a.ldq = rows > 1 ? ld_q : 0;
+  a.ldq_head = num_heads > 1 ? ld_q_head : 0;
+  a.out = out;
+  a.ldo = rows > 1 ? ld_out : 0;
+  a.ldo_head = num_heads > 1 ? ld_out_head : 0;
+  a.out_vec = aligned16(out) && a.ldo % 8 == 0 && a.ldo_head % 8 == 0;
+  a.lse = lse;
+  a.ld_lse = rows > 1 ? ld_lse : 0;
+  a.Hq = num_heads;
+  a.G = num_heads / H;
+  a.group = make_divisor(static_cast<uint32_t>(a.G));
+  a.causal = causal != 0;
+  a.scale_log2 = scale * kLog2e;
+  a.max_rows = max_rows;
+  a.row_lo = 0;
+  a.row_hi = INT64_MAX;
+  a.min_units = 1;
+  a.part_o = reinterpret_cast<float *>(ws + l.part_o);
+  a.part_lse = reinterpret_cast<float *>(ws + l.part_lse);
+  a.desc = reinterpret_cast<Desc *>(ws + l.desc);
+  const int64_t row_heads = rows * a.G;
+  if (prefix) {
+    AttnArgs p = a;
+    p.whole = m_offsets + num_segments;
+    p.rows.S = 1;
+    p.rows.lens = prefix_len;
+    p.rows.table = prefix_table;
+    p.rows.ld_table = prefix_pages;
+    const int64_t most = prefix_pages * a.cache.page_size;
+    p.rows.capacity = most < INT32_MAX ? most : INT32_MAX;
+    p.causal = 0;
+    p.raw_o = reinterpret_cast<float *>(ws + l.raw_o);
+    p.raw_lse = reinterpret_cast<float *>(ws + l.raw_lse);
+    st = launch_few(p, f32, cache->format, ctas, s);
+    if (st != FP8LA_OK) return st;
+    st = launch_join(p, kRows, DP, ctas, row_heads < kRows ? static_cast<int>(row_heads) : kRows, s);
+    if (st != FP8LA_OK) return st;
+    a.pre_o = p.raw_o;
+    a.pre_lse = p.raw_lse;
+    a.prefix_len = prefix_len;
+    a.prefix_capacity = p.rows.capacity;
+  }
+  st = launch_few(a, f32, cache->format, ctas, s);
+  if (st != FP8LA_OK) return st;
+  return launch_join(a, kRows, DP, ctas, row_heads < kRows ? static_cast<int>(row_heads) : kRows, s);
+}
+
+}  // extern "C"

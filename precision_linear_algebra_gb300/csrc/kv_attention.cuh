@@ -1,0 +1,244 @@
+// What the attention kernels share: their arguments, how the work is shared out
+// over the CTAs, and how a row's result is written.
+#pragma once
+
+#include "kv.cuh"
+
+namespace fp8la {
+namespace kv {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// A partial result that a later kernel joins with the others of its item.
+struct Desc {
+  int32_t s, h, rt;   // sequence, K/V head, row tile
+  int32_t parts;      // CTAs that share it, this one the first; 0: none
+};
+
+struct AttnArgs {
+  Rows rows;
+  Cache cache;
+  const void *q;             // fp32 or bf16 [T][Hq][D]
+  int64_t ldq, ldq_head;
+  uint16_t *out;             // bf16 [T][Hq][D]
+  int64_t ldo, ldo_head;
+  int32_t out_vec;           // out can be written in 16-byte units
+  float *lse;                // [T][ld_lse], natural logarithm; may be null
+  int64_t ld_lse;
+  int32_t Hq, G, causal;
+  Divisor group;             // by G
+  float scale_log2;          // of scores, times log2 e
+  int64_t row_lo, row_hi;    // rows (tokens times G) of the sequences that are this kernel's
+  int64_t max_rows;          // of a segment
+  int32_t min_units;         // of a CTA
+  // Shared prefix.  Its own pass takes all rows as one segment (`whole`, S = 1) and
+  // writes raw_o, raw_lse; the sequences' pass joins them with its own result.
+  const int32_t *whole;      // null, or the word that holds the rows' number
+  float *raw_o, *raw_lse;    // [T][Hq][D] and [T][Hq], base 2, or null
+  const float *pre_o, *pre_lse;
+  const int32_t *prefix_len; // checked by the sequences' pass, too
+  int64_t prefix_capacity;
+  // Partial results: two of each CTA, rows of a tile each.
+  float *part_o, *part_lse;
+  Desc *desc;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// m16n8k16 with half operands.
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// One sequence of the call: rows row0 .. row0+n-1, len tokens.
+struct Seq {
+  int row0, n, len;
+};
+__device__ __forceinline__ Seq load_seq(const AttnArgs &a, int s) {
+  if (a.whole) return {0, *a.whole, *a.rows.lens};
+  const int lo = a.rows.offsets[s];
+  return {lo, a.rows.offsets[s + 1] - lo, a.rows.lens[s]};
+}
+
+// Tokens that rows up to `row` (token times G + head) of a sequence see.
+__device__ __forceinline__ int tokens_seen(const AttnArgs &a, const Seq &q, int row) {
+  if (!a.causal) return q.len;
+  const int end = q.len - q.n + divide(row, a.group) + 1;
+  return end < 0 ? 0 : end > q.len ? q.len : end;
+}
+
+// Tiles of BN tokens that row tile rt of BM rows goes through, one at least.
+template <int BM, int BN, bool TRIM>
+__device__ __forceinline__ int tiles_of(const AttnArgs &a, const Seq &q, int rt) {
+  int seen = q.len;
+  if (TRIM) {
+    const int last = min((rt + 1) * BM, q.n * a.G) - 1;
+    seen = tokens_seen(a, q, last);
+  }
+  return seen > 0 ? (seen + BN - 1) / BN : 1;
+}
+
+// Units of work (tiles) of a sequence on one K/V head; 0 where it has no rows or is
+// another kernel's.
+template <int BM, int BN, bool TRIM>
+__device__ __forceinline__ int64_t units_of(const AttnArgs &a, const Seq &q) {
+  const int64_t rows = static_cast<int64_t>(q.n) * a.G;
+  if (rows <= 0 || rows < a.row_lo || rows > a.row_hi) return 0;
+  const int rts = static_cast<int>((rows + BM - 1) / BM);
+  if (!TRIM || !a.causal)
+    return static_cast<int64_t>(rts) * tiles_of<BM, BN, false>(a, q, 0);
+  int64_t sum = 0;
+  for (int rt = 0; rt < rts; ++rt) sum += tiles_of<BM, BN, true>(a, q, rt);
+  return sum;
+}
+
+struct Share {
+  int64_t units, begin, end;  // all units; this CTA's
+  int64_t before;             // units of the sequences before `seq`
+  int32_t ctas, seq;          // CTAs that have work; the sequence where it begins
+  int32_t ok;
+};
+
+__device__ __forceinline__ int64_t shfl_up64(int64_t v, int d) {
+  return __shfl_up_sync(0xffffffffu, v, d);
+}
+
+// All units in order (sequence, K/V head, row tile, token tile) are cut into equal
+// ranges, one for each CTA: every SM has the same work whatever the lengths are.
+// Checks the segments: where they cannot be used, nothing is to be done.
+template <int THREADS, int BM, int BN, bool TRIM>
+__device__ __forceinline__ Share share_out(const AttnArgs &a, Share *slot,
+                                           int64_t *warp_sums) {
+  constexpr int kPer = (kMaxSegments + THREADS - 1) / THREADS;
+  const int S = a.whole ? 1 : a.rows.S;
+  const int per = (S + THREADS - 1) / THREADS;
+  const int H = a.cache.heads;
+  int64_t u[kPer], sum = 0;
+  bool bad = false;
+  if (a.prefix_len) {
+    const int n = *a.prefix_len;
+    bad = n < 0 || n > a.prefix_capacity;
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int s = threadIdx.x * per + i;
+    u[i] = 0;
+    if (i < per && s < S) {
+      const Seq q = load_seq(a, s);
+      const bool off = q.row0 < 0 || q.n < 0 || q.n > a.rows.T - q.row0 || q.len < 0 ||
+                       q.len > a.rows.capacity || (s == 0 && q.row0 != 0) ||
+                       (!a.whole && q.n > a.max_rows);
+      bad |= off;
+      if (!off) u[i] = H * units_of<BM, BN, TRIM>(a, q);
+      sum += u[i];
+    }
+  }
+  bad = __syncthreads_or(bad);
+  if (bad) {
+    if (threadIdx.x == 0) atomicOr(a.rows.status, kStatusBadDeviceArg);
+    return {0, 0, 0, 0, 0, 0, 0};
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int64_t run = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t o = shfl_up64(run, d);
+    if (lane >= d) run += o;
+  }
+  if (lane == 31) warp_sums[warp] = run;
+  __syncthreads();
+  int64_t before = run - sum, total = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) before += warp_sums[w];
+    total += warp_sums[w];
+  }
+  const int64_t most = (total + a.min_units - 1) / a.min_units;
+  const int64_t ctas = most < gridDim.x ? most : gridDim.x;
+  if (blockIdx.x >= ctas) return {total, 0, 0, 0, static_cast<int>(ctas), 0, 1};
+  const int64_t begin = total * blockIdx.x / ctas;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (begin >= before && begin < before + u[i]) {
+      slot->seq = threadIdx.x * per + i;
+      slot->before = before;
+    }
+    before += u[i];
+  }
+  __syncthreads();
+  return {total, begin, total * (blockIdx.x + 1) / ctas, slot->before,
+          static_cast<int>(ctas), slot->seq, 1};
+}
+
+// The CTA whose range holds unit u.
+__device__ __forceinline__ int owner_of(const Share &sh, int64_t u) {
+  return static_cast<int>(((u + 1) * sh.ctas - 1) / sh.units);
+}
+
+// Where and how much a joined row weighs: own result and the prefix's.
+struct Weights {
+  float own, pre, lse;  // lse: base 2, of both
+};
+__device__ __forceinline__ Weights weigh(const AttnArgs &a, int64_t t, int hq, float lse) {
+  if (!a.pre_lse) return {1.0f, 0.0f, lse};
+  const float p = a.pre_lse[t * a.Hq + hq];
+  const float top = fmaxf(lse, p);
+  if (top == -INFINITY) return {0.0f, 0.0f, top};
+  const float x = exp2f(lse - top), y = exp2f(p - top), inv = 1.0f / (x + y);
+  return {x * inv, y * inv, top + log2f(x + y)};
+}
+
+// Writes N consecutive elements of a row's result, own ones in o, and where `d` is 0
+// its logarithm.
+template <int N>
+__device__ __forceinline__ void emit(const AttnArgs &a, int64_t t, int hq, int d,
+                                     const float (&o)[N], float lse, const Weights &w) {
+  if (a.raw_o) {
+    float *p = a.raw_o + (t * a.Hq + hq) * a.cache.D + d;
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = o[i];
+    if (d == 0) a.raw_lse[t * a.Hq + hq] = lse;
+    return;
+  }
+  uint16_t *p = a.out + t * a.ldo + hq * a.ldo_head + d;
+  const float *q = a.pre_o ? a.pre_o + (t * a.Hq + hq) * a.cache.D + d : nullptr;
+  uint32_t u[N / 2];
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    // A side without tokens has weight 0 and zeros.
+    const float x = q ? o[i] * w.own + q[i] * w.pre : o[i];
+    const float y = q ? o[i + 1] * w.own + q[i + 1] * w.pre : o[i + 1];
+    const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+    u[i / 2] = *reinterpret_cast<const uint32_t *>(&b);
+  }
+  if (a.out_vec && N % 8 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 2; i += 4)
+      *reinterpret_cast<uint4 *>(p + 2 * i) = make_uint4(u[i], u[i + 1], u[i + 2], u[i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = static_cast<uint16_t>(u[i / 2] >> (16 * (i & 1)));
+  }
+  if (d == 0 && a.lse) a.lse[t * a.ld_lse + hq] = w.lse * kLn2;
+}
+
+// Joins the partial results of items that several CTAs shared.
+fp8la_status launch_join(const AttnArgs &a, int BM, int DP, int ctas, int rows, cudaStream_t s);
+
+}  // namespace kv
+}  // namespace fp8la
