@@ -585,73 +585,89 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
 }
 
 // ---------------------------------------------------------------------- join
-// Joins the partial results of an item that several CTAs shared: CTA b began it
+// Joins the partial results of items that several CTAs shared: CTA b began it
 // (its second partial result), the next parts - 1 went on (their first ones).  A
-// block takes four rows, two warps each; rows are added in the CTAs' order.
+// block takes four rows at a time, two warps each; parts are added in the CTAs'
+// order.  Both kernels' items are joined in one launch.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinRows = 4;
 
+struct JoinSide {
+  const float *part_o, *part_lse;
+  const Desc *desc;
+  int32_t BM, ctas;
+};
+
 template <int DP>
 __global__ void __launch_bounds__(kJoinThreads)
-    kv_join_kernel(const AttnArgs a, const int BM) {
+    kv_join_kernel(const AttnArgs a, const JoinSide few, const JoinSide many) {
   constexpr int V = DP / 32;
   __shared__ float sums[kJoinRows][DP + 2];
   pdl_wait();
   pdl_launch_dependents();
-  const Desc d = a.desc[blockIdx.x];
+  const bool first = static_cast<int>(blockIdx.x) < few.ctas;
+  const int cta = blockIdx.x - (first ? 0 : few.ctas);
+  const float *part_o = first ? few.part_o : many.part_o;
+  const float *part_lse = first ? few.part_lse : many.part_lse;
+  const int BM = first ? few.BM : many.BM;
+  const Desc d = (first ? few.desc : many.desc)[cta];
   if (d.parts == 0) return;
   const Seq q = load_seq(a, d.s);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int side = warp & 1, slot = warp >> 1;
-  const int r = blockIdx.y * kJoinRows + slot;
-  const int rr = d.rt * BM + r;
-  const bool on = r < BM && rr < q.n * a.G;
-  auto part = [&](int i) {
-    return static_cast<int64_t>(2 * (static_cast<int>(blockIdx.x) + i) + (i == 0 ? 1 : 0)) * BM + r;
-  };
-  float best = -INFINITY, x[V] = {}, sum = 0.0f;
+  const int rows = min(BM, q.n * a.G - d.rt * BM);
   const int half = (d.parts + 1) / 2;
   const int i0 = side * half, i1 = min(d.parts, i0 + half);
-  if (on) {
-    for (int i = lane; i < d.parts; i += 32) best = fmaxf(best, a.part_lse[part(i)]);
+  for (int r0 = blockIdx.y * kJoinRows; r0 < rows; r0 += gridDim.y * kJoinRows) {
+    const int r = r0 + slot, rr = d.rt * BM + r;
+    const bool on = r < rows;
+    auto part = [&](int i) {
+      return static_cast<int64_t>(2 * (cta + i) + (i == 0 ? 1 : 0)) * BM + r;
+    };
+    float best = -INFINITY, x[V] = {}, sum = 0.0f;
+    if (on) {
+      for (int i = lane; i < d.parts; i += 32) best = fmaxf(best, part_lse[part(i)]);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
+      for (int o = 16; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
 #pragma unroll 4
-    for (int i = i0; i < i1; ++i) {
-      const float lse = a.part_lse[part(i)];
-      const float w = lse == -INFINITY ? 0.0f : exp2f(lse - best);
-      const float *p = a.part_o + part(i) * DP + lane * V;
-      float y[V];
-      if (V >= 4) {
+      for (int i = i0; i < i1; ++i) {
+        const float lse = part_lse[part(i)];
+        const float w = lse == -INFINITY ? 0.0f : exp2f(lse - best);
+        const float *p = part_o + part(i) * DP + lane * V;
+        float y[V];
+        if (V >= 4) {
 #pragma unroll
-        for (int j = 0; j < V; j += 4)
-          *reinterpret_cast<float4 *>(&y[j]) = *reinterpret_cast<const float4 *>(p + j);
-      } else {
-        *reinterpret_cast<float2 *>(&y[0]) = *reinterpret_cast<const float2 *>(p);
-      }
-      sum += w;
-      if (w != 0.0f) {
+          for (int j = 0; j < V; j += 4)
+            *reinterpret_cast<float4 *>(&y[j]) = *reinterpret_cast<const float4 *>(p + j);
+        } else {
+          *reinterpret_cast<float2 *>(&y[0]) = *reinterpret_cast<const float2 *>(p);
+        }
+        sum += w;
+        if (w != 0.0f) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) x[j] = fmaf(w, y[j], x[j]);
+          for (int j = 0; j < V; ++j) x[j] = fmaf(w, y[j], x[j]);
+        }
       }
     }
-  }
-  if (side == 1) {
+    if (side == 1) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) sums[slot][lane * V + j] = x[j];
-    if (lane == 0) sums[slot][DP] = sum;
-  }
-  __syncthreads();
-  if (!on || side == 1 || lane * V >= a.cache.D) return;
-  sum += sums[slot][DP];
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      for (int j = 0; j < V; ++j) sums[slot][lane * V + j] = x[j];
+      if (lane == 0) sums[slot][DP] = sum;
+    }
+    __syncthreads();
+    if (on && side == 0 && lane * V < a.cache.D) {
+      sum += sums[slot][DP];
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
-  for (int j = 0; j < V; ++j) x[j] = (x[j] + sums[slot][lane * V + j]) * inv;
-  const float lse = sum == 0.0f ? -INFINITY : best + log2f(sum);
-  const int t = divide(rr, a.group);
-  const int64_t row = static_cast<int64_t>(q.row0) + t;
-  const int hq = d.h * a.G + rr - t * a.G;
-  emit<V>(a, row, hq, lane * V, x, lse, weigh(a, row, hq, lse));
+      for (int j = 0; j < V; ++j) x[j] = (x[j] + sums[slot][lane * V + j]) * inv;
+      const float lse = sum == 0.0f ? -INFINITY : best + log2f(sum);
+      const int t = divide(rr, a.group);
+      const int64_t row = static_cast<int64_t>(q.row0) + t;
+      const int hq = d.h * a.G + rr - t * a.G;
+      emit<V>(a, row, hq, lane * V, x, lse, weigh(a, row, hq, lse));
+    }
+    __syncthreads();
+  }
 }
 
 template <typename Kern, typename... Args>
@@ -709,33 +725,93 @@ fp8la_status launch_few(const AttnArgs &a, bool f32, int format, int ctas, cudaS
                                      : launch_few_fmt<false, 1>(a, DP, 89, ctas, s);
 }
 
-// Workspace: partial results and their descriptions, then the prefix's results.
-struct Layout {
-  int64_t part_o, part_lse, desc, raw_o, raw_lse, bytes;
+// CTAs of the many-row kernel.
+int many_ctas() {
+  const int n = sm_count();
+  return n > 0 ? n : 1;
+}
+
+// Workspace: each kernel's partial results and their descriptions, then the prefix's
+// results.
+struct Part {
+  int64_t o, lse, desc;
 };
-Layout layout_of(int64_t T, int Hq, int D, int ctas, int BM, bool prefix) {
+struct Layout {
+  Part few, many;
+  int64_t raw_o, raw_lse, bytes;
+};
+Layout layout_of(int64_t T, int Hq, int D, bool prefix) {
   Layout l;
-  auto up = [](int64_t n) { return (n + 255) / 256 * 256; };
+  int64_t at = 0;
+  auto take = [&](int64_t n) {
+    const int64_t p = at;
+    at += (n + 255) / 256 * 256;
+    return p;
+  };
   const int DP = padded_dim(D);
-  l.part_o = 0;
-  l.part_lse = up(static_cast<int64_t>(2 * ctas) * BM * DP * 4);
-  l.desc = l.part_lse + up(static_cast<int64_t>(2 * ctas) * BM * 4);
-  l.raw_o = l.desc + up(static_cast<int64_t>(ctas) * sizeof(Desc));
-  l.raw_lse = l.raw_o + (prefix ? up(T * Hq * D * 4) : 0);
-  l.bytes = l.raw_lse + (prefix ? up(T * Hq * 4) : 0);
+  auto part = [&](int64_t ctas, int64_t BM) {
+    Part p;
+    p.o = take(2 * ctas * BM * DP * 4);
+    p.lse = take(2 * ctas * BM * 4);
+    p.desc = take(ctas * static_cast<int64_t>(sizeof(Desc)));
+    return p;
+  };
+  l.few = part(few_ctas(false, DP), kRows);
+  l.many = part(DP <= 128 ? many_ctas() : 0, kTcItemRows);
+  l.raw_o = take(prefix ? T * Hq * D * 4 : 0);
+  l.raw_lse = take(prefix ? T * Hq * 4 : 0);
+  l.bytes = at;
   return l;
+}
+
+// Rows (tokens times heads of a group) of a sequence up to which it takes mma.sync.
+constexpr int64_t kFewRows = 64;
+
+fp8la_status launch_join(const AttnArgs &a, const JoinSide &few, const JoinSide &many, int DP,
+                         int64_t rows, cudaStream_t s) {
+  // Rows in turn where there are many: most blocks find nothing to join.
+  const int64_t most = many.ctas > 0 ? 32 : kRows;
+  const int64_t y = ((rows < most ? rows : most) + kJoinRows - 1) / kJoinRows;
+  const dim3 grid(few.ctas + many.ctas, static_cast<unsigned>(y));
+  if (DP == 64) return launch(kv_join_kernel<64>, grid, kJoinThreads, 0, s, a, few, many);
+  if (DP == 128) return launch(kv_join_kernel<128>, grid, kJoinThreads, 0, s, a, few, many);
+  return launch(kv_join_kernel<256>, grid, kJoinThreads, 0, s, a, few, many);
+}
+
+// One pass over all sequences whose rows are at most max_rows (times G): the many-row
+// kernel for those with more than kFewRows, the few-row kernel for the others, the join.
+fp8la_status launch_pass(AttnArgs a, const Layout &l, uint8_t *ws, bool f32, int format,
+                         int64_t max_rows, cudaStream_t s) {
+  const int DP = padded_dim(a.cache.D);
+  const bool tc = DP <= 128 && max_rows > kFewRows;
+  // All rows of a prefix are one sequence, which is all of one kernel's.
+  const bool both = !(a.whole && tc);
+  JoinSide few = {}, many = {};
+  fp8la_status st = FP8LA_OK;
+  auto use = [&](const Part &p, int BM, int ctas) {
+    a.part_o = reinterpret_cast<float *>(ws + p.o);
+    a.part_lse = reinterpret_cast<float *>(ws + p.lse);
+    a.desc = reinterpret_cast<Desc *>(ws + p.desc);
+    return JoinSide{a.part_o, a.part_lse, a.desc, BM, ctas};
+  };
+  if (tc) {
+    many = use(l.many, kTcItemRows, many_ctas());
+    a.row_lo = both ? kFewRows + 1 : 0;
+    a.row_hi = INT64_MAX;
+    st = launch_many(a, f32, format, many.ctas, s);
+  }
+  if (st == FP8LA_OK && both) {
+    few = use(l.few, kRows, few_ctas(f32, DP));
+    a.row_lo = 0;
+    a.row_hi = tc ? kFewRows : INT64_MAX;
+    st = launch_few(a, f32, format, few.ctas, s);
+  }
+  return st == FP8LA_OK ? launch_join(a, few, many, DP, max_rows, s) : st;
 }
 
 constexpr int64_t kMaxRowHeads = (int64_t(1) << 31) - (int64_t(1) << 20);
 
 }  // namespace
-
-fp8la_status launch_join(const AttnArgs &a, int BM, int DP, int ctas, int rows, cudaStream_t s) {
-  const dim3 grid(ctas, ((rows < BM ? rows : BM) + kJoinRows - 1) / kJoinRows);
-  if (DP == 64) return launch(kv_join_kernel<64>, grid, kJoinThreads, 0, s, a, BM);
-  if (DP == 128) return launch(kv_join_kernel<128>, grid, kJoinThreads, 0, s, a, BM);
-  return launch(kv_join_kernel<256>, grid, kJoinThreads, 0, s, a, BM);
-}
 
 }  // namespace kv
 }  // namespace fp8la
@@ -751,8 +827,7 @@ int64_t fp8_kv_attention_workspace_bytes(int64_t rows, int32_t num_heads, int32_
   if (head_dim % 16 != 0 || head_dim > kMaxHeadDim || rows * num_heads >= kMaxRowHeads ||
       rows > INT32_MAX)
     return FP8LA_ERR_UNSUPPORTED;
-  const int ctas = few_ctas(false, padded_dim(head_dim));
-  return layout_of(rows, num_heads, head_dim, ctas, kRows, prefix != 0).bytes;
+  return layout_of(rows, num_heads, head_dim, prefix != 0).bytes;
 }
 
 fp8la_status fp8_kv_attention(const void *q, int32_t q_dtype, int64_t ld_q, int64_t ld_q_head,
@@ -799,9 +874,7 @@ fp8la_status fp8_kv_attention(const void *q, int32_t q_dtype, int64_t ld_q, int6
   if (!a.rows.status) return FP8LA_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool f32 = q_dtype == FP8LA_TYPE_F32;
-  const int DP = padded_dim(D);
-  const int ctas = few_ctas(f32, DP);
-  const Layout l = layout_of(rows, num_heads, D, few_ctas(false, DP), kRows, prefix);
+  const Layout l = layout_of(rows, num_heads, D, prefix);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   a.q = q;
   a.ldq = rows > 1 ? ld_q : 0;
@@ -818,13 +891,7 @@ fp8la_status fp8_kv_attention(const void *q, int32_t q_dtype, int64_t ld_q, int6
   a.causal = causal != 0;
   a.scale_log2 = scale * kLog2e;
   a.max_rows = max_rows;
-  a.row_lo = 0;
-  a.row_hi = INT64_MAX;
   a.min_units = 1;
-  a.part_o = reinterpret_cast<float *>(ws + l.part_o);
-  a.part_lse = reinterpret_cast<float *>(ws + l.part_lse);
-  a.desc = reinterpret_cast<Desc *>(ws + l.desc);
-  const int64_t row_heads = rows * a.G;
   if (prefix) {
     AttnArgs p = a;
     p.whole = m_offsets + num_segments;
@@ -837,18 +904,15 @@ fp8la_status fp8_kv_attention(const void *q, int32_t q_dtype, int64_t ld_q, int6
     p.causal = 0;
     p.raw_o = reinterpret_cast<float *>(ws + l.raw_o);
     p.raw_lse = reinterpret_cast<float *>(ws + l.raw_lse);
-    st = launch_few(p, f32, cache->format, ctas, s);
-    if (st != FP8LA_OK) return st;
-    st = launch_join(p, kRows, DP, ctas, row_heads < kRows ? static_cast<int>(row_heads) : kRows, s);
+    st = launch_pass(p, l, ws, f32, cache->format, rows * a.G, s);
     if (st != FP8LA_OK) return st;
     a.pre_o = p.raw_o;
     a.pre_lse = p.raw_lse;
     a.prefix_len = prefix_len;
     a.prefix_capacity = p.rows.capacity;
   }
-  st = launch_few(a, f32, cache->format, ctas, s);
-  if (st != FP8LA_OK) return st;
-  return launch_join(a, kRows, DP, ctas, row_heads < kRows ? static_cast<int>(row_heads) : kRows, s);
+  const int64_t longest = (max_rows < rows ? max_rows : rows) * a.G;
+  return launch_pass(a, l, ws, f32, cache->format, longest, s);
 }
 
 }  // extern "C"

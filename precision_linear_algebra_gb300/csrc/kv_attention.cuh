@@ -237,8 +237,9 @@ __device__ __forceinline__ void emit(const AttnArgs &a, int64_t t, int hq, int d
   if (d == 0 && a.lse) a.lse[t * a.ld_lse + hq] = w.lse * kLn2;
 }
 
-// Joins the partial results of items that several CTAs shared.
-fp8la_status launch_join(const AttnArgs &a, int BM, int DP, int ctas, int rows, cudaStream_t s);
+// Rows from which a sequence takes the tensor cores of kv_attention_tc.cu.
+constexpr int kTcItemRows = 256;
+fp8la_status launch_many(const AttnArgs &a, bool f32, int format, int ctas, cudaStream_t s);
 
 }  // namespace kv
 }  // namespace fp8la
