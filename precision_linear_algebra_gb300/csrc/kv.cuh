@@ -95,6 +95,18 @@ struct Format {
   static __device__ __forceinline__ bool finite(uint32_t code) {
     return FMT == 0 ? (code & 0x7fu) != 0x7fu : (code & 0x7cu) != 0x7cu;
   }
+  // The top bit of each of four codes that is not finite.
+  static __device__ __forceinline__ uint32_t not_finite4(uint32_t codes) {
+    return (FMT == 0 ? (codes & 0x7f7f7f7fu) + 0x01010101u
+                     : (codes & 0x7c7c7c7cu) + 0x04040404u) &
+           0x80808080u;
+  }
+  // Takes them out; whether there were any.
+  static __device__ __forceinline__ bool clear4(uint32_t &codes) {
+    const uint32_t m = not_finite4(codes);
+    if (m) codes &= ~((m >> 7) * 255u);
+    return m != 0;
+  }
 };
 
 // Two codes as halves: exact for both formats.

@@ -160,45 +160,35 @@ __device__ __forceinline__ void load_q(const AttnArgs &a, int64_t at, bool on, f
 
 template <bool F32Q, int FMT, int DP>
 __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
-    kv_attention_kernel(const AttnArgs a) {
+    kv_attention_kernel(const __grid_constant__ AttnArgs a) {
   using C = Cfg<F32Q, DP>;
   using Fm = Format<FMT>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ Share share_slot;
+  __shared__ Share sh;
   __shared__ int64_t warp_sums[kWarps];
+  __shared__ Walk walk;
+  __shared__ Item it;
+  __shared__ int more;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   pdl_wait();
   pdl_launch_dependents();
   if (threadIdx.x == 0 && a.desc) a.desc[blockIdx.x].parts = 0;
-  const Share sh = share_out<kThreads, kRows, kTile, false>(a, &share_slot, warp_sums);
+  share_out<kThreads, kRows, kTile>(a, &sh, warp_sums);
   const Cache &kc = a.cache;
   const uint32_t ring = smem_addr(smem) + warp * C::kRing;
   const uint32_t qsm = smem_addr(smem) + C::kQ;
 
-  int64_t at = sh.begin, before = sh.before;
-  int s = sh.seq;
-  while (at < sh.end) {
-    // The item that holds unit `at`.
-    Seq q = load_seq(a, s);
-    int64_t units = units_of<kRows, kTile, false>(a, q);
-    while (at >= before + units * kc.heads) {
-      before += units * kc.heads;
-      q = load_seq(a, ++s);
-      units = units_of<kRows, kTile, false>(a, q);
-    }
-    const int NT = tiles_of<kRows, kTile, false>(a, q, 0);
-    const int rts = (q.n * a.G + kRows - 1) / kRows;
-    const int64_t local = at - before;
-    const int64_t item = local / NT;
-    const int tile0 = static_cast<int>(local - item * NT);
-    const int h = static_cast<int>(item / rts), rt = static_cast<int>(item - static_cast<int64_t>(h) * rts);
-    const int count = static_cast<int>(min(static_cast<int64_t>(NT - tile0), sh.end - at));
-    at += count;
+  if (threadIdx.x == 0) start_walk<kRows>(a, sh, &walk);
+  for (;;) {
+    if (threadIdx.x == 0) more = next_item<kRows, kTile>(a, &walk, &it);
+    __syncthreads();
+    if (!more) break;
+    const Seq q = it.q;
+    const int s = it.s, h = it.h, rt = it.rt, tile0 = it.tile0, count = it.count, rows = it.rows;
 
     // This lane's rows are rt * 16 + g and that + 8; they see the tokens below
     // seen[0] and seen[1].  Tokens from `all` on are not seen by every row.
-    const int rows = min(kRows, q.n * a.G - rt * kRows);
     int tok[2], head[2], seen[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -349,7 +339,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
         const bool fine = v > 0.0f && v < INFINITY;
         const bool in = base + lane < end;
         sts_f(scales + 64 + 4 * lane, !in ? 0.0f : fine ? log2f(v) - e0 : NAN);
-        sts_f(scales + 128 + 4 * lane, !in ? 0.0f : fine ? __fdiv_rn(power_of_two(e0), v) : NAN);
+        // A bad scale is in the exponent alone: rows that do not see it have weight 0.
+        sts_f(scales + 128 + 4 * lane,
+              fine ? fminf(__fdiv_rn(power_of_two(e0), v), 3.0e38f) : 1.0f);
       }
       // Scores of tokens g and 8 + g against the 16 rows.
       float sc[2][4] = {};
@@ -440,10 +432,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           w[i][k] = ex2(sc[i][k] - top[k >> 1]);
-          float p = w[i][k] * iv[i][k & 1];
-          // 1 / vs of a token that the row does not see may be anything.
-          if (edge && sc[i][k] == -INFINITY) p = 0.0f;
-          l[k >> 1] += p;
+          l[k >> 1] = fmaf(w[i][k], iv[i][k & 1], l[k >> 1]);
         }
       const uint32_t pf[4] = {pack_half(w[0][0], w[0][1]), pack_half(w[0][2], w[0][3]),
                               pack_half(w[1][0], w[1][1]), pack_half(w[1][2], w[1][3])};
@@ -466,13 +455,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
           }
           if (partial) {
 #pragma unroll
-            for (int j = 0; j < C::VW / 4; ++j)
-#pragma unroll
-              for (int b = 0; b < 4; ++b)
-                if (!Fm::finite(vw[i][j] >> (8 * b))) {
-                  vw[i][j] &= ~(0xffu << (8 * b));
-                  poison = true;
-                }
+            for (int j = 0; j < C::VW / 4; ++j) poison |= Fm::clear4(vw[i][j]);
           }
         }
 #pragma unroll
@@ -537,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
             sum > 0.0f || sum != sum ? M[k] - kShift + log2f(sum) : -INFINITY;
     }
     __syncthreads();
-    const bool whole = count == NT;
+    const bool whole = count == it.tiles;
     const int part = 2 * blockIdx.x + (tile0 > 0 ? 0 : 1);
     constexpr int kPieces = DP / 8;
     for (int i = threadIdx.x; i < rows * kPieces; i += kThreads) {
@@ -579,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
       }
     }
     if (threadIdx.x == 0 && !whole && tile0 == 0)
-      a.desc[blockIdx.x] = {s, h, rt, owner_of(sh, at - count + NT - 1) - static_cast<int>(blockIdx.x) + 1};
+      a.desc[blockIdx.x] = {s, h, rt, owner_of(sh, it.begin + it.tiles - 1) - static_cast<int>(blockIdx.x) + 1};
     __syncthreads();  // the results overlay the rings
   }
 }

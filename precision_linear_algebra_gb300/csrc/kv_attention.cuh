@@ -83,79 +83,100 @@ __device__ __forceinline__ int tokens_seen(const AttnArgs &a, const Seq &q, int 
 }
 
 // Tiles of BN tokens that row tile rt of BM rows goes through, one at least.
-template <int BM, int BN, bool TRIM>
+template <int BM, int BN>
 __device__ __forceinline__ int tiles_of(const AttnArgs &a, const Seq &q, int rt) {
-  int seen = q.len;
-  if (TRIM) {
-    const int last = min((rt + 1) * BM, q.n * a.G) - 1;
-    seen = tokens_seen(a, q, last);
-  }
-  return seen > 0 ? (seen + BN - 1) / BN : 1;
+  const int last = min((rt + 1) * BM, q.n * a.G) - 1;
+  const int seen = tokens_seen(a, q, last);
+  return seen > 0 ? (seen - 1) / BN + 1 : 1;
 }
 
-// Units of work (tiles) of a sequence on one K/V head; 0 where it has no rows or is
-// another kernel's.
-template <int BM, int BN, bool TRIM>
-__device__ __forceinline__ int64_t units_of(const AttnArgs &a, const Seq &q) {
+// Sum over i < n of floor((x i + b) / m), x, b >= 0, m > 0: whole parts first, then
+// the lattice points under the line counted along the other axis.
+__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t x, int64_t b) {
+  int64_t sum = 0;
+  for (;;) {
+    sum += n * (n - 1) / 2 * (x / m) + n * (b / m);
+    x %= m;
+    b %= m;
+    const int64_t y = x * n + b;
+    if (y < m) return sum;
+    n = y / m;
+    b = y % m;
+    const int64_t t = m;
+    m = x;
+    x = t;
+  }
+}
+
+// Tiles of the row tiles below R of a sequence with `rts` of them.  Row tile rt but the
+// last one sees len - n + floor(((rt + 1) BM - 1) / G) + 1 tokens, which makes floor((G
+// (len - n + BN) + (rt + 1) BM - 1) / (BN G)) tiles, and one where that is less.
+template <int BM, int BN>
+__device__ __noinline__ int64_t units_below(const AttnArgs &a, const Seq &q, int rts, int R) {
+  if (!a.causal) return static_cast<int64_t>(R) * tiles_of<BM, BN>(a, q, 0);
+  int64_t sum = 0;
+  if (R == rts) sum += tiles_of<BM, BN>(a, q, --R);
+  const int64_t G = a.G, c = static_cast<int64_t>(q.len) - q.n;
+  int64_t k = c < 0 ? -G * c / BM : 0;
+  if (k > R) k = R;
+  return sum + k + floor_sum(R - k, BN * G, BM, G * (c + BN) + (k + 1) * BM - 1);
+}
+
+// Row tiles of a sequence; 0 where it has no rows or is another kernel's.
+template <int BM>
+__device__ __forceinline__ int row_tiles_of(const AttnArgs &a, const Seq &q) {
   const int64_t rows = static_cast<int64_t>(q.n) * a.G;
   if (rows <= 0 || rows < a.row_lo || rows > a.row_hi) return 0;
-  const int rts = static_cast<int>((rows + BM - 1) / BM);
-  if (!TRIM || !a.causal)
-    return static_cast<int64_t>(rts) * tiles_of<BM, BN, false>(a, q, 0);
-  int64_t sum = 0;
-  for (int rt = 0; rt < rts; ++rt) sum += tiles_of<BM, BN, true>(a, q, rt);
-  return sum;
+  return static_cast<int>((rows + BM - 1) / BM);
 }
 
 struct Share {
-  int64_t units, begin, end;  // all units; this CTA's
-  int64_t before;             // units of the sequences before `seq`
-  int32_t ctas, seq;          // CTAs that have work; the sequence where it begins
-  int32_t ok;
+  int64_t units, begin, end;   // all units; this CTA's
+  int32_t ctas;                // that have work
+  int32_t s, h, rt, tile;      // where this CTA begins
 };
 
 __device__ __forceinline__ int64_t shfl_up64(int64_t v, int d) {
   return __shfl_up_sync(0xffffffffu, v, d);
 }
 
-// All units in order (sequence, K/V head, row tile, token tile) are cut into equal
-// ranges, one for each CTA: every SM has the same work whatever the lengths are.
-// Checks the segments: where they cannot be used, nothing is to be done.
-template <int THREADS, int BM, int BN, bool TRIM>
-__device__ __forceinline__ Share share_out(const AttnArgs &a, Share *slot,
-                                           int64_t *warp_sums) {
-  constexpr int kPer = (kMaxSegments + THREADS - 1) / THREADS;
+// All units (tiles) in the order (sequence, K/V head, row tile, token tile) are cut
+// into equal ranges, one for each CTA: every SM has the same work whatever the lengths
+// are.  Checks the segments: where they cannot be used, nothing is to be done.
+template <int THREADS, int BM, int BN>
+__device__ __noinline__ void share_out(const AttnArgs &a, Share *sh, int64_t *warp_sums) {
   const int S = a.whole ? 1 : a.rows.S;
   const int per = (S + THREADS - 1) / THREADS;
   const int H = a.cache.heads;
-  int64_t u[kPer], sum = 0;
+  const int s0 = min(S, static_cast<int>(threadIdx.x) * per), s1 = min(S, s0 + per);
+  int64_t sum = 0;
   bool bad = false;
   if (a.prefix_len) {
     const int n = *a.prefix_len;
     bad = n < 0 || n > a.prefix_capacity;
   }
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int s = threadIdx.x * per + i;
-    u[i] = 0;
-    if (i < per && s < S) {
-      const Seq q = load_seq(a, s);
-      const bool off = q.row0 < 0 || q.n < 0 || q.n > a.rows.T - q.row0 || q.len < 0 ||
-                       q.len > a.rows.capacity || (s == 0 && q.row0 != 0) ||
-                       (!a.whole && q.n > a.max_rows);
-      bad |= off;
-      if (!off) u[i] = H * units_of<BM, BN, TRIM>(a, q);
-      sum += u[i];
-    }
+#pragma unroll 1
+  for (int s = s0; s < s1; ++s) {
+    const Seq q = load_seq(a, s);
+    const bool off = q.row0 < 0 || q.n < 0 || q.n > a.rows.T - q.row0 || q.len < 0 ||
+                     q.len > a.rows.capacity || (s == 0 && q.row0 != 0) ||
+                     (!a.whole && q.n > a.max_rows);
+    bad |= off;
+    const int rts = off ? 0 : row_tiles_of<BM>(a, q);
+    if (rts > 0) sum += H * units_below<BM, BN>(a, q, rts, rts);
   }
   bad = __syncthreads_or(bad);
   if (bad) {
-    if (threadIdx.x == 0) atomicOr(a.rows.status, kStatusBadDeviceArg);
-    return {0, 0, 0, 0, 0, 0, 0};
+    if (threadIdx.x == 0) {
+      atomicOr(a.rows.status, kStatusBadDeviceArg);
+      *sh = {0, 0, 0, 0, 0, 0, 0, 0};
+    }
+    __syncthreads();
+    return;
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int64_t run = sum;
-#pragma unroll
+#pragma unroll 1
   for (int d = 1; d < 32; d <<= 1) {
     const int64_t o = shfl_up64(run, d);
     if (lane >= d) run += o;
@@ -163,31 +184,111 @@ __device__ __forceinline__ Share share_out(const AttnArgs &a, Share *slot,
   if (lane == 31) warp_sums[warp] = run;
   __syncthreads();
   int64_t before = run - sum, total = 0;
-#pragma unroll
+#pragma unroll 1
   for (int w = 0; w < THREADS / 32; ++w) {
     if (w < warp) before += warp_sums[w];
     total += warp_sums[w];
   }
   const int64_t most = (total + a.min_units - 1) / a.min_units;
-  const int64_t ctas = most < gridDim.x ? most : gridDim.x;
-  if (blockIdx.x >= ctas) return {total, 0, 0, 0, static_cast<int>(ctas), 0, 1};
-  const int64_t begin = total * blockIdx.x / ctas;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    if (begin >= before && begin < before + u[i]) {
-      slot->seq = threadIdx.x * per + i;
-      slot->before = before;
+  const int ctas = static_cast<int>(most < gridDim.x ? most : gridDim.x);
+  const bool idle = static_cast<int>(blockIdx.x) >= ctas;
+  const int64_t begin = idle ? 0 : total * blockIdx.x / ctas;
+  if (threadIdx.x == 0) {
+    sh->units = total;
+    sh->begin = begin;
+    sh->end = idle ? 0 : total * (blockIdx.x + 1) / ctas;
+    sh->ctas = ctas;
+  }
+  if (!idle && begin >= before && begin < before + sum) {
+    // The row tile that holds the unit: the last one with no more units below it.
+#pragma unroll 1
+    for (int s = s0;; ++s) {
+      const Seq q = load_seq(a, s);
+      const int rts = row_tiles_of<BM>(a, q);
+      if (rts == 0) continue;
+      const int64_t each = units_below<BM, BN>(a, q, rts, rts);
+      if (begin >= before + H * each) {
+        before += H * each;
+        continue;
+      }
+      const int h = static_cast<int>((begin - before) / each);
+      const int64_t left = begin - before - h * each;
+      int lo = 0, hi = rts - 1;
+#pragma unroll 1
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (units_below<BM, BN>(a, q, rts, mid) <= left) lo = mid;
+        else hi = mid - 1;
+      }
+      sh->s = s;
+      sh->h = h;
+      sh->rt = lo;
+      sh->tile = static_cast<int>(left - units_below<BM, BN>(a, q, rts, lo));
+      break;
     }
-    before += u[i];
   }
   __syncthreads();
-  return {total, begin, total * (blockIdx.x + 1) / ctas, slot->before,
-          static_cast<int>(ctas), slot->seq, 1};
 }
 
 // The CTA whose range holds unit u.
 __device__ __forceinline__ int owner_of(const Share &sh, int64_t u) {
   return static_cast<int>(((u + 1) * sh.ctas - 1) / sh.units);
+}
+
+// Tiles tile0 .. tile0+count-1 of the `tiles` of a row tile with `rows` rows; begin: the
+// first of them, among all units.
+struct Item {
+  Seq q;
+  int s, h, rt, tile0, count, tiles, rows;
+  int64_t begin;
+};
+
+// Walks through a CTA's items.
+struct Walk {
+  int64_t at, end;
+  int s, h, rt, tile, rts;
+  Seq q;
+};
+template <int BM>
+__device__ __noinline__ void start_walk(const AttnArgs &a, const Share &sh, Walk *w) {
+  w->at = sh.begin;
+  w->end = sh.end;
+  w->s = sh.s;
+  w->h = sh.h;
+  w->rt = sh.rt;
+  w->tile = sh.tile;
+  if (w->at < w->end) {
+    w->q = load_seq(a, w->s);
+    w->rts = row_tiles_of<BM>(a, w->q);
+  }
+}
+template <int BM, int BN>
+__device__ __noinline__ bool next_item(const AttnArgs &a, Walk *w, Item *it) {
+  if (w->at >= w->end) return false;
+  if (w->rt >= w->rts) {
+    w->rt = 0;
+    if (++w->h >= a.cache.heads) {
+      w->h = 0;
+      do {
+        w->q = load_seq(a, ++w->s);
+        w->rts = row_tiles_of<BM>(a, w->q);
+      } while (w->rts == 0);
+    }
+  }
+  const int tiles = tiles_of<BM, BN>(a, w->q, w->rt);
+  it->q = w->q;
+  it->s = w->s;
+  it->h = w->h;
+  it->rt = w->rt;
+  it->tile0 = w->tile;
+  it->tiles = tiles;
+  it->begin = w->at - w->tile;
+  it->count = static_cast<int>(min(static_cast<int64_t>(tiles - w->tile), w->end - w->at));
+  it->rows = min(BM, w->q.n * a.G - w->rt * BM);
+  w->at += it->count;
+  w->tile = 0;
+  ++w->rt;
+  return true;
 }
 
 // Where and how much a joined row weighs: own result and the prefix's.
