@@ -6,15 +6,22 @@
 // two tiles of 128, against tiles of 128 tokens, so that one tile's products run
 // while the other's weights are made:
 //
-//   warps 0-3, 4-7   a tile of rows each, one row a thread: scores from tensor
-//                    memory, running maximum, weights as halves back over them
-//   warps 8-11       K's and V's codes from the cache (any pages, 16 bytes a load) to
-//                    halves in shared memory, swizzled as the MMA reads them: K with
-//                    D along its rows, V the same, read as the transposed operand
-//   warp 12          issues the MMAs: S = Q K^T from shared memory, O += P V with P in
+//   warps 0-3, 4-7   a tile of rows each: scores from tensor memory, running maximum,
+//                    weights as halves back over them; before that the tile's rows of q,
+//                    scaled by a power of two to halves (an FP32 row as two terms), in
+//                    place over what cp.async brought while the last tile of the rows
+//                    before was at work
+//   warps 8-12       codes from the cache (16 bytes a copy) to halves in shared memory,
+//                    swizzled as the MMA reads them, 16 tokens of K or V at a time; V is
+//                    read as the transposed operand
+//   warps 13, 14     where the tokens lie (any pages), K's scales and V's
+//   warp 15          issues the MMAs: S = Q K^T from shared memory, O += P V with P in
 //                    tensor memory
-//   warps 13-15      the next rows of q, scaled by a power of two to halves (an FP32
-//                    row as two terms), in place over what cp.async brought
+//
+// Four warps an SM partition do four different things, so what bounds the loops is
+// first of all the fetching of their instructions: they are kept short (the first
+// version's unrolled ones did not fit the instruction cache and took 863 us instead of
+// what is below).
 //
 // Tensor memory: S (and P over it) and O of both tiles, 512 columns with D = 128.
 // O stays there; a row's is rescaled only where its maximum grew by 2^8.
@@ -32,12 +39,13 @@ constexpr int kThreads = 512;
 constexpr int kRows = 128;          // of a tile
 constexpr int kItemRows = 256;
 constexpr int kTokens = 128;        // of a tile
+constexpr int kConverters = 5;
+constexpr int kGroup = 16;          // tokens of a converter's job
+constexpr int kJobs = 2 * kTokens / kGroup;  // of a tile, K's first
 constexpr int kScaleBufs = 4;       // K's scales, log2 and reciprocal of V's, an exponent
 constexpr int kScaleBytes = 3 * kTokens * 4 + 16;
 constexpr float kShift = 7.0f;      // as in kv_attention.cu
 constexpr float kLazy = 8.0f;
-constexpr int kQWarps = 3;
-
 template <int DP, int TERMS>
 struct Cfg {
   static constexpr int kBlock = kRows * 128;            // 64 elements of each row
@@ -45,14 +53,15 @@ struct Cfg {
   static constexpr int kQ = 2 * TERMS * kTileBytes;
   static constexpr int SLOTS = TERMS == 1 ? 3 : 2;      // K's and V's tiles in turn
   static constexpr int kRing = kQ;
-  // Codes under way, in units of half a tile: K, K, V, V of the next tile, or two.
-  static constexpr int UNITS = TERMS == 1 ? 4 : 2;
-  static constexpr int kUnit = kTokens / 2 * DP;
+  // Jobs of a converter whose codes are under way.
+  static constexpr int AHEAD = TERMS == 1 ? 3 : 1;
+  static constexpr int kJob = kGroup * DP;
   static constexpr int kRaw = kRing + SLOTS * kTileBytes;
-  static constexpr int kScales = kRaw + UNITS * kUnit;
+  static constexpr int kPlaces = kRaw + kConverters * AHEAD * kJob;
+  static constexpr int kScales = kPlaces + kScaleBufs * kTokens * 8;
   static constexpr int kFactors = kScales + kScaleBufs * kScaleBytes;
-  static constexpr int kBar = kFactors + 2 * kItemRows * 4;
-  static constexpr int kBars = 2 * SLOTS + 2 * kScaleBufs + 19;
+  static constexpr int kBar = kFactors + kItemRows * 4;
+  static constexpr int kBars = 2 * SLOTS + 4 * kScaleBufs + 14;
   static constexpr int kMisc = kBar + kBars * 8;
   static constexpr int kAlloc = kMisc + 16 + 1024;
   static constexpr int kS = 0, kO = 256;                // tensor memory columns
@@ -108,19 +117,13 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t block) {
   return d;
 }
 
-// 32 columns of this thread's lane, without a wait.
-__device__ __forceinline__ void tmem_load32(uint32_t addr, float *r) {
+// 8 columns of this thread's lane.
+__device__ __forceinline__ void tmem_load8(uint32_t addr, float (&r)[8]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-      "%30, %31}, [%32];"
-      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]),
-        "=f"(r[6]), "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]),
-        "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]), "=f"(r[17]),
-        "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]),
-        "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]),
-        "=f"(r[30]), "=f"(r[31])
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
+        "=f"(r[7])
       : "r"(addr)
       : "memory");
 }
@@ -137,9 +140,26 @@ __device__ __forceinline__ void tmem_wait32(float *r) {
       : "memory");
   asm volatile("" : "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31])::"memory");
 }
-__device__ __forceinline__ void tmem_store32(uint32_t addr, const float *r) {
+// 16 lanes of 64 columns: registers 4 i + {0, 1} hold this thread's row (lane / 4) in
+// columns 8 i + 2 (lane % 4) + {0, 1}, registers 4 i + {2, 3} the row 8 further.
+__device__ __forceinline__ void tmem_load_rows(uint32_t addr, float *r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]),
+        "=f"(r[6]), "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]),
+        "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]), "=f"(r[17]),
+        "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]),
+        "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]),
+        "=f"(r[30]), "=f"(r[31])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store_rows(uint32_t addr, const float *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x8.b32 [%32], "
       "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
       "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
       "%30, %31};"
@@ -151,9 +171,11 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const float *r) {
         "r"(addr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&r)[16]) {
+// 16 lanes of 32 columns, a pair of halves each: registers 2 i and 2 i + 1 hold columns
+// 4 i + lane % 4 of the rows lane / 4 and 8 further.
+__device__ __forceinline__ void tmem_store_halves(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%16], "
       "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};"
       ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
         "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
@@ -208,7 +230,122 @@ __device__ __forceinline__ float power_of_two(int e) {
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-// Columns k .. k+31 of V that hold a code that is not finite at a token that a row sees,
+// A warp's 32 rows of q, 8 elements of a row a lane: copied to where their halves will be,
+// element 8 s of row r in chunk s % 8, swizzled by the row, of block s / 8.  Rows and
+// columns that there are not become zeros.
+template <int DP>
+__device__ __forceinline__ uint32_t q_chunk(uint32_t q_at, int r, int sub) {
+  return q_at + sub / 8 * (kRows * 128) + r * 128 + (((sub & 7) ^ (r & 7)) << 4);
+}
+template <bool F32Q, int DP>
+__device__ __noinline__ void fetch_q(const AttnArgs &a, const Item &it, uint32_t q_at, int row0) {
+  constexpr int TERMS = F32Q ? 2 : 1, SIZE = F32Q ? 4 : 2;
+  constexpr int LR = DP / 8, RP = 32 / LR;    // lanes of a row, rows of a pass
+  constexpr int kTerm = DP / 64 * kRows * 128;
+  const int lane = threadIdx.x & 31, sub = lane % LR;
+  const bool vec = (reinterpret_cast<uintptr_t>(a.q) & 15u) == 0 && a.ldq * SIZE % 16 == 0 &&
+                   a.ldq_head * SIZE % 16 == 0;
+  const int rows = it.rows, first = it.rt * kItemRows, head0 = it.h * a.G;
+  const int64_t token0 = it.q.row0;
+#pragma unroll 4
+  for (int i = 0; i < 32 / RP; ++i) {
+    const int r = i * RP + lane / LR;
+    const bool on = row0 + r < rows && 8 * sub < a.cache.D;
+    const int rr = first + min(row0 + r, rows - 1), tok = divide(rr, a.group);
+    const int64_t at = (token0 + tok) * a.ldq + (head0 + rr - tok * a.G) * a.ldq_head + 8 * sub;
+    const uint8_t *from = static_cast<const uint8_t *>(a.q) + (on ? at * SIZE : 0);
+    const uint32_t dst = q_chunk<DP>(q_at, r, sub);
+    if (vec || !on) {
+#pragma unroll
+      for (int term = 0; term < TERMS; ++term)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + term * kTerm),
+                     "l"(vec ? from + 16 * term : a.cache.k), "r"(on ? 16 : 0)
+                     : "memory");
+    } else if (F32Q) {
+      const uint32_t *p = reinterpret_cast<const uint32_t *>(from);
+      st_shared_v4(dst, p[0], p[1], p[2], p[3]);
+      st_shared_v4(dst + (TERMS - 1) * kTerm, p[4], p[5], p[6], p[7]);
+    } else {
+      const uint16_t *p = reinterpret_cast<const uint16_t *>(from);
+      st_shared_v4(dst, p[0] | p[1] << 16, p[2] | p[3] << 16, p[4] | p[5] << 16,
+                   p[6] | p[7] << 16);
+    }
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+// Waits for the rows (a lane reads what it copied), scales them to halves, and notes what
+// the scores are to be multiplied by.
+template <bool F32Q, int DP>
+__device__ __noinline__ void scale_q(const AttnArgs &a, uint32_t q_at, float *factors) {
+  constexpr int TERMS = F32Q ? 2 : 1;
+  constexpr int LR = DP / 8, RP = 32 / LR;
+  constexpr int kTerm = DP / 64 * kRows * 128;
+  const int lane = threadIdx.x & 31, sub = lane % LR;
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+#pragma unroll 1
+  for (int i = 0; i < 32 / RP; i += 4) {
+    // Four rows of a lane at a time, so that their steps overlap.
+    uint32_t w[4][TERMS][4];
+    float m[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      m[u] = 0.0f;
+#pragma unroll
+      for (int term = 0; term < TERMS; ++term) {
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[u][term][0]), "=r"(w[u][term][1]), "=r"(w[u][term][2]),
+                       "=r"(w[u][term][3])
+                     : "r"(q_chunk<DP>(q_at, (i + u) * RP + lane / LR, sub) + term * kTerm)
+                     : "memory");
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t b = w[u][term][e];
+          if (F32Q)
+            m[u] = fmaxf(m[u], fabsf(__uint_as_float(b)));
+          else
+            m[u] = max3(m[u], fabsf(__uint_as_float(b << 16)),
+                        fabsf(__uint_as_float(b & 0xffff0000u)));
+        }
+      }
+    }
+#pragma unroll
+    for (int o = LR / 2; o > 0; o >>= 1)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) m[u] = fmaxf(m[u], __shfl_xor_sync(0xffffffffu, m[u], o));
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int r = (i + u) * RP + lane / LR;
+      const int e = min(max(8 - exponent_of(m[u]), -126), 126);
+      const float up = power_of_two(e);
+      uint32_t h[TERMS][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float x, y;
+        if (F32Q) {  // elements 2 k, 2 k + 1
+          x = __uint_as_float(w[u][(TERMS - 1) * (k >> 1)][2 * (k & 1)]) * up;
+          y = __uint_as_float(w[u][(TERMS - 1) * (k >> 1)][2 * (k & 1) + 1]) * up;
+        } else {
+          x = __uint_as_float(w[u][0][k] << 16) * up;
+          y = __uint_as_float(w[u][0][k] & 0xffff0000u) * up;
+        }
+        h[0][k] = pack_half(x, y);
+        if (TERMS == 2) {
+          const float2 f = half2_floats(h[0][k]);
+          h[TERMS - 1][k] = pack_half(x - f.x, y - f.y);
+        }
+      }
+#pragma unroll
+      for (int term = 0; term < TERMS; ++term)
+        st_shared_v4(q_chunk<DP>(q_at, r, sub) + term * kTerm, h[term][0], h[term][1],
+                     h[term][2], h[term][3]);
+      if (sub == 0) factors[r] = power_of_two(-e) * a.scale_log2;
+    }
+  }
+  __syncwarp();
+}
+
+// Columns k .. k+7 of V that hold a code that is not finite at a token that a row sees,
 // of the tiles that were written without such codes: those that not all rows see.
 template <typename Fm>
 __device__ __noinline__ uint32_t lost_columns(const AttnArgs &a, const Item &it, int seen, int k) {
@@ -222,11 +359,18 @@ __device__ __noinline__ uint32_t lost_columns(const AttnArgs &a, const Item &it,
     const uint8_t *codes = a.cache.v + page * a.cache.page_stride +
                            it.h * a.cache.head_stride +
                            (j - p * a.cache.page_size) * a.cache.token_stride;
-    for (int i = 0; i < 32 && k + i < a.cache.D; ++i)
+    for (int i = 0; i < 8; ++i)
       if (!Fm::finite(codes[k + i])) bad |= 1u << i;
   }
   return bad;
 }
+
+// What a thread keeps of its two rows: the scores' factor, the running maximum, the sum
+// of the weights (of even and odd columns).
+struct Rows16 {
+  float factor[2], M[2];
+  uint64_t l2[2];
+};
 
 // mbar_wait by a whole warp, out of line: the kernel waits in many places.
 __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, uint64_t timeout_ns,
@@ -246,33 +390,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t *sbase = smem_raw + (base - raw);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // The same in all lanes, which the compiler would not see otherwise.
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t bars = base + C::kBar;
   auto full_bar = [&](int i) { return bars + 8u * i; };                       // K or V
   auto empty_bar = [&](int i) { return bars + 8u * (C::SLOTS + i); };
   auto scfull_bar = [&](int i) { return bars + 8u * (2 * C::SLOTS + i); };    // scales
   auto scfree_bar = [&](int i) { return bars + 8u * (2 * C::SLOTS + kScaleBufs + i); };
-  const uint32_t rest = bars + 8u * (2 * C::SLOTS + 2 * kScaleBufs);
+  auto atfull_bar = [&](int i) { return bars + 8u * (2 * C::SLOTS + 2 * kScaleBufs + i); };
+  auto atfree_bar = [&](int i) { return bars + 8u * (2 * C::SLOTS + 3 * kScaleBufs + i); };
+  const uint32_t rest = bars + 8u * (2 * C::SLOTS + 4 * kScaleBufs);
   auto s_bar = [&](int t) { return rest + 8u * t; };         // scores are there
   auto p_bar = [&](int t, int half) { return rest + 8u * (2 + 2 * t + half); };  // weights
   auto pv_bar = [&](int t) { return rest + 8u * (6 + t); };  // O holds the first half's
   auto ofree_bar = [&](int t) { return rest + 8u * (8 + t); };
-  auto factor_bar = [&](int i) { return rest + 8u * (10 + i); };
-  auto fread_bar = [&](int i) { return rest + 8u * (12 + i); };
-  const uint32_t qfull_bar = rest + 8u * 14, qempty_bar = rest + 8u * 15;
-  const uint32_t done_bar = rest + 8u * 16;
-  auto o_bar = [&](int t) { return rest + 8u * (17 + t); };  // O is an item's
+  const uint32_t qfull_bar = rest + 8u * 10, done_bar = rest + 8u * 11;
+  auto o_bar = [&](int t) { return rest + 8u * (12 + t); };  // O is an item's
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sbase + C::kMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sbase + C::kMisc + 4);
   volatile int *poison = reinterpret_cast<volatile int *>(sbase + C::kMisc + 8);
   float *factors = reinterpret_cast<float *>(sbase + C::kFactors);
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::SLOTS; ++i) {
-      mbar_init(full_bar(i), 4);
+      mbar_init(full_bar(i), kTokens / kGroup);
       mbar_init(empty_bar(i), 1);
     }
     for (int i = 0; i < kScaleBufs; ++i) {
-      mbar_init(scfull_bar(i), 4);
+      mbar_init(atfull_bar(i), 1);
+      mbar_init(atfree_bar(i), kConverters);
+      mbar_init(scfull_bar(i), 2);
       mbar_init(scfree_bar(i), 8);
     }
     for (int t = 0; t < 2; ++t) {
@@ -282,17 +428,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(pv_bar(t), 1);
       mbar_init(o_bar(t), 1);
       mbar_init(ofree_bar(t), 4);
-      mbar_init(factor_bar(t), kQWarps);
-      mbar_init(fread_bar(t), 8);
     }
-    mbar_init(qfull_bar, kQWarps);
-    mbar_init(qempty_bar, 1);
+    mbar_init(qfull_bar, 8);
     mbar_init(done_bar, 1);
     *abort_flag = 0;
     *poison = 0;
     fence_mbar_init();
   }
-  if (warp == 12) {
+  if (warp == 15) {
     tmem_alloc(smem_addr(tmem_slot), 512);
     tmem_relinquish();
   }
@@ -308,187 +451,285 @@ __global__ void __launch_bounds__(kThreads, 1)
     return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) ||
            wait_long(bar, parity, timeout_ns, a.rows.status, abort_flag);
   };
-  // Each warp's place in the work, in shared memory: registers are short.
+  // Each warp's place in the work, in shared memory: registers are short.  Two items, as
+  // the warps that make weights fetch one's rows of q while they are at the other.
   struct Place {
     Walk walk;
-    Item it;
+    Item items[2];
     int more;
+    float stats[64];
   };
   __shared__ Place places[kThreads / 32];
   Place &my = places[warp];
-  const Item &it = my.it;
   if (lane == 0) start_walk<kItemRows>(a, sh, &my.walk);
-  auto next = [&] {
+  auto next = [&](int i) {
     __syncwarp();
-    if (lane == 0) my.more = next_item<kItemRows, kTokens>(a, &my.walk, &my.it);
+    if (lane == 0) my.more = next_item<kItemRows, kTokens>(a, &my.walk, &my.items[i]);
     __syncwarp();
     return my.more != 0;
   };
 
   if (warp < 8) {
     // --------------------------------------------------- scores to weights
+    // A thread holds the columns 8 i + 2 c + {0, 1} of four rows, g + 8 u of its warp's
+    // 32, as a thread of one row would have to read every column's scales.
     const int t = warp >> 2;                    // tile
-    const int row = (warp & 3) * 32 + lane;     // of the tile
+    const int row0 = t * kRows + (warp & 3) * 32, g = lane >> 2, c = lane & 3;
     const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t s_tm = lanes + C::kS + 128 * t, o_tm = lanes + C::kO + DP * t;
+    constexpr uint32_t kLanes16 = 16u << 16;
     uint32_t sc = 0;      // tiles of tokens so far
     uint32_t tiles = 0;   // those of them that this tile of rows took part in
     uint32_t items = 0;   // likewise
-    bool ok = true;
-    for (int n = 0; ok && next(); ++n) {
-      const bool active = t * kRows < it.rows;
-      const int r = it.rt * kItemRows + min(t * kRows + row, it.rows - 1);
-      const int seen = t * kRows + row < it.rows ? tokens_seen(a, it.q, r) : 0;
-      if (!(ok = wait(factor_bar(n & 1), (n >> 1) & 1u))) break;
-      const float factor = factors[(n & 1) * kItemRows + t * kRows + row];
-      const uint64_t factor2 = pair(factor, factor);
+    const uint32_t q_at = base + t * TERMS * C::kTileBytes + (warp & 3) * 32 * 128;
+    float *const my_factors = factors + row0;
+    auto q_done = [&] {
+      fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(fread_bar(n & 1));
-      float M = -INFINITY, back = 1.0f;  // back: what V's scales are relative to
-      uint64_t l2 = pair(0.0f, 0.0f);
+      if (lane == 0) mbar_arrive(qfull_bar);
+    };
+    bool ok = true, more = next(0);
+    if (more) {
+      fetch_q<F32Q, DP>(a, my.items[0], q_at, row0);
+      scale_q<F32Q, DP>(a, q_at, my_factors);
+      q_done();
+    }
+    for (int n = 0; ok && more; ++n) {
+      const Item &it = my.items[n & 1], &upcoming = my.items[(n + 1) & 1];
+      const int rows = it.rows, count = it.count, tok0 = it.tile0 * kTokens;
+      const bool active = t * kRows < rows;
+      // Of the 16 rows in hand, and of the other 16.
+      Rows16 now, other;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        now.factor[u] = my_factors[8 * u + g];
+        other.factor[u] = my_factors[16 + 8 * u + g];
+        now.M[u] = other.M[u] = -INFINITY;
+        now.l2[u] = other.l2[u] = pair(0.0f, 0.0f);
+      }
+      // Tokens that each row of the warp sees: the first one's.
+      const int all = row0 + 32 <= rows ? tokens_seen(a, it.q, it.rt * kItemRows + row0) : 0;
+      float back = 1.0f;  // what V's scales are relative to
 #pragma unroll 1
-      for (int j = 0; j < it.count; ++j, ++sc) {
+      for (int j = 0; j < count; ++j, ++sc) {
         const int buf = sc % kScaleBufs;
         if (!(ok = wait(scfull_bar(buf), (sc / kScaleBufs) & 1u))) break;
+        if (j + 1 == count) more = next((n + 1) & 1);
         if (!active) {
           if (lane == 0) mbar_arrive(scfree_bar(buf));
           continue;
         }
         const uint32_t scales = base + C::kScales + buf * kScaleBytes;
-        if (j == 0) back = power_of_two(*reinterpret_cast<int *>(sbase + C::kScales + buf * kScaleBytes + 12 * kTokens));
+        if (j == 0)
+          back = power_of_two(*reinterpret_cast<const int *>(
+              sbase + C::kScales + buf * kScaleBytes + 12 * kTokens));
         if (!(ok = wait(s_bar(t), tiles & 1u))) break;
         tc_fence_after();
+        // The last scores of these rows are made: the next rows may take their place.
+        if (j + 1 == count && more) fetch_q<F32Q, DP>(a, upcoming, q_at, row0);
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
+        for (int part = 0; part < 4; ++part) {
+          // Half of the tokens, half of the rows: the loop's code has to be small, as
+          // four roles share the instruction cache.
           constexpr int HT = kTokens / 2;
-          const uint32_t hs = scales + 4 * HT * half;
-          float x[HT];
-          tmem_load32(s_tm + HT * half, x);
-          tmem_load32(s_tm + HT * half + 32, x + 32);
+          const int half = part >> 1, group = part & 1;
+          const uint32_t hs = scales + 4 * HT * half + 16 * c;
+          const uint32_t s_at = s_tm + (group ? kLanes16 : 0u);
+          float x[32];
+          tmem_load_rows(s_at + HT * half, x);
           tmem_wait32(x);
-          tmem_wait32(x + 32);
 #pragma unroll
-          for (int i = 0; i < HT; i += 4) {
+          for (int i = 0; i < 4; ++i) {
             uint64_t ks[2], lv[2];
-            lds_pairs(hs + 4 * i, ks[0], ks[1]);
-            lds_pairs(hs + 4 * kTokens + 4 * i, lv[0], lv[1]);
+            lds_pairs(hs + 64 * i, ks[0], ks[1]);
+            lds_pairs(hs + 4 * kTokens + 64 * i, lv[0], lv[1]);
 #pragma unroll
             for (int p = 0; p < 2; ++p)
-              unpair(fma2(mul2(pair(x[i + 2 * p], x[i + 2 * p + 1]), ks[p]), factor2, lv[p]),
-                     x[i + 2 * p], x[i + 2 * p + 1]);
-          }
-          const int limit = seen - (it.tile0 + j) * kTokens - HT * half;
-          if (__any_sync(0xffffffffu, limit < HT)) {
 #pragma unroll
-            for (int i = 0; i < HT; ++i)
-              if (i >= limit) x[i] = -INFINITY;
+              for (int u = 0; u < 2; ++u) {
+                float *v = &x[4 * (2 * i + p) + 2 * u];
+                unpair(fma2(mul2(pair(v[0], v[1]), ks[p]),
+                            pair(now.factor[u], now.factor[u]), lv[p]),
+                       v[0], v[1]);
+              }
           }
-          float best = x[0];
+          const int first = tok0 + j * kTokens + HT * half;
+          if (first + HT > all) {
 #pragma unroll
-          for (int i = 1; i + 1 < HT; i += 2) best = max3(best, x[i], x[i + 1]);
-          best = fmaxf(best, x[HT - 1]);
-          if (__any_sync(0xffffffffu, best > M + kLazy)) {
-            const float m = fmaxf(M, best);
-            const float down = m == -INFINITY ? 1.0f : ex2(M - m);
-            M = m;
-            l2 = mul2(l2, pair(down, down));
+            for (int u = 0; u < 2; ++u) {
+              const int r = row0 + 16 * group + 8 * u + g;
+              const int seen = r < rows ? tokens_seen(a, it.q, it.rt * kItemRows + r) : 0;
+              const int limit = seen - first - 2 * c;
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (8 * i + e >= limit) x[4 * i + 2 * u + e] = -INFINITY;
+            }
+          }
+          float best[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            best[u] = fmaxf(x[2 * u], x[2 * u + 1]);
+#pragma unroll
+            for (int i = 1; i < 8; ++i) best[u] = max3(best[u], x[4 * i + 2 * u], x[4 * i + 2 * u + 1]);
+          }
+          if (__any_sync(0xffffffffu,
+                         best[0] > now.M[0] + kLazy || best[1] > now.M[1] + kLazy)) {
+            float down[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              float m = fmaxf(best[u], now.M[u]);
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+              down[u] = m == -INFINITY ? 1.0f : ex2(now.M[u] - m);
+              now.M[u] = m;
+              now.l2[u] = mul2(now.l2[u], pair(down[u], down[u]));
+            }
             if (j > 0 || half > 0) {
               // The products of the tile before are in O, as the scores came after them.
               if (half > 0 && !(ok = wait(pv_bar(t), tiles & 1u))) break;
               tc_fence_after();
 #pragma unroll 1
-              for (int k = 0; k < DP; k += 32) {
+              for (int k = 0; k < DP; k += 64) {
+                const uint32_t at = o_tm + (group ? kLanes16 : 0u) + k;
                 float o[32];
-                tmem_load32(o_tm + k, o);
+                tmem_load_rows(at, o);
                 tmem_wait32(o);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] *= down;
-                tmem_store32(o_tm + k, o);
+                for (int i = 0; i < 32; ++i) o[i] *= down[i >> 1 & 1];
+                tmem_store_rows(at, o);
               }
             }
           }
-          const float top = M == -INFINITY ? 0.0f : kShift - M;
-          const uint64_t top2 = pair(top, top);
-          uint64_t sum2 = pair(0.0f, 0.0f);
+          uint64_t top[2];
 #pragma unroll
-          for (int k = 0; k < HT; k += 32) {
-            uint32_t w[16];
-#pragma unroll
-            for (int i = k; i < k + 32; i += 4) {
-              uint64_t iv[2];
-              lds_pairs(hs + 8 * kTokens + 4 * i, iv[0], iv[1]);
-#pragma unroll
-              for (int p = 0; p < 2; ++p) {
-                float u, v;
-                unpair(add2(pair(x[i + 2 * p], x[i + 2 * p + 1]), top2), u, v);
-                u = ex2(u);
-                v = ex2(v);
-                sum2 = fma2(pair(u, v), iv[p], sum2);
-                w[(i - k) / 2 + p] = pack_half(u, v);
-              }
-            }
-            tmem_store16(s_tm + (HT * half + k) / 2, w);
+          for (int u = 0; u < 2; ++u) {
+            const float v = now.M[u] == -INFINITY ? 0.0f : kShift - now.M[u];
+            top[u] = pair(v, v);
           }
-          l2 = add2(l2, sum2);
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint64_t iv[2];
+            lds_pairs(hs + 8 * kTokens + 64 * i, iv[0], iv[1]);
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const float *v = &x[4 * (2 * i + p) + 2 * u];
+                float y, z;
+                unpair(add2(pair(v[0], v[1]), top[u]), y, z);
+                y = ex2(y);
+                z = ex2(z);
+                now.l2[u] = fma2(pair(y, z), iv[p], now.l2[u]);
+                w[2 * (2 * i + p) + u] = pack_half(y, z);
+              }
+          }
+          tmem_store_halves(s_at + HT / 2 * half, w);
           tmem_wait_store();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(p_bar(t, half));
+          if (group && lane == 0) mbar_arrive(p_bar(t, half));
+          const Rows16 done = now;
+          now = other;
+          other = done;
         }
         if (!ok) break;
         if (lane == 0) mbar_arrive(scfree_bar(buf));
         ++tiles;
       }
       if (!ok) break;
+      if (more) {
+        if (!active) fetch_q<F32Q, DP>(a, upcoming, q_at, row0);
+        scale_q<F32Q, DP>(a, q_at, my_factors);
+        q_done();
+      }
       if (!active) continue;
+      // A row to each lane from here on.
+      float sum, best;
+      {
+        float *stats = reinterpret_cast<float *>(&my.stats);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const Rows16 &of = u < 2 ? now : other;
+          float y, z;
+          unpair(of.l2[u & 1], y, z);
+          y += z;
+          y += __shfl_xor_sync(0xffffffffu, y, 1);
+          y += __shfl_xor_sync(0xffffffffu, y, 2);
+          if (c == 0) {
+            stats[8 * u + g] = y;
+            stats[32 + 8 * u + g] = of.M[u & 1];
+          }
+        }
+        __syncwarp();
+        sum = stats[lane];
+        best = stats[32 + lane];
+      }
+      const int row = (warp & 3) * 32 + lane;     // of the tile
+      const int r = it.rt * kItemRows + min(row0 + lane, rows - 1);
+      const int my_seen = row0 + lane < rows ? tokens_seen(a, it.q, r) : 0;
       // The rows' results.
       if (!(ok = wait(o_bar(t), items & 1u))) break;
       ++items;
       tc_fence_after();
-      float u, v;
-      unpair(l2, u, v);
-      const float sum = u + v;
       const bool some = sum > 0.0f || sum != sum;
       const float inv = some ? 1.0f / sum * back : 0.0f;
-      const float lse = some ? M - kShift + log2f(sum) : -INFINITY;
+      const float lse = some ? best - kShift + log2f(sum) : -INFINITY;
       const bool mask = *poison != 0;
-      const bool on = t * kRows + row < it.rows;
+      const bool on = row0 + lane < rows;
       const bool whole = it.count == it.tiles;
-      const int part = 2 * blockIdx.x + (it.tile0 > 0 ? 0 : 1);
       const int tok = divide(r, a.group);
       const int64_t out_row = static_cast<int64_t>(it.q.row0) + tok;
       const int hq = it.h * a.G + r - tok * a.G;
+      const int64_t place = out_row * a.Hq + hq;
+      const int64_t part = (2 * static_cast<int64_t>(blockIdx.x) + (it.tile0 > 0 ? 0 : 1)) * kItemRows + t * kRows + row;
       Weights weights = {1.0f, 0.0f, lse};
-      if (whole && on) weights = weigh(a, out_row, hq, lse);
+      const float *pre = nullptr;
+      if (whole && !a.raw_o && on) {
+        weights = weigh(a, out_row, hq, lse);
+        if (a.pre_o) pre = a.pre_o + place * a.cache.D;
+        if (a.lse) a.lse[out_row * a.ld_lse + hq] = weights.lse * kLn2;
+      } else if (on) {
+        (whole ? a.raw_lse + place : a.part_lse + part)[0] = lse;
+      }
+      float *const f32 = !whole ? a.part_o + part * DP
+                         : a.raw_o ? a.raw_o + place * a.cache.D : nullptr;
+      uint16_t *const b16 = a.out + out_row * a.ldo + hq * a.ldo_head;
 #pragma unroll 1
-      for (int k = 0; k < DP; k += 32) {
-        float o[32];
-        tmem_load32(o_tm + k, o);
-        tmem_wait32(o);
+      for (int k = 0; k < a.cache.D; k += 8) {
+        float o[8];
+        tmem_load8(o_tm + k, o);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] *= inv;
+        for (int i = 0; i < 8; ++i) o[i] *= inv;
         if (mask && on) {
-          const uint32_t bad = lost_columns<Fm>(a, it, seen, k);
+          const uint32_t bad = lost_columns<Fm>(a, it, my_seen, k);
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
+          for (int i = 0; i < 8; ++i)
             if (bad >> i & 1u) o[i] = NAN;
         }
-        if (on) {
+        if (!on) continue;
+        if (f32) {
+          *reinterpret_cast<float4 *>(f32 + k) = make_float4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<float4 *>(f32 + k + 4) = make_float4(o[4], o[5], o[6], o[7]);
+          continue;
+        }
+        if (pre) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            if (k + i >= a.cache.D) break;
-            float y[8];
+          for (int i = 0; i < 8; ++i) o[i] = o[i] * weights.own + pre[k + i] * weights.pre;
+        }
+        uint32_t u[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = o[i + e];
-            if (whole) {
-              emit<8>(a, out_row, hq, k + i, y, lse, weights);
-            } else {
-              float *p = a.part_o + (static_cast<int64_t>(part) * kItemRows + t * kRows + row) * DP + k + i;
-              *reinterpret_cast<float4 *>(p) = make_float4(y[0], y[1], y[2], y[3]);
-              *reinterpret_cast<float4 *>(p + 4) = make_float4(y[4], y[5], y[6], y[7]);
-              if (k + i == 0) a.part_lse[part * kItemRows + t * kRows + row] = lse;
-            }
-          }
+        for (int i = 0; i < 4; ++i) {
+          const __nv_bfloat162 b = __floats2bfloat162_rn(o[2 * i], o[2 * i + 1]);
+          u[i] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+        if (a.out_vec) {
+          *reinterpret_cast<uint4 *>(b16 + k) = make_uint4(u[0], u[1], u[2], u[3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) b16[k + i] = static_cast<uint16_t>(u[i / 2] >> (16 * (i & 1)));
         }
       }
       tc_fence_before();
@@ -498,194 +739,219 @@ __global__ void __launch_bounds__(kThreads, 1)
         a.desc[blockIdx.x] = {it.s, it.h, it.rt,
                               owner_of(sh, it.begin + it.tiles - 1) - static_cast<int>(blockIdx.x) + 1};
     }
-  } else if (warp < 12) {
+  } else if (warp < 8 + kConverters) {
     // ------------------------------------------------- codes to halves
-    // Three tiles of tokens are under way: of one the page numbers are being read, of
-    // one the codes, and one is converted.  A warp has 16 tokens of each half of a tile,
-    // a lane of which knows one, and reads back what it copied itself.
-    const Cache &c = a.cache;
+    // Jobs n = w, w + 5, ...: job n is group n % 8 of K (n % 16 < 8) or V of tile n / 16.
+    // A lane reads back what it copied itself.
     constexpr int CH = DP / 16;        // 16-byte chunks of a row
-    constexpr int PER = CH / 2;        // of a lane in a unit: 16 tokens of a warp
-    const int tok0 = 16 * (warp - 8);
-    const int token = (lane >> 4) * (kTokens / 2) + tok0 + (lane & 15);
-    const uint32_t raw_at = base + C::kRaw + (warp - 8) * (C::kUnit / 4) + lane * 16;
-    // The lane's chunk i of a unit.  Eight lanes cover even chunks of halves that are
-    // swizzled by the token, so two tokens, one of them odd.
+    constexpr int PER = CH / 2;        // of a lane in a job
+    const uint32_t raw = base + C::kRaw + (warp - 8) * (C::AHEAD * C::kJob) + lane * 16;
+    // The lane's chunk i.  Eight lanes cover even chunks of halves that are swizzled by
+    // the token, so two tokens, one of them odd.
     const int ch = DP == 128 ? lane & 7 : lane & 3;
-    auto local = [&](int i) {
-      return DP == 128 ? (i >> 1) * 8 + (lane >> 3) * 2 + (((lane >> 2) & 1) ^ (i & 1))
-                       : i * 8 + (lane >> 2);
-    };
-    // Peeked tile.
-    bool peeked = false;
-    int pj = 0, p_page = -1, p_page0 = -1, p_tok = 0, p_tok0 = 0;
-    bool p_in = false, p_first = false, p_partial = false;
-    int64_t p_head = 0, p_shead = 0;
-    if (lane == 0) my.it.count = 0;
-    __syncwarp();
-    auto peek = [&] {
-      if (pj == it.count) {
-        peeked = next();
-        pj = 0;
-        if (!peeked) {
-          if (lane == 0) my.it.count = 0;  // and it stays so
+    const int tok = DP == 128 ? (lane >> 3) * 2 + ((lane >> 2) & 1) : lane >> 2;
+    auto local = [&](int i) { return DP == 128 ? (i >> 1) * 8 + (tok ^ (i & 1)) : i * 8 + tok; };
+    const uint32_t jobs = static_cast<uint32_t>(sh.end - sh.begin) * kJobs;
+    uint32_t flags = 0;                // of the jobs under way: not all rows see the tile
+    bool ok = true;
+    auto request = [&](uint32_t n) {
+      bool partial = false;
+      if (n < jobs) {
+        const uint32_t tile = n / kJobs, buf = tile % kScaleBufs;
+        if (!(ok = wait(atfull_bar(buf), (tile / kScaleBufs) & 1u))) return;
+        const bool is_v = n & (kJobs / 2);
+        const uint8_t *codes = is_v ? a.cache.v : a.cache.k;
+        const uint32_t from = base + C::kPlaces + (buf * kTokens + n % (kJobs / 2) * kGroup) * 8;
+        const uint32_t dst = raw + n / kConverters % C::AHEAD * C::kJob;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          int64_t o;
+          asm volatile("ld.shared.b64 %0, [%1];" : "=l"(o) : "r"(from + local(i) * 8) : "memory");
+          // The lowest bit of a place marks a tile that not all rows see.
+          partial = is_v && (o & 1);
+          const bool on = o >= 0 && ch * 16 < a.cache.D;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * 512),
+                       "l"(codes + (on ? (o & ~1ll) + ch * 16 : 0)), "r"(on ? 16 : 0)
+                       : "memory");
+        }
+        if ((n + kConverters) / kJobs != tile) {  // the last of this tile's
           __syncwarp();
-          return;
+          if (lane == 0) mbar_arrive(atfree_bar(buf));
         }
       }
+      flags |= (partial ? 1u : 0u) << (C::AHEAD - 1);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll 1
+    for (uint32_t n = warp - 8; ok; n += kConverters) {
+      // The first rounds only request.
+      if (n >= C::AHEAD * kConverters) {
+        const uint32_t m = n - C::AHEAD * kConverters;
+        if (m >= jobs) break;
+        const uint32_t use = m / (kJobs / 2), slot = use % C::SLOTS;
+        if (!(ok = wait(empty_bar(slot), ((use / C::SLOTS) & 1u) ^ 1u))) break;
+        asm volatile("cp.async.wait_group %0;" ::"n"(C::AHEAD - 1) : "memory");
+        const uint32_t src = raw + m / kConverters % C::AHEAD * C::kJob;
+        const uint32_t dst = base + C::kRing + slot * C::kTileBytes + (ch >> 2) * C::kBlock +
+                             m % (kJobs / 2) * (kGroup * 128);
+        bool found = false;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          uint32_t w[4], h[8];
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                       : "r"(src + i * 512)
+                       : "memory");
+          if (flags & 1u) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) found |= Fm::clear4(w[q]);
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            h[2 * q] = decode2<FMT>(w[q] & 0xffffu);
+            h[2 * q + 1] = decode2<FMT>(w[q] >> 16);
+          }
+          const uint32_t r = local(i), row = dst + r * 128;
+          const uint32_t c0 = 2 * (ch & 3), sw = r & 7;
+          st_shared_v4(row + ((c0 ^ sw) << 4), h[0], h[1], h[2], h[3]);
+          st_shared_v4(row + (((c0 + 1) ^ sw) << 4), h[4], h[5], h[6], h[7]);
+        }
+        if (found) *poison = 1;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full_bar(slot));
+      }
+      flags >>= 1;
+      request(n);
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+  } else if (warp < 15) {
+    // ------------------------------------------------- places and scales
+    // A lane has four tokens of a tile, 32 apart.  The page numbers are read a tile
+    // ahead, and the scales of a tile are written when the next one's places are.
+    const bool is_v = warp == 14;
+    const Cache &c = a.cache;
+    const float *const scales_from = is_v ? c.v_scale : c.k_scale;
+    // Scales of the columns 2 c, 2 c + 1, 2 c + 8, 2 c + 9 of 16 lie together: a thread
+    // that makes weights has those.
+    const int scale_at = (lane & ~15) + ((lane >> 1) & 3) * 4 + ((lane >> 3) & 1) * 2 + (lane & 1);
+    const Item &it = my.items[0];
+    int page[4], pj = 0, tok0 = 0, most = 0, h = 0, e0 = 0;
+    bool partial = false, first = false, more = next(0);
+    auto peek = [&] {
+      if (!more) return;
+      if (pj == it.count) {
+        pj = 0;
+        if (!(more = next(0))) return;
+      }
       const int all = tokens_seen(a, it.q, it.rt * kItemRows);
-      const int most = tokens_seen(a, it.q, it.rt * kItemRows + it.rows - 1);
       const int32_t *table = a.rows.table + it.s * a.rows.ld_table;
-      p_first = pj == 0;
-      p_tok0 = (it.tile0 + pj) * kTokens;
-      p_tok = p_tok0 + token;
-      p_in = p_tok < most;
-      p_page = p_in ? table[divide(p_tok, c.page)] : -1;
-      p_page0 = p_first && p_tok0 < most ? table[divide(p_tok0, c.page)] : -1;
-      p_partial = p_tok0 + kTokens > all && all < most;
-      p_head = it.h * c.head_stride;
-      p_shead = it.h * c.scale_head_stride;
+      most = tokens_seen(a, it.q, it.rt * kItemRows + it.rows - 1);
+      tok0 = (it.tile0 + pj) * kTokens;
+      h = it.h;
+      first = pj == 0;
+      partial = tok0 + kTokens > all && all < most;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int tk = tok0 + lane + 32 * i;
+        page[i] = tk < most ? table[divide(tk, c.page)] : -1;
+      }
       ++pj;
     };
-    // Located tile: where the lane's token is (-1: nowhere), its scales, and V's of the
-    // item's first token.
-    int64_t off = -1;
-    float ks = 0.0f, vs = 1.0f, vs0 = 1.0f;
-    bool located = false, first = false, partial = false;
-    auto locate = [&] {
-      located = peeked;
-      if (!peeked) return;
-      const bool good = p_in && p_page >= 0 && p_page < c.num_pages;
-      if (p_in && !good) atomicOr(a.rows.status, kStatusBadDeviceArg);
-      const int place = p_tok - divide(p_tok, c.page) * c.page_size;
-      off = good ? p_page * c.page_stride + place * c.token_stride + p_head : -1;
-      const int64_t so = p_page * c.scale_page_stride + place * c.scale_token_stride + p_shead;
-      ks = good ? c.k_scale[so] : 0.0f;
-      vs = good ? c.v_scale[so] : p_in ? NAN : 1.0f;
-      first = p_first;
-      partial = p_partial;
-      vs0 = 1.0f;
-      if (p_first && p_page0 >= 0 && p_page0 < c.num_pages)
-        vs0 = c.v_scale[p_page0 * c.scale_page_stride +
-                        (p_tok0 - divide(p_tok0, c.page) * c.page_size) * c.scale_token_stride +
-                        p_shead];
-    };
-    // Unit `kind` (K, K, V, V) of the located tile.
-    auto request = [&](int kind) {
-      const uint8_t *from = kind < 2 ? c.k : c.v;
-      const uint32_t dst = raw_at + kind % C::UNITS * C::kUnit;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int64_t o = __shfl_sync(0xffffffffu, off, (kind & 1) * 16 + local(i));
-        const bool on = o >= 0 && ch * 16 < c.D;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * 512),
-                     "l"(from + (on ? o + ch * 16 : 0)), "r"(on ? 16 : 0)
-                     : "memory");
-      }
-    };
-    int e0 = 0;
-    uint32_t step = 0;                 // tiles of tokens
+    peek();
+    const uint32_t count = static_cast<uint32_t>(sh.end - sh.begin);
+    float scale[4];
+    bool was_first = false;
     bool ok = true;
-    do {
-      // The tile that is converted now, if any: its scales first.
-      const bool cur = located, cur_partial = partial;
-      if (cur) {
-        if (first) e0 = exponent_of(vs0);
-        const int buf = step % kScaleBufs;
-        if (!(ok = wait(scfree_bar(buf), ((step / kScaleBufs) & 1u) ^ 1u))) break;
-        float *scales = reinterpret_cast<float *>(sbase + C::kScales + buf * kScaleBytes);
-        const bool fine = vs > 0.0f && vs < INFINITY;
-        scales[token] = ks;
-        scales[kTokens + token] = fine ? log2f(vs) - e0 : NAN;
-        // A bad scale is in the exponent alone: rows that do not see it have weight 0.
-        scales[2 * kTokens + token] =
-            fine ? fminf(__fdiv_rn(power_of_two(e0), vs), 3.0e38f) : 1.0f;
-        if (threadIdx.x == 8 * 32) *reinterpret_cast<int *>(scales + 3 * kTokens) = e0;
+#pragma unroll 1
+    for (uint32_t step = 0; step <= count; ++step) {
+      float fresh[4];
+      int64_t at[4];
+      const bool now_first = first;
+      if (step < count) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int tk = tok0 + lane + 32 * i;
+          const bool in = tk < most, good = in && page[i] >= 0 && page[i] < c.num_pages;
+          if (in && !good) atomicOr(a.rows.status, kStatusBadDeviceArg);
+          const int place = tk - divide(tk, c.page) * c.page_size;
+          at[i] = good ? page[i] * c.page_stride + place * c.token_stride +
+                             h * c.head_stride + (partial ? 1 : 0)
+                       : -1;
+          fresh[i] = good ? scales_from[page[i] * c.scale_page_stride + h * c.scale_head_stride +
+                                        place * c.scale_token_stride]
+                          : in ? NAN : 1.0f;
+        }
+        peek();
+        if (!is_v) {
+          const int buf = step % kScaleBufs;
+          if (!(ok = wait(atfree_bar(buf), ((step / kScaleBufs) & 1u) ^ 1u))) break;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            asm volatile("st.shared.b64 [%0], %1;" ::"r"(
+                             base + C::kPlaces + (buf * kTokens + lane + 32 * i) * 8),
+                         "l"(at[i])
+                         : "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(atfull_bar(buf));
+        }
+      }
+      if (step > 0) {
+        const int buf = (step - 1) % kScaleBufs;
+        if (!(ok = wait(scfree_bar(buf), (((step - 1) / kScaleBufs) & 1u) ^ 1u))) break;
+        float *out = reinterpret_cast<float *>(sbase + C::kScales + buf * kScaleBytes);
+        if (is_v) {
+          // Relative to a power of two near the scale of the item's first token.
+          if (was_first) e0 = exponent_of(__shfl_sync(0xffffffffu, scale[0], 0));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool fine = scale[i] > 0.0f && scale[i] < INFINITY;
+            out[kTokens + 32 * i + scale_at] = fine ? log2f(scale[i]) - e0 : NAN;
+            // A bad scale is in the exponent alone: rows that do not see it have weight 0.
+            out[2 * kTokens + 32 * i + scale_at] =
+                fine ? fminf(__fdividef(power_of_two(e0), scale[i]), 3.0e38f) : 1.0f;
+          }
+          if (lane == 0) *reinterpret_cast<int *>(out + 3 * kTokens) = e0;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) out[32 * i + scale_at] = scale[i];
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(scfull_bar(buf));
       }
-#pragma unroll 1
-      for (int kind = 0; kind < 4; ++kind) {
-        const uint32_t use = 2 * step + (kind >> 1);
-        const int slot = use % C::SLOTS;
-        if (kind == (C::UNITS == 4 ? 0 : 2)) {
-          // With two units, V of this tile has been requested by now.
-          locate();
-          peek();
-        }
-        if (cur) {
-          if ((kind & 1) == 0 &&
-              !(ok = wait(empty_bar(slot), ((use / C::SLOTS) & 1u) ^ 1u)))
-            break;
-          asm volatile("cp.async.wait_group %0;" ::"n"(C::UNITS - 1) : "memory");
-          const uint32_t src = raw_at + kind % C::UNITS * C::kUnit;
-          const uint32_t dst = base + C::kRing + slot * C::kTileBytes + (ch >> 2) * C::kBlock;
-          const bool clean = cur_partial && kind >= 2;
-          bool found = false;
 #pragma unroll
-          for (int i = 0; i < PER; ++i) {
-            uint32_t w[4], h[8];
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                         : "r"(src + i * 512)
-                         : "memory");
-            if (clean) {
-#pragma unroll
-              for (int q = 0; q < 4; ++q) found |= Fm::clear4(w[q]);
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              h[2 * q] = decode2<FMT>(w[q] & 0xffffu);
-              h[2 * q + 1] = decode2<FMT>(w[q] >> 16);
-            }
-            const uint32_t r = (kind & 1) * (kTokens / 2) + tok0 + local(i);
-            const uint32_t row = dst + r * 128;
-            const uint32_t c0 = 2 * (ch & 3), sw = r & 7;
-            st_shared_v4(row + ((c0 ^ sw) << 4), h[0], h[1], h[2], h[3]);
-            st_shared_v4(row + (((c0 + 1) ^ sw) << 4), h[4], h[5], h[6], h[7]);
-          }
-          if (found) *poison = 1;
-        }
-        const int ahead = (kind + C::UNITS) & 3;
-        if (C::UNITS == 2 && kind < 2 ? cur : located) request(ahead);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        if (cur && (kind & 1)) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(full_bar(slot));
-        }
-      }
-      if (!ok) break;
-      if (cur) ++step;
-    } while (located || peeked);
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+      for (int i = 0; i < 4; ++i) scale[i] = fresh[i];
+      was_first = now_first;
+    }
   } else {
-    if (warp == 12) {
+    {
       // ----------------------------------------------------------- MMAs
       constexpr uint32_t s_idesc = idesc_f16(kTokens, false), o_idesc = idesc_f16(DP, true);
       uint32_t s_step = 0, v_step = 0;      // tiles of tokens of S and of O
       uint32_t p_uses[2] = {0, 0}, o_uses[2] = {0, 0};
       // S of tile t against the K tile s_step.
+      const uint64_t q_desc = smem_desc_k128_sw128(base);
+      const uint64_t k_desc = smem_desc_k128_sw128(base + C::kRing);
+      const uint64_t v_desc = desc_mn(base + C::kRing, C::kBlock);
       auto scores = [&](int t) {
-        const uint32_t k = base + C::kRing + (2 * s_step) % C::SLOTS * C::kTileBytes;
+        const uint64_t ad = q_desc + t * (TERMS * C::kTileBytes / 16);
+        const uint64_t bd = k_desc + (2 * s_step) % C::SLOTS * (C::kTileBytes / 16);
+        const uint32_t d = tmem + C::kS + 128 * t;
 #pragma unroll
         for (int term = 0; term < TERMS; ++term)
 #pragma unroll
-          for (int b = 0; b < DP / 64; ++b) {
-            const uint64_t ad = smem_desc_k128_sw128(
-                base + (t * TERMS + term) * C::kTileBytes + b * C::kBlock);
-            const uint64_t bd = smem_desc_k128_sw128(k + b * C::kBlock);
+          for (int b = 0; b < DP / 64; ++b)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              umma_ss(tmem + C::kS + 128 * t, ad + 2u * q, bd + 2u * q, s_idesc,
-                      term > 0 || b > 0 || q > 0);
-          }
+              umma_ss(d, ad + (term * C::kTileBytes + b * C::kBlock) / 16 + 2 * q,
+                      bd + b * C::kBlock / 16 + 2 * q, s_idesc, term > 0 || b > 0 || q > 0);
         commit(s_bar(t));
       };
       auto k_ready = [&] {
         return wait(full_bar((2 * s_step) % C::SLOTS), ((2 * s_step) / C::SLOTS) & 1u);
       };
-      bool ok = true, more = next();
+      const Item &it = my.items[0];
+      bool ok = true, more = next(0);
       int rows = it.rows, count = it.count, n = 0;
       if (more) {
         ok = wait(qfull_bar, 0) && k_ready();
@@ -695,7 +961,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int t = 0; t < 2; ++t)
             if (t * kRows < rows) scores(t);
           commit(empty_bar((2 * s_step) % C::SLOTS));
-          if (count == 1) commit(qempty_bar);
           ++s_step;
         }
       }
@@ -705,18 +970,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; ok && j < count; ++j, ++v_step) {
           const bool last = j + 1 == count;
           if (last) {
-            more = next();
+            more = next(0);
             next_rows = more ? it.rows : 0;
             next_count = it.count;
           }
           const int s_rows = last ? next_rows : rows;
           const int v_slot = (2 * v_step + 1) % C::SLOTS;
           ok = wait(full_bar(v_slot), ((2 * v_step + 1) / C::SLOTS) & 1u);
-          bool ready = false;
 #pragma unroll 1
           for (int t = 0; ok && t < 2; ++t) {
             if (t * kRows < rows) {
-              const uint32_t v = base + C::kRing + v_slot * C::kTileBytes;
 #pragma unroll 1
               for (int half = 0; half < 2; ++half) {
                 ok = wait(p_bar(t, half), (t ? p_uses[1] : p_uses[0]) & 1u);
@@ -724,11 +987,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                   ok = wait(ofree_bar(t), ((t ? o_uses[1] : o_uses[0]) - 1) & 1u);
                 if (!ok) break;
                 tc_fence_after();
+                const uint64_t bd = v_desc + (v_slot * C::kTileBytes + half * (kTokens / 2 * 128)) / 16;
+                const uint32_t d = tmem + C::kO + DP * t, p = tmem + C::kS + 128 * t + 32 * half;
 #pragma unroll
                 for (int q = 0; q < kTokens / 32; ++q)
-                  umma_ts(tmem + C::kO + DP * t, tmem + C::kS + 128 * t + 32 * half + 8 * q,
-                          desc_mn(v + (half * (kTokens / 32) + q) * 2048, C::kBlock), o_idesc,
-                          j > 0 || half > 0 || q > 0);
+                  umma_ts(d, p + 8 * q, bd + q * (2048 / 16), o_idesc, j + half > 0 || q > 0);
                 if (half == 0) commit(pv_bar(t));
               }
               if (!ok) break;
@@ -736,22 +999,26 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (j == 0) ++(t ? o_uses[1] : o_uses[0]);
               if (last) commit(o_bar(t));
             }
-            if (t * kRows < s_rows) {
-              if (!ready) {
-                if (last) ok = wait(qfull_bar, (n + 1) & 1u);
-                ok = ok && k_ready();
-                if (!ok) break;
+            if (!last && t * kRows < s_rows) {
+              if (t == 0) {
+                if (!(ok = k_ready())) break;
                 tc_fence_after();
-                ready = true;
               }
               scores(t);
             }
+          }
+          // The next rows' scores come after all of these rows' products, which the warps
+          // that bring the next rows may still wait for.
+          if (ok && last && s_rows > 0 && (ok = wait(qfull_bar, (n + 1) & 1u) && k_ready())) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int t = 0; t < 2; ++t)
+              if (t * kRows < s_rows) scores(t);
           }
           if (!ok) break;
           commit(empty_bar(v_slot));
           if (s_rows > 0) {
             commit(empty_bar((2 * s_step) % C::SLOTS));
-            if (last ? next_count == 1 : j + 2 == count) commit(qempty_bar);
             ++s_step;
           }
         }
@@ -761,133 +1028,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       commit(done_bar);
       mbar_wait_drain(done_bar, 0, timeout_ns, a.rows.status);
-    } else {
-      // -------------------------------------------------------- query rows
-      constexpr int LR = DP / 8;          // lanes of a row, 8 elements each
-      constexpr int RP = 32 / LR;         // rows of a pass
-      const int sub = lane % LR;
-      const bool vec = (reinterpret_cast<uintptr_t>(a.q) & 15u) == 0 &&
-                       (a.ldq * (F32Q ? 4 : 2)) % 16 == 0 &&
-                       (a.ldq_head * (F32Q ? 4 : 2)) % 16 == 0;
-      for (int n = 0; next(); ++n) {
-        // q's rows are in use until the scores of the item before are done, its
-        // factors (two items' worth) until every warp has read them.
-        if (!wait(qempty_bar, (n & 1u) ^ 1u) || !wait(fread_bar(n & 1), ((n >> 1) & 1u) ^ 1u))
-          break;
-        auto place = [&](int rr, int term) {
-          const int t = rr / kRows, row = rr % kRows;
-          return base + (t * TERMS + term) * C::kTileBytes + (sub / 8) * C::kBlock + row * 128 +
-                 (((sub & 7) ^ (row & 7)) << 4);
-        };
-        const int rows = it.rows > kRows ? kItemRows : kRows;
-        constexpr int kPass = RP * kQWarps;     // rows of a pass of all three warps
-        const int r_first = RP * (warp - 13) + lane / LR;
-#pragma unroll 2
-        for (int rr = r_first; rr < rows; rr += kPass) {
-          const bool on = rr < it.rows && 8 * sub < a.cache.D;
-          const int r = it.rt * kItemRows + min(rr, it.rows - 1);
-          const int tok = divide(r, a.group);
-          const int64_t at = (static_cast<int64_t>(it.q.row0) + tok) * a.ldq +
-                             (it.h * a.G + r - tok * a.G) * a.ldq_head + 8 * sub;
-          if (vec || !on) {
-#pragma unroll
-            for (int term = 0; term < TERMS; ++term) {
-              const uint8_t *from = static_cast<const uint8_t *>(a.q) +
-                                    (on ? at * (F32Q ? 4 : 2) + 16 * term : 0);
-              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(place(rr, term)),
-                           "l"(vec ? from : reinterpret_cast<const uint8_t *>(a.cache.k)),
-                           "r"(on ? 16 : 0)
-                           : "memory");
-            }
-          } else if (F32Q) {
-            const uint32_t *p = static_cast<const uint32_t *>(a.q) + at;
-            st_shared_v4(place(rr, 0), p[0], p[1], p[2], p[3]);
-            st_shared_v4(place(rr, TERMS - 1), p[4], p[5], p[6], p[7]);
-          } else {
-            const uint16_t *p = static_cast<const uint16_t *>(a.q) + at;
-            st_shared_v4(place(rr, 0), p[0] | p[1] << 16, p[2] | p[3] << 16,
-                         p[4] | p[5] << 16, p[6] | p[7] << 16);
-          }
-        }
-        asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
-        // Four rows of a lane at a time, so that their steps overlap.
-#pragma unroll 1
-        for (int r0 = r_first; r0 - lane / LR < rows; r0 += 4 * kPass) {
-          uint32_t w[4][TERMS][4];
-          float m[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int rr = r0 + u * kPass;
-            m[u] = 0.0f;
-#pragma unroll
-            for (int term = 0; term < TERMS; ++term) {
-              w[u][term][0] = w[u][term][1] = w[u][term][2] = w[u][term][3] = 0;
-              if (rr < rows)
-                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(w[u][term][0]), "=r"(w[u][term][1]), "=r"(w[u][term][2]),
-                               "=r"(w[u][term][3])
-                             : "r"(place(rr, term))
-                             : "memory");
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint32_t b = w[u][term][i];
-                if (F32Q) {
-                  m[u] = fmaxf(m[u], fabsf(__uint_as_float(b)));
-                } else {
-                  m[u] = fmaxf(m[u], fabsf(__uint_as_float(b << 16)));
-                  m[u] = fmaxf(m[u], fabsf(__uint_as_float(b & 0xffff0000u)));
-                }
-              }
-            }
-          }
-#pragma unroll
-          for (int o = LR / 2; o > 0; o >>= 1)
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-              m[u] = fmaxf(m[u], __shfl_xor_sync(0xffffffffu, m[u], o));
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int rr = r0 + u * kPass;
-            if (rr >= rows) continue;
-            const int e = min(max(8 - exponent_of(m[u]), -126), 126);
-            const float up = power_of_two(e);
-            uint32_t h[TERMS][4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float x, y;
-              if (F32Q) {  // elements 2 i, 2 i + 1
-                x = __uint_as_float(w[u][TERMS == 2 ? i >> 1 : 0][2 * (i & 1)]) * up;
-                y = __uint_as_float(w[u][TERMS == 2 ? i >> 1 : 0][2 * (i & 1) + 1]) * up;
-              } else {
-                x = __uint_as_float(w[u][0][i] << 16) * up;
-                y = __uint_as_float(w[u][0][i] & 0xffff0000u) * up;
-              }
-              h[0][i] = pack_half(x, y);
-              if (TERMS == 2) {
-                const float2 f = half2_floats(h[0][i]);
-                h[TERMS - 1][i] = pack_half(x - f.x, y - f.y);
-              }
-            }
-#pragma unroll
-            for (int term = 0; term < TERMS; ++term)
-              st_shared_v4(place(rr, term), h[term][0], h[term][1], h[term][2], h[term][3]);
-            if (sub == 0)
-              factors[(n & 1) * kItemRows + rr] = power_of_two(-e) * a.scale_log2;
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(factor_bar(n & 1));
-          mbar_arrive(qfull_bar);
-        }
-      }
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 15) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
