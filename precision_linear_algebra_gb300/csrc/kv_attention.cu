@@ -30,6 +30,7 @@ constexpr int kWarps = 4;
 constexpr int kRows = 16;       // rows of a tile
 constexpr int kGroup = 16;      // tokens of a warp's step
 constexpr int kTile = kWarps * kGroup;
+constexpr int kItemCost = 1;    // of an item beside its tiles, in tiles
 constexpr int kStages = 4;
 constexpr float kShift = 7.0f;  // w of the running maximum is 2^7
 constexpr float kLazy = 8.0f;   // it is raised where 2^8 is passed
@@ -174,14 +175,14 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
   pdl_wait();
   pdl_launch_dependents();
   if (threadIdx.x == 0 && a.desc) a.desc[blockIdx.x].parts = 0;
-  share_out<kThreads, kRows, kTile>(a, &sh, warp_sums);
+  share_out<kThreads, kRows, kTile, kItemCost>(a, &sh, warp_sums);
   const Cache &kc = a.cache;
   const uint32_t ring = smem_addr(smem) + warp * C::kRing;
   const uint32_t qsm = smem_addr(smem) + C::kQ;
 
   if (threadIdx.x == 0) start_walk<kRows>(a, sh, &walk);
   for (;;) {
-    if (threadIdx.x == 0) more = next_item<kRows, kTile>(a, &walk, &it);
+    if (threadIdx.x == 0) more = next_item<kRows, kTile, kItemCost>(a, &walk, &it);
     __syncthreads();
     if (!more) break;
     const Seq q = it.q;
@@ -562,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
       }
     }
     if (threadIdx.x == 0 && !whole && tile0 == 0)
-      a.desc[blockIdx.x] = {s, h, rt, owner_of(sh, it.begin + it.tiles - 1) - static_cast<int>(blockIdx.x) + 1};
+      a.desc[blockIdx.x] = {s, h, rt, owner_of(sh, it.end - 1) - static_cast<int>(blockIdx.x) + 1};
     __syncthreads();  // the results overlay the rings
   }
 }

@@ -108,13 +108,14 @@ __device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t x, in
   }
 }
 
-// Tiles of the row tiles below R of a sequence with `rts` of them.  Row tile rt but the
+// Units of the row tiles below R of a sequence with `rts` of them: their tiles and COST
+// each.  Row tile rt but the
 // last one sees len - n + floor(((rt + 1) BM - 1) / G) + 1 tokens, which makes floor((G
 // (len - n + BN) + (rt + 1) BM - 1) / (BN G)) tiles, and one where that is less.
-template <int BM, int BN>
+template <int BM, int BN, int COST>
 __device__ __noinline__ int64_t units_below(const AttnArgs &a, const Seq &q, int rts, int R) {
-  if (!a.causal) return static_cast<int64_t>(R) * tiles_of<BM, BN>(a, q, 0);
-  int64_t sum = 0;
+  if (!a.causal) return static_cast<int64_t>(R) * (tiles_of<BM, BN>(a, q, 0) + COST);
+  int64_t sum = static_cast<int64_t>(R) * COST;
   if (R == rts) sum += tiles_of<BM, BN>(a, q, --R);
   const int64_t G = a.G, c = static_cast<int64_t>(q.len) - q.n;
   int64_t k = c < 0 ? -G * c / BM : 0;
@@ -133,17 +134,17 @@ __device__ __forceinline__ int row_tiles_of(const AttnArgs &a, const Seq &q) {
 struct Share {
   int64_t units, begin, end;   // all units; this CTA's
   int32_t ctas;                // that have work
-  int32_t s, h, rt, tile;      // where this CTA begins
+  int32_t s, h, rt, pos;       // where this CTA begins: unit `pos` of a row tile
 };
 
 __device__ __forceinline__ int64_t shfl_up64(int64_t v, int d) {
   return __shfl_up_sync(0xffffffffu, v, d);
 }
 
-// All units (tiles) in the order (sequence, K/V head, row tile, token tile) are cut
-// into equal ranges, one for each CTA: every SM has the same work whatever the lengths
-// are.  Checks the segments: where they cannot be used, nothing is to be done.
-template <int THREADS, int BM, int BN>
+// All units in the order (sequence, K/V head, row tile, then its COST units that are no
+// tiles, then its tiles) are cut into equal ranges, one for each CTA: every SM has the
+// same work whatever the lengths are.  Checks the segments: where they cannot be used, nothing is to be done.
+template <int THREADS, int BM, int BN, int COST>
 __device__ __noinline__ void share_out(const AttnArgs &a, Share *sh, int64_t *warp_sums) {
   const int S = a.whole ? 1 : a.rows.S;
   const int per = (S + THREADS - 1) / THREADS;
@@ -163,7 +164,7 @@ __device__ __noinline__ void share_out(const AttnArgs &a, Share *sh, int64_t *wa
                      (!a.whole && q.n > a.max_rows);
     bad |= off;
     const int rts = off ? 0 : row_tiles_of<BM>(a, q);
-    if (rts > 0) sum += H * units_below<BM, BN>(a, q, rts, rts);
+    if (rts > 0) sum += H * units_below<BM, BN, COST>(a, q, rts, rts);
   }
   bad = __syncthreads_or(bad);
   if (bad) {
@@ -206,7 +207,7 @@ __device__ __noinline__ void share_out(const AttnArgs &a, Share *sh, int64_t *wa
       const Seq q = load_seq(a, s);
       const int rts = row_tiles_of<BM>(a, q);
       if (rts == 0) continue;
-      const int64_t each = units_below<BM, BN>(a, q, rts, rts);
+      const int64_t each = units_below<BM, BN, COST>(a, q, rts, rts);
       if (begin >= before + H * each) {
         before += H * each;
         continue;
@@ -217,13 +218,13 @@ __device__ __noinline__ void share_out(const AttnArgs &a, Share *sh, int64_t *wa
 #pragma unroll 1
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (units_below<BM, BN>(a, q, rts, mid) <= left) lo = mid;
+        if (units_below<BM, BN, COST>(a, q, rts, mid) <= left) lo = mid;
         else hi = mid - 1;
       }
       sh->s = s;
       sh->h = h;
       sh->rt = lo;
-      sh->tile = static_cast<int>(left - units_below<BM, BN>(a, q, rts, lo));
+      sh->pos = static_cast<int>(left - units_below<BM, BN, COST>(a, q, rts, lo));
       break;
     }
   }
@@ -235,18 +236,18 @@ __device__ __forceinline__ int owner_of(const Share &sh, int64_t u) {
   return static_cast<int>(((u + 1) * sh.ctas - 1) / sh.units);
 }
 
-// Tiles tile0 .. tile0+count-1 of the `tiles` of a row tile with `rows` rows; begin: the
-// first of them, among all units.
+// Tiles tile0 .. tile0+count-1 of the `tiles` of a row tile with `rows` rows, whose last
+// unit, among all units, is the one before `end`.
 struct Item {
   Seq q;
   int s, h, rt, tile0, count, tiles, rows;
-  int64_t begin;
+  int64_t end;
 };
 
 // Walks through a CTA's items.
 struct Walk {
   int64_t at, end;
-  int s, h, rt, tile, rts;
+  int s, h, rt, pos, rts;
   Seq q;
 };
 template <int BM>
@@ -256,15 +257,17 @@ __device__ __noinline__ void start_walk(const AttnArgs &a, const Share &sh, Walk
   w->s = sh.s;
   w->h = sh.h;
   w->rt = sh.rt;
-  w->tile = sh.tile;
+  w->pos = sh.pos;
   if (w->at < w->end) {
     w->q = load_seq(a, w->s);
     w->rts = row_tiles_of<BM>(a, w->q);
   }
 }
-template <int BM, int BN>
+template <int BM, int BN, int COST>
 __device__ __noinline__ bool next_item(const AttnArgs &a, Walk *w, Item *it) {
-  if (w->at >= w->end) return false;
+  // A range that ends before a row tile's first tile leaves it to the next CTA.
+  const int64_t left = w->end - w->at;
+  if (left <= 0 || w->pos + left <= COST) return false;
   if (w->rt >= w->rts) {
     w->rt = 0;
     if (++w->h >= a.cache.heads) {
@@ -276,17 +279,19 @@ __device__ __noinline__ bool next_item(const AttnArgs &a, Walk *w, Item *it) {
     }
   }
   const int tiles = tiles_of<BM, BN>(a, w->q, w->rt);
+  const int tile0 = w->pos > COST ? w->pos - COST : 0;
+  const int64_t rest = COST + tiles - w->pos, mine = rest < left ? rest : left;
   it->q = w->q;
   it->s = w->s;
   it->h = w->h;
   it->rt = w->rt;
-  it->tile0 = w->tile;
+  it->tile0 = tile0;
   it->tiles = tiles;
-  it->begin = w->at - w->tile;
-  it->count = static_cast<int>(min(static_cast<int64_t>(tiles - w->tile), w->end - w->at));
+  it->end = w->at + rest;
+  it->count = static_cast<int>(w->pos + mine) - COST - tile0;
   it->rows = min(BM, w->q.n * a.G - w->rt * BM);
-  w->at += it->count;
-  w->tile = 0;
+  w->at += mine;
+  w->pos = 0;
   ++w->rt;
   return true;
 }

@@ -39,6 +39,8 @@ constexpr int kThreads = 512;
 constexpr int kRows = 128;          // of a tile
 constexpr int kItemRows = 256;
 constexpr int kTokens = 128;        // of a tile
+// What an item costs beside its tiles, in tiles: bringing its rows, writing them out.
+constexpr int kItemCost = 3;
 constexpr int kConverters = 5;
 constexpr int kGroup = 16;          // tokens of a converter's job
 constexpr int kJobs = 2 * kTokens / kGroup;  // of a tile, K's first
@@ -117,13 +119,15 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t block) {
   return d;
 }
 
-// 8 columns of this thread's lane.
-__device__ __forceinline__ void tmem_load8(uint32_t addr, float (&r)[8]) {
+// 16 columns of this thread's lane.
+__device__ __forceinline__ void tmem_load16(uint32_t addr, float (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, "
+      "%8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
-        "=f"(r[7])
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]),
+        "=f"(r[6]), "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]),
+        "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
       : "r"(addr)
       : "memory");
 }
@@ -157,18 +161,25 @@ __device__ __forceinline__ void tmem_load_rows(uint32_t addr, float *r) {
       : "r"(addr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_store_rows(uint32_t addr, const float *r) {
+// The same of 32 columns; the load waits.
+__device__ __forceinline__ void tmem_load_rows16(uint32_t addr, float (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.16x256b.x8.b32 [%32], "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-      "%30, %31};"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]),
+        "=f"(r[6]), "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]),
+        "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store_rows16(uint32_t addr, const float (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};"
       ::"f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]),
         "f"(r[7]), "f"(r[8]), "f"(r[9]), "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]),
-        "f"(r[14]), "f"(r[15]), "f"(r[16]), "f"(r[17]), "f"(r[18]), "f"(r[19]),
-        "f"(r[20]), "f"(r[21]), "f"(r[22]), "f"(r[23]), "f"(r[24]), "f"(r[25]),
-        "f"(r[26]), "f"(r[27]), "f"(r[28]), "f"(r[29]), "f"(r[30]), "f"(r[31]),
-        "r"(addr)
+        "f"(r[14]), "f"(r[15]), "r"(addr)
       : "memory");
 }
 // 16 lanes of 32 columns, a pair of halves each: registers 2 i and 2 i + 1 hold columns
@@ -247,7 +258,7 @@ __device__ __noinline__ void fetch_q(const AttnArgs &a, const Item &it, uint32_t
                    a.ldq_head * SIZE % 16 == 0;
   const int rows = it.rows, first = it.rt * kItemRows, head0 = it.h * a.G;
   const int64_t token0 = it.q.row0;
-#pragma unroll 4
+#pragma unroll 1
   for (int i = 0; i < 32 / RP; ++i) {
     const int r = i * RP + lane / LR;
     const bool on = row0 + r < rows && 8 * sub < a.cache.D;
@@ -261,14 +272,18 @@ __device__ __noinline__ void fetch_q(const AttnArgs &a, const Item &it, uint32_t
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + term * kTerm),
                      "l"(vec ? from + 16 * term : a.cache.k), "r"(on ? 16 : 0)
                      : "memory");
-    } else if (F32Q) {
-      const uint32_t *p = reinterpret_cast<const uint32_t *>(from);
-      st_shared_v4(dst, p[0], p[1], p[2], p[3]);
-      st_shared_v4(dst + (TERMS - 1) * kTerm, p[4], p[5], p[6], p[7]);
     } else {
-      const uint16_t *p = reinterpret_cast<const uint16_t *>(from);
-      st_shared_v4(dst, p[0] | p[1] << 16, p[2] | p[3] << 16, p[4] | p[5] << 16,
-                   p[6] | p[7] << 16);
+#pragma unroll 1
+      for (int e = 0; e < 8; ++e) {
+        if (F32Q)
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + (e >> 2) * kTerm + (e & 3) * 4),
+                       "r"(reinterpret_cast<const uint32_t *>(from)[e])
+                       : "memory");
+        else
+          asm volatile("st.shared.b16 [%0], %1;" ::"r"(dst + 2 * e),
+                       "h"(reinterpret_cast<const uint16_t *>(from)[e])
+                       : "memory");
+      }
     }
   }
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -280,16 +295,17 @@ template <bool F32Q, int DP>
 __device__ __noinline__ void scale_q(const AttnArgs &a, uint32_t q_at, float *factors) {
   constexpr int TERMS = F32Q ? 2 : 1;
   constexpr int LR = DP / 8, RP = 32 / LR;
+  constexpr int U = 2;
   constexpr int kTerm = DP / 64 * kRows * 128;
   const int lane = threadIdx.x & 31, sub = lane % LR;
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll 1
-  for (int i = 0; i < 32 / RP; i += 4) {
-    // Four rows of a lane at a time, so that their steps overlap.
-    uint32_t w[4][TERMS][4];
-    float m[4];
+  for (int i = 0; i < 32 / RP; i += U) {
+    // A few rows of a lane at a time, so that their steps overlap.
+    uint32_t w[U][TERMS][4];
+    float m[U];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < U; ++u) {
       m[u] = 0.0f;
 #pragma unroll
       for (int term = 0; term < TERMS; ++term) {
@@ -312,9 +328,9 @@ __device__ __noinline__ void scale_q(const AttnArgs &a, uint32_t q_at, float *fa
 #pragma unroll
     for (int o = LR / 2; o > 0; o >>= 1)
 #pragma unroll
-      for (int u = 0; u < 4; ++u) m[u] = fmaxf(m[u], __shfl_xor_sync(0xffffffffu, m[u], o));
+      for (int u = 0; u < U; ++u) m[u] = fmaxf(m[u], __shfl_xor_sync(0xffffffffu, m[u], o));
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < U; ++u) {
       const int r = (i + u) * RP + lane / LR;
       const int e = min(max(8 - exponent_of(m[u]), -126), 126);
       const float up = power_of_two(e);
@@ -345,7 +361,7 @@ __device__ __noinline__ void scale_q(const AttnArgs &a, uint32_t q_at, float *fa
   __syncwarp();
 }
 
-// Columns k .. k+7 of V that hold a code that is not finite at a token that a row sees,
+// Columns k .. k+15 of V that hold a code that is not finite at a token that a row sees,
 // of the tiles that were written without such codes: those that not all rows see.
 template <typename Fm>
 __device__ __noinline__ uint32_t lost_columns(const AttnArgs &a, const Item &it, int seen, int k) {
@@ -359,18 +375,11 @@ __device__ __noinline__ uint32_t lost_columns(const AttnArgs &a, const Item &it,
     const uint8_t *codes = a.cache.v + page * a.cache.page_stride +
                            it.h * a.cache.head_stride +
                            (j - p * a.cache.page_size) * a.cache.token_stride;
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 16; ++i)
       if (!Fm::finite(codes[k + i])) bad |= 1u << i;
   }
   return bad;
 }
-
-// What a thread keeps of its two rows: the scores' factor, the running maximum, the sum
-// of the weights (of even and odd columns).
-struct Rows16 {
-  float factor[2], M[2];
-  uint64_t l2[2];
-};
 
 // mbar_wait by a whole warp, out of line: the kernel waits in many places.
 __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, uint64_t timeout_ns,
@@ -400,16 +409,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto atfull_bar = [&](int i) { return bars + 8u * (2 * C::SLOTS + 2 * kScaleBufs + i); };
   auto atfree_bar = [&](int i) { return bars + 8u * (2 * C::SLOTS + 3 * kScaleBufs + i); };
   const uint32_t rest = bars + 8u * (2 * C::SLOTS + 4 * kScaleBufs);
-  auto s_bar = [&](int t) { return rest + 8u * t; };         // scores are there
-  auto p_bar = [&](int t, int half) { return rest + 8u * (2 + 2 * t + half); };  // weights
-  auto pv_bar = [&](int t) { return rest + 8u * (6 + t); };  // O holds the first half's
-  auto ofree_bar = [&](int t) { return rest + 8u * (8 + t); };
-  const uint32_t qfull_bar = rest + 8u * 10, done_bar = rest + 8u * 11;
-  auto o_bar = [&](int t) { return rest + 8u * (12 + t); };  // O is an item's
+  // Of tile t of rows: its scores, the weights of half h of the tokens, the first half's
+  // products in O, an item's O, and that it has been read.
+  auto s_bar = [&](int t) { return rest + 8u * t; };
+  auto p_bar = [&](int t, int h) { return rest + 8u * (2 + 2 * t + h); };
+  auto pv_bar = [&](int t) { return rest + 8u * (6 + t); };
+  auto o_bar = [&](int t) { return rest + 8u * (8 + t); };
+  auto ofree_bar = [&](int t) { return rest + 8u * (10 + t); };
+  const uint32_t qfull_bar = rest + 8u * 12, done_bar = rest + 8u * 13;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sbase + C::kMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sbase + C::kMisc + 4);
   volatile int *poison = reinterpret_cast<volatile int *>(sbase + C::kMisc + 8);
   float *factors = reinterpret_cast<float *>(sbase + C::kFactors);
+  __shared__ volatile int more_tiles[kScaleBufs];
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::SLOTS; ++i) {
       mbar_init(full_bar(i), kTokens / kGroup);
@@ -442,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   pdl_launch_dependents();
   if (threadIdx.x == 0) a.desc[blockIdx.x].parts = 0;
-  share_out<kThreads, kItemRows, kTokens>(a, &sh, warp_sums);
+  share_out<kThreads, kItemRows, kTokens, kItemCost>(a, &sh, warp_sums);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -464,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (lane == 0) start_walk<kItemRows>(a, sh, &my.walk);
   auto next = [&](int i) {
     __syncwarp();
-    if (lane == 0) my.more = next_item<kItemRows, kTokens>(a, &my.walk, &my.items[i]);
+    if (lane == 0) my.more = next_item<kItemRows, kTokens, kItemCost>(a, &my.walk, &my.items[i]);
     __syncwarp();
     return my.more != 0;
   };
@@ -498,14 +510,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Item &it = my.items[n & 1], &upcoming = my.items[(n + 1) & 1];
       const int rows = it.rows, count = it.count, tok0 = it.tile0 * kTokens;
       const bool active = t * kRows < rows;
-      // Of the 16 rows in hand, and of the other 16.
-      Rows16 now, other;
+      float factor[4], M[4];
+      uint64_t l2[4];                  // of even and odd columns
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        now.factor[u] = my_factors[8 * u + g];
-        other.factor[u] = my_factors[16 + 8 * u + g];
-        now.M[u] = other.M[u] = -INFINITY;
-        now.l2[u] = other.l2[u] = pair(0.0f, 0.0f);
+      for (int u = 0; u < 4; ++u) {
+        factor[u] = my_factors[8 * u + g];
+        M[u] = -INFINITY;
+        l2[u] = pair(0.0f, 0.0f);
       }
       // Tokens that each row of the warp sees: the first one's.
       const int all = row0 + 32 <= rows ? tokens_seen(a, it.q, it.rt * kItemRows + row0) : 0;
@@ -528,16 +539,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The last scores of these rows are made: the next rows may take their place.
         if (j + 1 == count && more) fetch_q<F32Q, DP>(a, upcoming, q_at, row0);
 #pragma unroll 1
-        for (int part = 0; part < 4; ++part) {
-          // Half of the tokens, half of the rows: the loop's code has to be small, as
-          // four roles share the instruction cache.
+        for (int half = 0; half < 2; ++half) {
           constexpr int HT = kTokens / 2;
-          const int half = part >> 1, group = part & 1;
           const uint32_t hs = scales + 4 * HT * half + 16 * c;
-          const uint32_t s_at = s_tm + (group ? kLanes16 : 0u);
-          float x[32];
-          tmem_load_rows(s_at + HT * half, x);
-          tmem_wait32(x);
+          float x[2][32];
+#pragma unroll
+          for (int b = 0; b < 2; ++b) tmem_load_rows(s_tm + HT * half + b * kLanes16, x[b]);
+          tmem_wait32(x[0]);
+          tmem_wait32(x[1]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint64_t ks[2], lv[2];
@@ -546,94 +555,95 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int p = 0; p < 2; ++p)
 #pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                float *v = &x[4 * (2 * i + p) + 2 * u];
-                unpair(fma2(mul2(pair(v[0], v[1]), ks[p]),
-                            pair(now.factor[u], now.factor[u]), lv[p]),
+              for (int u = 0; u < 4; ++u) {
+                float *v = &x[u >> 1][4 * (2 * i + p) + 2 * (u & 1)];
+                unpair(fma2(mul2(pair(v[0], v[1]), ks[p]), pair(factor[u], factor[u]), lv[p]),
                        v[0], v[1]);
               }
           }
           const int first = tok0 + j * kTokens + HT * half;
           if (first + HT > all) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int r = row0 + 16 * group + 8 * u + g;
+            for (int u = 0; u < 4; ++u) {
+              const int r = row0 + 8 * u + g;
               const int seen = r < rows ? tokens_seen(a, it.q, it.rt * kItemRows + r) : 0;
               const int limit = seen - first - 2 * c;
 #pragma unroll
               for (int i = 0; i < 8; ++i)
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                  if (8 * i + e >= limit) x[4 * i + 2 * u + e] = -INFINITY;
+                  if (8 * i + e >= limit) x[u >> 1][4 * i + 2 * (u & 1) + e] = -INFINITY;
             }
           }
-          float best[2];
+          float best[4];
+          bool raise = false;
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            best[u] = fmaxf(x[2 * u], x[2 * u + 1]);
+          for (int u = 0; u < 4; ++u) {
+            const float *v = &x[u >> 1][2 * (u & 1)];
+            best[u] = fmaxf(v[0], v[1]);
 #pragma unroll
-            for (int i = 1; i < 8; ++i) best[u] = max3(best[u], x[4 * i + 2 * u], x[4 * i + 2 * u + 1]);
+            for (int i = 1; i < 8; ++i) best[u] = max3(best[u], v[4 * i], v[4 * i + 1]);
+            raise |= best[u] > M[u] + kLazy;
           }
-          if (__any_sync(0xffffffffu,
-                         best[0] > now.M[0] + kLazy || best[1] > now.M[1] + kLazy)) {
-            float down[2];
+          if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              float m = fmaxf(best[u], now.M[u]);
+            for (int u = 0; u < 4; ++u) {
+              float m = fmaxf(best[u], M[u]);
               m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
               m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-              down[u] = m == -INFINITY ? 1.0f : ex2(now.M[u] - m);
-              now.M[u] = m;
-              now.l2[u] = mul2(now.l2[u], pair(down[u], down[u]));
+              best[u] = m == -INFINITY ? 1.0f : ex2(M[u] - m);
+              M[u] = m;
+              l2[u] = mul2(l2[u], pair(best[u], best[u]));
             }
-            if (j > 0 || half > 0) {
+            if (j + half > 0) {
               // The products of the tile before are in O, as the scores came after them.
               if (half > 0 && !(ok = wait(pv_bar(t), tiles & 1u))) break;
               tc_fence_after();
 #pragma unroll 1
-              for (int k = 0; k < DP; k += 64) {
-                const uint32_t at = o_tm + (group ? kLanes16 : 0u) + k;
-                float o[32];
-                tmem_load_rows(at, o);
-                tmem_wait32(o);
+              for (int k = 0; k < DP / 16; ++k) {
+                // 16 lanes of 32 columns at a time.
+                const uint32_t at = o_tm + (k >> 1) * 32 + (k & 1) * kLanes16;
+                const float d0 = k & 1 ? best[2] : best[0], d1 = k & 1 ? best[3] : best[1];
+                float o[16];
+                tmem_load_rows16(at, o);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] *= down[i >> 1 & 1];
-                tmem_store_rows(at, o);
+                for (int i = 0; i < 16; ++i) o[i] *= i & 2 ? d1 : d0;
+                tmem_store_rows16(at, o);
               }
             }
           }
-          uint64_t top[2];
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const float v = now.M[u] == -INFINITY ? 0.0f : kShift - now.M[u];
-            top[u] = pair(v, v);
+          for (int b = 0; b < 2; ++b) {
+            uint64_t top[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const float v = M[2 * b + u] == -INFINITY ? 0.0f : kShift - M[2 * b + u];
+              top[u] = pair(v, v);
+            }
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint64_t iv[2];
+              lds_pairs(hs + 8 * kTokens + 64 * i, iv[0], iv[1]);
+#pragma unroll
+              for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                  const float *v = &x[b][4 * (2 * i + p) + 2 * u];
+                  float y, z;
+                  unpair(add2(pair(v[0], v[1]), top[u]), y, z);
+                  y = ex2(y);
+                  z = ex2(z);
+                  l2[2 * b + u] = fma2(pair(y, z), iv[p], l2[2 * b + u]);
+                  w[2 * (2 * i + p) + u] = pack_half(y, z);
+                }
+            }
+            tmem_store_halves(s_tm + HT / 2 * half + b * kLanes16, w);
           }
-          uint32_t w[16];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint64_t iv[2];
-            lds_pairs(hs + 8 * kTokens + 64 * i, iv[0], iv[1]);
-#pragma unroll
-            for (int p = 0; p < 2; ++p)
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const float *v = &x[4 * (2 * i + p) + 2 * u];
-                float y, z;
-                unpair(add2(pair(v[0], v[1]), top[u]), y, z);
-                y = ex2(y);
-                z = ex2(z);
-                now.l2[u] = fma2(pair(y, z), iv[p], now.l2[u]);
-                w[2 * (2 * i + p) + u] = pack_half(y, z);
-              }
-          }
-          tmem_store_halves(s_at + HT / 2 * half, w);
           tmem_wait_store();
           tc_fence_before();
           __syncwarp();
-          if (group && lane == 0) mbar_arrive(p_bar(t, half));
-          const Rows16 done = now;
-          now = other;
-          other = done;
+          if (lane == 0) mbar_arrive(p_bar(t, half));
         }
         if (!ok) break;
         if (lane == 0) mbar_arrive(scfree_bar(buf));
@@ -652,15 +662,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         float *stats = reinterpret_cast<float *>(&my.stats);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const Rows16 &of = u < 2 ? now : other;
           float y, z;
-          unpair(of.l2[u & 1], y, z);
+          unpair(l2[u], y, z);
           y += z;
           y += __shfl_xor_sync(0xffffffffu, y, 1);
           y += __shfl_xor_sync(0xffffffffu, y, 2);
           if (c == 0) {
             stats[8 * u + g] = y;
-            stats[32 + 8 * u + g] = of.M[u & 1];
+            stats[32 + 8 * u + g] = M[u];
           }
         }
         __syncwarp();
@@ -698,38 +707,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                          : a.raw_o ? a.raw_o + place * a.cache.D : nullptr;
       uint16_t *const b16 = a.out + out_row * a.ldo + hq * a.ldo_head;
 #pragma unroll 1
-      for (int k = 0; k < a.cache.D; k += 8) {
-        float o[8];
-        tmem_load8(o_tm + k, o);
+      for (int k = 0; k < a.cache.D; k += 16) {
+        float o[16];
+        tmem_load16(o_tm + k, o);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] *= inv;
+        for (int i = 0; i < 16; ++i) o[i] *= inv;
         if (mask && on) {
           const uint32_t bad = lost_columns<Fm>(a, it, my_seen, k);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
+          for (int i = 0; i < 16; ++i)
             if (bad >> i & 1u) o[i] = NAN;
         }
         if (!on) continue;
         if (f32) {
-          *reinterpret_cast<float4 *>(f32 + k) = make_float4(o[0], o[1], o[2], o[3]);
-          *reinterpret_cast<float4 *>(f32 + k + 4) = make_float4(o[4], o[5], o[6], o[7]);
+#pragma unroll
+          for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<float4 *>(f32 + k + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
           continue;
         }
         if (pre) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = o[i] * weights.own + pre[k + i] * weights.pre;
+          for (int i = 0; i < 16; ++i) o[i] = o[i] * weights.own + pre[k + i] * weights.pre;
         }
-        uint32_t u[4];
+        uint32_t u[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 8; ++i) {
           const __nv_bfloat162 b = __floats2bfloat162_rn(o[2 * i], o[2 * i + 1]);
           u[i] = *reinterpret_cast<const uint32_t *>(&b);
         }
         if (a.out_vec) {
-          *reinterpret_cast<uint4 *>(b16 + k) = make_uint4(u[0], u[1], u[2], u[3]);
+          uint4 *p = reinterpret_cast<uint4 *>(b16 + k);
+          p[0] = make_uint4(u[0], u[1], u[2], u[3]);
+          p[1] = make_uint4(u[4], u[5], u[6], u[7]);
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) b16[k + i] = static_cast<uint16_t>(u[i / 2] >> (16 * (i & 1)));
+          for (int i = 0; i < 16; ++i) b16[k + i] = static_cast<uint16_t>(u[i / 2] >> (16 * (i & 1)));
         }
       }
       tc_fence_before();
@@ -737,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(ofree_bar(t));
       if (threadIdx.x == 0 && !whole && it.tile0 == 0)
         a.desc[blockIdx.x] = {it.s, it.h, it.rt,
-                              owner_of(sh, it.begin + it.tiles - 1) - static_cast<int>(blockIdx.x) + 1};
+                              owner_of(sh, it.end - 1) - static_cast<int>(blockIdx.x) + 1};
     }
   } else if (warp < 8 + kConverters) {
     // ------------------------------------------------- codes to halves
@@ -751,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ch = DP == 128 ? lane & 7 : lane & 3;
     const int tok = DP == 128 ? (lane >> 3) * 2 + ((lane >> 2) & 1) : lane >> 2;
     auto local = [&](int i) { return DP == 128 ? (i >> 1) * 8 + (tok ^ (i & 1)) : i * 8 + tok; };
-    const uint32_t jobs = static_cast<uint32_t>(sh.end - sh.begin) * kJobs;
+    uint32_t jobs = 0xffffffffu;       // until the last tile's places say so
     uint32_t flags = 0;                // of the jobs under way: not all rows see the tile
     bool ok = true;
     auto request = [&](uint32_t n) {
@@ -759,6 +771,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (n < jobs) {
         const uint32_t tile = n / kJobs, buf = tile % kScaleBufs;
         if (!(ok = wait(atfull_bar(buf), (tile / kScaleBufs) & 1u))) return;
+        if (!more_tiles[buf]) jobs = tile * kJobs;
+        if (n >= jobs) return;
         const bool is_v = n & (kJobs / 2);
         const uint8_t *codes = is_v ? a.cache.v : a.cache.k;
         const uint32_t from = base + C::kPlaces + (buf * kTokens + n % (kJobs / 2) * kGroup) * 8;
@@ -780,7 +794,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       flags |= (partial ? 1u : 0u) << (C::AHEAD - 1);
-      asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll 1
     for (uint32_t n = warp - 8; ok; n += kConverters) {
@@ -823,6 +836,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       flags >>= 1;
       request(n);
+      asm volatile("cp.async.commit_group;" ::: "memory");
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   } else if (warp < 15) {
@@ -859,16 +873,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++pj;
     };
     peek();
-    const uint32_t count = static_cast<uint32_t>(sh.end - sh.begin);
     float scale[4];
     bool was_first = false;
     bool ok = true;
 #pragma unroll 1
-    for (uint32_t step = 0; step <= count; ++step) {
+    for (uint32_t step = 0;; ++step) {
       float fresh[4];
       int64_t at[4];
-      const bool now_first = first;
-      if (step < count) {
+      const bool now_first = first, here = more;
+      if (here) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int tk = tok0 + lane + 32 * i;
@@ -883,18 +896,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                           : in ? NAN : 1.0f;
         }
         peek();
-        if (!is_v) {
-          const int buf = step % kScaleBufs;
-          if (!(ok = wait(atfree_bar(buf), ((step / kScaleBufs) & 1u) ^ 1u))) break;
+      }
+      if (!is_v) {
+        const int buf = step % kScaleBufs;
+        if (!(ok = wait(atfree_bar(buf), ((step / kScaleBufs) & 1u) ^ 1u))) break;
+        if (here) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             asm volatile("st.shared.b64 [%0], %1;" ::"r"(
                              base + C::kPlaces + (buf * kTokens + lane + 32 * i) * 8),
                          "l"(at[i])
                          : "memory");
-          __syncwarp();
-          if (lane == 0) mbar_arrive(atfull_bar(buf));
         }
+        if (lane == 0) more_tiles[buf] = here;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(atfull_bar(buf));
       }
       if (step > 0) {
         const int buf = (step - 1) % kScaleBufs;
@@ -902,14 +918,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         float *out = reinterpret_cast<float *>(sbase + C::kScales + buf * kScaleBytes);
         if (is_v) {
           // Relative to a power of two near the scale of the item's first token.
-          if (was_first) e0 = exponent_of(__shfl_sync(0xffffffffu, scale[0], 0));
+          if (was_first) e0 = min(exponent_of(__shfl_sync(0xffffffffu, scale[0], 0)), 126);
+          const float down = power_of_two(-e0);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const bool fine = scale[i] > 0.0f && scale[i] < INFINITY;
-            out[kTokens + 32 * i + scale_at] = fine ? log2f(scale[i]) - e0 : NAN;
+            const float v = scale[i] * down;
+            float lg, rcp;
+            asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg) : "f"(v));
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rcp) : "f"(v));
+            out[kTokens + 32 * i + scale_at] = fine ? lg : NAN;
             // A bad scale is in the exponent alone: rows that do not see it have weight 0.
-            out[2 * kTokens + 32 * i + scale_at] =
-                fine ? fminf(__fdividef(power_of_two(e0), scale[i]), 3.0e38f) : 1.0f;
+            out[2 * kTokens + 32 * i + scale_at] = fine ? fminf(rcp, 3.0e38f) : 1.0f;
           }
           if (lane == 0) *reinterpret_cast<int *>(out + 3 * kTokens) = e0;
         } else {
@@ -919,6 +939,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(scfull_bar(buf));
       }
+      if (!here) break;
 #pragma unroll
       for (int i = 0; i < 4; ++i) scale[i] = fresh[i];
       was_first = now_first;
@@ -926,13 +947,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     {
       // ----------------------------------------------------------- MMAs
+      constexpr int HT = kTokens / 2;
       constexpr uint32_t s_idesc = idesc_f16(kTokens, false), o_idesc = idesc_f16(DP, true);
-      uint32_t s_step = 0, v_step = 0;      // tiles of tokens of S and of O
-      uint32_t p_uses[2] = {0, 0}, o_uses[2] = {0, 0};
-      // S of tile t against the K tile s_step.
       const uint64_t q_desc = smem_desc_k128_sw128(base);
       const uint64_t k_desc = smem_desc_k128_sw128(base + C::kRing);
       const uint64_t v_desc = desc_mn(base + C::kRing, C::kBlock);
+      uint32_t s_step = 0, v_step = 0;      // tiles of tokens of S and of O
+      uint32_t p_uses[2] = {0, 0}, o_uses[2] = {0, 0};
+      // S of tile t against the K tile s_step.
       auto scores = [&](int t) {
         const uint64_t ad = q_desc + t * (TERMS * C::kTileBytes / 16);
         const uint64_t bd = k_desc + (2 * s_step) % C::SLOTS * (C::kTileBytes / 16);
@@ -948,82 +970,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         commit(s_bar(t));
       };
       auto k_ready = [&] {
-        return wait(full_bar((2 * s_step) % C::SLOTS), ((2 * s_step) / C::SLOTS) & 1u);
+        const bool r = wait(full_bar((2 * s_step) % C::SLOTS), ((2 * s_step) / C::SLOTS) & 1u);
+        tc_fence_after();
+        return r;
+      };
+      auto k_done = [&] {
+        commit(empty_bar((2 * s_step) % C::SLOTS));
+        ++s_step;
       };
       const Item &it = my.items[0];
       bool ok = true, more = next(0);
-      int rows = it.rows, count = it.count, n = 0;
-      if (more) {
-        ok = wait(qfull_bar, 0) && k_ready();
-        if (ok) {
-          tc_fence_after();
+      int n = 0;
+      while (more) {
+        // An item's first scores come after all of the last one's products, which the
+        // warps that bring its rows may wait for.
+        const int rows = it.rows, count = it.count;
+        if (!(ok = wait(qfull_bar, n & 1u) && k_ready())) break;
 #pragma unroll 1
-          for (int t = 0; t < 2; ++t)
-            if (t * kRows < rows) scores(t);
-          commit(empty_bar((2 * s_step) % C::SLOTS));
-          ++s_step;
-        }
-      }
-      while (ok && more) {
-        int next_rows = 0, next_count = 0;
+        for (int t = 0; t * kRows < rows; ++t) scores(t);
+        k_done();
 #pragma unroll 1
         for (int j = 0; ok && j < count; ++j, ++v_step) {
           const bool last = j + 1 == count;
-          if (last) {
-            more = next(0);
-            next_rows = more ? it.rows : 0;
-            next_count = it.count;
-          }
-          const int s_rows = last ? next_rows : rows;
           const int v_slot = (2 * v_step + 1) % C::SLOTS;
           ok = wait(full_bar(v_slot), ((2 * v_step + 1) / C::SLOTS) & 1u);
 #pragma unroll 1
-          for (int t = 0; ok && t < 2; ++t) {
-            if (t * kRows < rows) {
+          for (int t = 0; ok && t * kRows < rows; ++t) {
 #pragma unroll 1
-              for (int half = 0; half < 2; ++half) {
-                ok = wait(p_bar(t, half), (t ? p_uses[1] : p_uses[0]) & 1u);
-                if (ok && j + half == 0 && (t ? o_uses[1] : o_uses[0]) > 0)
-                  ok = wait(ofree_bar(t), ((t ? o_uses[1] : o_uses[0]) - 1) & 1u);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t bd = v_desc + (v_slot * C::kTileBytes + half * (kTokens / 2 * 128)) / 16;
-                const uint32_t d = tmem + C::kO + DP * t, p = tmem + C::kS + 128 * t + 32 * half;
-#pragma unroll
-                for (int q = 0; q < kTokens / 32; ++q)
-                  umma_ts(d, p + 8 * q, bd + q * (2048 / 16), o_idesc, j + half > 0 || q > 0);
-                if (half == 0) commit(pv_bar(t));
-              }
+            for (int half = 0; half < 2; ++half) {
+              ok = wait(p_bar(t, half), (t ? p_uses[1] : p_uses[0]) & 1u);
+              if (ok && j + half == 0 && (t ? o_uses[1] : o_uses[0]) > 0)
+                ok = wait(ofree_bar(t), ((t ? o_uses[1] : o_uses[0]) - 1) & 1u);
               if (!ok) break;
-              ++(t ? p_uses[1] : p_uses[0]);
-              if (j == 0) ++(t ? o_uses[1] : o_uses[0]);
-              if (last) commit(o_bar(t));
+              tc_fence_after();
+              const uint64_t bd = v_desc + (v_slot * C::kTileBytes + half * (HT * 128)) / 16;
+              const uint32_t d = tmem + C::kO + DP * t, p = tmem + C::kS + 128 * t + HT / 2 * half;
+#pragma unroll
+              for (int q = 0; q < HT / 16; ++q)
+                umma_ts(d, p + 8 * q, bd + q * (2048 / 16), o_idesc, j + half > 0 || q > 0);
+              if (half == 0) commit(pv_bar(t));
             }
-            if (!last && t * kRows < s_rows) {
-              if (t == 0) {
-                if (!(ok = k_ready())) break;
-                tc_fence_after();
-              }
+            if (!ok) break;
+            ++(t ? p_uses[1] : p_uses[0]);
+            if (j == 0) ++(t ? o_uses[1] : o_uses[0]);
+            if (last) commit(o_bar(t));
+            if (!last) {
+              if (t == 0 && !(ok = k_ready())) break;
               scores(t);
             }
           }
-          // The next rows' scores come after all of these rows' products, which the warps
-          // that bring the next rows may still wait for.
-          if (ok && last && s_rows > 0 && (ok = wait(qfull_bar, (n + 1) & 1u) && k_ready())) {
-            tc_fence_after();
-#pragma unroll 1
-            for (int t = 0; t < 2; ++t)
-              if (t * kRows < s_rows) scores(t);
-          }
           if (!ok) break;
           commit(empty_bar(v_slot));
-          if (s_rows > 0) {
-            commit(empty_bar((2 * s_step) % C::SLOTS));
-            ++s_step;
-          }
+          if (!last) k_done();
         }
-        rows = next_rows;
-        count = next_count;
+        if (!ok) break;
+        more = next(0);
         ++n;
       }
       commit(done_bar);
