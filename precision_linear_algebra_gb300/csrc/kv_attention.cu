@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
       float sum = l[k];
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+      const float inv = sum > 0.0f || sum != sum ? rcp(sum) : 0.0f;
       float *row = red + (warp * kRows + g + 8 * k) * C::kLdO;
 #pragma unroll
       for (int j = 0; j < C::VH * C::VW; ++j)
@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
               o[j][2 * k + i] * inv * back;
       if (c == 0)
         red_lse[warp * kRows + g + 8 * k] =
-            sum > 0.0f || sum != sum ? M[k] - kShift + log2f(sum) : -INFINITY;
+            sum > 0.0f || sum != sum ? M[k] - kShift + lg2(sum) : -INFINITY;
     }
     __syncthreads();
     const bool whole = count == it.tiles;
@@ -536,11 +536,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
       float weight[kWarps], sum = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        weight[w] = lse[w] == -INFINITY ? 0.0f : exp2f(lse[w] - best);
+        weight[w] = lse[w] == -INFINITY ? 0.0f : ex2(lse[w] - best);
         sum += weight[w];
       }
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-      const float joined = sum == 0.0f ? -INFINITY : best + log2f(sum);
+      const float inv = sum == 0.0f ? 0.0f : rcp(sum);
+      const float joined = sum == 0.0f ? -INFINITY : best + lg2(sum);
       float x[8] = {};
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(kJoinThreads)
 #pragma unroll 4
       for (int i = i0; i < i1; ++i) {
         const float lse = part_lse[part(i)];
-        const float w = lse == -INFINITY ? 0.0f : exp2f(lse - best);
+        const float w = lse == -INFINITY ? 0.0f : ex2(lse - best);
         const float *p = part_o + part(i) * DP + lane * V;
         float y[V];
         if (V >= 4) {
@@ -641,10 +641,10 @@ __global__ void __launch_bounds__(kJoinThreads)
     __syncthreads();
     if (on && side == 0 && lane * V < a.cache.D) {
       sum += sums[slot][DP];
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      const float inv = sum == 0.0f ? 0.0f : rcp(sum);
 #pragma unroll
       for (int j = 0; j < V; ++j) x[j] = (x[j] + sums[slot][lane * V + j]) * inv;
-      const float lse = sum == 0.0f ? -INFINITY : best + log2f(sum);
+      const float lse = sum == 0.0f ? -INFINITY : best + lg2(sum);
       const int t = divide(rr, a.group);
       const int64_t row = static_cast<int64_t>(q.row0) + t;
       const int hq = d.h * a.G + rr - t * a.G;
@@ -767,7 +767,12 @@ fp8la_status launch_join(const AttnArgs &a, const JoinSide &few, const JoinSide 
 fp8la_status launch_pass(AttnArgs a, const Layout &l, uint8_t *ws, bool f32, int format,
                          int64_t max_rows, cudaStream_t s) {
   const int DP = padded_dim(a.cache.D);
-  const bool tc = DP <= 128 && max_rows > kFewRows;
+  auto fits = [](int64_t stride) { return stride >= 0 && stride < (int64_t(1) << 31); };
+  const Cache &c = a.cache;
+  const bool tc = DP <= 128 && max_rows > kFewRows && fits(c.page_stride / 16) &&
+                  fits(c.head_stride / 16) && fits(c.token_stride / 16) &&
+                  fits(c.scale_page_stride) && fits(c.scale_head_stride) &&
+                  fits(c.scale_token_stride);
   // All rows of a prefix are one sequence, which is all of one kernel's.
   const bool both = !(a.whole && tc);
   JoinSide few = {}, many = {};
@@ -875,7 +880,6 @@ fp8la_status fp8_kv_attention(const void *q, int32_t q_dtype, int64_t ld_q, int6
   a.causal = causal != 0;
   a.scale_log2 = scale * kLog2e;
   a.max_rows = max_rows;
-  a.min_units = 1;
   if (prefix) {
     AttnArgs p = a;
     p.whole = m_offsets + num_segments;

@@ -31,7 +31,6 @@ struct AttnArgs {
   float scale_log2;          // of scores, times log2 e
   int64_t row_lo, row_hi;    // rows (tokens times G) of the sequences that are this kernel's
   int64_t max_rows;          // of a segment
-  int32_t min_units;         // of a CTA
   // Shared prefix.  Its own pass takes all rows as one segment (`whole`, S = 1) and
   // writes raw_o, raw_lse; the sequences' pass joins them with its own result.
   const int32_t *whole;      // null, or the word that holds the rows' number
@@ -47,6 +46,17 @@ struct AttnArgs {
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
@@ -90,19 +100,26 @@ __device__ __forceinline__ int tiles_of(const AttnArgs &a, const Seq &q, int rt)
   return seen > 0 ? (seen - 1) / BN + 1 : 1;
 }
 
+// y / m for y >= 0, 0 < m < 2^31; nearly always of 32 bits.
+__device__ __forceinline__ int64_t quotient(int64_t y, uint32_t m) {
+  if (static_cast<uint64_t>(y) >> 32 == 0) return static_cast<uint32_t>(y) / m;
+  return y / m;
+}
+
 // Sum over i < n of floor((x i + b) / m), x, b >= 0, m > 0: whole parts first, then
 // the lattice points under the line counted along the other axis.
-__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t x, int64_t b) {
+__device__ __forceinline__ int64_t floor_sum(int64_t n, uint32_t m, uint32_t x, int64_t b) {
   int64_t sum = 0;
+#pragma unroll 1
   for (;;) {
-    sum += n * (n - 1) / 2 * (x / m) + n * (b / m);
+    const int64_t whole = quotient(b, m);
+    sum += n * (n - 1) / 2 * (x / m) + n * whole;
     x %= m;
-    b %= m;
-    const int64_t y = x * n + b;
-    if (y < m) return sum;
-    n = y / m;
-    b = y % m;
-    const int64_t t = m;
+    const int64_t y = x * n + (b - whole * m);
+    n = quotient(y, m);
+    if (n == 0) return sum;
+    b = y - n * m;
+    const uint32_t t = m;
     m = x;
     x = t;
   }
@@ -118,7 +135,7 @@ __device__ __noinline__ int64_t units_below(const AttnArgs &a, const Seq &q, int
   int64_t sum = static_cast<int64_t>(R) * COST;
   if (R == rts) sum += tiles_of<BM, BN>(a, q, --R);
   const int64_t G = a.G, c = static_cast<int64_t>(q.len) - q.n;
-  int64_t k = c < 0 ? -G * c / BM : 0;
+  int64_t k = c < 0 ? -G * c / BM : 0;  // BM is a power of two
   if (k > R) k = R;
   return sum + k + floor_sum(R - k, BN * G, BM, G * (c + BN) + (k + 1) * BM - 1);
 }
@@ -132,10 +149,16 @@ __device__ __forceinline__ int row_tiles_of(const AttnArgs &a, const Seq &q) {
 }
 
 struct Share {
-  int64_t units, begin, end;   // all units; this CTA's
+  int32_t units, begin, end;   // all units; this CTA's
   int32_t ctas;                // that have work
   int32_t s, h, rt, pos;       // where this CTA begins: unit `pos` of a row tile
 };
+
+// Where the range of CTA b begins: floor(units b / ctas).
+__device__ __forceinline__ int begin_of(int units, int ctas, int b) {
+  const int q = units / ctas;
+  return q * b + (units - q * ctas) * b / ctas;
+}
 
 __device__ __forceinline__ int64_t shfl_up64(int64_t v, int d) {
   return __shfl_up_sync(0xffffffffu, v, d);
@@ -143,7 +166,8 @@ __device__ __forceinline__ int64_t shfl_up64(int64_t v, int d) {
 
 // All units in the order (sequence, K/V head, row tile, then its COST units that are no
 // tiles, then its tiles) are cut into equal ranges, one for each CTA: every SM has the
-// same work whatever the lengths are.  Checks the segments: where they cannot be used, nothing is to be done.
+// same work whatever the lengths are.  2^31 units or more (70 TB of codes) are refused.
+// Checks the segments: where they cannot be used, nothing is to be done.
 template <int THREADS, int BM, int BN, int COST>
 __device__ __noinline__ void share_out(const AttnArgs &a, Share *sh, int64_t *warp_sums) {
   const int S = a.whole ? 1 : a.rows.S;
@@ -190,14 +214,22 @@ __device__ __noinline__ void share_out(const AttnArgs &a, Share *sh, int64_t *wa
     if (w < warp) before += warp_sums[w];
     total += warp_sums[w];
   }
-  const int64_t most = (total + a.min_units - 1) / a.min_units;
-  const int ctas = static_cast<int>(most < gridDim.x ? most : gridDim.x);
+  if (total > INT32_MAX) {
+    if (threadIdx.x == 0) {
+      atomicOr(a.rows.status, kStatusBadDeviceArg);
+      *sh = {0, 0, 0, 0, 0, 0, 0, 0};
+    }
+    __syncthreads();
+    return;
+  }
+  const int units = static_cast<int>(total);
+  const int ctas = min(units, static_cast<int>(gridDim.x));
   const bool idle = static_cast<int>(blockIdx.x) >= ctas;
-  const int64_t begin = idle ? 0 : total * blockIdx.x / ctas;
+  const int begin = idle ? 0 : begin_of(units, ctas, blockIdx.x);
   if (threadIdx.x == 0) {
-    sh->units = total;
+    sh->units = units;
     sh->begin = begin;
-    sh->end = idle ? 0 : total * (blockIdx.x + 1) / ctas;
+    sh->end = idle ? 0 : begin_of(units, ctas, blockIdx.x + 1);
     sh->ctas = ctas;
   }
   if (!idle && begin >= before && begin < before + sum) {
@@ -207,13 +239,12 @@ __device__ __noinline__ void share_out(const AttnArgs &a, Share *sh, int64_t *wa
       const Seq q = load_seq(a, s);
       const int rts = row_tiles_of<BM>(a, q);
       if (rts == 0) continue;
-      const int64_t each = units_below<BM, BN, COST>(a, q, rts, rts);
-      if (begin >= before + H * each) {
-        before += H * each;
+      const int each = static_cast<int>(units_below<BM, BN, COST>(a, q, rts, rts));
+      if (begin >= before + static_cast<int64_t>(H) * each) {
+        before += static_cast<int64_t>(H) * each;
         continue;
       }
-      const int h = static_cast<int>((begin - before) / each);
-      const int64_t left = begin - before - h * each;
+      const int at = begin - static_cast<int>(before), h = at / each, left = at - h * each;
       int lo = 0, hi = rts - 1;
 #pragma unroll 1
       while (lo < hi) {
@@ -224,7 +255,7 @@ __device__ __noinline__ void share_out(const AttnArgs &a, Share *sh, int64_t *wa
       sh->s = s;
       sh->h = h;
       sh->rt = lo;
-      sh->pos = static_cast<int>(left - units_below<BM, BN, COST>(a, q, rts, lo));
+      sh->pos = lo == 0 ? left : left - static_cast<int>(units_below<BM, BN, COST>(a, q, rts, lo));
       break;
     }
   }
@@ -232,22 +263,24 @@ __device__ __noinline__ void share_out(const AttnArgs &a, Share *sh, int64_t *wa
 }
 
 // The CTA whose range holds unit u.
-__device__ __forceinline__ int owner_of(const Share &sh, int64_t u) {
-  return static_cast<int>(((u + 1) * sh.ctas - 1) / sh.units);
+__device__ __forceinline__ int owner_of(const Share &sh, int u) {
+  int b = static_cast<int>(static_cast<float>(u) * sh.ctas / sh.units);
+  b = min(max(b, 0), sh.ctas - 1);
+  while (begin_of(sh.units, sh.ctas, b) > u) --b;
+  while (b + 1 < sh.ctas && begin_of(sh.units, sh.ctas, b + 1) <= u) ++b;
+  return b;
 }
 
 // Tiles tile0 .. tile0+count-1 of the `tiles` of a row tile with `rows` rows, whose last
 // unit, among all units, is the one before `end`.
 struct Item {
   Seq q;
-  int s, h, rt, tile0, count, tiles, rows;
-  int64_t end;
+  int s, h, rt, tile0, count, tiles, rows, end;
 };
 
 // Walks through a CTA's items.
 struct Walk {
-  int64_t at, end;
-  int s, h, rt, pos, rts;
+  int at, end, s, h, rt, pos, rts;
   Seq q;
 };
 template <int BM>
@@ -266,7 +299,7 @@ __device__ __noinline__ void start_walk(const AttnArgs &a, const Share &sh, Walk
 template <int BM, int BN, int COST>
 __device__ __noinline__ bool next_item(const AttnArgs &a, Walk *w, Item *it) {
   // A range that ends before a row tile's first tile leaves it to the next CTA.
-  const int64_t left = w->end - w->at;
+  const int left = w->end - w->at;
   if (left <= 0 || w->pos + left <= COST) return false;
   if (w->rt >= w->rts) {
     w->rt = 0;
@@ -280,7 +313,7 @@ __device__ __noinline__ bool next_item(const AttnArgs &a, Walk *w, Item *it) {
   }
   const int tiles = tiles_of<BM, BN>(a, w->q, w->rt);
   const int tile0 = w->pos > COST ? w->pos - COST : 0;
-  const int64_t rest = COST + tiles - w->pos, mine = rest < left ? rest : left;
+  const int rest = COST + tiles - w->pos, mine = min(rest, left);
   it->q = w->q;
   it->s = w->s;
   it->h = w->h;
@@ -288,7 +321,7 @@ __device__ __noinline__ bool next_item(const AttnArgs &a, Walk *w, Item *it) {
   it->tile0 = tile0;
   it->tiles = tiles;
   it->end = w->at + rest;
-  it->count = static_cast<int>(w->pos + mine) - COST - tile0;
+  it->count = w->pos + mine - COST - tile0;
   it->rows = min(BM, w->q.n * a.G - w->rt * BM);
   w->at += mine;
   w->pos = 0;
@@ -305,8 +338,8 @@ __device__ __forceinline__ Weights weigh(const AttnArgs &a, int64_t t, int hq, f
   const float p = a.pre_lse[t * a.Hq + hq];
   const float top = fmaxf(lse, p);
   if (top == -INFINITY) return {0.0f, 0.0f, top};
-  const float x = exp2f(lse - top), y = exp2f(p - top), inv = 1.0f / (x + y);
-  return {x * inv, y * inv, top + log2f(x + y)};
+  const float x = ex2(lse - top), y = ex2(p - top), inv = rcp(x + y);
+  return {x * inv, y * inv, top + lg2(x + y)};
 }
 
 // Writes N consecutive elements of a row's result, own ones in o, and where `d` is 0

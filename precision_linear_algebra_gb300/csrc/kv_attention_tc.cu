@@ -41,6 +41,8 @@ constexpr int kItemRows = 256;
 constexpr int kTokens = 128;        // of a tile
 // What an item costs beside its tiles, in tiles: bringing its rows, writing them out.
 constexpr int kItemCost = 3;
+constexpr int kItemBufs = 4;
+constexpr int kItemReaders = 10;    // the warps that make weights, 14 and 15
 constexpr int kConverters = 5;
 constexpr int kGroup = 16;          // tokens of a converter's job
 constexpr int kJobs = 2 * kTokens / kGroup;  // of a tile, K's first
@@ -63,7 +65,7 @@ struct Cfg {
   static constexpr int kScales = kPlaces + kScaleBufs * kTokens * 8;
   static constexpr int kFactors = kScales + kScaleBufs * kScaleBytes;
   static constexpr int kBar = kFactors + kItemRows * 4;
-  static constexpr int kBars = 2 * SLOTS + 4 * kScaleBufs + 14;
+  static constexpr int kBars = 2 * SLOTS + 4 * kScaleBufs + 14 + 2 * kItemBufs;
   static constexpr int kMisc = kBar + kBars * 8;
   static constexpr int kAlloc = kMisc + 16 + 1024;
   static constexpr int kS = 0, kO = 256;                // tensor memory columns
@@ -197,6 +199,21 @@ __device__ __forceinline__ void tmem_wait_store() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// 32 bytes, 32-byte aligned: a row's whole sector at once.
+__device__ __forceinline__ void store32(void *p, const uint32_t (&u)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(u[0]),
+               "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+               : "memory");
+}
+
+// A condition that is the same in every turn of a loop, hidden from the compiler: it
+// would make a copy of the loop for each value, and the instruction cache is short.
+__device__ __forceinline__ bool opaque(bool b) {
+  int v;
+  asm volatile("mov.b32 %0, %1;" : "=r"(v) : "r"(static_cast<int>(b)));
+  return v != 0;
+}
+
 // Pairs of FP32 values.
 __device__ __forceinline__ uint64_t pair(float x, float y) {
   uint64_t r;
@@ -258,15 +275,23 @@ __device__ __noinline__ void fetch_q(const AttnArgs &a, const Item &it, uint32_t
                    a.ldq_head * SIZE % 16 == 0;
   const int rows = it.rows, first = it.rt * kItemRows, head0 = it.h * a.G;
   const int64_t token0 = it.q.row0;
+  // Row r of the lane's, its token and head; the next one is RP further.
+  int r = lane / LR;
+  const int rr = first + min(row0 + r, rows - 1);
+  int tok = divide(rr, a.group), head = rr - tok * a.G;
+  const uint8_t *token_at = static_cast<const uint8_t *>(a.q) +
+                            ((token0 + tok) * a.ldq + head0 * a.ldq_head + 8 * sub) * SIZE;
 #pragma unroll 1
-  for (int i = 0; i < 32 / RP; ++i) {
-    const int r = i * RP + lane / LR;
+  for (; r < 32; r += RP) {
     const bool on = row0 + r < rows && 8 * sub < a.cache.D;
-    const int rr = first + min(row0 + r, rows - 1), tok = divide(rr, a.group);
-    const int64_t at = (token0 + tok) * a.ldq + (head0 + rr - tok * a.G) * a.ldq_head + 8 * sub;
-    const uint8_t *from = static_cast<const uint8_t *>(a.q) + (on ? at * SIZE : 0);
+    const uint8_t *from = on ? token_at + head * a.ldq_head * SIZE : static_cast<const uint8_t *>(a.q);
+    head += RP;
+    while (head >= a.G) {
+      head -= a.G;
+      token_at += a.ldq * SIZE;
+    }
     const uint32_t dst = q_chunk<DP>(q_at, r, sub);
-    if (vec || !on) {
+    if (opaque(vec) || !on) {
 #pragma unroll
       for (int term = 0; term < TERMS; ++term)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + term * kTerm),
@@ -417,11 +442,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto o_bar = [&](int t) { return rest + 8u * (8 + t); };
   auto ofree_bar = [&](int t) { return rest + 8u * (10 + t); };
   const uint32_t qfull_bar = rest + 8u * 12, done_bar = rest + 8u * 13;
+  auto itfull_bar = [&](int i) { return rest + 8u * (14 + i); };
+  auto itfree_bar = [&](int i) { return rest + 8u * (14 + kItemBufs + i); };
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sbase + C::kMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sbase + C::kMisc + 4);
   volatile int *poison = reinterpret_cast<volatile int *>(sbase + C::kMisc + 8);
   float *factors = reinterpret_cast<float *>(sbase + C::kFactors);
   __shared__ volatile int more_tiles[kScaleBufs];
+  __shared__ Item items[kItemBufs];
+  __shared__ Walk walk;
+  __shared__ float row_stats[8][64];
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::SLOTS; ++i) {
       mbar_init(full_bar(i), kTokens / kGroup);
@@ -432,6 +462,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(atfree_bar(i), kConverters);
       mbar_init(scfull_bar(i), 2);
       mbar_init(scfree_bar(i), 8);
+    }
+    for (int i = 0; i < kItemBufs; ++i) {
+      mbar_init(itfull_bar(i), 1);
+      mbar_init(itfree_bar(i), kItemReaders);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(s_bar(t), 1);
@@ -463,22 +497,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) ||
            wait_long(bar, parity, timeout_ns, a.rows.status, abort_flag);
   };
-  // Each warp's place in the work, in shared memory: registers are short.  Two items, as
-  // the warps that make weights fetch one's rows of q while they are at the other.
-  struct Place {
-    Walk walk;
-    Item items[2];
-    int more;
-    float stats[64];
+  // Items come from warp 13 through a ring; every warp that wants them takes each in
+  // turn: number n, or none where the work is done.
+  auto item_ready = [&](uint32_t n, bool &ok) {
+    ok = wait(itfull_bar(n % kItemBufs), (n / kItemBufs) & 1u);
+    return ok && items[n % kItemBufs].count > 0;
   };
-  __shared__ Place places[kThreads / 32];
-  Place &my = places[warp];
-  if (lane == 0) start_walk<kItemRows>(a, sh, &my.walk);
-  auto next = [&](int i) {
+  auto item_done = [&](uint32_t n) {
     __syncwarp();
-    if (lane == 0) my.more = next_item<kItemRows, kTokens, kItemCost>(a, &my.walk, &my.items[i]);
-    __syncwarp();
-    return my.more != 0;
+    if (lane == 0) mbar_arrive(itfree_bar(n % kItemBufs));
   };
 
   if (warp < 8) {
@@ -492,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t kLanes16 = 16u << 16;
     uint32_t sc = 0;      // tiles of tokens so far
     uint32_t tiles = 0;   // those of them that this tile of rows took part in
-    uint32_t items = 0;   // likewise
+    uint32_t o_uses = 0;  // items that it took part in
     const uint32_t q_at = base + t * TERMS * C::kTileBytes + (warp & 3) * 32 * 128;
     float *const my_factors = factors + row0;
     auto q_done = [&] {
@@ -500,14 +527,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(qfull_bar);
     };
-    bool ok = true, more = next(0);
+    bool ok, more = item_ready(0, ok);
     if (more) {
-      fetch_q<F32Q, DP>(a, my.items[0], q_at, row0);
+      fetch_q<F32Q, DP>(a, items[0], q_at, row0);
       scale_q<F32Q, DP>(a, q_at, my_factors);
       q_done();
     }
-    for (int n = 0; ok && more; ++n) {
-      const Item &it = my.items[n & 1], &upcoming = my.items[(n + 1) & 1];
+    for (uint32_t n = 0; ok && more; ++n) {
+      const Item &it = items[n % kItemBufs], &upcoming = items[(n + 1) % kItemBufs];
       const int rows = it.rows, count = it.count, tok0 = it.tile0 * kTokens;
       const bool active = t * kRows < rows;
       float factor[4], M[4];
@@ -525,8 +552,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < count; ++j, ++sc) {
         const int buf = sc % kScaleBufs;
         if (!(ok = wait(scfull_bar(buf), (sc / kScaleBufs) & 1u))) break;
-        if (j + 1 == count) more = next((n + 1) & 1);
-        if (!active) {
+        if (j + 1 == count) {
+          more = item_ready(n + 1, ok);
+          if (!ok) break;
+        }
+        if (!opaque(active)) {
           if (lane == 0) mbar_arrive(scfree_bar(buf));
           continue;
         }
@@ -655,11 +685,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         scale_q<F32Q, DP>(a, q_at, my_factors);
         q_done();
       }
-      if (!active) continue;
+      if (!active) {
+        item_done(n);
+        continue;
+      }
       // A row to each lane from here on.
       float sum, best;
       {
-        float *stats = reinterpret_cast<float *>(&my.stats);
+        float *stats = row_stats[warp];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           float y, z;
@@ -680,12 +713,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int r = it.rt * kItemRows + min(row0 + lane, rows - 1);
       const int my_seen = row0 + lane < rows ? tokens_seen(a, it.q, r) : 0;
       // The rows' results.
-      if (!(ok = wait(o_bar(t), items & 1u))) break;
-      ++items;
+      if (!(ok = wait(o_bar(t), o_uses & 1u))) break;
+      ++o_uses;
       tc_fence_after();
       const bool some = sum > 0.0f || sum != sum;
-      const float inv = some ? 1.0f / sum * back : 0.0f;
-      const float lse = some ? best - kShift + log2f(sum) : -INFINITY;
+      const float inv = some ? rcp(sum) * back : 0.0f;
+      const float lse = some ? best - kShift + lg2(sum) : -INFINITY;
       const bool mask = *poison != 0;
       const bool on = row0 + lane < rows;
       const bool whole = it.count == it.tiles;
@@ -706,26 +739,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       float *const f32 = !whole ? a.part_o + part * DP
                          : a.raw_o ? a.raw_o + place * a.cache.D : nullptr;
       uint16_t *const b16 = a.out + out_row * a.ldo + hq * a.ldo_head;
+      const bool wide = ((reinterpret_cast<uintptr_t>(a.out) | a.ldo * 2 | a.ldo_head * 2) & 31) == 0;
 #pragma unroll 1
       for (int k = 0; k < a.cache.D; k += 16) {
         float o[16];
         tmem_load16(o_tm + k, o);
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[i] *= inv;
-        if (mask && on) {
+        if (opaque(mask && on)) {
           const uint32_t bad = lost_columns<Fm>(a, it, my_seen, k);
 #pragma unroll
           for (int i = 0; i < 16; ++i)
             if (bad >> i & 1u) o[i] = NAN;
         }
-        if (!on) continue;
-        if (f32) {
+        if (!opaque(on)) continue;
+        if (opaque(f32 != nullptr)) {
 #pragma unroll
-          for (int i = 0; i < 16; i += 4)
-            *reinterpret_cast<float4 *>(f32 + k + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          for (int i = 0; i < 16; i += 8) {
+            uint32_t u[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) u[e] = __float_as_uint(o[i + e]);
+            store32(f32 + k + i, u);
+          }
           continue;
         }
-        if (pre) {
+        if (opaque(pre != nullptr)) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) o[i] = o[i] * weights.own + pre[k + i] * weights.pre;
         }
@@ -735,10 +773,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const __nv_bfloat162 b = __floats2bfloat162_rn(o[2 * i], o[2 * i + 1]);
           u[i] = *reinterpret_cast<const uint32_t *>(&b);
         }
-        if (a.out_vec) {
-          uint4 *p = reinterpret_cast<uint4 *>(b16 + k);
-          p[0] = make_uint4(u[0], u[1], u[2], u[3]);
-          p[1] = make_uint4(u[4], u[5], u[6], u[7]);
+        if (opaque(wide)) {
+          store32(b16 + k, u);
         } else {
 #pragma unroll
           for (int i = 0; i < 16; ++i) b16[k + i] = static_cast<uint16_t>(u[i / 2] >> (16 * (i & 1)));
@@ -750,6 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (threadIdx.x == 0 && !whole && it.tile0 == 0)
         a.desc[blockIdx.x] = {it.s, it.h, it.rt,
                               owner_of(sh, it.end - 1) - static_cast<int>(blockIdx.x) + 1};
+      item_done(n);
     }
   } else if (warp < 8 + kConverters) {
     // ------------------------------------------------- codes to halves
@@ -815,7 +852,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                        : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                        : "r"(src + i * 512)
                        : "memory");
-          if (flags & 1u) {
+          if (opaque(flags & 1u)) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) found |= Fm::clear4(w[q]);
           }
@@ -849,55 +886,86 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Scales of the columns 2 c, 2 c + 1, 2 c + 8, 2 c + 9 of 16 lie together: a thread
     // that makes weights has those.
     const int scale_at = (lane & ~15) + ((lane >> 1) & 3) * 4 + ((lane >> 3) & 1) * 2 + (lane & 1);
-    const Item &it = my.items[0];
-    int page[4], pj = 0, tok0 = 0, most = 0, h = 0, e0 = 0;
-    bool partial = false, first = false, more = next(0);
-    auto peek = [&] {
-      if (!more) return;
-      if (pj == it.count) {
-        pj = 0;
-        if (!(more = next(0))) return;
-      }
-      const int all = tokens_seen(a, it.q, it.rt * kItemRows);
-      const int32_t *table = a.rows.table + it.s * a.rows.ld_table;
-      most = tokens_seen(a, it.q, it.rt * kItemRows + it.rows - 1);
-      tok0 = (it.tile0 + pj) * kTokens;
-      h = it.h;
-      first = pj == 0;
-      partial = tok0 + kTokens > all && all < most;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int tk = tok0 + lane + 32 * i;
-        page[i] = tk < most ? table[divide(tk, c.page)] : -1;
-      }
-      ++pj;
-    };
-    peek();
+    const uint32_t page16 = static_cast<uint32_t>(c.page_stride >> 4),
+                   token16 = static_cast<uint32_t>(c.token_stride >> 4),
+                   head16 = static_cast<uint32_t>(c.head_stride >> 4);
+    const uint32_t s_page = static_cast<uint32_t>(c.scale_page_stride),
+                   s_token = static_cast<uint32_t>(c.scale_token_stride),
+                   s_head = static_cast<uint32_t>(c.scale_head_stride);
+    // Of the tile whose page numbers have been asked for; place -1: no token.
+    int page[4], place[4], pj = 0, h = 0, e0 = 0;
+    uint32_t n_item = 0;
+    bool partial = false, first = false, have = false, ok = true;
+    if (!is_v && lane == 0) {
+      start_walk<kItemRows>(a, sh, &walk);
+      items[kItemBufs - 1].count = 0;
+    }
     float scale[4];
     bool was_first = false;
-    bool ok = true;
+    // The first turn only reads page numbers.
 #pragma unroll 1
-    for (uint32_t step = 0;; ++step) {
+    for (int step = -1; ok; ++step) {
       float fresh[4];
-      int64_t at[4];
-      const bool now_first = first, here = more;
+      uint64_t at[4];
+      const bool now_first = first, here = have;
       if (here) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int tk = tok0 + lane + 32 * i;
-          const bool in = tk < most, good = in && page[i] >= 0 && page[i] < c.num_pages;
+          const bool in = place[i] >= 0;
+          const bool good = in && page[i] >= 0 && page[i] < c.num_pages;
           if (in && !good) atomicOr(a.rows.status, kStatusBadDeviceArg);
-          const int place = tk - divide(tk, c.page) * c.page_size;
-          at[i] = good ? page[i] * c.page_stride + place * c.token_stride +
-                             h * c.head_stride + (partial ? 1 : 0)
-                       : -1;
-          fresh[i] = good ? scales_from[page[i] * c.scale_page_stride + h * c.scale_head_stride +
-                                        place * c.scale_token_stride]
-                          : in ? NAN : 1.0f;
+          const uint32_t p = page[i], pl = place[i];
+          // Lowest bit: not all rows see the tile.  All bits: there is no token.
+          at[i] = good ? (static_cast<uint64_t>(p) * page16 + static_cast<uint64_t>(pl) * token16 +
+                          static_cast<uint64_t>(h) * head16) * 16 + (partial ? 1 : 0)
+                       : ~0ull;
+          fresh[i] = in ? NAN : 1.0f;
+          if (good)
+            fresh[i] = scales_from[static_cast<uint64_t>(p) * s_page +
+                                   static_cast<uint64_t>(pl) * s_token +
+                                   static_cast<uint64_t>(h) * s_head];
         }
-        peek();
       }
-      if (!is_v) {
+      // The next tile, of this item or the next, which warp 13 makes.
+      const bool fetch = step < 0 || (here && pj == items[n_item % kItemBufs].count);
+      if (fetch) {
+        pj = 0;
+        if (step >= 0) {
+          if (opaque(is_v)) item_done(n_item);
+          ++n_item;
+        }
+        const int i = n_item % kItemBufs;
+        ok = wait(opaque(is_v) ? itfull_bar(i) : itfree_bar(i),
+                  ((n_item / kItemBufs) & 1u) ^ (opaque(is_v) ? 0u : 1u));
+        if (!ok) break;
+        if (!opaque(is_v)) {
+          if (lane == 0) {
+            if (!next_item<kItemRows, kTokens, kItemCost>(a, &walk, &items[i])) items[i].count = 0;
+            mbar_arrive(itfull_bar(i));
+          }
+          __syncwarp();
+        }
+        have = items[i].count > 0;
+      }
+      if (have) {
+        const Item &it = items[n_item % kItemBufs];
+        const int all = tokens_seen(a, it.q, it.rt * kItemRows);
+        const int most = tokens_seen(a, it.q, it.rt * kItemRows + it.rows - 1);
+        const int32_t *table = a.rows.table + it.s * a.rows.ld_table;
+        const int tok0 = (it.tile0 + pj) * kTokens;
+        h = it.h;
+        first = pj == 0;
+        partial = tok0 + kTokens > all && all < most;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int tk = tok0 + lane + 32 * i, p = divide(tk, c.page);
+          place[i] = tk < most ? tk - p * c.page_size : -1;
+          if (tk < most) page[i] = table[p];
+        }
+        ++pj;
+      }
+      if (step < 0) continue;
+      if (!opaque(is_v)) {
         const int buf = step % kScaleBufs;
         if (!(ok = wait(atfree_bar(buf), ((step / kScaleBufs) & 1u) ^ 1u))) break;
         if (here) {
@@ -916,7 +984,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int buf = (step - 1) % kScaleBufs;
         if (!(ok = wait(scfree_bar(buf), (((step - 1) / kScaleBufs) & 1u) ^ 1u))) break;
         float *out = reinterpret_cast<float *>(sbase + C::kScales + buf * kScaleBytes);
-        if (is_v) {
+        if (opaque(is_v)) {
           // Relative to a power of two near the scale of the item's first token.
           if (was_first) e0 = min(exponent_of(__shfl_sync(0xffffffffu, scale[0], 0)), 126);
           const float down = power_of_two(-e0);
@@ -978,13 +1046,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         commit(empty_bar((2 * s_step) % C::SLOTS));
         ++s_step;
       };
-      const Item &it = my.items[0];
-      bool ok = true, more = next(0);
-      int n = 0;
-      while (more) {
+      bool ok;
+      for (uint32_t n = 0; item_ready(n, ok); ++n) {
         // An item's first scores come after all of the last one's products, which the
         // warps that bring its rows may wait for.
-        const int rows = it.rows, count = it.count;
+        const int rows = items[n % kItemBufs].rows, count = items[n % kItemBufs].count;
+        item_done(n);
         if (!(ok = wait(qfull_bar, n & 1u) && k_ready())) break;
 #pragma unroll 1
         for (int t = 0; t * kRows < rows; ++t) scores(t);
@@ -1024,8 +1091,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!last) k_done();
         }
         if (!ok) break;
-        more = next(0);
-        ++n;
       }
       commit(done_bar);
       mbar_wait_drain(done_bar, 0, timeout_ns, a.rows.status);
