@@ -451,6 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ volatile int more_tiles[kScaleBufs];
   __shared__ Item items[kItemBufs];
   __shared__ Walk walk;
+  __shared__ int page_ids[2][kTokens];
   __shared__ float row_stats[8][64];
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::SLOTS; ++i) {
@@ -878,8 +879,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   } else if (warp < 15) {
     // ------------------------------------------------- places and scales
-    // A lane has four tokens of a tile, 32 apart.  The page numbers are read a tile
-    // ahead, and the scales of a tile are written when the next one's places are.
+    // A lane has four tokens of a tile, 32 apart.  In turn `step`, page numbers of tile
+    // step + 1 and scales of tile step are requested, by copies into shared memory, and
+    // the scales of tile step - 1 are written.
     const bool is_v = warp == 14;
     const Cache &c = a.cache;
     const float *const scales_from = is_v ? c.v_scale : c.k_scale;
@@ -892,43 +894,56 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_page = static_cast<uint32_t>(c.scale_page_stride),
                    s_token = static_cast<uint32_t>(c.scale_token_stride),
                    s_head = static_cast<uint32_t>(c.scale_head_stride);
-    // Of the tile whose page numbers have been asked for; place -1: no token.
-    int page[4], place[4], pj = 0, h = 0, e0 = 0;
+    const uint32_t pages = smem_addr(page_ids[warp - 13]) + 4 * lane;
+    auto scales_of = [&](int step) {
+      return base + C::kScales + step % kScaleBufs * kScaleBytes;
+    };
+    auto copy4 = [&](uint32_t dst, const void *src) {
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+    };
+    int pj = 0, h = 0, e0 = 0, tok0 = 0, most = 0;
     uint32_t n_item = 0;
-    bool partial = false, first = false, have = false, ok = true;
-    if (!is_v && lane == 0) {
-      start_walk<kItemRows>(a, sh, &walk);
-      items[kItemBufs - 1].count = 0;
-    }
-    float scale[4];
-    bool was_first = false;
-    // The first turn only reads page numbers.
+    bool partial = false, first = false, was_first = false, have = false, ok = true;
+    if (!is_v && lane == 0) start_walk<kItemRows>(a, sh, &walk);
+    // The first turn only requests page numbers.
 #pragma unroll 1
     for (int step = -1; ok; ++step) {
-      float fresh[4];
-      uint64_t at[4];
-      const bool now_first = first, here = have;
+      const bool here = have;
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
       if (here) {
-#pragma unroll
+        const int buf = step % kScaleBufs;
+        ok = wait(scfree_bar(buf), ((step / kScaleBufs) & 1u) ^ 1u);
+        if (ok && !opaque(is_v)) ok = wait(atfree_bar(buf), ((step / kScaleBufs) & 1u) ^ 1u);
+        if (!ok) break;
+#pragma unroll 1
         for (int i = 0; i < 4; ++i) {
-          const bool in = place[i] >= 0;
-          const bool good = in && page[i] >= 0 && page[i] < c.num_pages;
+          const int tk = tok0 + lane + 32 * i;
+          int p;
+          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(p) : "r"(pages + 128 * i) : "memory");
+          const bool in = tk < most, good = in && p >= 0 && p < c.num_pages;
           if (in && !good) atomicOr(a.rows.status, kStatusBadDeviceArg);
-          const uint32_t p = page[i], pl = place[i];
-          // Lowest bit: not all rows see the tile.  All bits: there is no token.
-          at[i] = good ? (static_cast<uint64_t>(p) * page16 + static_cast<uint64_t>(pl) * token16 +
-                          static_cast<uint64_t>(h) * head16) * 16 + (partial ? 1 : 0)
-                       : ~0ull;
-          fresh[i] = in ? NAN : 1.0f;
+          const uint64_t pl = tk - divide(tk, c.page) * c.page_size;
+          const uint32_t dst = scales_of(step) + 4 * (scale_at + 32 * i + (opaque(is_v) ? kTokens : 0));
           if (good)
-            fresh[i] = scales_from[static_cast<uint64_t>(p) * s_page +
-                                   static_cast<uint64_t>(pl) * s_token +
-                                   static_cast<uint64_t>(h) * s_head];
+            copy4(dst, scales_from + static_cast<uint64_t>(p) * s_page + pl * s_token +
+                           static_cast<uint64_t>(h) * s_head);
+          else
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(dst), "f"(in ? NAN : 1.0f) : "memory");
+          if (!opaque(is_v)) {
+            // Lowest bit: not all rows see the tile.  All bits: there is no token.
+            const uint64_t at = good ? (static_cast<uint64_t>(p) * page16 + pl * token16 +
+                                        static_cast<uint64_t>(h) * head16) * 16 + (partial ? 1 : 0)
+                                     : ~0ull;
+            asm volatile("st.shared.b64 [%0], %1;" ::"r"(
+                             base + C::kPlaces + (buf * kTokens + lane + 32 * i) * 8),
+                         "l"(at)
+                         : "memory");
+          }
         }
       }
+      const bool now_first = first;
       // The next tile, of this item or the next, which warp 13 makes.
-      const bool fetch = step < 0 || (here && pj == items[n_item % kItemBufs].count);
-      if (fetch) {
+      if (step < 0 || (here && pj == items[n_item % kItemBufs].count)) {
         pj = 0;
         if (step >= 0) {
           if (opaque(is_v)) item_done(n_item);
@@ -950,66 +965,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (have) {
         const Item &it = items[n_item % kItemBufs];
         const int all = tokens_seen(a, it.q, it.rt * kItemRows);
-        const int most = tokens_seen(a, it.q, it.rt * kItemRows + it.rows - 1);
+        most = tokens_seen(a, it.q, it.rt * kItemRows + it.rows - 1);
         const int32_t *table = a.rows.table + it.s * a.rows.ld_table;
-        const int tok0 = (it.tile0 + pj) * kTokens;
+        tok0 = (it.tile0 + pj) * kTokens;
         h = it.h;
         first = pj == 0;
         partial = tok0 + kTokens > all && all < most;
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < 4; ++i) {
-          const int tk = tok0 + lane + 32 * i, p = divide(tk, c.page);
-          place[i] = tk < most ? tk - p * c.page_size : -1;
-          if (tk < most) page[i] = table[p];
+          const int tk = tok0 + lane + 32 * i;
+          if (tk < most) copy4(pages + 128 * i, table + divide(tk, c.page));
         }
         ++pj;
       }
+      asm volatile("cp.async.commit_group;" ::: "memory");
       if (step < 0) continue;
       if (!opaque(is_v)) {
         const int buf = step % kScaleBufs;
-        if (!(ok = wait(atfree_bar(buf), ((step / kScaleBufs) & 1u) ^ 1u))) break;
-        if (here) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            asm volatile("st.shared.b64 [%0], %1;" ::"r"(
-                             base + C::kPlaces + (buf * kTokens + lane + 32 * i) * 8),
-                         "l"(at[i])
-                         : "memory");
-        }
+        if (!here && !(ok = wait(atfree_bar(buf), ((step / kScaleBufs) & 1u) ^ 1u))) break;
         if (lane == 0) more_tiles[buf] = here;
         __syncwarp();
         if (lane == 0) mbar_arrive(atfull_bar(buf));
       }
       if (step > 0) {
-        const int buf = (step - 1) % kScaleBufs;
-        if (!(ok = wait(scfree_bar(buf), (((step - 1) / kScaleBufs) & 1u) ^ 1u))) break;
-        float *out = reinterpret_cast<float *>(sbase + C::kScales + buf * kScaleBytes);
+        // Of the tile before, whose scales have come.
+        float *out = reinterpret_cast<float *>(smem_raw + (scales_of(step - 1) - raw));
+        __syncwarp();
         if (opaque(is_v)) {
           // Relative to a power of two near the scale of the item's first token.
-          if (was_first) e0 = min(exponent_of(__shfl_sync(0xffffffffu, scale[0], 0)), 126);
+          if (was_first) e0 = min(exponent_of(out[kTokens]), 126);
+          __syncwarp();
           const float down = power_of_two(-e0);
-#pragma unroll
+#pragma unroll 1
           for (int i = 0; i < 4; ++i) {
-            const bool fine = scale[i] > 0.0f && scale[i] < INFINITY;
-            const float v = scale[i] * down;
-            float lg, rcp;
+            float *at = out + kTokens + 32 * i + scale_at;
+            const float scale = *at, v = scale * down;
+            const bool fine = scale > 0.0f && scale < INFINITY;
+            float lg, inv;
             asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg) : "f"(v));
-            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rcp) : "f"(v));
-            out[kTokens + 32 * i + scale_at] = fine ? lg : NAN;
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(v));
+            at[0] = fine ? lg : NAN;
             // A bad scale is in the exponent alone: rows that do not see it have weight 0.
-            out[2 * kTokens + 32 * i + scale_at] = fine ? fminf(rcp, 3.0e38f) : 1.0f;
+            at[kTokens] = fine ? fminf(inv, 3.0e38f) : 1.0f;
           }
           if (lane == 0) *reinterpret_cast<int *>(out + 3 * kTokens) = e0;
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) out[32 * i + scale_at] = scale[i];
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(scfull_bar(buf));
+        if (lane == 0) mbar_arrive(scfull_bar((step - 1) % kScaleBufs));
       }
       if (!here) break;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) scale[i] = fresh[i];
       was_first = now_first;
     }
   } else {
@@ -1052,42 +1056,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         // warps that bring its rows may wait for.
         const int rows = items[n % kItemBufs].rows, count = items[n % kItemBufs].count;
         item_done(n);
-        if (!(ok = wait(qfull_bar, n & 1u) && k_ready())) break;
+        // Turn j: the products of tile j, then the scores of tile j + 1 of the item; an
+        // item's first scores come after all of the last one's products, which the warps
+        // that bring its rows may wait for.
 #pragma unroll 1
-        for (int t = 0; t * kRows < rows; ++t) scores(t);
-        k_done();
-#pragma unroll 1
-        for (int j = 0; ok && j < count; ++j, ++v_step) {
+        for (int j = -1; ok && j < count; ++j) {
           const bool last = j + 1 == count;
           const int v_slot = (2 * v_step + 1) % C::SLOTS;
-          ok = wait(full_bar(v_slot), ((2 * v_step + 1) / C::SLOTS) & 1u);
+          if (j >= 0) ok = wait(full_bar(v_slot), ((2 * v_step + 1) / C::SLOTS) & 1u);
 #pragma unroll 1
           for (int t = 0; ok && t * kRows < rows; ++t) {
+            if (j >= 0) {
 #pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-              ok = wait(p_bar(t, half), (t ? p_uses[1] : p_uses[0]) & 1u);
-              if (ok && j + half == 0 && (t ? o_uses[1] : o_uses[0]) > 0)
-                ok = wait(ofree_bar(t), ((t ? o_uses[1] : o_uses[0]) - 1) & 1u);
-              if (!ok) break;
-              tc_fence_after();
-              const uint64_t bd = v_desc + (v_slot * C::kTileBytes + half * (HT * 128)) / 16;
-              const uint32_t d = tmem + C::kO + DP * t, p = tmem + C::kS + 128 * t + HT / 2 * half;
+              for (int half = 0; half < 2; ++half) {
+                ok = wait(p_bar(t, half), (t ? p_uses[1] : p_uses[0]) & 1u);
+                if (ok && j + half == 0 && (t ? o_uses[1] : o_uses[0]) > 0)
+                  ok = wait(ofree_bar(t), ((t ? o_uses[1] : o_uses[0]) - 1) & 1u);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t bd = v_desc + (v_slot * C::kTileBytes + half * (HT * 128)) / 16;
+                const uint32_t d = tmem + C::kO + DP * t, p = tmem + C::kS + 128 * t + HT / 2 * half;
 #pragma unroll
-              for (int q = 0; q < HT / 16; ++q)
-                umma_ts(d, p + 8 * q, bd + q * (2048 / 16), o_idesc, j + half > 0 || q > 0);
-              if (half == 0) commit(pv_bar(t));
+                for (int q = 0; q < HT / 16; ++q)
+                  umma_ts(d, p + 8 * q, bd + q * (2048 / 16), o_idesc, j + half > 0 || q > 0);
+                if (half == 0) commit(pv_bar(t));
+              }
+              if (!ok) break;
+              ++(t ? p_uses[1] : p_uses[0]);
+              if (j == 0) ++(t ? o_uses[1] : o_uses[0]);
+              if (last) commit(o_bar(t));
             }
-            if (!ok) break;
-            ++(t ? p_uses[1] : p_uses[0]);
-            if (j == 0) ++(t ? o_uses[1] : o_uses[0]);
-            if (last) commit(o_bar(t));
             if (!last) {
-              if (t == 0 && !(ok = k_ready())) break;
+              if (t == 0) {
+                ok = (j >= 0 || wait(qfull_bar, n & 1u)) && k_ready();
+                if (!ok) break;
+              }
               scores(t);
             }
           }
           if (!ok) break;
-          commit(empty_bar(v_slot));
+          if (j >= 0) {
+            commit(empty_bar(v_slot));
+            ++v_step;
+          }
           if (!last) k_done();
         }
         if (!ok) break;
