@@ -39,17 +39,19 @@ template <bool F32Q, int DP>
 struct Cfg {
   static constexpr int CH = DP / 16;                  // 16-byte chunks of a row
   static constexpr int kK = kGroup * DP;
-  static constexpr int kStage = 2 * kK + 3 * kGroup * 4;  // K, V, ks, vs, 1 / vs
-  static constexpr int kRing = kStages * kStage;
+  static constexpr int kRing = kStages * 2 * kK;      // of a warp: K and V
+  static constexpr int kScales = kWarps * kRing;      // ks, log2 vs, 1 / vs of each stage
+  static constexpr int kScaleStage = 3 * kGroup * 4;
+  static constexpr int kBar = kScales + kWarps * kStages * kScaleStage;
   static constexpr int KS = DP / 16;                  // MMA steps along D
   static constexpr int TERMS = F32Q ? 2 : 1;
   static constexpr bool QREG = KS * TERMS <= 8;
-  static constexpr int kQ = kWarps * kRing;           // query fragments
+  static constexpr int kQ = kBar + kWarps * kStages * 8;  // query fragments
   static constexpr int kQBytes = QREG ? 0 : KS * TERMS * 32 * 16;
   static constexpr int kLdO = DP + 4;                 // of the warps' results, floats
   static constexpr int kRed = kWarps * kRows * (kLdO + 1) * 4;
-  static constexpr int kSmem =
-      kQ + kQBytes > kRed ? kQ + kQBytes : kRed;
+  static_assert(kRed <= kScales, "the results overlay the rings");
+  static constexpr int kSmem = kQ + kQBytes + 1024;
   static constexpr int CTAS = F32Q || DP > 128 ? (DP > 128 ? 1 : 2) : 3;
   static constexpr int VW = DP == 64 ? 8 : 16;        // V bytes of a lane
   static constexpr int VH = DP == 256 ? 2 : 1;        // ... times
@@ -99,15 +101,23 @@ __device__ __forceinline__ void sts_f(uint32_t a, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
 
-// Bank spreading of the 16-byte chunks: a phase of K's reads takes 4 chunks of 2
-// tokens, one of V's 2 chunks of every other token of 8.
+// Where chunk ch of a token's row lies in a group's 16 rows, as TMA swizzles them: rows
+// of 128 bytes (64 with DP = 64), halves of longer ones one behind the other.  A phase
+// of K's reads takes the even or odd chunks of 2 tokens, one of V's 2 chunks of every
+// other token of 8: all in different banks.
 template <int DP>
-__device__ __forceinline__ int swizzle_k(int token) {
-  return DP == 64 ? 0 : (token & 1) * 4;
+__device__ __forceinline__ uint32_t chunk_at(int token, int ch) {
+  if (DP == 64) return token * 64 + ((ch ^ ((token >> 1) & 3)) << 4);
+  return (ch >> 3) * (kGroup * 128) + token * 128 + (((ch ^ token) & 7) << 4);
 }
-template <int DP>
-__device__ __forceinline__ int swizzle_v(int token) {
-  return DP == 64 ? 2 * ((token >> 1) & 1) : 2 * ((token >> 1) & 3);
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, uint32_t bar,
+                                            int32_t c0, int32_t c1, int32_t c2, int32_t c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
 }
 
 // 2^e with the exponent of v (0 where v is not a positive finite number).
@@ -161,24 +171,41 @@ __device__ __forceinline__ void load_q(const AttnArgs &a, int64_t at, bool on, f
 
 template <bool F32Q, int FMT, int DP>
 __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
-    kv_attention_kernel(const __grid_constant__ AttnArgs a) {
+    kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
+                        const __grid_constant__ CUtensorMap tmV,
+                        const __grid_constant__ AttnArgs a, const uint64_t timeout_ns) {
   using C = Cfg<F32Q, DP>;
   using Fm = Format<FMT>;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ uint8_t smem_raw[];
   __shared__ Share sh;
   __shared__ int64_t warp_sums[kWarps];
   __shared__ Walk walk;
   __shared__ Item it;
   __shared__ int more;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ volatile int abort_flag;
+  const uint32_t raw = smem_addr(smem_raw), sbase = (raw + 1023u) & ~1023u;
+  uint8_t *const smem = smem_raw + (sbase - raw);
+  // The same in all lanes, which the compiler would not see otherwise.
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
+  const uint32_t bars = sbase + C::kBar + warp * kStages * 8;
+  if (lane == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(bars + 8 * i, 1);
+    fence_mbar_init();
+    abort_flag = 0;
+  }
   pdl_wait();
   pdl_launch_dependents();
-  if (threadIdx.x == 0 && a.desc) a.desc[blockIdx.x].parts = 0;
+  if (threadIdx.x == 0) a.desc[blockIdx.x].parts = 0;
   share_out<kThreads, kRows, kTile, kItemCost>(a, &sh, warp_sums);
   const Cache &kc = a.cache;
-  const uint32_t ring = smem_addr(smem) + warp * C::kRing;
-  const uint32_t qsm = smem_addr(smem) + C::kQ;
+  const uint32_t ring = sbase + warp * C::kRing;
+  const uint32_t scale_ring = sbase + C::kScales + warp * kStages * C::kScaleStage;
+  const uint32_t qsm = sbase + C::kQ;
+  uint32_t put = 0, taken = 0;         // groups requested and taken so far
+  auto el = [](int f, int c) {         // first element of a lane's chunk f of K's rows
+    return DP == 64 ? 16 * c : (f >> 1) * 128 + 32 * c + 16 * (f & 1);
+  };
 
   if (threadIdx.x == 0) start_walk<kRows>(a, sh, &walk);
   for (;;) {
@@ -202,8 +229,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
     const int most = tokens_seen(a, q, rt * kRows + rows - 1);
     const int begin = tile0 * kTile, end = min(begin + count * kTile, most);
 
-    // Token `first + lane`'s place in the cache, for lanes below 16, in bytes of
-    // codes and in scales; the table is read one step before it is needed.
+    // Pages are looked up one step before they are needed.  Where pages are made of
+    // whole groups, a group is two copies by TMA (a page that there is not: zeros);
+    // else each row is copied in chunks of 16 bytes.
     const int32_t *table = a.rows.table + s * a.rows.ld_table;
     const uint8_t *kbase = kc.k + h * kc.head_stride, *vbase = kc.v + h * kc.head_stride;
     const float *ksbase = kc.k_scale + h * kc.scale_head_stride;
@@ -212,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
       const int t = first + (lane & 15);
       return t < end ? table[divide(t, kc.page)] : -1;
     };
-    auto request = [&](int first, int page, int slot) {
+    auto request = [&](int first, int page) {
       const int t = first + (lane & 15);
       bool on = t < end;
       if (on && (page < 0 || page >= kc.num_pages)) {
@@ -220,34 +248,49 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
         on = false;
       }
       const int place = t - divide(t, kc.page) * kc.page_size;
-      const int64_t code = on ? page * kc.page_stride + place * kc.token_stride : -1;
+      const int slot = put % kStages;
+      const uint32_t dst = ring + slot * 2 * C::kK;
       const int64_t sc = on ? page * kc.scale_page_stride + place * kc.scale_token_stride : 0;
-      const uint32_t dst = ring + slot * C::kStage;
-      cp_async4(dst + 2 * C::kK + lane * 4, (lane < 16 ? ksbase : vsbase) + sc, on);
+      cp_async4(scale_ring + slot * C::kScaleStage + lane * 4, (lane < 16 ? ksbase : vsbase) + sc, on);
+      if (a.tma) {
+        // The slot was read by all lanes before the barrier that ended its turn.
+        if (lane == 0) {
+          const int p = on ? page : kc.num_pages;
+          mbar_arrive_expect_tx(bars + 8 * slot, 2 * C::kK);
 #pragma unroll
-      for (int i = 0; i < kGroup * C::CH / 32; ++i) {
-        const int id = lane + 32 * i, token = id / C::CH, ch = id % C::CH;
-        const int64_t off = __shfl_sync(0xffffffffu, code, token);
-        const bool ok = off >= 0 && ch * 16 < kc.D;
-        const int64_t from = ok ? off + ch * 16 : 0;
-        cp_async16(dst + token * DP + (ch ^ swizzle_k<DP>(token)) * 16, kbase + from, ok);
-        cp_async16(dst + C::kK + token * DP + (ch ^ swizzle_v<DP>(token)) * 16, vbase + from, ok);
+          for (int f = 0; f < C::VH; ++f) {
+            tma_load_4d(dst + f * kGroup * 128, &tmK, bars + 8 * slot, 128 * f, place, h, p);
+            tma_load_4d(dst + C::kK + f * kGroup * 128, &tmV, bars + 8 * slot, 128 * f, place, h, p);
+          }
+        }
+      } else {
+        const int64_t code = on ? page * kc.page_stride + place * kc.token_stride : -1;
+#pragma unroll 1
+        for (int i = 0; i < kGroup * C::CH / 32; ++i) {
+          const int id = lane + 32 * i, token = id / C::CH, ch = id % C::CH;
+          const int64_t off = __shfl_sync(0xffffffffu, code, token);
+          const bool ok = off >= 0 && ch * 16 < kc.D;
+          const int64_t from = ok ? off + ch * 16 : 0;
+          cp_async16(dst + chunk_at<DP>(token, ch), kbase + from, ok);
+          cp_async16(dst + C::kK + chunk_at<DP>(token, ch), vbase + from, ok);
+        }
       }
+      ++put;
     };
     const int first = begin + warp * kGroup;
     int page = page_at(first);
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < kStages - 1; ++i) {
       if (first + i * kTile < end) {
         const int p = page;
         page = page_at(first + (i + 1) * kTile);
-        request(first + i * kTile, p, i);
+        request(first + i * kTile, p);
       }
       cp_commit();
     }
 
     // Query fragments: k 2c, 2c+1, 2c+8, 2c+9 of step 4 f + j stand for the elements
-    // 64 f + 16 c + 4 j .. + 3, so that a lane's codes are 16 bytes of a row.
+    // el(f, c) + 4 j .. + 3, so that a lane's codes are 16 bytes of a row.
     uint32_t qf[C::QREG ? C::KS * C::TERMS : 1][4];
     float factor[2];
     {
@@ -259,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
 #pragma unroll 1
         for (int f = 0; f < DP / 64; ++f) {
           float x[16];
-          load_q<F32Q>(a, row + 64 * f + 16 * c, 64 * f + 16 * c < kc.D, x);
+          load_q<F32Q>(a, row + el(f, c), el(f, c) < kc.D, x);
 #pragma unroll
           for (int j = 0; j < 16; ++j) m = fmaxf(m, fabsf(x[j]));
         }
@@ -274,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int64_t row = (static_cast<int64_t>(q.row0) + tok[i]) * a.ldq + head[i] * a.ldq_head;
-          load_q<F32Q>(a, row + 64 * f + 16 * c, 64 * f + 16 * c < kc.D, x[i]);
+          load_q<F32Q>(a, row + el(f, c), el(f, c) < kc.D, x[i]);
           const float up = power_of_two(e[i]);
 #pragma unroll
           for (int j = 0; j < 16; ++j) x[i][j] *= up;
@@ -315,34 +358,36 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
     float M[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
     int e0 = 0;
     bool poison = false;
-    int slot = 0;
 #pragma unroll 1
     for (int base = first; base < end; base += kTile) {
       cp_wait<kStages - 2>();
+      const int slot = taken % kStages;
+      if (a.tma && !__all_sync(0xffffffffu, mbar_wait(bars + 8 * slot, (taken / kStages) & 1u,
+                                                      timeout_ns, a.rows.status, &abort_flag)))
+        break;
+      ++taken;
       __syncwarp();
       {
         const int ahead = base + (kStages - 1) * kTile;
         if (ahead < end) {
           const int p = page;
           page = page_at(ahead + kTile);
-          request(ahead, p, (slot + kStages - 1) % kStages);
+          request(ahead, p);
         }
         cp_commit();
       }
-      const uint32_t st = ring + slot * C::kStage, scales = st + 2 * C::kK;
+      const uint32_t st = ring + slot * 2 * C::kK, scales = scale_ring + slot * C::kScaleStage;
       // V's scales: logarithm and reciprocal, relative to a power of two near the first.
       if (base == first) {
-        e0 = exponent_of(lds_f(scales + 64));
+        e0 = min(exponent_of(lds_f(scales + 64)), 126);
         __syncwarp();
       }
       if (lane < 16) {
-        const float v = lds_f(scales + 64 + 4 * lane);
-        const bool fine = v > 0.0f && v < INFINITY;
-        const bool in = base + lane < end;
-        sts_f(scales + 64 + 4 * lane, !in ? 0.0f : fine ? log2f(v) - e0 : NAN);
+        const float v = lds_f(scales + 64 + 4 * lane), near = v * power_of_two(-e0);
+        const bool in = base + lane < end, fine = v > 0.0f && v < INFINITY;
+        sts_f(scales + 64 + 4 * lane, !in ? 0.0f : fine ? lg2(near) : NAN);
         // A bad scale is in the exponent alone: rows that do not see it have weight 0.
-        sts_f(scales + 128 + 4 * lane,
-              fine ? fminf(__fdiv_rn(power_of_two(e0), v), 3.0e38f) : 1.0f);
+        sts_f(scales + 128 + 4 * lane, in && fine ? fminf(rcp(near), 3.0e38f) : 1.0f);
       }
       // Scores of tokens g and 8 + g against the 16 rows.
       float sc[2][4] = {};
@@ -352,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int token = g + 8 * i;
-          const uint4 w = lds128(st + token * DP + ((4 * f + c) ^ swizzle_k<DP>(token)) * 16);
+          const uint4 w = lds128(st + chunk_at<DP>(token, el(f, c) / 16));
           kw[i][0] = w.x; kw[i][1] = w.y; kw[i][2] = w.z; kw[i][3] = w.w;
         }
 #pragma unroll
@@ -439,20 +484,25 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
                               pack_half(w[1][0], w[1][1]), pack_half(w[1][2], w[1][3])};
       // Values.  Where some rows do not see a token (weight 0), its codes that are not
       // finite must not reach them: they are taken out here and put in at the end.
-      const bool partial = all < most && base + kGroup > all;
+      const bool partial = all < most && base + kGroup > all, tail = base + kGroup > end;
 #pragma unroll
       for (int f = 0; f < C::VH; ++f) {
         uint32_t vw[4][C::VW / 4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int token = 2 * c + (i & 1) + 8 * (i >> 1);
-          const uint32_t row = st + C::kK + token * DP;
+          const uint32_t v_at = st + C::kK;
           if (C::VW == 16) {
-            const uint4 v = lds128(row + ((8 * f + g) ^ swizzle_v<DP>(token)) * 16);
+            const uint4 v = lds128(v_at + chunk_at<DP>(token, 8 * f + g));
             vw[i][0] = v.x; vw[i][1] = v.y; vw[i][C::VW / 8] = v.z; vw[i][C::VW / 4 - 1] = v.w;
           } else {
-            const uint2 v = lds64(row + ((g >> 1) ^ swizzle_v<DP>(token)) * 16 + (g & 1) * 8);
+            const uint2 v = lds64(v_at + chunk_at<DP>(token, g >> 1) + (g & 1) * 8);
             vw[i][0] = v.x; vw[i][1] = v.y;
+          }
+          // What lies behind the end may be anything.
+          if (tail && base + token >= end) {
+#pragma unroll
+            for (int j = 0; j < C::VW / 4; ++j) vw[i][j] = 0;
           }
           if (partial) {
 #pragma unroll
@@ -473,9 +523,14 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
           mma_f16(o[f * C::VW + 4 * j + 3], pf, decode2<FMT>(a1 >> 16), decode2<FMT>(b1 >> 16));
         }
       }
-      if (++slot == kStages) slot = 0;
+      // Reads before the copies that a next turn asks for.
+      if (a.tma) fence_proxy_async_smem();
     }
     cp_wait<0>();
+    for (; taken < put; ++taken)  // where a wait ran out
+      if (a.tma)
+        mbar_wait_drain(bars + 8 * (taken % kStages), (taken / kStages) & 1u, timeout_ns,
+                        a.rows.status);
     if (__any_sync(0xffffffffu, poison)) {
       for (int base = first; base < end; base += kTile) {
         if (base + kGroup <= all) continue;
@@ -564,7 +619,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
     }
     if (threadIdx.x == 0 && !whole && tile0 == 0)
       a.desc[blockIdx.x] = {s, h, rt, owner_of(sh, it.end - 1) - static_cast<int>(blockIdx.x) + 1};
+    fence_proxy_async_smem();
     __syncthreads();  // the results overlay the rings
+    if (abort_flag) break;
   }
 }
 
@@ -670,8 +727,29 @@ fp8la_status launch(Kern kern, dim3 grid, int threads, size_t smem, cudaStream_t
   return cudaLaunchKernelEx(&cfg, kern, a...) == cudaSuccess ? FP8LA_OK : FP8LA_ERR_CUDA;
 }
 
+// Codes as [page][head][place][D] in boxes of 16 places and up to 128 bytes.  A
+// dimension of one element has a stride of no meaning, for which TMA gets another one.
+bool code_map(CUtensorMap *m, const uint8_t *p, const Cache &c, int DP) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.D), static_cast<cuuint64_t>(c.page_size),
+                              static_cast<cuuint64_t>(c.heads),
+                              static_cast<cuuint64_t>(c.num_pages)};
+  const cuuint64_t strides[3] = {
+      static_cast<cuuint64_t>(c.page_size > 1 ? c.token_stride : 256),
+      static_cast<cuuint64_t>(c.heads > 1 ? c.head_stride : 256),
+      static_cast<cuuint64_t>(c.num_pages > 1 ? c.page_stride : 256)};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(DP < 128 ? DP : 128), kGroup, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t *>(p), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             DP == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <bool F32Q, int FMT, int DP>
-fp8la_status launch_few_one(const AttnArgs &a, int slot, int ctas, cudaStream_t s) {
+fp8la_status launch_few_one(AttnArgs a, int slot, int ctas, cudaStream_t s) {
   using C = Cfg<F32Q, DP>;
   auto kern = kv_attention_kernel<F32Q, FMT, DP>;
   if (once_per_device(slot, [&] {
@@ -679,7 +757,14 @@ fp8la_status launch_few_one(const AttnArgs &a, int slot, int ctas, cudaStream_t 
                                     C::kSmem);
       }) != cudaSuccess)
     return FP8LA_ERR_CUDA;
-  return launch(kern, dim3(ctas), kThreads, C::kSmem, s, a);
+  // TMA's limits: strides below 2^40 bytes.  Measured, us, with TMA / in chunks of 16
+  // bytes: see above.
+  CUtensorMap k = {}, v = {};
+  const int64_t most = int64_t(1) << 40;
+  a.tma = a.cache.page_size % kGroup == 0 && a.cache.page_stride < most &&
+          a.cache.head_stride < most && a.cache.token_stride < most &&
+          code_map(&k, a.cache.k, a.cache, DP) && code_map(&v, a.cache.v, a.cache, DP);
+  return launch(kern, dim3(ctas), kThreads, C::kSmem, s, k, v, a, wait_timeout_ns());
 }
 
 int padded_dim(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }

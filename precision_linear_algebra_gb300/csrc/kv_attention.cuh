@@ -27,6 +27,7 @@ struct AttnArgs {
   float *lse;                // [T][ld_lse], natural logarithm; may be null
   int64_t ld_lse;
   int32_t Hq, G, causal;
+  int32_t tma;               // whether 16 tokens lie together, as TMA takes them
   Divisor group;             // by G
   float scale_log2;          // of scores, times log2 e
   int64_t row_lo, row_hi;    // rows (tokens times G) of the sequences that are this kernel's
@@ -131,7 +132,8 @@ __device__ __forceinline__ int64_t floor_sum(int64_t n, uint32_t m, uint32_t x, 
 // (len - n + BN) + (rt + 1) BM - 1) / (BN G)) tiles, and one where that is less.
 template <int BM, int BN, int COST>
 __device__ __noinline__ int64_t units_below(const AttnArgs &a, const Seq &q, int rts, int R) {
-  if (!a.causal) return static_cast<int64_t>(R) * (tiles_of<BM, BN>(a, q, 0) + COST);
+  if (!a.causal || rts == 1)
+    return static_cast<int64_t>(R) * (tiles_of<BM, BN>(a, q, 0) + COST);
   int64_t sum = static_cast<int64_t>(R) * COST;
   if (R == rts) sum += tiles_of<BM, BN>(a, q, --R);
   const int64_t G = a.G, c = static_cast<int64_t>(q.len) - q.n;
