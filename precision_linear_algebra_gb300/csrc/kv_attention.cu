@@ -28,10 +28,12 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = 4;
 constexpr int kRows = 16;       // rows of a tile
-constexpr int kGroup = 16;      // tokens of a warp's step
-constexpr int kTile = kWarps * kGroup;
+constexpr int kGroup = 16;      // tokens that TMA brings at once
+constexpr int kSubs = 2;        // groups of a warp's step
+constexpr int kStep = kSubs * kGroup;
+constexpr int kTile = kWarps * kStep;
 constexpr int kItemCost = 1;    // of an item beside its tiles, in tiles
-constexpr int kStages = 4;
+constexpr int kStages = 2;
 constexpr float kShift = 7.0f;  // w of the running maximum is 2^7
 constexpr float kLazy = 8.0f;   // it is raised where 2^8 is passed
 
@@ -39,9 +41,10 @@ template <bool F32Q, int DP>
 struct Cfg {
   static constexpr int CH = DP / 16;                  // 16-byte chunks of a row
   static constexpr int kK = kGroup * DP;
-  static constexpr int kRing = kStages * 2 * kK;      // of a warp: K and V
+  static constexpr int kStage = kSubs * 2 * kK;       // of a warp: K and V of each group
+  static constexpr int kRing = kStages * kStage;
   static constexpr int kScales = kWarps * kRing;      // ks, log2 vs, 1 / vs of each stage
-  static constexpr int kScaleStage = 3 * kGroup * 4;
+  static constexpr int kScaleStage = 3 * kStep * 4;
   static constexpr int kBar = kScales + kWarps * kStages * kScaleStage;
   static constexpr int KS = DP / 16;                  // MMA steps along D
   static constexpr int TERMS = F32Q ? 2 : 1;
@@ -237,11 +240,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
     const float *ksbase = kc.k_scale + h * kc.scale_head_stride;
     const float *vsbase = kc.v_scale + h * kc.scale_head_stride;
     auto page_at = [&](int first) {
-      const int t = first + (lane & 15);
+      const int t = first + lane;
       return t < end ? table[divide(t, kc.page)] : -1;
     };
     auto request = [&](int first, int page) {
-      const int t = first + (lane & 15);
+      const int t = first + lane;
       bool on = t < end;
       if (on && (page < 0 || page >= kc.num_pages)) {
         atomicOr(a.rows.status, kStatusBadDeviceArg);
@@ -249,35 +252,40 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
       }
       const int place = t - divide(t, kc.page) * kc.page_size;
       const int slot = put % kStages;
-      const uint32_t dst = ring + slot * 2 * C::kK;
+      const uint32_t dst = ring + slot * C::kStage, bar = bars + 8 * slot;
+      const uint32_t sdst = scale_ring + slot * C::kScaleStage + lane * 4;
       const int64_t sc = on ? page * kc.scale_page_stride + place * kc.scale_token_stride : 0;
-      cp_async4(scale_ring + slot * C::kScaleStage + lane * 4, (lane < 16 ? ksbase : vsbase) + sc, on);
+      cp_async4(sdst, ksbase + sc, on);
+      cp_async4(sdst + 4 * kStep, vsbase + sc, on);
       if (a.tma) {
-        // The slot was read by all lanes before the barrier that ended its turn.
-        if (lane == 0) {
+        // Every lane has read the slot before the barrier that ended its turn.
+        if (lane == 0) mbar_arrive_expect_tx(bar, C::kStage);
+        __syncwarp();
+        if (lane % kGroup == 0) {
           const int p = on ? page : kc.num_pages;
-          mbar_arrive_expect_tx(bars + 8 * slot, 2 * C::kK);
+          const uint32_t at = dst + lane / kGroup * 2 * C::kK;
 #pragma unroll
           for (int f = 0; f < C::VH; ++f) {
-            tma_load_4d(dst + f * kGroup * 128, &tmK, bars + 8 * slot, 128 * f, place, h, p);
-            tma_load_4d(dst + C::kK + f * kGroup * 128, &tmV, bars + 8 * slot, 128 * f, place, h, p);
+            tma_load_4d(at + f * kGroup * 128, &tmK, bar, 128 * f, place, h, p);
+            tma_load_4d(at + C::kK + f * kGroup * 128, &tmV, bar, 128 * f, place, h, p);
           }
         }
       } else {
         const int64_t code = on ? page * kc.page_stride + place * kc.token_stride : -1;
 #pragma unroll 1
-        for (int i = 0; i < kGroup * C::CH / 32; ++i) {
+        for (int i = 0; i < kStep * C::CH / 32; ++i) {
           const int id = lane + 32 * i, token = id / C::CH, ch = id % C::CH;
           const int64_t off = __shfl_sync(0xffffffffu, code, token);
           const bool ok = off >= 0 && ch * 16 < kc.D;
           const int64_t from = ok ? off + ch * 16 : 0;
-          cp_async16(dst + chunk_at<DP>(token, ch), kbase + from, ok);
-          cp_async16(dst + C::kK + chunk_at<DP>(token, ch), vbase + from, ok);
+          const uint32_t at = dst + token / kGroup * 2 * C::kK + chunk_at<DP>(token % kGroup, ch);
+          cp_async16(at, kbase + from, ok);
+          cp_async16(at + C::kK, vbase + from, ok);
         }
       }
       ++put;
     };
-    const int first = begin + warp * kGroup;
+    const int first = begin + warp * kStep;
     int page = page_at(first);
 #pragma unroll 1
     for (int i = 0; i < kStages - 1; ++i) {
@@ -376,83 +384,80 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
         }
         cp_commit();
       }
-      const uint32_t st = ring + slot * 2 * C::kK, scales = scale_ring + slot * C::kScaleStage;
+      const uint32_t st = ring + slot * C::kStage, scales = scale_ring + slot * C::kScaleStage;
       // V's scales: logarithm and reciprocal, relative to a power of two near the first.
       if (base == first) {
-        e0 = min(exponent_of(lds_f(scales + 64)), 126);
+        e0 = min(exponent_of(lds_f(scales + 4 * kStep)), 126);
         __syncwarp();
       }
-      if (lane < 16) {
-        const float v = lds_f(scales + 64 + 4 * lane), near = v * power_of_two(-e0);
+      {
+        const float v = lds_f(scales + 4 * (kStep + lane)), near = v * power_of_two(-e0);
         const bool in = base + lane < end, fine = v > 0.0f && v < INFINITY;
-        sts_f(scales + 64 + 4 * lane, !in ? 0.0f : fine ? lg2(near) : NAN);
+        sts_f(scales + 4 * (kStep + lane), !in ? 0.0f : fine ? lg2(near) : NAN);
         // A bad scale is in the exponent alone: rows that do not see it have weight 0.
-        sts_f(scales + 128 + 4 * lane, in && fine ? fminf(rcp(near), 3.0e38f) : 1.0f);
+        sts_f(scales + 4 * (2 * kStep + lane), in && fine ? fminf(rcp(near), 3.0e38f) : 1.0f);
       }
-      // Scores of tokens g and 8 + g against the 16 rows.
-      float sc[2][4] = {};
+      // Scores of tokens 16 u + 8 i + g against the 16 rows, in sc[2 u + i].
+      float sc[2 * kSubs][4] = {};
 #pragma unroll
-      for (int f = 0; f < DP / 64; ++f) {
-        uint32_t kw[2][4];
+      for (int u = 0; u < kSubs; ++u) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int token = g + 8 * i;
-          const uint4 w = lds128(st + chunk_at<DP>(token, el(f, c) / 16));
-          kw[i][0] = w.x; kw[i][1] = w.y; kw[i][2] = w.z; kw[i][3] = w.w;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t b[2][2];
+        for (int f = 0; f < DP / 64; ++f) {
+          uint32_t kw[2][4];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            b[i][0] = decode2<FMT>(kw[i][j] & 0xffffu);
-            b[i][1] = decode2<FMT>(kw[i][j] >> 16);
+            const uint4 w = lds128(st + u * 2 * C::kK + chunk_at<DP>(g + 8 * i, el(f, c) / 16));
+            kw[i][0] = w.x; kw[i][1] = w.y; kw[i][2] = w.z; kw[i][3] = w.w;
           }
 #pragma unroll
-          for (int t = 0; t < C::TERMS; ++t) {
-            const int step = (4 * f + j) * C::TERMS + t;
-            if (C::QREG) {
-              mma_f16(sc[0], qf[step], b[0][0], b[0][1]);
-              mma_f16(sc[1], qf[step], b[1][0], b[1][1]);
-            } else {
-              const uint4 w = lds128(qsm + (step * 32 + lane) * 16);
-              const uint32_t qw[4] = {w.x, w.y, w.z, w.w};
-              mma_f16(sc[0], qw, b[0][0], b[0][1]);
-              mma_f16(sc[1], qw, b[1][0], b[1][1]);
+          for (int j = 0; j < 4; ++j) {
+            uint32_t b[2][2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              b[i][0] = decode2<FMT>(kw[i][j] & 0xffffu);
+              b[i][1] = decode2<FMT>(kw[i][j] >> 16);
+            }
+#pragma unroll
+            for (int t = 0; t < C::TERMS; ++t) {
+              const int step = (4 * f + j) * C::TERMS + t;
+              if (C::QREG) {
+                mma_f16(sc[2 * u], qf[step], b[0][0], b[0][1]);
+                mma_f16(sc[2 * u + 1], qf[step], b[1][0], b[1][1]);
+              } else {
+                const uint4 w = lds128(qsm + (step * 32 + lane) * 16);
+                const uint32_t qw[4] = {w.x, w.y, w.z, w.w};
+                mma_f16(sc[2 * u], qw, b[0][0], b[0][1]);
+                mma_f16(sc[2 * u + 1], qw, b[1][0], b[1][1]);
+              }
             }
           }
         }
       }
       __syncwarp();
-      // Exponents and weights of tokens 2c, 2c+1, 8+2c, 9+2c.
-      float iv[2][2];
+      // Exponents and weights of tokens 8 i + 2c, 8 i + 2c + 1.
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 2 * kSubs; ++i) {
         const float2 ks = lds_f2(scales + 32 * i + 8 * c);
-        const float2 lv = lds_f2(scales + 64 + 32 * i + 8 * c);
-        const float2 r = lds_f2(scales + 128 + 32 * i + 8 * c);
-        iv[i][0] = r.x;
-        iv[i][1] = r.y;
+        const float2 lv = lds_f2(scales + 4 * kStep + 32 * i + 8 * c);
         sc[i][0] = fmaf(sc[i][0] * ks.x, factor[0], lv.x);
         sc[i][1] = fmaf(sc[i][1] * ks.y, factor[0], lv.y);
         sc[i][2] = fmaf(sc[i][2] * ks.x, factor[1], lv.x);
         sc[i][3] = fmaf(sc[i][3] * ks.y, factor[1], lv.y);
       }
-      const bool edge = base + kGroup > min(all, end);
-      if (edge) {
+      if (base + kStep > min(all, end)) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 2 * kSubs; ++i)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            if (base + 8 * i + 2 * c + (k & 1) >= min(seen[k >> 1], end)) {
-              sc[i][k] = -INFINITY;
-            }
+            if (base + 8 * i + 2 * c + (k & 1) >= min(seen[k >> 1], end)) sc[i][k] = -INFINITY;
       }
       float mx[2];
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        mx[k] = fmaxf(fmaxf(sc[0][2 * k], sc[0][2 * k + 1]),
-                      fmaxf(sc[1][2 * k], sc[1][2 * k + 1]));
+      for (int k = 0; k < 2; ++k) {
+        mx[k] = fmaxf(sc[0][2 * k], sc[0][2 * k + 1]);
+#pragma unroll
+        for (int i = 1; i < 2 * kSubs; ++i) mx[k] = fmaxf(mx[k], fmaxf(sc[i][2 * k], sc[i][2 * k + 1]));
+      }
       if (__any_sync(0xffffffffu, mx[0] > M[0] + kLazy || mx[1] > M[1] + kLazy)) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -472,55 +477,59 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
       }
       const float top[2] = {M[0] == -INFINITY ? 0.0f : M[0] - kShift,
                             M[1] == -INFINITY ? 0.0f : M[1] - kShift};
-      float w[2][4];
+      uint32_t pf[kSubs][4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2 * kSubs; ++i) {
+        const float2 iv = lds_f2(scales + 8 * kStep + 32 * i + 8 * c);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          w[i][k] = ex2(sc[i][k] - top[k >> 1]);
-          l[k >> 1] = fmaf(w[i][k], iv[i][k & 1], l[k >> 1]);
-        }
-      const uint32_t pf[4] = {pack_half(w[0][0], w[0][1]), pack_half(w[0][2], w[0][3]),
-                              pack_half(w[1][0], w[1][1]), pack_half(w[1][2], w[1][3])};
+        for (int k = 0; k < 4; ++k) sc[i][k] = ex2(sc[i][k] - top[k >> 1]);
+        l[0] = fmaf(sc[i][0], iv.x, fmaf(sc[i][1], iv.y, l[0]));
+        l[1] = fmaf(sc[i][2], iv.x, fmaf(sc[i][3], iv.y, l[1]));
+        pf[i >> 1][2 * (i & 1)] = pack_half(sc[i][0], sc[i][1]);
+        pf[i >> 1][2 * (i & 1) + 1] = pack_half(sc[i][2], sc[i][3]);
+      }
       // Values.  Where some rows do not see a token (weight 0), its codes that are not
       // finite must not reach them: they are taken out here and put in at the end.
-      const bool partial = all < most && base + kGroup > all, tail = base + kGroup > end;
+      const bool partial = all < most && base + kStep > all, tail = base + kStep > end;
 #pragma unroll
-      for (int f = 0; f < C::VH; ++f) {
-        uint32_t vw[4][C::VW / 4];
+      for (int u = 0; u < kSubs; ++u) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int token = 2 * c + (i & 1) + 8 * (i >> 1);
-          const uint32_t v_at = st + C::kK;
-          if (C::VW == 16) {
-            const uint4 v = lds128(v_at + chunk_at<DP>(token, 8 * f + g));
-            vw[i][0] = v.x; vw[i][1] = v.y; vw[i][C::VW / 8] = v.z; vw[i][C::VW / 4 - 1] = v.w;
-          } else {
-            const uint2 v = lds64(v_at + chunk_at<DP>(token, g >> 1) + (g & 1) * 8);
-            vw[i][0] = v.x; vw[i][1] = v.y;
+        for (int f = 0; f < C::VH; ++f) {
+          uint32_t vw[4][C::VW / 4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int token = 2 * c + (i & 1) + 8 * (i >> 1);
+            const uint32_t v_at = st + u * 2 * C::kK + C::kK;
+            if (C::VW == 16) {
+              const uint4 v = lds128(v_at + chunk_at<DP>(token, 8 * f + g));
+              vw[i][0] = v.x; vw[i][1] = v.y; vw[i][C::VW / 8] = v.z; vw[i][C::VW / 4 - 1] = v.w;
+            } else {
+              const uint2 v = lds64(v_at + chunk_at<DP>(token, g >> 1) + (g & 1) * 8);
+              vw[i][0] = v.x; vw[i][1] = v.y;
+            }
           }
-          // What lies behind the end may be anything.
-          if (tail && base + token >= end) {
+          if (tail || partial) {
 #pragma unroll
-            for (int j = 0; j < C::VW / 4; ++j) vw[i][j] = 0;
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int j = 0; j < C::VW / 4; ++j) {
+                // What lies behind the end may be anything.
+                if (base + 16 * u + 2 * c + (i & 1) + 8 * (i >> 1) >= end) vw[i][j] = 0;
+                if (partial) poison |= Fm::clear4(vw[i][j]);
+              }
           }
-          if (partial) {
 #pragma unroll
-            for (int j = 0; j < C::VW / 4; ++j) poison |= Fm::clear4(vw[i][j]);
+          for (int j = 0; j < C::VW / 4; ++j) {
+            const uint32_t a0 = __byte_perm(vw[0][j], vw[1][j], 0x5140);
+            const uint32_t a1 = __byte_perm(vw[0][j], vw[1][j], 0x7362);
+            const uint32_t b0 = __byte_perm(vw[2][j], vw[3][j], 0x5140);
+            const uint32_t b1 = __byte_perm(vw[2][j], vw[3][j], 0x7362);
+            float(*oo)[4] = &o[f * C::VW + 4 * j];
+            mma_f16(oo[0], pf[u], decode2<FMT>(a0 & 0xffffu), decode2<FMT>(b0 & 0xffffu));
+            mma_f16(oo[1], pf[u], decode2<FMT>(a0 >> 16), decode2<FMT>(b0 >> 16));
+            mma_f16(oo[2], pf[u], decode2<FMT>(a1 & 0xffffu), decode2<FMT>(b1 & 0xffffu));
+            mma_f16(oo[3], pf[u], decode2<FMT>(a1 >> 16), decode2<FMT>(b1 >> 16));
           }
-        }
-#pragma unroll
-        for (int j = 0; j < C::VW / 4; ++j) {
-          const uint32_t a0 = __byte_perm(vw[0][j], vw[1][j], 0x5140);
-          const uint32_t a1 = __byte_perm(vw[0][j], vw[1][j], 0x7362);
-          const uint32_t b0 = __byte_perm(vw[2][j], vw[3][j], 0x5140);
-          const uint32_t b1 = __byte_perm(vw[2][j], vw[3][j], 0x7362);
-          float(&oo)[4] = o[f * C::VW + 4 * j];
-          mma_f16(oo, pf, decode2<FMT>(a0 & 0xffffu), decode2<FMT>(b0 & 0xffffu));
-          mma_f16(o[f * C::VW + 4 * j + 1], pf, decode2<FMT>(a0 >> 16), decode2<FMT>(b0 >> 16));
-          mma_f16(o[f * C::VW + 4 * j + 2], pf, decode2<FMT>(a1 & 0xffffu),
-                  decode2<FMT>(b1 & 0xffffu));
-          mma_f16(o[f * C::VW + 4 * j + 3], pf, decode2<FMT>(a1 >> 16), decode2<FMT>(b1 >> 16));
         }
       }
       // Reads before the copies that a next turn asks for.
@@ -533,8 +542,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
                         a.rows.status);
     if (__any_sync(0xffffffffu, poison)) {
       for (int base = first; base < end; base += kTile) {
-        if (base + kGroup <= all) continue;
-        for (int t = base; t < min(base + kGroup, end); ++t) {
+        if (base + kStep <= all) continue;
+        for (int t = base; t < min(base + kStep, end); ++t) {
           const int p = table[divide(t, kc.page)];
           if (p < 0 || p >= kc.num_pages) continue;
           const uint8_t *row = vbase + p * kc.page_stride +
