@@ -548,7 +548,8 @@ FP8LA_API fp8la_status fp8_kv_read(
  * All sequences' rows go through the prefix together, so that it is read once.
  *
  * q: fp32 or bf16 [rows][num_heads][head_dim], rows ld_q and heads ld_q_head
- * elements apart; out: bf16, likewise; lse: fp32 [rows][ld_lse], or NULL.
+ * elements apart; out: bf16, likewise; lse: fp32 [rows][ld_lse], or NULL; neither may
+ * overlap q, the cache or the other.
  * max_rows: the rows of the longest segment, or more (`rows`, if nothing better is
  * known): it chooses the kernels, and a segment with more makes the call write
  * nothing and record FP8LA_ERR_DEVICE_ARG.  num_heads a multiple of kv_heads, rows *

@@ -657,7 +657,7 @@ class KVCache:
     with the heads inside the page's tokens (transpose(1, 2)) is as good.
     """
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "fmt", "shape", "struct", "ref")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "fmt", "shape", "device", "struct", "ref")
 
     def __init__(self, k, v, k_scale, v_scale, fmt="e4m3"):
         import torch
@@ -671,6 +671,7 @@ class KVCache:
         assert v_scale.stride() == sst
         self.k, self.v, self.k_scale, self.v_scale, self.fmt = k, v, k_scale, v_scale, fmt
         self.shape = (P, H, page, D)
+        self.device = k.get_device()
         self.struct = fp8la_kv_cache(
             k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), P, page, H, D,
             _FORMATS[fmt], st[0], st[1], st[2], sst[0], sst[1], sst[2])
@@ -704,6 +705,13 @@ def _heads(t, shape, dtype=None):
     return s0, s1
 
 
+def _on_current_device(t, cache):
+    """A launch goes to the current device, whose memory the pointers have to be of."""
+    import torch
+    dev = t.get_device()
+    assert dev == cache.device == torch._C._cuda_getDevice()
+
+
 def kv_append(k, v, cache, m_offsets, kv_lens, page_table):
     """Quantises k and v, fp32 or bf16 CUDA [T][heads][D], into a KVCache.
 
@@ -714,6 +722,7 @@ def kv_append(k, v, cache, m_offsets, kv_lens, page_table):
     """
     T = k.shape[0]
     _, H, _, D = cache.shape
+    _on_current_device(k, cache)
     ldk, ldkh = _heads(k, (T, H, D))
     ldv, ldvh = _heads(v, (T, H, D), k.dtype)
     S, po, pl, pt, ldt, pages = _sequences(m_offsets, kv_lens, page_table)
@@ -735,6 +744,7 @@ def kv_read(cache, m_offsets, kv_lens, page_table, rows, dtype=None, k=None, v=N
         k = torch.empty((rows, H, D), dtype=dtype, device=dev)
     if v is None:
         v = torch.empty((rows, H, D), dtype=dtype, device=dev)
+    _on_current_device(k, cache)
     ldk, ldkh = _heads(k, (rows, H, D), dtype)
     ldv, ldvh = _heads(v, (rows, H, D), dtype)
     S, po, pl, pt, ldt, pages = _sequences(m_offsets, kv_lens, page_table)
@@ -760,6 +770,7 @@ def kv_attention(q, cache, m_offsets, kv_lens, page_table, max_rows=None, scale=
     import torch
     T, Hq, D = q.shape
     dev = q.device
+    _on_current_device(q, cache)
     ldq, ldqh = _heads(q, (T, Hq, cache.shape[3]))
     if out is None:
         out, ldo, ldoh = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev), Hq * D, D

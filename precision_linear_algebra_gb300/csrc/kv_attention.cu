@@ -32,7 +32,9 @@ constexpr int kGroup = 16;      // tokens that TMA brings at once
 constexpr int kSubs = 2;        // groups of a warp's step
 constexpr int kStep = kSubs * kGroup;
 constexpr int kTile = kWarps * kStep;
-constexpr int kItemCost = 1;    // of an item beside its tiles, in tiles
+// What an item costs beside its tiles, in tiles.  64 requests of up to 8192 tokens, us,
+// with 0 to 5: 141, 130, 121, 110, 109, 110.
+constexpr int kItemCost = 4;
 constexpr int kStages = 2;
 constexpr float kShift = 7.0f;  // w of the running maximum is 2^7
 constexpr float kLazy = 8.0f;   // it is raised where 2^8 is passed
@@ -636,87 +638,134 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
 
 // ---------------------------------------------------------------------- join
 // Joins the partial results of items that several CTAs shared: CTA b began it
-// (its second partial result), the next parts - 1 went on (their first ones).  A
-// block takes four rows at a time, two warps each; parts are added in the CTAs'
-// order.  Both kernels' items are joined in one launch.
+// (its second partial result), the next parts - 1 went on (their first ones).  A row
+// has one warp or, where there are many parts, several, whose sums are added in order;
+// both kernels' items are joined in one launch.
 constexpr int kJoinThreads = 256;
-constexpr int kJoinRows = 4;
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kFewJoinRows = 4;
+constexpr int kManyParts = 16;
+constexpr int kJoinCtasPerSm = 8;
+constexpr int kAtOnce = 8;      // parts whose loads are under way
 
 struct JoinSide {
   const float *part_o, *part_lse;
   const Desc *desc;
-  int32_t BM, ctas;
+  int32_t BM, ctas, blocks;  // blocks for each CTA
 };
 
 template <int DP>
 __global__ void __launch_bounds__(kJoinThreads)
-    kv_join_kernel(const AttnArgs a, const JoinSide few, const JoinSide many) {
+    kv_join_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ JoinSide few,
+                   const __grid_constant__ JoinSide many) {
   constexpr int V = DP / 32;
-  __shared__ float sums[kJoinRows][DP + 2];
+  __shared__ float sums[kJoinWarps][DP + 1];
   pdl_wait();
   pdl_launch_dependents();
-  const bool first = static_cast<int>(blockIdx.x) < few.ctas;
-  const int cta = blockIdx.x - (first ? 0 : few.ctas);
-  const float *part_o = first ? few.part_o : many.part_o;
-  const float *part_lse = first ? few.part_lse : many.part_lse;
-  const int BM = first ? few.BM : many.BM;
-  const Desc d = (first ? few.desc : many.desc)[cta];
-  if (d.parts == 0) return;
-  const Seq q = load_seq(a, d.s);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int side = warp & 1, slot = warp >> 1;
-  const int rows = min(BM, q.n * a.G - d.rt * BM);
-  const int half = (d.parts + 1) / 2;
-  const int i0 = side * half, i1 = min(d.parts, i0 + half);
-  for (int r0 = blockIdx.y * kJoinRows; r0 < rows; r0 += gridDim.y * kJoinRows) {
-    const int r = r0 + slot, rr = d.rt * BM + r;
-    const bool on = r < rows;
-    auto part = [&](int i) {
-      return static_cast<int64_t>(2 * (cta + i) + (i == 0 ? 1 : 0)) * BM + r;
-    };
-    float best = -INFINITY, x[V] = {}, sum = 0.0f;
-    if (on) {
-      for (int i = lane; i < d.parts; i += 32) best = fmaxf(best, part_lse[part(i)]);
+  const int few_blocks = few.ctas * few.blocks;
+  const int blocks = few_blocks + many.ctas * many.blocks;
+  // A few rows of a CTA's item in each turn.  Most have nothing to join, and CTAs that
+  // have are about equally far apart: a grid of an odd size deals them out.
+  auto turn_of = [&](int block, bool *first, int *cta) {
+    *first = block < few_blocks;
+    const int at = *first ? block : block - few_blocks, ctas = *first ? few.ctas : many.ctas;
+    *cta = at % ctas;
+    return at / ctas;
+  };
+  // Each lane looks at one of the next 32 turns.
+  for (int round = 0; blockIdx.x + round * gridDim.x < blocks; round += 32) {
+    const int64_t mine = blockIdx.x + static_cast<int64_t>(round + lane) * gridDim.x;
+    Desc look = {0, 0, 0, 0};
+    if (mine < blocks) {
+      bool first;
+      int cta;
+      turn_of(static_cast<int>(mine), &first, &cta);
+      look = (first ? few.desc : many.desc)[cta];
+    }
+    for (uint32_t some = __ballot_sync(0xffffffffu, look.parts > 0); some; some &= some - 1) {
+      const int i = __ffs(some) - 1;
+      const Desc d = {__shfl_sync(0xffffffffu, look.s, i), __shfl_sync(0xffffffffu, look.h, i),
+                      __shfl_sync(0xffffffffu, look.rt, i), __shfl_sync(0xffffffffu, look.parts, i)};
+      bool first;
+      int cta;
+      const int turn = turn_of(blockIdx.x + (round + i) * gridDim.x, &first, &cta);
+      const float *part_o = first ? few.part_o : many.part_o;
+      const float *part_lse = first ? few.part_lse : many.part_lse;
+      const int BM = first ? few.BM : many.BM;
+      const Seq q = load_seq(a, d.s);
+      const int rows = min(BM, q.n * a.G - d.rt * BM);
+      const int group = first ? kFewJoinRows : kJoinWarps;      // rows of this turn
+      const int each = d.parts > kManyParts ? min(group, 2) : group;  // rows at a time
+      const int warps = kJoinWarps / each;                      // of a row
+      const int r_end = min(rows, (turn + 1) * group);
+      for (int r0 = turn * group; r0 < r_end; r0 += each) {
+        const int r = r0 + warp / warps, rr = d.rt * BM + r;
+        const bool on = r < r_end;
+        auto part = [&](int i) {
+          return static_cast<int64_t>(2 * (cta + i) + (i == 0 ? 1 : 0)) * BM + r;
+        };
+        float best = -INFINITY, x[V] = {}, sum = 0.0f;
+        if (on) {
+          for (int i = lane; i < d.parts; i += 32) best = fmaxf(best, part_lse[part(i)]);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
-#pragma unroll 4
-      for (int i = i0; i < i1; ++i) {
-        const float lse = part_lse[part(i)];
-        const float w = lse == -INFINITY ? 0.0f : ex2(lse - best);
-        const float *p = part_o + part(i) * DP + lane * V;
-        float y[V];
-        if (V >= 4) {
+          for (int o = 16; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
+          const int i1 = d.parts * (warp % warps + 1) / warps;
+          for (int i0 = d.parts * (warp % warps) / warps; i0 < i1; i0 += 32) {
+            // A weight to each lane, so that the parts' loads wait for nothing.
+            const int n = min(32, i1 - i0);
+            const float lse = lane < n ? part_lse[part(i0 + lane)] : -INFINITY;
+            const float mine = lse == -INFINITY ? 0.0f : ex2(lse - best);
+#pragma unroll 1
+            for (int i = 0; i < n; i += kAtOnce) {
+              float y[kAtOnce][V];
 #pragma unroll
-          for (int j = 0; j < V; j += 4)
-            *reinterpret_cast<float4 *>(&y[j]) = *reinterpret_cast<const float4 *>(p + j);
-        } else {
-          *reinterpret_cast<float2 *>(&y[0]) = *reinterpret_cast<const float2 *>(p);
+              for (int u = 0; u < kAtOnce; ++u) {
+                const float *p = part_o + part(i0 + min(i + u, n - 1)) * DP + lane * V;
+                if (V >= 4) {
+#pragma unroll
+                  for (int j = 0; j < V; j += 4)
+                    *reinterpret_cast<float4 *>(&y[u][j]) = *reinterpret_cast<const float4 *>(p + j);
+                } else {
+                  *reinterpret_cast<float2 *>(&y[u][0]) = *reinterpret_cast<const float2 *>(p);
+                }
+              }
+#pragma unroll
+              for (int u = 0; u < kAtOnce; ++u) {
+                if (i + u >= n) break;
+                const float w = __shfl_sync(0xffffffffu, mine, i + u);
+                sum += w;
+#pragma unroll
+                for (int j = 0; j < V; ++j) x[j] = fmaf(w, y[u][j], x[j]);
+              }
+            }
+          }
         }
-        sum += w;
-        if (w != 0.0f) {
+        if (warps > 1) {
+          __syncthreads();
 #pragma unroll
-          for (int j = 0; j < V; ++j) x[j] = fmaf(w, y[j], x[j]);
+          for (int j = 0; j < V; ++j) sums[warp][lane * V + j] = x[j];
+          if (lane == 0) sums[warp][DP] = sum;
+          __syncthreads();
+          if (warp % warps > 0) continue;
+          for (int w = warp + 1; w < warp + warps; ++w) {
+            sum += sums[w][DP];
+#pragma unroll
+            for (int j = 0; j < V; ++j) x[j] += sums[w][lane * V + j];
+          }
+        }
+        if (on && lane * V < a.cache.D) {
+          const float inv = sum == 0.0f ? 0.0f : rcp(sum);
+#pragma unroll
+          for (int j = 0; j < V; ++j) x[j] *= inv;
+          const float lse = sum == 0.0f ? -INFINITY : best + lg2(sum);
+          const int t = divide(rr, a.group);
+          const int64_t row = static_cast<int64_t>(q.row0) + t;
+          const int hq = d.h * a.G + rr - t * a.G;
+          emit<V>(a, row, hq, lane * V, x, lse, weigh(a, row, hq, lse));
         }
       }
     }
-    if (side == 1) {
-#pragma unroll
-      for (int j = 0; j < V; ++j) sums[slot][lane * V + j] = x[j];
-      if (lane == 0) sums[slot][DP] = sum;
-    }
-    __syncthreads();
-    if (on && side == 0 && lane * V < a.cache.D) {
-      sum += sums[slot][DP];
-      const float inv = sum == 0.0f ? 0.0f : rcp(sum);
-#pragma unroll
-      for (int j = 0; j < V; ++j) x[j] = (x[j] + sums[slot][lane * V + j]) * inv;
-      const float lse = sum == 0.0f ? -INFINITY : best + lg2(sum);
-      const int t = divide(rr, a.group);
-      const int64_t row = static_cast<int64_t>(q.row0) + t;
-      const int hq = d.h * a.G + rr - t * a.G;
-      emit<V>(a, row, hq, lane * V, x, lse, weigh(a, row, hq, lse));
-    }
-    __syncthreads();
   }
 }
 
@@ -843,14 +892,19 @@ Layout layout_of(int64_t T, int Hq, int D, bool prefix) {
 }
 
 // Rows (tokens times heads of a group) of a sequence up to which it takes mma.sync.
+// Measured, us, mma.sync / tcgen05, 8 K/V heads of 128: 16 sequences of 4000 tokens with
+// 32 rows 65 / 101, 64 rows 105 / 103, 128 rows 182 / 108; one of 8000 tokens with 64 rows
+// 34 / 41, 128 rows 42 / 42; 64 of 500 tokens with 32 rows 57 / 84, 64 rows 94 / 86, 128
+// rows 164 / 100.
 constexpr int64_t kFewRows = 64;
 
-fp8la_status launch_join(const AttnArgs &a, const JoinSide &few, const JoinSide &many, int DP,
+fp8la_status launch_join(const AttnArgs &a, JoinSide few, JoinSide many, int DP,
                          int64_t rows, cudaStream_t s) {
-  // Rows in turn where there are many: most blocks find nothing to join.
-  const int64_t most = many.ctas > 0 ? 32 : kRows;
-  const int64_t y = ((rows < most ? rows : most) + kJoinRows - 1) / kJoinRows;
-  const dim3 grid(few.ctas + many.ctas, static_cast<unsigned>(y));
+  few.blocks = static_cast<int32_t>(((rows < kRows ? rows : kRows) + kFewJoinRows - 1) / kFewJoinRows);
+  many.blocks = kTcItemRows / kJoinWarps;
+  const int blocks = few.ctas * few.blocks + many.ctas * many.blocks;
+  const int most = many_ctas() * kJoinCtasPerSm - 1;
+  const dim3 grid(blocks < most ? blocks : most);
   if (DP == 64) return launch(kv_join_kernel<64>, grid, kJoinThreads, 0, s, a, few, many);
   if (DP == 128) return launch(kv_join_kernel<128>, grid, kJoinThreads, 0, s, a, few, many);
   return launch(kv_join_kernel<256>, grid, kJoinThreads, 0, s, a, few, many);
@@ -875,7 +929,7 @@ fp8la_status launch_pass(AttnArgs a, const Layout &l, uint8_t *ws, bool f32, int
     a.part_o = reinterpret_cast<float *>(ws + p.o);
     a.part_lse = reinterpret_cast<float *>(ws + p.lse);
     a.desc = reinterpret_cast<Desc *>(ws + p.desc);
-    return JoinSide{a.part_o, a.part_lse, a.desc, BM, ctas};
+    return JoinSide{a.part_o, a.part_lse, a.desc, BM, ctas, 0};
   };
   if (tc) {
     many = use(l.many, kTcItemRows, many_ctas());

@@ -117,7 +117,8 @@ def reference(c, causal=True, scale=None, q=None):
         if total and rows:
             j = torch.arange(total, device="cuda") - c["prefix"]
             pos = torch.arange(n - rows, n, device="cuda")
-            seen = j[None, :] <= (pos[:, None] if causal else n)
+            # every row sees the whole prefix
+            seen = (j[None, :] < 0) | (j[None, :] <= (pos[:, None] if causal else n))
             for h in range(H * G):
                 qh, k, v = q[row:row + rows, h], K[h // G], V[h // G]
                 x = (qh @ k.t()).masked_fill(~seen, -math.inf)
