@@ -646,7 +646,7 @@ constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kFewJoinRows = 4;
 constexpr int kManyParts = 16;
 constexpr int kJoinCtasPerSm = 8;
-constexpr int kAtOnce = 8;      // parts whose loads are under way
+constexpr int kAtOnce = 4;      // parts whose loads are under way
 
 struct JoinSide {
   const float *part_o, *part_lse;
