@@ -481,9 +481,9 @@ FP8LA_API fp8la_status fp8la_lora_backward(
  * position kv_lens[s] - n + i.  Position j of sequence s lies in page
  * page_table[s * ld_table + j / page_size], at place j % page_size.  m_offsets:
  * int32 [num_segments + 1], starting at 0, non-decreasing, at most `rows`;
- * kv_lens: int32 [num_segments], at most max_pages * page_size; page_table: int32
- * [num_segments][ld_table], max_pages entries of a row at most, of which only those
- * below kv_lens[s] are read.  All on the device; the host reads none of it, so a
+ * kv_lens: int32 [num_segments], at most max_pages * page_size and 2^31 - 4096;
+ * page_table: int32 [num_segments][ld_table], max_pages entries of a row at most, of
+ * which only those below kv_lens[s] are read.  All on the device; the host reads none of it, so a
  * captured step can be replayed for other lengths.  Offsets and lengths that break
  * these rules make the call write nothing and record FP8LA_ERR_DEVICE_ARG; a page
  * outside 0 .. num_pages-1 records it, too, and nothing is read or written there.
@@ -552,8 +552,10 @@ FP8LA_API fp8la_status fp8_kv_read(
  * overlap q, the cache or the other.
  * max_rows: the rows of the longest segment, or more (`rows`, if nothing better is
  * known): it chooses the kernels, and a segment with more makes the call write
- * nothing and record FP8LA_ERR_DEVICE_ARG.  num_heads a multiple of kv_heads, rows *
- * num_heads < 2^31 - 2^20.
+ * nothing and record FP8LA_ERR_DEVICE_ARG, as does a call of 2^31 tiles or more: 128
+ * tokens of a K/V head for 256 rows of its heads (16 with head_dim > 128; a prompt of
+ * a million tokens with 8 K/V heads, 8 query heads each, has 2^30).  num_heads a multiple of kv_heads, at most 65536, rows * num_heads
+ * < 2^31 - 2^20.
  *
  * Sums are FP32.  Codes enter the tensor cores exactly, q with an error of at most
  * 2^-22 of an element (fp32) or none (bf16), but 2^-33 of the row's largest where

@@ -668,7 +668,7 @@ class KVCache:
         assert v.shape == k.shape and v.stride() == st and st[3] == 1
         assert k_scale.dtype is torch.float32 and v_scale.dtype is torch.float32
         assert k_scale.shape == (P, H, page) and v_scale.shape == (P, H, page)
-        assert v_scale.stride() == sst
+        assert v_scale.stride() == sst and k.device == v.device == k_scale.device == v_scale.device
         self.k, self.v, self.k_scale, self.v_scale, self.fmt = k, v, k_scale, v_scale, fmt
         self.shape = (P, H, page, D)
         self.device = k.get_device()
@@ -783,6 +783,7 @@ def kv_attention(q, cache, m_offsets, kv_lens, page_table, max_rows=None, scale=
     S, po, pl, pt, ldt, pages = _sequences(m_offsets, kv_lens, page_table)
     pp = pn = None
     shared = 0
+    assert prefix_len is not None or prefix_table is None
     if prefix_len is not None:
         _dense(prefix_len, (1,), torch.int32)
         shared = prefix_table.numel()

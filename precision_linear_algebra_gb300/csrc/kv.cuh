@@ -14,6 +14,8 @@ namespace kv {
 
 constexpr int kMaxSegments = 1024;
 constexpr int kMaxHeadDim = 256;
+// Tokens of a sequence: a tile and what is requested ahead of it stay below 2^31.
+constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 4096;
 
 // n / d for 0 <= n < 2^31, by a multiplication: mul = ceil(2^(31 + l) / d) with
 // 2^(l-1) < d <= 2^l exceeds 2^(31 + l) / d by less than 2^l / d, so n mul /

@@ -887,7 +887,7 @@ Layout layout_of(int64_t T, int Hq, int D, bool prefix) {
   l.many = part(DP <= 128 ? many_ctas() : 0, kTcItemRows);
   l.raw_o = take(prefix ? T * Hq * D * 4 : 0);
   l.raw_lse = take(prefix ? T * Hq * 4 : 0);
-  l.bytes = at;
+  l.bytes = at + 256 - 16;  // begins at a multiple of 256, wherever the caller's does
   return l;
 }
 
@@ -947,6 +947,7 @@ fp8la_status launch_pass(AttnArgs a, const Layout &l, uint8_t *ws, bool f32, int
 }
 
 constexpr int64_t kMaxRowHeads = (int64_t(1) << 31) - (int64_t(1) << 20);
+constexpr int32_t kMaxHeads = 65536;  // a tile's tokens times a group's heads fit in 32 bits
 
 }  // namespace
 
@@ -961,8 +962,8 @@ extern "C" {
 int64_t fp8_kv_attention_workspace_bytes(int64_t rows, int32_t num_heads, int32_t head_dim,
                                          int32_t prefix) {
   if (rows < 0 || num_heads < 1 || head_dim < 1) return FP8LA_ERR_INVALID_ARG;
-  if (head_dim % 16 != 0 || head_dim > kMaxHeadDim || rows * num_heads >= kMaxRowHeads ||
-      rows > INT32_MAX)
+  if (head_dim % 16 != 0 || head_dim > kMaxHeadDim || num_heads > kMaxHeads ||
+      rows > INT32_MAX || rows * num_heads >= kMaxRowHeads)
     return FP8LA_ERR_UNSUPPORTED;
   return layout_of(rows, num_heads, head_dim, prefix != 0).bytes;
 }
@@ -985,7 +986,8 @@ fp8la_status fp8_kv_attention(const void *q, int32_t q_dtype, int64_t ld_q, int6
   if (num_heads < 1 || num_heads % H != 0 || max_rows < 0 || prefix_pages < 0 ||
       !(scale > -INFINITY && scale < INFINITY))
     return FP8LA_ERR_INVALID_ARG;
-  if (rows > INT32_MAX || rows * num_heads >= kMaxRowHeads) return FP8LA_ERR_UNSUPPORTED;
+  if (num_heads > kMaxHeads || rows > INT32_MAX || rows * num_heads >= kMaxRowHeads)
+    return FP8LA_ERR_UNSUPPORTED;
   st = check_rows(a.cache, m_offsets, kv_lens, page_table, ld_table, max_pages, num_segments,
                   rows, &a.rows);
   if (st != FP8LA_OK || rows == 0 || num_segments == 0) return st;
@@ -1012,7 +1014,8 @@ fp8la_status fp8_kv_attention(const void *q, int32_t q_dtype, int64_t ld_q, int6
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool f32 = q_dtype == FP8LA_TYPE_F32;
   const Layout l = layout_of(rows, num_heads, D, prefix);
-  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  uint8_t *ws = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(workspace) + 255) &
+                                            ~uintptr_t(255));
   a.q = q;
   a.ldq = rows > 1 ? ld_q : 0;
   a.ldq_head = num_heads > 1 ? ld_q_head : 0;
@@ -1036,7 +1039,7 @@ fp8la_status fp8_kv_attention(const void *q, int32_t q_dtype, int64_t ld_q, int6
     p.rows.table = prefix_table;
     p.rows.ld_table = prefix_pages;
     const int64_t most = prefix_pages * a.cache.page_size;
-    p.rows.capacity = most < INT32_MAX ? most : INT32_MAX;
+    p.rows.capacity = most < kMaxTokens ? most : kMaxTokens;
     p.causal = 0;
     p.raw_o = reinterpret_cast<float *>(ws + l.raw_o);
     p.raw_lse = reinterpret_cast<float *>(ws + l.raw_lse);

@@ -114,7 +114,7 @@ __device__ __forceinline__ int page_of(const CopyArgs &a, int t, const int *offs
 }
 
 template <bool F32, int FMT, bool VEC, bool APPEND>
-__global__ void __launch_bounds__(kThreads, APPEND || F32 ? 4 : 8)
+__global__ void __launch_bounds__(kThreads, APPEND ? 4 : F32 ? 5 : 8)
     kv_copy_kernel(const CopyArgs a) {
   __shared__ int offsets[kMaxSegments + 1], lens[kMaxSegments + 1];
   pdl_wait();
@@ -315,8 +315,11 @@ fp8la_status check_cache(const fp8la_kv_cache *c, Cache *out) {
       (c->page_size > 1 && c->token_stride % 16 != 0))
     return FP8LA_ERR_ALIGNMENT;
   *out = {c->k, c->v, c->k_scale, c->v_scale,
-          c->page_stride, c->head_stride, c->token_stride,
-          c->scale_page_stride, c->scale_head_stride, c->scale_token_stride,
+          c->num_pages > 1 ? c->page_stride : 0, c->kv_heads > 1 ? c->head_stride : 0,
+          c->page_size > 1 ? c->token_stride : 0,
+          c->num_pages > 1 ? c->scale_page_stride : 0,
+          c->kv_heads > 1 ? c->scale_head_stride : 0,
+          c->page_size > 1 ? c->scale_token_stride : 0,
           static_cast<int32_t>(c->num_pages), c->page_size, c->kv_heads, c->head_dim,
           make_divisor(static_cast<uint32_t>(c->page_size))};
   return FP8LA_OK;
@@ -335,7 +338,7 @@ fp8la_status check_rows(const Cache &c, const int32_t *offsets, const int32_t *l
     return FP8LA_ERR_ALIGNMENT;
   const int64_t most = max_pages * c.page_size;
   *out = {offsets, lens, table, ld_table,
-          most < INT32_MAX ? most : INT32_MAX,
+          most < kMaxTokens ? most : kMaxTokens,
           static_cast<int32_t>(S), static_cast<int32_t>(T), nullptr};
   return FP8LA_OK;
 }

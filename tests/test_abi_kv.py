@@ -104,7 +104,7 @@ def attention(lib, **kw):
     (dict(ldq=-1), -1), (dict(ldqh=-64), -1), (dict(ldo=511), -1), (dict(ldoh=63), -1),
     (dict(ldl=7), -1), (dict(scale=math.nan), -1), (dict(scale=math.inf), -1),
     (dict(ppages=-1), -1), (dict(ppages=2, plen=A), -1), (dict(ppages=2, ptable=A), -1),
-    (dict(cache=None), -1), (dict(T=2 ** 28), -3), (dict(q=A + 1), -2),
+    (dict(cache=None), -1), (dict(T=2 ** 28), -3), (dict(T=1, Hq=65538), -3), (dict(q=A + 1), -2),
     (dict(q=A + 2, dtype=0), -2), (dict(out=A + 1), -2), (dict(lse=A + 2), -2),
     (dict(ws=A + 8), -2), (dict(ptable=A + 2, ppages=2, plen=A), -2),
     (dict(ptable=A, ppages=2, plen=A + 1), -2), (dict(T=0), 0),
@@ -118,6 +118,7 @@ def test_attention_workspace(lib):
     assert f(-1, 8, 64, 0) == -1 and f(4, 0, 64, 0) == -1 and f(4, 8, 0, 0) == -1
     assert f(4, 8, 72, 0) == -3 and f(4, 8, 272, 0) == -3 and f(2 ** 28, 8, 64, 0) == -3
     assert f(4, 8, 64, 0) > 0
+    assert f(1, 65536, 64, 0) > 0 and f(1, 65538, 64, 0) == -3 and f(2 ** 62, 4, 64, 0) == -3
     # the prefix's results of every row
     assert f(1000, 8, 64, 1) - f(1000, 8, 64, 0) >= 1000 * 8 * 65 * 4
 

@@ -249,3 +249,102 @@ def test_lse_is_optional():
                         torch.cuda.current_stream().cuda_stream)
     torch.cuda.synchronize()
     assert fl.device_status() == 0 and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("rows", [2, 70])
+def test_workspace_of_any_16_byte_alignment(rows):
+    """Sequences shared by several CTAs, whose partial results go through it."""
+    import torch
+    fl = lib()
+    c = make((3000, 2000), (rows, rows), 2, 4, 64, 16, prefix=100)
+    want, wl = check(fl, c)
+    need = fl.fp8_kv_attention_workspace_bytes(c["T"], 8, 64, 1)
+    ws = torch.full((need + 256,), 0x7F, dtype=torch.uint8, device="cuda")
+    for at in (16, 48, 240):
+        got, gl = attend(fl, c, workspace=ws[at:at + need])
+        torch.cuda.synchronize()
+        assert fl.device_status() == 0
+        assert torch.equal(got, want) and torch.equal(gl, wl)
+        assert torch.all(ws[:at] == 0x7F) and torch.all(ws[at + need:] == 0x7F)
+        ws.fill_(0x7F)
+
+
+@pytest.mark.parametrize("rows", [1, 70])
+def test_lengths_whose_tiles_would_pass_2_31(rows):
+    """2^31 - 4096 tokens is the most; the page table's row has room for more."""
+    import torch
+    fl = lib()
+    page, pages = 2 ** 16, 2 ** 15
+    cache = fl.kv_cache(1, 1, page, 16)
+    table = torch.zeros(1, pages, dtype=torch.int32, device="cuda")
+    offs = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    kvl = torch.tensor([2 ** 31 - 4095], dtype=torch.int32, device="cuda")
+    x = torch.ones(rows, 1, 16, dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(x, 5.0)
+    for call in (lambda: fl.kv_append(x, x, cache, offs, kvl, table),
+                 lambda: fl.kv_read(cache, offs, kvl, table, rows, k=out, v=out.clone()),
+                 lambda: fl.kv_attention(x, cache, offs, kvl, table, out=out),
+                 lambda: fl.kv_attention(x, cache, offs, torch.ones_like(kvl), table, out=out,
+                                         prefix_table=table[0], prefix_len=kvl)):
+        call()
+        torch.cuda.synchronize()
+        assert fl.device_status() == fl.FP8LA_ERR_DEVICE_ARG
+        assert torch.all(out == 5.0) and torch.all(cache.k == 0)
+    kvl -= 1
+    fl.kv_append(x, x, cache, offs, kvl, table)
+    fl.kv_read(cache, offs, kvl, table, rows, k=out, v=out.clone())
+    torch.cuda.synchronize()
+    assert fl.device_status() == 0
+    # 1 and 1 / 448 are off by 2^-24 each, BF16's rounding takes that away
+    assert torch.all(out == 1.0) and (cache.k != 0).any(-1).sum() == rows
+
+
+@pytest.mark.parametrize("rows", [1, 70])
+def test_strides_of_dimensions_of_one_element_address_nothing(rows):
+    import torch
+    fl = lib()
+    c = make((30,), (min(rows, 20),), 1, 8, 64, 32, spare=0)
+    want, wl = check(fl, c)
+    for stride in (1 << 62, -17):
+        s = c["cache"].struct
+        assert s.num_pages == 1 and s.kv_heads == 1
+        s.page_stride = s.head_stride = s.scale_page_stride = s.scale_head_stride = stride
+        got, gl = attend(fl, c)
+        torch.cuda.synchronize()
+        assert fl.device_status() == 0
+        assert torch.equal(got, want) and torch.equal(gl, wl)
+
+
+def test_host_tensors_are_refused():
+    import torch
+    fl = lib()
+    c = make((30, 20), (2, 1), 2, 4, 64, 16, prefix=20)
+    x = torch.zeros(3, 2, 64, dtype=torch.bfloat16, device="cuda")
+    cache, seqs = c["cache"], (c["offs"], c["kv_lens"], c["table"])
+    out, lse = attend(fl, c)
+    ws = torch.empty(1 << 26, dtype=torch.uint8, device="cuda")
+
+    def refused(f, args, at, kw={}):
+        args, kw = list(args), dict(kw)
+        if isinstance(at, int):
+            args[at] = args[at].cpu()
+        else:
+            kw[at] = kw[at].cpu()
+        with pytest.raises(AssertionError):
+            f(*args, **kw)
+
+    for at in (0, 1, 3, 4, 5):
+        refused(fl.kv_append, (x, x, cache, *seqs), at)
+    for at in (1, 2, 3, "k", "v"):
+        refused(fl.kv_read, (cache, *seqs, 3), at, dict(k=x.clone(), v=x.clone()))
+    kw = dict(prefix_table=c["prefix_table"], prefix_len=c["prefix_len"], out=out, lse=lse,
+              workspace=ws)
+    for at in (0, 2, 3, 4, *kw):
+        refused(fl.kv_attention, (c["q"], cache, *seqs), at, kw)
+    codes = [cache.k, cache.v, cache.k_scale, cache.v_scale]
+    for at in range(4):
+        refused(fl.KVCache, codes, at)
+    with pytest.raises(AssertionError):  # a prefix without its length
+        fl.kv_attention(c["q"], cache, *seqs, prefix_table=c["prefix_table"])
+    torch.cuda.synchronize()
+    assert fl.device_status() == 0
