@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
     fence_mbar_init();
     abort_flag = 0;
   }
-  pdl_wait();
+  if (!a.late) pdl_wait();
   pdl_launch_dependents();
   if (threadIdx.x == 0) a.desc[blockIdx.x].parts = 0;
   share_out<kThreads, kRows, kTile, kItemCost>(a, &sh, warp_sums);
@@ -305,20 +305,25 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
     float factor[2];
     {
       int e[2];
+      int64_t at[2];
+      float m[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        at[i] = (static_cast<int64_t>(q.row0) + tok[i]) * a.ldq + head[i] * a.ldq_head;
+#pragma unroll 2
+      for (int f = 0; f < DP / 64; ++f)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float x[16];
+          load_q<F32Q>(a, at[i] + el(f, c), el(f, c) < kc.D, x);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) m[i] = fmaxf(m[i], fabsf(x[j]));
+        }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int64_t row = (static_cast<int64_t>(q.row0) + tok[i]) * a.ldq + head[i] * a.ldq_head;
-        float m = 0.0f;
-#pragma unroll 1
-        for (int f = 0; f < DP / 64; ++f) {
-          float x[16];
-          load_q<F32Q>(a, row + el(f, c), el(f, c) < kc.D, x);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) m = fmaxf(m, fabsf(x[j]));
-        }
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        e[i] = min(max(8 - exponent_of(m), -126), 126);
+        m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], 1));
+        m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], 2));
+        e[i] = min(max(8 - exponent_of(m[i]), -126), 126);
         factor[i] = power_of_two(-e[i]) * a.scale_log2;
       }
 #pragma unroll
@@ -326,8 +331,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
         float x[2][16];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int64_t row = (static_cast<int64_t>(q.row0) + tok[i]) * a.ldq + head[i] * a.ldq_head;
-          load_q<F32Q>(a, row + el(f, c), el(f, c) < kc.D, x[i]);
+          load_q<F32Q>(a, at[i] + el(f, c), el(f, c) < kc.D, x[i]);
           const float up = power_of_two(e[i]);
 #pragma unroll
           for (int j = 0; j < 16; ++j) x[i][j] *= up;
@@ -587,6 +591,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
             sum > 0.0f || sum != sum ? M[k] - kShift + lg2(sum) : -INFINITY;
     }
     __syncthreads();
+    if (a.late) pdl_wait();  // the prefix's results
     const bool whole = count == it.tiles;
     const int part = 2 * blockIdx.x + (tile0 > 0 ? 0 : 1);
     constexpr int kPieces = DP / 8;
@@ -634,6 +639,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
     __syncthreads();  // the results overlay the rings
     if (abort_flag) break;
   }
+  if (a.late) pdl_wait();  // who waits for this kernel waits for the one before it
 }
 
 // ---------------------------------------------------------------------- join
@@ -912,8 +918,9 @@ fp8la_status launch_join(const AttnArgs &a, JoinSide few, JoinSide many, int DP,
 
 // One pass over all sequences whose rows are at most max_rows (times G): the many-row
 // kernel for those with more than kFewRows, the few-row kernel for the others, the join.
+// by_many: whether the pass before was the many-row kernel's; becomes whether this one was.
 fp8la_status launch_pass(AttnArgs a, const Layout &l, uint8_t *ws, bool f32, int format,
-                         int64_t max_rows, cudaStream_t s) {
+                         int64_t max_rows, bool *by_many, cudaStream_t s) {
   const int DP = padded_dim(a.cache.D);
   auto fits = [](int64_t stride) { return stride >= 0 && stride < (int64_t(1) << 31); };
   const Cache &c = a.cache;
@@ -941,8 +948,12 @@ fp8la_status launch_pass(AttnArgs a, const Layout &l, uint8_t *ws, bool f32, int
     few = use(l.few, kRows, few_ctas(f32, DP));
     a.row_lo = 0;
     a.row_hi = tc ? kFewRows : INT64_MAX;
+    // After the many-row kernel, whose workspace is another one; or after the join of a
+    // prefix by that kernel, which is the only reader of what this one writes.
+    a.late = tc || *by_many;
     st = launch_few(a, f32, format, few.ctas, s);
   }
+  *by_many = tc;
   return st == FP8LA_OK ? launch_join(a, few, many, DP, max_rows, s) : st;
 }
 
@@ -1031,6 +1042,7 @@ fp8la_status fp8_kv_attention(const void *q, int32_t q_dtype, int64_t ld_q, int6
   a.causal = causal != 0;
   a.scale_log2 = scale * kLog2e;
   a.max_rows = max_rows;
+  bool by_many = false;
   if (prefix) {
     AttnArgs p = a;
     p.whole = m_offsets + num_segments;
@@ -1043,7 +1055,7 @@ fp8la_status fp8_kv_attention(const void *q, int32_t q_dtype, int64_t ld_q, int6
     p.causal = 0;
     p.raw_o = reinterpret_cast<float *>(ws + l.raw_o);
     p.raw_lse = reinterpret_cast<float *>(ws + l.raw_lse);
-    st = launch_pass(p, l, ws, f32, cache->format, rows * a.G, s);
+    st = launch_pass(p, l, ws, f32, cache->format, rows * a.G, &by_many, s);
     if (st != FP8LA_OK) return st;
     a.pre_o = p.raw_o;
     a.pre_lse = p.raw_lse;
@@ -1051,7 +1063,7 @@ fp8la_status fp8_kv_attention(const void *q, int32_t q_dtype, int64_t ld_q, int6
     a.prefix_capacity = p.rows.capacity;
   }
   const int64_t longest = (max_rows < rows ? max_rows : rows) * a.G;
-  return launch_pass(a, l, ws, f32, cache->format, longest, s);
+  return launch_pass(a, l, ws, f32, cache->format, longest, &by_many, s);
 }
 
 }  // extern "C"

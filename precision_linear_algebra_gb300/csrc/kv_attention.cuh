@@ -28,6 +28,9 @@ struct AttnArgs {
   int64_t ld_lse;
   int32_t Hq, G, causal;
   int32_t tma;               // whether 16 tokens lie together, as TMA takes them
+  // The few-row kernel waits for the kernel before it only where it needs that one's
+  // results, and at its end: what it reads was complete when that one began.
+  int32_t late;
   Divisor group;             // by G
   float scale_log2;          // of scores, times log2 e
   int64_t row_lo, row_hi;    // rows (tokens times G) of the sequences that are this kernel's

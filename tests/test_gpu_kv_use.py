@@ -348,3 +348,28 @@ def test_host_tensors_are_refused():
         fl.kv_attention(c["q"], cache, *seqs, prefix_table=c["prefix_table"])
     torch.cuda.synchronize()
     assert fl.device_status() == 0
+
+
+def test_calls_in_a_row_share_a_workspace():
+    """Short and long segments in one call, behind a prefix and without one, decoding
+    steps and a prompt, queued one behind the other: each as when it is alone."""
+    import torch
+    fl = lib()
+    problems = [make((900, 300, 40, 1200), (200, 1, 3, 130), 2, 4, 64, 16),
+                make((90, 0, 40, 35, 7), (1, 0, 3, 33, 1), 2, 4, 64, 16, prefix=700),
+                make((900, 300, 40, 1200), (150, 1, 3, 1), 2, 4, 64, 16, prefix=300),
+                make((5000, 3000), (1, 2), 2, 4, 64, 16),
+                make((400,), (400,), 2, 4, 64, 16)]
+    want = []
+    for c in problems:
+        out, lse = attend(fl, c)
+        torch.cuda.synchronize()
+        want.append((out, lse))
+    ws = torch.empty(max(fl.fp8_kv_attention_workspace_bytes(c["T"], 8, 64, 1) for c in problems),
+                     dtype=torch.uint8, device="cuda")
+    order = torch.randperm(60, generator=torch.Generator().manual_seed(3)) % len(problems)
+    got = [(i, attend(fl, problems[i], workspace=ws)) for i in order.tolist()]
+    torch.cuda.synchronize()
+    assert fl.device_status() == 0
+    for i, (out, lse) in got:
+        assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
