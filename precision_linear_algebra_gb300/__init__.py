@@ -663,15 +663,16 @@ class KVCache:
         import torch
         P, H, page, D = k.shape
         st, sst = k.stride(), k_scale.stride()
-        assert k.is_cuda and v.is_cuda and k_scale.is_cuda and v_scale.is_cuda
+        dev = k.get_device()  # -1: the host
+        assert dev >= 0 and dev == v.get_device() == k_scale.get_device() == v_scale.get_device()
         assert k.dtype is torch.uint8 and v.dtype is torch.uint8
         assert v.shape == k.shape and v.stride() == st and st[3] == 1
         assert k_scale.dtype is torch.float32 and v_scale.dtype is torch.float32
         assert k_scale.shape == (P, H, page) and v_scale.shape == (P, H, page)
-        assert v_scale.stride() == sst and k.device == v.device == k_scale.device == v_scale.device
+        assert v_scale.stride() == sst
         self.k, self.v, self.k_scale, self.v_scale, self.fmt = k, v, k_scale, v_scale, fmt
         self.shape = (P, H, page, D)
-        self.device = k.get_device()
+        self.device = dev
         self.struct = fp8la_kv_cache(
             k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), P, page, H, D,
             _FORMATS[fmt], st[0], st[1], st[2], sst[0], sst[1], sst[2])

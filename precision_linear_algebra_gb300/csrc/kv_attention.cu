@@ -14,11 +14,16 @@
 // 2^-22.  w_j is rounded to a half, 2^-11, at most 2^7 (2^15 between two rescalings),
 // so that only what is 2^-21 of the largest or less loses more.  Sums are FP32.
 //
-// Bound: HBM, K's and V's codes once for all heads of a group.  A warp streams 16
-// tokens at a time through a ring of its own, filled by cp.async four deep: no
-// barrier in the loop.  mma.sync m16n8k16 takes 16 rows, which is what a group of
-// heads of one token needs; the fragments come from codes by one conversion for
-// two of them.  tcgen05 wants 64 rows at least, which kv_attention_tc.cu has.
+// Bound: HBM, K's and V's codes once for all heads of a group.  A warp streams 32
+// tokens at a time through a ring of its own, two steps deep, filled by TMA (16 tokens
+// of a page a copy) or, where pages are not made of whole groups of 16, by cp.async in
+// chunks of 16 bytes: no barrier in the loop.  mma.sync m16n8k16 takes 16 rows, which is
+// what a group of heads of one token needs; the fragments come from codes by one
+// conversion for two of them.  tcgen05 wants 64 rows at least, which kv_attention_tc.cu
+// has.  Measured, 8 K/V heads of 128 with 8 query heads each, the join included: 64
+// sequences of 8192 tokens 179 us (6.2 TB/s), of lengths up to 8192 108 us (5.5; 128 with
+// steps of 32 tokens, 149 with 16, both before kItemCost); one of 131072 59 us (4.7); one
+// of 2048 16 us, two launches whose addresses and instructions come one after the other.
 #include "kv_attention.cuh"
 
 namespace fp8la {
@@ -644,14 +649,22 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
 
 // ---------------------------------------------------------------------- join
 // Joins the partial results of items that several CTAs shared: CTA b began it
-// (its second partial result), the next parts - 1 went on (their first ones).  A row
-// has one warp or, where there are many parts, several, whose sums are added in order;
-// both kernels' items are joined in one launch.
+// (its second partial result), the next parts - 1 went on (their first ones).  Where
+// parts are few, which is what a boundary between two CTAs makes, a warp takes a few
+// rows at once; else a row has one warp or several, whose sums are added in order.
+// Both kernels' items are joined in one launch.
+//
+// Bound: latency, as most of it is a chain of loads (what there is to join, whose rows,
+// their logarithms, the parts).  A row at a time of each warp took 22 us behind two
+// prompts of 2048 tokens (150 items of two parts, 256 rows each), 18 behind 6 ragged
+// ones and 13 behind one sequence of 131072 tokens (8 items of 57 parts); this 12, 8 and
+// 7.  With 2, 3, 4 or 8 CTAs an SM (calls, us): 64 requests 123, 108, 121, 106; two
+// prompts 272, 257, 257, 255; one request of 2048 tokens 16.4, 15.8, 15.8, 17.1.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
-constexpr int kFewJoinRows = 4;
+constexpr int kFewParts = 4;
 constexpr int kManyParts = 16;
-constexpr int kJoinCtasPerSm = 8;
+constexpr int kJoinCtasPerSm = 3;
 constexpr int kAtOnce = 4;      // parts whose loads are under way
 
 struct JoinSide {
@@ -660,11 +673,27 @@ struct JoinSide {
   int32_t BM, ctas, blocks;  // blocks for each CTA
 };
 
+// V floats, 4 V-byte aligned.
+template <int V>
+__device__ __forceinline__ void load_part(const float *p, float (&y)[V]) {
+  if (V >= 4) {
+#pragma unroll
+    for (int j = 0; j < V; j += 4) {
+      const float4 f = *reinterpret_cast<const float4 *>(p + j);
+      y[j] = f.x; y[j + 1] = f.y; y[V >= 4 ? j + 2 : 0] = f.z; y[V >= 4 ? j + 3 : 0] = f.w;
+    }
+  } else {
+    const float2 f = *reinterpret_cast<const float2 *>(p);
+    y[0] = f.x; y[1] = f.y;
+  }
+}
+
 template <int DP>
-__global__ void __launch_bounds__(kJoinThreads)
+__global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm)
     kv_join_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ JoinSide few,
                    const __grid_constant__ JoinSide many) {
   constexpr int V = DP / 32;
+  constexpr int R = DP > 128 ? 2 : 4;   // rows of a warp at once, where parts are few
   __shared__ float sums[kJoinWarps][DP + 1];
   pdl_wait();
   pdl_launch_dependents();
@@ -686,8 +715,10 @@ __global__ void __launch_bounds__(kJoinThreads)
     if (mine < blocks) {
       bool first;
       int cta;
-      turn_of(static_cast<int>(mine), &first, &cta);
+      const int turn = turn_of(static_cast<int>(mine), &first, &cta);
       look = (first ? few.desc : many.desc)[cta];
+      const int group = look.parts <= kFewParts ? kJoinWarps * R : first ? 1 : kJoinWarps;
+      if (turn * group >= (first ? few.BM : many.BM)) look.parts = 0;
     }
     for (uint32_t some = __ballot_sync(0xffffffffu, look.parts > 0); some; some &= some - 1) {
       const int i = __ffs(some) - 1;
@@ -701,7 +732,63 @@ __global__ void __launch_bounds__(kJoinThreads)
       const int BM = first ? few.BM : many.BM;
       const Seq q = load_seq(a, d.s);
       const int rows = min(BM, q.n * a.G - d.rt * BM);
-      const int group = first ? kFewJoinRows : kJoinWarps;      // rows of this turn
+      if (d.parts <= kFewParts) {
+        const int r0 = (turn * kJoinWarps + warp) * R;
+        if (r0 >= rows) continue;
+        auto part = [&](int i) {
+          return static_cast<int64_t>(2 * (cta + i) + (i == 0 ? 1 : 0)) * BM + r0;
+        };
+        // Lane 4 u + i: part i of row u.
+        const int own = lane & 3, row = (lane >> 2) % R;
+        const float lse =
+            own < d.parts && r0 + row < rows ? part_lse[part(own) + row] : -INFINITY;
+        float x[R][V] = {}, weight = 0.0f, joined = -INFINITY;
+#pragma unroll 1
+        for (int i0 = 0; i0 < d.parts; i0 += 2) {
+          float y[R][2][V];
+#pragma unroll
+          for (int u = 0; u < R; ++u)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const bool on = r0 + u < rows && i0 + k < d.parts;
+              const float *p = part_o + (part(i0 + k) + u) * DP + lane * V;
+#pragma unroll
+              for (int j = 0; j < V; ++j) y[u][k][j] = 0.0f;
+              if (on) load_part<V>(p, y[u][k]);
+            }
+          if (i0 == 0) {  // weights, while the first parts come
+            float best = lse;
+            best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 1));
+            best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 2));
+            const float w = lse == -INFINITY ? 0.0f : ex2(lse - best);
+            float sum = w;
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            weight = sum == 0.0f ? 0.0f : w * rcp(sum);
+            joined = sum == 0.0f ? -INFINITY : best + lg2(sum);
+          }
+#pragma unroll
+          for (int u = 0; u < R; ++u)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float w = __shfl_sync(0xffffffffu, weight, 4 * u + i0 + k);
+              if (w == 0.0f) continue;
+#pragma unroll
+              for (int j = 0; j < V; ++j) x[u][j] = fmaf(w, y[u][k][j], x[u][j]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+          const float l = __shfl_sync(0xffffffffu, joined, 4 * u);
+          if (r0 + u >= rows || lane * V >= a.cache.D) continue;
+          const int rr = d.rt * BM + r0 + u, t = divide(rr, a.group);
+          const int64_t row = static_cast<int64_t>(q.row0) + t;
+          const int hq = d.h * a.G + rr - t * a.G;
+          emit<V>(a, row, hq, lane * V, x[u], l, weigh(a, row, hq, l));
+        }
+        continue;
+      }
+      const int group = first ? 1 : kJoinWarps;                 // rows of this turn
       const int each = d.parts > kManyParts ? min(group, 2) : group;  // rows at a time
       const int warps = kJoinWarps / each;                      // of a row
       const int r_end = min(rows, (turn + 1) * group);
@@ -726,16 +813,8 @@ __global__ void __launch_bounds__(kJoinThreads)
             for (int i = 0; i < n; i += kAtOnce) {
               float y[kAtOnce][V];
 #pragma unroll
-              for (int u = 0; u < kAtOnce; ++u) {
-                const float *p = part_o + part(i0 + min(i + u, n - 1)) * DP + lane * V;
-                if (V >= 4) {
-#pragma unroll
-                  for (int j = 0; j < V; j += 4)
-                    *reinterpret_cast<float4 *>(&y[u][j]) = *reinterpret_cast<const float4 *>(p + j);
-                } else {
-                  *reinterpret_cast<float2 *>(&y[u][0]) = *reinterpret_cast<const float2 *>(p);
-                }
-              }
+              for (int u = 0; u < kAtOnce; ++u)
+                load_part<V>(part_o + part(i0 + min(i + u, n - 1)) * DP + lane * V, y[u]);
 #pragma unroll
               for (int u = 0; u < kAtOnce; ++u) {
                 if (i + u >= n) break;
@@ -821,8 +900,8 @@ fp8la_status launch_few_one(AttnArgs a, int slot, int ctas, cudaStream_t s) {
                                     C::kSmem);
       }) != cudaSuccess)
     return FP8LA_ERR_CUDA;
-  // TMA's limits: strides below 2^40 bytes.  Measured, us, with TMA / in chunks of 16
-  // bytes: see above.
+  // TMA's limits: strides below 2^40 bytes.  Measured, 64 sequences of 8192 tokens: 179
+  // us with TMA, 193 with pages of 24, which are copied in chunks of 16 bytes.
   CUtensorMap k = {}, v = {};
   const int64_t most = int64_t(1) << 40;
   a.tma = a.cache.page_size % kGroup == 0 && a.cache.page_stride < most &&
@@ -906,7 +985,7 @@ constexpr int64_t kFewRows = 64;
 
 fp8la_status launch_join(const AttnArgs &a, JoinSide few, JoinSide many, int DP,
                          int64_t rows, cudaStream_t s) {
-  few.blocks = static_cast<int32_t>(((rows < kRows ? rows : kRows) + kFewJoinRows - 1) / kFewJoinRows);
+  few.blocks = static_cast<int32_t>(rows < kRows ? rows : kRows);
   many.blocks = kTcItemRows / kJoinWarps;
   const int blocks = few.ctas * few.blocks + many.ctas * many.blocks;
   const int most = many_ctas() * kJoinCtasPerSm - 1;
