@@ -488,7 +488,7 @@ FP8LA_API fp8la_status fp8la_lora_backward(
  * these rules make the call write nothing and record FP8LA_ERR_DEVICE_ARG; a page
  * outside 0 .. num_pages-1 records it, too, and nothing is read or written there.
  * Rows after the last segment are neither read nor written.  Segments may be
- * empty.  num_segments <= 1024, rows < 2^31.
+ * empty.  num_segments <= 1024, rows * kv_heads < 2^31 - 2^20.
  */
 typedef struct fp8la_kv_cache {
   uint8_t *k, *v;

@@ -766,7 +766,8 @@ def kv_attention(q, cache, m_offsets, kv_lens, page_table, max_rows=None, scale=
     prefix_table (int32 [pages]) and prefix_len (int32 [1]): tokens that every
     sequence begins with, before those of its own page_table and kv_lens.  Returns
     (out bf16 [T][query heads][D], lse fp32 [T][query heads]); rows that see
-    nothing get 0 and -inf.  Nothing is synchronised.
+    nothing get 0 and -inf, rows from m_offsets[S] on are left as they were.
+    Nothing is synchronised.
     """
     import torch
     T, Hq, D = q.shape

@@ -373,3 +373,64 @@ def test_calls_in_a_row_share_a_workspace():
     assert fl.device_status() == 0
     for i, (out, lse) in got:
         assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+def test_captured_calls_in_a_row():
+    """The same in one graph, whose launches overlap as far as they do on a stream."""
+    import torch
+    fl = lib()
+    problems = [make((900, 300, 40, 1200), (200, 1, 3, 130), 2, 4, 64, 16),
+                make((90, 0, 40, 35, 7), (1, 0, 3, 33, 1), 2, 4, 64, 16, prefix=700),
+                make((2000, 300), (1, 1), 2, 4, 64, 24, prefix=40),
+                make((5000, 3000), (1, 2), 2, 4, 64, 16, q="float32")]
+    want = [attend(fl, c) for c in problems]
+    need = max(fl.fp8_kv_attention_workspace_bytes(c["T"], 8, 64, 1) for c in problems)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [attend(fl, c, workspace=ws) for c in problems * 3]
+    for _ in range(8):
+        for out, lse in got:
+            out.fill_(5.0)
+            lse.fill_(5.0)
+        ws.fill_(0x7F)
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert fl.device_status() == 0
+        for (out, lse), (a, b) in zip(got, want * 3):
+            assert torch.equal(out, a) and torch.equal(lse, b)
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_sequences_without_pages_of_their_own(rows):
+    """A page table without columns: only the prefix is there."""
+    import torch
+    fl = lib()
+    c = make((0, 0, 0), (rows, 1, 0), 2, 4, 64, 16, prefix=333)
+    c["table"] = c["table"][:, :0].contiguous()
+    want, wl, *_ = check(fl, c)
+    assert torch.isfinite(wl).all()
+    # without the prefix there is nothing at all
+    out, lse = fl.kv_attention(c["q"], c["cache"], c["offs"], c["kv_lens"], c["table"])
+    torch.cuda.synchronize()
+    assert fl.device_status() == 0
+    assert torch.all(out == 0) and torch.all(lse == -math.inf)
+
+
+def test_broadcast_rows():
+    """One row for all heads (stride 0): each head has the same codes and result."""
+    import torch
+    fl = lib()
+    H, D, T = 4, 64, 37
+    cache, table = empty(fl, 1, T, H, D, 16)
+    offs = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    x = torch.randn(T, 1, D, device="cuda").to(torch.bfloat16)
+    k = x.expand(T, H, D)
+    fl.kv_append(k, k, cache, offs, offs[1:], table)
+    out, lse = fl.kv_attention(x.expand(T, 2 * H, D), cache, offs, offs[1:], table)
+    torch.cuda.synchronize()
+    assert fl.device_status() == 0
+    assert torch.equal(out, out[:, :1].expand_as(out)) and torch.isfinite(lse).all()
+    assert torch.equal(lse, lse[:, :1].expand_as(lse))
