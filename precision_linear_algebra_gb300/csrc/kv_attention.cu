@@ -21,9 +21,9 @@
 // what a group of heads of one token needs; the fragments come from codes by one
 // conversion for two of them.  tcgen05 wants 64 rows at least, which kv_attention_tc.cu
 // has.  Measured, 8 K/V heads of 128 with 8 query heads each, the join included: 64
-// sequences of 8192 tokens 179 us (6.2 TB/s), of lengths up to 8192 108 us (5.5; 128 with
+// sequences of 8192 tokens 179 us (6.2 TB/s), of lengths up to 8192 106 us (5.6; 128 with
 // steps of 32 tokens, 149 with 16, both before kItemCost); one of 131072 59 us (4.7); one
-// of 2048 16 us, two launches whose addresses and instructions come one after the other.
+// of 2048 17 us, two launches whose addresses and instructions come one after the other.
 #include "kv_attention.cuh"
 
 namespace fp8la {
@@ -658,13 +658,15 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
 // their logarithms, the parts).  A row at a time of each warp took 22 us behind two
 // prompts of 2048 tokens (150 items of two parts, 256 rows each), 18 behind 6 ragged
 // ones and 13 behind one sequence of 131072 tokens (8 items of 57 parts); this 12, 8 and
-// 7.  With 2, 3, 4 or 8 CTAs an SM (calls, us): 64 requests 123, 108, 121, 106; two
-// prompts 272, 257, 257, 255; one request of 2048 tokens 16.4, 15.8, 15.8, 17.1.
+// 7.  The grid: with 3, 4, 6 or 8 CTAs an SM 64 requests take 108, 120, 117, 106 us a
+// call in a graph and 120, 146, 143, 108 called one by one (why so much more was not
+// found; without the join it is 102), one request of 2048 tokens 15.8, 15.8, 15.8, 17.1.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kFewParts = 4;
 constexpr int kManyParts = 16;
-constexpr int kJoinCtasPerSm = 3;
+constexpr int kJoinResident = 3;  // CTAs of an SM at once
+constexpr int kJoinCtasPerSm = 8;
 constexpr int kAtOnce = 4;      // parts whose loads are under way
 
 struct JoinSide {
@@ -689,7 +691,7 @@ __device__ __forceinline__ void load_part(const float *p, float (&y)[V]) {
 }
 
 template <int DP>
-__global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm)
+__global__ void __launch_bounds__(kJoinThreads, kJoinResident)
     kv_join_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ JoinSide few,
                    const __grid_constant__ JoinSide many) {
   constexpr int V = DP / 32;
