@@ -691,7 +691,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       if (more) {
-        if (!active) fetch_q<F32Q, DP>(a, upcoming, q_at, row0);
+        if (!active) {
+          // These warps wait for no scores: without this one that is tiles ahead of the
+          // other row tile's would arrive for item n + 1 in item n's place.
+          if (!(ok = wait(qfull_bar, n & 1u))) break;
+          fetch_q<F32Q, DP>(a, upcoming, q_at, row0);
+        }
         scale_q<F32Q, DP>(a, q_at, my_factors);
         q_done();
       }
