@@ -990,6 +990,7 @@ fp8la_status launch_join(const AttnArgs &a, JoinSide few, JoinSide many, int DP,
   few.blocks = static_cast<int32_t>(rows < kRows ? rows : kRows);
   many.blocks = kTcItemRows / kJoinWarps;
   const int blocks = few.ctas * few.blocks + many.ctas * many.blocks;
+  if (blocks == 0) return FP8LA_OK;  // no segment has rows, or the call writes nothing
   const int most = many_ctas() * kJoinCtasPerSm - 1;
   const dim3 grid(blocks < most ? blocks : most);
   if (DP == 64) return launch(kv_join_kernel<64>, grid, kJoinThreads, 0, s, a, few, many);
