@@ -341,8 +341,9 @@ struct Weights {
 __device__ __forceinline__ Weights weigh(const AttnArgs &a, int64_t t, int hq, float lse) {
   if (!a.pre_lse) return {1.0f, 0.0f, lse};
   const float p = a.pre_lse[t * a.Hq + hq];
+  // A maximum drops a NaN, which the weights and the logarithm are to keep.
+  if (lse == -INFINITY && p == -INFINITY) return {0.0f, 0.0f, -INFINITY};
   const float top = fmaxf(lse, p);
-  if (top == -INFINITY) return {0.0f, 0.0f, top};
   const float x = ex2(lse - top), y = ex2(p - top), inv = rcp(x + y);
   return {x * inv, y * inv, top + lg2(x + y)};
 }

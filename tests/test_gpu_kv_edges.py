@@ -30,3 +30,29 @@ def test_segments_without_rows(D, prefix):
     torch.cuda.synchronize()
     assert fl.device_status() == fl.FP8LA_ERR_DEVICE_ARG
     assert torch.all(out == 9.0) and torch.all(lse == 9.0)
+
+
+@pytest.mark.parametrize("what", ["k", "k_scale", "v_scale"])
+@pytest.mark.parametrize("rows,tokens", [(1, 100), (2, 20000), (70, 100), (70, 20000)])
+def test_nan_beside_a_side_without_tokens(rows, tokens, what):
+    """A row that a token made NaN stays so, its logarithm too, where the prefix or what
+    follows it has no tokens; with many tokens its result is a joined one."""
+    import torch
+    fl = lib()
+    c = make((tokens,), (rows,), 2, 2, 64, 16)
+    want, wl = check(fl, c)
+    bad = 0x7F if what == "k" else math.nan
+    getattr(c["cache"], what)[int(c["table"][0, 1]), 1, 3] = bad
+    out, lse = attend(fl, c, prefix_table=c["table"][0, :3].contiguous(),
+                      prefix_len=torch.zeros(1, dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    assert torch.equal(out[:, :2], want[:, :2]) and torch.isnan(out[:, 2:]).all()
+    assert (lse[:, :2] - wl[:, :2]).abs().max() < 1e-5 and torch.isnan(lse[:, 2:]).all()
+    c = make((0, 0), (rows, rows), 2, 2, 64, 16, prefix=tokens)
+    want, wl = check(fl, c)
+    getattr(c["cache"], what)[int(c["prefix_table"][1]), 1, 3] = bad
+    out, lse = attend(fl, c)
+    torch.cuda.synchronize()
+    assert fl.device_status() == 0
+    assert torch.equal(out[:, :2], want[:, :2]) and torch.isnan(out[:, 2:]).all()
+    assert torch.equal(lse[:, :2], wl[:, :2]) and torch.isnan(lse[:, 2:]).all()
