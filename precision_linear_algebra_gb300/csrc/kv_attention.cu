@@ -619,8 +619,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
       const float joined = sum == 0.0f ? -INFINITY : best + lg2(sum);
       float x[8] = {};
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        if (weight[w] == 0.0f) continue;
+      for (int w = 0; w < kWarps; ++w) {  // 0 x NaN too: a V that is not finite
         const float *p = red + (w * kRows + r) * C::kLdO + d;
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = fmaf(weight[w] * inv, p[j], x[j]);
@@ -774,7 +773,6 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinResident)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               const float w = __shfl_sync(0xffffffffu, weight, 4 * u + i0 + k);
-              if (w == 0.0f) continue;
 #pragma unroll
               for (int j = 0; j < V; ++j) x[u][j] = fmaf(w, y[u][k][j], x[u][j]);
             }

@@ -56,3 +56,23 @@ def test_nan_beside_a_side_without_tokens(rows, tokens, what):
     assert fl.device_status() == 0
     assert torch.equal(out[:, :2], want[:, :2]) and torch.isnan(out[:, 2:]).all()
     assert torch.equal(lse[:, :2], wl[:, :2]) and torch.isnan(lse[:, 2:]).all()
+
+
+@pytest.mark.parametrize("rows,tokens,first", [(1, 40, 32), (1, 384, 256), (2, 20000, 15000),
+                                               (100, 640, 384)])
+def test_not_finite_value_of_a_negligible_token(rows, tokens, first):
+    """Every token from `first` on has a weight that underflows, those of a whole warp or
+    CTA among them; a V that is not finite still reaches its element of the rows."""
+    import torch
+    fl = lib()
+    c = make((tokens,), (rows,), 1, 1, 64, 16)
+    cache, j = c["cache"], torch.arange(first, tokens, device="cuda")
+    page, place = c["table"][0][j // 16].long(), j % 16
+    sign = torch.where(torch.randn(64, device="cuda") > 0, 1.0, -1.0)
+    c["q"] = (sign * (1 + torch.rand(c["q"].shape, device="cuda"))).to(torch.bfloat16)
+    cache.k[page, 0, place] = (-448 * sign).to(fp8("e4m3")).view(torch.uint8)
+    cache.k_scale[page, 0, place] = 1.0
+    cache.v[page[1], 0, place[1], 5] = 0x7F
+    out, lse = check(fl, c)
+    assert torch.isnan(out[:, 0, 5]).all() and int(torch.isnan(out).sum()) == rows
+    assert torch.isfinite(lse).all()
