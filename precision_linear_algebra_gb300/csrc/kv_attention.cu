@@ -32,14 +32,15 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = 4;
-constexpr int kRows = 16;       // rows of a tile
+constexpr int kRows = kFewItemRows;  // rows of a tile
 constexpr int kGroup = 16;      // tokens that TMA brings at once
 constexpr int kSubs = 2;        // groups of a warp's step
 constexpr int kStep = kSubs * kGroup;
 constexpr int kTile = kWarps * kStep;
+static_assert(kTile == kTileTokens, "what the prefix's units are counted in");
 // What an item costs beside its tiles, in tiles.  64 requests of up to 8192 tokens, us,
 // with 0 to 5: 141, 130, 121, 110, 109, 110.
-constexpr int kItemCost = 4;
+constexpr int kItemCost = kFewItemCost;
 constexpr int kStages = 2;
 constexpr float kShift = 7.0f;  // w of the running maximum is 2^7
 constexpr float kLazy = 8.0f;   // it is raised where 2^8 is passed
@@ -188,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
   using Fm = Format<FMT>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Share sh;
-  __shared__ int64_t warp_sums[kWarps];
+  __shared__ int64_t warp_sums[2 * kWarps];
   __shared__ Walk walk;
   __shared__ Item it;
   __shared__ int more;
@@ -969,7 +970,7 @@ Layout layout_of(int64_t T, int Hq, int D, bool prefix) {
     return p;
   };
   l.few = part(few_ctas(false, DP), kRows);
-  l.many = part(DP <= 128 ? many_ctas() : 0, kTcItemRows);
+  l.many = part(DP <= 128 ? many_ctas() : 0, kManyItemRows);
   l.raw_o = take(prefix ? T * Hq * D * 4 : 0);
   l.raw_lse = take(prefix ? T * Hq * 4 : 0);
   l.bytes = at + 256 - 16;  // begins at a multiple of 256, wherever the caller's does
@@ -986,7 +987,7 @@ constexpr int64_t kFewRows = 64;
 fp8la_status launch_join(const AttnArgs &a, JoinSide few, JoinSide many, int DP,
                          int64_t rows, cudaStream_t s) {
   few.blocks = static_cast<int32_t>(rows < kRows ? rows : kRows);
-  many.blocks = kTcItemRows / kJoinWarps;
+  many.blocks = kManyItemRows / kJoinWarps;
   const int blocks = few.ctas * few.blocks + many.ctas * many.blocks;
   if (blocks == 0) return FP8LA_OK;  // no segment has rows, or the call writes nothing
   const int most = many_ctas() * kJoinCtasPerSm - 1;
@@ -1010,6 +1011,7 @@ fp8la_status launch_pass(AttnArgs a, const Layout &l, uint8_t *ws, bool f32, int
                   fits(c.scale_token_stride);
   // All rows of a prefix are one sequence, which is all of one kernel's.
   const bool both = !(a.whole && tc);
+  a.both = tc && both;
   JoinSide few = {}, many = {};
   fp8la_status st = FP8LA_OK;
   auto use = [&](const Part &p, int BM, int ctas) {
@@ -1019,7 +1021,7 @@ fp8la_status launch_pass(AttnArgs a, const Layout &l, uint8_t *ws, bool f32, int
     return JoinSide{a.part_o, a.part_lse, a.desc, BM, ctas, 0};
   };
   if (tc) {
-    many = use(l.many, kTcItemRows, many_ctas());
+    many = use(l.many, kManyItemRows, many_ctas());
     a.row_lo = both ? kFewRows + 1 : 0;
     a.row_hi = INT64_MAX;
     st = launch_many(a, f32, format, many.ctas, s);
@@ -1140,6 +1142,7 @@ fp8la_status fp8_kv_attention(const void *q, int32_t q_dtype, int64_t ld_q, int6
     a.pre_o = p.raw_o;
     a.pre_lse = p.raw_lse;
     a.prefix_len = prefix_len;
+    a.prefix_many = by_many;
     a.prefix_capacity = p.rows.capacity;
   }
   const int64_t longest = (max_rows < rows ? max_rows : rows) * a.G;

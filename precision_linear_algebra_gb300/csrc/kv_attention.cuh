@@ -10,6 +10,13 @@ namespace kv {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// The two kernels' tiles, and what an item costs beside them, in tiles (measured beside
+// the kernels).  Each counts the other's work, too: a call that has too much of either
+// writes nothing.
+constexpr int kTileTokens = 128;
+constexpr int kFewItemRows = 16, kFewItemCost = 4;
+constexpr int kManyItemRows = 256, kManyItemCost = 3;
+
 // A partial result that a later kernel joins with the others of its item.
 struct Desc {
   int32_t s, h, rt;   // sequence, K/V head, row tile
@@ -42,6 +49,8 @@ struct AttnArgs {
   const float *pre_o, *pre_lse;
   const int32_t *prefix_len; // checked by the sequences' pass, too
   int64_t prefix_capacity;
+  int32_t prefix_many;       // the prefix's pass was the many-row kernel's
+  int32_t both;              // sequences outside row_lo .. row_hi are the other kernel's
   // Partial results: two of each CTA, rows of a tile each.
   float *part_o, *part_lse;
   Desc *desc;
@@ -153,6 +162,24 @@ __device__ __forceinline__ int row_tiles_of(const AttnArgs &a, const Seq &q) {
   return static_cast<int>((rows + BM - 1) / BM);
 }
 
+// Units of a sequence that is the other kernel's, whose row tiles have BM rows.
+template <int BM, int BN, int COST>
+__device__ __forceinline__ int64_t units_elsewhere(const AttnArgs &a, const Seq &q) {
+  const int64_t rows = static_cast<int64_t>(q.n) * a.G;
+  if (rows <= 0 || (rows >= a.row_lo && rows <= a.row_hi)) return 0;
+  const int rts = static_cast<int>((rows + BM - 1) / BM);
+  return a.cache.heads * units_below<BM, BN, COST>(a, q, rts, rts);
+}
+
+// Units of the prefix's pass, of `tokens` tokens.
+__device__ __forceinline__ int64_t prefix_units(const AttnArgs &a, int tokens) {
+  const int64_t rows = static_cast<int64_t>(a.rows.offsets[a.rows.S]) * a.G;
+  const int BM = a.prefix_many ? kManyItemRows : kFewItemRows;
+  const int cost = a.prefix_many ? kManyItemCost : kFewItemCost;
+  const int tiles = tokens > 0 ? (tokens - 1) / kTileTokens + 1 : 1;
+  return (rows + BM - 1) / BM * (tiles + cost) * a.cache.heads;
+}
+
 struct Share {
   int32_t units, begin, end;   // all units; this CTA's
   int32_t ctas;                // that have work
@@ -171,7 +198,8 @@ __device__ __forceinline__ int64_t shfl_up64(int64_t v, int d) {
 
 // All units in the order (sequence, K/V head, row tile, then its COST units that are no
 // tiles, then its tiles) are cut into equal ranges, one for each CTA: every SM has the
-// same work whatever the lengths are.  2^31 units or more (70 TB of codes) are refused.
+// same work whatever the lengths are.  2^31 units or more (70 TB of codes) are refused, of
+// this kernel, of the other one or of the prefix's pass, by all that would write.
 // Checks the segments: where they cannot be used, nothing is to be done.
 template <int THREADS, int BM, int BN, int COST>
 __device__ __noinline__ void share_out(const AttnArgs &a, Share *sh, int64_t *warp_sums) {
@@ -179,11 +207,12 @@ __device__ __noinline__ void share_out(const AttnArgs &a, Share *sh, int64_t *wa
   const int per = (S + THREADS - 1) / THREADS;
   const int H = a.cache.heads;
   const int s0 = min(S, static_cast<int>(threadIdx.x) * per), s1 = min(S, s0 + per);
-  int64_t sum = 0;
+  constexpr bool kMany = BM == kManyItemRows;
+  int64_t sum = 0, elsewhere = 0;
   bool bad = false;
   if (a.prefix_len) {
     const int n = *a.prefix_len;
-    bad = n < 0 || n > a.prefix_capacity;
+    bad = n < 0 || n > a.prefix_capacity || prefix_units(a, n) > INT32_MAX;
   }
 #pragma unroll 1
   for (int s = s0; s < s1; ++s) {
@@ -194,6 +223,9 @@ __device__ __noinline__ void share_out(const AttnArgs &a, Share *sh, int64_t *wa
     bad |= off;
     const int rts = off ? 0 : row_tiles_of<BM>(a, q);
     if (rts > 0) sum += H * units_below<BM, BN, COST>(a, q, rts, rts);
+    else if (a.both && !off)
+      elsewhere += units_elsewhere<kMany ? kFewItemRows : kManyItemRows, BN,
+                                   kMany ? kFewItemCost : kManyItemCost>(a, q);
   }
   bad = __syncthreads_or(bad);
   if (bad) {
@@ -211,15 +243,24 @@ __device__ __noinline__ void share_out(const AttnArgs &a, Share *sh, int64_t *wa
     const int64_t o = shfl_up64(run, d);
     if (lane >= d) run += o;
   }
-  if (lane == 31) warp_sums[warp] = run;
+  if (a.both) {
+#pragma unroll 1
+    for (int d = 16; d > 0; d >>= 1) elsewhere += __shfl_xor_sync(0xffffffffu, elsewhere, d);
+  }
+  if (lane == 31) {
+    warp_sums[warp] = run;
+    warp_sums[THREADS / 32 + warp] = elsewhere;
+  }
   __syncthreads();
   int64_t before = run - sum, total = 0;
+  elsewhere = 0;
 #pragma unroll 1
   for (int w = 0; w < THREADS / 32; ++w) {
     if (w < warp) before += warp_sums[w];
     total += warp_sums[w];
+    elsewhere += warp_sums[THREADS / 32 + w];
   }
-  if (total > INT32_MAX) {
+  if (total > INT32_MAX || elsewhere > INT32_MAX) {
     if (threadIdx.x == 0) {
       atomicOr(a.rows.status, kStatusBadDeviceArg);
       *sh = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -382,8 +423,6 @@ __device__ __forceinline__ void emit(const AttnArgs &a, int64_t t, int hq, int d
   if (d == 0 && a.lse) a.lse[t * a.ld_lse + hq] = w.lse * kLn2;
 }
 
-// Rows from which a sequence takes the tensor cores of kv_attention_tc.cu.
-constexpr int kTcItemRows = 256;
 fp8la_status launch_many(const AttnArgs &a, bool f32, int format, int ctas, cudaStream_t s);
 
 }  // namespace kv

@@ -45,11 +45,11 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kRows = 128;          // of a tile
-constexpr int kItemRows = 256;
-constexpr int kTokens = 128;        // of a tile
+constexpr int kItemRows = kManyItemRows;
+constexpr int kTokens = kTileTokens;
 // What an item costs beside its tiles, in tiles: bringing its rows, writing them out.
 // Two prompts of 2048 tokens, us, with 2, 3, 4: 273, 267, 273.
-constexpr int kItemCost = 3;
+constexpr int kItemCost = kManyItemCost;
 constexpr int kItemBufs = 4;
 constexpr int kItemReaders = 10;    // the warps that make weights, 14 and 15
 constexpr int kConverters = 5;
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using Fm = Format<FMT>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Share sh;
-  __shared__ int64_t warp_sums[kThreads / 32];
+  __shared__ int64_t warp_sums[2 * kThreads / 32];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t *sbase = smem_raw + (base - raw);

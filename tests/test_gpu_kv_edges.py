@@ -76,3 +76,53 @@ def test_not_finite_value_of_a_negligible_token(rows, tokens, first):
     out, lse = check(fl, c)
     assert torch.isnan(out[:, 0, 5]).all() and int(torch.isnan(out).sum()) == rows
     assert torch.isfinite(lse).all()
+
+
+def _endless(fl, S_long, rows, len_long, D, short_rows, prefix=None):
+    """Sequences of the greatest length, all of their pages the same one, and a short one;
+    out and lse to be left alone."""
+    import torch
+    page = 2 ** 20
+    cache = fl.kv_cache(1, 1, page, D)
+    table = torch.zeros(S_long + 1, 2 ** 11, dtype=torch.int32, device="cuda")
+    lens = torch.tensor([len_long] * S_long + [200], dtype=torch.int32, device="cuda")
+    offs = torch.tensor([rows * i for i in range(S_long + 1)] + [rows * S_long + short_rows],
+                        dtype=torch.int32, device="cuda")
+    T = rows * S_long + short_rows
+    q = torch.ones(T, 1, D, dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(q, 5.0)
+    lse = torch.full((T, 1), 5.0, device="cuda")
+    fl.kv_attention(q, cache, offs, lens, table, max_rows=max(rows, short_rows), out=out, lse=lse)
+    torch.cuda.synchronize()
+    return fl.device_status(), out, lse
+
+
+@pytest.mark.parametrize("S,rows,short", [(40, 64, 100), (140, 256, 3)])
+def test_too_much_work_for_either_kernel_writes_nothing(S, rows, short):
+    """2^31 tiles of short segments, or of long ones, beside one of the other kind."""
+    import torch
+    fl = lib()
+    status, out, lse = _endless(fl, S, rows, 2 ** 31 - 4096, 16, short)
+    assert status == fl.FP8LA_ERR_DEVICE_ARG
+    assert torch.all(out == 5.0) and torch.all(lse == 5.0)
+
+
+@pytest.mark.parametrize("D,rows,G,pages", [(256, 8192, 128, 64), (16, 32768, 64, 256)])
+def test_too_much_work_for_the_prefix_writes_nothing(D, rows, G, pages):
+    """2^31 tiles of the prefix, by either kernel, before sequences without tokens."""
+    import torch
+    fl = lib()
+    cache = fl.kv_cache(1, 1, 2 ** 16 if D > 128 else 2 ** 20, D)
+    table = torch.zeros(1, pages * (1 if D > 128 else 8), dtype=torch.int32, device="cuda")
+    most = table.shape[1] * cache.shape[2]
+    plen = torch.tensor([min(most, 2 ** 31 - 4096)], dtype=torch.int32, device="cuda")
+    offs = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    lens = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q = torch.ones(rows, G, D, dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(q, 5.0)
+    lse = torch.full((rows, G), 5.0, device="cuda")
+    fl.kv_attention(q, cache, offs, lens, table, out=out, lse=lse, prefix_table=table[0],
+                    prefix_len=plen)
+    torch.cuda.synchronize()
+    assert fl.device_status() == fl.FP8LA_ERR_DEVICE_ARG
+    assert torch.all(out == 5.0) and torch.all(lse == 5.0)
