@@ -7,6 +7,7 @@
 // the exponent, w_j = 2^(x_j log2 e + log2 vs_j - M) with a running maximum M of
 // those sums, so that the products are w_j times codes, and the denominator is
 // sum_j w_j / vs_j.  One exponential an element, no product with dequantised values.
+// Where V's scales lie far apart, the denominator has a second part (kSpan).
 //
 // Precision: codes are halves exactly.  A BF16 query row, scaled by a power of
 // two to a maximum of 2^8, is halves exactly but for elements below 2^-22 of its
@@ -129,17 +130,6 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, uint
       "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
       : "memory");
-}
-
-// 2^e with the exponent of v (0 where v is not a positive finite number).
-__device__ __forceinline__ int exponent_of(float v) {
-  const uint32_t b = __float_as_uint(v);
-  const int e = static_cast<int>(b >> 23);  // a sign makes it more than 255
-  if (v == 0.0f || e >= 255) return 0;
-  return e > 0 ? e - 127 : -126;
-}
-__device__ __forceinline__ float power_of_two(int e) {  // -126 .. 127
-  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
 // 16 consecutive elements of a query row, from d on, as FP32.
@@ -376,6 +366,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[j][i] = 0.0f;
     float M[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    float far_top[2] = {-INFINITY, -INFINITY}, far_sum[2] = {0.0f, 0.0f};  // see kSpan
     int e0 = 0;
     bool poison = false;
 #pragma unroll 1
@@ -402,12 +393,29 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
         e0 = min(exponent_of(lds_f(scales + 4 * kStep)), 126);
         __syncwarp();
       }
+      uint32_t far;  // tokens whose shares are added up beside
       {
-        const float v = lds_f(scales + 4 * (kStep + lane)), near = v * power_of_two(-e0);
-        const bool in = base + lane < end, fine = v > 0.0f && v < INFINITY;
-        sts_f(scales + 4 * (kStep + lane), !in ? 0.0f : fine ? lg2(near) : NAN);
+        const float v = lds_f(scales + 4 * (kStep + lane));
+        const bool fine = base + lane < end && v > 0.0f && v < INFINITY;
+        const int top = __reduce_max_sync(0xffffffffu, fine ? min(exponent_of(v), 126) : -126);
+        if (top > e0 + kSpan) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            add_share(far_top[k], far_sum[k], M[k] - kShift, l[k]);
+            l[k] = 0.0f;
+            M[k] -= static_cast<float>(top - e0);
+          }
+          e0 = top;
+        }
+        const float near = v * power_of_two(-e0);
+        const bool less = fine && exponent_of(v) < e0 - kSpan;
+        far = __ballot_sync(0xffffffffu, less);
+        sts_f(scales + 4 * (kStep + lane), base + lane >= end ? 0.0f
+                                           : !fine            ? NAN
+                                           : less             ? log2_far(v, e0)
+                                                              : lg2(near));
         // A bad scale is in the exponent alone: rows that do not see it have weight 0.
-        sts_f(scales + 4 * (2 * kStep + lane), in && fine ? fminf(rcp(near), 3.0e38f) : 1.0f);
+        sts_f(scales + 4 * (2 * kStep + lane), !fine ? 1.0f : less ? 0.0f : rcp(near));
       }
       // Scores of tokens 16 u + 8 i + g against the 16 rows, in sc[2 u + i].
       float sc[2 * kSubs][4] = {};
@@ -446,6 +454,28 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
         }
       }
       __syncwarp();
+      if (far) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float x[4 * kSubs], top = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 4 * kSubs; ++i) {
+            const int t = 8 * (i >> 1) + 2 * c + (i & 1);
+            x[i] = (far >> t & 1) && base + t < seen[k]
+                       ? sc[i >> 1][2 * k + (i & 1)] * lds_f(scales + 4 * t) * factor[k]
+                       : -INFINITY;
+            top = fmaxf(top, x[i]);
+          }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          // The row's four lanes have the same maximum and a part of the sum each.
+          const float base2 = top == -INFINITY ? 0.0f : top;
+          float sum = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 4 * kSubs; ++i) sum += ex2(x[i] - base2);
+          add_share(far_top[k], far_sum[k], top, sum);
+        }
+      }
       // Exponents and weights of tokens 8 i + 2c, 8 i + 2c + 1.
 #pragma unroll
       for (int i = 0; i < 2 * kSubs; ++i) {
@@ -578,23 +608,22 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
     __syncthreads();
     float *red = reinterpret_cast<float *>(smem);
     float *red_lse = red + kWarps * kRows * C::kLdO;
-    const float back = power_of_two(e0);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      float sum = l[k];
+      float sum = l[k], beside = far_sum[k];
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      const float inv = sum > 0.0f || sum != sum ? rcp(sum) : 0.0f;
+      beside += __shfl_xor_sync(0xffffffffu, beside, 1);
+      beside += __shfl_xor_sync(0xffffffffu, beside, 2);
+      const Total all_of = total_of(M[k] - kShift, sum, far_top[k], beside, e0);
       float *row = red + (warp * kRows + g + 8 * k) * C::kLdO;
 #pragma unroll
       for (int j = 0; j < C::VH * C::VW; ++j)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           row[j / C::VW * 128 + (2 * c + i) * C::VW + j % C::VW] =
-              o[j][2 * k + i] * inv * back;
-      if (c == 0)
-        red_lse[warp * kRows + g + 8 * k] =
-            sum > 0.0f || sum != sum ? M[k] - kShift + lg2(sum) : -INFINITY;
+              o[j][2 * k + i] * all_of.f0 * all_of.f1;
+      if (c == 0) red_lse[warp * kRows + g + 8 * k] = all_of.lse;
     }
     __syncthreads();
     if (a.late) pdl_wait();  // the prefix's results
@@ -610,32 +639,33 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
         best = fmaxf(best, lse[w]);
       }
       // A NaN is in no maximum, but in its weight.
-      float weight[kWarps], sum = 0.0f;
+      Factors weight[kWarps];
+      float sum = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        weight[w] = lse[w] == -INFINITY ? 0.0f : ex2(lse[w] - best);
-        sum += weight[w];
+        weight[w] = weight_of(lse[w] == -INFINITY ? -INFINITY : lse[w] - best);
+        sum += weight[w].f0 * weight[w].f1;
       }
       const float inv = sum == 0.0f ? 0.0f : rcp(sum);
-      const float joined = sum == 0.0f ? -INFINITY : best + lg2(sum);
+      const float all_lse = sum == 0.0f ? -INFINITY : best + lg2(sum);
       float x[8] = {};
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {  // 0 x NaN too: a V that is not finite
         const float *p = red + (w * kRows + r) * C::kLdO + d;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = fmaf(weight[w] * inv, p[j], x[j]);
+        for (int j = 0; j < 8; ++j) x[j] = fmaf(weight[w].f0 * inv, p[j] * weight[w].f1, x[j]);
       }
       if (d >= kc.D) continue;
       if (whole) {
         const int rr = rt * kRows + r, t = divide(rr, a.group);
         const int64_t row = static_cast<int64_t>(q.row0) + t;
         const int hq = h * a.G + rr - t * a.G;
-        emit<8>(a, row, hq, d, x, joined, weigh(a, row, hq, joined));
+        emit<8>(a, row, hq, d, x, all_lse, weigh(a, row, hq, all_lse));
       } else {
         float *p = a.part_o + (static_cast<int64_t>(part) * kRows + r) * DP + d;
         *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
         *reinterpret_cast<float4 *>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
-        if (d == 0) a.part_lse[part * kRows + r] = joined;
+        if (d == 0) a.part_lse[part * kRows + r] = all_lse;
       }
     }
     if (threadIdx.x == 0 && !whole && tile0 == 0)
@@ -744,7 +774,8 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinResident)
         const int own = lane & 3, row = (lane >> 2) % R;
         const float lse =
             own < d.parts && r0 + row < rows ? part_lse[part(own) + row] : -INFINITY;
-        float x[R][V] = {}, weight = 0.0f, joined = -INFINITY;
+        float x[R][V] = {}, all_lse = -INFINITY;
+        Factors weight = {0.0f, 0.0f};
 #pragma unroll 1
         for (int i0 = 0; i0 < d.parts; i0 += 2) {
           float y[R][2][V];
@@ -762,25 +793,26 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinResident)
             float best = lse;
             best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 1));
             best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 2));
-            const float w = lse == -INFINITY ? 0.0f : ex2(lse - best);
-            float sum = w;
+            weight = weight_of(lse == -INFINITY ? -INFINITY : lse - best);
+            float sum = weight.f0 * weight.f1;
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            weight = sum == 0.0f ? 0.0f : w * rcp(sum);
-            joined = sum == 0.0f ? -INFINITY : best + lg2(sum);
+            weight.f0 = sum == 0.0f ? 0.0f : weight.f0 * rcp(sum);
+            all_lse = sum == 0.0f ? -INFINITY : best + lg2(sum);
           }
 #pragma unroll
           for (int u = 0; u < R; ++u)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const float w = __shfl_sync(0xffffffffu, weight, 4 * u + i0 + k);
+              const float w = __shfl_sync(0xffffffffu, weight.f0, 4 * u + i0 + k);
+              const float f1 = __shfl_sync(0xffffffffu, weight.f1, 4 * u + i0 + k);
 #pragma unroll
-              for (int j = 0; j < V; ++j) x[u][j] = fmaf(w, y[u][k][j], x[u][j]);
+              for (int j = 0; j < V; ++j) x[u][j] = fmaf(w, y[u][k][j] * f1, x[u][j]);
             }
         }
 #pragma unroll
         for (int u = 0; u < R; ++u) {
-          const float l = __shfl_sync(0xffffffffu, joined, 4 * u);
+          const float l = __shfl_sync(0xffffffffu, all_lse, 4 * u);
           if (r0 + u >= rows || lane * V >= a.cache.D) continue;
           const int rr = d.rt * BM + r0 + u, t = divide(rr, a.group);
           const int64_t row = static_cast<int64_t>(q.row0) + t;
@@ -809,7 +841,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinResident)
             // A weight to each lane, so that the parts' loads wait for nothing.
             const int n = min(32, i1 - i0);
             const float lse = lane < n ? part_lse[part(i0 + lane)] : -INFINITY;
-            const float mine = lse == -INFINITY ? 0.0f : ex2(lse - best);
+            const Factors mine = weight_of(lse == -INFINITY ? -INFINITY : lse - best);
 #pragma unroll 1
             for (int i = 0; i < n; i += kAtOnce) {
               float y[kAtOnce][V];
@@ -819,10 +851,11 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinResident)
 #pragma unroll
               for (int u = 0; u < kAtOnce; ++u) {
                 if (i + u >= n) break;
-                const float w = __shfl_sync(0xffffffffu, mine, i + u);
-                sum += w;
+                const float w = __shfl_sync(0xffffffffu, mine.f0, i + u);
+                const float f1 = __shfl_sync(0xffffffffu, mine.f1, i + u);
+                sum += w * f1;
 #pragma unroll
-                for (int j = 0; j < V; ++j) x[j] = fmaf(w, y[u][j], x[j]);
+                for (int j = 0; j < V; ++j) x[j] = fmaf(w, y[u][j] * f1, x[j]);
               }
             }
           }

@@ -73,6 +73,73 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
+// 2^e with the exponent of v (0 where v is not a positive finite number).
+__device__ __forceinline__ int exponent_of(float v) {
+  const uint32_t b = __float_as_uint(v);
+  const int e = static_cast<int>(b >> 23);  // a sign makes it more than 255
+  if (v == 0.0f || e >= 255) return 0;
+  return e > 0 ? e - 127 : -126;
+}
+__device__ __forceinline__ float power_of_two(int e) {  // -126 .. 127
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+// V's scales stand in the exponents, relative to a power of two e0, and a token's share of
+// the denominator is its weight over that relative scale.  That holds in FP32 while the
+// scales lie within 2^kSpan of e0: what is lost then is 2^-51 of the largest share or less
+// (a weight underflows 2^133 below the largest, which is at most 2^kSpan larger by its scale
+// than by its share, and the lost one at most 2^kSpan smaller).  A token whose scale is
+// smaller keeps its weight, and its share is added up beside, a sum with a maximum of its own
+// (set_aside); where a larger one comes, e0 rises to it and what was added up until then
+// goes there.  So any positive finite scales are right, and those that an ordinary cache
+// holds cost a comparison.
+constexpr int kSpan = 40;
+
+// log2 of a scale of any size, relative to 2^e0.
+__device__ __forceinline__ float log2_far(float v, int e0) {
+  const bool small = v < 1.0f;  // 2^-149 and up: subnormal ones become normal
+  return lg2(small ? v * 1.2676506002282294e30f : v) - static_cast<float>((small ? 100 : 0) + e0);
+}
+
+// A sum of 2^x as sum * 2^top; adds n * 2^x.  NaN stays.
+__device__ __forceinline__ void add_share(float &top, float &sum, float x, float n) {
+  const float m = fmaxf(top, x), base = m == -INFINITY ? 0.0f : m;
+  // Without shares so far, or of this one, the other's factor is 2^0 or it is not finite.
+  const float down = top == -INFINITY ? 0.0f : ex2(top - base);
+  sum = sum * down + (x == -INFINITY ? n * 0.0f : n * ex2(x - base));
+  top = m;
+}
+
+// A row's logarithm, and the two factors (to be applied one after the other, as their
+// product may leave FP32's range) that make its result of sums of weights times codes:
+// `sum` shares relative to 2^top, `far_sum` relative to 2^far_top, scales relative to 2^e0.
+struct Total {
+  float lse, f0, f1;
+};
+__device__ __forceinline__ Total total_of(float top, float sum, float far_top, float far_sum,
+                                          int e0) {
+  if (far_sum == 0.0f) {
+    const bool some = sum > 0.0f || sum != sum;
+    return {some ? top + lg2(sum) : -INFINITY, some ? rcp(sum) : 0.0f, power_of_two(e0)};
+  }
+  add_share(far_top, far_sum, top, sum);
+  const float lse = far_top + lg2(far_sum);
+  // top is -inf where no weight was more than 0.
+  const float f = ex2(0.5f * (top - lse + static_cast<float>(e0)));
+  return {lse, f, f};
+}
+
+// A part's weight 2^x, x <= 0, as a product: below 2^-126, which FP32 ends at, a part still
+// counts where its values, by V's scales, are as much larger than the others'.
+struct Factors {
+  float f0, f1;
+};
+__device__ __forceinline__ Factors weight_of(float x) {
+  const bool far = x < -100.0f;
+  const float f = ex2(far ? 0.5f * x : x);
+  return {f, far ? f : 1.0f};
+}
+
 // m16n8k16 with half operands.
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                         uint32_t b1) {
@@ -377,16 +444,23 @@ __device__ __noinline__ bool next_item(const AttnArgs &a, Walk *w, Item *it) {
 
 // Where and how much a joined row weighs: own result and the prefix's.
 struct Weights {
-  float own, pre, lse;  // lse: base 2, of both
+  Factors own, pre;
+  float lse;  // base 2, of both
 };
 __device__ __forceinline__ Weights weigh(const AttnArgs &a, int64_t t, int hq, float lse) {
-  if (!a.pre_lse) return {1.0f, 0.0f, lse};
+  if (!a.pre_lse) return {{1.0f, 1.0f}, {0.0f, 0.0f}, lse};
   const float p = a.pre_lse[t * a.Hq + hq];
   // A maximum drops a NaN, which the weights and the logarithm are to keep.
-  if (lse == -INFINITY && p == -INFINITY) return {0.0f, 0.0f, -INFINITY};
+  if (lse == -INFINITY && p == -INFINITY) return {{0.0f, 0.0f}, {0.0f, 0.0f}, -INFINITY};
   const float top = fmaxf(lse, p);
-  const float x = ex2(lse - top), y = ex2(p - top), inv = rcp(x + y);
-  return {x * inv, y * inv, top + lg2(x + y)};
+  Factors x = weight_of(lse - top), y = weight_of(p - top);
+  const float sum = x.f0 * x.f1 + y.f0 * y.f1, inv = rcp(sum);
+  x.f0 *= inv;
+  y.f0 *= inv;
+  return {x, y, top + lg2(sum)};
+}
+__device__ __forceinline__ float joined(const Weights &w, float own, float pre) {
+  return own * w.own.f1 * w.own.f0 + pre * w.pre.f1 * w.pre.f0;
 }
 
 // Writes N consecutive elements of a row's result, own ones in o, and where `d` is 0
@@ -407,8 +481,8 @@ __device__ __forceinline__ void emit(const AttnArgs &a, int64_t t, int hq, int d
 #pragma unroll
   for (int i = 0; i < N; i += 2) {
     // A side without tokens has weight 0 and zeros.
-    const float x = q ? o[i] * w.own + q[i] * w.pre : o[i];
-    const float y = q ? o[i + 1] * w.own + q[i + 1] * w.pre : o[i + 1];
+    const float x = q ? joined(w, o[i], q[i]) : o[i];
+    const float y = q ? joined(w, o[i + 1], q[i + 1]) : o[i + 1];
     const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
     u[i / 2] = *reinterpret_cast<const uint32_t *>(&b);
   }

@@ -55,8 +55,12 @@ constexpr int kItemReaders = 10;    // the warps that make weights, 14 and 15
 constexpr int kConverters = 5;
 constexpr int kGroup = 16;          // tokens of a converter's job
 constexpr int kJobs = 2 * kTokens / kGroup;  // of a tile, K's first
-constexpr int kScaleBufs = 4;       // K's scales, log2 and reciprocal of V's, an exponent
-constexpr int kScaleBytes = 3 * kTokens * 4 + 16;
+// K's scales, log2 and reciprocal of V's, and of the tile: what V's are relative to, by how
+// much that rose, whether there are tokens whose shares are added up beside, and those
+// tokens' bits (see kSpan).
+constexpr int kScaleBufs = 4;
+constexpr int kTileHead = 3 * kTokens * 4;
+constexpr int kScaleBytes = kTileHead + 32;
 constexpr float kShift = 7.0f;      // as in kv_attention.cu
 constexpr float kLazy = 8.0f;
 template <int DP, int TERMS>
@@ -258,15 +262,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-__device__ __forceinline__ int exponent_of(float v) {
-  const int e = static_cast<int>(__float_as_uint(v) >> 23);
-  if (v == 0.0f || e >= 255) return 0;
-  return e > 0 ? e - 127 : -126;
-}
-__device__ __forceinline__ float power_of_two(int e) {
-  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-}
-
 // A warp's 32 rows of q, 8 elements of a row a lane: copied to where their halves will be,
 // element 8 s of row r in chunk s % 8, swizzled by the row, of block s / 8.  Rows and
 // columns that there are not become zeros.
@@ -395,6 +390,36 @@ __device__ __noinline__ void scale_q(const AttnArgs &a, uint32_t q_at, float *fa
   __syncwarp();
 }
 
+// Where the scale of a tile's column lies: columns 2 c, 2 c + 1, 2 c + 8, 2 c + 9 of 16 lie
+// together, as a thread that makes weights has those.
+__device__ __forceinline__ int scale_place(int col) {
+  return (col & ~15) + ((col >> 1) & 3) * 4 + ((col >> 3) & 1) * 2 + (col & 1);
+}
+
+// Adds up beside the shares of the columns in `mask`, 32 from `col` on, of a warp's rows, one
+// a lane, which sees `limit` columns.  The scores are read again, from `scores` on: this is
+// done before weights take their place.
+__device__ __noinline__ void set_aside(uint32_t scores, uint32_t k_scales, uint32_t mask, int col,
+                                       int limit, float factor, float *far_top, float *far_sum) {
+  float top = *far_top, sum = *far_sum;
+#pragma unroll 1
+  for (; mask; mask &= mask - 1) {
+    const int j = col + __ffs(mask) - 1;
+    float x, ks;
+    __syncwarp();
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(x)
+        : "r"(scores + j)
+        : "memory");
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ks) : "r"(k_scales + 4 * scale_place(j)) : "memory");
+    if (j < limit) add_share(top, sum, x * ks * factor, 1.0f);
+  }
+  *far_top = top;
+  *far_sum = sum;
+}
+
 // Columns k .. k+15 of V that hold a code that is not finite at a token that a row sees,
 // of the tiles that were written without such codes: those that not all rows see.
 template <typename Fm>
@@ -462,6 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Walk walk;
   __shared__ int page_ids[2][kTokens];
   __shared__ float row_stats[8][64];
+  __shared__ float beside[8][64];  // of a warp's rows: the maximum and the sum of add_share
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::SLOTS; ++i) {
       mbar_init(full_bar(i), kTokens / kGroup);
@@ -549,6 +575,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool active = t * kRows < rows;
       float factor[4], M[4];
       uint64_t l2[4];                  // of even and odd columns
+      float *const far_top = beside[warp], *const far_sum = beside[warp] + 32;
+      far_top[lane] = -INFINITY;
+      far_sum[lane] = 0.0f;
+      __syncwarp();
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         factor[u] = my_factors[8 * u + g];
@@ -557,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // Tokens that each row of the warp sees: the first one's.
       const int all = row0 + 32 <= rows ? tokens_seen(a, it.q, it.rt * kItemRows + row0) : 0;
-      float back = 1.0f;  // what V's scales are relative to
+      int e0 = 0;  // V's scales are relative to 2^e0
 #pragma unroll 1
       for (int j = 0; j < count; ++j, ++sc) {
         const int buf = sc % kScaleBufs;
@@ -571,11 +601,42 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         const uint32_t scales = base + C::kScales + buf * kScaleBytes;
-        if (j == 0)
-          back = power_of_two(*reinterpret_cast<const int *>(
-              sbase + C::kScales + buf * kScaleBytes + 12 * kTokens));
+        const int4 head = *reinterpret_cast<const int4 *>(
+            sbase + C::kScales + buf * kScaleBytes + kTileHead);
+        if (j == 0) e0 = head.x;
         if (!(ok = wait(s_bar(t), tiles & 1u))) break;
         tc_fence_after();
+        if (opaque(head.y > 0 && j > 0)) {
+          e0 += head.y;
+#pragma unroll 1
+          for (int u = 0; u < 4; ++u) {
+            float y, z;
+            const uint64_t l = u < 2 ? (u == 0 ? l2[0] : l2[1]) : (u == 2 ? l2[2] : l2[3]);
+            const float m = u < 2 ? (u == 0 ? M[0] : M[1]) : (u == 2 ? M[2] : M[3]);
+            unpair(l, y, z);
+            y += z;
+            y += __shfl_xor_sync(0xffffffffu, y, 1);
+            y += __shfl_xor_sync(0xffffffffu, y, 2);
+            if (c == 0) add_share(far_top[8 * u + g], far_sum[8 * u + g], m - kShift, y);
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            M[u] -= static_cast<float>(head.y);
+            l2[u] = pair(0.0f, 0.0f);
+          }
+          __syncwarp();
+        }
+        if (opaque(head.z != 0)) {
+          const int r = row0 + lane;
+          const int seen = r < rows ? tokens_seen(a, it.q, it.rt * kItemRows + r) : 0;
+          const uint32_t *masks = reinterpret_cast<const uint32_t *>(
+              sbase + C::kScales + buf * kScaleBytes + kTileHead + 16);
+#pragma unroll 1
+          for (int i = 0; i < kTokens / 32; ++i)
+            set_aside(s_tm, scales, masks[i], 32 * i, seen - tok0 - j * kTokens, my_factors[lane],
+                      far_top + lane, far_sum + lane);
+          __syncwarp();
+        }
         // The last scores of these rows are made: the next rows may take their place.
         if (j + 1 == count && more) fetch_q<F32Q, DP>(a, upcoming, q_at, row0);
 #pragma unroll 1
@@ -731,9 +792,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = wait(o_bar(t), o_uses & 1u))) break;
       ++o_uses;
       tc_fence_after();
-      const bool some = sum > 0.0f || sum != sum;
-      const float inv = some ? rcp(sum) * back : 0.0f;
-      const float lse = some ? best - kShift + lg2(sum) : -INFINITY;
+      const Total all_of = total_of(best - kShift, sum, far_top[lane], far_sum[lane], e0);
+      const float lse = all_of.lse;
       const bool mask = *poison != 0;
       const bool on = row0 + lane < rows;
       const bool whole = it.count == it.tiles;
@@ -742,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int hq = it.h * a.G + r - tok * a.G;
       const int64_t place = out_row * a.Hq + hq;
       const int64_t part = (2 * static_cast<int64_t>(blockIdx.x) + (it.tile0 > 0 ? 0 : 1)) * kItemRows + t * kRows + row;
-      Weights weights = {1.0f, 0.0f, lse};
+      Weights weights = {{1.0f, 1.0f}, {0.0f, 0.0f}, lse};
       const float *pre = nullptr;
       if (whole && !a.raw_o && on) {
         weights = weigh(a, out_row, hq, lse);
@@ -760,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float o[16];
         tmem_load16(o_tm + k, o);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] *= inv;
+        for (int i = 0; i < 16; ++i) o[i] = o[i] * all_of.f0 * all_of.f1;
         if (opaque(mask && on)) {
           const uint32_t bad = lost_columns<Fm>(a, it, my_seen, k);
 #pragma unroll
@@ -780,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (opaque(pre != nullptr)) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = o[i] * weights.own + pre[k + i] * weights.pre;
+          for (int i = 0; i < 16; ++i) o[i] = joined(weights, o[i], pre[k + i]);
         }
         uint32_t u[8];
 #pragma unroll
@@ -899,9 +959,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool is_v = warp == 14;
     const Cache &c = a.cache;
     const float *const scales_from = is_v ? c.v_scale : c.k_scale;
-    // Scales of the columns 2 c, 2 c + 1, 2 c + 8, 2 c + 9 of 16 lie together: a thread
-    // that makes weights has those.
-    const int scale_at = (lane & ~15) + ((lane >> 1) & 3) * 4 + ((lane >> 3) & 1) * 2 + (lane & 1);
+    const int scale_at = scale_place(lane);
     const uint32_t page16 = static_cast<uint32_t>(c.page_stride >> 4),
                    token16 = static_cast<uint32_t>(c.token_stride >> 4),
                    head16 = static_cast<uint32_t>(c.head_stride >> 4);
@@ -942,7 +1000,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             copy4(dst, scales_from + static_cast<uint64_t>(p) * s_page + pl * s_token +
                            static_cast<uint64_t>(h) * s_head);
           else
-            asm volatile("st.shared.f32 [%0], %1;" ::"r"(dst), "f"(in ? NAN : 1.0f) : "memory");
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(dst),
+                         "f"(in ? NAN : is_v ? 0.0f : 1.0f) : "memory");
           if (!opaque(is_v)) {
             // Lowest bit: not all rows see the tile.  All bits: there is no token.
             const uint64_t at = good ? (static_cast<uint64_t>(p) * page16 + pl * token16 +
@@ -1008,21 +1067,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (opaque(is_v)) {
           // Relative to a power of two near the scale of the item's first token.
           if (was_first) e0 = min(exponent_of(out[kTokens]), 126);
-          __syncwarp();
+          int top = -126;
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            const float v = out[kTokens + 32 * i + scale_at];
+            if (v > 0.0f && v < INFINITY) top = max(top, min(exponent_of(v), 126));
+          }
+          top = __reduce_max_sync(0xffffffffu, top);
+          const int rise = top > e0 + kSpan ? top - e0 : 0;
+          e0 += rise;
           const float down = power_of_two(-e0);
+          uint32_t any = 0;
+          uint32_t *const head = reinterpret_cast<uint32_t *>(out) + kTileHead / 4;
 #pragma unroll 1
           for (int i = 0; i < 4; ++i) {
             float *at = out + kTokens + 32 * i + scale_at;
             const float scale = *at, v = scale * down;
             const bool fine = scale > 0.0f && scale < INFINITY;
+            const bool less = fine && exponent_of(scale) < e0 - kSpan;
+            const uint32_t far = __ballot_sync(0xffffffffu, less);
+            any |= far;
             float lg, inv;
             asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg) : "f"(v));
             asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(v));
+            if (less) {
+              lg = log2_far(scale, e0);
+              inv = 0.0f;
+            }
             at[0] = fine ? lg : NAN;
             // A bad scale is in the exponent alone: rows that do not see it have weight 0.
-            at[kTokens] = fine ? fminf(inv, 3.0e38f) : 1.0f;
+            at[kTokens] = fine ? inv : 1.0f;
+            if (lane == 0) head[4 + i] = far;
           }
-          if (lane == 0) *reinterpret_cast<int *>(out + 3 * kTokens) = e0;
+          if (lane == 0) {
+            head[0] = static_cast<uint32_t>(e0);
+            head[1] = static_cast<uint32_t>(was_first ? 0 : rise);
+            head[2] = any;
+          }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(scfull_bar((step - 1) % kScaleBufs));

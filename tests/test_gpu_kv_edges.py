@@ -126,3 +126,44 @@ def test_too_much_work_for_the_prefix_writes_nothing(D, rows, G, pages):
     torch.cuda.synchronize()
     assert fl.device_status() == fl.FP8LA_ERR_DEVICE_ARG
     assert torch.all(out == 5.0) and torch.all(lse == 5.0)
+
+
+SPREADS = {
+    "small first": lambda j, n, r: -148.0 if j == 0 else 2.0,
+    "small last": lambda j, n, r: -140.0 if j == n - 1 else 2.0,
+    "large first": lambda j, n, r: 100.0 if j == 0 else -40.0,
+    "large last": lambda j, n, r: 100.0 if j == n - 1 else -40.0,
+    "in turn": lambda j, n, r: 90.0 if j % 2 else -110.0,
+    "rising": lambda j, n, r: -145.0 + 260.0 * j / n,
+    "falling": lambda j, n, r: 115.0 - 260.0 * j / n,
+    "any": lambda j, n, r: r.uniform(-145.0, 115.0),
+    "all small": lambda j, n, r: r.uniform(-148.0, -130.0),
+    "all large": lambda j, n, r: r.uniform(100.0, 115.0),
+}
+
+
+@pytest.mark.parametrize("spread", list(SPREADS))
+@pytest.mark.parametrize("scale", [0.0, 0.125, 4.0, 60.0])
+@pytest.mark.parametrize("rows,tokens,prefix", [(1, 70, 0), (3, 900, 0), (100, 300, 0),
+                                                (2, 90, 150), (80, 100, 200)])
+def test_scales_of_v_over_all_exponents(rows, tokens, prefix, scale, spread):
+    """Whatever V's scales are, each token's mass and value count: with sharp scores a
+    small one's alone, with scores of 0 all masses the same."""
+    import random
+    import torch
+    fl = lib()
+    r = random.Random(rows + tokens)
+    c = make((tokens,), (rows,), 2, 2, 64, 16, prefix=prefix)
+    for pages, n in ((c["table"][0], tokens), (c["prefix_table"], prefix)):
+        j = torch.arange(n, device="cuda")
+        size = torch.tensor([2.0 ** SPREADS[spread](i, n, r) for i in range(n)],
+                            dtype=torch.float64, device="cuda").float()
+        for h in range(2):
+            c["cache"].v_scale[pages[j // 16].long(), h, j % 16] = size
+    out, lse = attend(fl, c, scale=scale)
+    torch.cuda.synchronize()
+    assert fl.device_status() == 0
+    ro, ob, rl, lb = reference(c, scale=scale)
+    # BF16's subnormals are 2^-133 apart, FP32's 2^-149
+    assert close(out, ro, ob + 2.0 ** -134 + 2.0 ** -148)
+    assert close(lse, rl, lb)
