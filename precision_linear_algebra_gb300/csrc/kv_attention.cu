@@ -7,7 +7,8 @@
 // the exponent, w_j = 2^(x_j log2 e + log2 vs_j - M) with a running maximum M of
 // those sums, so that the products are w_j times codes, and the denominator is
 // sum_j w_j / vs_j.  One exponential an element, no product with dequantised values.
-// Where V's scales lie far apart, the denominator has a second part (kSpan).
+// Where V's scales lie far apart, the denominator has a second part (kSpan), and so it has
+// for rows of zeros in V, which would otherwise set M by a scale that scales nothing.
 //
 // Precision: codes are halves exactly.  A BF16 query row, scaled by a power of
 // two to a maximum of 2^8, is halves exactly but for elements below 2^-22 of its
@@ -454,28 +455,30 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
         }
       }
       __syncwarp();
-      if (far) {
+      // Adds up beside the shares of the tokens in `mask`, whose scores x(i, k) gives.
+      auto set_aside = [&](uint32_t mask, auto score) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           float x[4 * kSubs], top = -INFINITY;
 #pragma unroll
           for (int i = 0; i < 4 * kSubs; ++i) {
             const int t = 8 * (i >> 1) + 2 * c + (i & 1);
-            x[i] = (far >> t & 1) && base + t < seen[k]
-                       ? sc[i >> 1][2 * k + (i & 1)] * lds_f(scales + 4 * t) * factor[k]
-                       : -INFINITY;
+            x[i] = (mask >> t & 1) && base + t < seen[k] ? score(sc[i >> 1][2 * k + (i & 1)], t, k)
+                                                         : -INFINITY;
             top = fmaxf(top, x[i]);
           }
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
           // The row's four lanes have the same maximum and a part of the sum each.
-          const float base2 = top == -INFINITY ? 0.0f : top;
+          const float from = top == -INFINITY ? 0.0f : top;
           float sum = 0.0f;
 #pragma unroll
-          for (int i = 0; i < 4 * kSubs; ++i) sum += ex2(x[i] - base2);
+          for (int i = 0; i < 4 * kSubs; ++i) sum += ex2(x[i] - from);
           add_share(far_top[k], far_sum[k], top, sum);
         }
-      }
+      };
+      if (far)
+        set_aside(far, [&](float s, int t, int k) { return s * lds_f(scales + 4 * t) * factor[k]; });
       // Exponents and weights of tokens 8 i + 2c, 8 i + 2c + 1.
 #pragma unroll
       for (int i = 0; i < 2 * kSubs; ++i) {
@@ -501,6 +504,27 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
         for (int i = 1; i < 2 * kSubs; ++i) mx[k] = fmaxf(mx[k], fmaxf(sc[i][2 * k], sc[i][2 * k + 1]));
       }
       if (__any_sync(0xffffffffu, mx[0] > M[0] + kLazy || mx[1] > M[1] + kLazy)) {
+        // A row of zeros in V adds nothing to the result, whatever its scale: it must not
+        // take the others' weights towards a half's end.
+        uint32_t some = 0;
+#pragma unroll 1
+        for (int ch = 0; ch < C::CH; ++ch) {
+          const uint4 w = lds128(st + (lane / kGroup * 2 + 1) * C::kK +
+                                 chunk_at<DP>(lane % kGroup, ch));
+          some |= w.x | w.y | w.z | w.w;
+        }
+        const uint32_t zeros = __ballot_sync(0xffffffffu, (some & 0x7f7f7f7fu) == 0) & ~far;
+        if (zeros) {
+          set_aside(zeros, [&](float s, int t, int) { return s - lds_f(scales + 4 * (kStep + t)); });
+          mx[0] = mx[1] = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 2 * kSubs; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (zeros >> (8 * i + 2 * c + (k & 1)) & 1) sc[i][k] = -INFINITY;
+              mx[k >> 1] = fmaxf(mx[k >> 1], sc[i][k]);
+            }
+        }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           float m = mx[k];

@@ -55,9 +55,9 @@ constexpr int kItemReaders = 10;    // the warps that make weights, 14 and 15
 constexpr int kConverters = 5;
 constexpr int kGroup = 16;          // tokens of a converter's job
 constexpr int kJobs = 2 * kTokens / kGroup;  // of a tile, K's first
-// K's scales, log2 and reciprocal of V's, and of the tile: what V's are relative to, by how
-// much that rose, whether there are tokens whose shares are added up beside, and those
-// tokens' bits (see kSpan).
+// K's scales, log2 and reciprocal of V's, and of the tile: the exponent that V's are relative
+// to, whether it rose (1) and whether there are tokens whose shares are added up beside (2),
+// by how much it rose, and, from the fifth word on, those tokens' bits (see kSpan).
 constexpr int kScaleBufs = 4;
 constexpr int kTileHead = 3 * kTokens * 4;
 constexpr int kScaleBytes = kTileHead + 32;
@@ -487,7 +487,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Walk walk;
   __shared__ int page_ids[2][kTokens];
   __shared__ float row_stats[8][64];
-  __shared__ float beside[8][64];  // of a warp's rows: the maximum and the sum of add_share
+  // Of a warp's rows: the maximum and the sum of add_share; what V's scales are relative to.
+  __shared__ float beside[8][65];
+  __shared__ uint16_t zero_rows[C::SLOTS][kTokens / kGroup];  // a bit for each row of V
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::SLOTS; ++i) {
       mbar_init(full_bar(i), kTokens / kGroup);
@@ -587,7 +589,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // Tokens that each row of the warp sees: the first one's.
       const int all = row0 + 32 <= rows ? tokens_seen(a, it.q, it.rt * kItemRows + row0) : 0;
-      int e0 = 0;  // V's scales are relative to 2^e0
 #pragma unroll 1
       for (int j = 0; j < count; ++j, ++sc) {
         const int buf = sc % kScaleBufs;
@@ -601,13 +602,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         const uint32_t scales = base + C::kScales + buf * kScaleBytes;
-        const int4 head = *reinterpret_cast<const int4 *>(
-            sbase + C::kScales + buf * kScaleBytes + kTileHead);
-        if (j == 0) e0 = head.x;
         if (!(ok = wait(s_bar(t), tiles & 1u))) break;
         tc_fence_after();
-        if (opaque(head.y > 0 && j > 0)) {
-          e0 += head.y;
+        const int *const head = reinterpret_cast<const int *>(
+            sbase + C::kScales + buf * kScaleBytes + kTileHead);
+        if (j == 0) far_top[64] = __int_as_float(head[0]);
+        const int apart = head[1];
+        if (opaque(apart & 1)) {
+          const int rise = head[2];
+          far_top[64] = __int_as_float(head[0]);
 #pragma unroll 1
           for (int u = 0; u < 4; ++u) {
             float y, z;
@@ -621,19 +624,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            M[u] -= static_cast<float>(head.y);
+            M[u] -= static_cast<float>(rise);
             l2[u] = pair(0.0f, 0.0f);
           }
           __syncwarp();
         }
-        if (opaque(head.z != 0)) {
+        if (opaque(apart & 2)) {
           const int r = row0 + lane;
           const int seen = r < rows ? tokens_seen(a, it.q, it.rt * kItemRows + r) : 0;
-          const uint32_t *masks = reinterpret_cast<const uint32_t *>(
-              sbase + C::kScales + buf * kScaleBytes + kTileHead + 16);
 #pragma unroll 1
           for (int i = 0; i < kTokens / 32; ++i)
-            set_aside(s_tm, scales, masks[i], 32 * i, seen - tok0 - j * kTokens, my_factors[lane],
+            set_aside(s_tm, scales, head[4 + i], 32 * i, seen - tok0 - j * kTokens, my_factors[lane],
                       far_top + lane, far_sum + lane);
           __syncwarp();
         }
@@ -644,49 +645,77 @@ __global__ void __launch_bounds__(kThreads, 1)
           constexpr int HT = kTokens / 2;
           const uint32_t hs = scales + 4 * HT * half + 16 * c;
           float x[2][32];
+          const int first = tok0 + j * kTokens + HT * half;
+          bool again = false;  // rows of zeros have been taken out
+#pragma unroll 1
+          for (;;) {
 #pragma unroll
-          for (int b = 0; b < 2; ++b) tmem_load_rows(s_tm + HT * half + b * kLanes16, x[b]);
-          tmem_wait32(x[0]);
-          tmem_wait32(x[1]);
+            for (int b = 0; b < 2; ++b) tmem_load_rows(s_tm + HT * half + b * kLanes16, x[b]);
+            tmem_wait32(x[0]);
+            tmem_wait32(x[1]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint64_t ks[2], lv[2];
-            lds_pairs(hs + 64 * i, ks[0], ks[1]);
-            lds_pairs(hs + 4 * kTokens + 64 * i, lv[0], lv[1]);
+            for (int i = 0; i < 4; ++i) {
+              uint64_t ks[2], lv[2];
+              lds_pairs(hs + 64 * i, ks[0], ks[1]);
+              lds_pairs(hs + 4 * kTokens + 64 * i, lv[0], lv[1]);
 #pragma unroll
-            for (int p = 0; p < 2; ++p)
+              for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                  float *v = &x[u >> 1][4 * (2 * i + p) + 2 * (u & 1)];
+                  unpair(fma2(mul2(pair(v[0], v[1]), ks[p]), pair(factor[u], factor[u]), lv[p]),
+                         v[0], v[1]);
+                }
+            }
+            // The half's rows of zeros in V, but for those that are set aside anyway.
+            auto zeros = [&](int w) {
+              const uint16_t *z = &zero_rows[(2 * sc + 1) % C::SLOTS][4 * half + 2 * w];
+              return (z[0] | static_cast<uint32_t>(z[1]) << 16) &
+                     ~(head[1] & 2 ? head[4 + 2 * half + w] : 0);
+            };
+            if (first + HT > all || opaque(again)) {
+              const uint32_t z0 = again ? zeros(0) >> 2 * c : 0, z1 = again ? zeros(1) >> 2 * c : 0;
 #pragma unroll
               for (int u = 0; u < 4; ++u) {
-                float *v = &x[u >> 1][4 * (2 * i + p) + 2 * (u & 1)];
-                unpair(fma2(mul2(pair(v[0], v[1]), ks[p]), pair(factor[u], factor[u]), lv[p]),
-                       v[0], v[1]);
+                const int r = row0 + 8 * u + g;
+                const int seen = r < rows ? tokens_seen(a, it.q, it.rt * kItemRows + r) : 0;
+                const int limit = seen - first - 2 * c;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e)
+                    if (8 * i + e >= limit || ((i < 4 ? z0 : z1) >> (8 * (i & 3) + e) & 1))
+                      x[u >> 1][4 * i + 2 * (u & 1) + e] = -INFINITY;
               }
-          }
-          const int first = tok0 + j * kTokens + HT * half;
-          if (first + HT > all) {
+            }
+            float best[4];
+            bool raise = false;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-              const int r = row0 + 8 * u + g;
-              const int seen = r < rows ? tokens_seen(a, it.q, it.rt * kItemRows + r) : 0;
-              const int limit = seen - first - 2 * c;
+              const float *v = &x[u >> 1][2 * (u & 1)];
+              best[u] = fmaxf(v[0], v[1]);
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  if (8 * i + e >= limit) x[u >> 1][4 * i + 2 * (u & 1) + e] = -INFINITY;
+              for (int i = 1; i < 8; ++i) best[u] = max3(best[u], v[4 * i], v[4 * i + 1]);
+              raise |= best[u] > M[u] + kLazy;
             }
-          }
-          float best[4];
-          bool raise = false;
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const float *v = &x[u >> 1][2 * (u & 1)];
-            best[u] = fmaxf(v[0], v[1]);
-#pragma unroll
-            for (int i = 1; i < 8; ++i) best[u] = max3(best[u], v[4 * i], v[4 * i + 1]);
-            raise |= best[u] > M[u] + kLazy;
-          }
-          if (__any_sync(0xffffffffu, raise)) {
+            if (!__any_sync(0xffffffffu, raise)) break;
+            // A row of zeros in V adds nothing to the result, whatever its scale: it must not
+            // take the others' weights towards a half's end.  Its share is added up beside.
+            if (!opaque(again)) {
+              const uint32_t use = 2 * sc + 1;
+              if (!(ok = wait(full_bar(use % C::SLOTS), (use / C::SLOTS) & 1u))) break;
+              if (zeros(0) | zeros(1)) {
+                const int r = row0 + lane;
+                const int seen = r < rows ? tokens_seen(a, it.q, it.rt * kItemRows + r) : 0;
+#pragma unroll 1
+                for (int w = 0; w < 2; ++w)
+                  set_aside(s_tm, scales, zeros(w), HT * half + 32 * w, seen - tok0 - j * kTokens,
+                            my_factors[lane], far_top + lane, far_sum + lane);
+                __syncwarp();
+                again = true;
+                continue;
+              }
+            }
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
               float m = fmaxf(best[u], M[u]);
@@ -712,7 +741,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_store_rows16(at, o);
               }
             }
+            break;
           }
+          if (!ok) break;
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
             uint64_t top[2];
@@ -792,7 +823,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = wait(o_bar(t), o_uses & 1u))) break;
       ++o_uses;
       tc_fence_after();
-      const Total all_of = total_of(best - kShift, sum, far_top[lane], far_sum[lane], e0);
+      const Total all_of = total_of(best - kShift, sum, far_top[lane], far_sum[lane],
+                                    __float_as_int(far_top[64]));
       const float lse = all_of.lse;
       const bool mask = *poison != 0;
       const bool on = row0 + lane < rows;
@@ -920,6 +952,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t dst = base + C::kRing + slot * C::kTileBytes + (ch >> 2) * C::kBlock +
                              m % (kJobs / 2) * (kGroup * 128);
         bool found = false;
+        uint32_t some = 0;  // tokens with a code that is not 0
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
           uint32_t w[4], h[8];
@@ -927,6 +960,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                        : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                        : "r"(src + i * 512)
                        : "memory");
+          some |= (((w[0] | w[1] | w[2] | w[3]) & 0x7f7f7f7fu) != 0 ? 1u : 0u) << local(i);
           if (opaque(flags & 1u)) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) found |= Fm::clear4(w[q]);
@@ -942,6 +976,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           st_shared_v4(row + (((c0 + 1) ^ sw) << 4), h[4], h[5], h[6], h[7]);
         }
         if (found) *poison = 1;
+        if (m & (kJobs / 2)) {
+          some = __reduce_or_sync(0xffffffffu, some);
+          if (lane == 0)
+            zero_rows[slot][m % (kJobs / 2)] = static_cast<uint16_t>(~some);
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(full_bar(slot));
@@ -1101,8 +1140,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (lane == 0) {
             head[0] = static_cast<uint32_t>(e0);
-            head[1] = static_cast<uint32_t>(was_first ? 0 : rise);
-            head[2] = any;
+            head[1] = (rise > 0 && !was_first ? 1u : 0u) | (any ? 2u : 0u);
+            head[2] = static_cast<uint32_t>(rise);
           }
         }
         __syncwarp();

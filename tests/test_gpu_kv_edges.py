@@ -167,3 +167,87 @@ def test_scales_of_v_over_all_exponents(rows, tokens, prefix, scale, spread):
     # BF16's subnormals are 2^-133 apart, FP32's 2^-149
     assert close(out, ro, ob + 2.0 ** -134 + 2.0 ** -148)
     assert close(lse, rl, lb)
+
+
+def _sink(c, s, j, x, value_scale=1.0):
+    """Token j of sequence s (-1: the prefix) gets a score of about x in every row, and a
+    row of V of zeros as kv_append writes it."""
+    import torch
+    cache, D, page = c["cache"], c["D"], c["page"]
+    pages = c["prefix_table"] if s < 0 else c["table"][s]
+    p, place = int(pages[j // page]), j % page
+    u = c["u"]
+    code = (u * (448.0 / float(u.abs().max()))).to(fp8("e4m3" if c["fmt"] == "e4m3" else "e5m2"))
+    got = float((code.float() * u).sum()) * D ** -0.5
+    for h in range(c["H"]):
+        cache.k[p, h, place] = code.view(torch.uint8)
+        cache.k_scale[p, h, place] = x / got
+        cache.v[p, h, place] = torch.tensor([0, 0x80] * (D // 2), dtype=torch.uint8, device="cuda")
+        cache.v_scale[p, h, place] = value_scale
+
+
+def _with_direction(c):
+    """Queries near one direction, so that a token can have the same score in all rows."""
+    import torch
+    D = c["D"]
+    u = torch.randn(D, device="cuda").to(torch.bfloat16).float()
+    c["u"] = u
+    c["q"] = (u + 0.05 * torch.randn(c["q"].shape, device="cuda")).to(c["q"].dtype)
+    return c
+
+
+@pytest.mark.parametrize("fmt,sigma", [("e5m2", 1.0), ("e4m3", 0.05), ("e4m3", 1e-4), ("e4m3", 1e-6),
+                                       ("e5m2", 1e-12)])
+@pytest.mark.parametrize("x", [0.0, 5.0, 10.0, 20.0, 60.0])
+@pytest.mark.parametrize("rows,tokens,D,prefix,q", [
+    (1, 300, 64, 0, "bfloat16"), (2, 2000, 128, 0, "float32"), (3, 200, 256, 0, "bfloat16"),
+    (130, 400, 128, 0, "bfloat16"), (70, 300, 64, 0, "float32"), (4, 100, 64, 300, "bfloat16"),
+    (90, 100, 128, 500, "bfloat16")])
+def test_rows_of_zeros_in_v(rows, tokens, D, prefix, q, x, fmt, sigma):
+    """Tokens whose V is zero (a sink, a null key, padding), whose scale is 1 as kv_append
+    writes it, far above the others'; they take mass and no precision."""
+    import torch
+    fl = lib()
+    c = _with_direction(make((tokens,), (rows,), 2, 2, D, 16, q, fmt, prefix=prefix))
+    c["cache"].v_scale.mul_(sigma)
+    for j in (0, 1, 17, tokens - rows, tokens // 2):
+        _sink(c, 0, j, x)
+    if prefix:
+        _sink(c, -1, 0, x)
+        _sink(c, -1, prefix - 1, x / 2)
+    check(fl, c)
+
+
+@pytest.mark.parametrize("rows,D", [(1, 64), (2, 128), (90, 128), (1, 256)])
+def test_nothing_but_zeros_in_v(rows, D):
+    """All of V zero: out is 0, the logarithms are as ever."""
+    import torch
+    fl = lib()
+    c = make((700, 40), (rows, min(rows, 40)), 2, 2, D, 16)
+    c["cache"].v.fill_(0)
+    c["cache"].v_scale.copy_(torch.where(c["cache"].v_scale.isnan(), math.nan, 1.0))
+    out, _ = check(fl, c)
+    assert torch.all(out == 0)
+
+
+def test_rows_of_zeros_written_by_append():
+    """The same through kv_append, in a program's order: append, attend."""
+    import torch
+    fl = lib()
+    H, G, D, T = 2, 4, 128, 500
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for fmt, rows in (("e5m2", 1), ("e4m3", 100)):
+        cache = fl.kv_cache(-(-T // 16), H, 16, D, fmt)
+        table = torch.arange(-(-T // 16), dtype=torch.int32, device="cuda").view(1, -1)
+        offs = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+        u = torch.randn(D, generator=g, device="cuda")
+        k = torch.randn(T, H, D, generator=g, device="cuda")
+        v = 1e-3 * torch.randn(T, H, D, generator=g, device="cuda")
+        k[:4], v[:4] = 1.5 * u, 0.0
+        fl.kv_append(k, v, cache, offs, offs[1:], table)
+        q = (u + 0.1 * torch.randn(rows, H * G, D, generator=g, device="cuda")).to(torch.bfloat16)
+        c = dict(H=H, G=G, D=D, page=16, fmt=fmt, lens=[T], rows=[rows], prefix=0, table=table,
+                 prefix_table=table[0, :0], cache=cache, q=q, T=rows, kv_lens=offs[1:],
+                 offs=torch.tensor([0, rows], dtype=torch.int32, device="cuda"))
+        assert float(cache.v_scale[0, 0, 0]) == 1.0
+        check(fl, c)
