@@ -663,12 +663,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
         best = fmaxf(best, lse[w]);
       }
       // A NaN is in no maximum, but in its weight.
-      Factors weight[kWarps];
-      float sum = 0.0f;
+      float weight[kWarps], sum = 0.0f;
+      bool far = false;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        weight[w] = weight_of(lse[w] == -INFINITY ? -INFINITY : lse[w] - best);
-        sum += weight[w].f0 * weight[w].f1;
+        weight[w] = lse[w] == -INFINITY ? 0.0f : ex2(lse[w] - best);
+        sum += weight[w];
+        far |= far_below(lse[w] - best);
       }
       const float inv = sum == 0.0f ? 0.0f : rcp(sum);
       const float all_lse = sum == 0.0f ? -INFINITY : best + lg2(sum);
@@ -676,8 +677,14 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {  // 0 x NaN too: a V that is not finite
         const float *p = red + (w * kRows + r) * C::kLdO + d;
+        if (far && far_below(lse[w] - best)) {
+          const float f = ex2(0.5f * (lse[w] - best));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = fmaf(weight[w].f0 * inv, p[j] * weight[w].f1, x[j]);
+          for (int j = 0; j < 8; ++j) x[j] = fmaf(f * inv, p[j] * f, x[j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = fmaf(weight[w] * inv, p[j], x[j]);
+        }
       }
       if (d >= kc.D) continue;
       if (whole) {
@@ -719,7 +726,7 @@ constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kFewParts = 4;
 constexpr int kManyParts = 16;
-constexpr int kJoinResident = 3;  // CTAs of an SM at once
+constexpr int kJoinResident = 3;  // CTAs of an SM at once, 2 with heads above 128
 constexpr int kJoinCtasPerSm = 8;
 constexpr int kAtOnce = 4;      // parts whose loads are under way
 
@@ -745,7 +752,7 @@ __device__ __forceinline__ void load_part(const float *p, float (&y)[V]) {
 }
 
 template <int DP>
-__global__ void __launch_bounds__(kJoinThreads, kJoinResident)
+__global__ void __launch_bounds__(kJoinThreads, DP > 128 ? 2 : kJoinResident)
     kv_join_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ JoinSide few,
                    const __grid_constant__ JoinSide many) {
   constexpr int V = DP / 32;
@@ -799,7 +806,8 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinResident)
         const float lse =
             own < d.parts && r0 + row < rows ? part_lse[part(own) + row] : -INFINITY;
         float x[R][V] = {}, all_lse = -INFINITY;
-        Factors weight = {0.0f, 0.0f};
+        float weight = 0.0f, half = 1.0f;  // `half` where a part is far below
+        bool far = false;
 #pragma unroll 1
         for (int i0 = 0; i0 < d.parts; i0 += 2) {
           float y[R][2][V];
@@ -817,21 +825,30 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinResident)
             float best = lse;
             best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 1));
             best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 2));
-            weight = weight_of(lse == -INFINITY ? -INFINITY : lse - best);
-            float sum = weight.f0 * weight.f1;
+            const float w = lse == -INFINITY ? 0.0f : ex2(lse - best);
+            far = __any_sync(0xffffffffu, far_below(lse - best));
+            float sum = w;
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            weight.f0 = sum == 0.0f ? 0.0f : weight.f0 * rcp(sum);
+            weight = sum == 0.0f ? 0.0f : w * rcp(sum);
+            if (far_below(lse - best)) {
+              half = ex2(0.5f * (lse - best));
+              weight = half * rcp(sum);
+            }
             all_lse = sum == 0.0f ? -INFINITY : best + lg2(sum);
           }
 #pragma unroll
           for (int u = 0; u < R; ++u)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const float w = __shfl_sync(0xffffffffu, weight.f0, 4 * u + i0 + k);
-              const float f1 = __shfl_sync(0xffffffffu, weight.f1, 4 * u + i0 + k);
+              const float w = __shfl_sync(0xffffffffu, weight, 4 * u + i0 + k);
+              if (far) {
+                const float f = __shfl_sync(0xffffffffu, half, 4 * u + i0 + k);
 #pragma unroll
-              for (int j = 0; j < V; ++j) x[u][j] = fmaf(w, y[u][k][j] * f1, x[u][j]);
+                for (int j = 0; j < V; ++j) y[u][k][j] *= f;
+              }
+#pragma unroll
+              for (int j = 0; j < V; ++j) x[u][j] = fmaf(w, y[u][k][j], x[u][j]);
             }
         }
 #pragma unroll
@@ -865,7 +882,9 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinResident)
             // A weight to each lane, so that the parts' loads wait for nothing.
             const int n = min(32, i1 - i0);
             const float lse = lane < n ? part_lse[part(i0 + lane)] : -INFINITY;
-            const Factors mine = weight_of(lse == -INFINITY ? -INFINITY : lse - best);
+            float mine = lse == -INFINITY ? 0.0f : ex2(lse - best), half = 1.0f;
+            if (far_below(lse - best)) mine = half = ex2(0.5f * (lse - best));
+            const bool far = __any_sync(0xffffffffu, half < 1.0f);
 #pragma unroll 1
             for (int i = 0; i < n; i += kAtOnce) {
               float y[kAtOnce][V];
@@ -875,11 +894,16 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinResident)
 #pragma unroll
               for (int u = 0; u < kAtOnce; ++u) {
                 if (i + u >= n) break;
-                const float w = __shfl_sync(0xffffffffu, mine.f0, i + u);
-                const float f1 = __shfl_sync(0xffffffffu, mine.f1, i + u);
-                sum += w * f1;
+                const float w = __shfl_sync(0xffffffffu, mine, i + u);
+                float f = 1.0f;
+                if (far) {
+                  f = __shfl_sync(0xffffffffu, half, i + u);
 #pragma unroll
-                for (int j = 0; j < V; ++j) x[j] = fmaf(w, y[u][j] * f1, x[j]);
+                  for (int j = 0; j < V; ++j) y[u][j] *= f;
+                }
+                sum = fmaf(w, f, sum);
+#pragma unroll
+                for (int j = 0; j < V; ++j) x[j] = fmaf(w, y[u][j], x[j]);
               }
             }
           }

@@ -116,29 +116,27 @@ __device__ __forceinline__ void add_share(float &top, float &sum, float x, float
 struct Total {
   float lse, f0, f1;
 };
-__device__ __forceinline__ Total total_of(float top, float sum, float far_top, float far_sum,
-                                          int e0) {
-  if (far_sum == 0.0f) {
-    const bool some = sum > 0.0f || sum != sum;
-    return {some ? top + lg2(sum) : -INFINITY, some ? rcp(sum) : 0.0f, power_of_two(e0)};
-  }
+static __device__ __noinline__ Total total_with_far(float top, float sum, float far_top, float far_sum,
+                                                    int e0) {
   add_share(far_top, far_sum, top, sum);
   const float lse = far_top + lg2(far_sum);
   // top is -inf where no weight was more than 0.
   const float f = ex2(0.5f * (top - lse + static_cast<float>(e0)));
   return {lse, f, f};
 }
-
-// A part's weight 2^x, x <= 0, as a product: below 2^-126, which FP32 ends at, a part still
-// counts where its values, by V's scales, are as much larger than the others'.
-struct Factors {
-  float f0, f1;
-};
-__device__ __forceinline__ Factors weight_of(float x) {
-  const bool far = x < -100.0f;
-  const float f = ex2(far ? 0.5f * x : x);
-  return {f, far ? f : 1.0f};
+__device__ __forceinline__ Total total_of(float top, float sum, float far_top, float far_sum,
+                                          int e0) {
+  if (far_sum == 0.0f) {
+    const bool some = sum > 0.0f || sum != sum;
+    return {some ? top + lg2(sum) : -INFINITY, some ? rcp(sum) : 0.0f, power_of_two(e0)};
+  }
+  return total_with_far(top, sum, far_top, far_sum, e0);
 }
+
+// A part's weight is 2^x, x <= 0.  Below 2^-126, where FP32 ends, the part still counts if
+// its values, by V's scales, are as much larger than the others': then a half of the
+// exponent is in the weight and the other half is applied to the values first.
+__device__ __forceinline__ bool far_below(float x) { return x < -100.0f && x > -INFINITY; }
 
 // m16n8k16 with half operands.
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -229,13 +227,15 @@ __device__ __forceinline__ int row_tiles_of(const AttnArgs &a, const Seq &q) {
   return static_cast<int>((rows + BM - 1) / BM);
 }
 
-// Units of a sequence that is the other kernel's, whose row tiles have BM rows.
+// Units of a sequence that is the other kernel's, whose row tiles have BM rows; with
+// `bound`, or a few more, without the counting of a diagonal.
 template <int BM, int BN, int COST>
-__device__ __forceinline__ int64_t units_elsewhere(const AttnArgs &a, const Seq &q) {
+__device__ __forceinline__ int64_t units_elsewhere(const AttnArgs &a, const Seq &q, bool bound) {
   const int64_t rows = static_cast<int64_t>(q.n) * a.G;
   if (rows <= 0 || (rows >= a.row_lo && rows <= a.row_hi)) return 0;
   const int rts = static_cast<int>((rows + BM - 1) / BM);
-  return a.cache.heads * units_below<BM, BN, COST>(a, q, rts, rts);
+  return a.cache.heads * (bound ? static_cast<int64_t>(rts) * (q.len / BN + 1 + COST)
+                                : units_below<BM, BN, COST>(a, q, rts, rts));
 }
 
 // Units of the prefix's pass, of `tokens` tokens.
@@ -275,6 +275,8 @@ __device__ __noinline__ void share_out(const AttnArgs &a, Share *sh, int64_t *wa
   const int H = a.cache.heads;
   const int s0 = min(S, static_cast<int>(threadIdx.x) * per), s1 = min(S, s0 + per);
   constexpr bool kMany = BM == kManyItemRows;
+  constexpr int kOtherRows = kMany ? kFewItemRows : kManyItemRows;
+  constexpr int kOtherCost = kMany ? kFewItemCost : kManyItemCost;
   int64_t sum = 0, elsewhere = 0;
   bool bad = false;
   if (a.prefix_len) {
@@ -291,8 +293,7 @@ __device__ __noinline__ void share_out(const AttnArgs &a, Share *sh, int64_t *wa
     const int rts = off ? 0 : row_tiles_of<BM>(a, q);
     if (rts > 0) sum += H * units_below<BM, BN, COST>(a, q, rts, rts);
     else if (a.both && !off)
-      elsewhere += units_elsewhere<kMany ? kFewItemRows : kManyItemRows, BN,
-                                   kMany ? kFewItemCost : kManyItemCost>(a, q);
+      elsewhere += units_elsewhere<kOtherRows, BN, kOtherCost>(a, q, true);
   }
   bad = __syncthreads_or(bad);
   if (bad) {
@@ -310,9 +311,15 @@ __device__ __noinline__ void share_out(const AttnArgs &a, Share *sh, int64_t *wa
     const int64_t o = shfl_up64(run, d);
     if (lane >= d) run += o;
   }
-  if (a.both) {
+  if (a.both && __syncthreads_or(elsewhere > INT32_MAX / THREADS)) {  // that may be too much
+    elsewhere = 0;
+#pragma unroll 1
+    for (int s = s0; s < s1; ++s)
+      elsewhere += units_elsewhere<kOtherRows, BN, kOtherCost>(a, load_seq(a, s), false);
 #pragma unroll 1
     for (int d = 16; d > 0; d >>= 1) elsewhere += __shfl_xor_sync(0xffffffffu, elsewhere, d);
+  } else {
+    elsewhere = 0;
   }
   if (lane == 31) {
     warp_sums[warp] = run;
@@ -444,23 +451,24 @@ __device__ __noinline__ bool next_item(const AttnArgs &a, Walk *w, Item *it) {
 
 // Where and how much a joined row weighs: own result and the prefix's.
 struct Weights {
-  Factors own, pre;
-  float lse;  // base 2, of both
+  float own, pre, lse;  // lse: base 2, of both
+  float far;            // less than 1: applied first to the side that far_below is about
 };
 __device__ __forceinline__ Weights weigh(const AttnArgs &a, int64_t t, int hq, float lse) {
-  if (!a.pre_lse) return {{1.0f, 1.0f}, {0.0f, 0.0f}, lse};
+  if (!a.pre_lse) return {1.0f, 0.0f, lse, 1.0f};
   const float p = a.pre_lse[t * a.Hq + hq];
   // A maximum drops a NaN, which the weights and the logarithm are to keep.
-  if (lse == -INFINITY && p == -INFINITY) return {{0.0f, 0.0f}, {0.0f, 0.0f}, -INFINITY};
+  if (lse == -INFINITY && p == -INFINITY) return {0.0f, 0.0f, -INFINITY, 1.0f};
   const float top = fmaxf(lse, p);
-  Factors x = weight_of(lse - top), y = weight_of(p - top);
-  const float sum = x.f0 * x.f1 + y.f0 * y.f1, inv = rcp(sum);
-  x.f0 *= inv;
-  y.f0 *= inv;
-  return {x, y, top + lg2(sum)};
+  float x = ex2(lse - top), y = ex2(p - top), far = 1.0f;
+  const float inv = rcp(x + y), all = top + lg2(x + y);
+  if (far_below(lse - top)) x = far = ex2(0.5f * (lse - top));
+  if (far_below(p - top)) y = far = ex2(0.5f * (p - top));
+  return {x * inv, y * inv, all, far};
 }
 __device__ __forceinline__ float joined(const Weights &w, float own, float pre) {
-  return own * w.own.f1 * w.own.f0 + pre * w.pre.f1 * w.pre.f0;
+  if (w.far < 1.0f) (w.own < w.pre ? own : pre) *= w.far;
+  return own * w.own + pre * w.pre;
 }
 
 // Writes N consecutive elements of a row's result, own ones in o, and where `d` is 0

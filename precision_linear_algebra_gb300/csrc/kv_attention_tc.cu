@@ -77,7 +77,8 @@ struct Cfg {
   static constexpr int kPlaces = kRaw + kConverters * AHEAD * kJob;
   static constexpr int kScales = kPlaces + kScaleBufs * kTokens * 8;
   static constexpr int kFactors = kScales + kScaleBufs * kScaleBytes;
-  static constexpr int kBar = kFactors + kItemRows * 4;
+  static constexpr int kFirst = kFactors + kItemRows * 4;  // 16 codes of each row of V, two tiles
+  static constexpr int kBar = kFirst + 2 * kTokens * 16;
   static constexpr int kBars = 2 * SLOTS + 4 * kScaleBufs + 14 + 2 * kItemBufs;
   static constexpr int kMisc = kBar + kBars * 8;
   static constexpr int kAlloc = kMisc + 16 + 1024;
@@ -396,28 +397,61 @@ __device__ __forceinline__ int scale_place(int col) {
   return (col & ~15) + ((col >> 1) & 3) * 4 + ((col >> 3) & 1) * 2 + (col & 1);
 }
 
-// Adds up beside the shares of the columns in `mask`, 32 from `col` on, of a warp's rows, one
-// a lane, which sees `limit` columns.  The scores are read again, from `scores` on: this is
-// done before weights take their place.
-__device__ __noinline__ void set_aside(uint32_t scores, uint32_t k_scales, uint32_t mask, int col,
+// Adds up beside the shares of the columns whose bits are set in `masks`, of a warp's rows,
+// one a lane, which sees `limit` columns.  The scores are read again, from `scores` on,
+// eight columns at a time: this is done before weights take their place.
+__device__ __noinline__ void set_aside(uint32_t scores, uint32_t k_scales, const uint8_t *masks,
                                        int limit, float factor, float *far_top, float *far_sum) {
   float top = *far_top, sum = *far_sum;
 #pragma unroll 1
-  for (; mask; mask &= mask - 1) {
-    const int j = col + __ffs(mask) - 1;
-    float x, ks;
+  for (int j = 0; j < kTokens; j += 8) {
+    const uint32_t mask = masks[j / 8];
+    if (mask == 0) continue;
+    float x[8], best = -INFINITY;
     __syncwarp();
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
-        : "=f"(x)
+        : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]),
+          "=f"(x[7])
         : "r"(scores + j)
         : "memory");
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ks) : "r"(k_scales + 4 * scale_place(j)) : "memory");
-    if (j < limit) add_share(top, sum, x * ks * factor, 1.0f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float ks;
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ks) : "r"(k_scales + 4 * scale_place(j + i))
+                   : "memory");
+      x[i] = (mask >> i & 1) && j + i < limit ? x[i] * ks * factor : -INFINITY;
+      best = fmaxf(best, x[i]);
+    }
+    const float from = best == -INFINITY ? 0.0f : best;
+    float part = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) part += ex2(x[i] - from);
+    add_share(top, sum, best, part);
   }
   *far_top = top;
   *far_sum = sum;
+}
+
+// Which of the tokens whose places are `places` and 32, 64, 96 further, if their bits are set
+// in `which`, have rows of zeros in V.  Where there is no token it is of no account.
+__device__ __noinline__ uint32_t rows_of_zeros(const Cache &c, uint32_t places, uint32_t which) {
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    int64_t at;
+    asm volatile("ld.shared.b64 %0, [%1];" : "=l"(at) : "r"(places + 32 * i * 8) : "memory");
+    if (!(which >> i & 1) || at < 0) continue;
+    const uint8_t *row = c.v + (at & ~1ll);
+    uint32_t some = 0;
+    for (int d = 16; d < c.D && (some & 0x7f7f7f7fu) == 0; d += 16) {
+      const uint4 w = *reinterpret_cast<const uint4 *>(row + d);
+      some |= w.x | w.y | w.z | w.w;
+    }
+    if (some & 0x7f7f7f7fu) which &= ~(1u << i);
+  }
+  __syncwarp();
+  return which;
 }
 
 // Columns k .. k+15 of V that hold a code that is not finite at a token that a row sees,
@@ -489,7 +523,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ float row_stats[8][64];
   // Of a warp's rows: the maximum and the sum of add_share; what V's scales are relative to.
   __shared__ float beside[8][65];
-  __shared__ uint16_t zero_rows[C::SLOTS][kTokens / kGroup];  // a bit for each row of V
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::SLOTS; ++i) {
       mbar_init(full_bar(i), kTokens / kGroup);
@@ -602,12 +635,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         const uint32_t scales = base + C::kScales + buf * kScaleBytes;
-        if (!(ok = wait(s_bar(t), tiles & 1u))) break;
-        tc_fence_after();
         const int *const head = reinterpret_cast<const int *>(
             sbase + C::kScales + buf * kScaleBytes + kTileHead);
         if (j == 0) far_top[64] = __int_as_float(head[0]);
         const int apart = head[1];
+        if (!(ok = wait(s_bar(t), tiles & 1u))) break;
+        tc_fence_after();
         if (opaque(apart & 1)) {
           const int rise = head[2];
           far_top[64] = __int_as_float(head[0]);
@@ -632,10 +665,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (opaque(apart & 2)) {
           const int r = row0 + lane;
           const int seen = r < rows ? tokens_seen(a, it.q, it.rt * kItemRows + r) : 0;
-#pragma unroll 1
-          for (int i = 0; i < kTokens / 32; ++i)
-            set_aside(s_tm, scales, head[4 + i], 32 * i, seen - tok0 - j * kTokens, my_factors[lane],
-                      far_top + lane, far_sum + lane);
+          set_aside(s_tm, scales, reinterpret_cast<const uint8_t *>(head + 4),
+                    seen - tok0 - j * kTokens, my_factors[lane], far_top + lane, far_sum + lane);
           __syncwarp();
         }
         // The last scores of these rows are made: the next rows may take their place.
@@ -645,77 +676,49 @@ __global__ void __launch_bounds__(kThreads, 1)
           constexpr int HT = kTokens / 2;
           const uint32_t hs = scales + 4 * HT * half + 16 * c;
           float x[2][32];
-          const int first = tok0 + j * kTokens + HT * half;
-          bool again = false;  // rows of zeros have been taken out
-#pragma unroll 1
-          for (;;) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b) tmem_load_rows(s_tm + HT * half + b * kLanes16, x[b]);
-            tmem_wait32(x[0]);
-            tmem_wait32(x[1]);
+          for (int b = 0; b < 2; ++b) tmem_load_rows(s_tm + HT * half + b * kLanes16, x[b]);
+          tmem_wait32(x[0]);
+          tmem_wait32(x[1]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint64_t ks[2], lv[2];
-              lds_pairs(hs + 64 * i, ks[0], ks[1]);
-              lds_pairs(hs + 4 * kTokens + 64 * i, lv[0], lv[1]);
+          for (int i = 0; i < 4; ++i) {
+            uint64_t ks[2], lv[2];
+            lds_pairs(hs + 64 * i, ks[0], ks[1]);
+            lds_pairs(hs + 4 * kTokens + 64 * i, lv[0], lv[1]);
 #pragma unroll
-              for (int p = 0; p < 2; ++p)
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                  float *v = &x[u >> 1][4 * (2 * i + p) + 2 * (u & 1)];
-                  unpair(fma2(mul2(pair(v[0], v[1]), ks[p]), pair(factor[u], factor[u]), lv[p]),
-                         v[0], v[1]);
-                }
-            }
-            // The half's rows of zeros in V, but for those that are set aside anyway.
-            auto zeros = [&](int w) {
-              const uint16_t *z = &zero_rows[(2 * sc + 1) % C::SLOTS][4 * half + 2 * w];
-              return (z[0] | static_cast<uint32_t>(z[1]) << 16) &
-                     ~(head[1] & 2 ? head[4 + 2 * half + w] : 0);
-            };
-            if (first + HT > all || opaque(again)) {
-              const uint32_t z0 = again ? zeros(0) >> 2 * c : 0, z1 = again ? zeros(1) >> 2 * c : 0;
+            for (int p = 0; p < 2; ++p)
 #pragma unroll
               for (int u = 0; u < 4; ++u) {
-                const int r = row0 + 8 * u + g;
-                const int seen = r < rows ? tokens_seen(a, it.q, it.rt * kItemRows + r) : 0;
-                const int limit = seen - first - 2 * c;
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-#pragma unroll
-                  for (int e = 0; e < 2; ++e)
-                    if (8 * i + e >= limit || ((i < 4 ? z0 : z1) >> (8 * (i & 3) + e) & 1))
-                      x[u >> 1][4 * i + 2 * (u & 1) + e] = -INFINITY;
+                float *v = &x[u >> 1][4 * (2 * i + p) + 2 * (u & 1)];
+                unpair(fma2(mul2(pair(v[0], v[1]), ks[p]), pair(factor[u], factor[u]), lv[p]),
+                       v[0], v[1]);
               }
-            }
-            float best[4];
-            bool raise = false;
+          }
+          const int first = tok0 + j * kTokens + HT * half;
+          if (first + HT > all) {
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-              const float *v = &x[u >> 1][2 * (u & 1)];
-              best[u] = fmaxf(v[0], v[1]);
+              const int r = row0 + 8 * u + g;
+              const int seen = r < rows ? tokens_seen(a, it.q, it.rt * kItemRows + r) : 0;
+              const int limit = seen - first - 2 * c;
 #pragma unroll
-              for (int i = 1; i < 8; ++i) best[u] = max3(best[u], v[4 * i], v[4 * i + 1]);
-              raise |= best[u] > M[u] + kLazy;
+              for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (8 * i + e >= limit) x[u >> 1][4 * i + 2 * (u & 1) + e] = -INFINITY;
             }
-            if (!__any_sync(0xffffffffu, raise)) break;
-            // A row of zeros in V adds nothing to the result, whatever its scale: it must not
-            // take the others' weights towards a half's end.  Its share is added up beside.
-            if (!opaque(again)) {
-              const uint32_t use = 2 * sc + 1;
-              if (!(ok = wait(full_bar(use % C::SLOTS), (use / C::SLOTS) & 1u))) break;
-              if (zeros(0) | zeros(1)) {
-                const int r = row0 + lane;
-                const int seen = r < rows ? tokens_seen(a, it.q, it.rt * kItemRows + r) : 0;
-#pragma unroll 1
-                for (int w = 0; w < 2; ++w)
-                  set_aside(s_tm, scales, zeros(w), HT * half + 32 * w, seen - tok0 - j * kTokens,
-                            my_factors[lane], far_top + lane, far_sum + lane);
-                __syncwarp();
-                again = true;
-                continue;
-              }
-            }
+          }
+          float best[4];
+          bool raise = false;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float *v = &x[u >> 1][2 * (u & 1)];
+            best[u] = fmaxf(v[0], v[1]);
+#pragma unroll
+            for (int i = 1; i < 8; ++i) best[u] = max3(best[u], v[4 * i], v[4 * i + 1]);
+            raise |= best[u] > M[u] + kLazy;
+          }
+          if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
               float m = fmaxf(best[u], M[u]);
@@ -741,9 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_store_rows16(at, o);
               }
             }
-            break;
           }
-          if (!ok) break;
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
             uint64_t top[2];
@@ -834,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int hq = it.h * a.G + r - tok * a.G;
       const int64_t place = out_row * a.Hq + hq;
       const int64_t part = (2 * static_cast<int64_t>(blockIdx.x) + (it.tile0 > 0 ? 0 : 1)) * kItemRows + t * kRows + row;
-      Weights weights = {{1.0f, 1.0f}, {0.0f, 0.0f}, lse};
+      Weights weights = {1.0f, 0.0f, lse, 1.0f};
       const float *pre = nullptr;
       if (whole && !a.raw_o && on) {
         weights = weigh(a, out_row, hq, lse);
@@ -952,7 +953,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t dst = base + C::kRing + slot * C::kTileBytes + (ch >> 2) * C::kBlock +
                              m % (kJobs / 2) * (kGroup * 128);
         bool found = false;
-        uint32_t some = 0;  // tokens with a code that is not 0
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
           uint32_t w[4], h[8];
@@ -960,7 +960,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                        : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                        : "r"(src + i * 512)
                        : "memory");
-          some |= (((w[0] | w[1] | w[2] | w[3]) & 0x7f7f7f7fu) != 0 ? 1u : 0u) << local(i);
           if (opaque(flags & 1u)) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) found |= Fm::clear4(w[q]);
@@ -976,11 +975,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           st_shared_v4(row + (((c0 + 1) ^ sw) << 4), h[4], h[5], h[6], h[7]);
         }
         if (found) *poison = 1;
-        if (m & (kJobs / 2)) {
-          some = __reduce_or_sync(0xffffffffu, some);
-          if (lane == 0)
-            zero_rows[slot][m % (kJobs / 2)] = static_cast<uint16_t>(~some);
-        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(full_bar(slot));
@@ -1035,6 +1029,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (in && !good) atomicOr(a.rows.status, kStatusBadDeviceArg);
           const uint64_t pl = tk - divide(tk, c.page) * c.page_size;
           const uint32_t dst = scales_of(step) + 4 * (scale_at + 32 * i + (opaque(is_v) ? kTokens : 0));
+          if (opaque(is_v)) {
+            const uint64_t at = (static_cast<uint64_t>(p) * page16 + pl * token16 +
+                                 static_cast<uint64_t>(h) * head16) * 16;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                             base + C::kFirst + ((step & 1) * kTokens + lane + 32 * i) * 16),
+                         "l"(c.v + (good ? at : 0)), "r"(good ? 16 : 0)
+                         : "memory");
+          }
           if (good)
             copy4(dst, scales_from + static_cast<uint64_t>(p) * s_page + pl * s_token +
                            static_cast<uint64_t>(h) * s_head);
@@ -1106,31 +1108,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (opaque(is_v)) {
           // Relative to a power of two near the scale of the item's first token.
           if (was_first) e0 = min(exponent_of(out[kTokens]), 126);
-          int top = -126;
-#pragma unroll 1
+          // A row of zeros in V adds nothing to the result, whatever its scale: it must not
+          // take the others' weights towards a half's end, and so gets none.  Nearly all have
+          // another code among the first 16.
+          float scale[4];
+          uint32_t zeros = 0;  // a bit for each of the lane's tokens
+          int top = 0;         // positive numbers are in the order of their bits
+#pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float v = out[kTokens + 32 * i + scale_at];
-            if (v > 0.0f && v < INFINITY) top = max(top, min(exponent_of(v), 126));
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(base + C::kFirst + (((step - 1) & 1) * kTokens + lane + 32 * i) * 16)
+                         : "memory");
+            scale[i] = out[kTokens + 32 * i + scale_at];
+            if (((w[0] | w[1] | w[2] | w[3]) & 0x7f7f7f7fu) == 0) zeros |= 1u << i;
+            if (scale[i] < INFINITY) top = max(top, __float_as_int(scale[i]));
           }
-          top = __reduce_max_sync(0xffffffffu, top);
+          if (__any_sync(0xffffffffu, zeros != 0)) {
+            const int buf = (step - 1) % kScaleBufs;
+            if (!(ok = wait(atfull_bar(buf), ((step - 1) / kScaleBufs) & 1u))) break;
+            zeros = rows_of_zeros(a.cache, base + C::kPlaces + (buf * kTokens + lane) * 8, zeros);
+          }
+          top = min(exponent_of(__int_as_float(__reduce_max_sync(0xffffffffu, top))), 126);
           const int rise = top > e0 + kSpan ? top - e0 : 0;
           e0 += rise;
           const float down = power_of_two(-e0);
           uint32_t any = 0;
           uint32_t *const head = reinterpret_cast<uint32_t *>(out) + kTileHead / 4;
-#pragma unroll 1
+#pragma unroll
           for (int i = 0; i < 4; ++i) {
             float *at = out + kTokens + 32 * i + scale_at;
-            const float scale = *at, v = scale * down;
-            const bool fine = scale > 0.0f && scale < INFINITY;
-            const bool less = fine && exponent_of(scale) < e0 - kSpan;
+            const float v = scale[i] * down;
+            const bool fine = scale[i] > 0.0f && scale[i] < INFINITY;
+            const bool zero = zeros >> i & 1;
+            const bool less = fine && (zero || exponent_of(scale[i]) < e0 - kSpan);
             const uint32_t far = __ballot_sync(0xffffffffu, less);
             any |= far;
             float lg, inv;
             asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg) : "f"(v));
             asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(v));
             if (less) {
-              lg = log2_far(scale, e0);
+              lg = zero ? -INFINITY : log2_far(scale[i], e0);
               inv = 0.0f;
             }
             at[0] = fine ? lg : NAN;
