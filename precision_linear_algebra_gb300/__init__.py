@@ -458,17 +458,31 @@ def grouped_gemm(m_offsets, A, B, scale_a, scale_b, C=None):
 
 # The calls below run in the microseconds of a decoding step, so they look at
 # each tensor's shape and strides once and pass them straight to the library.
-# A tensor of the host is refused here: its pointer would reach a kernel.
+# A tensor of the host, or of another device than the one that the launch goes to, is
+# refused here: its pointer would reach a kernel.
+_current_device = None
+
+
+def _here(t):
+    """Whether a tensor is on the current device."""
+    global _current_device
+    if _current_device is None:
+        import torch
+        _current_device = torch._C._cuda_getDevice
+    dev = t.get_device()  # -1: the host
+    return dev >= 0 and dev == _current_device()
+
+
 def _rows(t, rows, cols, dtype=None):
     """Row stride of a CUDA [rows][cols] tensor whose rows are contiguous."""
-    assert t.is_cuda and t.shape == (rows, cols) and (dtype is None or t.dtype is dtype)
+    assert _here(t) and t.shape == (rows, cols) and (dtype is None or t.dtype is dtype)
     s0, s1 = t.stride()
     assert s1 == 1 or cols == 1
     return s0 if rows > 1 else max(cols, 1)
 
 
 def _dense(t, shape, dtype):
-    assert t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+    assert _here(t) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
 
 
 def _type(t):
@@ -488,7 +502,7 @@ def _workspace(workspace, need, device):
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
         return workspace.data_ptr(), need, workspace
-    assert workspace.is_cuda and workspace.is_contiguous()
+    assert _here(workspace) and workspace.is_contiguous()
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
@@ -549,7 +563,7 @@ def moe_layer(x, ids, weights, w13, scale13, w2, scale2, y=None, workspace=None,
     top_k = ids.shape[1]
     assert w13.shape == (E, 2 * F, D) and w2.shape[1] == D
     assert w13.dtype is torch.uint8 and w2.dtype is torch.uint8
-    assert w13.is_cuda and w2.is_cuda
+    assert _here(w13) and _here(w2)
     e13, ld13, one13 = w13.stride()
     e2, ld2, one2 = w2.stride()
     assert (one13 == 1 or D == 1) and (one2 == 1 or F == 1)
@@ -575,7 +589,7 @@ def _adapters(A, B, alpha, m_offsets, adapter_ids, N):
     import torch
     n, R, K = A.shape
     assert A.dtype is torch.bfloat16 and B.dtype is torch.bfloat16 and B.shape == (n, R, N)
-    assert A.is_cuda and B.is_cuda
+    assert _here(A) and _here(B)
     sa, lda, onea = A.stride()
     sb, ldb, oneb = B.stride()
     assert (onea == 1 or K == 1) and (oneb == 1 or N == 1)
@@ -678,6 +692,9 @@ class KVCache:
             _FORMATS[fmt], st[0], st[1], st[2], sst[0], sst[1], sst[2])
         self.ref = ctypes.addressof(self.struct)
 
+    def get_device(self):
+        return self.device
+
 
 def kv_cache(num_pages, kv_heads, page_size, head_dim, fmt="e4m3", device="cuda"):
     """A KVCache of zeros."""
@@ -700,17 +717,10 @@ def _sequences(m_offsets, kv_lens, page_table):
 
 def _heads(t, shape, dtype=None):
     """Row and head strides of a CUDA [rows][heads][D] tensor, D contiguous."""
-    assert t.is_cuda and t.shape == shape and (dtype is None or t.dtype is dtype)
+    assert _here(t) and t.shape == shape and (dtype is None or t.dtype is dtype)
     s0, s1, s2 = t.stride()
     assert s2 == 1
     return s0, s1
-
-
-def _on_current_device(t, cache):
-    """A launch goes to the current device, whose memory the pointers have to be of."""
-    import torch
-    dev = t.get_device()
-    assert dev == cache.device == torch._C._cuda_getDevice()
 
 
 def kv_append(k, v, cache, m_offsets, kv_lens, page_table):
@@ -723,7 +733,7 @@ def kv_append(k, v, cache, m_offsets, kv_lens, page_table):
     """
     T = k.shape[0]
     _, H, _, D = cache.shape
-    _on_current_device(k, cache)
+    assert _here(cache)
     ldk, ldkh = _heads(k, (T, H, D))
     ldv, ldvh = _heads(v, (T, H, D), k.dtype)
     S, po, pl, pt, ldt, pages = _sequences(m_offsets, kv_lens, page_table)
@@ -745,7 +755,7 @@ def kv_read(cache, m_offsets, kv_lens, page_table, rows, dtype=None, k=None, v=N
         k = torch.empty((rows, H, D), dtype=dtype, device=dev)
     if v is None:
         v = torch.empty((rows, H, D), dtype=dtype, device=dev)
-    _on_current_device(k, cache)
+    assert _here(cache)
     ldk, ldkh = _heads(k, (rows, H, D), dtype)
     ldv, ldvh = _heads(v, (rows, H, D), dtype)
     S, po, pl, pt, ldt, pages = _sequences(m_offsets, kv_lens, page_table)
@@ -772,7 +782,7 @@ def kv_attention(q, cache, m_offsets, kv_lens, page_table, max_rows=None, scale=
     import torch
     T, Hq, D = q.shape
     dev = q.device
-    _on_current_device(q, cache)
+    assert _here(cache)
     ldq, ldqh = _heads(q, (T, Hq, cache.shape[3]))
     if out is None:
         out, ldo, ldoh = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev), Hq * D, D
