@@ -536,23 +536,13 @@ static_assert(PairSmem::kB % 1024 == 0 && PairSmem::kABytes % 1024 == 0 &&
               "pair layout");
 static_assert(PairSmem::kAlloc <= 227 * 1024, "shared memory");
 
-// QUAD (per-tensor GEMM only): clusters of four CTAs, two CTA pairs that
-// compute horizontally adjacent 256 x 256 tiles (one 256 x 512 cluster tile)
-// and so need the same rows of A.  Each CTA loads 64 of the 128 A rows its
-// pair position needs and multicasts them to itself and to the CTA at the
-// same position in the other pair, which loads the other 64: every A byte
-// leaves L2 once per cluster instead of once per pair.  A stage is refilled
-// only after both pairs' MMAs have finished with it (each pair's commit
-// arrives on the stage's empty barrier in all four CTAs).
-template <bool GROUPED, bool QUAD = false>
+template <bool GROUPED>
 __global__ void __launch_bounds__(P_THREADS, 1)
     gemm_e4m3_pair_kernel(const __grid_constant__ CUtensorMap tmA,
                           const __grid_constant__ CUtensorMap tmB,
                           const __grid_constant__ CUtensorMap tmB64,
                           const __grid_constant__ CUtensorMap tmC,
-                          const __grid_constant__ CUtensorMap tmA64,
                           const GemmArgs a) {
-  static_assert(!(GROUPED && QUAD), "clusters of four: per-tensor GEMM only");
   using L = PairSmem;
   constexpr int STAGES = P_STAGES;
   extern __shared__ uint8_t smem_raw[];
@@ -567,7 +557,6 @@ __global__ void __launch_bounds__(P_THREADS, 1)
   // stream serialization).
   if (GROUPED) pdl_wait();
   const uint32_t rank = cluster_ctarank();
-  const uint32_t pair = QUAD ? rank >> 1 : 0;      // which CTA pair
   const uint32_t prank = rank & 1u;                // position in the pair
   const uint32_t lrank = rank & ~1u;               // this pair's leader
   const bool leader = prank == 0;
@@ -584,17 +573,15 @@ __global__ void __launch_bounds__(P_THREADS, 1)
   int32_t *pref = reinterpret_cast<int32_t *>(sbase + L::kPrefix);
   __shared__ int32_t offs_smem[GROUPED ? kMaxGroups + 1 : 1];
 
-  // Column tiles of the work items: 256 per pair, 512 per cluster of four.
-  constexpr int kCBN = QUAD ? 2 * P_BN : P_BN;
-  const int tiles_n = (a.N + kCBN - 1) / kCBN;
+  const int tiles_n = (a.N + P_BN - 1) / P_BN;
   const int nkb = (a.K + BK - 1) / BK;
-  const int cluster_id = QUAD ? blockIdx.x >> 2 : blockIdx.x >> 1;
-  const int num_clusters = QUAD ? gridDim.x >> 2 : gridDim.x >> 1;
+  const int cluster_id = blockIdx.x >> 1;
+  const int num_clusters = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(full_bar(s), 1);
-      mbar_init(empty_bar(s), QUAD ? 2 : 1);   // one commit per pair
+      mbar_init(empty_bar(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull_bar(b), 1);
@@ -605,7 +592,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     fence_mbar_init();
   }
   if (warp == 4 && lane == 0) {
-    tma_prefetch_desc(QUAD ? &tmA64 : &tmA);
+    tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
     if (a.split_tail > 0) tma_prefetch_desc(&tmB64);
   }
@@ -639,14 +626,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
       t = n_whole + ((i - n_whole) >> 1);
       half = (i - n_whole) & 1;
     }
-    TileInfo ti = tile_info<GROUPED, P_BM>(t, a, tiles_n, pref, offs_smem, kCBN);
-    // A cluster of four splits its 512 columns between the pairs: 256 each
-    // for a whole tile, 128 each for a half (half h covers 256 h .. +255).
-    if (QUAD)
-      ti.n0 += half < 0 ? 256 * static_cast<int>(pair)
-                        : 256 * half + 128 * static_cast<int>(pair);
-    else if (half >= 0)
-      ti.n0 += 128 * half;
+    TileInfo ti = tile_info<GROUPED, P_BM>(t, a, tiles_n, pref, offs_smem, P_BN);
+    if (half >= 0) ti.n0 += 128 * half;
     return ti;
   };
 
@@ -682,15 +663,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                                                  : L::kA + s * L::kABytes);
             const uint32_t bslot = base + (ti.tn ? L::kA + s * L::kABytes
                                                  : L::kB + s * L::kBBytes);
-            if (QUAD)
-              // This CTA's 64-row half of its A rows, to itself and to the
-              // CTA at the same position in the other pair.
-              tma_load_2d_pair_mc(aslot + 8192u * pair, &tmA64, lf, kb * BK,
-                                  arow + 64 * static_cast<int>(pair),
-                                  static_cast<uint16_t>((1u << rank) |
-                                                        (1u << (rank ^ 2u))));
-            else
-              tma_load_2d_pair(aslot, &tmA, lf, kb * BK, arow);
+            tma_load_2d_pair(aslot, &tmA, lf, kb * BK, arow);
             if (GROUPED)
               tma_load_3d_pair(bslot, &tmB, lf, kb * BK, brow, ti.group);
             else
@@ -752,12 +725,12 @@ __global__ void __launch_bounds__(P_THREADS, 1)
           for (int k = 0; k < BK / UMMA_K; ++k)
             umma_f8f6f4_pair_warp(d_tmem, adesc + 2u * k, bdesc + 2u * k,
                                   idesc, (kb | k) != 0 ? 1u : 0u);
-          umma_commit_pair_warp(empty_bar(s), QUAD ? 0xF : 0x3);
+          umma_commit_pair_warp(empty_bar(s), 0x3);
           if (++s == STAGES) { s = 0; ph ^= 1u; }
         }
         if (!ok) break;
         umma_commit_pair_warp(tfull_bar(buf),
-                              static_cast<uint16_t>(0x3u << (2u * pair)));
+                              0x3);
       }
       umma_commit_pair_warp(final_bar, static_cast<uint16_t>(1u << rank));
       mbar_wait_drain(final_bar, 0, a.timeout_ns, a.status);
@@ -984,18 +957,16 @@ bool encode_c(CUtensorMap *m, const uint16_t *C, int64_t ldc, int64_t rows,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Launch the CTA-pair kernel on clusters of two CTAs (QUAD: four, two
-// pairs), as many clusters as can be resident at once (at most one per work
-// tile: a pair tile, or for QUAD a 256 x 512 cluster tile).
-template <bool GROUPED, bool QUAD = false>
+// Launch the CTA-pair kernel on clusters of two CTAs, as many clusters as can
+// be resident at once (at most one per work tile).
+template <bool GROUPED>
 fp8la_status launch_gemm_pair(const CUtensorMap &tmA, const CUtensorMap &tmB,
                               const CUtensorMap &tmB64, const CUtensorMap &tmC,
-                              const CUtensorMap &tmA64, GemmArgs args,
-                              int64_t max_tiles, cudaStream_t s) {
+                              GemmArgs args, int64_t max_tiles, cudaStream_t s) {
   using L = PairSmem;
-  auto kern = gemm_e4m3_pair_kernel<GROUPED, QUAD>;
-  constexpr int kCluster = QUAD ? 4 : 2;
-  const int slot = QUAD ? 6 : (GROUPED ? 3 : 2);
+  auto kern = gemm_e4m3_pair_kernel<GROUPED>;
+  constexpr int kCluster = 2;
+  const int slot = GROUPED ? 3 : 2;
   if (once_per_device(slot, [&] {
         return cudaFuncSetAttribute(
             kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
@@ -1038,15 +1009,15 @@ fp8la_status launch_gemm_pair(const CUtensorMap &tmA, const CUtensorMap &tmB,
   attrs[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attrs;
   cfg.numAttrs = GROUPED ? 1 : 2;
-  if (cudaLaunchKernelEx(&cfg, kern, tmA, tmB, tmB64, tmC, tmA64, args) !=
+  if (cudaLaunchKernelEx(&cfg, kern, tmA, tmB, tmB64, tmC, args) !=
       cudaSuccess)
     return FP8LA_ERR_CUDA;
   return launch_status();
 }
 
 // Kernel choice: 0 = by shape, 1 = single-CTA kernel (128 x 256 tiles),
-// 2 = CTA-pair kernel, 3 = single-CTA kernel with 128 x 128 tiles, 4 = two
-// CTA pairs per cluster sharing A by multicast.
+// 2 = CTA-pair kernel, 3 = single-CTA kernel with 128 x 128 tiles, 4 = as 2
+// for fp8_gemm.
 std::atomic<int> g_variant{0};
 
 fp8la_status check_operands(const uint8_t *A, int64_t lda, const uint8_t *B,
@@ -1088,19 +1059,17 @@ fp8la_status gemm_pertensor_impl(const uint8_t *A, int64_t lda,
   // three quarters of the SMs idle (then 128 x 128 single-CTA tiles), or the
   // caller asked otherwise.  The diagnostic path uses the single-CTA 128 x 256
   // kernel (withhold == 1) or the CTA-pair kernel (withhold == 2).
-  const int v = g_variant.load();
+  const int v = g_variant.load() == 4 ? 2 : g_variant.load();
   const int sms = sm_count();
   const int64_t pair_tiles = ((M + P_BM - 1) / P_BM) * ((N + P_BN - 1) / P_BN);
   const bool small = !withhold &&
                      (v == 3 || (v == 0 && sms > 0 && pair_tiles * 4 < sms));
-  const bool quad = !withhold && !small && v == 4;
-  const bool pair = withhold == 2 || quad ||
+  const bool pair = withhold == 2 ||
                     (!withhold && !small && (v == 2 || (v == 0 && M > BM)));
-  CUtensorMap tmA, tmB, tmB64, tmA64{};
+  CUtensorMap tmA, tmB, tmB64;
   if (!encode_2d(&tmA, A, K, M, lda, BK, BM) ||
       !encode_2d(&tmB, B, K, N, ldb, BK, pair || small ? 128 : kBN) ||
-      (pair && !encode_2d(&tmB64, B, K, N, ldb, BK, 64)) ||
-      (quad && !encode_2d(&tmA64, A, K, M, lda, BK, 64)))
+      (pair && !encode_2d(&tmB64, B, K, N, ldb, BK, 64)))
     return FP8LA_ERR_CUDA;
   unsigned *status = status_word_ptr();
   if (!status) return FP8LA_ERR_CUDA;
@@ -1123,13 +1092,8 @@ fp8la_status gemm_pertensor_impl(const uint8_t *A, int64_t lda,
       if (!encode_c(&tmC, C, ldc, M, N)) return FP8LA_ERR_CUDA;
       args.c_tma = 1;
     }
-    if (quad) {
-      const int64_t ctiles = ((M + P_BM - 1) / P_BM) * ((N + 2 * P_BN - 1) / (2 * P_BN));
-      return launch_gemm_pair<false, true>(tmA, tmB, tmB64, tmC, tmA64, args,
-                                           ctiles, s);
-    }
     const int64_t tiles = ((M + P_BM - 1) / P_BM) * ((N + P_BN - 1) / P_BN);
-    return launch_gemm_pair<false>(tmA, tmB, tmB64, tmC, tmA64, args, tiles, s);
+    return launch_gemm_pair<false>(tmA, tmB, tmB64, tmC, args, tiles, s);
   }
   if (small) {
     const int64_t tiles = ((M + BM - 1) / BM) * ((N + kSmallBN - 1) / kSmallBN);
@@ -1253,7 +1217,7 @@ extern "C" fp8la_status fp8_grouped_gemm(
     }
     const int64_t tiles = ((m_capacity + P_BM - 1) / P_BM + num_groups) *
                           ((N + P_BN - 1) / P_BN);
-    return launch_gemm_pair<true>(tmA, tmB, tmB, tmC, tmA, args, tiles, s);
+    return launch_gemm_pair<true>(tmA, tmB, tmB, tmC, args, tiles, s);
   }
   const int64_t tiles =
       ((m_capacity + BM - 1) / BM + num_groups) * ((N + kBN - 1) / kBN);
