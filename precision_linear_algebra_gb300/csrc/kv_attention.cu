@@ -394,23 +394,28 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
         e0 = min(exponent_of(lds_f(scales + 4 * kStep)), 126);
         __syncwarp();
       }
-      uint32_t far;  // tokens whose shares are added up beside
+      uint32_t far = 0;  // tokens whose shares are added up beside
       {
         const float v = lds_f(scales + 4 * (kStep + lane));
         const bool fine = base + lane < end && v > 0.0f && v < INFINITY;
-        const int top = __reduce_max_sync(0xffffffffu, fine ? min(exponent_of(v), 126) : -126);
-        if (top > e0 + kSpan) {
+        // Whether the exponent (of subnormal numbers one less than exponent_of) is within
+        // e0 - kSpan .. e0 + kSpan.
+        const uint32_t above = (__float_as_uint(v) >> 23) - static_cast<uint32_t>(e0 + 127 - kSpan);
+        if (__any_sync(0xffffffffu, fine && above > 2 * kSpan)) {
+          const int top = __reduce_max_sync(0xffffffffu, fine ? min(exponent_of(v), 126) : -126);
+          if (top > e0 + kSpan) {
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            add_share(far_top[k], far_sum[k], M[k] - kShift, l[k]);
-            l[k] = 0.0f;
-            M[k] -= static_cast<float>(top - e0);
+            for (int k = 0; k < 2; ++k) {
+              add_share(far_top[k], far_sum[k], M[k] - kShift, l[k]);
+              l[k] = 0.0f;
+              M[k] -= static_cast<float>(top - e0);
+            }
+            e0 = top;
           }
-          e0 = top;
+          far = __ballot_sync(0xffffffffu, fine && exponent_of(v) < e0 - kSpan);
         }
         const float near = v * power_of_two(-e0);
-        const bool less = fine && exponent_of(v) < e0 - kSpan;
-        far = __ballot_sync(0xffffffffu, less);
+        const bool less = far >> lane & 1;
         sts_f(scales + 4 * (kStep + lane), base + lane >= end ? 0.0f
                                            : !fine            ? NAN
                                            : less             ? log2_far(v, e0)
@@ -505,15 +510,15 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
       }
       if (__any_sync(0xffffffffu, mx[0] > M[0] + kLazy || mx[1] > M[1] + kLazy)) {
         // A row of zeros in V adds nothing to the result, whatever its scale: it must not
-        // take the others' weights towards a half's end.
-        uint32_t some = 0;
+        // take the others' weights towards a half's end.  Nearly all have another code
+        // among the first 16.
+        uint32_t zeros = ~far;
 #pragma unroll 1
-        for (int ch = 0; ch < C::CH; ++ch) {
+        for (int ch = 0; ch < C::CH && zeros != 0; ++ch) {
           const uint4 w = lds128(st + (lane / kGroup * 2 + 1) * C::kK +
                                  chunk_at<DP>(lane % kGroup, ch));
-          some |= w.x | w.y | w.z | w.w;
+          zeros &= __ballot_sync(0xffffffffu, ((w.x | w.y | w.z | w.w) & 0x7f7f7f7fu) == 0);
         }
-        const uint32_t zeros = __ballot_sync(0xffffffffu, (some & 0x7f7f7f7fu) == 0) & ~far;
         if (zeros) {
           set_aside(zeros, [&](float s, int t, int) { return s - lds_f(scales + 4 * (kStep + t)); });
           mx[0] = mx[1] = -INFINITY;

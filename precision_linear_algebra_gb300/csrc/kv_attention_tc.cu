@@ -1122,8 +1122,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                          : "r"(base + C::kFirst + (((step - 1) & 1) * kTokens + lane + 32 * i) * 16)
                          : "memory");
             scale[i] = out[kTokens + 32 * i + scale_at];
-            if (((w[0] | w[1] | w[2] | w[3]) & 0x7f7f7f7fu) == 0) zeros |= 1u << i;
-            if (scale[i] < INFINITY) top = max(top, __float_as_int(scale[i]));
+            const bool fine = scale[i] > 0.0f && scale[i] < INFINITY;
+            if (fine && ((w[0] | w[1] | w[2] | w[3]) & 0x7f7f7f7fu) == 0) zeros |= 1u << i;
+            if (fine) top = max(top, __float_as_int(scale[i]));
           }
           if (__any_sync(0xffffffffu, zeros != 0)) {
             const int buf = (step - 1) % kScaleBufs;
