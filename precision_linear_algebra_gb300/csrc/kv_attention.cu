@@ -171,6 +171,22 @@ __device__ __forceinline__ void load_q(const AttnArgs &a, int64_t at, bool on, f
   }
 }
 
+// Joins what the pieces of a part before this one made with the first warp's results.
+template <int DP>
+__device__ __noinline__ void join_pieces(const AttnArgs &a, int part, int rows, float *red,
+                                         float *red_lse) {
+  const int64_t row0 = static_cast<int64_t>(part) * kRows;
+  for (int i = threadIdx.x; i < rows * a.cache.D; i += kThreads) {
+    const int r = i / a.cache.D, d = i - r * a.cache.D;
+    float *p = red + r * (DP + 4) + d;
+    *p = joined(weigh(red_lse[r], a.part_lse[row0 + r]), *p, a.part_o[(row0 + r) * DP + d]);
+  }
+  __syncthreads();
+  if (threadIdx.x < rows)
+    red_lse[threadIdx.x] = weigh(red_lse[threadIdx.x], a.part_lse[row0 + threadIdx.x]).lse;
+  __syncthreads();
+}
+
 template <bool F32Q, int FMT, int DP>
 __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
     kv_attention_kernel(const __grid_constant__ CUtensorMap tmK,
@@ -211,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
 
   if (threadIdx.x == 0) start_walk<kRows>(a, sh, &walk);
   for (;;) {
-    if (threadIdx.x == 0) more = next_item<kRows, kTile, kItemCost>(a, &walk, &it);
+    if (threadIdx.x == 0) more = next_item<kRows, kTile, kItemCost, kWarps * kPiece>(a, &walk, &it);
     __syncthreads();
     if (!more) break;
     const Seq q = it.q;
@@ -656,8 +672,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
     }
     __syncthreads();
     if (a.late) pdl_wait();  // the prefix's results
-    const bool whole = count == it.tiles;
-    const int part = 2 * blockIdx.x + (tile0 > 0 ? 0 : 1);
+    const bool whole = it.first == 0 && tile0 + count == it.tiles;
+    const int part = 2 * blockIdx.x + (it.first > 0 ? 0 : 1);
+    if (it.after) join_pieces<DP>(a, part, rows, red, red_lse);
     constexpr int kPieces = DP / 8;
     for (int i = threadIdx.x; i < rows * kPieces; i += kThreads) {
       const int r = i / kPieces, d = i % kPieces * 8;
@@ -704,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
         if (d == 0) a.part_lse[part * kRows + r] = all_lse;
       }
     }
-    if (threadIdx.x == 0 && !whole && tile0 == 0)
+    if (threadIdx.x == 0 && !whole && !it.more && it.first == 0)
       a.desc[blockIdx.x] = {s, h, rt, owner_of(sh, it.end - 1) - static_cast<int>(blockIdx.x) + 1};
     fence_proxy_async_smem();
     __syncthreads();  // the results overlay the rings

@@ -209,6 +209,16 @@ __device__ __forceinline__ void tmem_store_halves(uint32_t addr, const uint32_t 
         "r"(r[14]), "r"(r[15]), "r"(addr)
       : "memory");
 }
+// 16 columns of this thread's lane.
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const float (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};"
+      ::"f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]),
+        "f"(r[7]), "f"(r[8]), "f"(r[9]), "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]),
+        "f"(r[14]), "f"(r[15]), "r"(addr)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_wait_store() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -472,6 +482,27 @@ __device__ __noinline__ uint32_t lost_columns(const AttnArgs &a, const Item &it,
       if (!Fm::finite(codes[k + i])) bad |= 1u << i;
   }
   return bad;
+}
+
+// Joins a row's sums with what the pieces of its part before this one made, over them in
+// tensor memory, a row a lane.
+__device__ __noinline__ Total join_pieces(uint32_t o_tm, const float *before, const float *lse,
+                                          int D, bool on, Total t) {
+  const Weights w = on ? weigh(t.lse, *lse) : Weights{1.0f, 0.0f, t.lse, 1.0f};
+#pragma unroll 1
+  for (int k = 0; k < D; k += 16) {
+    float o[16];
+    __syncwarp();
+    tmem_load16(o_tm + k, o);
+    if (on) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[i] = joined(w, o[i] * t.f0 * t.f1, before[k + i]);
+    }
+    __syncwarp();
+    tmem_store16(o_tm + k, o);
+  }
+  tmem_wait_store();
+  return {w.lse, 1.0f, 1.0f};
 }
 
 // mbar_wait by a whole warp, out of line: the kernel waits in many places.
@@ -824,17 +855,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = wait(o_bar(t), o_uses & 1u))) break;
       ++o_uses;
       tc_fence_after();
-      const Total all_of = total_of(best - kShift, sum, far_top[lane], far_sum[lane],
+      Total all_of = total_of(best - kShift, sum, far_top[lane], far_sum[lane],
                                     __float_as_int(far_top[64]));
-      const float lse = all_of.lse;
       const bool mask = *poison != 0;
       const bool on = row0 + lane < rows;
-      const bool whole = it.count == it.tiles;
+      const bool whole = it.first == 0 && it.tile0 + it.count == it.tiles;
       const int tok = divide(r, a.group);
       const int64_t out_row = static_cast<int64_t>(it.q.row0) + tok;
       const int hq = it.h * a.G + r - tok * a.G;
       const int64_t place = out_row * a.Hq + hq;
-      const int64_t part = (2 * static_cast<int64_t>(blockIdx.x) + (it.tile0 > 0 ? 0 : 1)) * kItemRows + t * kRows + row;
+      const int64_t part =
+          (2 * static_cast<int64_t>(blockIdx.x) + (it.first > 0 ? 0 : 1)) * kItemRows + t * kRows + row;
+      if (opaque(it.after))
+        all_of = join_pieces(o_tm, a.part_o + part * DP, a.part_lse + part, a.cache.D, on, all_of);
+      const float lse = all_of.lse;
       Weights weights = {1.0f, 0.0f, lse, 1.0f};
       const float *pre = nullptr;
       if (whole && !a.raw_o && on) {
@@ -891,7 +925,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(ofree_bar(t));
-      if (threadIdx.x == 0 && !whole && it.tile0 == 0)
+      if (threadIdx.x == 0 && !whole && !it.more && it.first == 0)
         a.desc[blockIdx.x] = {it.s, it.h, it.rt,
                               owner_of(sh, it.end - 1) - static_cast<int>(blockIdx.x) + 1};
       item_done(n);
@@ -1069,7 +1103,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         if (!opaque(is_v)) {
           if (lane == 0) {
-            if (!next_item<kItemRows, kTokens, kItemCost>(a, &walk, &items[i])) items[i].count = 0;
+            if (!next_item<kItemRows, kTokens, kItemCost, kPiece>(a, &walk, &items[i])) items[i].count = 0;
             mbar_arrive(itfull_bar(i));
           }
           __syncwarp();

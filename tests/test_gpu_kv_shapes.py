@@ -28,32 +28,97 @@ def test_many_rows_in_every_form(D, fmt, q, inside):
     check(fl, c, causal=False)
 
 
+def _mean_error(c, few, heads, got, gl):
+    """The mean relative error of some rows and heads, all of them within their bounds."""
+    import torch
+    G = len(heads) // c["H"]
+    q = c["q"][few][:, heads]
+    # without causal a row sees what the last one of its sequence sees
+    each = [reference(dict(c, lens=c["lens"][:1], rows=[1], T=1, G=G, q=q[i:i + 1]), scale=0.01)
+            for i in range(len(few))]
+    ro, ob, rl, lb = (torch.cat(x) for x in zip(*each))
+    got, gl = got[few][:, heads], gl[few][:, heads]
+    assert close(got, ro, ob) and close(gl, rl, lb)
+    return ((got.double() - ro) / ro).mean().abs().item()
+
+
+def _mean_bound(H, D):
+    """A cut of 2^-23 at most for each 16 tokens of a piece of 16384 (of a warp's), all the
+    same way: 2^-13.  And BF16's roundings, each even over 2^-8 of a value at most, so with a
+    variance of 2^-16 / 3: with nearly even weights all rows have the same results, so that
+    only those of the H D columns are independent; four of their mean's deviations."""
+    return 2.0 ** -13 + 4 * 2.0 ** -8 / math.sqrt(3 * H * D)
+
+
 @pytest.mark.parametrize("q", ["bfloat16", "float32"])
-@pytest.mark.parametrize("D", [64, 128])
-def test_long_sums(D, q):
-    """Items of 32768 tokens, whose values all have the same sign: every step's cut on the
-    tensor cores goes the same way.  A few rows of each head are compared."""
+@pytest.mark.parametrize("D,n", [(64, 32768), (128, 32768), (128, 131072)])
+def test_long_sums(D, n, q):
+    """Values of one sign, whose sums the tensor cores cut: errors do not grow with the
+    length."""
     import torch
     fl = lib()
-    n, rows, H, G, page = 32768, 80, 8, 64, 64
-    c = make((n,), (rows,), H, G, D, page, q, spare=0)
+    H, G = 8, 64
+    c = make((n,), (80,), H, G, D, 64, q, spare=0)
     c["cache"].v.bitwise_and_(0x7F)
     out, lse = attend(fl, c, causal=False, scale=0.01)
     torch.cuda.synchronize()
     assert fl.device_status() == 0
-    few = [0, 1, 41, 79]
-    heads = [h * G + i for h in range(H) for i in (0, 63)]
-    d = dict(c, rows=[len(few)], T=len(few), G=2, q=c["q"][few][:, heads])
-    # without causal a row sees what the last one of its sequence sees
-    each = [reference(dict(d, rows=[1], T=1, q=d["q"][i:i + 1]), scale=0.01) for i in range(len(few))]
-    ro, ob, rl, lb = (torch.cat(x) for x in zip(*each))
-    got, gl = out[few][:, heads], lse[few][:, heads]
-    assert close(got, ro, ob) and close(gl, rl, lb)
-    # BF16's roundings go both ways, so the mean shows the cuts: 2^-23 of the sum so far for
-    # each 16 tokens, half of that on average, of a sum that is half of the last on average,
-    # twice over for what a mean of roundings leaves
-    bias = ((got.double() - ro) / ro).mean().abs().item()
-    assert bias <= 2 * (n / 16) * 2.0 ** -25 + 2.0 ** -9 / math.sqrt(got.numel()) * 4
+    mean = _mean_error(c, [0, 1, 41, 79], [h * G + i for h in range(H) for i in (0, 63)], out, lse)
+    assert mean <= _mean_bound(H, D)
+
+
+def test_long_sums_of_few_rows():
+    """The same for the few-row kernel, 65536 tokens of a sequence a piece, a fourth of
+    which a warp adds up: 512 sequences of the same pages."""
+    import torch
+    fl = lib()
+    S, n, H, G, D = 512, 2 ** 20, 1, 8, 128
+    c = make((n,), (1,), H, G, D, 64, spare=0)
+    c["cache"].v.bitwise_and_(0x7F)
+    q = (1.5 * torch.randn(S, H * G, D, device="cuda")).to(torch.bfloat16)
+    out, lse = fl.kv_attention(q, c["cache"], torch.arange(S + 1, dtype=torch.int32, device="cuda"),
+                               c["kv_lens"].expand(S).contiguous(),
+                               c["table"].expand(S, -1).contiguous(),
+                               max_rows=1, scale=0.01)
+    torch.cuda.synchronize()
+    assert fl.device_status() == 0
+    mean = _mean_error(dict(c, q=q), [0, 31, 200, 511], list(range(8)), out, lse)
+    assert mean <= _mean_bound(H, D)
+
+
+@pytest.mark.parametrize("rows,H,G,lens", [
+    (1, 8, 8, [70000 + 811 * i for i in range(60)]),          # few rows: two pieces each
+    (40, 8, 4, [17000 + 2300 * i for i in range(20)]),        # many: two to five
+    (100, 1, 3, [40000, 100, 33000]),                         # parts of several CTAs
+])
+@pytest.mark.parametrize("prefix", [0, 20000])
+def test_pieces(rows, H, G, lens, prefix):
+    """Parts that go through in several pieces, items that one CTA does whole and those
+    that are shared, behind a prefix too; sequences share pages."""
+    import torch
+    fl = lib()
+    n = max(lens)
+    c = make((n,), (rows,), H, G, 64, 64, prefix=prefix)
+    S = len(lens)
+    c.update(lens=lens, rows=[rows] * S, T=S * rows, table=c["table"].expand(S, -1).contiguous(),
+             kv_lens=torch.tensor(lens, dtype=torch.int32, device="cuda"),
+             offs=torch.arange(S + 1, dtype=torch.int32, device="cuda") * rows)
+    c["q"] = (1.5 * torch.randn(S * rows, H * G, 64, device="cuda")).to(torch.bfloat16)
+    out, lse = attend(fl, c, max_rows=rows)
+    again, lse2 = attend(fl, c, max_rows=rows)
+    torch.cuda.synchronize()
+    assert fl.device_status() == 0
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+    for s in sorted({0, 1, S // 2, S - 1}):
+        for h in sorted({0, H - 1}):
+            lo = s * rows
+            one = dict(c, lens=[lens[s]], rows=[rows], T=rows, H=1, G=G, table=c["table"][s:s + 1],
+                       q=c["q"][lo:lo + rows, h * G:(h + 1) * G])
+            one["cache"] = fl.KVCache(*(t[:, h:h + 1] for t in (
+                c["cache"].k, c["cache"].v, c["cache"].k_scale, c["cache"].v_scale)))
+            ro, ob, rl, lb = reference(one)
+            assert close(out[lo:lo + rows, h * G:(h + 1) * G], ro, ob)
+            assert close(lse[lo:lo + rows, h * G:(h + 1) * G], rl, lb)
 
 
 def _drawn(seed):
