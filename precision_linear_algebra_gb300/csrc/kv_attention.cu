@@ -1179,8 +1179,9 @@ fp8la_status fp8_kv_attention(const void *q, int32_t q_dtype, int64_t ld_q, int6
   if (st != FP8LA_OK) return st;
   const int H = a.cache.heads, D = a.cache.D;
   if (q_dtype != FP8LA_TYPE_F32 && q_dtype != FP8LA_TYPE_BF16) return FP8LA_ERR_INVALID_ARG;
+  const float scale_log2 = scale * kLog2e;
   if (num_heads < 1 || num_heads % H != 0 || max_rows < 0 || prefix_pages < 0 ||
-      !(scale > -INFINITY && scale < INFINITY))
+      !(scale_log2 > -INFINITY && scale_log2 < INFINITY))
     return FP8LA_ERR_INVALID_ARG;
   if (num_heads > kMaxHeads || rows > INT32_MAX || rows * num_heads >= kMaxRowHeads)
     return FP8LA_ERR_UNSUPPORTED;
@@ -1225,7 +1226,7 @@ fp8la_status fp8_kv_attention(const void *q, int32_t q_dtype, int64_t ld_q, int6
   a.G = num_heads / H;
   a.group = make_divisor(static_cast<uint32_t>(a.G));
   a.causal = causal != 0;
-  a.scale_log2 = scale * kLog2e;
+  a.scale_log2 = scale_log2;
   a.max_rows = max_rows;
   bool by_many = false;
   if (prefix) {
