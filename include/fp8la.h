@@ -552,15 +552,22 @@ FP8LA_API fp8la_status fp8_kv_read(
  * overlap q, the cache or the other.
  * max_rows: the rows of the longest segment, or more (`rows`, if nothing better is
  * known): it chooses the kernels, and a segment with more makes the call write
- * nothing and record FP8LA_ERR_DEVICE_ARG, as does a call of 2^31 tiles or more: 128
- * tokens of a K/V head for 256 rows of its heads (16 with head_dim > 128; a prompt of
- * a million tokens with 8 K/V heads, 8 query heads each, has 2^30).  num_heads a multiple of kv_heads, at most 65536, rows * num_heads
- * < 2^31 - 2^20.
+ * nothing and record FP8LA_ERR_DEVICE_ARG, as does a call with 2^31 tiles or more of
+ * one kind, or of the prefix: 128 tokens of a K/V head for 256 rows of its heads, or for
+ * 16 where a sequence has no more than 64 or head_dim > 128 (a prompt of a million
+ * tokens with 8 K/V heads, 8 query heads each, has 2^30).  0 where no segment has rows.
+ * num_heads a multiple of kv_heads, at most 65536, rows * num_heads < 2^31 - 2^20.
+ * |scale| < 2.3e38.
  *
- * Sums are FP32.  Codes enter the tensor cores exactly, q with an error of at most
+ * Sums are FP32, those of products on the tensor cores, which cut them by up to 2^-23
+ * for each 16 tokens, in pieces of 16384 tokens at most that are joined in FP32.
+ * Exponentials, logarithms and reciprocals are within 2^-22.  Codes enter the tensor
+ * cores exactly, q with an error of at most
  * 2^-22 of an element (fp32) or none (bf16), but 2^-33 of the row's largest where
- * that is more; the weights exp(x_j) are rounded to 11 bits (and below 2^-21 of the
- * row's largest weight times V's scale to 2^-32 of it).  A token makes the rows that
+ * that is more; the weights exp(x_j) of the products are rounded to 11 bits, for fp32 q
+ * too (and below 2^-21 of the row's largest weight times V's scale, among tokens whose V
+ * is not all zeros, to 2^-32 of it); those of the denominator and of lse are not rounded.
+ * V's scales may be any positive finite numbers.  A token makes the rows that
  * see it NaN if its K or K's scale is not finite (but counts for nothing where its
  * score is -inf), if its V's scale is not a positive finite number, or if its page is
  * outside the cache; a V that is not finite makes that element of those rows infinite
