@@ -123,18 +123,6 @@ __host__ __device__ constexpr uint32_t idesc_f16(uint32_t N, bool b_mn) {
   return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((N >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-// An MN-major operand: a 128-byte swizzled row of 64 elements for each K, blocks of 64
-// elements `block` bytes apart.
-__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t block) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(block >> 4) << 16;
-  d |= static_cast<uint64_t>(1024u >> 4) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(2u) << 61;
-  return d;
-}
-
 // 16 columns of this thread's lane.
 __device__ __forceinline__ void tmem_load16(uint32_t addr, float (&r)[16]) {
   asm volatile(
@@ -1211,7 +1199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t s_idesc = idesc_f16(kTokens, false), o_idesc = idesc_f16(DP, true);
       const uint64_t q_desc = smem_desc_k128_sw128(base);
       const uint64_t k_desc = smem_desc_k128_sw128(base + C::kRing);
-      const uint64_t v_desc = desc_mn(base + C::kRing, C::kBlock);
+      const uint64_t v_desc = smem_desc_mn_sw128(base + C::kRing, C::kBlock);
       uint32_t s_step = 0, v_step = 0;      // tiles of tokens of S and of O
       uint32_t p_uses[2] = {0, 0}, o_uses[2] = {0, 0};
       // S of tile t against the K tile s_step.

@@ -66,20 +66,6 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(uint32_t M, uint32_t N,
          ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
-// Descriptor of an MN-major operand of 64-element (128-byte) swizzled rows, a
-// row for each K: 8-row groups 1024 bytes apart, 64-element blocks
-// `block_bytes` apart.
-__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr,
-                                                       uint32_t block_bytes) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(block_bytes >> 4) << 16;
-  d |= static_cast<uint64_t>(1024u >> 4) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(2u) << 61;
-  return d;
-}
-
 // 16 TMEM columns of this thread's lane.
 __device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&u)[16]) {
   asm volatile(

@@ -287,6 +287,20 @@ __device__ __forceinline__ uint64_t smem_desc_k128_sw128(uint32_t saddr) {
   return d;
 }
 
+// Descriptor of an MN-major operand of 64-element (128-byte) swizzled rows, a
+// row for each K: 8-row groups 1024 bytes apart, 64-element blocks
+// `block_bytes` apart.
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr,
+                                                       uint32_t block_bytes) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(block_bytes >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
 // Instruction descriptor for kind::f8f6f4: E4M3 A and B, F32 accumulator,
 // both operands K-major, dense.
 //   bits 4-5 D format (1 = F32)   bits 7-9 A format (0 = E4M3)
