@@ -171,6 +171,49 @@ __device__ __forceinline__ void load_q(const AttnArgs &a, int64_t at, bool on, f
   }
 }
 
+// Puts V's codes that are not finite, of the steps of 32 tokens that a warp went through
+// without them, into the results of the rows that see them.
+template <int FMT, int DP>
+__device__ __noinline__ void put_not_finite(const AttnArgs &a, const Item &it, int first, int all,
+                                            int end, float *rows) {
+  const Cache &c = a.cache;
+#pragma unroll 1
+  for (int base = first; base < end; base += kTile) {
+    if (base + kStep <= all) continue;
+#pragma unroll 1
+    for (int t = base; t < min(base + kStep, end); ++t) {
+      const int p = divide(t, c.page), page = a.rows.table[it.s * a.rows.ld_table + p];
+      if (page < 0 || page >= c.num_pages) continue;
+      const uint8_t *v = c.v + it.h * c.head_stride + page * c.page_stride +
+                         (t - p * c.page_size) * c.token_stride;
+#pragma unroll 1
+      for (int d = threadIdx.x & 31; d < c.D; d += 32) {
+        if (Format<FMT>::finite(v[d])) continue;
+#pragma unroll 1
+        for (int r = 0; r < it.rows; ++r)
+          if (t < tokens_seen(a, it.q, it.rt * kRows + r)) rows[r * (DP + 4) + d] = NAN;
+      }
+    }
+  }
+}
+
+// Four elements of row r, of all warps' results, where some are far below others.
+template <int DP>
+__device__ __noinline__ float4 join_far(const float *red, const float *red_lse, int r, int d,
+                                        float best, float inv) {
+  float x[4] = {};
+#pragma unroll 1
+  for (int w = 0; w < kWarps; ++w) {
+    const float lse = red_lse[w * kRows + r];
+    const bool far = far_below(lse - best);
+    const float f = lse == -INFINITY ? 0.0f : ex2(far ? 0.5f * (lse - best) : lse - best);
+    const float *p = red + (w * kRows + r) * (DP + 4) + d;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = fmaf(f * inv, far ? p[j] * f : p[j], x[j]);
+  }
+  return make_float4(x[0], x[1], x[2], x[3]);
+}
+
 // Joins what the pieces of a part before this one made with the first warp's results.
 template <int DP>
 __device__ __noinline__ void join_pieces(const AttnArgs &a, int part, int rows, float *red,
@@ -196,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
   using Fm = Format<FMT>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Share sh;
-  __shared__ int64_t warp_sums[2 * kWarps];
+  __shared__ int64_t warp_sums[kWarps];
   __shared__ Walk walk;
   __shared__ Item it;
   __shared__ int more;
@@ -323,14 +366,14 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
 #pragma unroll
       for (int i = 0; i < 2; ++i)
         at[i] = (static_cast<int64_t>(q.row0) + tok[i]) * a.ldq + head[i] * a.ldq_head;
-#pragma unroll 2
+      float all_x[DP / 64][2][16];
+#pragma unroll
       for (int f = 0; f < DP / 64; ++f)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float x[16];
-          load_q<F32Q>(a, at[i] + el(f, c), el(f, c) < kc.D, x);
+          load_q<F32Q>(a, at[i] + el(f, c), el(f, c) < kc.D, all_x[f][i]);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) m[i] = fmaxf(m[i], fabsf(x[j]));
+          for (int j = 0; j < 16; ++j) m[i] = fmaxf(m[i], fabsf(all_x[f][i][j]));
         }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -341,10 +384,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
       }
 #pragma unroll
       for (int f = 0; f < DP / 64; ++f) {
-        float x[2][16];
+        float(&x)[2][16] = all_x[f];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          load_q<F32Q>(a, at[i] + el(f, c), el(f, c) < kc.D, x[i]);
           const float up = power_of_two(e[i]);
 #pragma unroll
           for (int j = 0; j < 16; ++j) x[i][j] *= up;
@@ -386,268 +428,275 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
     float far_top[2] = {-INFINITY, -INFINITY}, far_sum[2] = {0.0f, 0.0f};  // see kSpan
     int e0 = 0;
     bool poison = false;
+    // Tokens whose shares are added up beside are rare: the loop stands here twice, first
+    // without the code for them, which would be fetched past in every turn (256 requests of
+    // 1024 tokens 128 us with it), and then with it, from the first such step on, of which
+    // `done` parts are done.
+    int base = first, done = 0;
+    bool alive = true;
+#pragma unroll
+    for (int rare = 0; rare < 2; ++rare) {
 #pragma unroll 1
-    for (int base = first; base < end; base += kTile) {
-      cp_wait<kStages - 2>();
-      const int slot = taken % kStages;
-      if (a.tma && !__all_sync(0xffffffffu, mbar_wait(bars + 8 * slot, (taken / kStages) & 1u,
-                                                      timeout_ns, a.rows.status, &abort_flag)))
-        break;
-      ++taken;
-      __syncwarp();
-      {
-        const int ahead = base + (kStages - 1) * kTile;
-        if (ahead < end) {
-          const int p = page;
-          page = page_at(ahead + kTile);
-          request(ahead, p);
+      for (; alive && base < end; base += kTile) {
+        if (!rare || done == 0) {
+          cp_wait<kStages - 2>();
+          const int next = taken % kStages;
+          if (a.tma && !__all_sync(0xffffffffu, mbar_wait(bars + 8 * next, (taken / kStages) & 1u,
+                                                          timeout_ns, a.rows.status, &abort_flag))) {
+            alive = false;
+            break;
+          }
+          ++taken;
+          __syncwarp();
+          const int ahead = base + (kStages - 1) * kTile;
+          if (ahead < end) {
+            const int p = page;
+            page = page_at(ahead + kTile);
+            request(ahead, p);
+          }
+          cp_commit();
         }
-        cp_commit();
-      }
-      const uint32_t st = ring + slot * C::kStage, scales = scale_ring + slot * C::kScaleStage;
-      // V's scales: logarithm and reciprocal, relative to a power of two near the first.
-      if (base == first) {
-        e0 = min(exponent_of(lds_f(scales + 4 * kStep)), 126);
-        __syncwarp();
-      }
-      uint32_t far = 0;  // tokens whose shares are added up beside
-      {
-        const float v = lds_f(scales + 4 * (kStep + lane));
-        const bool fine = base + lane < end && v > 0.0f && v < INFINITY;
-        // Whether the exponent (of subnormal numbers one less than exponent_of) is within
-        // e0 - kSpan .. e0 + kSpan.
-        const uint32_t above = (__float_as_uint(v) >> 23) - static_cast<uint32_t>(e0 + 127 - kSpan);
-        if (__any_sync(0xffffffffu, fine && above > 2 * kSpan)) {
-          const int top = __reduce_max_sync(0xffffffffu, fine ? min(exponent_of(v), 126) : -126);
-          if (top > e0 + kSpan) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              add_share(far_top[k], far_sum[k], M[k] - kShift, l[k]);
-              l[k] = 0.0f;
-              M[k] -= static_cast<float>(top - e0);
+        const int slot = (taken - 1) % kStages;
+        const uint32_t st = ring + slot * C::kStage, scales = scale_ring + slot * C::kScaleStage;
+        // V's scales: logarithm and reciprocal, relative to a power of two near the first.
+        if (base == first && (!rare || done == 0)) {
+          e0 = min(exponent_of(lds_f(scales + 4 * kStep)), 126);
+          __syncwarp();
+        }
+        uint32_t far = 0;  // tokens whose shares are added up beside
+        if (!rare || done < 2) {
+          const float v = lds_f(scales + 4 * (kStep + lane));
+          const bool fine = base + lane < end && v > 0.0f && v < INFINITY;
+          // Whether the exponent (of subnormal numbers one less than exponent_of) is within
+          // e0 - kSpan .. e0 + kSpan.
+          const uint32_t above = (__float_as_uint(v) >> 23) - static_cast<uint32_t>(e0 + 127 - kSpan);
+          if (__any_sync(0xffffffffu, fine && above > 2 * kSpan)) {
+            if (!rare) {
+              done = 1;
+              break;
             }
-            e0 = top;
+            const int top = __reduce_max_sync(0xffffffffu, fine ? min(exponent_of(v), 126) : -126);
+            if (top > e0 + kSpan) {
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                add_share(far_top[k], far_sum[k], M[k] - kShift, l[k]);
+                l[k] = 0.0f;
+                M[k] -= static_cast<float>(top - e0);
+              }
+              e0 = top;
+            }
+            far = __ballot_sync(0xffffffffu, fine && exponent_of(v) < e0 - kSpan);
           }
-          far = __ballot_sync(0xffffffffu, fine && exponent_of(v) < e0 - kSpan);
+          const float near = v * power_of_two(-e0);
+          const bool less = far >> lane & 1;
+          sts_f(scales + 4 * (kStep + lane), base + lane >= end ? 0.0f
+                                             : !fine            ? NAN
+                                             : less             ? log2_far(v, e0)
+                                                                : lg2(near));
+          // A bad scale is in the exponent alone: rows that do not see it have weight 0.
+          sts_f(scales + 4 * (2 * kStep + lane), !fine ? 1.0f : less ? 0.0f : rcp(near));
         }
-        const float near = v * power_of_two(-e0);
-        const bool less = far >> lane & 1;
-        sts_f(scales + 4 * (kStep + lane), base + lane >= end ? 0.0f
-                                           : !fine            ? NAN
-                                           : less             ? log2_far(v, e0)
-                                                              : lg2(near));
-        // A bad scale is in the exponent alone: rows that do not see it have weight 0.
-        sts_f(scales + 4 * (2 * kStep + lane), !fine ? 1.0f : less ? 0.0f : rcp(near));
-      }
-      // Scores of tokens 16 u + 8 i + g against the 16 rows, in sc[2 u + i].
-      float sc[2 * kSubs][4] = {};
+        // What lies behind the end may be anything.  Where some rows do not see a token (weight
+        // 0), its codes of V that are not finite must not reach them: they are taken out and put
+        // in at the end.
+        const bool partial = all < most && base + kStep > all;
+        if (partial || base + kStep > end) {
+          const uint32_t row = st + (lane / kGroup * 2 + 1) * C::kK;
+#pragma unroll 1
+          for (int ch = 0; ch < C::CH; ++ch) {
+            const uint32_t at = row + chunk_at<DP>(lane % kGroup, ch);
+            const uint4 v = lds128(at);
+            uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int u = 0; u < kSubs; ++u) {
-#pragma unroll
-        for (int f = 0; f < DP / 64; ++f) {
-          uint32_t kw[2][4];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint4 w = lds128(st + u * 2 * C::kK + chunk_at<DP>(g + 8 * i, el(f, c) / 16));
-            kw[i][0] = w.x; kw[i][1] = w.y; kw[i][2] = w.z; kw[i][3] = w.w;
+            for (int j = 0; j < 4; ++j) {
+              if (base + lane >= end) w[j] = 0;
+              if (partial) poison |= Fm::clear4(w[j]);
+            }
+            st_shared_v4(at, w[0], w[1], w[2], w[3]);
           }
+        }
+        // Scores of tokens 16 u + 8 i + g against the 16 rows, in sc[2 u + i].
+        float sc[2 * kSubs][4] = {};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t b[2][2];
+        for (int u = 0; u < kSubs; ++u) {
+#pragma unroll
+          for (int f = 0; f < DP / 64; ++f) {
+            uint32_t kw[2][4];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              b[i][0] = decode2<FMT>(kw[i][j] & 0xffffu);
-              b[i][1] = decode2<FMT>(kw[i][j] >> 16);
+              const uint4 w = lds128(st + u * 2 * C::kK + chunk_at<DP>(g + 8 * i, el(f, c) / 16));
+              kw[i][0] = w.x; kw[i][1] = w.y; kw[i][2] = w.z; kw[i][3] = w.w;
             }
 #pragma unroll
-            for (int t = 0; t < C::TERMS; ++t) {
-              const int step = (4 * f + j) * C::TERMS + t;
-              if (C::QREG) {
-                mma_f16(sc[2 * u], qf[step], b[0][0], b[0][1]);
-                mma_f16(sc[2 * u + 1], qf[step], b[1][0], b[1][1]);
-              } else {
-                const uint4 w = lds128(qsm + (step * 32 + lane) * 16);
-                const uint32_t qw[4] = {w.x, w.y, w.z, w.w};
-                mma_f16(sc[2 * u], qw, b[0][0], b[0][1]);
-                mma_f16(sc[2 * u + 1], qw, b[1][0], b[1][1]);
+            for (int j = 0; j < 4; ++j) {
+              uint32_t b[2][2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                b[i][0] = decode2<FMT>(kw[i][j] & 0xffffu);
+                b[i][1] = decode2<FMT>(kw[i][j] >> 16);
+              }
+#pragma unroll
+              for (int t = 0; t < C::TERMS; ++t) {
+                const int step = (4 * f + j) * C::TERMS + t;
+                if (C::QREG) {
+                  mma_f16(sc[2 * u], qf[step], b[0][0], b[0][1]);
+                  mma_f16(sc[2 * u + 1], qf[step], b[1][0], b[1][1]);
+                } else {
+                  const uint4 w = lds128(qsm + (step * 32 + lane) * 16);
+                  const uint32_t qw[4] = {w.x, w.y, w.z, w.w};
+                  mma_f16(sc[2 * u], qw, b[0][0], b[0][1]);
+                  mma_f16(sc[2 * u + 1], qw, b[1][0], b[1][1]);
+                }
               }
             }
           }
         }
-      }
-      __syncwarp();
-      // Adds up beside the shares of the tokens in `mask`, whose scores x(i, k) gives.
-      auto set_aside = [&](uint32_t mask, auto score) {
+        __syncwarp();
+        // Adds up beside the shares of the tokens in `mask`, whose scores x(i, k) gives.
+        auto set_aside = [&](uint32_t mask, auto score) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float x[4 * kSubs], top = -INFINITY;
+          for (int k = 0; k < 2; ++k) {
+            float x[4 * kSubs], top = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < 4 * kSubs; ++i) {
-            const int t = 8 * (i >> 1) + 2 * c + (i & 1);
-            x[i] = (mask >> t & 1) && base + t < seen[k] ? score(sc[i >> 1][2 * k + (i & 1)], t, k)
-                                                         : -INFINITY;
-            top = fmaxf(top, x[i]);
+            for (int i = 0; i < 4 * kSubs; ++i) {
+              const int t = 8 * (i >> 1) + 2 * c + (i & 1);
+              x[i] = (mask >> t & 1) && base + t < seen[k] ? score(sc[i >> 1][2 * k + (i & 1)], t, k)
+                                                           : -INFINITY;
+              top = fmaxf(top, x[i]);
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // The row's four lanes have the same maximum and a part of the sum each.
+            const float from = top == -INFINITY ? 0.0f : top;
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4 * kSubs; ++i) sum += ex2(x[i] - from);
+            add_share(far_top[k], far_sum[k], top, sum);
           }
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          // The row's four lanes have the same maximum and a part of the sum each.
-          const float from = top == -INFINITY ? 0.0f : top;
-          float sum = 0.0f;
+        };
+        if (rare && far)
+          set_aside(far, [&](float s, int t, int k) { return s * lds_f(scales + 4 * t) * factor[k]; });
+        // Exponents and weights of tokens 8 i + 2c, 8 i + 2c + 1.
 #pragma unroll
-          for (int i = 0; i < 4 * kSubs; ++i) sum += ex2(x[i] - from);
-          add_share(far_top[k], far_sum[k], top, sum);
+        for (int i = 0; i < 2 * kSubs; ++i) {
+          const float2 ks = lds_f2(scales + 32 * i + 8 * c);
+          const float2 lv = lds_f2(scales + 4 * kStep + 32 * i + 8 * c);
+          sc[i][0] = fmaf(sc[i][0] * ks.x, factor[0], lv.x);
+          sc[i][1] = fmaf(sc[i][1] * ks.y, factor[0], lv.y);
+          sc[i][2] = fmaf(sc[i][2] * ks.x, factor[1], lv.x);
+          sc[i][3] = fmaf(sc[i][3] * ks.y, factor[1], lv.y);
         }
-      };
-      if (far)
-        set_aside(far, [&](float s, int t, int k) { return s * lds_f(scales + 4 * t) * factor[k]; });
-      // Exponents and weights of tokens 8 i + 2c, 8 i + 2c + 1.
-#pragma unroll
-      for (int i = 0; i < 2 * kSubs; ++i) {
-        const float2 ks = lds_f2(scales + 32 * i + 8 * c);
-        const float2 lv = lds_f2(scales + 4 * kStep + 32 * i + 8 * c);
-        sc[i][0] = fmaf(sc[i][0] * ks.x, factor[0], lv.x);
-        sc[i][1] = fmaf(sc[i][1] * ks.y, factor[0], lv.y);
-        sc[i][2] = fmaf(sc[i][2] * ks.x, factor[1], lv.x);
-        sc[i][3] = fmaf(sc[i][3] * ks.y, factor[1], lv.y);
-      }
-      if (base + kStep > min(all, end)) {
-#pragma unroll
-        for (int i = 0; i < 2 * kSubs; ++i)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (base + 8 * i + 2 * c + (k & 1) >= min(seen[k >> 1], end)) sc[i][k] = -INFINITY;
-      }
-      float mx[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        mx[k] = fmaxf(sc[0][2 * k], sc[0][2 * k + 1]);
-#pragma unroll
-        for (int i = 1; i < 2 * kSubs; ++i) mx[k] = fmaxf(mx[k], fmaxf(sc[i][2 * k], sc[i][2 * k + 1]));
-      }
-      if (__any_sync(0xffffffffu, mx[0] > M[0] + kLazy || mx[1] > M[1] + kLazy)) {
-        // A row of zeros in V adds nothing to the result, whatever its scale: it must not
-        // take the others' weights towards a half's end.  Nearly all have another code
-        // among the first 16.
-        uint32_t zeros = ~far;
-#pragma unroll 1
-        for (int ch = 0; ch < C::CH && zeros != 0; ++ch) {
-          const uint4 w = lds128(st + (lane / kGroup * 2 + 1) * C::kK +
-                                 chunk_at<DP>(lane % kGroup, ch));
-          zeros &= __ballot_sync(0xffffffffu, ((w.x | w.y | w.z | w.w) & 0x7f7f7f7fu) == 0);
-        }
-        if (zeros) {
-          set_aside(zeros, [&](float s, int t, int) { return s - lds_f(scales + 4 * (kStep + t)); });
-          mx[0] = mx[1] = -INFINITY;
+        if (base + kStep > min(all, end)) {
 #pragma unroll
           for (int i = 0; i < 2 * kSubs; ++i)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if (zeros >> (8 * i + 2 * c + (k & 1)) & 1) sc[i][k] = -INFINITY;
-              mx[k >> 1] = fmaxf(mx[k >> 1], sc[i][k]);
-            }
+            for (int k = 0; k < 4; ++k)
+              if (base + 8 * i + 2 * c + (k & 1) >= min(seen[k >> 1], end)) sc[i][k] = -INFINITY;
         }
+        float mx[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          float m = mx[k];
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-          m = fmaxf(m, M[k]);
-          const float down = m == -INFINITY ? 1.0f : ex2(M[k] - m);
-          M[k] = m;
-          l[k] *= down;
+          mx[k] = fmaxf(sc[0][2 * k], sc[0][2 * k + 1]);
 #pragma unroll
-          for (int j = 0; j < C::VH * C::VW; ++j) {
-            o[j][2 * k] *= down;
-            o[j][2 * k + 1] *= down;
-          }
+          for (int i = 1; i < 2 * kSubs; ++i) mx[k] = fmaxf(mx[k], fmaxf(sc[i][2 * k], sc[i][2 * k + 1]));
         }
-      }
-      const float top[2] = {M[0] == -INFINITY ? 0.0f : M[0] - kShift,
-                            M[1] == -INFINITY ? 0.0f : M[1] - kShift};
-      uint32_t pf[kSubs][4];
-#pragma unroll
-      for (int i = 0; i < 2 * kSubs; ++i) {
-        const float2 iv = lds_f2(scales + 8 * kStep + 32 * i + 8 * c);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) sc[i][k] = ex2(sc[i][k] - top[k >> 1]);
-        l[0] = fmaf(sc[i][0], iv.x, fmaf(sc[i][1], iv.y, l[0]));
-        l[1] = fmaf(sc[i][2], iv.x, fmaf(sc[i][3], iv.y, l[1]));
-        pf[i >> 1][2 * (i & 1)] = pack_half(sc[i][0], sc[i][1]);
-        pf[i >> 1][2 * (i & 1) + 1] = pack_half(sc[i][2], sc[i][3]);
-      }
-      // Values.  Where some rows do not see a token (weight 0), its codes that are not
-      // finite must not reach them: they are taken out here and put in at the end.
-      const bool partial = all < most && base + kStep > all, tail = base + kStep > end;
-#pragma unroll
-      for (int u = 0; u < kSubs; ++u) {
-#pragma unroll
-        for (int f = 0; f < C::VH; ++f) {
-          uint32_t vw[4][C::VW / 4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int token = 2 * c + (i & 1) + 8 * (i >> 1);
-            const uint32_t v_at = st + u * 2 * C::kK + C::kK;
-            if (C::VW == 16) {
-              const uint4 v = lds128(v_at + chunk_at<DP>(token, 8 * f + g));
-              vw[i][0] = v.x; vw[i][1] = v.y; vw[i][C::VW / 8] = v.z; vw[i][C::VW / 4 - 1] = v.w;
-            } else {
-              const uint2 v = lds64(v_at + chunk_at<DP>(token, g >> 1) + (g & 1) * 8);
-              vw[i][0] = v.x; vw[i][1] = v.y;
-            }
+        if (__any_sync(0xffffffffu, mx[0] > M[0] + kLazy || mx[1] > M[1] + kLazy)) {
+          // A row of zeros in V adds nothing to the result, whatever its scale: it must not
+          // take the others' weights towards a half's end.  Nearly all have another code
+          // among the first 16.
+          uint32_t zeros = base + kStep <= end ? ~far : ~far & ((1u << (end - base)) - 1);
+#pragma unroll 1
+          for (int ch = 0; ch < C::CH && zeros != 0; ++ch) {
+            const uint4 w = lds128(st + (lane / kGroup * 2 + 1) * C::kK +
+                                   chunk_at<DP>(lane % kGroup, ch));
+            zeros &= __ballot_sync(0xffffffffu, ((w.x | w.y | w.z | w.w) & 0x7f7f7f7fu) == 0);
           }
-          if (tail || partial) {
+          if (zeros && !rare) {
+            done = 2;
+            break;
+          }
+          if (rare && zeros) {
+            set_aside(zeros, [&](float s, int t, int) { return s - lds_f(scales + 4 * (kStep + t)); });
+            mx[0] = mx[1] = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 2 * kSubs; ++i)
 #pragma unroll
-              for (int j = 0; j < C::VW / 4; ++j) {
-                // What lies behind the end may be anything.
-                if (base + 16 * u + 2 * c + (i & 1) + 8 * (i >> 1) >= end) vw[i][j] = 0;
-                if (partial) poison |= Fm::clear4(vw[i][j]);
+              for (int k = 0; k < 4; ++k) {
+                if (zeros >> (8 * i + 2 * c + (k & 1)) & 1) sc[i][k] = -INFINITY;
+                mx[k >> 1] = fmaxf(mx[k >> 1], sc[i][k]);
               }
           }
 #pragma unroll
-          for (int j = 0; j < C::VW / 4; ++j) {
-            const uint32_t a0 = __byte_perm(vw[0][j], vw[1][j], 0x5140);
-            const uint32_t a1 = __byte_perm(vw[0][j], vw[1][j], 0x7362);
-            const uint32_t b0 = __byte_perm(vw[2][j], vw[3][j], 0x5140);
-            const uint32_t b1 = __byte_perm(vw[2][j], vw[3][j], 0x7362);
-            float(*oo)[4] = &o[f * C::VW + 4 * j];
-            mma_f16(oo[0], pf[u], decode2<FMT>(a0 & 0xffffu), decode2<FMT>(b0 & 0xffffu));
-            mma_f16(oo[1], pf[u], decode2<FMT>(a0 >> 16), decode2<FMT>(b0 >> 16));
-            mma_f16(oo[2], pf[u], decode2<FMT>(a1 & 0xffffu), decode2<FMT>(b1 & 0xffffu));
-            mma_f16(oo[3], pf[u], decode2<FMT>(a1 >> 16), decode2<FMT>(b1 >> 16));
+          for (int k = 0; k < 2; ++k) {
+            float m = mx[k];
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            m = fmaxf(m, M[k]);
+            const float down = m == -INFINITY ? 1.0f : ex2(M[k] - m);
+            M[k] = m;
+            l[k] *= down;
+#pragma unroll
+            for (int j = 0; j < C::VH * C::VW; ++j) {
+              o[j][2 * k] *= down;
+              o[j][2 * k + 1] *= down;
+            }
           }
         }
+        const float top[2] = {M[0] == -INFINITY ? 0.0f : M[0] - kShift,
+                              M[1] == -INFINITY ? 0.0f : M[1] - kShift};
+        uint32_t pf[kSubs][4];
+#pragma unroll
+        for (int i = 0; i < 2 * kSubs; ++i) {
+          const float2 iv = lds_f2(scales + 8 * kStep + 32 * i + 8 * c);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sc[i][k] = ex2(sc[i][k] - top[k >> 1]);
+          l[0] = fmaf(sc[i][0], iv.x, fmaf(sc[i][1], iv.y, l[0]));
+          l[1] = fmaf(sc[i][2], iv.x, fmaf(sc[i][3], iv.y, l[1]));
+          pf[i >> 1][2 * (i & 1)] = pack_half(sc[i][0], sc[i][1]);
+          pf[i >> 1][2 * (i & 1) + 1] = pack_half(sc[i][2], sc[i][3]);
+        }
+        // Values.
+#pragma unroll
+        for (int u = 0; u < kSubs; ++u) {
+#pragma unroll
+          for (int f = 0; f < C::VH; ++f) {
+            uint32_t vw[4][C::VW / 4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int token = 2 * c + (i & 1) + 8 * (i >> 1);
+              const uint32_t v_at = st + u * 2 * C::kK + C::kK;
+              if (C::VW == 16) {
+                const uint4 v = lds128(v_at + chunk_at<DP>(token, 8 * f + g));
+                vw[i][0] = v.x; vw[i][1] = v.y; vw[i][C::VW / 8] = v.z; vw[i][C::VW / 4 - 1] = v.w;
+              } else {
+                const uint2 v = lds64(v_at + chunk_at<DP>(token, g >> 1) + (g & 1) * 8);
+                vw[i][0] = v.x; vw[i][1] = v.y;
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < C::VW / 4; ++j) {
+              const uint32_t a0 = __byte_perm(vw[0][j], vw[1][j], 0x5140);
+              const uint32_t a1 = __byte_perm(vw[0][j], vw[1][j], 0x7362);
+              const uint32_t b0 = __byte_perm(vw[2][j], vw[3][j], 0x5140);
+              const uint32_t b1 = __byte_perm(vw[2][j], vw[3][j], 0x7362);
+              float(*oo)[4] = &o[f * C::VW + 4 * j];
+              mma_f16(oo[0], pf[u], decode2<FMT>(a0 & 0xffffu), decode2<FMT>(b0 & 0xffffu));
+              mma_f16(oo[1], pf[u], decode2<FMT>(a0 >> 16), decode2<FMT>(b0 >> 16));
+              mma_f16(oo[2], pf[u], decode2<FMT>(a1 & 0xffffu), decode2<FMT>(b1 & 0xffffu));
+              mma_f16(oo[3], pf[u], decode2<FMT>(a1 >> 16), decode2<FMT>(b1 >> 16));
+            }
+          }
+        }
+        // Reads before the copies that a next turn asks for.
+        if (a.tma) fence_proxy_async_smem();
+        if (rare) done = 0;
       }
-      // Reads before the copies that a next turn asks for.
-      if (a.tma) fence_proxy_async_smem();
     }
     cp_wait<0>();
     for (; taken < put; ++taken)  // where a wait ran out
       if (a.tma)
         mbar_wait_drain(bars + 8 * (taken % kStages), (taken / kStages) & 1u, timeout_ns,
                         a.rows.status);
-    if (__any_sync(0xffffffffu, poison)) {
-      for (int base = first; base < end; base += kTile) {
-        if (base + kStep <= all) continue;
-        for (int t = base; t < min(base + kStep, end); ++t) {
-          const int p = table[divide(t, kc.page)];
-          if (p < 0 || p >= kc.num_pages) continue;
-          const uint8_t *row = vbase + p * kc.page_stride +
-                               (t - divide(t, kc.page) * kc.page_size) * kc.token_stride;
-#pragma unroll
-          for (int j = 0; j < C::VH * C::VW; ++j)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int d = j / C::VW * 128 + (2 * c + i) * C::VW + j % C::VW;
-              if (d < kc.D && !Fm::finite(row[d])) {
-                if (t < seen[0]) o[j][i] = NAN;
-                if (t < seen[1]) o[j][2 + i] = NAN;
-              }
-            }
-        }
-      }
-    }
 
     // Each warp's result, normalised, with its logarithm (base 2); then all four's.
     __syncthreads();
@@ -669,6 +718,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
           row[j / C::VW * 128 + (2 * c + i) * C::VW + j % C::VW] =
               o[j][2 * k + i] * all_of.f0 * all_of.f1;
       if (c == 0) red_lse[warp * kRows + g + 8 * k] = all_of.lse;
+    }
+    if (__any_sync(0xffffffffu, poison)) {
+      __syncwarp();
+      put_not_finite<FMT, DP>(a, it, first, all, end, red + warp * kRows * C::kLdO);
     }
     __syncthreads();
     if (a.late) pdl_wait();  // the prefix's results
@@ -699,14 +752,14 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {  // 0 x NaN too: a V that is not finite
         const float *p = red + (w * kRows + r) * C::kLdO + d;
-        if (far && far_below(lse[w] - best)) {
-          const float f = ex2(0.5f * (lse[w] - best));
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = fmaf(f * inv, p[j] * f, x[j]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = fmaf(weight[w] * inv, p[j], x[j]);
-        }
+        for (int j = 0; j < 8; ++j) x[j] = fmaf(weight[w] * inv, p[j], x[j]);
+      }
+      if (far) {
+        const float4 lo = join_far<DP>(red, red_lse, r, d, best, inv);
+        const float4 hi = join_far<DP>(red, red_lse, r, d + 4, best, inv);
+        x[0] = lo.x; x[1] = lo.y; x[2] = lo.z; x[3] = lo.w;
+        x[4] = hi.x; x[5] = hi.y; x[6] = hi.z; x[7] = hi.w;
       }
       if (d >= kc.D) continue;
       if (whole) {
@@ -1114,7 +1167,14 @@ fp8la_status launch_pass(AttnArgs a, const Layout &l, uint8_t *ws, bool f32, int
                   fits(c.scale_token_stride);
   // All rows of a prefix are one sequence, which is all of one kernel's.
   const bool both = !(a.whole && tc);
-  a.both = tc && both;
+  // In tiles of either kernel: no more than in tiles of 16 rows against all that the table
+  // has room for.
+  const auto may_pass = [&](int64_t segments, int64_t tokens) {
+    const int64_t rows = static_cast<int64_t>(a.rows.T) * a.G / kRows + segments;
+    return rows * c.heads >= INT32_MAX / (tokens / kTile + 1 + kItemCost);
+  };
+  a.count_other = tc && both && may_pass(a.rows.S, a.rows.capacity);
+  a.count_prefix = may_pass(1, a.prefix_capacity);
   JoinSide few = {}, many = {};
   fp8la_status st = FP8LA_OK;
   auto use = [&](const Part &p, int BM, int ctas) {

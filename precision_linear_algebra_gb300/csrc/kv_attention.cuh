@@ -50,7 +50,10 @@ struct AttnArgs {
   const int32_t *prefix_len; // checked by the sequences' pass, too
   int64_t prefix_capacity;
   int32_t prefix_many;       // the prefix's pass was the many-row kernel's
-  int32_t both;              // sequences outside row_lo .. row_hi are the other kernel's
+  // Whether the work may pass 2^31 units: of the sequences outside row_lo .. row_hi, which
+  // are the other kernel's, and of the prefix.  The host knows what a call's table has room
+  // for; counting in every call cost 2 us of instructions fetched.
+  int32_t count_other, count_prefix;
   // Partial results: two of each CTA, rows of a tile each.
   float *part_o, *part_lse;
   Desc *desc;
@@ -227,15 +230,25 @@ __device__ __forceinline__ int row_tiles_of(const AttnArgs &a, const Seq &q) {
   return static_cast<int>((rows + BM - 1) / BM);
 }
 
-// Units of a sequence that is the other kernel's, whose row tiles have BM rows; with
-// `bound`, or a few more, without the counting of a diagonal.
-template <int BM, int BN, int COST>
-__device__ __forceinline__ int64_t units_elsewhere(const AttnArgs &a, const Seq &q, bool bound) {
-  const int64_t rows = static_cast<int64_t>(q.n) * a.G;
-  if (rows <= 0 || (rows >= a.row_lo && rows <= a.row_hi)) return 0;
-  const int rts = static_cast<int>((rows + BM - 1) / BM);
-  return a.cache.heads * (bound ? static_cast<int64_t>(rts) * (q.len / BN + 1 + COST)
-                                : units_below<BM, BN, COST>(a, q, rts, rts));
+// Units of the sequences that are the other kernel's, whose row tiles have BM rows; each
+// thread counts s0 .. s1-1.
+template <int THREADS, int BM, int BN, int COST>
+__device__ __noinline__ int64_t other_units(const AttnArgs &a, int s0, int s1, int64_t *sums) {
+  int64_t sum = 0;
+  for (int s = s0; s < s1; ++s) {
+    const Seq q = load_seq(a, s);
+    const int64_t rows = static_cast<int64_t>(q.n) * a.G;
+    if (rows <= 0 || (rows >= a.row_lo && rows <= a.row_hi)) continue;
+    const int rts = static_cast<int>((rows + BM - 1) / BM);
+    sum += a.cache.heads * units_below<BM, BN, COST>(a, q, rts, rts);
+  }
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = sum;
+  __syncthreads();
+  sum = 0;
+  for (int w = 0; w < THREADS / 32; ++w) sum += sums[w];
+  return sum;
 }
 
 // Units of the prefix's pass, of `tokens` tokens.
@@ -277,11 +290,11 @@ __device__ __noinline__ void share_out(const AttnArgs &a, Share *sh, int64_t *wa
   constexpr bool kMany = BM == kManyItemRows;
   constexpr int kOtherRows = kMany ? kFewItemRows : kManyItemRows;
   constexpr int kOtherCost = kMany ? kFewItemCost : kManyItemCost;
-  int64_t sum = 0, elsewhere = 0;
+  int64_t sum = 0;
   bool bad = false;
   if (a.prefix_len) {
     const int n = *a.prefix_len;
-    bad = n < 0 || n > a.prefix_capacity || prefix_units(a, n) > INT32_MAX;
+    bad = n < 0 || n > a.prefix_capacity || (a.count_prefix && prefix_units(a, n) > INT32_MAX);
   }
 #pragma unroll 1
   for (int s = s0; s < s1; ++s) {
@@ -292,8 +305,6 @@ __device__ __noinline__ void share_out(const AttnArgs &a, Share *sh, int64_t *wa
     bad |= off;
     const int rts = off ? 0 : row_tiles_of<BM>(a, q);
     if (rts > 0) sum += H * units_below<BM, BN, COST>(a, q, rts, rts);
-    else if (a.both && !off)
-      elsewhere += units_elsewhere<kOtherRows, BN, kOtherCost>(a, q, true);
   }
   bad = __syncthreads_or(bad);
   if (bad) {
@@ -311,30 +322,17 @@ __device__ __noinline__ void share_out(const AttnArgs &a, Share *sh, int64_t *wa
     const int64_t o = shfl_up64(run, d);
     if (lane >= d) run += o;
   }
-  if (a.both && __syncthreads_or(elsewhere > INT32_MAX / THREADS)) {  // that may be too much
-    elsewhere = 0;
-#pragma unroll 1
-    for (int s = s0; s < s1; ++s)
-      elsewhere += units_elsewhere<kOtherRows, BN, kOtherCost>(a, load_seq(a, s), false);
-#pragma unroll 1
-    for (int d = 16; d > 0; d >>= 1) elsewhere += __shfl_xor_sync(0xffffffffu, elsewhere, d);
-  } else {
-    elsewhere = 0;
-  }
-  if (lane == 31) {
-    warp_sums[warp] = run;
-    warp_sums[THREADS / 32 + warp] = elsewhere;
-  }
+  if (lane == 31) warp_sums[warp] = run;
   __syncthreads();
   int64_t before = run - sum, total = 0;
-  elsewhere = 0;
 #pragma unroll 1
   for (int w = 0; w < THREADS / 32; ++w) {
     if (w < warp) before += warp_sums[w];
     total += warp_sums[w];
-    elsewhere += warp_sums[THREADS / 32 + w];
   }
-  if (total > INT32_MAX || elsewhere > INT32_MAX) {
+  if (total > INT32_MAX ||
+      (a.count_other && other_units<THREADS, kOtherRows, BN, kOtherCost>(a, s0, s1, warp_sums) >
+                            INT32_MAX)) {
     if (threadIdx.x == 0) {
       atomicOr(a.rows.status, kStatusBadDeviceArg);
       *sh = {0, 0, 0, 0, 0, 0, 0, 0};

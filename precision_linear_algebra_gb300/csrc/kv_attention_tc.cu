@@ -432,24 +432,58 @@ __device__ __noinline__ void set_aside(uint32_t scores, uint32_t k_scales, const
   *far_sum = sum;
 }
 
-// Which of the tokens whose places are `places` and 32, 64, 96 further, if their bits are set
-// in `which`, have rows of zeros in V.  Where there is no token it is of no account.
-__device__ __noinline__ uint32_t rows_of_zeros(const Cache &c, uint32_t places, uint32_t which) {
+// A tile's scales of V where some lie far apart, or rows may be all zeros: log2 and
+// reciprocal over the scales at `at`, 32 tokens apart, and the tile's head.  A row of zeros
+// adds nothing to the result, whatever its scale: it must not take the others' weights
+// towards a half's end, and so gets none.  Returns what the scales are relative to.
+__device__ __noinline__ int rare_scales(const Cache &c, float *at, int *head, uint32_t firsts,
+                                        uint32_t places, int e0, bool first) {
+  const int lane = threadIdx.x & 31;
+  uint32_t zeros = 0;
+  int top = 0;         // positive numbers are in the order of their bits
 #pragma unroll 1
   for (int i = 0; i < 4; ++i) {
-    int64_t at;
-    asm volatile("ld.shared.b64 %0, [%1];" : "=l"(at) : "r"(places + 32 * i * 8) : "memory");
-    if (!(which >> i & 1) || at < 0) continue;
-    const uint8_t *row = c.v + (at & ~1ll);
-    uint32_t some = 0;
+    const float scale = at[32 * i];
+    if (!(scale > 0.0f && scale < INFINITY)) continue;
+    top = max(top, __float_as_int(scale));
+    uint32_t w[4];
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(firsts + 32 * 16 * i)
+                 : "memory");
+    uint32_t some = w[0] | w[1] | w[2] | w[3];
+    int64_t place;
+    asm volatile("ld.shared.b64 %0, [%1];" : "=l"(place) : "r"(places + 32 * 8 * i) : "memory");
+    const uint8_t *row = c.v + (place & ~1ll);
+#pragma unroll 1
     for (int d = 16; d < c.D && (some & 0x7f7f7f7fu) == 0; d += 16) {
-      const uint4 w = *reinterpret_cast<const uint4 *>(row + d);
-      some |= w.x | w.y | w.z | w.w;
+      const uint4 v = *reinterpret_cast<const uint4 *>(row + d);
+      some |= v.x | v.y | v.z | v.w;
     }
-    if (some & 0x7f7f7f7fu) which &= ~(1u << i);
+    if ((some & 0x7f7f7f7fu) == 0) zeros |= 1u << i;
   }
   __syncwarp();
-  return which;
+  top = min(exponent_of(__int_as_float(__reduce_max_sync(0xffffffffu, top))), 126);
+  const int rise = top > e0 + kSpan ? top - e0 : 0;
+  e0 += rise;
+  uint32_t any = 0;
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    const float scale = at[32 * i], v = scale * power_of_two(-e0);
+    const bool fine = scale > 0.0f && scale < INFINITY, zero = zeros >> i & 1;
+    const bool less = fine && (zero || exponent_of(scale) < e0 - kSpan);
+    const uint32_t far = __ballot_sync(0xffffffffu, less);
+    any |= far;
+    at[32 * i] = !fine ? NAN : !less ? lg2(v) : zero ? -INFINITY : log2_far(scale, e0);
+    at[32 * i + kTokens] = !fine ? 1.0f : less ? 0.0f : rcp(v);
+    if (lane == 0) head[4 + i] = static_cast<int>(far);
+  }
+  if (lane == 0) {
+    head[0] = e0;
+    head[1] = (rise > 0 && !first ? 1 : 0) | (any ? 2 : 0);
+    head[2] = rise;
+  }
+  return e0;
 }
 
 // Columns k .. k+15 of V that hold a code that is not finite at a token that a row sees,
@@ -507,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using Fm = Format<FMT>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Share sh;
-  __shared__ int64_t warp_sums[2 * kThreads / 32];
+  __shared__ int64_t warp_sums[kThreads / 32];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t *sbase = smem_raw + (base - raw);
@@ -1130,60 +1164,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (opaque(is_v)) {
           // Relative to a power of two near the scale of the item's first token.
           if (was_first) e0 = min(exponent_of(out[kTokens]), 126);
-          // A row of zeros in V adds nothing to the result, whatever its scale: it must not
-          // take the others' weights towards a half's end, and so gets none.  Nearly all have
+          // Whether the exponents (of subnormal numbers one less than exponent_of) are within
+          // e0 - kSpan .. e0 + kSpan, and whether rows of V may be all zeros: nearly all have
           // another code among the first 16.
+          const uint32_t low = static_cast<uint32_t>(e0 + 127 - kSpan);
+          const float down = power_of_two(-e0);
+          const uint32_t firsts = base + C::kFirst + (((step - 1) & 1) * kTokens + lane) * 16;
+          bool rare = false;
           float scale[4];
-          uint32_t zeros = 0;  // a bit for each of the lane's tokens
-          int top = 0;         // positive numbers are in the order of their bits
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t w[4];
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                         : "r"(base + C::kFirst + (((step - 1) & 1) * kTokens + lane + 32 * i) * 16)
+                         : "r"(firsts + 32 * 16 * i)
                          : "memory");
             scale[i] = out[kTokens + 32 * i + scale_at];
             const bool fine = scale[i] > 0.0f && scale[i] < INFINITY;
-            if (fine && ((w[0] | w[1] | w[2] | w[3]) & 0x7f7f7f7fu) == 0) zeros |= 1u << i;
-            if (fine) top = max(top, __float_as_int(scale[i]));
+            rare |= fine && ((__float_as_uint(scale[i]) >> 23) - low > 2 * kSpan ||
+                             ((w[0] | w[1] | w[2] | w[3]) & 0x7f7f7f7fu) == 0);
           }
-          if (__any_sync(0xffffffffu, zeros != 0)) {
+          int *const head = reinterpret_cast<int *>(out) + kTileHead / 4;
+          if (__any_sync(0xffffffffu, rare)) {
             const int buf = (step - 1) % kScaleBufs;
             if (!(ok = wait(atfull_bar(buf), ((step - 1) / kScaleBufs) & 1u))) break;
-            zeros = rows_of_zeros(a.cache, base + C::kPlaces + (buf * kTokens + lane) * 8, zeros);
-          }
-          top = min(exponent_of(__int_as_float(__reduce_max_sync(0xffffffffu, top))), 126);
-          const int rise = top > e0 + kSpan ? top - e0 : 0;
-          e0 += rise;
-          const float down = power_of_two(-e0);
-          uint32_t any = 0;
-          uint32_t *const head = reinterpret_cast<uint32_t *>(out) + kTileHead / 4;
+            e0 = rare_scales(a.cache, out + kTokens + scale_at, head, firsts,
+                             base + C::kPlaces + (buf * kTokens + lane) * 8, e0, was_first);
+          } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float *at = out + kTokens + 32 * i + scale_at;
-            const float v = scale[i] * down;
-            const bool fine = scale[i] > 0.0f && scale[i] < INFINITY;
-            const bool zero = zeros >> i & 1;
-            const bool less = fine && (zero || exponent_of(scale[i]) < e0 - kSpan);
-            const uint32_t far = __ballot_sync(0xffffffffu, less);
-            any |= far;
-            float lg, inv;
-            asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg) : "f"(v));
-            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(v));
-            if (less) {
-              lg = zero ? -INFINITY : log2_far(scale[i], e0);
-              inv = 0.0f;
+            for (int i = 0; i < 4; ++i) {
+              float *at = out + kTokens + 32 * i + scale_at;
+              const float v = scale[i] * down;
+              const bool fine = scale[i] > 0.0f && scale[i] < INFINITY;
+              float lg, inv;
+              asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg) : "f"(v));
+              asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(v));
+              at[0] = fine ? lg : NAN;
+              // A bad scale is in the exponent alone: rows that do not see it have weight 0.
+              at[kTokens] = fine ? inv : 1.0f;
             }
-            at[0] = fine ? lg : NAN;
-            // A bad scale is in the exponent alone: rows that do not see it have weight 0.
-            at[kTokens] = fine ? inv : 1.0f;
-            if (lane == 0) head[4 + i] = far;
-          }
-          if (lane == 0) {
-            head[0] = static_cast<uint32_t>(e0);
-            head[1] = (rise > 0 && !was_first ? 1u : 0u) | (any ? 2u : 0u);
-            head[2] = static_cast<uint32_t>(rise);
+            if (lane == 0) {
+              head[0] = e0;
+              head[1] = 0;
+            }
           }
         }
         __syncwarp();
