@@ -440,12 +440,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
       for (; alive && base < end; base += kTile) {
         if (!rare || done == 0) {
           cp_wait<kStages - 2>();
-          const int next = taken % kStages;
-          if (a.tma && !__all_sync(0xffffffffu, mbar_wait(bars + 8 * next, (taken / kStages) & 1u,
-                                                          timeout_ns, a.rows.status, &abort_flag))) {
-            alive = false;
-            break;
-          }
+          if (a.tma)
+            alive = __all_sync(0xffffffffu,
+                               mbar_wait(bars + 8 * (taken % kStages), (taken / kStages) & 1u,
+                                         timeout_ns, a.rows.status, &abort_flag));
+          if (!alive) break;
           ++taken;
           __syncwarp();
           const int ahead = base + (kStages - 1) * kTile;

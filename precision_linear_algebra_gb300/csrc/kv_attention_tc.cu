@@ -694,33 +694,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int apart = head[1];
         if (!(ok = wait(s_bar(t), tiles & 1u))) break;
         tc_fence_after();
-        if (opaque(apart & 1)) {
-          const int rise = head[2];
-          far_top[64] = __int_as_float(head[0]);
+        if (opaque(apart)) {
+          if (apart & 1) {
+            const int rise = head[2];
+            far_top[64] = __int_as_float(head[0]);
 #pragma unroll 1
-          for (int u = 0; u < 4; ++u) {
-            float y, z;
-            const uint64_t l = u < 2 ? (u == 0 ? l2[0] : l2[1]) : (u == 2 ? l2[2] : l2[3]);
-            const float m = u < 2 ? (u == 0 ? M[0] : M[1]) : (u == 2 ? M[2] : M[3]);
-            unpair(l, y, z);
-            y += z;
-            y += __shfl_xor_sync(0xffffffffu, y, 1);
-            y += __shfl_xor_sync(0xffffffffu, y, 2);
-            if (c == 0) add_share(far_top[8 * u + g], far_sum[8 * u + g], m - kShift, y);
-          }
+            for (int u = 0; u < 4; ++u) {
+              float y, z;
+              const uint64_t l = u < 2 ? (u == 0 ? l2[0] : l2[1]) : (u == 2 ? l2[2] : l2[3]);
+              const float m = u < 2 ? (u == 0 ? M[0] : M[1]) : (u == 2 ? M[2] : M[3]);
+              unpair(l, y, z);
+              y += z;
+              y += __shfl_xor_sync(0xffffffffu, y, 1);
+              y += __shfl_xor_sync(0xffffffffu, y, 2);
+              if (c == 0) add_share(far_top[8 * u + g], far_sum[8 * u + g], m - kShift, y);
+            }
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            M[u] -= static_cast<float>(rise);
-            l2[u] = pair(0.0f, 0.0f);
+            for (int u = 0; u < 4; ++u) {
+              M[u] -= static_cast<float>(rise);
+              l2[u] = pair(0.0f, 0.0f);
+            }
+            __syncwarp();
           }
-          __syncwarp();
-        }
-        if (opaque(apart & 2)) {
-          const int r = row0 + lane;
-          const int seen = r < rows ? tokens_seen(a, it.q, it.rt * kItemRows + r) : 0;
-          set_aside(s_tm, scales, reinterpret_cast<const uint8_t *>(head + 4),
-                    seen - tok0 - j * kTokens, my_factors[lane], far_top + lane, far_sum + lane);
-          __syncwarp();
+          if (apart & 2) {
+            const int r = row0 + lane;
+            const int seen = r < rows ? tokens_seen(a, it.q, it.rt * kItemRows + r) : 0;
+            set_aside(s_tm, scales, reinterpret_cast<const uint8_t *>(head + 4),
+                      seen - tok0 - j * kTokens, my_factors[lane], far_top + lane, far_sum + lane);
+            __syncwarp();
+          }
         }
         // The last scores of these rows are made: the next rows may take their place.
         if (j + 1 == count && more) fetch_q<F32Q, DP>(a, upcoming, q_at, row0);
