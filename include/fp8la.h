@@ -560,7 +560,7 @@ FP8LA_API fp8la_status fp8_kv_read(
  * |scale| < 2.3e38.
  *
  * Sums are FP32, those of products on the tensor cores, which cut them by up to 2^-23
- * for each 16 tokens, in pieces of 16384 tokens at most that are joined in FP32.
+ * for each 16 tokens, in pieces of 32768 tokens at most that are joined in FP32 (2^-12).
  * Exponentials, logarithms and reciprocals are within 2^-22.  Codes enter the tensor
  * cores exactly, q with an error of at most
  * 2^-22 of an element (fp32) or none (bf16), but 2^-33 of the row's largest where

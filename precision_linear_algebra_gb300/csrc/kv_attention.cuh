@@ -397,13 +397,16 @@ __device__ __forceinline__ int owner_of(const Share &sh, int u) {
 // through in pieces, an item each, of kPiece tiles at most (four times as many where four
 // warps share the tokens): what those before it made (`after` them) lies in the workspace,
 // where the part's result will, and is joined with the piece's own.  In one piece, values of
-// one sign came out 7.7e-4 too small over 131072 tokens and, with few rows, 1.7e-3 over 2^20.
+// one sign came out 7.7e-4 too small over 131072 tokens and, with few rows, 1.7e-3 over 2^20;
+// a piece of 32768 tokens (of a warp's) loses 2^-12 at most.  A piece costs what an item
+// costs: 512 rows after 131072 tokens take 2367 us in one, 2457 in pieces of 256 tiles, 2550
+// of 128.
 struct Item {
   Seq q;
   int s, h, rt, tile0, count, tiles, rows, end, first;
   bool after, more;   // pieces of the part before this one, and behind it
 };
-constexpr int kPiece = 128;
+constexpr int kPiece = 256;
 
 // Walks through a CTA's items.
 struct Walk {
