@@ -14,7 +14,9 @@
 // two to a maximum of 2^8, is halves exactly but for elements below 2^-22 of its
 // maximum (off by 2^-33 of it at most); an FP32 one is the sum of two halves,
 // 2^-22.  w_j is rounded to a half, 2^-11, at most 2^7 (2^15 between two rescalings),
-// so that only what is 2^-21 of the largest or less loses more.  Sums are FP32.
+// so that only what is 2^-21 of the largest or less loses more; unrounded in the
+// denominator.  Halves because the result is BF16 and mma.sync has no wider type that the
+// codes fit without a loss of rate.  Sums are FP32, in pieces (kPiece).
 //
 // Bound: HBM, K's and V's codes once for all heads of a group.  A warp streams 32
 // tokens at a time through a ring of its own, two steps deep, filled by TMA (16 tokens
@@ -23,9 +25,12 @@
 // what a group of heads of one token needs; the fragments come from codes by one
 // conversion for two of them.  tcgen05 wants 64 rows at least, which kv_attention_tc.cu
 // has.  Measured, 8 K/V heads of 128 with 8 query heads each, the join included: 64
-// sequences of 8192 tokens 179 us (6.2 TB/s), of lengths up to 8192 106 us (5.6; 128 with
-// steps of 32 tokens, 149 with 16, both before kItemCost); one of 131072 59 us (4.7); one
-// of 2048 17 us, two launches whose addresses and instructions come one after the other.
+// sequences of 8192 tokens 181 us (6.1 TB/s), of lengths up to 8192 108 us (5.6; 128 with
+// steps of 32 tokens, 149 with 16, both before kItemCost); one of 131072 60 us (4.7); one
+// of 2048 17 us, two launches whose addresses and instructions come one after the other;
+// 256 of 1024 113 us (5.0).  Items of few tiles are bound by the fetching of instructions:
+// what they seldom need (shares beside, codes that are not finite, the ends of pages) is
+// kept out of their way, in loops of its own and out of line.
 #include "kv_attention.cuh"
 
 namespace fp8la {
@@ -1057,7 +1062,7 @@ fp8la_status launch_few_one(AttnArgs a, int slot, int ctas, cudaStream_t s) {
       }) != cudaSuccess)
     return FP8LA_ERR_CUDA;
   // TMA's limits: strides below 2^40 bytes.  Measured, 64 sequences of 8192 tokens: 179
-  // us with TMA, 193 with pages of 24, which are copied in chunks of 16 bytes.
+  // us with TMA, 193 with pages of 24, which are copied in chunks of 16 bytes (181, 195 since).
   CUtensorMap k = {}, v = {};
   const int64_t most = int64_t(1) << 40;
   a.tma = a.cache.page_size % kGroup == 0 && a.cache.page_stride < most &&

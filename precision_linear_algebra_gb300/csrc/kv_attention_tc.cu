@@ -14,7 +14,9 @@
 //   warps 8-12       codes from the cache (16 bytes a copy) to halves in shared memory,
 //                    swizzled as the MMA reads them, 16 tokens of K or V at a time; V is
 //                    read as the transposed operand
-//   warps 13, 14     where the tokens lie (any pages), K's scales and V's
+//   warps 13, 14     where the tokens lie (any pages), K's scales and V's, and which tokens
+//                    have shares of the denominator that are added up beside (see kSpan),
+//                    rows of zeros in V among them
 //   warp 15          issues the MMAs: S = Q K^T from shared memory, O += P V with P in
 //                    tensor memory
 //
@@ -24,15 +26,16 @@
 // what is below).
 //
 // Measured, 8 K/V heads of 128, 8 query heads each, us and TFLOP/s of what is visible:
-// two prompts of 2048 tokens 257 (536; this kernel 242), one of 8192 1358 (810), 512
-// rows after 32768 tokens 629 (881), 4096 FP32 rows 567 (485: two terms, twice the
+// two prompts of 2048 tokens 264 (520; this kernel 250), one of 8192 1383 (795), 512
+// rows after 32768 tokens 640 (865), 4096 FP32 rows 572 (481: two terms, twice the
 // scores' products).  A tile of 256 rows and 128 tokens takes 3 us, 1.3 of them on the
 // tensor cores; the rest is the chain from scores to weights in 8 warps (64 registers of
 // scores each, 1.9 instructions a cycle and SM), and an item's rows of q and of O are
 // not hidden behind it, which is what kItemCost counts.
 //
 // Tensor memory: S (and P over it) and O of both tiles, 512 columns with D = 128.
-// O stays there; a row's is rescaled only where its maximum grew by 2^8.
+// O stays there; a row's is rescaled only where its maximum grew by 2^8.  A part of more
+// than kPiece tiles goes through in pieces, as the tensor cores cut what they add.
 //
 // V codes that are not finite and that some row of the CTA does not see would reach
 // it as 0 x NaN: such a tile's are written as zeros, and the rows that do see them get
