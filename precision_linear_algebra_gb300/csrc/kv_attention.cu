@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
           // A row of zeros in V adds nothing to the result, whatever its scale: it must not
           // take the others' weights towards a half's end.  Nearly all have another code
           // among the first 16.
-          uint32_t zeros = base + kStep <= end ? ~far : ~far & ((1u << (end - base)) - 1);
+          uint32_t zeros = base + kStep <= end ? 0xffffffffu : (1u << (end - base)) - 1;
 #pragma unroll 1
           for (int ch = 0; ch < C::CH && zeros != 0; ++ch) {
             const uint4 w = lds128(st + (lane / kGroup * 2 + 1) * C::kK +
@@ -620,7 +620,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
             break;
           }
           if (rare && zeros) {
-            set_aside(zeros, [&](float s, int t, int) { return s - lds_f(scales + 4 * (kStep + t)); });
+            set_aside(zeros & ~far,
+                      [&](float s, int t, int) { return s - lds_f(scales + 4 * (kStep + t)); });
             mx[0] = mx[1] = -INFINITY;
 #pragma unroll
             for (int i = 0; i < 2 * kSubs; ++i)

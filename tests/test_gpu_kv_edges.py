@@ -251,3 +251,47 @@ def test_rows_of_zeros_written_by_append():
                  offs=torch.tensor([0, rows], dtype=torch.int32, device="cuda"))
         assert float(cache.v_scale[0, 0, 0]) == 1.0
         check(fl, c)
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_drawn_values(seed):
+    """Scales of V of any exponent, rows of zeros with any scale and scores of any
+    sharpness together, on drawn shapes."""
+    import random
+    import torch
+    fl = lib()
+    r = random.Random(seed)
+    S = r.choice([1, 2, 5])
+    lens = [r.choice([r.randint(1, 40), r.randint(1, 900)]) for _ in range(S)]
+    rows = [r.randint(1, n) if r.random() < 0.5 else min(n, r.randint(1, 3)) for n in lens]
+    prefix = r.choice([0, 0, r.randint(1, 400)])
+    c = make(lens, rows, r.choice([1, 2]), r.choice([1, 3, 8]), 16 * r.choice([1, 4, 5, 8, 8, 16]),
+             r.choice([5, 16, 48]), r.choice(["bfloat16", "float32"]), r.choice(["e4m3", "e5m2"]),
+             prefix=prefix, inside=r.random() < 0.3, seed=seed)
+    cache, H, page = c["cache"], c["H"], c["page"]
+    low, high = sorted((r.uniform(-145, 110), r.uniform(-145, 110)))
+    some, zeros = r.choice([0.0, 0.02, 0.5, 1.0]), r.choice([0.0, 0.02, 0.5])
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    for pages, n in [(c["table"][s], n) for s, n in enumerate(lens)] + [(c["prefix_table"], prefix)]:
+        if n == 0:
+            continue
+        j = torch.arange(n, device="cuda")
+        p, place = pages[j // page].long(), j % page
+        for h in range(H):
+            v = cache.v_scale[p, h, place]
+            pick = torch.rand(n, generator=g, device="cuda") < some
+            e = low + (high - low) * torch.rand(n, generator=g, device="cuda", dtype=torch.float64)
+            v = torch.where(pick, torch.exp2(e).float(), v)
+            z = torch.rand(n, generator=g, device="cuda") < zeros
+            one = torch.rand(n, generator=g, device="cuda") < 0.7
+            cache.v_scale[p, h, place] = torch.where(z & one, 1.0, v)
+            codes = cache.v[p, h, place]
+            codes[z] &= 0x80
+            cache.v[p, h, place] = codes
+    scale = r.choice([0.0, c["D"] ** -0.5, 2.0, 30.0])
+    out, lse = attend(fl, c, scale=scale, max_rows=r.choice([None, max(rows)]))
+    torch.cuda.synchronize()
+    assert fl.device_status() == 0
+    ro, ob, rl, lb = reference(c, scale=scale)
+    assert close(out, ro, ob + 2.0 ** -134 + 2.0 ** -148)
+    assert close(lse, rl, lb)
