@@ -567,7 +567,8 @@ FP8LA_API fp8la_status fp8_kv_read(
  * that is more; the weights exp(x_j) of the products are rounded to 11 bits, for fp32 q
  * too (and below 2^-21 of the row's largest weight times V's scale, among tokens whose V
  * is not all zeros, to 2^-32 of it); those of the denominator and of lse are not rounded.
- * V's scales may be any positive finite numbers.  A token makes the rows that
+ * V's scales may be any positive finite numbers; exp(x_j) below 2^-251 of the row's
+ * largest may count as 0.  A token makes the rows that
  * see it NaN if its K or K's scale is not finite (but counts for nothing where its
  * score is -inf), if its V's scale is not a positive finite number, or if its page is
  * outside the cache; a V that is not finite makes that element of those rows infinite

@@ -7,7 +7,7 @@ import math
 import pytest
 
 from _helpers import lib
-from _kv import attend, check, close, fp8, make, reference
+from _kv import attend, check, close, fp8, make, reference, tokens
 
 pytestmark = pytest.mark.gpu
 
@@ -253,6 +253,37 @@ def test_rows_of_zeros_written_by_append():
         check(fl, c)
 
 
+def _lost(c, scale):
+    """What an element may lose beside its bound, where the tokens that make it weigh next to
+    nothing: a weight is a half, 2^-24 apart at the least where the row's largest one times
+    V's scale is 2^7, so off by 2^-32 of that largest; and a part of a row weighs a product
+    of two exponentials, of 2^-126 or more each, so 2^-252 or 0."""
+    import torch
+    T, H, G, D = c["T"], c["H"], c["G"], c["D"]
+    res = torch.zeros(T, H * G, D, dtype=torch.float64, device="cuda")
+    cache, row = c["cache"], 0
+    for s, (n, rows) in enumerate(zip(c["lens"], c["rows"])):
+        at = []
+        for pages, m in ((c["prefix_table"], c["prefix"]), (c["table"][s], n)):
+            j = torch.arange(m, device="cuda")
+            at.append((pages[j // c["page"]].long(), j % c["page"]))
+        page, place = (torch.cat(x) for x in zip(*at))
+        K, V = (torch.cat(x, 1) for x in zip(tokens(c, -1), tokens(c, s)))
+        j = torch.arange(K.shape[1], device="cuda") - c["prefix"]
+        seen = j[None] <= torch.arange(n - rows, n, device="cuda")[:, None]
+        for h in range(H * G):
+            x = c["q"][row:row + rows, h].double() * scale @ K[h // G].t()
+            p = torch.softmax(x.masked_fill(~seen, -math.inf), 1)
+            size = cache.v_scale[page, h // G, place].double()
+            codes = V[h // G].abs() / size[:, None]
+            some = (codes.amax(1) > 0).double()     # rows of zeros do not count
+            top = (p * size * some).amax(1, keepdim=True)
+            res[row:row + rows, h] = (2.0 ** -32 * top * (seen.double() @ codes) +
+                                      torch.where(p < 2.0 ** -251, p, 0.0) @ V[h // G].abs())
+        row += rows
+    return res
+
+
 @pytest.mark.parametrize("seed", range(60))
 def test_drawn_values(seed):
     """Scales of V of any exponent, rows of zeros with any scale and scores of any
@@ -293,5 +324,5 @@ def test_drawn_values(seed):
     torch.cuda.synchronize()
     assert fl.device_status() == 0
     ro, ob, rl, lb = reference(c, scale=scale)
-    assert close(out, ro, ob + 2.0 ** -134 + 2.0 ** -148)
+    assert close(out, ro, ob + 1.01 * _lost(c, scale) + 2.0 ** -134 + 2.0 ** -148)
     assert close(lse, rl, lb)
