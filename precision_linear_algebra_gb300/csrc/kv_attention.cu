@@ -435,268 +435,281 @@ __global__ void __launch_bounds__(kThreads, (Cfg<F32Q, DP>::CTAS))
     bool poison = false;
     // Tokens whose shares are added up beside are rare: the loop stands here twice, first
     // without the code for them, which would be fetched past in every turn (256 requests of
-    // 1024 tokens 128 us with it), and then with it, from the first such step on, of which
-    // `done` parts are done.
+    // 1024 tokens 128 us with it), and then with it, from a step with such tokens on, of which
+    // `done` parts are done, to one without; the second time to the end.  The same requests
+    // take 114 us, with one such token in each 136 (171 if the first time were to the end),
+    // with a tenth of all tokens 222 (169).
     int base = first, done = 0;
-    bool alive = true;
+    bool alive = true, back = true;
+    do {
 #pragma unroll
-    for (int rare = 0; rare < 2; ++rare) {
+      for (int rare = 0; rare < 2; ++rare) {
 #pragma unroll 1
-      for (; alive && base < end; base += kTile) {
-        if (!rare || done == 0) {
-          cp_wait<kStages - 2>();
-          if (a.tma)
-            alive = __all_sync(0xffffffffu,
-                               mbar_wait(bars + 8 * (taken % kStages), (taken / kStages) & 1u,
-                                         timeout_ns, a.rows.status, &abort_flag));
-          if (!alive) break;
-          ++taken;
-          __syncwarp();
-          const int ahead = base + (kStages - 1) * kTile;
-          if (ahead < end) {
-            const int p = page;
-            page = page_at(ahead + kTile);
-            request(ahead, p);
-          }
-          cp_commit();
-        }
-        const int slot = (taken - 1) % kStages;
-        const uint32_t st = ring + slot * C::kStage, scales = scale_ring + slot * C::kScaleStage;
-        // V's scales: logarithm and reciprocal, relative to a power of two near the first.
-        if (base == first && (!rare || done == 0)) {
-          e0 = min(exponent_of(lds_f(scales + 4 * kStep)), 126);
-          __syncwarp();
-        }
-        uint32_t far = 0;  // tokens whose shares are added up beside
-        if (!rare || done < 2) {
-          const float v = lds_f(scales + 4 * (kStep + lane));
-          const bool fine = base + lane < end && v > 0.0f && v < INFINITY;
-          // Whether the exponent (of subnormal numbers one less than exponent_of) is within
-          // e0 - kSpan .. e0 + kSpan.
-          const uint32_t above = (__float_as_uint(v) >> 23) - static_cast<uint32_t>(e0 + 127 - kSpan);
-          if (__any_sync(0xffffffffu, fine && above > 2 * kSpan)) {
-            if (!rare) {
-              done = 1;
-              break;
+        for (; alive && base < end; base += kTile) {
+          if (!rare || done == 0) {
+            cp_wait<kStages - 2>();
+            if (a.tma)
+              alive = __all_sync(0xffffffffu,
+                                 mbar_wait(bars + 8 * (taken % kStages), (taken / kStages) & 1u,
+                                           timeout_ns, a.rows.status, &abort_flag));
+            if (!alive) break;
+            ++taken;
+            __syncwarp();
+            const int ahead = base + (kStages - 1) * kTile;
+            if (ahead < end) {
+              const int p = page;
+              page = page_at(ahead + kTile);
+              request(ahead, p);
             }
-            const int top = __reduce_max_sync(0xffffffffu, fine ? min(exponent_of(v), 126) : -126);
-            if (top > e0 + kSpan) {
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                add_share(far_top[k], far_sum[k], M[k] - kShift, l[k]);
-                l[k] = 0.0f;
-                M[k] -= static_cast<float>(top - e0);
+            cp_commit();
+          }
+          const int slot = (taken - 1) % kStages;
+          const uint32_t st = ring + slot * C::kStage, scales = scale_ring + slot * C::kScaleStage;
+          // V's scales: logarithm and reciprocal, relative to a power of two near the first.
+          if (base == first && (!rare || done == 0)) {
+            e0 = min(exponent_of(lds_f(scales + 4 * kStep)), 126);
+            __syncwarp();
+          }
+          uint32_t far = 0;  // tokens whose shares are added up beside
+          bool some = false;
+          if (!rare || done < 2) {
+            const float v = lds_f(scales + 4 * (kStep + lane));
+            const bool fine = base + lane < end && v > 0.0f && v < INFINITY;
+            // Whether the exponent (of subnormal numbers one less than exponent_of) is within
+            // e0 - kSpan .. e0 + kSpan.
+            const uint32_t above = (__float_as_uint(v) >> 23) - static_cast<uint32_t>(e0 + 127 - kSpan);
+            if (__any_sync(0xffffffffu, fine && above > 2 * kSpan)) {
+              if (!rare) {
+                done = 1;
+                break;
               }
-              e0 = top;
+              const int top = __reduce_max_sync(0xffffffffu, fine ? min(exponent_of(v), 126) : -126);
+              if (top > e0 + kSpan) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  add_share(far_top[k], far_sum[k], M[k] - kShift, l[k]);
+                  l[k] = 0.0f;
+                  M[k] -= static_cast<float>(top - e0);
+                }
+                e0 = top;
+              }
+              far = __ballot_sync(0xffffffffu, fine && exponent_of(v) < e0 - kSpan);
             }
-            far = __ballot_sync(0xffffffffu, fine && exponent_of(v) < e0 - kSpan);
+            const float near = v * power_of_two(-e0);
+            const bool less = far >> lane & 1;
+            sts_f(scales + 4 * (kStep + lane), base + lane >= end ? 0.0f
+                                               : !fine            ? NAN
+                                               : less             ? log2_far(v, e0)
+                                                                  : lg2(near));
+            // A bad scale is in the exponent alone: rows that do not see it have weight 0.
+            sts_f(scales + 4 * (2 * kStep + lane), !fine ? 1.0f : less ? 0.0f : rcp(near));
           }
-          const float near = v * power_of_two(-e0);
-          const bool less = far >> lane & 1;
-          sts_f(scales + 4 * (kStep + lane), base + lane >= end ? 0.0f
-                                             : !fine            ? NAN
-                                             : less             ? log2_far(v, e0)
-                                                                : lg2(near));
-          // A bad scale is in the exponent alone: rows that do not see it have weight 0.
-          sts_f(scales + 4 * (2 * kStep + lane), !fine ? 1.0f : less ? 0.0f : rcp(near));
-        }
-        // What lies behind the end may be anything.  Where some rows do not see a token (weight
-        // 0), its codes of V that are not finite must not reach them: they are taken out and put
-        // in at the end.
-        const bool partial = all < most && base + kStep > all;
-        if (partial || base + kStep > end) {
-          const uint32_t row = st + (lane / kGroup * 2 + 1) * C::kK;
+          // What lies behind the end may be anything.  Where some rows do not see a token (weight
+          // 0), its codes of V that are not finite must not reach them: they are taken out and put
+          // in at the end.
+          const bool partial = all < most && base + kStep > all;
+          if (partial || base + kStep > end) {
+            const uint32_t row = st + (lane / kGroup * 2 + 1) * C::kK;
 #pragma unroll 1
-          for (int ch = 0; ch < C::CH; ++ch) {
-            const uint32_t at = row + chunk_at<DP>(lane % kGroup, ch);
-            const uint4 v = lds128(at);
-            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            for (int ch = 0; ch < C::CH; ++ch) {
+              const uint32_t at = row + chunk_at<DP>(lane % kGroup, ch);
+              const uint4 v = lds128(at);
+              uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (base + lane >= end) w[j] = 0;
-              if (partial) poison |= Fm::clear4(w[j]);
+              for (int j = 0; j < 4; ++j) {
+                if (base + lane >= end) w[j] = 0;
+                if (partial) poison |= Fm::clear4(w[j]);
+              }
+              st_shared_v4(at, w[0], w[1], w[2], w[3]);
             }
-            st_shared_v4(at, w[0], w[1], w[2], w[3]);
           }
-        }
-        // Scores of tokens 16 u + 8 i + g against the 16 rows, in sc[2 u + i].
-        float sc[2 * kSubs][4] = {};
+          // Scores of tokens 16 u + 8 i + g against the 16 rows, in sc[2 u + i].
+          float sc[2 * kSubs][4] = {};
 #pragma unroll
-        for (int u = 0; u < kSubs; ++u) {
+          for (int u = 0; u < kSubs; ++u) {
 #pragma unroll
-          for (int f = 0; f < DP / 64; ++f) {
-            uint32_t kw[2][4];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint4 w = lds128(st + u * 2 * C::kK + chunk_at<DP>(g + 8 * i, el(f, c) / 16));
-              kw[i][0] = w.x; kw[i][1] = w.y; kw[i][2] = w.z; kw[i][3] = w.w;
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t b[2][2];
+            for (int f = 0; f < DP / 64; ++f) {
+              uint32_t kw[2][4];
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                b[i][0] = decode2<FMT>(kw[i][j] & 0xffffu);
-                b[i][1] = decode2<FMT>(kw[i][j] >> 16);
+                const uint4 w = lds128(st + u * 2 * C::kK + chunk_at<DP>(g + 8 * i, el(f, c) / 16));
+                kw[i][0] = w.x; kw[i][1] = w.y; kw[i][2] = w.z; kw[i][3] = w.w;
               }
 #pragma unroll
-              for (int t = 0; t < C::TERMS; ++t) {
-                const int step = (4 * f + j) * C::TERMS + t;
-                if (C::QREG) {
-                  mma_f16(sc[2 * u], qf[step], b[0][0], b[0][1]);
-                  mma_f16(sc[2 * u + 1], qf[step], b[1][0], b[1][1]);
-                } else {
-                  const uint4 w = lds128(qsm + (step * 32 + lane) * 16);
-                  const uint32_t qw[4] = {w.x, w.y, w.z, w.w};
-                  mma_f16(sc[2 * u], qw, b[0][0], b[0][1]);
-                  mma_f16(sc[2 * u + 1], qw, b[1][0], b[1][1]);
+              for (int j = 0; j < 4; ++j) {
+                uint32_t b[2][2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  b[i][0] = decode2<FMT>(kw[i][j] & 0xffffu);
+                  b[i][1] = decode2<FMT>(kw[i][j] >> 16);
+                }
+#pragma unroll
+                for (int t = 0; t < C::TERMS; ++t) {
+                  const int step = (4 * f + j) * C::TERMS + t;
+                  if (C::QREG) {
+                    mma_f16(sc[2 * u], qf[step], b[0][0], b[0][1]);
+                    mma_f16(sc[2 * u + 1], qf[step], b[1][0], b[1][1]);
+                  } else {
+                    const uint4 w = lds128(qsm + (step * 32 + lane) * 16);
+                    const uint32_t qw[4] = {w.x, w.y, w.z, w.w};
+                    mma_f16(sc[2 * u], qw, b[0][0], b[0][1]);
+                    mma_f16(sc[2 * u + 1], qw, b[1][0], b[1][1]);
+                  }
                 }
               }
             }
           }
-        }
-        __syncwarp();
-        // Adds up beside the shares of the tokens in `mask`, whose scores x(i, k) gives.
-        auto set_aside = [&](uint32_t mask, auto score) {
+          __syncwarp();
+          // Adds up beside the shares of the tokens in `mask`, whose scores x(i, k) gives.
+          auto set_aside = [&](uint32_t mask, auto score) {
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float x[4 * kSubs], top = -INFINITY;
+            for (int k = 0; k < 2; ++k) {
+              float x[4 * kSubs], top = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 4 * kSubs; ++i) {
-              const int t = 8 * (i >> 1) + 2 * c + (i & 1);
-              x[i] = (mask >> t & 1) && base + t < seen[k] ? score(sc[i >> 1][2 * k + (i & 1)], t, k)
-                                                           : -INFINITY;
-              top = fmaxf(top, x[i]);
+              for (int i = 0; i < 4 * kSubs; ++i) {
+                const int t = 8 * (i >> 1) + 2 * c + (i & 1);
+                x[i] = (mask >> t & 1) && base + t < seen[k] ? score(sc[i >> 1][2 * k + (i & 1)], t, k)
+                                                             : -INFINITY;
+                top = fmaxf(top, x[i]);
+              }
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+              // The row's four lanes have the same maximum and a part of the sum each.
+              const float from = top == -INFINITY ? 0.0f : top;
+              float sum = 0.0f;
+#pragma unroll
+              for (int i = 0; i < 4 * kSubs; ++i) sum += ex2(x[i] - from);
+              add_share(far_top[k], far_sum[k], top, sum);
             }
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // The row's four lanes have the same maximum and a part of the sum each.
-            const float from = top == -INFINITY ? 0.0f : top;
-            float sum = 0.0f;
+          };
+          if (rare && far)
+            set_aside(far, [&](float s, int t, int k) { return s * lds_f(scales + 4 * t) * factor[k]; });
+          // Exponents and weights of tokens 8 i + 2c, 8 i + 2c + 1.
 #pragma unroll
-            for (int i = 0; i < 4 * kSubs; ++i) sum += ex2(x[i] - from);
-            add_share(far_top[k], far_sum[k], top, sum);
+          for (int i = 0; i < 2 * kSubs; ++i) {
+            const float2 ks = lds_f2(scales + 32 * i + 8 * c);
+            const float2 lv = lds_f2(scales + 4 * kStep + 32 * i + 8 * c);
+            sc[i][0] = fmaf(sc[i][0] * ks.x, factor[0], lv.x);
+            sc[i][1] = fmaf(sc[i][1] * ks.y, factor[0], lv.y);
+            sc[i][2] = fmaf(sc[i][2] * ks.x, factor[1], lv.x);
+            sc[i][3] = fmaf(sc[i][3] * ks.y, factor[1], lv.y);
           }
-        };
-        if (rare && far)
-          set_aside(far, [&](float s, int t, int k) { return s * lds_f(scales + 4 * t) * factor[k]; });
-        // Exponents and weights of tokens 8 i + 2c, 8 i + 2c + 1.
-#pragma unroll
-        for (int i = 0; i < 2 * kSubs; ++i) {
-          const float2 ks = lds_f2(scales + 32 * i + 8 * c);
-          const float2 lv = lds_f2(scales + 4 * kStep + 32 * i + 8 * c);
-          sc[i][0] = fmaf(sc[i][0] * ks.x, factor[0], lv.x);
-          sc[i][1] = fmaf(sc[i][1] * ks.y, factor[0], lv.y);
-          sc[i][2] = fmaf(sc[i][2] * ks.x, factor[1], lv.x);
-          sc[i][3] = fmaf(sc[i][3] * ks.y, factor[1], lv.y);
-        }
-        if (base + kStep > min(all, end)) {
-#pragma unroll
-          for (int i = 0; i < 2 * kSubs; ++i)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (base + 8 * i + 2 * c + (k & 1) >= min(seen[k >> 1], end)) sc[i][k] = -INFINITY;
-        }
-        float mx[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          mx[k] = fmaxf(sc[0][2 * k], sc[0][2 * k + 1]);
-#pragma unroll
-          for (int i = 1; i < 2 * kSubs; ++i) mx[k] = fmaxf(mx[k], fmaxf(sc[i][2 * k], sc[i][2 * k + 1]));
-        }
-        if (__any_sync(0xffffffffu, mx[0] > M[0] + kLazy || mx[1] > M[1] + kLazy)) {
-          // A row of zeros in V adds nothing to the result, whatever its scale: it must not
-          // take the others' weights towards a half's end.  Nearly all have another code
-          // among the first 16.
-          uint32_t zeros = base + kStep <= end ? 0xffffffffu : (1u << (end - base)) - 1;
-#pragma unroll 1
-          for (int ch = 0; ch < C::CH && zeros != 0; ++ch) {
-            const uint4 w = lds128(st + (lane / kGroup * 2 + 1) * C::kK +
-                                   chunk_at<DP>(lane % kGroup, ch));
-            zeros &= __ballot_sync(0xffffffffu, ((w.x | w.y | w.z | w.w) & 0x7f7f7f7fu) == 0);
-          }
-          if (zeros && !rare) {
-            done = 2;
-            break;
-          }
-          if (rare && zeros) {
-            set_aside(zeros & ~far,
-                      [&](float s, int t, int) { return s - lds_f(scales + 4 * (kStep + t)); });
-            mx[0] = mx[1] = -INFINITY;
+          if (base + kStep > min(all, end)) {
 #pragma unroll
             for (int i = 0; i < 2 * kSubs; ++i)
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                if (zeros >> (8 * i + 2 * c + (k & 1)) & 1) sc[i][k] = -INFINITY;
-                mx[k >> 1] = fmaxf(mx[k >> 1], sc[i][k]);
-              }
+              for (int k = 0; k < 4; ++k)
+                if (base + 8 * i + 2 * c + (k & 1) >= min(seen[k >> 1], end)) sc[i][k] = -INFINITY;
           }
+          float mx[2];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            float m = mx[k];
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            m = fmaxf(m, M[k]);
-            const float down = m == -INFINITY ? 1.0f : ex2(M[k] - m);
-            M[k] = m;
-            l[k] *= down;
+            mx[k] = fmaxf(sc[0][2 * k], sc[0][2 * k + 1]);
 #pragma unroll
-            for (int j = 0; j < C::VH * C::VW; ++j) {
-              o[j][2 * k] *= down;
-              o[j][2 * k + 1] *= down;
-            }
+            for (int i = 1; i < 2 * kSubs; ++i) mx[k] = fmaxf(mx[k], fmaxf(sc[i][2 * k], sc[i][2 * k + 1]));
           }
-        }
-        const float top[2] = {M[0] == -INFINITY ? 0.0f : M[0] - kShift,
-                              M[1] == -INFINITY ? 0.0f : M[1] - kShift};
-        uint32_t pf[kSubs][4];
+          if (__any_sync(0xffffffffu, mx[0] > M[0] + kLazy || mx[1] > M[1] + kLazy)) {
+            // A row of zeros in V adds nothing to the result, whatever its scale: it must not
+            // take the others' weights towards a half's end.  Nearly all have another code
+            // among the first 16.
+            uint32_t zeros = base + kStep <= end ? 0xffffffffu : (1u << (end - base)) - 1;
+#pragma unroll 1
+            for (int ch = 0; ch < C::CH && zeros != 0; ++ch) {
+              const uint4 w = lds128(st + (lane / kGroup * 2 + 1) * C::kK +
+                                     chunk_at<DP>(lane % kGroup, ch));
+              zeros &= __ballot_sync(0xffffffffu, ((w.x | w.y | w.z | w.w) & 0x7f7f7f7fu) == 0);
+            }
+            if (zeros && !rare) {
+              done = 2;
+              break;
+            }
+            some = zeros != 0;
+            if (rare && zeros) {
+              set_aside(zeros & ~far,
+                        [&](float s, int t, int) { return s - lds_f(scales + 4 * (kStep + t)); });
+              mx[0] = mx[1] = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 2 * kSubs; ++i) {
-          const float2 iv = lds_f2(scales + 8 * kStep + 32 * i + 8 * c);
+              for (int i = 0; i < 2 * kSubs; ++i)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) sc[i][k] = ex2(sc[i][k] - top[k >> 1]);
-          l[0] = fmaf(sc[i][0], iv.x, fmaf(sc[i][1], iv.y, l[0]));
-          l[1] = fmaf(sc[i][2], iv.x, fmaf(sc[i][3], iv.y, l[1]));
-          pf[i >> 1][2 * (i & 1)] = pack_half(sc[i][0], sc[i][1]);
-          pf[i >> 1][2 * (i & 1) + 1] = pack_half(sc[i][2], sc[i][3]);
-        }
-        // Values.
+                for (int k = 0; k < 4; ++k) {
+                  if (zeros >> (8 * i + 2 * c + (k & 1)) & 1) sc[i][k] = -INFINITY;
+                  mx[k >> 1] = fmaxf(mx[k >> 1], sc[i][k]);
+                }
+            }
 #pragma unroll
-        for (int u = 0; u < kSubs; ++u) {
+            for (int k = 0; k < 2; ++k) {
+              float m = mx[k];
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+              m = fmaxf(m, M[k]);
+              const float down = m == -INFINITY ? 1.0f : ex2(M[k] - m);
+              M[k] = m;
+              l[k] *= down;
 #pragma unroll
-          for (int f = 0; f < C::VH; ++f) {
-            uint32_t vw[4][C::VW / 4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int token = 2 * c + (i & 1) + 8 * (i >> 1);
-              const uint32_t v_at = st + u * 2 * C::kK + C::kK;
-              if (C::VW == 16) {
-                const uint4 v = lds128(v_at + chunk_at<DP>(token, 8 * f + g));
-                vw[i][0] = v.x; vw[i][1] = v.y; vw[i][C::VW / 8] = v.z; vw[i][C::VW / 4 - 1] = v.w;
-              } else {
-                const uint2 v = lds64(v_at + chunk_at<DP>(token, g >> 1) + (g & 1) * 8);
-                vw[i][0] = v.x; vw[i][1] = v.y;
+              for (int j = 0; j < C::VH * C::VW; ++j) {
+                o[j][2 * k] *= down;
+                o[j][2 * k + 1] *= down;
               }
             }
+          }
+          const float top[2] = {M[0] == -INFINITY ? 0.0f : M[0] - kShift,
+                                M[1] == -INFINITY ? 0.0f : M[1] - kShift};
+          uint32_t pf[kSubs][4];
 #pragma unroll
-            for (int j = 0; j < C::VW / 4; ++j) {
-              const uint32_t a0 = __byte_perm(vw[0][j], vw[1][j], 0x5140);
-              const uint32_t a1 = __byte_perm(vw[0][j], vw[1][j], 0x7362);
-              const uint32_t b0 = __byte_perm(vw[2][j], vw[3][j], 0x5140);
-              const uint32_t b1 = __byte_perm(vw[2][j], vw[3][j], 0x7362);
-              float(*oo)[4] = &o[f * C::VW + 4 * j];
-              mma_f16(oo[0], pf[u], decode2<FMT>(a0 & 0xffffu), decode2<FMT>(b0 & 0xffffu));
-              mma_f16(oo[1], pf[u], decode2<FMT>(a0 >> 16), decode2<FMT>(b0 >> 16));
-              mma_f16(oo[2], pf[u], decode2<FMT>(a1 & 0xffffu), decode2<FMT>(b1 & 0xffffu));
-              mma_f16(oo[3], pf[u], decode2<FMT>(a1 >> 16), decode2<FMT>(b1 >> 16));
+          for (int i = 0; i < 2 * kSubs; ++i) {
+            const float2 iv = lds_f2(scales + 8 * kStep + 32 * i + 8 * c);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sc[i][k] = ex2(sc[i][k] - top[k >> 1]);
+            l[0] = fmaf(sc[i][0], iv.x, fmaf(sc[i][1], iv.y, l[0]));
+            l[1] = fmaf(sc[i][2], iv.x, fmaf(sc[i][3], iv.y, l[1]));
+            pf[i >> 1][2 * (i & 1)] = pack_half(sc[i][0], sc[i][1]);
+            pf[i >> 1][2 * (i & 1) + 1] = pack_half(sc[i][2], sc[i][3]);
+          }
+          // Values.
+#pragma unroll
+          for (int u = 0; u < kSubs; ++u) {
+#pragma unroll
+            for (int f = 0; f < C::VH; ++f) {
+              uint32_t vw[4][C::VW / 4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int token = 2 * c + (i & 1) + 8 * (i >> 1);
+                const uint32_t v_at = st + u * 2 * C::kK + C::kK;
+                if (C::VW == 16) {
+                  const uint4 v = lds128(v_at + chunk_at<DP>(token, 8 * f + g));
+                  vw[i][0] = v.x; vw[i][1] = v.y; vw[i][C::VW / 8] = v.z; vw[i][C::VW / 4 - 1] = v.w;
+                } else {
+                  const uint2 v = lds64(v_at + chunk_at<DP>(token, g >> 1) + (g & 1) * 8);
+                  vw[i][0] = v.x; vw[i][1] = v.y;
+                }
+              }
+#pragma unroll
+              for (int j = 0; j < C::VW / 4; ++j) {
+                const uint32_t a0 = __byte_perm(vw[0][j], vw[1][j], 0x5140);
+                const uint32_t a1 = __byte_perm(vw[0][j], vw[1][j], 0x7362);
+                const uint32_t b0 = __byte_perm(vw[2][j], vw[3][j], 0x5140);
+                const uint32_t b1 = __byte_perm(vw[2][j], vw[3][j], 0x7362);
+                float(*oo)[4] = &o[f * C::VW + 4 * j];
+                mma_f16(oo[0], pf[u], decode2<FMT>(a0 & 0xffffu), decode2<FMT>(b0 & 0xffffu));
+                mma_f16(oo[1], pf[u], decode2<FMT>(a0 >> 16), decode2<FMT>(b0 >> 16));
+                mma_f16(oo[2], pf[u], decode2<FMT>(a1 & 0xffffu), decode2<FMT>(b1 & 0xffffu));
+                mma_f16(oo[3], pf[u], decode2<FMT>(a1 >> 16), decode2<FMT>(b1 >> 16));
+              }
+            }
+          }
+          // Reads before the copies that a next turn asks for.
+          if (a.tma) fence_proxy_async_smem();
+          if (rare) {
+            done = 0;
+            if (back && !some && far == 0) {
+              back = false;
+              base += kTile;
+              break;
             }
           }
         }
-        // Reads before the copies that a next turn asks for.
-        if (a.tma) fence_proxy_async_smem();
-        if (rare) done = 0;
       }
-    }
+    } while (alive && base < end);
     cp_wait<0>();
     for (; taken < put; ++taken)  // where a wait ran out
       if (a.tma)
