@@ -28,7 +28,7 @@
 // sequences of 8192 tokens 181 us (6.1 TB/s), of lengths up to 8192 108 us (5.6; 128 with
 // steps of 32 tokens, 149 with 16, both before kItemCost); one of 131072 60 us (4.7); one
 // of 2048 17 us, two launches whose addresses and instructions come one after the other;
-// 256 of 1024 113 us (5.0).  Items of few tiles are bound by the fetching of instructions:
+// 256 of 1024 115 us (4.9).  Items of few tiles are bound by the fetching of instructions:
 // what they seldom need (shares beside, codes that are not finite, the ends of pages) is
 // kept out of their way, in loops of its own and out of line.
 #include "kv_attention.cuh"
@@ -1076,7 +1076,7 @@ fp8la_status launch_few_one(AttnArgs a, int slot, int ctas, cudaStream_t s) {
       }) != cudaSuccess)
     return FP8LA_ERR_CUDA;
   // TMA's limits: strides below 2^40 bytes.  Measured, 64 sequences of 8192 tokens: 179
-  // us with TMA, 193 with pages of 24, which are copied in chunks of 16 bytes (181, 195 since).
+  // us with TMA, 193 with pages of 24, which are copied in chunks of 16 bytes (181, 198 since).
   CUtensorMap k = {}, v = {};
   const int64_t most = int64_t(1) << 40;
   a.tma = a.cache.page_size % kGroup == 0 && a.cache.page_stride < most &&

@@ -26,8 +26,8 @@
 // what is below).
 //
 // Measured, 8 K/V heads of 128, 8 query heads each, us and TFLOP/s of what is visible:
-// two prompts of 2048 tokens 264 (520; this kernel 250), one of 8192 1383 (795), 512
-// rows after 32768 tokens 640 (865), 4096 FP32 rows 572 (481: two terms, twice the
+// two prompts of 2048 tokens 264 (520; this kernel 250), one of 8192 1379 (797), 512
+// rows after 32768 tokens 638 (868), 4096 FP32 rows 572 (481: two terms, twice the
 // scores' products).  A tile of 256 rows and 128 tokens takes 3 us, 1.3 of them on the
 // tensor cores; the rest is the chain from scores to weights in 8 warps (64 registers of
 // scores each, 1.9 instructions a cycle and SM), and an item's rows of q and of O are
